@@ -398,6 +398,112 @@ QSM_API qsm_status q8_gemv_i8(const int8_t* qx, const float* dx, const int8_t* q
                               const uint16_t* d, int32_t N, int32_t K, uint16_t* y,
                               int32_t* dev_status, cudaStream_t stream);
 
+/* ----------------------------------------------------------------- MXFP4 */
+
+/* Element types of dense matrices in the MXFP4 calls. */
+typedef enum { QSM_BF16 = 0, QSM_FP16 = 1, QSM_FP32 = 2 } qsm_dtype;
+
+/* MXFP4 matrices [experts, rows, cols], cols a multiple of 32: 4-bit
+ * floating-point codes (e2m1: sign, two exponent bits, one mantissa bit; 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6) and one scale 2^(s - 127) (e8m0) per block of 32
+ * columns; value = code * scale.  s = 255 makes its block not a number.
+ *   codes   [experts, rows, cols / 2] bytes, column 2c in the low nibble of
+ *           byte c
+ *   scales  per expert mx4_scale_bytes(rows, cols) bytes: tiles of 128 rows
+ *           x 4 blocks, 512 bytes each, in order [row tile][column tile];
+ *           byte 16 (r % 32) + 4 (r / 32) + b of a tile is the scale of its
+ *           row r, block b.  Rows and blocks past the matrix hold 0.
+ * Both 16-byte aligned. */
+typedef struct {
+  int32_t experts, rows, cols;
+  const uint8_t* codes;
+  const uint8_t* scales;
+} qsm_mx4;
+
+/* Bytes of the scale tiles of one [rows, cols] matrix. */
+QSM_API size_t mx4_scale_bytes(int32_t rows, int32_t cols);
+
+/* x [rows, cols] -> codes and scale tiles (padding included):
+ *   s = max(floor(log2 max|x in the block|) + 125, 0), 0 for a block of zeros;
+ *   code = the value nearest to x / 2^(s - 127), ties to the even code,
+ *   magnitudes over 6 become 6.
+ * A block that holds an infinity or a NaN gets s = 255 and sets
+ * QSM_DEV_NONFINITE.
+ *   x  of type dtype (qsm_dtype), row_stride elements from row to row (a
+ *      multiple of 8, at least cols), 16-byte aligned
+ * Requires rows >= 0, cols >= 32 and a multiple of 32. */
+QSM_API qsm_status mx4_quantize(const void* x, int32_t dtype, int64_t row_stride, int32_t rows,
+                                int32_t cols, uint8_t* codes, uint8_t* scales,
+                                int32_t* dev_status, cudaStream_t stream);
+
+/* y [experts, rows, cols] (dtype, dense, 16-byte aligned) = the values that
+ * a stands for, rounded to dtype (fp16: beyond 65504 infinite). */
+QSM_API qsm_status mx4_dequantize(const qsm_mx4* a, int32_t dtype, void* y, cudaStream_t stream);
+
+/* y[m, n] = sum_c a[m, c] * w[n, c], products exact, fp32 accumulation.
+ *   a [1, M, K], w [1, N, K];  y [M, N] bf16 or fp32, ldy elements from row
+ *   to row (ldy >= N), aligned to its element.
+ * An operand row with s = 255 makes its row or column of y not a number. */
+QSM_API qsm_status mx4_gemm(const qsm_mx4* a, const qsm_mx4* w, int32_t dtype, void* y,
+                            int64_t ldy, int32_t* dev_status, cudaStream_t stream);
+
+/* Most rows of x that mx4_gemv takes. */
+#define QSM_MX4_GEMV_MAX_ROWS 32
+
+/* y[t, n] = sum_c x[t, c] * w[n, c] for a few rows of 16-bit activations,
+ * which are not rounded: each block of 32 of a row enters the product to
+ * 2^-23 of its largest magnitude, products exact, fp32 accumulation.
+ *   x [T, K] bf16, row_stride elements from row to row (a multiple of 8);
+ *   w [1, N, K];  y [T, N] bf16 (2-byte aligned).
+ * A block of x that holds an infinity, a NaN or a magnitude of 2^127 or more
+ * makes its row of y not a number and sets QSM_DEV_NONFINITE.
+ * Requires 0 <= T <= QSM_MX4_GEMV_MAX_ROWS, K <= 65536. */
+QSM_API qsm_status mx4_gemv(const uint16_t* x, int64_t row_stride, int32_t T, const qsm_mx4* w,
+                            uint16_t* y, int32_t* dev_status, cudaStream_t stream);
+
+/* One MoE FFN layer as qsm_moe_layer, with MXFP4 weights: gate_up [E, 2I, H],
+ * down [E, H, I], shared_gate_up [1, 2I, H], shared_down [1, H, I], and
+ * shared_gate [H] fp32 or NULL.  Requires H % 128 == 0, I % 128 == 0,
+ * H, I <= 16384, 1 <= k <= min(E, 32), E <= 1024. */
+typedef struct {
+  int32_t H, I, E, k;
+  qsm_mx4 gate_up, down, shared_gate_up, shared_down;
+  const float* shared_gate;
+} qsm_mx4_layer;
+
+/* What the expert products of moe_mx4_forward multiply the weights with:
+ *   QSM_ACTS_BF16  x and h unrounded, as mx4_gemv (T <= QSM_MX4_MOE_MAX_ROWS:
+ *                  every touched weight is read once, few tokens each)
+ *   QSM_ACTS_MX4   x and h quantized to MXFP4 by the rule of mx4_quantize (any
+ *                  number of tokens: grouped 4-bit products) */
+typedef enum { QSM_ACTS_BF16 = 0, QSM_ACTS_MX4 = 1 } qsm_acts;
+#define QSM_MX4_MOE_MAX_ROWS 64
+
+/* Bytes of workspace moe_mx4_forward needs; 0 if the layer, T or acts is not
+ * supported. */
+QSM_API size_t moe_mx4_workspace_bytes(const qsm_mx4_layer* L, int32_t T, int32_t acts);
+
+/* The whole layer: route (as moe_route, ids and weights the same bits),
+ * group, and for every assignment of token t to expert e
+ *     gu = W_gate_up[e] x[t],  h = silu(gu[:I]) * gu[I:],  o = W_down[e] h,
+ * the same for the shared expert, and
+ *     y[t] = sum_j topk_w[t, j] * o(t, j) + g[t] * o_shared(t),
+ * g[t] = sigmoid(x[t] . shared_gate), or 1 when shared_gate is NULL.
+ * The sums over j run in ascending j, the shared expert first: y does not
+ * depend on timing.
+ *   x [T, H] bf16;  flags, w_router, logit_bias, topk_idx, topk_w, y, y_f32
+ *   as for moe_layer_forward;
+ *   workspace  >= moe_mx4_workspace_bytes(L, T, acts) bytes, zeros before
+ *              its first use, and every call leaves it fit for the next of
+ *              the same layer shape, T and acts.
+ * With QSM_ACTS_MX4 the outputs of the experts are held in fp16 (scaled by
+ * 1/16) until they are summed: one beyond that range sets QSM_DEV_FP16_RANGE. */
+QSM_API qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x, int32_t T,
+                                   int32_t acts, const float* w_router, const float* logit_bias,
+                                   int32_t flags, int32_t* topk_idx, float* topk_w, uint16_t* y,
+                                   float* y_f32, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_status, cudaStream_t stream);
+
 /* ------------------------------------------------------------------ misc */
 
 /* Static description of a status code. */

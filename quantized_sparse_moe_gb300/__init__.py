@@ -11,7 +11,7 @@ importing the binding's functions fails.
 Entry points (see include/qsmoe.h for the exact contracts):
   moe_route, moe_group_tokens, moe_ffn_forward, q8_gemv
 plus ``MoEForward``, which owns the buffers of one layer call and issues the
-three calls in order on one stream.
+three calls in order on one stream; the MXFP4 calls are in mx4.py.
 """
 from __future__ import annotations
 
@@ -22,6 +22,10 @@ import threading
 import torch
 
 from . import build as _build
+from . import mx4 as _mx4
+from .mx4 import (Mx4Forward, Mx4Layer, Mx4Tensor, moe_mx4_workspace_bytes,  # noqa: F401
+                  mx4_dequantize, mx4_gemm, mx4_gemv, mx4_quantize, mx4_scale_bytes,
+                  mx4_tile_scales)
 
 Q8_0 = 0
 AFFINE4_G64 = 1
@@ -124,6 +128,7 @@ def lib() -> ctypes.CDLL:
             L.qsm_decode_layer_fits.restype = i32
             L.qsm_launch_count.argtypes = []
             L.qsm_launch_count.restype = ctypes.c_uint64
+            _mx4.declare(L)
             _lib = L
     return _lib
 

@@ -1,0 +1,430 @@
+// The product of two MXFP4 matrices on the block-scaled tensor cores, and
+// the grouped products of an MoE layer whose activations are MXFP4 as well.
+//
+//   y[m, n] = sum_b 2^(sa[m,b] + sw[n,b] - 254) sum_{c in b} a[m, c] w[n, c]
+//
+// The tensor cores take the 4-bit codes and the scales as they lie in
+// memory, so nothing is expanded: a stage of the pipeline is 256 columns of
+// 128 rows of a and of BN rows of w (128 bytes a row, TMA with the 128-byte
+// swizzle) and their scale tiles (bulk copies), which go on to tensor
+// memory with tcgen05.cp; four 64-wide MMAs then work off a stage.  Every
+// product of two codes is exact, and the sums are fp32.
+//
+// Roles in a persistent CTA (one per SM): warp 0 loads, warp 1 issues the
+// scale copies and the MMAs, warps 4-11 are the epilogue.  One accumulator
+// of BN columns: the epilogue's threads take their half rows into registers
+// at once (BN / 2 columns each), hand the accumulator back and convert and
+// store while the next tile's MMAs run.
+#include "mx4_gemm.cuh"
+
+namespace qsm {
+namespace mx4 {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kStagePitch = 144;  // bytes of a staged epilogue row (128 + 16)
+
+template <int BN>
+struct Cfg {
+  static constexpr int kGroups = BN >= 128 ? BN / 128 : 1;  // scale tiles per column tile of w
+  static constexpr int kABytes = 128 * 128;
+  static constexpr int kWBytes = BN * 128;
+  static constexpr int kSfaBytes = 2 * kTileBytes;
+  static constexpr int kSfwBytes = 2 * kTileBytes * kGroups;
+  static constexpr int kStage = kABytes + kWBytes + kSfaBytes + kSfwBytes;
+  static constexpr int kStages = BN == 256 ? 3 : BN == 128 ? 5 : 6;
+  static constexpr int kStaging = kEpiWarps * 32 * kStagePitch;
+  static constexpr int kSmem = kStages * kStage + kStaging + 1024;
+  static constexpr int kSfCols = 8 + 8 * kGroups;  // scale columns of one stage
+  static constexpr int kTmem = BN == 256 ? 512 : BN == 128 ? 256 : 128;
+  static_assert(kStage % 1024 == 0 && BN + 2 * kSfCols <= kTmem && kSmem <= 227 * 1024, "tile");
+};
+
+// Where a tile's operands and results lie.
+struct Tile {
+  int a_row, a_tile;   // first row of a, and its row tile of scales
+  int cnt;             // rows of a that exist
+  int e;               // expert, -1 = shared (grouped modes)
+  int n0;              // first column of y (dense, down) or intermediate (gate_up)
+  int w_row[2];        // first row of each box of w
+  int w_tile[2];       // row tile of the scales of each 128 rows of w, -1: none
+};
+
+template <int MODE, int BN>
+__device__ __forceinline__ Tile tile_of(const GemmParams& p, int item) {
+  Tile t;
+  const int tau = item / p.nsub, sub = item - tau * p.nsub;
+  t.a_tile = tau;
+  t.a_row = tau * 128;
+  t.e = -1;
+  int ebase = 0;  // the expert's first row of w
+  if (MODE == kDense) {
+    t.cnt = min(128, p.M - t.a_row);
+  } else if (tau < p.shared_tiles) {
+    t.cnt = min(128, p.T - t.a_row);
+  } else {
+    const int2 te = __ldcg(reinterpret_cast<const int2*>(p.tile_map) + (tau - p.shared_tiles));
+    t.e = te.x;
+    t.cnt = min(128, __ldcg(p.offsets + te.x + 1) - te.y);
+    ebase = te.x * p.N;
+  }
+  if (MODE == kGateUp) {
+    t.n0 = sub * 128;
+    t.w_row[0] = ebase + t.n0;
+    t.w_row[1] = ebase + p.N / 2 + t.n0;
+    t.w_tile[0] = t.w_row[0] >> 7;
+    t.w_tile[1] = t.w_row[1] >> 7;
+  } else {
+    t.n0 = sub * BN;
+    t.w_row[0] = t.w_row[1] = ebase + t.n0;
+    t.w_tile[0] = (ebase >> 7) + (t.n0 >> 7);
+    t.w_tile[1] = t.n0 + 128 < p.N ? t.w_tile[0] + 1 : -1;
+  }
+  return t;
+}
+
+// Eight consecutive outputs of a row (16 bytes as bf16) or four (as fp32),
+// at column n of N: whole where they fit and are aligned, else one by one.
+template <bool F32>
+__device__ __forceinline__ void store_chunk(void* y, size_t off, int n, int N, bool vec, uint4 v) {
+  constexpr int kPer = F32 ? 4 : 8;
+  if (vec && n + kPer <= N) {
+    if (F32) *reinterpret_cast<uint4*>(static_cast<float*>(y) + off) = v;
+    else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + off) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (n + i >= N) break;
+    if (F32) static_cast<uint32_t*>(y)[off + i] = w[i];
+    else static_cast<uint16_t*>(y)[off + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// This thread's NC columns of its row into registers: halves of the tile's
+// columns for the dense and down modes; in gate_up, 64 gate columns and the
+// 64 up columns of the same intermediates.
+template <int MODE, int BN>
+__device__ __forceinline__ void take_acc(uint32_t taddr, int half, uint32_t (&r)[BN / 2]) {
+  constexpr int NC = BN / 2;
+#pragma unroll
+  for (int c = 0; c < NC; c += 32) {
+    const int col = MODE == kGateUp ? (c < NC / 2 ? half * (NC / 2) + c : NC + half * (NC / 2) + c - NC / 2)
+                                    : half * NC + c;
+    tmem_ld32_nowait(taddr + col, r + c);
+  }
+#pragma unroll
+  for (int c = 0; c < NC; c += 32) tmem_wait_ld32(r + c);
+}
+
+template <int MODE, int BN, bool F32>
+__global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_constant__ GemmParams p) {
+  using C = Cfg<BN>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], acc_full, acc_empty, done;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  volatile int* abort_p = &abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&acc_full, 1);
+    mbar_init(&acc_empty, kEpiWarps);
+    mbar_init(&done, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tc::prefetch_map(&p.a);
+    tc::prefetch_map(&p.w);
+  }
+  if (warp == 2) tc::tmem_alloc(&tmem_base, C::kTmem);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_base;
+
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tiles = MODE == kDense ? p.tiles : p.shared_tiles + __ldcg(p.n_tiles);
+  const int total = tiles * p.nsub;
+  const int nst = (p.K + kStageK - 1) / kStageK;
+  const int cts = col_tiles(p.K);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t f = 0;
+      for (int item = blockIdx.x; item < total && !*abort_p; item += gridDim.x) {
+        const Tile t = tile_of<MODE, BN>(p, item);
+        const bool sh = MODE != kDense && t.e < 0;
+        const CUtensorMap* wm = sh ? &p.w_sh : &p.w;
+        const uint8_t* wsc = sh ? p.w_scales_sh : p.w_scales;
+        const int groups = C::kGroups == 1 || t.w_tile[1] < 0 ? 1 : 2;
+        bool ok = true;
+        for (int ks = 0; ks < nst; ++ks, ++f) {
+          const int s = f % C::kStages;
+          if (f >= C::kStages && !wait_or_abort(&empty[s], (f / C::kStages - 1) & 1, abort_p, p.status)) {
+            ok = false;
+            break;
+          }
+          unsigned char* base = smem + s * C::kStage;
+          const uint32_t sfb = (uint32_t)min(2, cts - 2 * ks) * kTileBytes;  // scale bytes of a row tile
+          mbar_arrive_expect_tx(&full[s], C::kABytes + C::kWBytes + sfb * (1 + groups));
+          tc::tma_load_2d(base, &p.a, ks * 128, t.a_row, &full[s]);
+          unsigned char* wb = base + C::kABytes;
+          if (MODE == kGateUp) {
+            tc::tma_load_2d(wb, wm, ks * 128, t.w_row[0], &full[s]);
+            tc::tma_load_2d(wb + 128 * 128, wm, ks * 128, t.w_row[1], &full[s]);
+          } else {
+            tc::tma_load_2d(wb, wm, ks * 128, t.w_row[0], &full[s]);
+          }
+          unsigned char* sf = wb + C::kWBytes;
+          bulk_g2s(sf, p.a_scales + ((size_t)t.a_tile * cts + 2 * ks) * kTileBytes, sfb, &full[s]);
+          sf += C::kSfaBytes;
+          for (int g = 0; g < groups; ++g)
+            bulk_g2s(sf + g * 2 * kTileBytes,
+                     wsc + ((size_t)t.w_tile[g] * cts + 2 * ks) * kTileBytes, sfb, &full[s]);
+        }
+        if (!ok) break;
+      }
+      // after an abort, let the last copies land before the CTA exits
+      const uint32_t n = f < (uint32_t)C::kStages ? f : (uint32_t)C::kStages;
+      for (uint32_t i = 1; i <= n; ++i)
+        mbar_wait_bounded(&full[(f - i) % C::kStages], ((f - i) / C::kStages) & 1, 1u << 16);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t f = 0;
+      int j = 0;
+      for (int item = blockIdx.x; item < total && !*abort_p; item += gridDim.x, ++j) {
+        // in tiles of 64 rows of w, every other one starts in the middle of a
+        // scale tile: two columns on
+        const int sf_off = BN == 64 ? ((item % p.nsub) & 1) * 2 : 0;
+        if (j >= 1 && !wait_or_abort(&acc_empty, (j - 1) & 1, abort_p, p.status)) break;
+        tc::tc_fence_after();
+        bool ok = true;
+        for (int ks = 0; ks < nst; ++ks, ++f) {
+          const int s = f % C::kStages;
+          if (!wait_or_abort(&full[s], (f / C::kStages) & 1, abort_p, p.status)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t base = smem_u32(smem + s * C::kStage);
+          const uint32_t wb = base + C::kABytes, sfa_s = wb + C::kWBytes, sfw_s = sfa_s + C::kSfaBytes;
+          const uint32_t sfa = tmem + BN + (f & 1) * C::kSfCols, sfw = sfa + 8;
+          const int kv = min(kStageK, p.K - ks * kStageK);
+          for (int ct = 0; ct * kTileCols < kv; ++ct) {
+            copy_scales(sfa + 4 * ct, sfa_s + ct * kTileBytes);
+            for (int g = 0; g < C::kGroups; ++g)
+              copy_scales(sfw + 4 * (ct * C::kGroups + g), sfw_s + (2 * g + ct) * kTileBytes);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk * 64 >= kv) break;
+            mma_mxf4(tmem, tc::sw128_desc(base + kk * 32), tc::sw128_desc(wb + kk * 32),
+                     idesc_mxf4(BN, kk & 1), sfa + 4 * (kk >> 1),
+                     sfw + 4 * C::kGroups * (kk >> 1) + sf_off, (ks > 0 || kk > 0) ? 1u : 0u);
+          }
+          tc::mma_commit(&empty[s]);
+        }
+        if (!ok) break;
+        tc::mma_commit(&acc_full);
+      }
+      // every MMA issued has completed before tensor memory is freed
+      tc::mma_commit(&done);
+      mbar_wait_bounded(&done, 0, kWaitIters);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int q4 = warp & 3, half = (warp - 4) >> 2;
+    const int row = 32 * q4 + lane;
+    unsigned char* stage = smem + C::kStages * C::kStage + (warp - 4) * 32 * kStagePitch;
+    const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16);
+    bool bad = false;
+    int j = 0;
+    for (int item = blockIdx.x; item < total; item += gridDim.x, ++j) {
+      if (__any_sync(0xffffffffu, *abort_p != 0)) break;
+      const Tile t = tile_of<MODE, BN>(p, item);
+      if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full, j & 1, abort_p, p.status))) break;
+      tc::tc_fence_after();
+      constexpr int NC = BN / 2;
+      uint32_t r[NC];
+      take_acc<MODE, BN>(taddr, half, r);
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&acc_empty);
+      if (MODE == kGateUp) {
+        // h of this row's 64 intermediates, quantized where it is formed
+        if (row < t.cnt) {
+          const size_t pos = (size_t)t.a_row + row;
+          uint32_t sbytes = 0;
+#pragma unroll
+          for (int b = 0; b < NC / 64; ++b) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float h = silu(__uint_as_float(r[32 * b + i])) * __uint_as_float(r[NC / 2 + 32 * b + i]);
+              r[32 * b + i] = __float_as_uint(h);
+              m = max(m, r[32 * b + i] & 0x7fffffffu);
+            }
+            const uint32_t s = scale_of(m);
+            if (s == 255u) bad = true;
+            const float inv = s == 255u ? 0.f : inv_scale(s);
+            uint32_t c[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              float v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[32 * b + 8 * w + i]) * inv;
+              c[w] = f32x8_to_e2m1x8(v);
+            }
+            *reinterpret_cast<uint4*>(p.h_codes + (pos * p.I + t.n0 + half * (NC / 2) + 32 * b) / 2) =
+                make_uint4(c[0], c[1], c[2], c[3]);
+            sbytes |= s << (8 * b);
+          }
+          uint8_t* sw = p.h_scales + scale_word((int)pos, t.n0 >> 7, p.I >> 7);
+          *reinterpret_cast<uint16_t*>(sw + 2 * half) = (uint16_t)sbytes;
+        }
+      } else {
+        // through a staged copy of the warp's 32 rows, 128 bytes of each at
+        // a time, so that a row's outputs leave in whole 128-byte lines
+        constexpr bool kHalf = MODE == kDown;  // fp16 of 1/16 the value
+        constexpr int kCols = F32 ? 32 : 64;   // columns per step
+        constexpr int kStep = kCols < NC ? kCols : NC;
+        void* y = p.y;
+        const size_t ld = p.ldy;
+#pragma unroll
+        for (int c0 = 0; c0 < NC; c0 += kStep) {
+          unsigned char* mine = stage + lane * kStagePitch;
+#pragma unroll
+          for (int c = 0; c < kStep; c += F32 ? 4 : 8) {
+            uint4 v;
+            if (F32) {
+              v = make_uint4(r[c0 + c], r[c0 + c + 1], r[c0 + c + 2], r[c0 + c + 3]);
+            } else {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float a = __uint_as_float(r[c0 + c + 2 * i]), b = __uint_as_float(r[c0 + c + 2 * i + 1]);
+                if (kHalf) {
+                  const float a16 = a * kOutScale, b16 = b * kOutScale;
+                  if (row < t.cnt && (!(fabsf(a16) <= 65504.f) || !(fabsf(b16) <= 65504.f)))
+                    bad |= t.n0 + half * NC + c0 + c + 2 * i < p.N;
+                  const __half2 h2 = __floats2half2_rn(a16, b16);
+                  w[i] = *reinterpret_cast<const uint32_t*>(&h2);
+                } else {
+                  w[i] = pack_bf16(a, b);
+                }
+              }
+              v = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            *reinterpret_cast<uint4*>(mine + c * (F32 ? 4 : 2)) = v;
+          }
+          __syncwarp();
+          constexpr int kChunks = kStep * (F32 ? 4 : 2) / 16;  // 16-byte pieces of a row
+          for (int i = lane; i < 32 * kChunks; i += 32) {
+            const int rr = i / kChunks, ch = i % kChunks;
+            const int n = t.n0 + half * NC + c0 + ch * (F32 ? 4 : 8);
+            if (32 * q4 + rr < t.cnt && n < p.N)
+              store_chunk<F32>(y, ((size_t)t.a_row + 32 * q4 + rr) * ld + n, n, p.N, p.vec != 0,
+                               *reinterpret_cast<const uint4*>(stage + rr * kStagePitch + ch * 16));
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (bad) set_status(p.status, MODE == kGateUp ? QSM_DEV_NONFINITE : QSM_DEV_FP16_RANGE);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 2) tc::tmem_dealloc(tmem, C::kTmem);
+}
+
+template <int MODE, int BN, bool F32>
+qsm_status launch_tile(const GemmParams& p, int most, cudaStream_t stream) {
+  using C = Cfg<BN>;
+  auto* k = mx4_gemm_kernel<MODE, BN, F32>;
+  static thread_local int ready_dev = -1;  // the attribute is per device
+  int dev = 0;
+  QSM_CUDA_TRY(cudaGetDevice(&dev));
+  if (ready_dev != dev) {
+    QSM_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+    ready_dev = dev;
+  }
+  const int grid = most < sm_count() ? most : sm_count();
+  QSM_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(kThreads), C::kSmem, stream, p));
+  return QSM_OK;
+}
+
+template <int BN>
+qsm_status launch_dense(GemmParams& p, const qsm_mx4* w, bool f32, cudaStream_t stream) {
+  if (!make_codes_map(&p.w, w->codes, w->rows, w->cols, BN)) return QSM_ERR_CUDA;
+  p.nsub = (p.N + BN - 1) / BN;
+  if ((long long)p.tiles * p.nsub > (1ll << 30)) return QSM_ERR_UNSUPPORTED;
+  const int most = p.tiles * p.nsub;
+  return f32 ? launch_tile<kDense, BN, true>(p, most, stream)
+             : launch_tile<kDense, BN, false>(p, most, stream);
+}
+
+}  // namespace
+
+qsm_status launch_grouped(const GemmParams& p, int mode, cudaStream_t stream) {
+  const int most = 1 << 30;  // how many tiles there are is known on the device only
+  return mode == kGateUp ? launch_tile<kGateUp, 256, false>(p, most, stream)
+                         : launch_tile<kDown, 256, false>(p, most, stream);
+}
+
+}  // namespace mx4
+}  // namespace qsm
+
+extern "C" qsm_status mx4_gemm(const qsm_mx4* a, const qsm_mx4* w, int32_t dtype, void* y,
+                               int64_t ldy, int32_t* dev_status, cudaStream_t stream) {
+  using namespace qsm;
+  using namespace qsm::mx4;
+  if (!a || !w || (dtype != QSM_BF16 && dtype != QSM_FP32)) return QSM_ERR_INVALID_ARGUMENT;
+  if (a->experts != 1 || w->experts != 1 || a->cols != w->cols || a->rows < 0 || w->rows < 0 ||
+      ldy < w->rows)
+    return QSM_ERR_INVALID_ARGUMENT;
+  if (a->rows == 0 || w->rows == 0) return QSM_OK;
+  const size_t el = dtype == QSM_FP32 ? 4 : 2;
+  if (!mx4_valid(a) || !mx4_valid(w) || !y || !dev_status || !aligned4(dev_status) ||
+      reinterpret_cast<uintptr_t>(y) % el)
+    return QSM_ERR_INVALID_ARGUMENT;
+  GemmParams p = {};
+  p.M = a->rows;
+  p.N = w->rows;
+  p.K = a->cols;
+  p.tiles = row_tiles(p.M);
+  p.y = y;
+  p.ldy = (size_t)ldy;
+  p.vec = aligned16(y) && (size_t)ldy * el % 16 == 0;
+  p.a_scales = a->scales;
+  p.w_scales = w->scales;
+  p.status = dev_status;
+  if (!make_codes_map(&p.a, a->codes, a->rows, a->cols, 128)) return QSM_ERR_CUDA;
+  // the widest tile that still gives every SM one
+  const int nsm = sm_count();
+  const long long t256 = (long long)p.tiles * ((p.N + 255) / 256);
+  const long long t128 = (long long)p.tiles * ((p.N + 127) / 128);
+  const bool f32 = dtype == QSM_FP32;
+  if (t256 >= nsm) return launch_dense<256>(p, w, f32, stream);
+  if (t128 >= nsm) return launch_dense<128>(p, w, f32, stream);
+  return launch_dense<64>(p, w, f32, stream);
+}

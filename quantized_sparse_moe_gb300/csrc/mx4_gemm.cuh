@@ -1,0 +1,47 @@
+// Parameters of the MXFP4 product kernel (mx4_gemm.cu), shared with the MoE
+// layer that issues its grouped modes (mx4_moe.cu).
+#pragma once
+
+#include "mx4_common.cuh"
+
+namespace qsm {
+namespace mx4 {
+
+// kDense: y = a w^T.  kGateUp: rows of a grouped by expert, 128 gate and the
+// 128 up rows of the same intermediates, h = silu(gate) * up quantized to
+// MXFP4.  kDown: the grouped h times the expert's down rows, fp16 of the
+// outputs scaled by 1/16, one row per row of a.
+enum { kDense = 0, kGateUp = 1, kDown = 2 };
+
+constexpr float kOutScale = 1.0f / 16.0f;  // of the grouped outputs held in fp16
+
+struct GemmParams {
+  CUtensorMap a;         // codes of a, boxes of 128 rows
+  CUtensorMap w, w_sh;   // codes of w (routed, shared), boxes of BN rows (gate_up: 128)
+  const uint8_t* a_scales;
+  const uint8_t* w_scales;
+  const uint8_t* w_scales_sh;
+  int M, N, K;           // N: rows of w (per expert)
+  int tiles;             // row tiles of a (dense)
+  int nsub;              // column tiles
+  // dense and down
+  void* y;
+  size_t ldy;
+  int vec;               // rows of y are 16-byte aligned
+  // grouped: tile tau < shared_tiles holds tokens 128 tau .. of the shared
+  // expert, the others the blocks of tile_map (expert, first sorted row);
+  // tile tau's rows of a (and of h and of y) start at 128 tau
+  int T, I, shared_tiles;
+  const int32_t* offsets;
+  const int32_t* tile_map;
+  const int32_t* n_tiles;
+  uint8_t* h_codes;      // [tiles * 128, I / 2]
+  uint8_t* h_scales;
+  int32_t* status;
+};
+
+bool mx4_valid(const qsm_mx4* w);
+qsm_status launch_grouped(const GemmParams& p, int mode, cudaStream_t stream);
+
+}  // namespace mx4
+}  // namespace qsm

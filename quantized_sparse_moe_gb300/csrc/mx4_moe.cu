@@ -1,0 +1,440 @@
+// The MoE layer with MXFP4 weights: routing and grouping as in the other
+// paths, then the expert products in one of two ways, and the combine
+//   y[t] = g[t] o_shared(t) + sum_j w[t, j] o(t, j)      (j ascending).
+//
+// QSM_ACTS_BF16 (few tokens): gate_up + SwiGLU and down by the streaming
+// kernel (mx4_stream.cu) over slots of up to 8 tokens of an expert, with the
+// activations unrounded; h and o are fp32.  Bound by the touched weights.
+//
+// QSM_ACTS_MX4 (many tokens): the token rows are quantized once and written
+// to their places in the grouped order, each expert's rows padded to blocks
+// of 128 (so that every block starts a scale tile); one grouped product
+// forms h, quantized in its epilogue, and a second one o, in fp16 scaled by
+// 1/16 (11 bits against the 8 of the bf16 result).
+//
+// Every assignment's output is written once and the combine adds them in a
+// fixed order, instead of reductions into y: the result does not depend on
+// timing, and nothing has to be zeroed.
+#include "mx4_gemm.cuh"
+#include "mx4_stream.cuh"
+
+namespace qsm {
+namespace mx4 {
+namespace {
+
+constexpr float kOutScaleInv = 16.0f;
+constexpr int kPrepThreads = 256;
+constexpr int kPrepTiles = 4;  // column tiles per warp and token
+constexpr int kCombThreads = 128;
+constexpr int kMaxK = 32;
+
+// Exclusive prefix sums over the experts of their blocks of 128 rows, into
+// start[0 .. E - 1] (shared memory).
+__device__ __forceinline__ void block_starts(const int32_t* counts, int E, int* start) {
+  __shared__ int warp_tot[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  int base = 0;
+  for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+    const int e = e0 + tid;
+    const int v = e < E ? (__ldcg(counts + e) + 127) >> 7 : 0;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) warp_tot[warp] = incl;
+    __syncthreads();
+    int before = base, all = base;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) before += warp_tot[w];
+      all += warp_tot[w];
+    }
+    if (e < E) start[e] = before + incl - v;
+    base = all;
+    __syncthreads();
+  }
+}
+
+// The tokens' rows in MXFP4, at every place where the grouped products read
+// them: row t (shared expert), and for assignment (t, j) row
+//   128 (shared_tiles + blocks of the experts before) + its rank in the expert,
+// kept in pos[t k + j] for the combine (-1: no valid expert).  One warp takes
+// kPrepTiles column tiles of a token, 16 lanes to a tile: x is read once and
+// its codes written k + 1 times.
+__global__ void __launch_bounds__(kPrepThreads)
+mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
+                   const int32_t* __restrict__ topk_idx, const int32_t* __restrict__ inv_perm,
+                   const int32_t* __restrict__ counts, const int32_t* __restrict__ offsets,
+                   int shared_tiles, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                   int32_t* __restrict__ pos, int32_t* status) {
+  extern __shared__ int start[];  // [E]
+  pdl_wait();
+  pdl_launch_dependents();
+  block_starts(counts, E, start);
+  const int lane = threadIdx.x & 31, l16 = lane & 15;
+  const int cts = col_tiles(H), cgs = (cts + kPrepTiles - 1) / kPrepTiles;
+  const long long units = (long long)T * cgs, stride = (long long)gridDim.x * (kPrepThreads / 32);
+  bool bad = false;
+  for (long long u = (long long)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5); u < units; u += stride) {
+    const int t = (int)(u / cgs), cg = (int)(u % cgs);
+    int dst = -1;  // lane j: the row of assignment (t, j)
+    if (lane < k) {
+      const int e = __ldcg(topk_idx + (size_t)t * k + lane);
+      const int at = __ldcg(inv_perm + (size_t)t * k + lane);
+      if (at >= 0 && e >= 0 && e < E)
+        dst = 128 * (shared_tiles + start[e]) + at - __ldcg(offsets + e);
+      if (cg == 0) pos[(size_t)t * k + lane] = dst;
+    }
+    uint4 raw[kPrepTiles / 2];
+#pragma unroll
+    for (int z = 0; z < kPrepTiles / 2; ++z) {
+      const int c = (cg * kPrepTiles + 2 * z + (lane >> 4)) * kTileCols + 8 * l16;
+      raw[z] = c < H ? __ldcg(reinterpret_cast<const uint4*>(x + (size_t)t * H + c))
+                     : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int z = 0; z < kPrepTiles / 2; ++z) {
+      const int ct = cg * kPrepTiles + 2 * z + (lane >> 4), c = ct * kTileCols + 8 * l16;
+      const uint32_t w[4] = {raw[z].x, raw[z].y, raw[z].z, raw[z].w};
+      float v[8];
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+        m = max(m, max(__float_as_uint(v[2 * i]) & 0x7fffffffu, __float_as_uint(v[2 * i + 1]) & 0x7fffffffu));
+      }
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const uint32_t s = scale_of(m);
+      uint32_t sw = s << (8 * (l16 >> 2));
+      sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
+      sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
+      if (s == 255u) bad = true;
+      const float inv = s == 255u ? 0.f : inv_scale(s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= inv;
+      const uint32_t word = f32x8_to_e2m1x8(v);
+      for (int j = -1; j < k; ++j) {
+        const int r = j < 0 ? t : __shfl_sync(0xffffffffu, dst, j);
+        if (r < 0 || c >= H) continue;
+        *reinterpret_cast<uint32_t*>(codes + ((size_t)r * H + c) / 2) = word;
+        if (l16 == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(r, ct, cts)) = sw;
+      }
+    }
+  }
+  if (bad) set_status(status, QSM_DEV_NONFINITE);
+}
+
+// y[t] from the shared expert's output row and those of the token's
+// assignments.  HALF: o holds fp16 of 1/16, rows pos[t k + j] and t; else
+// fp32, rows inv_perm[t k + j] and T k + t.  A CTA takes 4 columns per
+// thread of one token.
+template <bool HALF>
+__global__ void __launch_bounds__(kCombThreads)
+mx4_combine_kernel(const void* __restrict__ o, const int32_t* __restrict__ at,
+                   const float* __restrict__ topk_w, const uint16_t* __restrict__ x,
+                   const float* __restrict__ sgate, int T, int k, int H,
+                   uint16_t* __restrict__ y, float* __restrict__ y32) {
+  __shared__ int rows[kMaxK];
+  __shared__ float wts[kMaxK], red[kCombThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int per = (H / 4 + kCombThreads - 1) / kCombThreads;  // CTAs per token
+  const int t = blockIdx.x / per, tid = threadIdx.x;
+  if (tid < k) {
+    rows[tid] = __ldcg(at + (size_t)t * k + tid);
+    wts[tid] = __ldcg(topk_w + (size_t)t * k + tid);
+  }
+  float g = 1.f;
+  if (sgate) {
+    float z = 0.f;
+    for (int c = tid; c < H; c += kCombThreads)
+      z = fmaf(__uint_as_float((uint32_t)__ldg(x + (size_t)t * H + c) << 16), __ldg(sgate + c), z);
+    z = warp_sum(z);
+    if ((tid & 31) == 0) red[tid >> 5] = z;
+  }
+  __syncthreads();
+  if (sgate) {
+    float z = 0.f;
+#pragma unroll
+    for (int w = 0; w < kCombThreads / 32; ++w) z += red[w];
+    g = 1.0f / (1.0f + __expf(-z));
+  }
+  const int c = (blockIdx.x % per * kCombThreads + tid) * 4;
+  if (c >= H) return;
+  auto load = [&](size_t row) {
+    float4 v;
+    if (HALF) {
+      const uint2 h = __ldcg(reinterpret_cast<const uint2*>(static_cast<const __half*>(o) + row * H + c));
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
+      v = make_float4(a.x, a.y, b.x, b.y);
+    } else {
+      v = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(o) + row * H + c));
+    }
+    return v;
+  };
+  float4 s = load(HALF ? (size_t)t : (size_t)T * k + t);
+  s = make_float4(s.x * g, s.y * g, s.z * g, s.w * g);
+  for (int j0 = 0; j0 < k; j0 += 8) {  // eight rows' loads in flight
+    float4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < k && rows[j0 + j] >= 0) v[j] = load((size_t)rows[j0 + j]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j0 + j >= k || rows[j0 + j] < 0) continue;
+      const float w = wts[j0 + j];
+      s.x = fmaf(w, v[j].x, s.x);
+      s.y = fmaf(w, v[j].y, s.y);
+      s.z = fmaf(w, v[j].z, s.z);
+      s.w = fmaf(w, v[j].w, s.w);
+    }
+  }
+  if (HALF) s = make_float4(s.x * kOutScaleInv, s.y * kOutScaleInv, s.z * kOutScaleInv, s.w * kOutScaleInv);
+  const size_t off = (size_t)t * H + c;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+  *reinterpret_cast<uint2*>(y + off) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                  *reinterpret_cast<const uint32_t*>(&hi));
+  if (y32) *reinterpret_cast<float4*>(y32 + off) = s;
+}
+
+// ---------------------------------------------------------------------- host
+
+inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// Everything a call keeps in its workspace.
+struct Plan {
+  int acts, tile_rows, shared_tiles, max_tiles;
+  bool fused_route;         // routing and grouping in one launch
+  StreamParams gu, dn;      // QSM_ACTS_BF16: geometry
+  size_t rows;              // rows of h and o (BF16: T k + T; MX4: padded)
+  size_t route, counts, offsets, perm, inv_perm, tile_map, n_tiles;
+  size_t xc, xs, hc, hs, h, o, pos, total;
+};
+
+bool shape_ok(const qsm_mx4_layer* L) {
+  return L && L->H >= 128 && L->H % 128 == 0 && L->H <= 16384 && L->I >= 128 && L->I % 128 == 0 &&
+         L->I <= 16384 && L->E >= 1 && L->E <= 1024 && L->k >= 1 && L->k <= L->E && L->k <= kMaxK;
+}
+
+bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
+  if (!shape_ok(L) || T < 1 || (acts != QSM_ACTS_BF16 && acts != QSM_ACTS_MX4)) return false;
+  if ((long long)T * L->k > (1 << 24)) return false;
+  const int H = L->H, I = L->I, E = L->E, k = L->k;
+  Plan p = {};
+  p.acts = acts;
+  if (acts == QSM_ACTS_BF16) {
+    if (T > QSM_MX4_MOE_MAX_ROWS) return false;
+    const int touched = (long long)T * k < E ? T * k : E;
+    bool fit = false;
+    for (int tok = 8; tok >= 1 && !fit; tok /= 2) {
+      const int slots = touched + (T + tok - 1) / tok;
+      p.gu.K = H;
+      p.gu.N = 2 * I;
+      p.dn.K = I;
+      p.dn.N = H;
+      fit = plan_rows(&p.gu, kRowsGateUp, slots * (I / 128), tok, sm_count()) &&
+            plan_rows(&p.dn, kRowsDown, slots * (H / 128), tok, sm_count());
+      p.tile_rows = tok;
+    }
+    if (!fit) return false;
+  } else {
+    p.tile_rows = 128;
+  }
+  p.shared_tiles = (T + p.tile_rows - 1) / p.tile_rows;
+  p.max_tiles = moe_group_max_tiles(T, k, E, p.tile_rows);
+  p.fused_route = T <= 8 && E <= 256;
+  p.rows = acts == QSM_ACTS_BF16 ? (size_t)T * k + T : (size_t)(p.shared_tiles + p.max_tiles) * 128;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += up256(bytes);
+    return at;
+  };
+  const size_t A = (size_t)T * k;
+  p.route = take(moe_route_workspace_bytes(T, H, E));
+  p.counts = take((size_t)E * 4);
+  p.offsets = take((size_t)(E + 1) * 4);
+  p.perm = take(A * 4);
+  p.inv_perm = take(A * 4);
+  p.tile_map = take((size_t)p.max_tiles * 8);
+  p.n_tiles = take(4);
+  if (acts == QSM_ACTS_BF16) {
+    p.h = take(p.rows * I * 4);
+    p.o = take(p.rows * H * 4);
+  } else {
+    p.xc = take(p.rows * H / 2);
+    p.xs = take(mx4_scale_bytes((int)p.rows, H));
+    p.hc = take(p.rows * I / 2);
+    p.hs = take(mx4_scale_bytes((int)p.rows, I));
+    p.o = take(p.rows * H * 2);
+    p.pos = take(A * 4);
+  }
+  p.total = off;
+  *out = p;
+  return true;
+}
+
+bool weights_ok(const qsm_mx4& w, int experts, int rows, int cols) {
+  return mx4_valid(&w) && w.experts == experts && w.rows == rows && w.cols == cols;
+}
+
+qsm_status few_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x, int T,
+                      const qsm_grouping& g, char* ws, int32_t* status, cudaStream_t stream) {
+  const int H = L->H, I = L->I, E = L->E;
+  StreamParams p = pl.gu;
+  if (!make_codes_map(&p.w, L->gate_up.codes, (uint64_t)E * 2 * I, H, 128) ||
+      !make_codes_map(&p.w_sh, L->shared_gate_up.codes, (uint64_t)2 * I, H, 128))
+    return QSM_ERR_CUDA;
+  p.w_scales = L->gate_up.scales;
+  p.w_scales_sh = L->shared_gate_up.scales;
+  p.ntiles = I / 128;
+  p.T = T;
+  p.k = L->k;
+  p.I = I;
+  p.H = H;
+  p.perm = g.perm;
+  p.offsets = g.offsets;
+  p.tile_map = g.tile_map;
+  p.n_tiles = g.n_tiles;
+  p.shared_tiles = pl.shared_tiles;
+  p.x = x;
+  p.ldx = H;
+  p.h = reinterpret_cast<float*>(ws + pl.h);
+  p.o = reinterpret_cast<float*>(ws + pl.o);
+  p.status = status;
+  StreamParams d = pl.dn;
+  if (!make_codes_map(&d.w, L->down.codes, (uint64_t)E * H, I, 128) ||
+      !make_codes_map(&d.w_sh, L->shared_down.codes, (uint64_t)H, I, 128))
+    return QSM_ERR_CUDA;
+  d.w_scales = L->down.scales;
+  d.w_scales_sh = L->shared_down.scales;
+  d.ntiles = H / 128;
+  d.T = T;
+  d.k = L->k;
+  d.I = I;
+  d.H = H;
+  d.perm = g.perm;
+  d.offsets = g.offsets;
+  d.tile_map = g.tile_map;
+  d.n_tiles = g.n_tiles;
+  d.shared_tiles = pl.shared_tiles;
+  d.h = p.h;
+  d.o = p.o;
+  d.status = status;
+  const int slots = pl.shared_tiles + pl.max_tiles;
+  const qsm_status st = launch_rows(p, kRowsGateUp, slots * p.ntiles, stream);
+  return st != QSM_OK ? st : launch_rows(d, kRowsDown, slots * d.ntiles, stream);
+}
+
+qsm_status many_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x, int T,
+                       const int32_t* topk_idx, const qsm_grouping& g, char* ws, int32_t* status,
+                       cudaStream_t stream) {
+  const int H = L->H, I = L->I, E = L->E;
+  uint8_t* xc = reinterpret_cast<uint8_t*>(ws + pl.xc);
+  uint8_t* xs = reinterpret_cast<uint8_t*>(ws + pl.xs);
+  const long long units = (long long)T * ((col_tiles(H) + kPrepTiles - 1) / kPrepTiles);
+  const long long ctas = (units + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
+  const int grid = (int)(ctas < 8ll * sm_count() ? ctas : 8ll * sm_count());
+  QSM_CUDA_TRY(launch_pdl(mx4_scatter_kernel, dim3(grid), dim3(kPrepThreads), (size_t)E * 4, stream, x,
+                          T, (int)L->k, H, E, topk_idx, (const int32_t*)g.inv_perm,
+                          (const int32_t*)g.counts, (const int32_t*)g.offsets, pl.shared_tiles, xc, xs,
+                          reinterpret_cast<int32_t*>(ws + pl.pos), status));
+  GemmParams p = {};
+  bool ok = make_codes_map(&p.a, xc, pl.rows, H, 128) &&
+            make_codes_map(&p.w, L->gate_up.codes, (uint64_t)E * 2 * I, H, 128) &&
+            make_codes_map(&p.w_sh, L->shared_gate_up.codes, (uint64_t)2 * I, H, 128);
+  p.a_scales = xs;
+  p.w_scales = L->gate_up.scales;
+  p.w_scales_sh = L->shared_gate_up.scales;
+  p.N = 2 * I;
+  p.K = H;
+  p.nsub = I / 128;
+  p.T = T;
+  p.I = I;
+  p.shared_tiles = pl.shared_tiles;
+  p.offsets = g.offsets;
+  p.tile_map = g.tile_map;
+  p.n_tiles = g.n_tiles;
+  p.h_codes = reinterpret_cast<uint8_t*>(ws + pl.hc);
+  p.h_scales = reinterpret_cast<uint8_t*>(ws + pl.hs);
+  p.status = status;
+  GemmParams d = p;
+  ok &= make_codes_map(&d.a, p.h_codes, pl.rows, I, 128) &&
+        make_codes_map(&d.w, L->down.codes, (uint64_t)E * H, I, 256) &&
+        make_codes_map(&d.w_sh, L->shared_down.codes, (uint64_t)H, I, 256);
+  if (!ok) return QSM_ERR_CUDA;
+  d.a_scales = p.h_scales;
+  d.w_scales = L->down.scales;
+  d.w_scales_sh = L->shared_down.scales;
+  d.N = H;
+  d.K = I;
+  d.nsub = (H + 255) / 256;
+  d.y = ws + pl.o;
+  d.ldy = H;
+  d.vec = 1;
+  const qsm_status st = launch_grouped(p, kGateUp, stream);
+  return st != QSM_OK ? st : launch_grouped(d, kDown, stream);
+}
+
+}  // namespace
+}  // namespace mx4
+}  // namespace qsm
+
+extern "C" size_t moe_mx4_workspace_bytes(const qsm_mx4_layer* L, int32_t T, int32_t acts) {
+  qsm::mx4::Plan p;
+  return qsm::mx4::plan_of(L, T, acts, &p) ? p.total : 0;
+}
+
+extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x, int32_t T,
+                                      int32_t acts, const float* w_router, const float* logit_bias,
+                                      int32_t flags, int32_t* topk_idx, float* topk_w, uint16_t* y,
+                                      float* y_f32, void* workspace, size_t workspace_bytes,
+                                      int32_t* dev_status, cudaStream_t stream) {
+  using namespace qsm;
+  using namespace qsm::mx4;
+  if (!L || T < 0 || (acts != QSM_ACTS_BF16 && acts != QSM_ACTS_MX4) ||
+      (flags & ~(QSM_ROUTE_RENORMALIZE | QSM_ROUTE_BIAS_SELECT_ONLY)))
+    return QSM_ERR_INVALID_ARGUMENT;
+  if (!shape_ok(L)) return QSM_ERR_UNSUPPORTED;
+  if (T == 0) return QSM_OK;
+  if (!x || !w_router || !topk_idx || !topk_w || !y || !workspace || !dev_status || !aligned16(x) ||
+      !aligned16(w_router) || !aligned16(workspace) || !aligned16(topk_idx) || !aligned16(topk_w) ||
+      !aligned16(y) || (y_f32 && !aligned16(y_f32)) || !aligned4(dev_status) ||
+      (logit_bias && !aligned4(logit_bias)) || (L->shared_gate && !aligned16(L->shared_gate)))
+    return QSM_ERR_INVALID_ARGUMENT;
+  if (!weights_ok(L->gate_up, L->E, 2 * L->I, L->H) || !weights_ok(L->down, L->E, L->H, L->I) ||
+      !weights_ok(L->shared_gate_up, 1, 2 * L->I, L->H) || !weights_ok(L->shared_down, 1, L->H, L->I))
+    return QSM_ERR_INVALID_ARGUMENT;
+  Plan p;
+  if (!plan_of(L, T, acts, &p)) return QSM_ERR_UNSUPPORTED;
+  if (workspace_bytes < p.total) return QSM_ERR_WORKSPACE_TOO_SMALL;
+  char* ws = static_cast<char*>(workspace);
+  auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
+  const qsm_grouping g = {i32(p.counts),   i32(p.offsets), i32(p.perm), i32(p.inv_perm),
+                          i32(p.tile_map), i32(p.n_tiles), p.tile_rows, p.max_tiles};
+  const size_t route_bytes = p.counts - p.route;
+  qsm_status st;
+  if (p.fused_route) {
+    st = moe_route_group(x, w_router, logit_bias, T, L->H, L->E, L->k, flags, topk_idx, topk_w, &g,
+                         ws + p.route, route_bytes, dev_status, stream);
+  } else {
+    st = moe_route(x, w_router, logit_bias, T, L->H, L->E, L->k, flags, topk_idx, topk_w, ws + p.route,
+                   route_bytes, dev_status, stream);
+    if (st == QSM_OK) st = moe_group_tokens(topk_idx, T, L->k, L->E, &g, dev_status, stream);
+  }
+  if (st != QSM_OK) return st;
+  st = acts == QSM_ACTS_BF16 ? few_tokens(L, p, x, T, g, ws, dev_status, stream)
+                             : many_tokens(L, p, x, T, topk_idx, g, ws, dev_status, stream);
+  if (st != QSM_OK) return st;
+  const bool half = acts == QSM_ACTS_MX4;
+  const dim3 grid((unsigned)T * ((L->H / 4 + kCombThreads - 1) / kCombThreads));
+  auto* comb = half ? mx4_combine_kernel<true> : mx4_combine_kernel<false>;
+  QSM_CUDA_TRY(launch_pdl(comb, grid, dim3(kCombThreads), 0, stream, (const void*)(ws + p.o),
+                          (const int32_t*)i32(half ? p.pos : p.inv_perm), (const float*)topk_w, x,
+                          L->shared_gate, T, (int)L->k, (int)L->H, y, y_f32));
+  return QSM_OK;
+}

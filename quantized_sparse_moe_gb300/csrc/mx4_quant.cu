@@ -1,0 +1,247 @@
+// Quantization to MXFP4 and back (layout in mx4_common.cuh).
+//
+//   s[r, b]    = 2^(floor(log2 max|x[r, 32b .. 32b+31]|) - 2), at least 2^-127
+//   code[r, c] = the e2m1 value nearest to x[r, c] / s[r, c / 32], ties to
+//                the even code, magnitudes over 6 become 6
+//   y[r, c]    = code[r, c] * s[r, c / 32]
+//
+// Both are bound by memory: x once in, 4.25 bits a value out, and the
+// reverse.  Sixteen lanes take the 128 columns of one scale tile row, eight
+// columns each: their loads are 16 contiguous bytes (32 for fp32), the codes
+// of a lane one 32-bit word, the four scales of the row in the tile one more,
+// and a block's maximum is two shuffles.  Each thread has four such rows in
+// flight.  The scale is a power of two, so the division is exact and the one
+// rounding is the one to the code.
+#include "mx4_common.cuh"
+
+namespace qsm {
+namespace mx4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+
+// Eight columns of a row as raw words (16 or 32 bytes).
+template <int DT>
+struct Raw {
+  uint4 a, b;
+};
+template <int DT>
+__device__ __forceinline__ Raw<DT> load8(const void* x, size_t i) {
+  Raw<DT> r;
+  if (DT == QSM_FP32) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + i);
+    r.a = __ldcg(p);
+    r.b = __ldcg(p + 1);
+  } else {
+    r.a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i));
+    r.b = make_uint4(0u, 0u, 0u, 0u);
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void widen(const Raw<DT>& r, float (&v)[8]) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  if (DT == QSM_FP32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+  } else if (DT == QSM_BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+mx4_quantize_kernel(const void* __restrict__ x, size_t row_stride, int rows, int cols, int cts,
+                    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                    int32_t* status) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int l16 = threadIdx.x & 15;
+  const size_t units = (size_t)row_tiles(rows) * kTileRows * cts;  // (row, column tile)
+  const size_t stride = (size_t)gridDim.x * (kThreads / 16);
+  bool bad = false;
+  for (size_t u0 = (size_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16; u0 < units;
+       u0 += kUnroll * stride) {
+    Raw<DT> raw[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const size_t u = u0 + k * stride;
+      const int r = (int)(u / cts), c = (int)(u % cts) * kTileCols + 8 * l16;
+      raw[k].a = raw[k].b = make_uint4(0u, 0u, 0u, 0u);
+      if (u < units && r < rows && c < cols) raw[k] = load8<DT>(x, (size_t)r * row_stride + c);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const size_t u = u0 + k * stride;
+      const int r = (int)(u / cts), ct = (int)(u % cts), c = ct * kTileCols + 8 * l16;
+      float v[8];
+      widen<DT>(raw[k], v);
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const uint32_t s = scale_of(m);
+      // the row's four scales in one word, in its first lane
+      uint32_t sw = s << (8 * (l16 >> 2));
+      sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
+      sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
+      if (u >= units) continue;
+      if (l16 == 0)
+        *reinterpret_cast<uint32_t*>(scales + scale_word(r, ct, cts)) = sw;
+      if (r >= rows || c >= cols) continue;
+      if (s == 255u) bad = true;
+      const float inv = s == 255u ? 0.f : inv_scale(s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= inv;
+      *reinterpret_cast<uint32_t*>(codes + ((size_t)r * cols + c) / 2) = f32x8_to_e2m1x8(v);
+    }
+  }
+  if (bad) set_status(status, QSM_DEV_NONFINITE);
+}
+
+// An e2m1 code as fp16 bits, without the factor 2^14: sign, exponent and
+// mantissa keep their order, subnormals included.
+__device__ __forceinline__ float code_value(uint32_t n) {
+  const uint32_t h = ((n & 8u) << 12) | ((n & 7u) << 9);
+  return __half2float(__ushort_as_half((unsigned short)h)) * 16384.f;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                      int experts, int rows, int cols, int cts, size_t scale_bytes,
+                      void* __restrict__ y) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int l16 = threadIdx.x & 15;
+  const size_t units = (size_t)experts * rows * cts;
+  const size_t stride = (size_t)gridDim.x * (kThreads / 16);
+  for (size_t u0 = (size_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16; u0 < units;
+       u0 += kUnroll * stride) {
+    uint32_t w[kUnroll], sw[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const size_t u = u0 + k * stride;
+      w[k] = sw[k] = 0u;
+      if (u >= units) continue;
+      const size_t row = u / cts;
+      const int ct = (int)(u % cts), c = ct * kTileCols + 8 * l16;
+      const int e = (int)(row / rows), r = (int)(row % rows);
+      if (c >= cols) continue;
+      w[k] = __ldcg(reinterpret_cast<const uint32_t*>(codes + (row * cols + c) / 2));
+      sw[k] = __ldcg(reinterpret_cast<const uint32_t*>(scales + e * scale_bytes +
+                                                       scale_word(r, ct, cts)));
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const size_t u = u0 + k * stride;
+      if (u >= units) continue;
+      const size_t row = u / cts;
+      const int c = (int)(u % cts) * kTileCols + 8 * l16;
+      if (c >= cols) continue;
+      const float s = scale_value((sw[k] >> (8 * (l16 >> 2))) & 255u);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = code_value((w[k] >> (4 * i)) & 15u) * s;
+      const size_t o = row * cols + c;
+      if (DT == QSM_FP32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(y) + o);
+        p[0] = make_float4(v[0], v[1], v[2], v[3]);
+        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (DT == QSM_BF16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            q[i] = *reinterpret_cast<const uint32_t*>(&b);
+          } else {
+            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            q[i] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + o) = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+    }
+  }
+}
+
+// CTAs for `units` groups of 16 lanes, each thread taking kUnroll of them:
+// enough for one pass, at most eight CTAs (all that fit) per SM.
+int grid_for(size_t units) {
+  const size_t per = (kThreads / 16) * (size_t)kUnroll;
+  const size_t need = (units + per - 1) / per, most = (size_t)sm_count() * 8;
+  return (int)(need < 1 ? 1 : need < most ? need : most);
+}
+
+bool valid_dtype(int dt) { return dt == QSM_BF16 || dt == QSM_FP16 || dt == QSM_FP32; }
+
+}  // namespace
+
+// Whether w describes a matrix that the kernels can read: `experts` and the
+// sizes positive, cols a multiple of 32, both arrays 16-byte aligned.
+bool mx4_valid(const qsm_mx4* w) {
+  return w && w->experts >= 1 && w->rows >= 1 && w->cols >= kBlock && w->cols % kBlock == 0 &&
+         w->codes && w->scales && aligned16(w->codes) && aligned16(w->scales);
+}
+
+}  // namespace mx4
+}  // namespace qsm
+
+extern "C" size_t mx4_scale_bytes(int32_t rows, int32_t cols) {
+  if (rows < 0 || cols < 0) return 0;
+  return (size_t)qsm::mx4::row_tiles(rows) * qsm::mx4::col_tiles(cols) * qsm::mx4::kTileBytes;
+}
+
+extern "C" qsm_status mx4_quantize(const void* x, int32_t dtype, int64_t row_stride, int32_t rows,
+                                   int32_t cols, uint8_t* codes, uint8_t* scales,
+                                   int32_t* dev_status, cudaStream_t stream) {
+  using namespace qsm;
+  using namespace qsm::mx4;
+  if (!valid_dtype(dtype) || rows < 0 || cols < kBlock || cols % kBlock || row_stride < cols ||
+      row_stride % 8)
+    return QSM_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return QSM_OK;
+  if (!x || !codes || !scales || !dev_status || !aligned16(x) || !aligned16(codes) ||
+      !aligned16(scales) || !aligned4(dev_status))
+    return QSM_ERR_INVALID_ARGUMENT;
+  const int cts = col_tiles(cols);
+  const dim3 grid(grid_for((size_t)row_tiles(rows) * kTileRows * cts));
+  auto* kernel = dtype == QSM_BF16   ? mx4_quantize_kernel<QSM_BF16>
+                 : dtype == QSM_FP16 ? mx4_quantize_kernel<QSM_FP16>
+                                     : mx4_quantize_kernel<QSM_FP32>;
+  QSM_CUDA_TRY(launch_pdl(kernel, grid, dim3(kThreads), 0, stream, x, (size_t)row_stride,
+                          (int)rows, (int)cols, cts, codes, scales, dev_status));
+  return QSM_OK;
+}
+
+extern "C" qsm_status mx4_dequantize(const qsm_mx4* a, int32_t dtype, void* y,
+                                     cudaStream_t stream) {
+  using namespace qsm;
+  using namespace qsm::mx4;
+  if (!a || !valid_dtype(dtype)) return QSM_ERR_INVALID_ARGUMENT;
+  if (a->rows == 0 && a->experts >= 1) return QSM_OK;
+  if (!mx4_valid(a) || !y || !aligned16(y)) return QSM_ERR_INVALID_ARGUMENT;
+  const int cts = col_tiles(a->cols);
+  const dim3 grid(grid_for((size_t)a->experts * a->rows * cts));
+  auto* kernel = dtype == QSM_BF16   ? mx4_dequantize_kernel<QSM_BF16>
+                 : dtype == QSM_FP16 ? mx4_dequantize_kernel<QSM_FP16>
+                                     : mx4_dequantize_kernel<QSM_FP32>;
+  QSM_CUDA_TRY(launch_pdl(kernel, grid, dim3(kThreads), 0, stream, a->codes, a->scales,
+                          (int)a->experts, (int)a->rows, (int)a->cols, cts,
+                          mx4_scale_bytes(a->rows, a->cols), y));
+  return QSM_OK;
+}

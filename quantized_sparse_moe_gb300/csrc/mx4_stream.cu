@@ -1,0 +1,575 @@
+// A few rows of 16-bit (or 32-bit) activations times MXFP4 weights, on the
+// block-scaled tensor cores, with the weights streamed once and never
+// expanded.
+//
+//   y[t, n] = sum_c x[t, c] w[n, c]
+//
+// The tensor cores multiply e2m1 by e2m1 only, so the activations are
+// written as sums of e2m1 matrices.  A block of 32 values of a row becomes
+// integers X = round(x 2^(21 - E)), E the exponent of its largest magnitude
+// (|X| <= 2^22: 2^-23 of that magnitude is kept, more than a bf16 holds), and
+// X eight digits of base 8 in -4..3:
+//   X = sum_i d_i 8^i,   x = sum_i (d_i / 2) 2^(E - 20 + 3 i)
+// d_i / 2 is one of 0, +-0.5, +-1, +-1.5, -2: an e2m1 value, and the power of
+// two is its block's scale.  A row of x is thus eight rows of an MXFP4
+// matrix, the eight results are added in fp32, and every product is exact.
+// With the digits of plus the bias sum_i 4 8^i taken as unsigned, they are
+// bit fields.
+//
+// The weights are the MMA's 128 rows and the digit rows its N = 8 per row of
+// x: an MMA of 128 x 8..64 x 64 costs what its weight operand takes to read
+// from shared memory (4 KB, 32 cycles), so the eightfold width is free up to
+// eight rows, and up to 32 rows the kernel stays bound by HBM (a quarter of
+// a byte per weight and cycle).  A dequantising kernel needs at least one
+// integer instruction per weight, which is what bounds the affine-4 kernels
+// of decode_stream.cu.
+//
+// Work items are (slot, tile of 128 rows of w); a slot is up to `tok` rows
+// of x (of one expert's).  A cluster of `cs` CTAs works on an item together,
+// each on its part of K, and exchanges partial sums through distributed
+// shared memory: CTA q adds up and writes rows 128 q / cs .. of the tile, in
+// CTA order.  Roles in a CTA: warp 0 loads (stages of 256 columns: codes by
+// TMA with the 128-byte swizzle, scale tiles by bulk copy), warp 1 issues the
+// scale copies and MMAs, warps 4-7 are the epilogue, warps 8-15 make the
+// digits of the next slot while the current one is multiplied.
+#include <mutex>
+#include <vector>
+
+#include "mx4_stream.cuh"
+
+namespace qsm {
+namespace mx4 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kConvWarps = 8;
+constexpr int kMaxStages = 12;
+constexpr int kSmemMax = 225 * 1024;
+constexpr int kMaxSplit = 8;  // CTAs per cluster
+constexpr int kDigits = 8;
+constexpr uint32_t kDigitBias = 9586980u;  // sum of 4 * 8^i, i < 8
+
+template <int MODE>
+constexpr int mats() { return MODE == kRowsGateUp ? 2 : 1; }  // row tiles of w per item
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Arrive on the mbarrier at cluster address `addr`; this thread's (and,
+// through a preceding __syncwarp, its warp's) stores before it are visible
+// to whoever waits for the phase.
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                             int32_t* status) {
+  for (uint32_t i = 0; i < kWaitIters; ++i) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if (*abort_flag) return false;
+  }
+  *abort_flag = 1;
+  set_status(status, QSM_DEV_TIMEOUT);
+  return false;
+}
+
+struct Slot {
+  int e;     // expert, -1: shared expert or dense
+  int row0;  // first row of x (dense, shared) or first sorted row (routed)
+  int cnt;
+};
+
+template <int MODE>
+__device__ __forceinline__ Slot slot_of(const StreamParams& p, int s) {
+  Slot r;
+  if (MODE == kRows || s < p.shared_tiles) {
+    r.e = -1;
+    r.row0 = s * p.tok;
+    r.cnt = min(p.tok, p.T - r.row0);
+  } else {
+    const int2 te = __ldcg(reinterpret_cast<const int2*>(p.tile_map) + (s - p.shared_tiles));
+    r.e = te.x;
+    r.row0 = te.y;
+    r.cnt = min(p.tok, __ldcg(p.offsets + te.x + 1) - te.y);
+  }
+  return r;
+}
+
+// Eight consecutive values of row i of the slot, from column c (zeros past K).
+template <int MODE>
+__device__ __forceinline__ void load_acts(const StreamParams& p, const Slot& s, int i, int c,
+                                          float (&v)[8]) {
+  if (c >= p.K) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    return;
+  }
+  if (MODE == kRowsDown) {
+    const size_t row = (size_t)(s.e < 0 ? p.T * p.k : 0) + s.row0 + i;
+    const float4* src = reinterpret_cast<const float4*>(p.h + row * p.I + c);
+    const float4 a = __ldcg(src), b = __ldcg(src + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    int t = s.row0 + i;
+    if (MODE == kRowsGateUp && s.e >= 0) t = __ldcg(p.perm + t) / p.k;
+    const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p.x + (size_t)t * p.ldx + c));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo(w[j]);
+      v[2 * j + 1] = bf16_hi(w[j]);
+    }
+  }
+}
+
+// The eight digit planes of eight values as e2m1 codes (one word each), and
+// the scale byte of plane 0 (plane i: + 3 i; 255: not a number).  Lanes 4 j
+// .. 4 j + 3 hold the four quarters of a block.
+__device__ __forceinline__ uint32_t digits_of(const float (&v)[8], uint32_t (&plane)[kDigits]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  // E, at least -105 so that 2^(21 - E) is finite; 127 and up (2^127,
+  // infinities, NaN) have no scale for their top digit
+  const int e = max((int)(m >> 23) - 127, -105);
+  if (e >= 127) {
+#pragma unroll
+    for (int i = 0; i < kDigits; ++i) plane[i] = 0u;
+    return 255u;
+  }
+  const float f = __uint_as_float((uint32_t)(21 - e + 127) << 23);
+  uint32_t y[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = (uint32_t)__float2int_rn(v[j] * f) + kDigitBias;
+#pragma unroll
+  for (int i = 0; i < kDigits; ++i) {
+    uint32_t w = 0;  // eight unsigned digits 0..7, one per nibble
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int sh = 3 * i - 4 * j;
+      w |= (sh >= 0 ? y[j] >> (sh & 31) : y[j] << (-sh & 31)) & (7u << (4 * j));
+    }
+    // digit - 4 as a code: 4..7 -> 0..3, 0..3 -> sign and magnitude 4 - digit
+    const uint32_t low = w & 0x33333333u, neg = ~w & 0x44444444u;
+    const uint32_t mask = (neg << 2) - (neg >> 2);
+    plane[i] = (mask & (0xCCCCCCCCu - low)) | (~mask & low);
+  }
+  return (uint32_t)(e - 20 + 127);
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_constant__ StreamParams p) {
+  constexpr int NM = mats<MODE>();
+  constexpr int kStage = NM * (128 * 128 + 2 * kTileBytes);
+  extern __shared__ unsigned char smem_raw[];
+  // the same offset in every CTA of a cluster, so that a shared-memory
+  // address of this CTA maps to the same place of the others
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], dig_full[2], dig_empty[2],
+      acc_full[2], acc_empty[2], part_full[2], part_empty[2], done;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  volatile int* abort_p = &abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cs = p.cs, stages = p.stages;
+  const int rank = cs > 1 ? (int)cluster_rank() : 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&dig_full[b], kConvWarps);
+      mbar_init(&dig_empty[b], 1);
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 4);
+      mbar_init(&part_full[b], cs < 4 ? 4 : cs);
+      mbar_init(&part_empty[b], 4 * cs);
+    }
+    mbar_init(&done, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) tc::prefetch_map(&p.w);
+  if (warp == 2) tc::tmem_alloc(&tmem_base, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (cs > 1) cluster_sync_all();
+  const uint32_t tmem = tmem_base;
+
+  pdl_wait();
+  pdl_launch_dependents();
+  const int slots = MODE == kRows ? p.slots : p.shared_tiles + __ldcg(p.n_tiles);
+  // this cluster's contiguous run of items (slot, tile)
+  const long long items = (long long)slots * p.ntiles;
+  const int nclus = gridDim.x / cs, clus = blockIdx.x / cs;
+  const int first = (int)(items * clus / nclus), last = (int)(items * (clus + 1) / nclus);
+  // this CTA's stages of K
+  const int nst = (p.K + kStageK - 1) / kStageK, cts = col_tiles(p.K);
+  const int s0 = nst * rank / cs, s1 = nst * (rank + 1) / cs;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t f = 0;
+      int slot = -1;
+      Slot sl = {};
+      for (int item = first; item < last && !*abort_p; ++item) {
+        const int s = item / p.ntiles, tile = item - s * p.ntiles;
+        if (s != slot) sl = slot_of<MODE>(p, slot = s);
+        const bool sh = MODE != kRows && sl.e < 0;
+        const CUtensorMap* wm = sh ? &p.w_sh : &p.w;
+        const uint8_t* wsc = sh ? p.w_scales_sh : p.w_scales;
+        const int row0 = (sl.e < 0 ? 0 : sl.e * p.N) + tile * 128;
+        bool ok = true;
+        for (int ks = s0; ks < s1; ++ks, ++f) {
+          const int st = f % stages;
+          if (f >= (uint32_t)stages && !wait_or_abort(&empty[st], (f / stages - 1) & 1, abort_p, p.status)) {
+            ok = false;
+            break;
+          }
+          unsigned char* base = smem + st * kStage;
+          const uint32_t sfb = (uint32_t)min(2, cts - 2 * ks) * kTileBytes;
+          mbar_arrive_expect_tx(&full[st], NM * (128 * 128 + sfb));
+#pragma unroll
+          for (int m = 0; m < NM; ++m) {
+            const int row = row0 + m * (p.N / 2);
+            tc::tma_load_2d(base + m * 128 * 128, wm, ks * 128, row, &full[st]);
+            bulk_g2s(base + NM * 128 * 128 + m * 2 * kTileBytes,
+                     wsc + ((size_t)(row >> 7) * cts + 2 * ks) * kTileBytes, sfb, &full[st]);
+          }
+        }
+        if (!ok) break;
+      }
+      // after an abort, let the last copies land before the CTA exits
+      const uint32_t n = f < (uint32_t)stages ? f : (uint32_t)stages;
+      for (uint32_t i = 1; i <= n; ++i)
+        mbar_wait_bounded(&full[(f - i) % stages], ((f - i) / stages) & 1, 1u << 16);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t f = 0;
+      int slot = -1, db = -1, n = 0, ndig = 0;
+      const int sfc = 8 * NM + 8 * p.groups;  // scale columns of one stage
+      const uint32_t sf0 = tmem + p.nacc * NM * p.acc_cols;
+      for (int item = first; item < last && !*abort_p; ++item) {
+        const int j = item - first, ab = j % p.nacc;
+        const int s = item / p.ntiles;
+        bool ok = true;
+        if (s != slot) {  // the next slot's digits; the previous one's are free
+          if (slot >= 0) tc::mma_commit(&dig_empty[db]);
+          slot = s;
+          n = kDigits * slot_of<MODE>(p, s).cnt;
+          db = ndig % p.nb;
+          if (!wait_or_abort(&dig_full[db], (ndig / p.nb) & 1, abort_p, p.status)) break;
+          ++ndig;
+        }
+        if (j >= p.nacc && !wait_or_abort(&acc_empty[ab], (j / p.nacc - 1) & 1, abort_p, p.status)) break;
+        tc::tc_fence_after();
+        const uint32_t acc = tmem + ab * NM * p.acc_cols;
+        for (int ks = s0; ks < s1; ++ks, ++f) {
+          const int st = f % stages, seg = ks - s0;
+          if (!wait_or_abort(&full[st], (f / stages) & 1, abort_p, p.status)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t wb = smem_u32(smem + st * kStage), wsf = wb + NM * 128 * 128;
+          const uint32_t xb = smem_u32(smem + p.dig_off) + (db * p.segs + seg) * p.tok * 1024;
+          const uint32_t xsf = smem_u32(smem + p.sf_off) + (db * p.segs + seg) * 2 * p.groups * kTileBytes;
+          const uint32_t sfw = sf0 + (f & 1) * sfc, sfx = sfw + 8 * NM;
+          const int kv = min(kStageK, p.K - ks * kStageK);
+          for (int ct = 0; ct * kTileCols < kv; ++ct) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m) copy_scales(sfw + 8 * m + 4 * ct, wsf + (2 * m + ct) * kTileBytes);
+            for (int g = 0; g < p.groups; ++g)
+              copy_scales(sfx + 4 * (ct * p.groups + g), xsf + (ct * p.groups + g) * kTileBytes);
+          }
+          for (int kk = 0; kk * 64 < kv; ++kk)
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+              mma_mxf4(acc + m * p.acc_cols, tc::sw128_desc(wb + m * 128 * 128 + kk * 32),
+                       tc::sw128_desc(xb + kk * 32), idesc_mxf4(n, kk & 1),
+                       sfw + 8 * m + 4 * (kk >> 1), sfx + 4 * p.groups * (kk >> 1),
+                       (seg > 0 || kk > 0) ? 1u : 0u);
+          tc::mma_commit(&empty[st]);
+        }
+        if (!ok) break;
+        tc::mma_commit(&acc_full[ab]);
+      }
+      // every MMA issued has completed before tensor memory is freed
+      tc::mma_commit(&done);
+      mbar_wait_bounded(&done, 0, kWaitIters);
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // digits: rows 8 i .. 8 i + 7 of the buffer are the planes of row i, in
+    // segments of 256 columns with the 128-byte swizzle
+    const int ct = threadIdx.x - 256;
+    int ndig = 0, slot = -1;
+    bool bad = false;
+    for (int item = first; item < last; ++item) {
+      const int s = item / p.ntiles;
+      if (s == slot) continue;
+      slot = s;
+      const int db = ndig % p.nb;
+      const bool ok = ndig < p.nb || wait_or_abort(&dig_empty[db], (ndig / p.nb - 1) & 1, abort_p, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      ++ndig;
+      const Slot sl = slot_of<MODE>(p, s);
+      const int per = (s1 - s0) * 32, total = sl.cnt * per;  // groups of 8 columns
+      unsigned char* dig = smem + p.dig_off + db * p.segs * p.tok * 1024;
+      unsigned char* sf = smem + p.sf_off + db * p.segs * 2 * p.groups * kTileBytes;
+      for (int u0 = 0; u0 < total; u0 += 32 * kConvWarps) {  // total is a multiple of 32
+        const int u = u0 + ct;
+        if (u - lane >= total) break;
+        const int i = u / per, w = u - i * per, seg = w >> 5, c8 = w & 31;
+        float v[8];
+        load_acts<MODE>(p, sl, i, (s0 + seg) * kStageK + 8 * c8, v);
+        uint32_t plane[kDigits];
+        const uint32_t sb = digits_of(v, plane);
+        if (sb == 255u) bad = true;
+        unsigned char* d = dig + (seg * p.tok + i) * 1024;
+#pragma unroll
+        for (int pl = 0; pl < kDigits; ++pl)
+          *reinterpret_cast<uint32_t*>(d + pl * 128 + (((c8 >> 2) ^ pl) << 4) + (c8 & 3) * 4) = plane[pl];
+        // the block's scales of planes 2 (lane % 4) and the next
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int pl = 2 * (lane & 3) + z, r = 8 * i + pl;
+          sf[((seg * 2 + (c8 >> 4)) * p.groups + (r >> 7)) * kTileBytes + (r & 31) * 16 +
+             ((r >> 5) & 3) * 4 + ((c8 >> 2) & 3)] = (unsigned char)(sb == 255u ? 255u : sb + 3 * pl);
+        }
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&dig_full[db]);
+    }
+    if (bad) set_status(p.status, QSM_DEV_NONFINITE);
+  } else if (warp >= 4) {
+    const int q4 = warp & 3, row = 32 * q4 + lane, et = threadIdx.x - 128;
+    const int R = 128 / cs;  // rows of a tile that a CTA of the cluster writes
+    const uint32_t lanes = (uint32_t)(32 * q4) << 16;
+    float* part = reinterpret_cast<float*>(smem + p.part_off);
+    int slot = -1;
+    Slot sl = {};
+    for (int item = first; item < last; ++item) {
+      const int j = item - first, ab = j % p.nacc, pb = j & 1;
+      const int s = item / p.ntiles, tile = item - s * p.ntiles;
+      if (s != slot) sl = slot_of<MODE>(p, slot = s);
+      if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full[ab], (j / p.nacc) & 1, abort_p, p.status))) break;
+      tc::tc_fence_after();
+      if (cs > 1 && j >= 2 &&
+          !__all_sync(0xffffffffu, wait_cluster(&part_empty[pb], (j / 2 - 1) & 1, abort_p, p.status)))
+        break;
+      // the value of (row `rr` of the tile, row i of the slot) goes out
+      auto put = [&](int i, int rr, float a, float b) {
+        const size_t hrow = (size_t)(sl.e < 0 ? p.T * p.k : 0) + sl.row0 + i;
+        const int n = tile * 128 + rr;
+        if (MODE == kRowsGateUp) p.h[hrow * p.I + n] = silu(a) * b;
+        else if (MODE == kRowsDown) p.o[hrow * p.H + n] = a;
+        else if (n < p.N)
+          p.y[(size_t)(sl.row0 + i) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(a));
+      };
+      const uint32_t acc = tmem + lanes + ab * NM * p.acc_cols;
+      const int owner = row / R;
+      const uint32_t dst = cs > 1 ? dsmem_addr(part + ((size_t)(pb * cs + rank) * NM * p.tok) * R + row % R,
+                                               owner)
+                                  : 0u;
+      for (int i0 = 0; i0 < sl.cnt; i0 += 2) {
+        float v[NM][16];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) tc::tmem_ld16(acc + m * p.acc_cols + kDigits * i0, v[m]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (i0 + u >= sl.cnt) break;
+          float sum[2];
+#pragma unroll
+          for (int m = 0; m < NM; ++m) {  // the smallest digits first
+            float a = 0.f;
+#pragma unroll
+            for (int d = 0; d < kDigits; ++d) a += v[m][kDigits * u + d];
+            sum[m] = a;
+          }
+          if (cs == 1) {
+            put(i0 + u, row, sum[0], sum[NM - 1]);
+          } else {
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+              dsmem_st_f32(dst + (uint32_t)((i0 + u) * NM + m) * R * 4, sum[m]);
+          }
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&acc_empty[ab]);
+      if (cs > 1) {
+        // tell the CTAs that this warp wrote to; then add up this CTA's rows
+        if (lane < (cs == 8 ? 2 : 1))
+          arrive_cluster(dsmem_addr(&part_full[pb], cs == 8 ? 2 * q4 + lane : owner));
+        if (!__all_sync(0xffffffffu, wait_cluster(&part_full[pb], (j / 2) & 1, abort_p, p.status))) break;
+        const float* mine = part + (size_t)pb * cs * NM * p.tok * R;
+        for (int u = et; u < sl.cnt * R; u += 128) {
+          const int i = u / R, rr = u % R;
+          float a = 0.f, b = 0.f;
+          for (int c = 0; c < cs; ++c) {
+            const float* src = mine + ((size_t)c * p.tok + i) * NM * R + rr;
+            a += src[0];
+            if (NM == 2) b += src[R];
+          }
+          put(i, rank * R + rr, a, b);
+        }
+        __syncwarp();
+        if (lane < cs) arrive_cluster(dsmem_addr(&part_empty[pb], lane));
+      }
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 2) tc::tmem_dealloc(tmem, 512);
+  if (cs > 1) cluster_sync_all();  // no CTA leaves while another writes to it
+}
+
+template <int MODE>
+constexpr int stage_bytes() { return mats<MODE>() * (128 * 128 + 2 * kTileBytes); }
+
+// Shared memory of a geometry with `stages` ring stages; fills the offsets.
+int layout(StreamParams* p, int stage, int nm) {
+  p->dig_off = p->stages * stage;
+  p->sf_off = p->dig_off + p->nb * p->segs * p->tok * 1024;
+  p->part_off = p->sf_off + p->nb * p->segs * 2 * p->groups * kTileBytes;
+  return p->part_off + (p->cs > 1 ? 2 * nm * p->tok * 128 * 4 : 0) + 1024;
+}
+
+// Clusters of cs CTAs of `kernel` that the current device holds at once.
+int resident_clusters(void* kernel, int cs, int smem, int nsm) {
+  struct Key {
+    int dev;
+    void* k;
+    int cs, smem, n;
+  };
+  static std::mutex mu;
+  static std::vector<Key> cache;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  for (const Key& c : cache)
+    if (c.dev == dev && c.k == kernel && c.cs == cs && c.smem == smem) return c.n;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
+    return 0;
+  int n = nsm;
+  if (cs > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(nsm / cs * cs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cs;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+  }
+  cache.push_back({dev, kernel, cs, smem, n});
+  return n;
+}
+
+template <int MODE>
+qsm_status launch_mode(StreamParams& p, int items, cudaStream_t stream) {
+  auto* k = mx4_rows_kernel<MODE>;
+  const int smem = layout(&p, stage_bytes<MODE>(), mats<MODE>());
+  const int nc = resident_clusters(reinterpret_cast<void*>(k), p.cs, smem, sm_count());
+  if (nc < 1) return QSM_ERR_CUDA;
+  const dim3 grid((items < nc ? items : nc) * p.cs);
+  if (p.cs > 1)
+    QSM_CUDA_TRY(launch_pdl_cluster(k, grid, dim3(kThreads), p.cs, smem, stream, p));
+  else
+    QSM_CUDA_TRY(launch_pdl(k, grid, dim3(kThreads), smem, stream, p));
+  return QSM_OK;
+}
+
+}  // namespace
+
+bool plan_rows(StreamParams* p, int mode, int tiles, int tok, int nsm) {
+  const int nm = mode == kRowsGateUp ? 2 : 1;
+  const int stage = mode == kRowsGateUp ? stage_bytes<kRowsGateUp>() : stage_bytes<kRows>();
+  const int nst = (p->K + kStageK - 1) / kStageK;
+  p->tok = tok;
+  p->nb = mode == kRows ? 1 : 2;
+  p->groups = (kDigits * tok + 127) / 128;
+  p->acc_cols = (kDigits * tok + 31) / 32 * 32;
+  p->nacc = 2 * nm * p->acc_cols + 2 * (8 * nm + 8 * p->groups) <= 512 ? 2 : 1;
+  // K is split while the tiles alone leave half the SMs idle, and further
+  // until the digits fit beside at least three stages
+  int cs = 1;
+  while (2 * cs <= kMaxSplit && 2 * cs <= nst && tiles * cs <= nsm / 2) cs *= 2;
+  for (; cs <= kMaxSplit && cs <= nst; cs *= 2) {
+    p->cs = cs;
+    p->segs = (nst + cs - 1) / cs;
+    p->stages = 0;
+    const int room = (kSmemMax - layout(p, stage, nm)) / stage;
+    p->stages = room < kMaxStages ? room : kMaxStages;
+    if (room >= 3) return true;
+  }
+  return false;
+}
+
+qsm_status launch_rows(StreamParams& p, int mode, int items, cudaStream_t stream) {
+  switch (mode) {
+    case kRows: return launch_mode<kRows>(p, items, stream);
+    case kRowsGateUp: return launch_mode<kRowsGateUp>(p, items, stream);
+    default: return launch_mode<kRowsDown>(p, items, stream);
+  }
+}
+
+}  // namespace mx4
+}  // namespace qsm
+
+extern "C" qsm_status mx4_gemv(const uint16_t* x, int64_t row_stride, int32_t T, const qsm_mx4* w,
+                               uint16_t* y, int32_t* dev_status, cudaStream_t stream) {
+  using namespace qsm;
+  using namespace qsm::mx4;
+  if (!w || T < 0 || w->experts != 1 || w->rows < 0) return QSM_ERR_INVALID_ARGUMENT;
+  if (T > QSM_MX4_GEMV_MAX_ROWS || w->cols > 65536) return QSM_ERR_UNSUPPORTED;
+  if (T == 0 || w->rows == 0) return QSM_OK;
+  if (!mx4_valid(w) || !x || !y || !dev_status || !aligned16(x) || !aligned4(dev_status) ||
+      reinterpret_cast<uintptr_t>(y) % 2 || row_stride < w->cols || row_stride % 8)
+    return QSM_ERR_INVALID_ARGUMENT;
+  StreamParams p = {};
+  p.N = w->rows;
+  p.K = w->cols;
+  p.T = T;
+  p.k = 1;
+  p.x = x;
+  p.ldx = (size_t)row_stride;
+  p.y = y;
+  p.w_scales = w->scales;
+  p.status = dev_status;
+  p.ntiles = row_tiles(p.N);
+  int tok = T;  // all rows at once, or as many as fit
+  while (tok > 0 && !plan_rows(&p, kRows, p.ntiles, tok, sm_count())) --tok;
+  if (tok == 0) return QSM_ERR_UNSUPPORTED;
+  p.slots = (T + p.tok - 1) / p.tok;
+  if (!make_codes_map(&p.w, w->codes, w->rows, w->cols, 128)) return QSM_ERR_CUDA;
+  if ((long long)p.slots * p.ntiles > (1ll << 30)) return QSM_ERR_UNSUPPORTED;
+  return launch_rows(p, kRows, p.slots * p.ntiles, stream);
+}
