@@ -148,6 +148,24 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
                : "memory");
 }
 
+// ------------------------------------------------- one thread of a warp
+
+// True in one thread of the (converged) warp.  The loading and the MMA warp
+// run their loops with all lanes, on values that are the same in all of
+// them, and issue from this thread: the compiler then keeps descriptors and
+// addresses in uniform registers.  Branching on the lane number instead cost
+// 125 cycles per MMA to issue, against 39 this way (M = 128, N = 8, K = 64).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n"
+      : "=r"(r));
+  return r != 0;
+}
+// A value that all lanes hold, as a uniform one.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // ------------------------------------------------------------ bounded waits
 
 // Bounded mbarrier wait shared by all roles of a CTA: gives up when the
@@ -162,6 +180,15 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
   *abort_flag = 1;
   set_status(status, QSM_DEV_TIMEOUT);
   return false;
+}
+
+// The same by all lanes of a warp, as one decision.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int32_t* status) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, status));
+}
+__device__ __forceinline__ bool warp_aborted(volatile int* abort_flag) {
+  return __any_sync(0xffffffffu, *abort_flag != 0);
 }
 
 // ---------------------------------------------------------------------- host

@@ -85,6 +85,17 @@ __device__ __forceinline__ Tile tile_of(const GemmParams& p, int item) {
   return t;
 }
 
+__device__ __forceinline__ Tile uniform_tile(Tile t) {
+  t.e = uniform(t.e);
+  t.a_row = uniform(t.a_row);
+  t.a_tile = uniform(t.a_tile);
+  t.w_row[0] = uniform(t.w_row[0]);
+  t.w_row[1] = uniform(t.w_row[1]);
+  t.w_tile[0] = uniform(t.w_tile[0]);
+  t.w_tile[1] = uniform(t.w_tile[1]);
+  return t;
+}
+
 // Eight consecutive outputs of a row (16 bytes as bf16) or four (as fp32),
 // at column n of N: whole where they fit and are aligned, else one by one.
 template <bool F32>
@@ -136,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
   __shared__ int abort_flag;
   volatile int* abort_p = &abort_flag;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -156,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = uniform(tmem_base);
 
   pdl_wait();
   pdl_launch_dependents();
@@ -166,91 +177,96 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
   const int cts = col_tiles(p.K);
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t f = 0;
-      for (int item = blockIdx.x; item < total && !*abort_p; item += gridDim.x) {
-        const Tile t = tile_of<MODE, BN>(p, item);
-        const bool sh = MODE != kDense && t.e < 0;
-        const CUtensorMap* wm = sh ? &p.w_sh : &p.w;
-        const uint8_t* wsc = sh ? p.w_scales_sh : p.w_scales;
-        const int groups = C::kGroups == 1 || t.w_tile[1] < 0 ? 1 : 2;
-        bool ok = true;
-        for (int ks = 0; ks < nst; ++ks, ++f) {
-          const int s = f % C::kStages;
-          if (f >= C::kStages && !wait_or_abort(&empty[s], (f / C::kStages - 1) & 1, abort_p, p.status)) {
-            ok = false;
-            break;
-          }
-          unsigned char* base = smem + s * C::kStage;
-          const uint32_t sfb = (uint32_t)min(2, cts - 2 * ks) * kTileBytes;  // scale bytes of a row tile
-          mbar_arrive_expect_tx(&full[s], C::kABytes + C::kWBytes + sfb * (1 + groups));
-          tc::tma_load_2d(base, &p.a, ks * 128, t.a_row, &full[s]);
-          unsigned char* wb = base + C::kABytes;
-          if (MODE == kGateUp) {
-            tc::tma_load_2d(wb, wm, ks * 128, t.w_row[0], &full[s]);
-            tc::tma_load_2d(wb + 128 * 128, wm, ks * 128, t.w_row[1], &full[s]);
-          } else {
-            tc::tma_load_2d(wb, wm, ks * 128, t.w_row[0], &full[s]);
-          }
-          unsigned char* sf = wb + C::kWBytes;
-          bulk_g2s(sf, p.a_scales + ((size_t)t.a_tile * cts + 2 * ks) * kTileBytes, sfb, &full[s]);
-          sf += C::kSfaBytes;
-          for (int g = 0; g < groups; ++g)
-            bulk_g2s(sf + g * 2 * kTileBytes,
-                     wsc + ((size_t)t.w_tile[g] * cts + 2 * ks) * kTileBytes, sfb, &full[s]);
+    int st = 0;          // ring position, and how often it came round
+    uint32_t round = 0;
+    for (int item = blockIdx.x; item < total && !warp_aborted(abort_p); item += gridDim.x) {
+      const Tile t = uniform_tile(tile_of<MODE, BN>(p, item));
+      const bool sh = MODE != kDense && t.e < 0;
+      const CUtensorMap* wm = sh ? &p.w_sh : &p.w;
+      const uint8_t* wsc = sh ? p.w_scales_sh : p.w_scales;
+      const int groups = C::kGroups == 1 || t.w_tile[1] < 0 ? 1 : 2;
+      const uint8_t* asf = p.a_scales + (size_t)t.a_tile * cts * kTileBytes;
+      const uint8_t* wsf0 = wsc + (size_t)t.w_tile[0] * cts * kTileBytes;
+      const uint8_t* wsf1 = wsc + (size_t)(groups == 2 ? t.w_tile[1] : 0) * cts * kTileBytes;
+      bool ok = true;
+      for (int ks = 0; ks < nst; ++ks) {
+        if (round > 0 && !warp_wait(&empty[st], (round - 1) & 1, abort_p, p.status)) {
+          ok = false;
+          break;
         }
-        if (!ok) break;
+        if (elect_one()) {
+          unsigned char* base = smem + st * C::kStage;
+          const uint32_t sfb = (uint32_t)min(2, cts - 2 * ks) * kTileBytes;  // scale bytes of a row tile
+          mbar_arrive_expect_tx(&full[st], C::kABytes + C::kWBytes + sfb * (1 + groups));
+          tc::tma_load_2d(base, &p.a, ks * 128, t.a_row, &full[st]);
+          unsigned char* wb = base + C::kABytes;
+          tc::tma_load_2d(wb, wm, ks * 128, t.w_row[0], &full[st]);
+          if (MODE == kGateUp) tc::tma_load_2d(wb + 128 * 128, wm, ks * 128, t.w_row[1], &full[st]);
+          unsigned char* sf = wb + C::kWBytes;
+          bulk_g2s(sf, asf + ks * 2 * kTileBytes, sfb, &full[st]);
+          bulk_g2s(sf + C::kSfaBytes, wsf0 + ks * 2 * kTileBytes, sfb, &full[st]);
+          if (groups == 2)
+            bulk_g2s(sf + C::kSfaBytes + 2 * kTileBytes, wsf1 + ks * 2 * kTileBytes, sfb, &full[st]);
+        }
+        __syncwarp();
+        if (++st == C::kStages) st = 0, ++round;
       }
-      // after an abort, let the last copies land before the CTA exits
-      const uint32_t n = f < (uint32_t)C::kStages ? f : (uint32_t)C::kStages;
-      for (uint32_t i = 1; i <= n; ++i)
-        mbar_wait_bounded(&full[(f - i) % C::kStages], ((f - i) / C::kStages) & 1, 1u << 16);
+      if (!ok) break;
+    }
+    // after an abort, let the copies in flight land before the CTA exits
+    for (int i = 0; i < C::kStages; ++i) {
+      const uint32_t r = i < st ? round : round - 1;  // the last round of this position
+      if (i < st || round > 0) mbar_wait_bounded(&full[i], r & 1, 1u << 16);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t f = 0;
-      int j = 0;
-      for (int item = blockIdx.x; item < total && !*abort_p; item += gridDim.x, ++j) {
-        // in tiles of 64 rows of w, every other one starts in the middle of a
-        // scale tile: two columns on
-        const int sf_off = BN == 64 ? ((item % p.nsub) & 1) * 2 : 0;
-        if (j >= 1 && !wait_or_abort(&acc_empty, (j - 1) & 1, abort_p, p.status)) break;
+    int st = 0, j = 0;
+    uint32_t round = 0;
+    const uint64_t desc0 = tc::sw128_desc(smem_u32(smem));
+    for (int item = blockIdx.x; item < total && !warp_aborted(abort_p); item += gridDim.x, ++j) {
+      // in tiles of 64 rows of w, every other one starts in the middle of a
+      // scale tile: two columns on
+      const int sf_off = BN == 64 ? ((item % p.nsub) & 1) * 2 : 0;
+      if (j >= 1 && !warp_wait(&acc_empty, (j - 1) & 1, abort_p, p.status)) break;
+      bool ok = true;
+      for (int ks = 0; ks < nst; ++ks) {
+        if (!warp_wait(&full[st], round & 1, abort_p, p.status)) {
+          ok = false;
+          break;
+        }
         tc::tc_fence_after();
-        bool ok = true;
-        for (int ks = 0; ks < nst; ++ks, ++f) {
-          const int s = f % C::kStages;
-          if (!wait_or_abort(&full[s], (f / C::kStages) & 1, abort_p, p.status)) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const uint32_t base = smem_u32(smem + s * C::kStage);
-          const uint32_t wb = base + C::kABytes, sfa_s = wb + C::kWBytes, sfw_s = sfa_s + C::kSfaBytes;
-          const uint32_t sfa = tmem + BN + (f & 1) * C::kSfCols, sfw = sfa + 8;
+        if (elect_one()) {
+          const uint64_t ad = desc0 + (uint64_t)(st * (C::kStage >> 4)), wd = ad + (C::kABytes >> 4);
+          const uint32_t sfa_s = smem_u32(smem) + st * C::kStage + C::kABytes + C::kWBytes;
+          const uint32_t sfw_s = sfa_s + C::kSfaBytes;
+          const uint32_t sfa = tmem + BN + (ks & 1) * C::kSfCols, sfw = sfa + 8;
           const int kv = min(kStageK, p.K - ks * kStageK);
-          for (int ct = 0; ct * kTileCols < kv; ++ct) {
+#pragma unroll
+          for (int ct = 0; ct < 2; ++ct) {
+            if (ct * kTileCols >= kv) break;
             copy_scales(sfa + 4 * ct, sfa_s + ct * kTileBytes);
+#pragma unroll
             for (int g = 0; g < C::kGroups; ++g)
               copy_scales(sfw + 4 * (ct * C::kGroups + g), sfw_s + (2 * g + ct) * kTileBytes);
           }
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (kk * 64 >= kv) break;
-            mma_mxf4(tmem, tc::sw128_desc(base + kk * 32), tc::sw128_desc(wb + kk * 32),
-                     idesc_mxf4(BN, kk & 1), sfa + 4 * (kk >> 1),
+            mma_mxf4(tmem, ad + 2 * kk, wd + 2 * kk, idesc_mxf4(BN, kk & 1), sfa + 4 * (kk >> 1),
                      sfw + 4 * C::kGroups * (kk >> 1) + sf_off, (ks > 0 || kk > 0) ? 1u : 0u);
           }
-          tc::mma_commit(&empty[s]);
+          tc::mma_commit(&empty[st]);
+          if (ks == nst - 1) tc::mma_commit(&acc_full);
         }
-        if (!ok) break;
-        tc::mma_commit(&acc_full);
+        __syncwarp();
+        if (++st == C::kStages) st = 0, ++round;
       }
-      // every MMA issued has completed before tensor memory is freed
-      tc::mma_commit(&done);
-      mbar_wait_bounded(&done, 0, kWaitIters);
+      if (!ok) break;
     }
+    // every MMA issued has completed before tensor memory is freed
+    if (elect_one()) tc::mma_commit(&done);
     __syncwarp();
+    mbar_wait_bounded(&done, 0, kWaitIters);
   } else if (warp >= 4) {
     const int q4 = warp & 3, half = (warp - 4) >> 2;
     const int row = 32 * q4 + lane;
@@ -259,9 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
     bool bad = false;
     int j = 0;
     for (int item = blockIdx.x; item < total; item += gridDim.x, ++j) {
-      if (__any_sync(0xffffffffu, *abort_p != 0)) break;
+      if (warp_aborted(abort_p)) break;
       const Tile t = tile_of<MODE, BN>(p, item);
-      if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full, j & 1, abort_p, p.status))) break;
+      if (!warp_wait(&acc_full, j & 1, abort_p, p.status)) break;
       tc::tc_fence_after();
       constexpr int NC = BN / 2;
       uint32_t r[NC];

@@ -91,6 +91,7 @@ struct Slot {
   int cnt;
 };
 
+// By all lanes of a warp.
 template <int MODE>
 __device__ __forceinline__ Slot slot_of(const StreamParams& p, int s) {
   Slot r;
@@ -100,9 +101,9 @@ __device__ __forceinline__ Slot slot_of(const StreamParams& p, int s) {
     r.cnt = min(p.tok, p.T - r.row0);
   } else {
     const int2 te = __ldcg(reinterpret_cast<const int2*>(p.tile_map) + (s - p.shared_tiles));
-    r.e = te.x;
-    r.row0 = te.y;
-    r.cnt = min(p.tok, __ldcg(p.offsets + te.x + 1) - te.y);
+    r.e = uniform(te.x);
+    r.row0 = uniform(te.y);
+    r.cnt = uniform(min(p.tok, __ldcg(p.offsets + r.e + 1) - r.row0));
   }
   return r;
 }
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
   __shared__ int abort_flag;
   volatile int* abort_p = &abort_flag;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int cs = p.cs, stages = p.stages;
   const int rank = cs > 1 ? (int)cluster_rank() : 0;
   if (threadIdx.x == 0) {
@@ -212,11 +213,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
   __syncthreads();
   tc::tc_fence_after();
   if (cs > 1) cluster_sync_all();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = uniform(tmem_base);
 
   pdl_wait();
   pdl_launch_dependents();
-  const int slots = MODE == kRows ? p.slots : p.shared_tiles + __ldcg(p.n_tiles);
+  const int slots = MODE == kRows ? p.slots : p.shared_tiles + uniform(__ldcg(p.n_tiles));
   // this cluster's contiguous run of items (slot, tile)
   const long long items = (long long)slots * p.ntiles;
   const int nclus = gridDim.x / cs, clus = blockIdx.x / cs;
@@ -226,99 +227,110 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
   const int s0 = nst * rank / cs, s1 = nst * (rank + 1) / cs;
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t f = 0;
-      int slot = -1;
-      Slot sl = {};
-      for (int item = first; item < last && !*abort_p; ++item) {
-        const int s = item / p.ntiles, tile = item - s * p.ntiles;
-        if (s != slot) sl = slot_of<MODE>(p, slot = s);
-        const bool sh = MODE != kRows && sl.e < 0;
-        const CUtensorMap* wm = sh ? &p.w_sh : &p.w;
-        const uint8_t* wsc = sh ? p.w_scales_sh : p.w_scales;
-        const int row0 = (sl.e < 0 ? 0 : sl.e * p.N) + tile * 128;
-        bool ok = true;
-        for (int ks = s0; ks < s1; ++ks, ++f) {
-          const int st = f % stages;
-          if (f >= (uint32_t)stages && !wait_or_abort(&empty[st], (f / stages - 1) & 1, abort_p, p.status)) {
-            ok = false;
-            break;
-          }
+    int st = 0, slot = -1;  // ring position
+    uint32_t round = 0;     // how often it came round
+    Slot sl = {};
+    for (int item = first; item < last && !warp_aborted(abort_p); ++item) {
+      const int s = item / p.ntiles, tile = item - s * p.ntiles;
+      if (s != slot) sl = slot_of<MODE>(p, slot = s);
+      const bool sh = MODE != kRows && sl.e < 0;
+      const CUtensorMap* wm = sh ? &p.w_sh : &p.w;
+      const int row0 = (sl.e < 0 ? 0 : sl.e * p.N) + tile * 128;
+      const uint8_t* wsf = (sh ? p.w_scales_sh : p.w_scales) + (size_t)(row0 >> 7) * cts * kTileBytes;
+      bool ok = true;
+      for (int ks = s0; ks < s1; ++ks) {
+        if (round > 0 && !warp_wait(&empty[st], (round - 1) & 1, abort_p, p.status)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           unsigned char* base = smem + st * kStage;
           const uint32_t sfb = (uint32_t)min(2, cts - 2 * ks) * kTileBytes;
           mbar_arrive_expect_tx(&full[st], NM * (128 * 128 + sfb));
 #pragma unroll
           for (int m = 0; m < NM; ++m) {
-            const int row = row0 + m * (p.N / 2);
-            tc::tma_load_2d(base + m * 128 * 128, wm, ks * 128, row, &full[st]);
+            tc::tma_load_2d(base + m * 128 * 128, wm, ks * 128, row0 + m * (p.N / 2), &full[st]);
             bulk_g2s(base + NM * 128 * 128 + m * 2 * kTileBytes,
-                     wsc + ((size_t)(row >> 7) * cts + 2 * ks) * kTileBytes, sfb, &full[st]);
+                     wsf + ((size_t)m * (p.N >> 8) * cts + 2 * ks) * kTileBytes, sfb, &full[st]);
           }
         }
-        if (!ok) break;
+        __syncwarp();
+        if (++st == stages) st = 0, ++round;
       }
-      // after an abort, let the last copies land before the CTA exits
-      const uint32_t n = f < (uint32_t)stages ? f : (uint32_t)stages;
-      for (uint32_t i = 1; i <= n; ++i)
-        mbar_wait_bounded(&full[(f - i) % stages], ((f - i) / stages) & 1, 1u << 16);
+      if (!ok) break;
+    }
+    // after an abort, let the copies in flight land before the CTA exits
+    for (int i = 0; i < stages; ++i) {
+      const uint32_t r = i < st ? round : round - 1;  // the last round of this position
+      if (i < st || round > 0) mbar_wait_bounded(&full[i], r & 1, 1u << 16);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t f = 0;
-      int slot = -1, db = -1, n = 0, ndig = 0;
-      const int sfc = 8 * NM + 8 * p.groups;  // scale columns of one stage
-      const uint32_t sf0 = tmem + p.nacc * NM * p.acc_cols;
-      for (int item = first; item < last && !*abort_p; ++item) {
-        const int j = item - first, ab = j % p.nacc;
-        const int s = item / p.ntiles;
-        bool ok = true;
-        if (s != slot) {  // the next slot's digits; the previous one's are free
-          if (slot >= 0) tc::mma_commit(&dig_empty[db]);
-          slot = s;
-          n = kDigits * slot_of<MODE>(p, s).cnt;
-          db = ndig % p.nb;
-          if (!wait_or_abort(&dig_full[db], (ndig / p.nb) & 1, abort_p, p.status)) break;
-          ++ndig;
+    int st = 0, slot = -1, db = 0, n = 0, ndig = 0, ab = 0;
+    uint32_t round = 0, acc_round = 0, fs = 0;
+    const int sfc = 8 * NM + 8 * p.groups;  // scale columns of one stage
+    const uint32_t sf0 = tmem + p.nacc * NM * p.acc_cols;
+    const uint32_t base = smem_u32(smem);
+    const uint64_t desc0 = tc::sw128_desc(base);
+    for (int item = first; item < last && !warp_aborted(abort_p); ++item) {
+      const int s = item / p.ntiles;
+      bool ok = true;
+      if (s != slot) {  // the next slot's digits; the previous one's are free
+        if (slot >= 0 && elect_one()) tc::mma_commit(&dig_empty[db]);
+        __syncwarp();
+        slot = s;
+        n = kDigits * slot_of<MODE>(p, s).cnt;
+        db = ndig % p.nb;
+        if (!warp_wait(&dig_full[db], (ndig / p.nb) & 1, abort_p, p.status)) break;
+        ++ndig;
+      }
+      if (acc_round > 0 && !warp_wait(&acc_empty[ab], (acc_round - 1) & 1, abort_p, p.status)) break;
+      const uint32_t acc = tmem + ab * NM * p.acc_cols;
+      for (int ks = s0; ks < s1; ++ks) {
+        const int seg = ks - s0;
+        if (!warp_wait(&full[st], round & 1, abort_p, p.status)) {
+          ok = false;
+          break;
         }
-        if (j >= p.nacc && !wait_or_abort(&acc_empty[ab], (j / p.nacc - 1) & 1, abort_p, p.status)) break;
         tc::tc_fence_after();
-        const uint32_t acc = tmem + ab * NM * p.acc_cols;
-        for (int ks = s0; ks < s1; ++ks, ++f) {
-          const int st = f % stages, seg = ks - s0;
-          if (!wait_or_abort(&full[st], (f / stages) & 1, abort_p, p.status)) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const uint32_t wb = smem_u32(smem + st * kStage), wsf = wb + NM * 128 * 128;
-          const uint32_t xb = smem_u32(smem + p.dig_off) + (db * p.segs + seg) * p.tok * 1024;
-          const uint32_t xsf = smem_u32(smem + p.sf_off) + (db * p.segs + seg) * 2 * p.groups * kTileBytes;
-          const uint32_t sfw = sf0 + (f & 1) * sfc, sfx = sfw + 8 * NM;
+        if (elect_one()) {
+          const uint32_t wsf = base + st * kStage + NM * 128 * 128;
+          const uint32_t xsf = base + p.sf_off + (db * p.segs + seg) * 2 * p.groups * kTileBytes;
+          const uint64_t wd = desc0 + (uint64_t)(st * (kStage >> 4));
+          const uint64_t xd = desc0 + (uint64_t)((p.dig_off + (db * p.segs + seg) * p.tok * 1024) >> 4);
+          const uint32_t sfw = sf0 + (fs & 1) * sfc, sfx = sfw + 8 * NM;
           const int kv = min(kStageK, p.K - ks * kStageK);
-          for (int ct = 0; ct * kTileCols < kv; ++ct) {
+#pragma unroll
+          for (int ct = 0; ct < 2; ++ct) {
+            if (ct * kTileCols >= kv) break;
 #pragma unroll
             for (int m = 0; m < NM; ++m) copy_scales(sfw + 8 * m + 4 * ct, wsf + (2 * m + ct) * kTileBytes);
-            for (int g = 0; g < p.groups; ++g)
-              copy_scales(sfx + 4 * (ct * p.groups + g), xsf + (ct * p.groups + g) * kTileBytes);
+            copy_scales(sfx + 4 * ct * p.groups, xsf + ct * p.groups * kTileBytes);
+            if (p.groups == 2) copy_scales(sfx + 4 * (2 * ct + 1), xsf + (2 * ct + 1) * kTileBytes);
           }
-          for (int kk = 0; kk * 64 < kv; ++kk)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk * 64 >= kv) break;
 #pragma unroll
             for (int m = 0; m < NM; ++m)
-              mma_mxf4(acc + m * p.acc_cols, tc::sw128_desc(wb + m * 128 * 128 + kk * 32),
-                       tc::sw128_desc(xb + kk * 32), idesc_mxf4(n, kk & 1),
-                       sfw + 8 * m + 4 * (kk >> 1), sfx + 4 * p.groups * (kk >> 1),
-                       (seg > 0 || kk > 0) ? 1u : 0u);
+              mma_mxf4(acc + m * p.acc_cols, wd + m * (128 * 128 >> 4) + 2 * kk, xd + 2 * kk,
+                       idesc_mxf4(n, kk & 1), sfw + 8 * m + 4 * (kk >> 1),
+                       sfx + 4 * p.groups * (kk >> 1), (seg > 0 || kk > 0) ? 1u : 0u);
+          }
           tc::mma_commit(&empty[st]);
+          if (ks == s1 - 1) tc::mma_commit(&acc_full[ab]);
         }
-        if (!ok) break;
-        tc::mma_commit(&acc_full[ab]);
+        __syncwarp();
+        ++fs;
+        if (++st == stages) st = 0, ++round;
       }
-      // every MMA issued has completed before tensor memory is freed
-      tc::mma_commit(&done);
-      mbar_wait_bounded(&done, 0, kWaitIters);
+      if (!ok) break;
+      if (++ab == p.nacc) ab = 0, ++acc_round;
     }
+    // every MMA issued has completed before tensor memory is freed
+    if (elect_one()) tc::mma_commit(&done);
     __syncwarp();
+    mbar_wait_bounded(&done, 0, kWaitIters);
   } else if (warp >= 8) {
     // digits: rows 8 i .. 8 i + 7 of the buffer are the planes of row i, in
     // segments of 256 columns with the 128-byte swizzle
@@ -330,8 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       if (s == slot) continue;
       slot = s;
       const int db = ndig % p.nb;
-      const bool ok = ndig < p.nb || wait_or_abort(&dig_empty[db], (ndig / p.nb - 1) & 1, abort_p, p.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (ndig >= p.nb && !warp_wait(&dig_empty[db], (ndig / p.nb - 1) & 1, abort_p, p.status)) break;
       ++ndig;
       const Slot sl = slot_of<MODE>(p, s);
       const int per = (s1 - s0) * 32, total = sl.cnt * per;  // groups of 8 columns
@@ -374,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       const int j = item - first, ab = j % p.nacc, pb = j & 1;
       const int s = item / p.ntiles, tile = item - s * p.ntiles;
       if (s != slot) sl = slot_of<MODE>(p, slot = s);
-      if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full[ab], (j / p.nacc) & 1, abort_p, p.status))) break;
+      if (!warp_wait(&acc_full[ab], (j / p.nacc) & 1, abort_p, p.status)) break;
       tc::tc_fence_after();
       if (cs > 1 && j >= 2 &&
           !__all_sync(0xffffffffu, wait_cluster(&part_empty[pb], (j / 2 - 1) & 1, abort_p, p.status)))
