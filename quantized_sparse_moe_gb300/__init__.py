@@ -22,10 +22,6 @@ import threading
 import torch
 
 from . import build as _build
-from . import mx4 as _mx4
-from .mx4 import (Mx4Forward, Mx4Layer, Mx4Tensor, moe_mx4_workspace_bytes,  # noqa: F401
-                  mx4_dequantize, mx4_gemm, mx4_gemv, mx4_quantize, mx4_scale_bytes,
-                  mx4_tile_scales)
 
 Q8_0 = 0
 AFFINE4_G64 = 1
@@ -584,3 +580,11 @@ def q8_gemv_i8(qx: torch.Tensor, dx: torch.Tensor, q: torch.Tensor, d: torch.Ten
     _check(lib().q8_gemv_i8(_p(qx), _p(dx), _p(q), _p(_u16(d)), N, K, _p(y),
                             _p(dev_status), _stream(stream)), "q8_gemv_i8")
     return y
+
+
+# ------------------------------------------------------------------ MXFP4
+
+from . import mx4 as _mx4  # noqa: E402
+from .mx4 import (Mx4Forward, Mx4Layer, Mx4Tensor, moe_mx4_workspace_bytes,  # noqa: E402, F401
+                  mx4_dequantize, mx4_gemm, mx4_gemv, mx4_quantize, mx4_scale_bytes,
+                  mx4_tile_scales)

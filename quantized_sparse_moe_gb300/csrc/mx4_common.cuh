@@ -35,6 +35,33 @@ __host__ __device__ inline size_t scale_word(int r, int ct, int cts) {
   return ((size_t)(r >> 7) * cts + ct) * kTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
 }
 
+// Division of n < 2^31 by a divisor fixed at launch, by one multiplication
+// (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994).
+struct FastDiv {
+  uint32_t d, m, l;
+  __host__ explicit FastDiv(uint32_t div = 1) : d(div), m(0), l(0) {
+    while ((1ull << l) < d) ++l;
+    m = (uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(m, n) + n) >> l; }
+};
+
+// A shared-memory box (swizzled as `map` says) to global memory; parts
+// outside the tensor are left out.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// This thread's stores have read their shared memory / have been written.
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // --------------------------------------------------------------- e2m1 codes
 
 // Two fp32 values (already divided by the block's scale) to one byte of

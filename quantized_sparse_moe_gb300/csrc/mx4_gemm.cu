@@ -14,7 +14,10 @@
 // scale copies and the MMAs, warps 4-11 are the epilogue.  One accumulator
 // of BN columns: the epilogue's threads take their half rows into registers
 // at once (BN / 2 columns each), hand the accumulator back and convert and
-// store while the next tile's MMAs run.
+// store while the next tile's MMAs run.  The outputs leave through swizzled
+// boxes of 32 rows x 128 bytes per warp and TMA stores (or, where rows of y
+// are not 16-byte aligned, through padded boxes and plain stores).  Of a
+// short tile only the 32-row groups that exist are loaded and stored.
 #include "mx4_gemm.cuh"
 
 namespace qsm {
@@ -22,11 +25,24 @@ namespace mx4 {
 
 namespace {
 
+// Rows of y (pitch ldy elements) as boxes of 32 rows.
+bool make_out_map(CUtensorMap* m, void* y, CUtensorMapDataType dt, int el, uint64_t rows, int cols,
+                  size_t ldy, int box_cols, CUtensorMapSwizzle swz) {
+  tc::EncodeTiledFn fn = tc::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, rows};
+  const cuuint64_t strides[1] = {ldy * el};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, dt, 2, y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
-constexpr int kStagePitch = 144;  // bytes of a staged epilogue row (128 + 16)
+constexpr int kStagePitch = 144;  // bytes of a row in a padded box (128 + 16)
 
-template <int BN>
+template <int MODE, int BN, bool F32>
 struct Cfg {
   static constexpr int kGroups = BN >= 128 ? BN / 128 : 1;  // scale tiles per column tile of w
   static constexpr int kABytes = 128 * 128;
@@ -34,12 +50,21 @@ struct Cfg {
   static constexpr int kSfaBytes = 2 * kTileBytes;
   static constexpr int kSfwBytes = 2 * kTileBytes * kGroups;
   static constexpr int kStage = kABytes + kWBytes + kSfaBytes + kSfwBytes;
-  static constexpr int kStages = BN == 256 ? 3 : BN == 128 ? 5 : 6;
-  static constexpr int kStaging = kEpiWarps * 32 * kStagePitch;
-  static constexpr int kSmem = kStages * kStage + kStaging + 1024;
+  static constexpr int kStages = MODE == kGateUp ? 4 : BN == 256 ? 3 : BN == 128 ? 4 : 6;
+  // the epilogue: a thread's columns, the bytes of them that make a box's
+  // row, and the boxes of a warp (at most two at a time)
+  static constexpr int NC = BN / 2;
+  static constexpr int kEl = F32 ? 4 : 2;
+  static constexpr int kInner = NC * kEl < 128 ? NC * kEl : 128;
+  static constexpr int kBoxCols = kInner / kEl;
+  static constexpr int kBoxes = NC / kBoxCols < 2 ? 1 : 2;
+  static constexpr int kBoxBytes = kBoxes * 32 * kInner;
+  static constexpr int kWarpBytes = MODE == kGateUp ? 0
+                                    : kBoxBytes > 32 * kStagePitch ? kBoxBytes : (32 * kStagePitch + 1023) / 1024 * 1024;
+  static constexpr int kSmem = kStages * kStage + kEpiWarps * kWarpBytes + 1024;
   static constexpr int kSfCols = 8 + 8 * kGroups;  // scale columns of one stage
   static constexpr int kTmem = BN == 256 ? 512 : BN == 128 ? 256 : 128;
-  static_assert(kStage % 1024 == 0 && BN + 2 * kSfCols <= kTmem && kSmem <= 227 * 1024, "tile");
+  static_assert(kStage % 1024 == 0 && BN + 2 * kSfCols <= kTmem && kSmem <= 226 * 1024, "tile");
 };
 
 // Where a tile's operands and results lie.
@@ -87,6 +112,7 @@ __device__ __forceinline__ Tile tile_of(const GemmParams& p, int item) {
 
 __device__ __forceinline__ Tile uniform_tile(Tile t) {
   t.e = uniform(t.e);
+  t.cnt = uniform(t.cnt);
   t.a_row = uniform(t.a_row);
   t.a_tile = uniform(t.a_tile);
   t.w_row[0] = uniform(t.w_row[0]);
@@ -96,19 +122,13 @@ __device__ __forceinline__ Tile uniform_tile(Tile t) {
   return t;
 }
 
-// Eight consecutive outputs of a row (16 bytes as bf16) or four (as fp32),
-// at column n of N: whole where they fit and are aligned, else one by one.
+// Eight (bf16) or four (fp32) consecutive outputs of a row, one by one, at
+// column n of N.
 template <bool F32>
-__device__ __forceinline__ void store_chunk(void* y, size_t off, int n, int N, bool vec, uint4 v) {
-  constexpr int kPer = F32 ? 4 : 8;
-  if (vec && n + kPer <= N) {
-    if (F32) *reinterpret_cast<uint4*>(static_cast<float*>(y) + off) = v;
-    else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + off) = v;
-    return;
-  }
+__device__ __forceinline__ void store_chunk(void* y, size_t off, int n, int N, uint4 v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+  for (int i = 0; i < (F32 ? 4 : 8); ++i) {
     if (n + i >= N) break;
     if (F32) static_cast<uint32_t*>(y)[off + i] = w[i];
     else static_cast<uint16_t*>(y)[off + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
@@ -138,7 +158,7 @@ __device__ __forceinline__ void take_acc(uint32_t taddr, int half, uint32_t (&r)
 
 template <int MODE, int BN, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_constant__ GemmParams p) {
-  using C = Cfg<BN>;
+  using C = Cfg<MODE, BN, F32>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -188,6 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
       const uint8_t* asf = p.a_scales + (size_t)t.a_tile * cts * kTileBytes;
       const uint8_t* wsf0 = wsc + (size_t)t.w_tile[0] * cts * kTileBytes;
       const uint8_t* wsf1 = wsc + (size_t)(groups == 2 ? t.w_tile[1] : 0) * cts * kTileBytes;
+      const int a32 = (t.cnt + 31) >> 5;  // groups of 32 rows of a that exist
+      const uint32_t abytes = a32 * 32 * 128;
       bool ok = true;
       for (int ks = 0; ks < nst; ++ks) {
         if (round > 0 && !warp_wait(&empty[st], (round - 1) & 1, abort_p, p.status)) {
@@ -197,8 +219,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
         if (elect_one()) {
           unsigned char* base = smem + st * C::kStage;
           const uint32_t sfb = (uint32_t)min(2, cts - 2 * ks) * kTileBytes;  // scale bytes of a row tile
-          mbar_arrive_expect_tx(&full[st], C::kABytes + C::kWBytes + sfb * (1 + groups));
-          tc::tma_load_2d(base, &p.a, ks * 128, t.a_row, &full[st]);
+          mbar_arrive_expect_tx(&full[st], abytes + C::kWBytes + sfb * (1 + groups));
+          if (a32 == 4) {
+            tc::tma_load_2d(base, &p.a, ks * 128, t.a_row, &full[st]);
+          } else {
+            for (int i = 0; i < a32; ++i)
+              tc::tma_load_2d(base + i * 32 * 128, &p.a32, ks * 128, t.a_row + 32 * i, &full[st]);
+          }
           unsigned char* wb = base + C::kABytes;
           tc::tma_load_2d(wb, wm, ks * 128, t.w_row[0], &full[st]);
           if (MODE == kGateUp) tc::tma_load_2d(wb + 128 * 128, wm, ks * 128, t.w_row[1], &full[st]);
@@ -270,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
   } else if (warp >= 4) {
     const int q4 = warp & 3, half = (warp - 4) >> 2;
     const int row = 32 * q4 + lane;
-    unsigned char* stage = smem + C::kStages * C::kStage + (warp - 4) * 32 * kStagePitch;
+    unsigned char* stage = smem + C::kStages * C::kStage + (warp - 4) * C::kWarpBytes;
+    const bool by_tma = p.vec != 0;
     const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16);
     bool bad = false;
     int j = 0;
@@ -279,7 +307,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
       const Tile t = tile_of<MODE, BN>(p, item);
       if (!warp_wait(&acc_full, j & 1, abort_p, p.status)) break;
       tc::tc_fence_after();
-      constexpr int NC = BN / 2;
+      constexpr int NC = C::NC;
+      if (32 * q4 >= t.cnt) {  // none of the warp's rows exist
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&acc_empty);
+        continue;
+      }
       uint32_t r[NC];
       take_acc<MODE, BN>(taddr, half, r);
       tc::tc_fence_before();
@@ -318,53 +351,76 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
           *reinterpret_cast<uint16_t*>(sw + 2 * half) = (uint16_t)sbytes;
         }
       } else {
-        // through a staged copy of the warp's 32 rows, 128 bytes of each at
-        // a time, so that a row's outputs leave in whole 128-byte lines
-        constexpr bool kHalf = MODE == kDown;  // fp16 of 1/16 the value
-        constexpr int kCols = F32 ? 32 : 64;   // columns per step
-        constexpr int kStep = kCols < NC ? kCols : NC;
-        void* y = p.y;
-        const size_t ld = p.ldy;
+        // 16-byte pieces of a row's outputs, from column c on
+        __half2 top = __half2half2(__ushort_as_half(0));
+        auto piece = [&](int c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (F32) {
+              w[i] = r[c + i];
+              continue;
+            }
+            const float a = __uint_as_float(r[c + 2 * i]), b = __uint_as_float(r[c + 2 * i + 1]);
+            if (MODE == kDown) {  // fp16 of 1/16 the value
+              const __half2 h = __floats2half2_rn(a * kOutScale, b * kOutScale);
+              top = __hmax2(top, __habs2(h));
+              w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+              w[i] = pack_bf16(a, b);
+            }
+          }
+          return make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        constexpr int kStep = C::kBoxes * C::kBoxCols;    // columns staged at a time
+        constexpr int kPer = 16 / C::kEl;                 // columns in a piece
+        const int col = t.n0 + half * NC;
 #pragma unroll
         for (int c0 = 0; c0 < NC; c0 += kStep) {
-          unsigned char* mine = stage + lane * kStagePitch;
+          if (by_tma) {
+            if (lane == 0) store_wait_read();  // the boxes may be written again
+            __syncwarp();
 #pragma unroll
-          for (int c = 0; c < kStep; c += F32 ? 4 : 8) {
-            uint4 v;
-            if (F32) {
-              v = make_uint4(r[c0 + c], r[c0 + c + 1], r[c0 + c + 2], r[c0 + c + 3]);
-            } else {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float a = __uint_as_float(r[c0 + c + 2 * i]), b = __uint_as_float(r[c0 + c + 2 * i + 1]);
-                if (kHalf) {
-                  const float a16 = a * kOutScale, b16 = b * kOutScale;
-                  if (row < t.cnt && (!(fabsf(a16) <= 65504.f) || !(fabsf(b16) <= 65504.f)))
-                    bad |= t.n0 + half * NC + c0 + c + 2 * i < p.N;
-                  const __half2 h2 = __floats2half2_rn(a16, b16);
-                  w[i] = *reinterpret_cast<const uint32_t*>(&h2);
-                } else {
-                  w[i] = pack_bf16(a, b);
-                }
-              }
-              v = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int c = 0; c < kStep; c += kPer) {
+              const int box = c / C::kBoxCols, ch = c % C::kBoxCols / kPer;
+              const int sw = C::kInner == 128 ? lane & 7 : (lane >> 1) & 3;
+              *reinterpret_cast<uint4*>(stage + box * 32 * C::kInner + lane * C::kInner + ((ch ^ sw) << 4)) =
+                  piece(c0 + c);
             }
-            *reinterpret_cast<uint4*>(mine + c * (F32 ? 4 : 2)) = v;
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+#pragma unroll
+              for (int box = 0; box < C::kBoxes; ++box)
+                if (col + c0 + box * C::kBoxCols < p.N)
+                  tma_store_2d(&p.y_map, stage + box * 32 * C::kInner, col + c0 + box * C::kBoxCols,
+                               t.a_row + 32 * q4);
+              store_commit();
+            }
+          } else {
+#pragma unroll
+            for (int box = 0; box < C::kBoxes; ++box) {
+              __syncwarp();
+#pragma unroll
+              for (int ch = 0; ch < C::kInner / 16; ++ch)
+                *reinterpret_cast<uint4*>(stage + lane * kStagePitch + ch * 16) =
+                    piece(c0 + box * C::kBoxCols + ch * kPer);
+              __syncwarp();
+              constexpr int kChunks = C::kInner / 16;
+              for (int i = lane; i < 32 * kChunks; i += 32) {
+                const int rr = i / kChunks, ch = i % kChunks;
+                const int n = col + c0 + box * C::kBoxCols + ch * kPer;
+                if (32 * q4 + rr < t.cnt && n < p.N)
+                  store_chunk<F32>(p.y, ((size_t)t.a_row + 32 * q4 + rr) * p.ldy + n, n, p.N,
+                                   *reinterpret_cast<const uint4*>(stage + rr * kStagePitch + ch * 16));
+              }
+            }
           }
-          __syncwarp();
-          constexpr int kChunks = kStep * (F32 ? 4 : 2) / 16;  // 16-byte pieces of a row
-          for (int i = lane; i < 32 * kChunks; i += 32) {
-            const int rr = i / kChunks, ch = i % kChunks;
-            const int n = t.n0 + half * NC + c0 + ch * (F32 ? 4 : 8);
-            if (32 * q4 + rr < t.cnt && n < p.N)
-              store_chunk<F32>(y, ((size_t)t.a_row + 32 * q4 + rr) * ld + n, n, p.N, p.vec != 0,
-                               *reinterpret_cast<const uint4*>(stage + rr * kStagePitch + ch * 16));
-          }
-          __syncwarp();
         }
+        if (MODE == kDown && row < t.cnt && (__hisinf(__low2half(top)) || __hisinf(__high2half(top)))) bad = true;
       }
     }
+    if (MODE != kGateUp && lane == 0) store_wait();
     if (bad) set_status(p.status, MODE == kGateUp ? QSM_DEV_NONFINITE : QSM_DEV_FP16_RANGE);
   }
   tc::tc_fence_before();
@@ -374,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
 }
 
 template <int MODE, int BN, bool F32>
-qsm_status launch_tile(const GemmParams& p, int most, cudaStream_t stream) {
-  using C = Cfg<BN>;
+qsm_status launch_tile(GemmParams& p, int most, uint64_t rows, cudaStream_t stream) {
+  using C = Cfg<MODE, BN, F32>;
   auto* k = mx4_gemm_kernel<MODE, BN, F32>;
   static thread_local int ready_dev = -1;  // the attribute is per device
   int dev = 0;
@@ -384,6 +440,13 @@ qsm_status launch_tile(const GemmParams& p, int most, cudaStream_t stream) {
     QSM_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
     ready_dev = dev;
   }
+  if (MODE != kGateUp && p.vec &&
+      !make_out_map(&p.y_map, p.y, MODE == kDown ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                   : F32         ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    C::kEl, rows, p.N, p.ldy, C::kBoxCols,
+                    C::kInner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return QSM_ERR_CUDA;
   const int grid = most < sm_count() ? most : sm_count();
   QSM_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(kThreads), C::kSmem, stream, p));
   return QSM_OK;
@@ -395,16 +458,20 @@ qsm_status launch_dense(GemmParams& p, const qsm_mx4* w, bool f32, cudaStream_t 
   p.nsub = (p.N + BN - 1) / BN;
   if ((long long)p.tiles * p.nsub > (1ll << 30)) return QSM_ERR_UNSUPPORTED;
   const int most = p.tiles * p.nsub;
-  return f32 ? launch_tile<kDense, BN, true>(p, most, stream)
-             : launch_tile<kDense, BN, false>(p, most, stream);
+  return f32 ? launch_tile<kDense, BN, true>(p, most, p.M, stream)
+             : launch_tile<kDense, BN, false>(p, most, p.M, stream);
 }
 
 }  // namespace
 
-qsm_status launch_grouped(const GemmParams& p, int mode, cudaStream_t stream) {
+bool make_a_maps(GemmParams* p, const void* codes, uint64_t rows, int K) {
+  return make_codes_map(&p->a, codes, rows, K, 128) && make_codes_map(&p->a32, codes, rows, K, 32);
+}
+
+qsm_status launch_grouped(GemmParams& p, int mode, uint64_t rows, cudaStream_t stream) {
   const int most = 1 << 30;  // how many tiles there are is known on the device only
-  return mode == kGateUp ? launch_tile<kGateUp, 256, false>(p, most, stream)
-                         : launch_tile<kDown, 256, false>(p, most, stream);
+  return mode == kGateUp ? launch_tile<kGateUp, 256, false>(p, most, rows, stream)
+                         : launch_tile<kDown, 256, false>(p, most, rows, stream);
 }
 
 }  // namespace mx4
@@ -434,7 +501,7 @@ extern "C" qsm_status mx4_gemm(const qsm_mx4* a, const qsm_mx4* w, int32_t dtype
   p.a_scales = a->scales;
   p.w_scales = w->scales;
   p.status = dev_status;
-  if (!make_codes_map(&p.a, a->codes, a->rows, a->cols, 128)) return QSM_ERR_CUDA;
+  if (!make_a_maps(&p, a->codes, a->rows, a->cols)) return QSM_ERR_CUDA;
   // the widest tile that still gives every SM one
   const int nsm = sm_count();
   const long long t256 = (long long)p.tiles * ((p.N + 255) / 256);

@@ -16,8 +16,9 @@ enum { kDense = 0, kGateUp = 1, kDown = 2 };
 constexpr float kOutScale = 1.0f / 16.0f;  // of the grouped outputs held in fp16
 
 struct GemmParams {
-  CUtensorMap a;         // codes of a, boxes of 128 rows
+  CUtensorMap a, a32;    // codes of a, boxes of 128 and of 32 rows
   CUtensorMap w, w_sh;   // codes of w (routed, shared), boxes of BN rows (gate_up: 128)
+  CUtensorMap y_map;     // y, boxes of 32 rows (where vec)
   const uint8_t* a_scales;
   const uint8_t* w_scales;
   const uint8_t* w_scales_sh;
@@ -27,7 +28,7 @@ struct GemmParams {
   // dense and down
   void* y;
   size_t ldy;
-  int vec;               // rows of y are 16-byte aligned
+  int vec;               // rows of y are 16-byte aligned: stored by TMA
   // grouped: tile tau < shared_tiles holds tokens 128 tau .. of the shared
   // expert, the others the blocks of tile_map (expert, first sorted row);
   // tile tau's rows of a (and of h and of y) start at 128 tau
@@ -41,7 +42,10 @@ struct GemmParams {
 };
 
 bool mx4_valid(const qsm_mx4* w);
-qsm_status launch_grouped(const GemmParams& p, int mode, cudaStream_t stream);
+// The maps of a (rows x K codes).
+bool make_a_maps(GemmParams* p, const void* codes, uint64_t rows, int K);
+// gate_up, or down with p.y of `rows` rows of p.N fp16.
+qsm_status launch_grouped(GemmParams& p, int mode, uint64_t rows, cudaStream_t stream);
 
 }  // namespace mx4
 }  // namespace qsm

@@ -24,8 +24,8 @@ namespace {
 
 constexpr float kOutScaleInv = 16.0f;
 constexpr int kPrepThreads = 256;
-constexpr int kPrepTiles = 4;  // column tiles per warp and token
 constexpr int kCombThreads = 128;
+constexpr int kCombCols = 8;
 constexpr int kMaxK = 32;
 
 // Exclusive prefix sums over the experts of their blocks of 128 rows, into
@@ -60,8 +60,10 @@ __device__ __forceinline__ void block_starts(const int32_t* counts, int E, int* 
 // them: row t (shared expert), and for assignment (t, j) row
 //   128 (shared_tiles + blocks of the experts before) + its rank in the expert,
 // kept in pos[t k + j] for the combine (-1: no valid expert).  One warp takes
-// kPrepTiles column tiles of a token, 16 lanes to a tile: x is read once and
-// its codes written k + 1 times.
+// 32 blocks (1024 columns) of a token, a block to a lane: x is read once, the
+// maximum needs no other lane, and each of the k + 1 copies of a block's
+// codes is one 16-byte store.  The lanes whose block starts a scale tile's
+// row store the row's four scales.
 __global__ void __launch_bounds__(kPrepThreads)
 mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
                    const int32_t* __restrict__ topk_idx, const int32_t* __restrict__ inv_perm,
@@ -72,12 +74,17 @@ mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
   pdl_wait();
   pdl_launch_dependents();
   block_starts(counts, E, start);
-  const int lane = threadIdx.x & 31, l16 = lane & 15;
-  const int cts = col_tiles(H), cgs = (cts + kPrepTiles - 1) / kPrepTiles;
-  const long long units = (long long)T * cgs, stride = (long long)gridDim.x * (kPrepThreads / 32);
+  const int lane = threadIdx.x & 31;
+  const int cts = col_tiles(H), cgs = (H + 1023) / 1024;
+  const int units = T * cgs, stride = gridDim.x * (kPrepThreads / 32);
   bool bad = false;
-  for (long long u = (long long)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5); u < units; u += stride) {
-    const int t = (int)(u / cgs), cg = (int)(u % cgs);
+  for (int u = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5); u < units; u += stride) {
+    const int t = u / cgs, cg = u - t * cgs, b = cg * 32 + lane;  // token, block
+    const bool live = b * kBlock < H;
+    uint4 raw[4];
+    const uint4* src = reinterpret_cast<const uint4*>(x + (size_t)t * H + (live ? b : 0) * kBlock);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i] = __ldg(src + i);
     int dst = -1;  // lane j: the row of assignment (t, j)
     if (lane < k) {
       const int e = __ldcg(topk_idx + (size_t)t * k + lane);
@@ -86,42 +93,34 @@ mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
         dst = 128 * (shared_tiles + start[e]) + at - __ldcg(offsets + e);
       if (cg == 0) pos[(size_t)t * k + lane] = dst;
     }
-    uint4 raw[kPrepTiles / 2];
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+    uint32_t m = 0;
 #pragma unroll
-    for (int z = 0; z < kPrepTiles / 2; ++z) {
-      const int c = (cg * kPrepTiles + 2 * z + (lane >> 4)) * kTileCols + 8 * l16;
-      raw[z] = c < H ? __ldcg(reinterpret_cast<const uint4*>(x + (size_t)t * H + c))
-                     : make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int i = 0; i < 16; ++i)
+      m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+    const uint32_t s = scale_of(m);
+    if (live && s == 255u) bad = true;
+    const float inv = s == 255u ? 0.f : inv_scale(s);
+    uint32_t c[4];
 #pragma unroll
-    for (int z = 0; z < kPrepTiles / 2; ++z) {
-      const int ct = cg * kPrepTiles + 2 * z + (lane >> 4), c = ct * kTileCols + 8 * l16;
-      const uint32_t w[4] = {raw[z].x, raw[z].y, raw[z].z, raw[z].w};
+    for (int i = 0; i < 4; ++i) {
       float v[8];
-      uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(w[i]);
-        v[2 * i + 1] = bf16_hi(w[i]);
-        m = max(m, max(__float_as_uint(v[2 * i]) & 0x7fffffffu, __float_as_uint(v[2 * i + 1]) & 0x7fffffffu));
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16_lo(w[4 * i + j]) * inv;
+        v[2 * j + 1] = bf16_hi(w[4 * i + j]) * inv;
       }
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const uint32_t s = scale_of(m);
-      uint32_t sw = s << (8 * (l16 >> 2));
-      sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
-      sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
-      if (s == 255u) bad = true;
-      const float inv = s == 255u ? 0.f : inv_scale(s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= inv;
-      const uint32_t word = f32x8_to_e2m1x8(v);
-      for (int j = -1; j < k; ++j) {
-        const int r = j < 0 ? t : __shfl_sync(0xffffffffu, dst, j);
-        if (r < 0 || c >= H) continue;
-        *reinterpret_cast<uint32_t*>(codes + ((size_t)r * H + c) / 2) = word;
-        if (l16 == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(r, ct, cts)) = sw;
-      }
+      c[i] = f32x8_to_e2m1x8(v);
+    }
+    const uint4 code = make_uint4(c[0], c[1], c[2], c[3]);
+    uint32_t sw = s << (8 * (lane & 3));
+    sw |= __shfl_xor_sync(0xffffffffu, sw, 1);
+    sw |= __shfl_xor_sync(0xffffffffu, sw, 2);
+    for (int j = -1; j < k; ++j) {
+      const int r = j < 0 ? t : __shfl_sync(0xffffffffu, dst, j);
+      if (r < 0 || !live) continue;
+      reinterpret_cast<uint4*>(codes)[(size_t)r * (H / kBlock) + b] = code;
+      if ((lane & 3) == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(r, b >> 2, cts)) = sw;
     }
   }
   if (bad) set_status(status, QSM_DEV_NONFINITE);
@@ -129,8 +128,8 @@ mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
 
 // y[t] from the shared expert's output row and those of the token's
 // assignments.  HALF: o holds fp16 of 1/16, rows pos[t k + j] and t; else
-// fp32, rows inv_perm[t k + j] and T k + t.  A CTA takes 4 columns per
-// thread of one token.
+// fp32, rows inv_perm[t k + j] and T k + t.  A thread takes 8 columns of one
+// token, with the loads of eight assignments in flight.
 template <bool HALF>
 __global__ void __launch_bounds__(kCombThreads)
 mx4_combine_kernel(const void* __restrict__ o, const int32_t* __restrict__ at,
@@ -141,7 +140,7 @@ mx4_combine_kernel(const void* __restrict__ o, const int32_t* __restrict__ at,
   __shared__ float wts[kMaxK], red[kCombThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
-  const int per = (H / 4 + kCombThreads - 1) / kCombThreads;  // CTAs per token
+  const int per = (H / kCombCols + kCombThreads - 1) / kCombThreads;  // CTAs per token
   const int t = blockIdx.x / per, tid = threadIdx.x;
   if (tid < k) {
     rows[tid] = __ldcg(at + (size_t)t * k + tid);
@@ -162,43 +161,58 @@ mx4_combine_kernel(const void* __restrict__ o, const int32_t* __restrict__ at,
     for (int w = 0; w < kCombThreads / 32; ++w) z += red[w];
     g = 1.0f / (1.0f + __expf(-z));
   }
-  const int c = (blockIdx.x % per * kCombThreads + tid) * 4;
+  const int c = (blockIdx.x % per * kCombThreads + tid) * kCombCols;
   if (c >= H) return;
-  auto load = [&](size_t row) {
-    float4 v;
-    if (HALF) {
-      const uint2 h = __ldcg(reinterpret_cast<const uint2*>(static_cast<const __half*>(o) + row * H + c));
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
-      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
-      v = make_float4(a.x, a.y, b.x, b.y);
-    } else {
-      v = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(o) + row * H + c));
-    }
-    return v;
+  constexpr int NV = HALF ? 1 : 2;  // 16-byte loads per row
+  struct Row {
+    uint4 v[NV];
   };
-  float4 s = load(HALF ? (size_t)t : (size_t)T * k + t);
-  s = make_float4(s.x * g, s.y * g, s.z * g, s.w * g);
+  auto load = [&](size_t row) {
+    Row r;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(o) + (row * H + c) * (HALF ? 2 : 4));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) r.v[i] = __ldcg(src + i);
+    return r;
+  };
+  auto add = [&](float (&s)[kCombCols], const Row& r, float w) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < kCombCols; ++i) {
+      float v;
+      if (HALF) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(q + i / 2));
+        v = i & 1 ? f.y : f.x;
+      } else {
+        v = __uint_as_float(q[i]);
+      }
+      s[i] = fmaf(w, v, s[i]);
+    }
+  };
+  float s[kCombCols] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const Row first = load(HALF ? (size_t)t : (size_t)T * k + t);
   for (int j0 = 0; j0 < k; j0 += 8) {  // eight rows' loads in flight
-    float4 v[8];
+    Row v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j0 + j < k && rows[j0 + j] >= 0) v[j] = load((size_t)rows[j0 + j]);
+    if (j0 == 0) add(s, first, g);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j0 + j >= k || rows[j0 + j] < 0) continue;
-      const float w = wts[j0 + j];
-      s.x = fmaf(w, v[j].x, s.x);
-      s.y = fmaf(w, v[j].y, s.y);
-      s.z = fmaf(w, v[j].z, s.z);
-      s.w = fmaf(w, v[j].w, s.w);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < k && rows[j0 + j] >= 0) add(s, v[j], wts[j0 + j]);
   }
-  if (HALF) s = make_float4(s.x * kOutScaleInv, s.y * kOutScaleInv, s.z * kOutScaleInv, s.w * kOutScaleInv);
   const size_t off = (size_t)t * H + c;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
-  *reinterpret_cast<uint2*>(y + off) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                                  *reinterpret_cast<const uint32_t*>(&hi));
-  if (y32) *reinterpret_cast<float4*>(y32 + off) = s;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (HALF) s[2 * i] *= kOutScaleInv, s[2 * i + 1] *= kOutScaleInv;
+    const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * i], s[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(y + off) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (y32) {
+    *reinterpret_cast<float4*>(y32 + off) = make_float4(s[0], s[1], s[2], s[3]);
+    *reinterpret_cast<float4*>(y32 + off + 4) = make_float4(s[4], s[5], s[6], s[7]);
+  }
 }
 
 // ---------------------------------------------------------------------- host
@@ -336,7 +350,7 @@ qsm_status many_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x
   const int H = L->H, I = L->I, E = L->E;
   uint8_t* xc = reinterpret_cast<uint8_t*>(ws + pl.xc);
   uint8_t* xs = reinterpret_cast<uint8_t*>(ws + pl.xs);
-  const long long units = (long long)T * ((col_tiles(H) + kPrepTiles - 1) / kPrepTiles);
+  const long long units = (long long)T * ((H + 1023) / 1024);
   const long long ctas = (units + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
   const int grid = (int)(ctas < 8ll * sm_count() ? ctas : 8ll * sm_count());
   QSM_CUDA_TRY(launch_pdl(mx4_scatter_kernel, dim3(grid), dim3(kPrepThreads), (size_t)E * 4, stream, x,
@@ -344,7 +358,7 @@ qsm_status many_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x
                           (const int32_t*)g.counts, (const int32_t*)g.offsets, pl.shared_tiles, xc, xs,
                           reinterpret_cast<int32_t*>(ws + pl.pos), status));
   GemmParams p = {};
-  bool ok = make_codes_map(&p.a, xc, pl.rows, H, 128) &&
+  bool ok = make_a_maps(&p, xc, pl.rows, H) &&
             make_codes_map(&p.w, L->gate_up.codes, (uint64_t)E * 2 * I, H, 128) &&
             make_codes_map(&p.w_sh, L->shared_gate_up.codes, (uint64_t)2 * I, H, 128);
   p.a_scales = xs;
@@ -363,7 +377,7 @@ qsm_status many_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x
   p.h_scales = reinterpret_cast<uint8_t*>(ws + pl.hs);
   p.status = status;
   GemmParams d = p;
-  ok &= make_codes_map(&d.a, p.h_codes, pl.rows, I, 128) &&
+  ok &= make_a_maps(&d, p.h_codes, pl.rows, I) &&
         make_codes_map(&d.w, L->down.codes, (uint64_t)E * H, I, 256) &&
         make_codes_map(&d.w_sh, L->shared_down.codes, (uint64_t)H, I, 256);
   if (!ok) return QSM_ERR_CUDA;
@@ -376,8 +390,8 @@ qsm_status many_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x
   d.y = ws + pl.o;
   d.ldy = H;
   d.vec = 1;
-  const qsm_status st = launch_grouped(p, kGateUp, stream);
-  return st != QSM_OK ? st : launch_grouped(d, kDown, stream);
+  const qsm_status st = launch_grouped(p, kGateUp, pl.rows, stream);
+  return st != QSM_OK ? st : launch_grouped(d, kDown, pl.rows, stream);
 }
 
 }  // namespace
@@ -431,7 +445,7 @@ extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x,
                              : many_tokens(L, p, x, T, topk_idx, g, ws, dev_status, stream);
   if (st != QSM_OK) return st;
   const bool half = acts == QSM_ACTS_MX4;
-  const dim3 grid((unsigned)T * ((L->H / 4 + kCombThreads - 1) / kCombThreads));
+  const dim3 grid((unsigned)T * ((L->H / kCombCols + kCombThreads - 1) / kCombThreads));
   auto* comb = half ? mx4_combine_kernel<true> : mx4_combine_kernel<false>;
   QSM_CUDA_TRY(launch_pdl(comb, grid, dim3(kCombThreads), 0, stream, (const void*)(ws + p.o),
                           (const int32_t*)i32(half ? p.pos : p.inv_perm), (const float*)topk_w, x,

@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
+constexpr size_t kMaxUnits = 1u << 30;  // (row, column tile) pairs of a call: 2^37 values
 
 // Eight columns of a row as raw words (16 or 32 bytes).
 template <int DT>
@@ -63,29 +64,31 @@ __device__ __forceinline__ void widen(const Raw<DT>& r, float (&v)[8]) {
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
-mx4_quantize_kernel(const void* __restrict__ x, size_t row_stride, int rows, int cols, int cts,
-                    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                    int32_t* status) {
+mx4_quantize_kernel(const void* __restrict__ x, size_t row_stride, uint32_t rows, uint32_t cols,
+                    FastDiv cts, uint32_t units, uint8_t* __restrict__ codes,
+                    uint8_t* __restrict__ scales, int32_t* status) {
   pdl_wait();
   pdl_launch_dependents();
-  const int l16 = threadIdx.x & 15;
-  const size_t units = (size_t)row_tiles(rows) * kTileRows * cts;  // (row, column tile)
-  const size_t stride = (size_t)gridDim.x * (kThreads / 16);
+  const uint32_t l16 = threadIdx.x & 15;
+  const uint32_t stride = gridDim.x * (kThreads / 16);
   bool bad = false;
-  for (size_t u0 = (size_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16; u0 < units;
-       u0 += kUnroll * stride) {
+  // units: (row, column tile), padded rows included; an even number, so the
+  // two halves of a warp stay together
+  for (uint32_t u0 = blockIdx.x * (kThreads / 16) + threadIdx.x / 16; u0 < units; u0 += kUnroll * stride) {
     Raw<DT> raw[kUnroll];
+    uint32_t row[kUnroll], ct[kUnroll];
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const size_t u = u0 + k * stride;
-      const int r = (int)(u / cts), c = (int)(u % cts) * kTileCols + 8 * l16;
+      const uint32_t u = u0 + k * stride;
+      row[k] = cts.div(u);
+      ct[k] = u - row[k] * cts.d;
+      const uint32_t c = ct[k] * kTileCols + 8 * l16;
       raw[k].a = raw[k].b = make_uint4(0u, 0u, 0u, 0u);
-      if (u < units && r < rows && c < cols) raw[k] = load8<DT>(x, (size_t)r * row_stride + c);
+      if (row[k] < rows && c < cols) raw[k] = load8<DT>(x, (size_t)row[k] * row_stride + c);
     }
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const size_t u = u0 + k * stride;
-      const int r = (int)(u / cts), ct = (int)(u % cts), c = ct * kTileCols + 8 * l16;
+      const uint32_t r = row[k], c = ct[k] * kTileCols + 8 * l16;
       float v[8];
       widen<DT>(raw[k], v);
       uint32_t m = 0;
@@ -98,9 +101,8 @@ mx4_quantize_kernel(const void* __restrict__ x, size_t row_stride, int rows, int
       uint32_t sw = s << (8 * (l16 >> 2));
       sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
       sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
-      if (u >= units) continue;
-      if (l16 == 0)
-        *reinterpret_cast<uint32_t*>(scales + scale_word(r, ct, cts)) = sw;
+      if (u0 + k * stride >= units) continue;
+      if (l16 == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(r, ct[k], cts.d)) = sw;
       if (r >= rows || c >= cols) continue;
       if (s == 255u) bad = true;
       const float inv = s == 255u ? 0.f : inv_scale(s);
@@ -122,41 +124,33 @@ __device__ __forceinline__ float code_value(uint32_t n) {
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
 mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                      int experts, int rows, int cols, int cts, size_t scale_bytes,
+                      FastDiv rows, uint32_t cols, FastDiv cts, uint32_t units, size_t scale_bytes,
                       void* __restrict__ y) {
   pdl_wait();
   pdl_launch_dependents();
-  const int l16 = threadIdx.x & 15;
-  const size_t units = (size_t)experts * rows * cts;
-  const size_t stride = (size_t)gridDim.x * (kThreads / 16);
-  for (size_t u0 = (size_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16; u0 < units;
-       u0 += kUnroll * stride) {
-    uint32_t w[kUnroll], sw[kUnroll];
+  const uint32_t l16 = threadIdx.x & 15;
+  const uint32_t stride = gridDim.x * (kThreads / 16);
+  for (uint32_t u0 = blockIdx.x * (kThreads / 16) + threadIdx.x / 16; u0 < units; u0 += kUnroll * stride) {
+    uint32_t w[kUnroll], sw[kUnroll], row[kUnroll], c[kUnroll];  // row: of all experts
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const size_t u = u0 + k * stride;
-      w[k] = sw[k] = 0u;
-      if (u >= units) continue;
-      const size_t row = u / cts;
-      const int ct = (int)(u % cts), c = ct * kTileCols + 8 * l16;
-      const int e = (int)(row / rows), r = (int)(row % rows);
-      if (c >= cols) continue;
-      w[k] = __ldcg(reinterpret_cast<const uint32_t*>(codes + (row * cols + c) / 2));
-      sw[k] = __ldcg(reinterpret_cast<const uint32_t*>(scales + e * scale_bytes +
-                                                       scale_word(r, ct, cts)));
+      const uint32_t u = u0 + k * stride;
+      row[k] = cts.div(u);
+      const uint32_t ct = u - row[k] * cts.d;
+      c[k] = u < units ? ct * kTileCols + 8 * l16 : cols;
+      if (c[k] >= cols) continue;
+      const uint32_t e = rows.div(row[k]), r = row[k] - e * rows.d;
+      w[k] = __ldcg(reinterpret_cast<const uint32_t*>(codes + ((size_t)row[k] * cols + c[k]) / 2));
+      sw[k] = __ldcg(reinterpret_cast<const uint32_t*>(scales + e * scale_bytes + scale_word(r, ct, cts.d)));
     }
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const size_t u = u0 + k * stride;
-      if (u >= units) continue;
-      const size_t row = u / cts;
-      const int c = (int)(u % cts) * kTileCols + 8 * l16;
-      if (c >= cols) continue;
+      if (c[k] >= cols) continue;
       const float s = scale_value((sw[k] >> (8 * (l16 >> 2))) & 255u);
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = code_value((w[k] >> (4 * i)) & 15u) * s;
-      const size_t o = row * cols + c;
+      const size_t o = (size_t)row[k] * cols + c[k];
       if (DT == QSM_FP32) {
         float4* p = reinterpret_cast<float4*>(static_cast<float*>(y) + o);
         p[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -219,12 +213,15 @@ extern "C" qsm_status mx4_quantize(const void* x, int32_t dtype, int64_t row_str
       !aligned16(scales) || !aligned4(dev_status))
     return QSM_ERR_INVALID_ARGUMENT;
   const int cts = col_tiles(cols);
-  const dim3 grid(grid_for((size_t)row_tiles(rows) * kTileRows * cts));
+  const size_t units = (size_t)row_tiles(rows) * kTileRows * cts;
+  if (units > kMaxUnits) return QSM_ERR_UNSUPPORTED;
+  const dim3 grid(grid_for(units));
   auto* kernel = dtype == QSM_BF16   ? mx4_quantize_kernel<QSM_BF16>
                  : dtype == QSM_FP16 ? mx4_quantize_kernel<QSM_FP16>
                                      : mx4_quantize_kernel<QSM_FP32>;
   QSM_CUDA_TRY(launch_pdl(kernel, grid, dim3(kThreads), 0, stream, x, (size_t)row_stride,
-                          (int)rows, (int)cols, cts, codes, scales, dev_status));
+                          (uint32_t)rows, (uint32_t)cols, FastDiv(cts), (uint32_t)units, codes,
+                          scales, dev_status));
   return QSM_OK;
 }
 
@@ -236,12 +233,14 @@ extern "C" qsm_status mx4_dequantize(const qsm_mx4* a, int32_t dtype, void* y,
   if (a->rows == 0 && a->experts >= 1) return QSM_OK;
   if (!mx4_valid(a) || !y || !aligned16(y)) return QSM_ERR_INVALID_ARGUMENT;
   const int cts = col_tiles(a->cols);
-  const dim3 grid(grid_for((size_t)a->experts * a->rows * cts));
+  const size_t units = (size_t)a->experts * a->rows * cts;
+  if (units > kMaxUnits) return QSM_ERR_UNSUPPORTED;
+  const dim3 grid(grid_for(units));
   auto* kernel = dtype == QSM_BF16   ? mx4_dequantize_kernel<QSM_BF16>
                  : dtype == QSM_FP16 ? mx4_dequantize_kernel<QSM_FP16>
                                      : mx4_dequantize_kernel<QSM_FP32>;
   QSM_CUDA_TRY(launch_pdl(kernel, grid, dim3(kThreads), 0, stream, a->codes, a->scales,
-                          (int)a->experts, (int)a->rows, (int)a->cols, cts,
+                          FastDiv(a->rows), (uint32_t)a->cols, FastDiv(cts), (uint32_t)units,
                           mx4_scale_bytes(a->rows, a->cols), y));
   return QSM_OK;
 }

@@ -12,6 +12,8 @@ import dataclasses
 
 import torch
 
+from . import QSMError, _check, lib, route_flags
+
 BLOCK = 32            # columns per scale
 TILE_ROWS = 128       # rows and columns of a scale tile
 TILE_COLS = 128
@@ -54,9 +56,39 @@ def declare(L: ctypes.CDLL) -> None:
         f.restype = st
 
 
-def _q():
-    import quantized_sparse_moe_gb300 as q
-    return q
+# The calls below take a few microseconds of host time each, which is what
+# bounds their smallest sizes: they look the library up once, read each
+# property of a tensor once, pass plain integers, and allocate with
+# torch.empty (Tensor.new_empty took 3.5 us more between launches).
+_lib = None
+_stream_of = torch._C._cuda_getCurrentRawStream
+_words: dict = {}
+
+
+def _load():
+    global _lib
+    _lib = lib()
+    return _lib
+
+
+def _word(device: int) -> int:
+    """A status word of the device, for the calls that are given none (it only
+    ever collects bits)."""
+    w = _words.get(device)
+    if w is None:
+        t = torch.zeros(1, dtype=torch.int32, device=f"cuda:{device}")
+        w = _words[device] = (t.data_ptr(), t)
+    return w[0]
+
+
+def _matrix(x: torch.Tensor, what: str):
+    """(device, rows, columns, row stride) of a CUDA matrix whose rows are
+    contiguous."""
+    shape, stride, dev = x.shape, x.stride(), x.get_device()
+    if len(shape) != 2 or dev < 0 or (stride[1] != 1 and shape[1] > 1):
+        raise QSMError(f"{what}: needs a CUDA matrix with contiguous rows")
+    rows, cols = shape
+    return dev, rows, cols, stride[0] if rows > 1 else (cols + 7) // 8 * 8
 
 
 def mx4_scale_bytes(rows: int, cols: int) -> int:
@@ -74,7 +106,7 @@ def mx4_tile_scales(scales: torch.Tensor) -> torch.Tensor:
     return t.permute(0, 1, 4, 3, 2, 5).reshape(-1).contiguous()
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(eq=False)
 class Mx4Tensor:
     """An MXFP4 matrix, or `experts` of them: codes uint8
     [experts * rows, cols / 2] (any shape of that size) and scale tiles uint8,
@@ -87,14 +119,18 @@ class Mx4Tensor:
 
     def __post_init__(self):
         if self.cols % BLOCK or self.cols < BLOCK or self.rows < 0 or self.experts < 1:
-            raise _q().QSMError("Mx4Tensor: cols must be a positive multiple of 32")
+            raise QSMError("Mx4Tensor: cols must be a positive multiple of 32")
         n = self.experts * self.rows * self.cols // 2
         sb = self.experts * mx4_scale_bytes(self.rows, self.cols)
         for t, size, what in ((self.codes, n, "codes"), (self.scales, sb, "scales")):
             if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != size:
-                raise _q().QSMError(f"Mx4Tensor: {what} must be {size} contiguous bytes")
+                raise QSMError(f"Mx4Tensor: {what} must be {size} contiguous bytes")
+        self.device, self.torch_device = self.codes.get_device(), self.codes.device
+        if self.device < 0 or self.scales.get_device() != self.device:
+            raise QSMError("Mx4Tensor: codes and scales must be on one GPU")
         self.c = Mx4C(self.experts, self.rows, self.cols, self.codes.data_ptr(),
                       self.scales.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, rows: int, cols: int, experts: int = 1, device="cuda") -> "Mx4Tensor":
@@ -106,97 +142,85 @@ class Mx4Tensor:
         return self.codes.numel() + self.scales.numel()
 
 
-_status_words: dict = {}
-
-
-def _word(dev_status, device):
-    """The caller's status word, or one per device that the calls without
-    one share (it only ever collects bits)."""
-    if dev_status is not None:
-        return dev_status.data_ptr()
-    w = _status_words.get(device)
-    if w is None:
-        w = _status_words[device] = torch.zeros(1, dtype=torch.int32, device=device)
-    return w.data_ptr()
-
-
-def _rows(x: torch.Tensor, what: str):
-    """(row stride) of a matrix whose rows are contiguous."""
-    if x.dim() != 2 or x.stride(1) != 1 or not x.is_cuda:
-        raise _q().QSMError(f"{what}: x must be a CUDA matrix with contiguous rows")
-    return x.stride(0) if x.shape[0] > 1 else max(x.shape[1], 8)
-
-
-def _raw_stream(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
 def mx4_quantize(x: torch.Tensor, out: Mx4Tensor | None = None, dev_status=None,
                  stream=None) -> Mx4Tensor:
     """x [rows, cols] (bf16, fp16 or fp32) -> MXFP4."""
-    q = _q()
-    if x.dtype not in _DTYPES:
-        raise q.QSMError("mx4_quantize: x must be bf16, fp16 or fp32")
-    ld = _rows(x, "mx4_quantize")
-    rows, cols = x.shape
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None:
+        raise QSMError("mx4_quantize: x must be bf16, fp16 or fp32")
+    dev, rows, cols, ld = _matrix(x, "mx4_quantize")
     if out is None:
         out = Mx4Tensor.empty(rows, cols, device=x.device)
-    elif out.rows != rows or out.cols != cols or out.experts != 1:
-        raise q.QSMError("mx4_quantize: out has another shape")
-    q._check(q.lib().mx4_quantize(x.data_ptr(), _DTYPES[x.dtype], ld, rows, cols,
-                                  out.c.codes, out.c.scales, _word(dev_status, x.device),
-                                  _raw_stream(stream, x.device)), "mx4_quantize")
+    elif out.rows != rows or out.cols != cols or out.experts != 1 or out.device != dev:
+        raise QSMError("mx4_quantize: out has another shape or device")
+    rc = (_lib or _load()).mx4_quantize(
+        x.data_ptr(), dtype, ld, rows, cols, out.c.codes, out.c.scales,
+        _word(dev) if dev_status is None else dev_status.data_ptr(),
+        _stream_of(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mx4_quantize")
     return out
 
 
 def mx4_dequantize(a: Mx4Tensor, dtype=torch.bfloat16, y=None, stream=None) -> torch.Tensor:
     """The values [experts * rows, cols] that a stands for."""
-    q = _q()
-    if dtype not in _DTYPES:
-        raise q.QSMError("mx4_dequantize: dtype must be bf16, fp16 or fp32")
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise QSMError("mx4_dequantize: dtype must be bf16, fp16 or fp32")
     if y is None:
-        y = torch.empty((a.experts * a.rows, a.cols), dtype=dtype, device=a.codes.device)
-    elif y.dtype != dtype or not y.is_contiguous() or y.numel() != a.experts * a.rows * a.cols:
-        raise q.QSMError("mx4_dequantize: y must be contiguous, of a's size and dtype")
-    q._check(q.lib().mx4_dequantize(ctypes.byref(a.c), _DTYPES[dtype], y.data_ptr(),
-                                    _raw_stream(stream, y.device)), "mx4_dequantize")
+        y = torch.empty((a.experts * a.rows, a.cols), dtype=dtype, device=a.torch_device)
+    elif (y.dtype != dtype or not y.is_contiguous() or y.numel() != a.experts * a.rows * a.cols
+          or y.get_device() != a.device):
+        raise QSMError("mx4_dequantize: y must be contiguous, of a's size and device, and dtype")
+    rc = (_lib or _load()).mx4_dequantize(
+        a.ref, dt, y.data_ptr(), _stream_of(a.device) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mx4_dequantize")
     return y
 
 
 def mx4_gemm(a: Mx4Tensor, w: Mx4Tensor, dtype=torch.bfloat16, y=None, dev_status=None,
              stream=None) -> torch.Tensor:
     """y [M, N] (bf16 or fp32) = a [M, K] w [N, K]^T."""
-    q = _q()
+    M, N, dev = a.rows, w.rows, a.device
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise QSMError("mx4_gemm: dtype must be bf16 or fp32")
+    if w.device != dev:
+        raise QSMError("mx4_gemm: a and w are on different devices")
     if y is None:
-        y = torch.empty((a.rows, w.rows), dtype=dtype, device=a.codes.device)
-    elif y.dtype != dtype or tuple(y.shape) != (a.rows, w.rows) or y.stride(1) != 1:
-        raise q.QSMError("mx4_gemm: y must be [M, N] of dtype with contiguous rows")
-    if dtype not in (torch.bfloat16, torch.float32):
-        raise q.QSMError("mx4_gemm: dtype must be bf16 or fp32")
-    ld = y.stride(0) if a.rows > 1 else max(w.rows, 1)
-    q._check(q.lib().mx4_gemm(ctypes.byref(a.c), ctypes.byref(w.c), _DTYPES[dtype], y.data_ptr(),
-                              ld, _word(dev_status, y.device), _raw_stream(stream, y.device)),
-             "mx4_gemm")
+        y = torch.empty((M, N), dtype=dtype, device=a.torch_device)
+        ld = N
+    else:
+        ydev, rows, cols, ld = _matrix(y, "mx4_gemm: y")
+        if y.dtype != dtype or rows != M or cols != N or ydev != dev:
+            raise QSMError("mx4_gemm: y must be [M, N] of dtype on the operands' device")
+    rc = (_lib or _load()).mx4_gemm(
+        a.ref, w.ref, _DTYPES[dtype], y.data_ptr(), ld,
+        _word(dev) if dev_status is None else dev_status.data_ptr(),
+        _stream_of(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mx4_gemm")
     return y
 
 
 def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, y=None, dev_status=None, stream=None) -> torch.Tensor:
     """y [T, N] bf16 = x [T, K] w [N, K]^T for at most 32 rows of bf16 x."""
-    q = _q()
-    if x.dtype != torch.bfloat16:
-        raise q.QSMError("mx4_gemv: x must be bf16")
-    ld = _rows(x, "mx4_gemv")
-    if x.shape[1] != w.cols:
-        raise q.QSMError("mx4_gemv: x and w differ in K")
+    if x.dtype is not torch.bfloat16:
+        raise QSMError("mx4_gemv: x must be bf16")
+    dev, T, K, ld = _matrix(x, "mx4_gemv")
+    if K != w.cols or w.device != dev:
+        raise QSMError("mx4_gemv: x and w differ in K or device")
     if y is None:
-        y = torch.empty((x.shape[0], w.rows), dtype=torch.bfloat16, device=x.device)
-    elif y.dtype != torch.bfloat16 or tuple(y.shape) != (x.shape[0], w.rows) or not y.is_contiguous():
-        raise q.QSMError("mx4_gemv: y must be a contiguous bf16 [T, N]")
-    q._check(q.lib().mx4_gemv(x.data_ptr(), ld, x.shape[0], ctypes.byref(w.c), y.data_ptr(),
-                              _word(dev_status, x.device), _raw_stream(stream, x.device)),
-             "mx4_gemv")
+        y = torch.empty((T, w.rows), dtype=torch.bfloat16, device=w.torch_device)
+    elif (y.dtype != torch.bfloat16 or tuple(y.shape) != (T, w.rows) or not y.is_contiguous()
+          or y.get_device() != dev):
+        raise QSMError("mx4_gemv: y must be a contiguous bf16 [T, N] on x's device")
+    rc = (_lib or _load()).mx4_gemv(
+        x.data_ptr(), ld, T, w.ref, y.data_ptr(),
+        _word(dev) if dev_status is None else dev_status.data_ptr(),
+        _stream_of(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mx4_gemv")
     return y
 
 
@@ -223,14 +247,14 @@ class Mx4Layer:
             t = mx4_quantize(w.reshape(-1, w.shape[2]))
             return Mx4Tensor(t.codes, t.scales, w.shape[1], w.shape[2], w.shape[0])
         if H % TILE_ROWS or I % TILE_ROWS:
-            raise _q().QSMError("Mx4Layer: H and I must be multiples of 128")
+            raise QSMError("Mx4Layer: H and I must be multiples of 128")
         return cls(H, I, E, k, one(gate_up), one(down), one(shared_gate_up), one(shared_down),
                    w_router, logit_bias, shared_gate)
 
 
 def moe_mx4_workspace_bytes(layer: Mx4Layer, T: int, acts: str = "bf16") -> int:
     """0 when the layer, T or acts is not supported."""
-    return int(_q().lib().moe_mx4_workspace_bytes(ctypes.byref(layer.c), T, _ACTS[acts]))
+    return int(lib().moe_mx4_workspace_bytes(ctypes.byref(layer.c), T, _ACTS[acts]))
 
 
 class Mx4Forward:
@@ -241,12 +265,11 @@ class Mx4Forward:
 
     def __init__(self, layer: Mx4Layer, T: int, acts: str = "bf16", device="cuda",
                  renormalize=True, want_f32=False, *, bias_select_only=False):
-        q = _q()
         if acts not in _ACTS:
-            raise q.QSMError('Mx4Forward: acts must be "bf16" or "mx4"')
+            raise QSMError('Mx4Forward: acts must be "bf16" or "mx4"')
         need = moe_mx4_workspace_bytes(layer, T, acts)
         if need == 0 and T > 0:
-            raise q.QSMError("Mx4Forward: unsupported layer or token count")
+            raise QSMError("Mx4Forward: unsupported layer or token count")
         self.layer, self.T, self.acts = layer, T, acts
         k, H = layer.k, layer.H
         self.topk_idx = torch.empty((T, k), dtype=torch.int32, device=device)
@@ -255,23 +278,23 @@ class Mx4Forward:
         self.y_f32 = torch.empty((T, H), dtype=torch.float32, device=device) if want_f32 else None
         self.workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=device)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=device)
-        self._fn = q.lib().moe_mx4_forward
+        self._fn = lib().moe_mx4_forward
         p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         self._mid = (T, _ACTS[acts], p(layer.w_router), p(layer.logit_bias),
-                     q.route_flags(renormalize, bias_select_only), p(self.topk_idx), p(self.topk_w))
+                     route_flags(renormalize, bias_select_only), p(self.topk_idx), p(self.topk_w))
         self._tail = (p(self.y_f32), p(self.workspace), self.workspace.numel(), p(self.dev_status))
         self._layer_ref = ctypes.byref(layer.c)
+        self._device, self._shape = self.y.get_device(), self.y.shape
 
     def __call__(self, x: torch.Tensor, stream=None, out=None) -> torch.Tensor:
         """Run the layer on x [T, H] bf16; the result goes to out (a [T, H] bf16
         tensor, contiguous) when given, else to self.y.  Returns it."""
         y = self.y if out is None else out
-        if (x.dtype != torch.bfloat16 or not x.is_contiguous() or x.shape != self.y.shape
-                or (out is not None and (out.dtype != torch.bfloat16 or not out.is_contiguous()
-                                         or out.shape != self.y.shape))):
-            raise _q().QSMError("Mx4Forward: x and out must be contiguous [T, H] bf16 tensors")
+        for t in (x,) if out is None else (x, out):
+            if t.dtype is not torch.bfloat16 or t.shape != self._shape or not t.is_contiguous():
+                raise QSMError("Mx4Forward: x and out must be contiguous [T, H] bf16 tensors")
         rc = self._fn(self._layer_ref, x.data_ptr(), *self._mid, y.data_ptr(), *self._tail,
-                      _raw_stream(stream, y.device))
+                      _stream_of(self._device) if stream is None else stream.cuda_stream)
         if rc:
-            _q()._check(rc, "moe_mx4_forward")
+            _check(rc, "moe_mx4_forward")
         return y
