@@ -189,16 +189,27 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
   tc::tc_fence_after();
   const uint32_t tmem = uniform(tmem_base);
 
-  pdl_wait();
-  pdl_launch_dependents();
-  const int tiles = MODE == kDense ? p.tiles : p.shared_tiles + __ldcg(p.n_tiles);
+  // Grouped: the routing and the weights are older than the previous launch
+  // (which let this one start after its own wait), so the first stages' weights
+  // are requested before the wait; a (and what the epilogue overwrites) is
+  // the previous launch's.
+  if (MODE == kDense) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  const int tiles = MODE == kDense ? p.tiles : p.shared_tiles + uniform(__ldcg(p.n_tiles));
   const int total = tiles * p.nsub;
   const int nst = (p.K + kStageK - 1) / kStageK;
   const int cts = col_tiles(p.K);
+  if (MODE != kDense && warp != 0) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
 
   if (warp == 0) {
     int st = 0;          // ring position, and how often it came round
     uint32_t round = 0;
+    bool waited = MODE == kDense;
     for (int item = blockIdx.x; item < total && !warp_aborted(abort_p); item += gridDim.x) {
       const Tile t = uniform_tile(tile_of<MODE, BN>(p, item));
       const bool sh = MODE != kDense && t.e < 0;
@@ -210,35 +221,60 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
       const uint8_t* wsf1 = wsc + (size_t)(groups == 2 ? t.w_tile[1] : 0) * cts * kTileBytes;
       const int a32 = (t.cnt + 31) >> 5;  // groups of 32 rows of a that exist
       const uint32_t abytes = a32 * 32 * 128;
+      auto load_w = [&](int ks, int s) {
+        unsigned char* wb = smem + s * C::kStage + C::kABytes;
+        const uint32_t sfb = (uint32_t)min(2, cts - 2 * ks) * kTileBytes;  // scale bytes of a row tile
+        mbar_arrive_expect_tx(&full[s], abytes + C::kWBytes + sfb * (1 + groups));
+        tc::tma_load_2d(wb, wm, ks * 128, t.w_row[0], &full[s]);
+        if (MODE == kGateUp) tc::tma_load_2d(wb + 128 * 128, wm, ks * 128, t.w_row[1], &full[s]);
+        unsigned char* sf = wb + C::kWBytes + C::kSfaBytes;
+        bulk_g2s(sf, wsf0 + ks * 2 * kTileBytes, sfb, &full[s]);
+        if (groups == 2) bulk_g2s(sf + 2 * kTileBytes, wsf1 + ks * 2 * kTileBytes, sfb, &full[s]);
+      };
+      auto load_a = [&](int ks, int s) {
+        unsigned char* base = smem + s * C::kStage;
+        const uint32_t sfb = (uint32_t)min(2, cts - 2 * ks) * kTileBytes;
+        if (a32 == 4) {
+          tc::tma_load_2d(base, &p.a, ks * 128, t.a_row, &full[s]);
+        } else {
+          for (int i = 0; i < a32; ++i)
+            tc::tma_load_2d(base + i * 32 * 128, &p.a32, ks * 128, t.a_row + 32 * i, &full[s]);
+        }
+        bulk_g2s(base + C::kABytes + C::kWBytes, asf + ks * 2 * kTileBytes, sfb, &full[s]);
+      };
+      int k0 = 0;
+      if (!waited) {  // the ring is empty
+        k0 = min(nst, C::kStages);
+        if (elect_one())
+          for (int ks = 0; ks < k0; ++ks) load_w(ks, ks);
+        __syncwarp();
+        pdl_wait();
+        pdl_launch_dependents();
+        waited = true;
+        if (elect_one())
+          for (int ks = 0; ks < k0; ++ks) load_a(ks, ks);
+        __syncwarp();
+        st = k0 % C::kStages;
+        round = k0 / C::kStages;
+      }
       bool ok = true;
-      for (int ks = 0; ks < nst; ++ks) {
+      for (int ks = k0; ks < nst; ++ks) {
         if (round > 0 && !warp_wait(&empty[st], (round - 1) & 1, abort_p, p.status)) {
           ok = false;
           break;
         }
         if (elect_one()) {
-          unsigned char* base = smem + st * C::kStage;
-          const uint32_t sfb = (uint32_t)min(2, cts - 2 * ks) * kTileBytes;  // scale bytes of a row tile
-          mbar_arrive_expect_tx(&full[st], abytes + C::kWBytes + sfb * (1 + groups));
-          if (a32 == 4) {
-            tc::tma_load_2d(base, &p.a, ks * 128, t.a_row, &full[st]);
-          } else {
-            for (int i = 0; i < a32; ++i)
-              tc::tma_load_2d(base + i * 32 * 128, &p.a32, ks * 128, t.a_row + 32 * i, &full[st]);
-          }
-          unsigned char* wb = base + C::kABytes;
-          tc::tma_load_2d(wb, wm, ks * 128, t.w_row[0], &full[st]);
-          if (MODE == kGateUp) tc::tma_load_2d(wb + 128 * 128, wm, ks * 128, t.w_row[1], &full[st]);
-          unsigned char* sf = wb + C::kWBytes;
-          bulk_g2s(sf, asf + ks * 2 * kTileBytes, sfb, &full[st]);
-          bulk_g2s(sf + C::kSfaBytes, wsf0 + ks * 2 * kTileBytes, sfb, &full[st]);
-          if (groups == 2)
-            bulk_g2s(sf + C::kSfaBytes + 2 * kTileBytes, wsf1 + ks * 2 * kTileBytes, sfb, &full[st]);
+          load_w(ks, st);
+          load_a(ks, st);
         }
         __syncwarp();
         if (++st == C::kStages) st = 0, ++round;
       }
       if (!ok) break;
+    }
+    if (!waited) {  // no item
+      pdl_wait();
+      pdl_launch_dependents();
     }
     // after an abort, let the copies in flight land before the CTA exits
     for (int i = 0; i < C::kStages; ++i) {

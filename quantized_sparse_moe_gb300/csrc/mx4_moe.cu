@@ -244,7 +244,7 @@ bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
     if (T > QSM_MX4_MOE_MAX_ROWS) return false;
     const int touched = (long long)T * k < E ? T * k : E;
     bool fit = false;
-    for (int tok = 8; tok >= 1 && !fit; tok /= 2) {
+    for (int tok = T < 8 ? T : 8; tok >= 1 && !fit; tok /= 2) {
       const int slots = touched + (T + tok - 1) / tok;
       p.gu.K = H;
       p.gu.N = 2 * I;

@@ -86,14 +86,13 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, vol
 }
 
 struct Slot {
-  int e;     // expert, -1: shared expert or dense
+  int e;     // expert, -1: shared expert or dense; -2: no such slot
   int row0;  // first row of x (dense, shared) or first sorted row (routed)
   int cnt;
 };
 
-// By all lanes of a warp.
 template <int MODE>
-__device__ __forceinline__ Slot slot_of(const StreamParams& p, int s) {
+__device__ __forceinline__ Slot load_slot(const StreamParams& p, int s) {
   Slot r;
   if (MODE == kRows || s < p.shared_tiles) {
     r.e = -1;
@@ -101,10 +100,23 @@ __device__ __forceinline__ Slot slot_of(const StreamParams& p, int s) {
     r.cnt = min(p.tok, p.T - r.row0);
   } else {
     const int2 te = __ldcg(reinterpret_cast<const int2*>(p.tile_map) + (s - p.shared_tiles));
-    r.e = uniform(te.x);
-    r.row0 = uniform(te.y);
-    r.cnt = uniform(min(p.tok, __ldcg(p.offsets + r.e + 1) - r.row0));
+    r.e = te.x < 0 ? -2 : te.x;  // entries past the last block are -1
+    r.row0 = te.y;
+    r.cnt = te.x < 0 ? 0 : p.tok == 1 ? 1 : min(p.tok, __ldcg(p.offsets + te.x + 1) - te.y);
   }
+  return r;
+}
+
+// The slots of a CTA's run of items, looked up once by all threads together.
+constexpr int kSlotTab = 64;
+
+// Slot s, by all lanes of a warp.
+template <int MODE>
+__device__ __forceinline__ Slot slot_of(const StreamParams& p, const Slot* tab, int tab0, int s) {
+  Slot r = MODE != kRows && s - tab0 < kSlotTab ? tab[s - tab0] : load_slot<MODE>(p, s);
+  r.e = uniform(r.e);
+  r.row0 = uniform(r.row0);
+  r.cnt = uniform(r.cnt);
   return r;
 }
 
@@ -185,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       acc_full[2], acc_empty[2], part_full[2], part_empty[2], done;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
+  __shared__ Slot tab[kSlotTab];
   volatile int* abort_p = &abort_flag;
 
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -208,20 +221,41 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) tc::prefetch_map(&p.w);
-  if (warp == 2) tc::tmem_alloc(&tmem_base, 512);
+  if (warp == 2) tc::tmem_alloc(&tmem_base, p.tmem_cols);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   if (cs > 1) cluster_sync_all();
   const uint32_t tmem = uniform(tmem_base);
 
-  pdl_wait();
-  pdl_launch_dependents();
-  const int slots = MODE == kRows ? p.slots : p.shared_tiles + uniform(__ldcg(p.n_tiles));
-  // this cluster's contiguous run of items (slot, tile)
-  const long long items = (long long)slots * p.ntiles;
+  // Down: the routing and the weights are older than the previous launch
+  // (which let this one start after its own wait), so the loading warp starts
+  // on them before the wait; h is the previous launch's.
+  if (MODE != kRowsDown) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  // this cluster's contiguous run of items (slot, tile): its share of all,
+  // or, with a cluster for every possible item, its own one
   const int nclus = gridDim.x / cs, clus = blockIdx.x / cs;
-  const int first = (int)(items * clus / nclus), last = (int)(items * (clus + 1) / nclus);
+  int first = clus, last = clus + 1;
+  if (!p.single) {
+    const int slots = MODE == kRows ? p.slots : p.shared_tiles + uniform(__ldcg(p.n_tiles));
+    const long long items = (long long)slots * p.ntiles;
+    first = (int)(items * clus / nclus);
+    last = (int)(items * (clus + 1) / nclus);
+  }
+  const int tab0 = first / p.ntiles;
+  if (MODE != kRows) {
+    if (threadIdx.x < kSlotTab && (int)threadIdx.x <= (last - 1) / p.ntiles - tab0)
+      tab[threadIdx.x] = load_slot<MODE>(p, tab0 + threadIdx.x);
+    __syncthreads();
+    if (p.single && tab[0].e == -2) last = first;
+  }
+  if (MODE == kRowsDown && warp != 0) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
   // this CTA's stages of K
   const int nst = (p.K + kStageK - 1) / kStageK, cts = col_tiles(p.K);
   const int s0 = nst * rank / cs, s1 = nst * (rank + 1) / cs;
@@ -232,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
     Slot sl = {};
     for (int item = first; item < last && !warp_aborted(abort_p); ++item) {
       const int s = item / p.ntiles, tile = item - s * p.ntiles;
-      if (s != slot) sl = slot_of<MODE>(p, slot = s);
+      if (s != slot) sl = slot_of<MODE>(p, tab, tab0, slot = s);
       const bool sh = MODE != kRows && sl.e < 0;
       const CUtensorMap* wm = sh ? &p.w_sh : &p.w;
       const int row0 = (sl.e < 0 ? 0 : sl.e * p.N) + tile * 128;
@@ -279,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
         if (slot >= 0 && elect_one()) tc::mma_commit(&dig_empty[db]);
         __syncwarp();
         slot = s;
-        n = kDigits * slot_of<MODE>(p, s).cnt;
+        n = kDigits * slot_of<MODE>(p, tab, tab0, s).cnt;
         db = ndig % p.nb;
         if (!warp_wait(&dig_full[db], (ndig / p.nb) & 1, abort_p, p.status)) break;
         ++ndig;
@@ -344,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       const int db = ndig % p.nb;
       if (ndig >= p.nb && !warp_wait(&dig_empty[db], (ndig / p.nb - 1) & 1, abort_p, p.status)) break;
       ++ndig;
-      const Slot sl = slot_of<MODE>(p, s);
+      const Slot sl = slot_of<MODE>(p, tab, tab0, s);
       const int per = (s1 - s0) * 32, total = sl.cnt * per;  // groups of 8 columns
       unsigned char* dig = smem + p.dig_off + db * p.segs * p.tok * 1024;
       unsigned char* sf = smem + p.sf_off + db * p.segs * 2 * p.groups * kTileBytes;
@@ -384,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
     for (int item = first; item < last; ++item) {
       const int j = item - first, ab = j % p.nacc, pb = j & 1;
       const int s = item / p.ntiles, tile = item - s * p.ntiles;
-      if (s != slot) sl = slot_of<MODE>(p, slot = s);
+      if (s != slot) sl = slot_of<MODE>(p, tab, tab0, slot = s);
       if (!warp_wait(&acc_full[ab], (j / p.nacc) & 1, abort_p, p.status)) break;
       tc::tc_fence_after();
       if (cs > 1 && j >= 2 &&
@@ -455,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (warp == 2) tc::tmem_dealloc(tmem, 512);
+  if (warp == 2) tc::tmem_dealloc(tmem, p.tmem_cols);
   if (cs > 1) cluster_sync_all();  // no CTA leaves while another writes to it
 }
 
@@ -504,12 +538,29 @@ int resident_clusters(void* kernel, int cs, int smem, int nsm) {
   return n;
 }
 
+void* kernel_of(int mode) {
+  return mode == kRows         ? reinterpret_cast<void*>(mx4_rows_kernel<kRows>)
+         : mode == kRowsGateUp ? reinterpret_cast<void*>(mx4_rows_kernel<kRowsGateUp>)
+                               : reinterpret_cast<void*>(mx4_rows_kernel<kRowsDown>);
+}
+
 template <int MODE>
 qsm_status launch_mode(StreamParams& p, int items, cudaStream_t stream) {
   auto* k = mx4_rows_kernel<MODE>;
-  const int smem = layout(&p, stage_bytes<MODE>(), mats<MODE>());
+  constexpr int NM = mats<MODE>();
+  int smem = layout(&p, stage_bytes<MODE>(), NM);
   const int nc = resident_clusters(reinterpret_cast<void*>(k), p.cs, smem, sm_count());
   if (nc < 1) return QSM_ERR_CUDA;
+  // With few items a CTA takes only the shared and tensor memory that its
+  // own need: the next launch's CTAs then start beside it.
+  const int per = (items + nc - 1) / nc;
+  p.single = per == 1 && MODE != kRows;
+  if (per == 1) p.nb = p.nacc = 1;
+  if (per * p.segs < p.stages) p.stages = per * p.segs;
+  smem = layout(&p, stage_bytes<MODE>(), NM);
+  const int cols = p.nacc * NM * p.acc_cols + 2 * (8 * NM + 8 * p.groups);
+  p.tmem_cols = 32;
+  while (p.tmem_cols < cols) p.tmem_cols *= 2;
   const dim3 grid((items < nc ? items : nc) * p.cs);
   if (p.cs > 1)
     QSM_CUDA_TRY(launch_pdl_cluster(k, grid, dim3(kThreads), p.cs, smem, stream, p));
@@ -529,18 +580,22 @@ bool plan_rows(StreamParams* p, int mode, int tiles, int tok, int nsm) {
   p->groups = (kDigits * tok + 127) / 128;
   p->acc_cols = (kDigits * tok + 31) / 32 * 32;
   p->nacc = 2 * nm * p->acc_cols + 2 * (8 * nm + 8 * p->groups) <= 512 ? 2 : 1;
-  // K is split while the tiles alone leave half the SMs idle, and further
-  // until the digits fit beside at least three stages
-  int cs = 1;
-  while (2 * cs <= kMaxSplit && 2 * cs <= nst && tiles * cs <= nsm / 2) cs *= 2;
-  for (; cs <= kMaxSplit && cs <= nst; cs *= 2) {
+  auto fit = [&](int cs) {  // the digits, and at least three stages
     p->cs = cs;
     p->segs = (nst + cs - 1) / cs;
     p->stages = 0;
     const int room = (kSmemMax - layout(p, stage, nm)) / stage;
     p->stages = room < kMaxStages ? room : kMaxStages;
-    if (room >= 3) return true;
-  }
+    return room >= 3;
+  };
+  // K is split as long as all items still run at once (clusters of 8 do not
+  // fill every SM), and further until the digits fit
+  int cs = 1;
+  while (2 * cs <= kMaxSplit && 2 * cs <= nst && tiles * 2 * cs <= nsm && fit(2 * cs) &&
+         tiles <= resident_clusters(kernel_of(mode), 2 * cs, layout(p, stage, nm), nsm))
+    cs *= 2;
+  for (; cs <= kMaxSplit && cs <= nst; cs *= 2)
+    if (fit(cs)) return true;
   return false;
 }
 

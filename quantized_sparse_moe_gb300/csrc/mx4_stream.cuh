@@ -36,7 +36,8 @@ struct StreamParams {
   int32_t* status;
   // geometry (host): CTAs per cluster (the split of K), rows of x per slot,
   // digit buffers, ring stages, accumulators, and shared-memory offsets
-  int cs, tok, nb, segs, stages, nacc, acc_cols, groups;
+  int cs, tok, nb, segs, stages, nacc, acc_cols, groups, tmem_cols;
+  int single;           // a cluster for every possible item
   int dig_off, sf_off, part_off;
 };
 

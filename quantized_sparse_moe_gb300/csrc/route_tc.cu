@@ -16,12 +16,12 @@
 // first).  Few tensor-core accumulation steps per accumulator keep the logit
 // error near plain fp32 accumulation, and the KS CTAs of a tile run on KS
 // SMs.  Warp 0 streams x tiles and split-weight tiles by TMA (128-byte
-// swizzle), lane 0 of warp 1 issues the MMAs, and warps 4-7 (one
+// swizzle), one elected thread of warp 1 issues the MMAs, and warps 4-7 (one
 // tensor-memory lane = one token each) write the slice's partial logits
 // into the CTA's own shared memory.  The KS CTAs of a tile form a cluster:
 // after a cluster barrier, CTA q adds, for its 128/KS tokens, the KS slices
 // in slice order, reading the others' shared memory (distributed shared
-// memory), and its eight warps select each token's experts with the
+// memory), and its sixteen warps select each token's experts with the
 // router's warp selection (route_select_warp: one warp per token, ties to
 // the lower index, the routing flags' weights).
 #include "route_select.cuh"
@@ -33,7 +33,7 @@ namespace route_tc {
 constexpr int BM = 128;  // tokens per tile
 constexpr int BK = 64;
 constexpr int kStages = 4;
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kMaxTopK = 8;
 constexpr int kMaxE = 256;
 
@@ -76,6 +76,15 @@ split_kernel(const float* __restrict__ w, __nv_bfloat16* __restrict__ out, size_
   }
 }
 
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
 // Instruction descriptor, kind::f16 with bf16 A and B (K-major), fp32 D.
 __device__ __forceinline__ uint32_t idesc_bf16_m128(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
@@ -94,7 +103,7 @@ route_tc_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], accf_bar;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int tile = blockIdx.x / KS, q = blockIdx.x - tile * KS;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -113,7 +122,7 @@ route_tc_kernel(const __grid_constant__ Params p) {
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
   pdl_wait();
   pdl_launch_dependents();
   volatile int* abort_p = &abort_flag;
@@ -145,15 +154,14 @@ route_tc_kernel(const __grid_constant__ Params p) {
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_m128(p.E);
-      bool ok = true;
-      for (int st = 0, s = 0; st < steps; ++st) {
-        if (!wait(&full_bar[s], (st / kStages) & 1)) {
-          ok = false;
-          break;
-        }
-        tc::tc_fence_after();
+    // the whole warp runs the loop and one elected thread issues: with the
+    // descriptors in uniform registers an MMA takes a third of the time to
+    // issue that it takes from a branch on the lane number
+    const uint32_t idesc = idesc_bf16_m128(p.E);
+    for (int st = 0, s = 0; st < steps; ++st) {
+      if (!__all_sync(0xffffffffu, wait(&full_bar[s], (st / kStages) & 1))) break;
+      tc::tc_fence_after();
+      if (elect_one()) {
         const uint32_t a0 = smem_u32(smem + s * STAGE);
         const uint32_t b0 = a0 + A_BYTES;
 #pragma unroll
@@ -161,12 +169,12 @@ route_tc_kernel(const __grid_constant__ Params p) {
           tc::mma_f16(tmem, tc::sw128_desc(a0 + kk * 32), tc::sw128_desc(b0 + kk * 32),
                       idesc, (st > 0 || kk > 0) ? 1u : 0u);
         tc::mma_commit(&empty_bar[s]);
-        s = (s + 1 == kStages) ? 0 : s + 1;
+        if (st == steps - 1) tc::mma_commit(&accf_bar);
       }
-      if (ok) tc::mma_commit(&accf_bar);
+      __syncwarp();
+      s = (s + 1 == kStages) ? 0 : s + 1;
     }
-    __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 8) {
     const int q4 = warp & 3;
     const int row = 32 * q4 + lane;  // token row of the tile = TMEM lane
     const bool ok = wait(&accf_bar, 0);
