@@ -451,8 +451,9 @@ QSM_API qsm_status mx4_gemm(const qsm_mx4* a, const qsm_mx4* w, int32_t dtype, v
 #define QSM_MX4_GEMV_MAX_ROWS 32
 
 /* y[t, n] = sum_c x[t, c] * w[n, c] for a few rows of 16-bit activations,
- * which are not rounded: each block of 32 of a row enters the product to
- * 2^-23 of its largest magnitude, products exact, fp32 accumulation.
+ * which enter the product to 2^-16 of the largest magnitude in their block of
+ * 32 (a bf16 within 2^-8 of it is not rounded at all); products exact, fp32
+ * accumulation.
  *   x [T, K] bf16, row_stride elements from row to row (a multiple of 8);
  *   w [1, N, K];  y [T, N] bf16 (2-byte aligned).
  * A block of x that holds an infinity, a NaN or a magnitude of 2^127 or more
@@ -472,7 +473,7 @@ typedef struct {
 } qsm_mx4_layer;
 
 /* What the expert products of moe_mx4_forward multiply the weights with:
- *   QSM_ACTS_BF16  x and h unrounded, as mx4_gemv (T <= QSM_MX4_MOE_MAX_ROWS:
+ *   QSM_ACTS_BF16  x and h in 16 bits or more, as mx4_gemv (T <= QSM_MX4_MOE_MAX_ROWS:
  *                  every touched weight is read once, few tokens each)
  *   QSM_ACTS_MX4   x and h quantized to MXFP4 by the rule of mx4_quantize (any
  *                  number of tokens: grouped 4-bit products) */

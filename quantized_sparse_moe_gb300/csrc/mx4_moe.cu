@@ -305,7 +305,7 @@ qsm_status few_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x,
     return QSM_ERR_CUDA;
   p.w_scales = L->gate_up.scales;
   p.w_scales_sh = L->shared_gate_up.scales;
-  p.ntiles = I / 128;
+  p.ntiles = FastDiv(I / 128);
   p.T = T;
   p.k = L->k;
   p.I = I;
@@ -326,7 +326,7 @@ qsm_status few_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x,
     return QSM_ERR_CUDA;
   d.w_scales = L->down.scales;
   d.w_scales_sh = L->shared_down.scales;
-  d.ntiles = H / 128;
+  d.ntiles = FastDiv(H / 128);
   d.T = T;
   d.k = L->k;
   d.I = I;
@@ -340,8 +340,8 @@ qsm_status few_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x,
   d.o = p.o;
   d.status = status;
   const int slots = pl.shared_tiles + pl.max_tiles;
-  const qsm_status st = launch_rows(p, kRowsGateUp, slots * p.ntiles, stream);
-  return st != QSM_OK ? st : launch_rows(d, kRowsDown, slots * d.ntiles, stream);
+  const qsm_status st = launch_rows(p, kRowsGateUp, slots * (I / 128), stream);
+  return st != QSM_OK ? st : launch_rows(d, kRowsDown, slots * (H / 128), stream);
 }
 
 qsm_status many_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x, int T,

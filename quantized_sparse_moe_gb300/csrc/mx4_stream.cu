@@ -6,21 +6,22 @@
 //
 // The tensor cores multiply e2m1 by e2m1 only, so the activations are
 // written as sums of e2m1 matrices.  A block of 32 values of a row becomes
-// integers X = round(x 2^(21 - E)), E the exponent of its largest magnitude
-// (|X| <= 2^22: 2^-23 of that magnitude is kept, more than a bf16 holds), and
-// X eight digits of base 8 in -4..3:
-//   X = sum_i d_i 8^i,   x = sum_i (d_i / 2) 2^(E - 20 + 3 i)
+// integers X = round(x 2^(15 - E)), E the exponent of its largest magnitude
+// (|X| <= 2^16), and X six digits of base 8 in -4..3:
+//   X = sum_i d_i 8^i,   x = sum_i (d_i / 2) 2^(E - 14 + 3 i)
 // d_i / 2 is one of 0, +-0.5, +-1, +-1.5, -2: an e2m1 value, and the power of
-// two is its block's scale.  A row of x is thus eight rows of an MXFP4
-// matrix, the eight results are added in fp32, and every product is exact.
-// With the digits of plus the bias sum_i 4 8^i taken as unsigned, they are
-// bit fields.
+// two is its block's scale.  A row of x is thus six rows of an MXFP4 matrix,
+// the six results are added in fp32, and every product is exact.  The one
+// rounding is that to X, at most 2^-16 of the block's largest magnitude: a
+// bf16 within 2^-8 of that magnitude is kept whole, and the fp32 h of the MoE
+// layer to twice the bits of its bf16 result.  Taken as unsigned after adding
+// the bias sum_i 4 8^i, the digits are bit fields.
 //
-// The weights are the MMA's 128 rows and the digit rows its N = 8 per row of
-// x: an MMA of 128 x 8..64 x 64 costs what its weight operand takes to read
-// from shared memory (4 KB, 32 cycles), so the eightfold width is free up to
-// eight rows, and up to 32 rows the kernel stays bound by HBM (a quarter of
-// a byte per weight and cycle).  A dequantising kernel needs at least one
+// The weights are the MMA's 128 rows and the digit rows its N, 6 per row of
+// x: an MMA of 128 x 8 x 64 takes 39 cycles and one of 128 x 64 x 64 48 (what
+// reading the weights from shared memory costs), so the sixfold width is
+// almost free up to ten rows, and up to 32 rows the kernel stays bound by HBM
+// (24 bytes per SM and cycle).  A dequantising kernel needs at least one
 // integer instruction per weight, which is what bounds the affine-4 kernels
 // of decode_stream.cu.
 //
@@ -30,8 +31,14 @@
 // shared memory: CTA q adds up and writes rows 128 q / cs .. of the tile, in
 // CTA order.  Roles in a CTA: warp 0 loads (stages of 256 columns: codes by
 // TMA with the 128-byte swizzle, scale tiles by bulk copy), warp 1 issues the
-// scale copies and MMAs, warps 4-7 are the epilogue, warps 8-15 make the
+// scale copies and MMAs, warps 4-7 are the epilogue, the other ten make the
 // digits of the next slot while the current one is multiplied.
+//
+// With one item per cluster (a few tokens) what counts is latency, and half
+// of that was instruction fetches: every part of the kernel runs once.  Such
+// a launch of the MoE layer first runs an item of zeros (the shared expert's
+// first tile) through the same code while the previous launch is still at
+// work, and drops its result.
 #include <mutex>
 #include <vector>
 
@@ -42,12 +49,15 @@ namespace mx4 {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kConvWarps = 8;
+constexpr int kConvWarps = 10;
 constexpr int kMaxStages = 12;
-constexpr int kSmemMax = 225 * 1024;
-constexpr int kMaxSplit = 8;  // CTAs per cluster
-constexpr int kDigits = 8;
-constexpr uint32_t kDigitBias = 9586980u;  // sum of 4 * 8^i, i < 8
+constexpr int kSmemMax = 224 * 1024;  // dynamic; barriers and tables take some of the rest
+constexpr int kMaxSplit = 8;          // CTAs per cluster
+constexpr int kDigits = 6;
+constexpr uint32_t kDigitBias = 149796u;  // sum of 4 * 8^i, i < 6
+
+// Rows of the MMA's digit operand for n rows of x.
+__host__ __device__ constexpr int digit_rows(int n) { return (kDigits * n + 7) / 8 * 8; }
 
 template <int MODE>
 constexpr int mats() { return MODE == kRowsGateUp ? 2 : 1; }  // row tiles of w per item
@@ -85,8 +95,10 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, vol
   return false;
 }
 
+constexpr int kNone = -2, kWarm = -3;
+
 struct Slot {
-  int e;     // expert, -1: shared expert or dense; -2: no such slot
+  int e;     // expert, -1: shared expert or dense, kNone: no such slot, kWarm
   int row0;  // first row of x (dense, shared) or first sorted row (routed)
   int cnt;
 };
@@ -100,7 +112,7 @@ __device__ __forceinline__ Slot load_slot(const StreamParams& p, int s) {
     r.cnt = min(p.tok, p.T - r.row0);
   } else {
     const int2 te = __ldcg(reinterpret_cast<const int2*>(p.tile_map) + (s - p.shared_tiles));
-    r.e = te.x < 0 ? -2 : te.x;  // entries past the last block are -1
+    r.e = te.x < 0 ? kNone : te.x;  // entries past the last block are -1
     r.row0 = te.y;
     r.cnt = te.x < 0 ? 0 : p.tok == 1 ? 1 : min(p.tok, __ldcg(p.offsets + te.x + 1) - te.y);
   }
@@ -120,11 +132,12 @@ __device__ __forceinline__ Slot slot_of(const StreamParams& p, const Slot* tab, 
   return r;
 }
 
-// Eight consecutive values of row i of the slot, from column c (zeros past K).
+// Eight consecutive values of row i of the slot, from column c (zeros past K,
+// and of the warm-up slot).
 template <int MODE>
 __device__ __forceinline__ void load_acts(const StreamParams& p, const Slot& s, int i, int c,
                                           float (&v)[8]) {
-  if (c >= p.K) {
+  if (c >= p.K || s.e == kWarm) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
     return;
@@ -148,27 +161,23 @@ __device__ __forceinline__ void load_acts(const StreamParams& p, const Slot& s, 
   }
 }
 
-// The eight digit planes of eight values as e2m1 codes (one word each), and
-// the scale byte of plane 0 (plane i: + 3 i; 255: not a number).  Lanes 4 j
-// .. 4 j + 3 hold the four quarters of a block.
+// The digit planes of eight values as e2m1 codes (one word each), and the
+// scale byte of plane 0 (plane i: + 3 i; 255: not a number).  Lanes 4 j ..
+// 4 j + 3 hold the four quarters of a block.
 __device__ __forceinline__ uint32_t digits_of(const float (&v)[8], uint32_t (&plane)[kDigits]) {
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  // E, at least -105 so that 2^(21 - E) is finite; 127 and up (2^127,
+  // E, at least -111 so that 2^(15 - E) is finite; 127 and up (2^127,
   // infinities, NaN) have no scale for their top digit
-  const int e = max((int)(m >> 23) - 127, -105);
-  if (e >= 127) {
-#pragma unroll
-    for (int i = 0; i < kDigits; ++i) plane[i] = 0u;
-    return 255u;
-  }
-  const float f = __uint_as_float((uint32_t)(21 - e + 127) << 23);
+  const int e = max((int)(m >> 23) - 127, -111);
+  const bool bad = e >= 127;
+  const float f = __uint_as_float((uint32_t)(15 - (bad ? 0 : e) + 127) << 23);
   uint32_t y[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = (uint32_t)__float2int_rn(v[j] * f) + kDigitBias;
+  for (int j = 0; j < 8; ++j) y[j] = (uint32_t)__float2int_rn(bad ? 0.f : v[j] * f) + kDigitBias;
 #pragma unroll
   for (int i = 0; i < kDigits; ++i) {
     uint32_t w = 0;  // eight unsigned digits 0..7, one per nibble
@@ -182,7 +191,7 @@ __device__ __forceinline__ uint32_t digits_of(const float (&v)[8], uint32_t (&pl
     const uint32_t mask = (neg << 2) - (neg >> 2);
     plane[i] = (mask & (0xCCCCCCCCu - low)) | (~mask & low);
   }
-  return (uint32_t)(e - 20 + 127);
+  return bad ? 255u : (uint32_t)(e - 14 + 127);
 }
 
 template <int MODE>
@@ -228,45 +237,60 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
   if (cs > 1) cluster_sync_all();
   const uint32_t tmem = uniform(tmem_base);
 
-  // Down: the routing and the weights are older than the previous launch
-  // (which let this one start after its own wait), so the loading warp starts
-  // on them before the wait; h is the previous launch's.
-  if (MODE != kRowsDown) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
-  // this cluster's contiguous run of items (slot, tile): its share of all,
-  // or, with a cluster for every possible item, its own one
-  const int nclus = gridDim.x / cs, clus = blockIdx.x / cs;
-  int first = clus, last = clus + 1;
-  if (!p.single) {
-    const int slots = MODE == kRows ? p.slots : p.shared_tiles + uniform(__ldcg(p.n_tiles));
-    const long long items = (long long)slots * p.ntiles;
-    first = (int)(items * clus / nclus);
-    last = (int)(items * (clus + 1) / nclus);
-  }
-  const int tab0 = first / p.ntiles;
-  if (MODE != kRows) {
-    if (threadIdx.x < kSlotTab && (int)threadIdx.x <= (last - 1) / p.ntiles - tab0)
-      tab[threadIdx.x] = load_slot<MODE>(p, tab0 + threadIdx.x);
-    __syncthreads();
-    if (p.single && tab[0].e == -2) last = first;
-  }
-  if (MODE == kRowsDown && warp != 0) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
   // this CTA's stages of K
   const int nst = (p.K + kStageK - 1) / kStageK, cts = col_tiles(p.K);
-  const int s0 = nst * rank / cs, s1 = nst * (rank + 1) / cs;
+  const int s0 = nst * rank >> p.cs_log, s1 = nst * (rank + 1) >> p.cs_log;
+  // This cluster's items, set by begin(): a contiguous run of (slot, tile), its
+  // share of all, or, with a cluster for every possible item, its own one.
+  int first = 0, last = 0, tab0 = 0;
+  // By every warp, when it is done with the warm-up item: waits for the
+  // previous launch and looks up the run's slots.  Down: the routing and the
+  // weights are older than the previous launch (which let this one start
+  // after its own wait), so the loading warp goes on without waiting; h is
+  // the previous launch's.
+  auto begin = [&]() {
+    if (MODE != kRowsDown) {
+      pdl_wait();
+      pdl_launch_dependents();
+    }
+    const uint32_t nclus = gridDim.x >> p.cs_log, clus = blockIdx.x >> p.cs_log;
+    first = (int)clus;
+    last = first + 1;
+    if (!p.single) {
+      const uint32_t slots = MODE == kRows ? p.slots : p.shared_tiles + uniform(__ldcg(p.n_tiles));
+      const uint32_t items = slots * p.ntiles.d, each = items / nclus, more = items - each * nclus;
+      first = (int)(clus * each + min(clus, more));
+      last = first + (int)(each + (clus < more ? 1 : 0));
+    }
+    tab0 = p.ntiles.div(first);
+    if (MODE != kRows) {
+      const int i = (int)threadIdx.x;
+      if (i < kSlotTab && first < last && i <= (int)p.ntiles.div(last - 1) - tab0)
+        tab[i] = load_slot<MODE>(p, tab0 + i);
+      asm volatile("barrier.sync 1, %0;" ::"n"(kThreads) : "memory");
+      if (p.single && tab[0].e == kNone) last = first;
+    }
+    if (MODE == kRowsDown && warp != 0) {
+      pdl_wait();
+      pdl_launch_dependents();
+    }
+  };
+  const int n0 = p.warm ? -1 : 0;  // item n of the run; -1: the warm-up one
+  const Slot warm = {kWarm, 0, 1};
 
   if (warp == 0) {
     int st = 0, slot = -1;  // ring position
     uint32_t round = 0;     // how often it came round
-    Slot sl = {};
-    for (int item = first; item < last && !warp_aborted(abort_p); ++item) {
-      const int s = item / p.ntiles, tile = item - s * p.ntiles;
-      if (s != slot) sl = slot_of<MODE>(p, tab, tab0, slot = s);
+    Slot sl = warm;
+    for (int n = n0;; ++n) {
+      if (n == 0) begin();
+      if ((n >= 0 && first + n >= last) || warp_aborted(abort_p)) break;
+      int tile = 0;
+      if (n >= 0) {
+        const int s = p.ntiles.div(first + n);
+        tile = first + n - s * p.ntiles.d;
+        if (s != slot) sl = slot_of<MODE>(p, tab, tab0, slot = s);
+      }
       const bool sh = MODE != kRows && sl.e < 0;
       const CUtensorMap* wm = sh ? &p.w_sh : &p.w;
       const int row0 = (sl.e < 0 ? 0 : sl.e * p.N) + tile * 128;
@@ -300,22 +324,24 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
     }
     __syncwarp();
   } else if (warp == 1) {
-    int st = 0, slot = -1, db = 0, n = 0, ndig = 0, ab = 0;
+    int st = 0, slot = -1, db = 0, rows = digit_rows(1), ndig = 0, ab = 0;
     uint32_t round = 0, acc_round = 0, fs = 0;
     const int sfc = 8 * NM + 8 * p.groups;  // scale columns of one stage
     const uint32_t sf0 = tmem + p.nacc * NM * p.acc_cols;
     const uint32_t base = smem_u32(smem);
     const uint64_t desc0 = tc::sw128_desc(base);
-    for (int item = first; item < last && !warp_aborted(abort_p); ++item) {
-      const int s = item / p.ntiles;
+    for (int n = n0;; ++n) {
+      if (n == 0) begin();
+      if ((n >= 0 && first + n >= last) || warp_aborted(abort_p)) break;
+      const int s = n < 0 ? -2 : (int)p.ntiles.div(first + n);
       bool ok = true;
       if (s != slot) {  // the next slot's digits; the previous one's are free
-        if (slot >= 0 && elect_one()) tc::mma_commit(&dig_empty[db]);
+        if (slot != -1 && elect_one()) tc::mma_commit(&dig_empty[db]);
         __syncwarp();
         slot = s;
-        n = kDigits * slot_of<MODE>(p, tab, tab0, s).cnt;
-        db = ndig % p.nb;
-        if (!warp_wait(&dig_full[db], (ndig / p.nb) & 1, abort_p, p.status)) break;
+        if (n >= 0) rows = digit_rows(slot_of<MODE>(p, tab, tab0, s).cnt);
+        db = p.nb == 2 ? ndig & 1 : 0;
+        if (!warp_wait(&dig_full[db], (p.nb == 2 ? ndig >> 1 : ndig) & 1, abort_p, p.status)) break;
         ++ndig;
       }
       if (acc_round > 0 && !warp_wait(&acc_empty[ab], (acc_round - 1) & 1, abort_p, p.status)) break;
@@ -331,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
           const uint32_t wsf = base + st * kStage + NM * 128 * 128;
           const uint32_t xsf = base + p.sf_off + (db * p.segs + seg) * 2 * p.groups * kTileBytes;
           const uint64_t wd = desc0 + (uint64_t)(st * (kStage >> 4));
-          const uint64_t xd = desc0 + (uint64_t)((p.dig_off + (db * p.segs + seg) * p.tok * 1024) >> 4);
+          const uint64_t xd = desc0 + (uint64_t)((p.dig_off + (db * p.segs + seg) * p.seg_bytes) >> 4);
           const uint32_t sfw = sf0 + (fs & 1) * sfc, sfx = sfw + 8 * NM;
           const int kv = min(kStageK, p.K - ks * kStageK);
 #pragma unroll
@@ -348,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
 #pragma unroll
             for (int m = 0; m < NM; ++m)
               mma_mxf4(acc + m * p.acc_cols, wd + m * (128 * 128 >> 4) + 2 * kk, xd + 2 * kk,
-                       idesc_mxf4(n, kk & 1), sfw + 8 * m + 4 * (kk >> 1),
+                       idesc_mxf4(rows, kk & 1), sfw + 8 * m + 4 * (kk >> 1),
                        sfx + 4 * p.groups * (kk >> 1), (seg > 0 || kk > 0) ? 1u : 0u);
           }
           tc::mma_commit(&empty[st]);
@@ -365,42 +391,59 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
     if (elect_one()) tc::mma_commit(&done);
     __syncwarp();
     mbar_wait_bounded(&done, 0, kWaitIters);
-  } else if (warp >= 8) {
-    // digits: rows 8 i .. 8 i + 7 of the buffer are the planes of row i, in
+  } else if (warp < 4 || warp >= 8) {
+    // digits: rows 6 i .. 6 i + 5 of the buffer are the planes of row i, in
     // segments of 256 columns with the 128-byte swizzle
-    const int ct = threadIdx.x - 256;
+    const int ct = (warp < 4 ? warp - 2 : warp - 6) * 32 + lane;
     int ndig = 0, slot = -1;
     bool bad = false;
-    for (int item = first; item < last; ++item) {
-      const int s = item / p.ntiles;
+    for (int n = n0;; ++n) {
+      if (n == 0) begin();
+      if (n >= 0 && first + n >= last) break;
+      const int s = n < 0 ? -2 : (int)p.ntiles.div(first + n);
       if (s == slot) continue;
       slot = s;
-      const int db = ndig % p.nb;
-      if (ndig >= p.nb && !warp_wait(&dig_empty[db], (ndig / p.nb - 1) & 1, abort_p, p.status)) break;
+      const int db = p.nb == 2 ? ndig & 1 : 0;
+      if (ndig >= p.nb &&
+          !warp_wait(&dig_empty[db], ((p.nb == 2 ? ndig >> 1 : ndig) - 1) & 1, abort_p, p.status))
+        break;
       ++ndig;
-      const Slot sl = slot_of<MODE>(p, tab, tab0, s);
-      const int per = (s1 - s0) * 32, total = sl.cnt * per;  // groups of 8 columns
-      unsigned char* dig = smem + p.dig_off + db * p.segs * p.tok * 1024;
+      const Slot sl = n < 0 ? warm : slot_of<MODE>(p, tab, tab0, s);
+      // groups of 8 columns, 32 to a row and segment; u / 32 / cnt by a
+      // multiplication (exact below 2^11)
+      const int total = (s1 - s0) * sl.cnt * 32;
+      const uint32_t magic = (65535u + (uint32_t)sl.cnt) / (uint32_t)sl.cnt;
+      unsigned char* dig = smem + p.dig_off + db * p.segs * p.seg_bytes;
       unsigned char* sf = smem + p.sf_off + db * p.segs * 2 * p.groups * kTileBytes;
-      for (int u0 = 0; u0 < total; u0 += 32 * kConvWarps) {  // total is a multiple of 32
-        const int u = u0 + ct;
-        if (u - lane >= total) break;
-        const int i = u / per, w = u - i * per, seg = w >> 5, c8 = w & 31;
+      float next[8];
+      auto fetch = [&](int u) {
+        const int seg = (int)(((uint32_t)u >> 5) * magic >> 16), i = (u >> 5) - seg * sl.cnt;
+        load_acts<MODE>(p, sl, i, (s0 + seg) * kStageK + 8 * (u & 31), next);
+      };
+      if (ct - lane < total) fetch(ct);
+      for (int u = ct; u - lane < total; u += 32 * kConvWarps) {  // total is a multiple of 32
+        const int seg = (int)(((uint32_t)u >> 5) * magic >> 16), i = (u >> 5) - seg * sl.cnt, c8 = u & 31;
         float v[8];
-        load_acts<MODE>(p, sl, i, (s0 + seg) * kStageK + 8 * c8, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = next[j];
+        if (u - lane + 32 * kConvWarps < total) fetch(u + 32 * kConvWarps);
         uint32_t plane[kDigits];
         const uint32_t sb = digits_of(v, plane);
         if (sb == 255u) bad = true;
-        unsigned char* d = dig + (seg * p.tok + i) * 1024;
+        unsigned char* d = dig + seg * p.seg_bytes;
 #pragma unroll
-        for (int pl = 0; pl < kDigits; ++pl)
-          *reinterpret_cast<uint32_t*>(d + pl * 128 + (((c8 >> 2) ^ pl) << 4) + (c8 & 3) * 4) = plane[pl];
-        // the block's scales of planes 2 (lane % 4) and the next
+        for (int pl = 0; pl < kDigits; ++pl) {
+          const int r = kDigits * i + pl;
+          *reinterpret_cast<uint32_t*>(d + r * 128 + (((c8 >> 2) ^ (r & 7)) << 4) + (c8 & 3) * 4) = plane[pl];
+        }
+        // the block's scales: lanes 0..2 of its four store two planes each
+        if ((lane & 3) < kDigits / 2) {
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const int pl = 2 * (lane & 3) + z, r = 8 * i + pl;
-          sf[((seg * 2 + (c8 >> 4)) * p.groups + (r >> 7)) * kTileBytes + (r & 31) * 16 +
-             ((r >> 5) & 3) * 4 + ((c8 >> 2) & 3)] = (unsigned char)(sb == 255u ? 255u : sb + 3 * pl);
+          for (int z = 0; z < 2; ++z) {
+            const int pl = 2 * (lane & 3) + z, r = kDigits * i + pl;
+            sf[((seg * 2 + (c8 >> 4)) * p.groups + (r >> 7)) * kTileBytes + (r & 31) * 16 +
+               ((r >> 5) & 3) * 4 + ((c8 >> 2) & 3)] = (unsigned char)(sb == 255u ? 255u : sb + 3 * pl);
+          }
         }
       }
       tc::fence_async_smem();
@@ -408,18 +451,25 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       if (lane == 0) tc::mbar_arrive(&dig_full[db]);
     }
     if (bad) set_status(p.status, QSM_DEV_NONFINITE);
-  } else if (warp >= 4) {
+  } else {
     const int q4 = warp & 3, row = 32 * q4 + lane, et = threadIdx.x - 128;
-    const int R = 128 / cs;  // rows of a tile that a CTA of the cluster writes
+    const int R = 128 >> p.cs_log;  // rows of a tile that a CTA of the cluster writes
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
     float* part = reinterpret_cast<float*>(smem + p.part_off);
-    int slot = -1;
-    Slot sl = {};
-    for (int item = first; item < last; ++item) {
-      const int j = item - first, ab = j % p.nacc, pb = j & 1;
-      const int s = item / p.ntiles, tile = item - s * p.ntiles;
-      if (s != slot) sl = slot_of<MODE>(p, tab, tab0, slot = s);
-      if (!warp_wait(&acc_full[ab], (j / p.nacc) & 1, abort_p, p.status)) break;
+    int slot = -1, j = 0, ab = 0;
+    uint32_t acc_round = 0;
+    Slot sl = warm;
+    for (int n = n0;; ++n, ++j) {
+      if (n == 0) begin();
+      if (n >= 0 && first + n >= last) break;
+      const int pb = j & 1;
+      int tile = 0;
+      if (n >= 0) {
+        const int s = p.ntiles.div(first + n);
+        tile = first + n - s * p.ntiles.d;
+        if (s != slot) sl = slot_of<MODE>(p, tab, tab0, slot = s);
+      }
+      if (!warp_wait(&acc_full[ab], acc_round & 1, abort_p, p.status)) break;
       tc::tc_fence_after();
       if (cs > 1 && j >= 2 &&
           !__all_sync(0xffffffffu, wait_cluster(&part_empty[pb], (j / 2 - 1) & 1, abort_p, p.status)))
@@ -427,15 +477,16 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       // the value of (row `rr` of the tile, row i of the slot) goes out
       auto put = [&](int i, int rr, float a, float b) {
         const size_t hrow = (size_t)(sl.e < 0 ? p.T * p.k : 0) + sl.row0 + i;
-        const int n = tile * 128 + rr;
-        if (MODE == kRowsGateUp) p.h[hrow * p.I + n] = silu(a) * b;
-        else if (MODE == kRowsDown) p.o[hrow * p.H + n] = a;
-        else if (n < p.N)
-          p.y[(size_t)(sl.row0 + i) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(a));
+        const int c = tile * 128 + rr;
+        if (n < 0) return;
+        if (MODE == kRowsGateUp) p.h[hrow * p.I + c] = silu(a) * b;
+        else if (MODE == kRowsDown) p.o[hrow * p.H + c] = a;
+        else if (c < p.N)
+          p.y[(size_t)(sl.row0 + i) * p.N + c] = __bfloat16_as_ushort(__float2bfloat16_rn(a));
       };
       const uint32_t acc = tmem + lanes + ab * NM * p.acc_cols;
-      const int owner = row / R;
-      const uint32_t dst = cs > 1 ? dsmem_addr(part + ((size_t)(pb * cs + rank) * NM * p.tok) * R + row % R,
+      const int owner = row >> (7 - p.cs_log);
+      const uint32_t dst = cs > 1 ? dsmem_addr(part + ((size_t)(pb * cs + rank) * NM * p.tok) * R + (row & (R - 1)),
                                                owner)
                                   : 0u;
       for (int i0 = 0; i0 < sl.cnt; i0 += 2) {
@@ -465,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&acc_empty[ab]);
+      if (++ab == p.nacc) ab = 0, ++acc_round;
       if (cs > 1) {
         // tell the CTAs that this warp wrote to; then add up this CTA's rows
         if (lane < (cs == 8 ? 2 : 1))
@@ -472,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
         if (!__all_sync(0xffffffffu, wait_cluster(&part_full[pb], (j / 2) & 1, abort_p, p.status))) break;
         const float* mine = part + (size_t)pb * cs * NM * p.tok * R;
         for (int u = et; u < sl.cnt * R; u += 128) {
-          const int i = u / R, rr = u % R;
+          const int i = u >> (7 - p.cs_log), rr = u & (R - 1);
           float a = 0.f, b = 0.f;
           for (int c = 0; c < cs; ++c) {
             const float* src = mine + ((size_t)c * p.tok + i) * NM * R + rr;
@@ -499,7 +551,8 @@ constexpr int stage_bytes() { return mats<MODE>() * (128 * 128 + 2 * kTileBytes)
 // Shared memory of a geometry with `stages` ring stages; fills the offsets.
 int layout(StreamParams* p, int stage, int nm) {
   p->dig_off = p->stages * stage;
-  p->sf_off = p->dig_off + p->nb * p->segs * p->tok * 1024;
+  p->seg_bytes = digit_rows(p->tok) * 128;
+  p->sf_off = p->dig_off + p->nb * p->segs * p->seg_bytes;
   p->part_off = p->sf_off + p->nb * p->segs * 2 * p->groups * kTileBytes;
   return p->part_off + (p->cs > 1 ? 2 * nm * p->tok * 128 * 4 : 0) + 1024;
 }
@@ -555,8 +608,10 @@ qsm_status launch_mode(StreamParams& p, int items, cudaStream_t stream) {
   // own need: the next launch's CTAs then start beside it.
   const int per = (items + nc - 1) / nc;
   p.single = per == 1 && MODE != kRows;
+  p.warm = p.single;
   if (per == 1) p.nb = p.nacc = 1;
   if (per * p.segs < p.stages) p.stages = per * p.segs;
+  p.cs_log = p.cs == 8 ? 3 : p.cs / 2;
   smem = layout(&p, stage_bytes<MODE>(), NM);
   const int cols = p.nacc * NM * p.acc_cols + 2 * (8 * NM + 8 * p.groups);
   p.tmem_cols = 32;
@@ -578,7 +633,7 @@ bool plan_rows(StreamParams* p, int mode, int tiles, int tok, int nsm) {
   p->tok = tok;
   p->nb = mode == kRows ? 1 : 2;
   p->groups = (kDigits * tok + 127) / 128;
-  p->acc_cols = (kDigits * tok + 31) / 32 * 32;
+  p->acc_cols = (digit_rows(tok) + 31) / 32 * 32;
   p->nacc = 2 * nm * p->acc_cols + 2 * (8 * nm + 8 * p->groups) <= 512 ? 2 : 1;
   auto fit = [&](int cs) {  // the digits, and at least three stages
     p->cs = cs;
@@ -630,12 +685,13 @@ extern "C" qsm_status mx4_gemv(const uint16_t* x, int64_t row_stride, int32_t T,
   p.y = y;
   p.w_scales = w->scales;
   p.status = dev_status;
-  p.ntiles = row_tiles(p.N);
+  const int ntiles = row_tiles(p.N);
+  p.ntiles = FastDiv(ntiles);
   int tok = T;  // all rows at once, or as many as fit
-  while (tok > 0 && !plan_rows(&p, kRows, p.ntiles, tok, sm_count())) --tok;
+  while (tok > 0 && !plan_rows(&p, kRows, ntiles, tok, sm_count())) --tok;
   if (tok == 0) return QSM_ERR_UNSUPPORTED;
   p.slots = (T + p.tok - 1) / p.tok;
   if (!make_codes_map(&p.w, w->codes, w->rows, w->cols, 128)) return QSM_ERR_CUDA;
-  if ((long long)p.slots * p.ntiles > (1ll << 30)) return QSM_ERR_UNSUPPORTED;
-  return launch_rows(p, kRows, p.slots * p.ntiles, stream);
+  if ((long long)p.slots * ntiles > (1ll << 30)) return QSM_ERR_UNSUPPORTED;
+  return launch_rows(p, kRows, p.slots * ntiles, stream);
 }

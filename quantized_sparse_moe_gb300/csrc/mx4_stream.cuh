@@ -18,7 +18,7 @@ struct StreamParams {
   const uint8_t* w_scales;
   const uint8_t* w_scales_sh;
   int N, K;             // rows of w (per expert), columns
-  int ntiles;           // items per slot: row tiles of w (gate_up: pairs of them)
+  FastDiv ntiles;       // items per slot: row tiles of w (gate_up: pairs of them)
   int slots;            // kRows: groups of `tok` rows of x
   int T, k, I, H;
   // routed slots: the blocks of tile_map (expert, first sorted row), after the
@@ -37,7 +37,8 @@ struct StreamParams {
   // geometry (host): CTAs per cluster (the split of K), rows of x per slot,
   // digit buffers, ring stages, accumulators, and shared-memory offsets
   int cs, tok, nb, segs, stages, nacc, acc_cols, groups, tmem_cols;
-  int single;           // a cluster for every possible item
+  int single, warm;     // a cluster for every possible item; a warm-up item first
+  int cs_log, seg_bytes;
   int dig_off, sf_off, part_off;
 };
 
