@@ -193,6 +193,20 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
+// ----------------------------------------------------------------- clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Arrive on the mbarrier at cluster address `addr`; this thread's (and,
+// through a preceding __syncwarp, its warp's) stores before it are visible
+// to whoever waits for the phase.
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
 // ------------------------------------------------------------ bounded waits
 
 // Bounded mbarrier wait shared by all roles of a CTA: gives up when the
@@ -216,6 +230,29 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 }
 __device__ __forceinline__ bool warp_aborted(volatile int* abort_flag) {
   return __any_sync(0xffffffffu, *abort_flag != 0);
+}
+
+// The waits again, for barriers that other CTAs of the cluster arrive on.
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                             int32_t* status) {
+  for (uint32_t i = 0; i < kWaitIters; ++i) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if (*abort_flag) return false;
+  }
+  *abort_flag = 1;
+  set_status(status, QSM_DEV_TIMEOUT);
+  return false;
 }
 
 // ---------------------------------------------------------------------- host

@@ -18,6 +18,8 @@
 // boxes of 32 rows x 128 bytes per warp and TMA stores (or, where rows of y
 // are not 16-byte aligned, through padded boxes and plain stores).  Of a
 // short tile only the 32-row groups that exist are loaded and stored.
+#include <mutex>
+
 #include "mx4_gemm.cuh"
 
 namespace qsm {
@@ -154,6 +156,82 @@ __device__ __forceinline__ void take_acc(uint32_t taddr, int half, uint32_t (&r)
   }
 #pragma unroll
   for (int c = 0; c < NC; c += 32) tmem_wait_ld32(r + c);
+}
+
+// The NC outputs that each lane of a warp holds of its row (row 32 q4 + lane of
+// the cnt that exist from row0 on), columns col .. of y, by way of the warp's
+// boxes at `stage`.
+template <int MODE, int BN, bool F32>
+__device__ __forceinline__ void store_tile(const GemmParams& p, const uint32_t (&r)[BN / 2], int row0,
+                                           int cnt, int col, int q4, int lane, unsigned char* stage,
+                                           bool& bad) {
+  using C = Cfg<MODE, BN, F32>;
+  constexpr int kStep = C::kBoxes * C::kBoxCols;  // columns staged at a time
+  constexpr int kPer = 16 / C::kEl;               // columns in a 16-byte piece
+  __half2 top = __half2half2(__ushort_as_half(0));
+  auto piece = [&](int c) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (F32) {
+        w[i] = r[c + i];
+        continue;
+      }
+      const float a = __uint_as_float(r[c + 2 * i]), b = __uint_as_float(r[c + 2 * i + 1]);
+      if (MODE == kDown) {  // fp16 of 1/16 the value
+        const __half2 h = __floats2half2_rn(a * kOutScale, b * kOutScale);
+        top = __hmax2(top, __habs2(h));
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        w[i] = pack_bf16(a, b);
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  };
+#pragma unroll
+  for (int c0 = 0; c0 < C::NC; c0 += kStep) {
+    if (p.vec) {
+      if (lane == 0) store_wait_read();  // the boxes may be written again
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < kStep; c += kPer) {
+        const int box = c / C::kBoxCols, ch = c % C::kBoxCols / kPer;
+        const int sw = C::kInner == 128 ? lane & 7 : (lane >> 1) & 3;
+        *reinterpret_cast<uint4*>(stage + box * 32 * C::kInner + lane * C::kInner + ((ch ^ sw) << 4)) =
+            piece(c0 + c);
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+#pragma unroll
+        for (int box = 0; box < C::kBoxes; ++box)
+          if (col + c0 + box * C::kBoxCols < p.N)
+            tma_store_2d(&p.y_map, stage + box * 32 * C::kInner, col + c0 + box * C::kBoxCols,
+                         row0 + 32 * q4);
+        store_commit();
+      }
+    } else {
+#pragma unroll
+      for (int box = 0; box < C::kBoxes; ++box) {
+        __syncwarp();
+#pragma unroll
+        for (int ch = 0; ch < C::kInner / 16; ++ch)
+          *reinterpret_cast<uint4*>(stage + lane * kStagePitch + ch * 16) =
+              piece(c0 + box * C::kBoxCols + ch * kPer);
+        __syncwarp();
+        constexpr int kChunks = C::kInner / 16;
+        for (int i = lane; i < 32 * kChunks; i += 32) {
+          const int rr = i / kChunks, ch = i % kChunks;
+          const int n = col + c0 + box * C::kBoxCols + ch * kPer;
+          if (32 * q4 + rr < cnt && n < p.N)
+            store_chunk<F32>(p.y, ((size_t)row0 + 32 * q4 + rr) * p.ldy + n, n, p.N,
+                             *reinterpret_cast<const uint4*>(stage + rr * kStagePitch + ch * 16));
+        }
+      }
+    }
+  }
+  if (MODE == kDown && 32 * q4 + lane < cnt && (__hisinf(__low2half(top)) || __hisinf(__high2half(top))))
+    bad = true;
 }
 
 template <int MODE, int BN, bool F32>
@@ -334,7 +412,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
     const int q4 = warp & 3, half = (warp - 4) >> 2;
     const int row = 32 * q4 + lane;
     unsigned char* stage = smem + C::kStages * C::kStage + (warp - 4) * C::kWarpBytes;
-    const bool by_tma = p.vec != 0;
     const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16);
     bool bad = false;
     int j = 0;
@@ -387,73 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
           *reinterpret_cast<uint16_t*>(sw + 2 * half) = (uint16_t)sbytes;
         }
       } else {
-        // 16-byte pieces of a row's outputs, from column c on
-        __half2 top = __half2half2(__ushort_as_half(0));
-        auto piece = [&](int c) {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (F32) {
-              w[i] = r[c + i];
-              continue;
-            }
-            const float a = __uint_as_float(r[c + 2 * i]), b = __uint_as_float(r[c + 2 * i + 1]);
-            if (MODE == kDown) {  // fp16 of 1/16 the value
-              const __half2 h = __floats2half2_rn(a * kOutScale, b * kOutScale);
-              top = __hmax2(top, __habs2(h));
-              w[i] = *reinterpret_cast<const uint32_t*>(&h);
-            } else {
-              w[i] = pack_bf16(a, b);
-            }
-          }
-          return make_uint4(w[0], w[1], w[2], w[3]);
-        };
-        constexpr int kStep = C::kBoxes * C::kBoxCols;    // columns staged at a time
-        constexpr int kPer = 16 / C::kEl;                 // columns in a piece
-        const int col = t.n0 + half * NC;
-#pragma unroll
-        for (int c0 = 0; c0 < NC; c0 += kStep) {
-          if (by_tma) {
-            if (lane == 0) store_wait_read();  // the boxes may be written again
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < kStep; c += kPer) {
-              const int box = c / C::kBoxCols, ch = c % C::kBoxCols / kPer;
-              const int sw = C::kInner == 128 ? lane & 7 : (lane >> 1) & 3;
-              *reinterpret_cast<uint4*>(stage + box * 32 * C::kInner + lane * C::kInner + ((ch ^ sw) << 4)) =
-                  piece(c0 + c);
-            }
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-#pragma unroll
-              for (int box = 0; box < C::kBoxes; ++box)
-                if (col + c0 + box * C::kBoxCols < p.N)
-                  tma_store_2d(&p.y_map, stage + box * 32 * C::kInner, col + c0 + box * C::kBoxCols,
-                               t.a_row + 32 * q4);
-              store_commit();
-            }
-          } else {
-#pragma unroll
-            for (int box = 0; box < C::kBoxes; ++box) {
-              __syncwarp();
-#pragma unroll
-              for (int ch = 0; ch < C::kInner / 16; ++ch)
-                *reinterpret_cast<uint4*>(stage + lane * kStagePitch + ch * 16) =
-                    piece(c0 + box * C::kBoxCols + ch * kPer);
-              __syncwarp();
-              constexpr int kChunks = C::kInner / 16;
-              for (int i = lane; i < 32 * kChunks; i += 32) {
-                const int rr = i / kChunks, ch = i % kChunks;
-                const int n = col + c0 + box * C::kBoxCols + ch * kPer;
-                if (32 * q4 + rr < t.cnt && n < p.N)
-                  store_chunk<F32>(p.y, ((size_t)t.a_row + 32 * q4 + rr) * p.ldy + n, n, p.N,
-                                   *reinterpret_cast<const uint4*>(stage + rr * kStagePitch + ch * 16));
-              }
-            }
-          }
-        }
-        if (MODE == kDown && row < t.cnt && (__hisinf(__low2half(top)) || __hisinf(__high2half(top)))) bad = true;
+        store_tile<MODE, BN, F32>(p, r, t.a_row, t.cnt, t.n0 + half * C::NC, q4, lane, stage, bad);
       }
     }
     if (MODE != kGateUp && lane == 0) store_wait();
@@ -463,6 +474,205 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
   __syncthreads();
   tc::tc_fence_after();
   if (warp == 2) tc::tmem_dealloc(tmem, C::kTmem);
+}
+
+// The dense product on pairs of SMs: one MMA of 256 rows of a x 256 rows of w
+// runs on the tensor cores of both CTAs of a cluster.  Each CTA loads its own
+// 128 rows of a and half of the rows of w, and the hardware reads the other
+// half from its neighbour: 256 rows a stage and CTA instead of 384, which is
+// what counts, because a 128 x 256 tile on one SM is bound by what an SM can
+// take from L2 (55 bytes a cycle, 26 us for 4096 x 8192 x 2048, where the MMAs
+// need 15).  Every copy of either CTA reports to the leader's (rank 0)
+// barrier; the leader issues the scale copies, which move each CTA's tiles
+// into its own tensor memory, and the MMAs, and its commits arrive in both.
+// The scales of w are needed whole in both.
+template <bool F32>
+struct Pair {
+  using C = Cfg<kDense, 256, F32>;
+  static constexpr int kHalf = 128 * 128;  // codes of 128 rows
+  static constexpr int kStage = 2 * kHalf + 6 * kTileBytes;
+  static constexpr int kStages = 4;
+  static constexpr int kSmem = kStages * kStage + kEpiWarps * C::kWarpBytes + 1024;
+  static_assert(kStage % 1024 == 0 && kSmem <= 226 * 1024, "stages");
+};
+
+// TMA load of a CTA pair: the box to this CTA, its bytes to the barrier at
+// cluster address `bar`, in either CTA.
+__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, int c0, int c1,
+                                             uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pair_copy_scales(uint32_t taddr, uint32_t saddr) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(scale_desc(saddr))
+               : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
+      " [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` of both CTAs once every MMA issued so far has completed.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kThreads, 1) mx4_gemm_pair_kernel(const __grid_constant__ GemmParams p) {
+  using C = Cfg<kDense, 256, F32>;
+  using P = Pair<F32>;
+  extern __shared__ unsigned char smem_raw[];
+  // the same offset in both CTAs: descriptors and barriers are shared
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) uint64_t full[P::kStages], empty[P::kStages], acc_full, acc_empty, done;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  volatile int* abort_p = &abort_flag;
+
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&acc_full, 1);
+    mbar_init(&acc_empty, 2 * kEpiWarps);
+    mbar_init(&done, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc::tc_fence_after();
+  const uint32_t tmem = uniform(tmem_base);
+
+  pdl_wait();
+  pdl_launch_dependents();
+  const int total = p.tiles * p.nsub, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+  const int nst = (p.K + kStageK - 1) / kStageK, cts = col_tiles(p.K);
+
+  if (warp == 0) {
+    int st = 0;
+    uint32_t round = 0;
+    for (int item = pair; item < total && !warp_aborted(abort_p); item += pairs) {
+      const int mt = item / p.nsub, nt = item - mt * p.nsub;
+      const int a_tile = 2 * mt + rank, w_row = nt * 256 + rank * 128;
+      bool ok = true;
+      for (int ks = 0; ks < nst; ++ks) {
+        if (round > 0 && !warp_wait(&empty[st], (round - 1) & 1, abort_p, p.status)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          unsigned char* base = smem + st * P::kStage;
+          const uint32_t bar = dsmem_addr(&full[st], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * P::kStage);
+          pair_load_2d(base, &p.a, ks * 128, a_tile * 128, bar);
+          pair_load_2d(base + P::kHalf, &p.w, ks * 128, w_row, bar);
+          unsigned char* sf = base + 2 * P::kHalf;  // two column tiles of each row tile
+          pair_load_2d(sf, &p.a_sf, 0, a_tile * cts + 2 * ks, bar);
+          pair_load_2d(sf + 2 * kTileBytes, &p.w_sf, 0, 2 * nt * cts + 2 * ks, bar);
+          pair_load_2d(sf + 4 * kTileBytes, &p.w_sf, 0, (2 * nt + 1) * cts + 2 * ks, bar);
+        }
+        __syncwarp();
+        if (++st == P::kStages) st = 0, ++round;
+      }
+      if (!ok) break;
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      int st = 0, j = 0;
+      uint32_t round = 0;
+      const uint64_t desc0 = tc::sw128_desc(smem_u32(smem));
+      for (int item = pair; item < total && !warp_aborted(abort_p); item += pairs, ++j) {
+        if (j >= 1 && !__all_sync(0xffffffffu, wait_cluster(&acc_empty, (j - 1) & 1, abort_p, p.status)))
+          break;
+        bool ok = true;
+        for (int ks = 0; ks < nst; ++ks) {
+          if (!warp_wait(&full[st], round & 1, abort_p, p.status)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          if (elect_one()) {
+            const uint64_t ad = desc0 + (uint64_t)(st * (P::kStage >> 4)), wd = ad + (P::kHalf >> 4);
+            const uint32_t sf = smem_u32(smem) + st * P::kStage + 2 * P::kHalf;
+            const uint32_t sfa = tmem + 256 + (ks & 1) * 24, sfw = sfa + 8;
+            const int kv = min(kStageK, p.K - ks * kStageK);
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) {
+              if (ct * kTileCols >= kv) break;
+              pair_copy_scales(sfa + 4 * ct, sf + ct * kTileBytes);
+              pair_copy_scales(sfw + 8 * ct, sf + (2 + ct) * kTileBytes);
+              pair_copy_scales(sfw + 8 * ct + 4, sf + (4 + ct) * kTileBytes);
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk * 64 >= kv) break;
+              // M = 256: twice the rows of the one-CTA descriptor
+              pair_mma(tmem, ad + 2 * kk, wd + 2 * kk, idesc_mxf4(256, kk & 1) + (8u << 24),
+                       sfa + 4 * (kk >> 1), sfw + 8 * (kk >> 1), (ks > 0 || kk > 0) ? 1u : 0u);
+            }
+            pair_commit(&empty[st]);
+            if (ks == nst - 1) pair_commit(&acc_full);
+          }
+          __syncwarp();
+          if (++st == P::kStages) st = 0, ++round;
+        }
+        if (!ok) break;
+      }
+      // every MMA issued has completed before tensor memory is freed
+      if (elect_one()) pair_commit(&done);
+      __syncwarp();
+    }
+    mbar_wait_bounded(&done, 0, kWaitIters);
+  } else if (warp >= 4) {
+    const int q4 = warp & 3, half = (warp - 4) >> 2;
+    unsigned char* stage = smem + P::kStages * P::kStage + (warp - 4) * C::kWarpBytes;
+    const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16);
+    const uint32_t acc_bar = dsmem_addr(&acc_empty, 0);
+    bool bad = false;
+    int j = 0;
+    for (int item = pair; item < total; item += pairs, ++j) {
+      if (warp_aborted(abort_p)) break;
+      const int mt = item / p.nsub, nt = item - mt * p.nsub;
+      const int row0 = (2 * mt + rank) * 128, cnt = min(128, p.M - row0);
+      if (!warp_wait(&acc_full, j & 1, abort_p, p.status)) break;
+      tc::tc_fence_after();
+      uint32_t r[C::NC];
+      if (32 * q4 < cnt) take_acc<kDense, 256>(taddr, half, r);
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(acc_bar);
+      if (32 * q4 < cnt)
+        store_tile<kDense, 256, F32>(p, r, row0, cnt, nt * 256 + half * C::NC, q4, lane, stage, bad);
+    }
+    if (lane == 0) store_wait();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while the other's copies and MMAs use it
+  tc::tc_fence_after();
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 template <int MODE, int BN, bool F32>
@@ -485,6 +695,66 @@ qsm_status launch_tile(GemmParams& p, int most, uint64_t rows, cudaStream_t stre
     return QSM_ERR_CUDA;
   const int grid = most < sm_count() ? most : sm_count();
   QSM_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(kThreads), C::kSmem, stream, p));
+  return QSM_OK;
+}
+
+// Clusters of two that the device holds at once (asked once per device).
+int resident_pairs(void* kernel, int smem) {
+  static std::mutex mu;
+  static int known[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sm_count() / 2 * 2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+    known[dev] = n;
+  }
+  return known[dev];
+}
+
+// Scale tiles of [rows, cols] as rows of 512 bytes, two at a time.
+bool make_scales_map(CUtensorMap* m, const uint8_t* scales, int rows, int cols) {
+  return tc::make_map_2d(m, scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4,
+                         (uint64_t)row_tiles(rows) * col_tiles(cols), kTileBytes / 4, kTileBytes / 4, 2,
+                         CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+template <bool F32>
+qsm_status launch_pair(GemmParams& p, const qsm_mx4* a, const qsm_mx4* w, cudaStream_t stream) {
+  using P = Pair<F32>;
+  using C = Cfg<kDense, 256, F32>;
+  auto* k = mx4_gemm_pair_kernel<F32>;
+  static thread_local int ready_dev = -1;
+  int dev = 0;
+  QSM_CUDA_TRY(cudaGetDevice(&dev));
+  if (ready_dev != dev) {
+    QSM_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem));
+    ready_dev = dev;
+  }
+  p.tiles = (p.M + 255) / 256;
+  p.nsub = (p.N + 255) / 256;
+  if ((long long)p.tiles * p.nsub > (1ll << 30)) return QSM_ERR_UNSUPPORTED;
+  if (!make_codes_map(&p.w, w->codes, w->rows, w->cols, 128) ||
+      !make_scales_map(&p.a_sf, a->scales, a->rows, a->cols) ||
+      !make_scales_map(&p.w_sf, w->scales, w->rows, w->cols) ||
+      (p.vec && !make_out_map(&p.y_map, p.y, F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              C::kEl, p.M, p.N, p.ldy, C::kBoxCols, CU_TENSOR_MAP_SWIZZLE_128B)))
+    return QSM_ERR_CUDA;
+  const int most = resident_pairs(reinterpret_cast<void*>(k), P::kSmem), items = p.tiles * p.nsub;
+  if (most < 1) return QSM_ERR_CUDA;
+  QSM_CUDA_TRY(launch_pdl_cluster(k, dim3(2 * (items < most ? items : most)), dim3(kThreads), 2, P::kSmem,
+                                  stream, p));
   return QSM_OK;
 }
 
@@ -538,11 +808,12 @@ extern "C" qsm_status mx4_gemm(const qsm_mx4* a, const qsm_mx4* w, int32_t dtype
   p.w_scales = w->scales;
   p.status = dev_status;
   if (!make_a_maps(&p, a->codes, a->rows, a->cols)) return QSM_ERR_CUDA;
-  // the widest tile that still gives every SM one
+  // the widest tile that still gives every SM one (a pair, two)
   const int nsm = sm_count();
   const long long t256 = (long long)p.tiles * ((p.N + 255) / 256);
   const long long t128 = (long long)p.tiles * ((p.N + 127) / 128);
   const bool f32 = dtype == QSM_FP32;
+  if (t256 >= 2 * nsm) return f32 ? launch_pair<true>(p, a, w, stream) : launch_pair<false>(p, a, w, stream);
   if (t256 >= nsm) return launch_dense<256>(p, w, f32, stream);
   if (t128 >= nsm) return launch_dense<128>(p, w, f32, stream);
   return launch_dense<64>(p, w, f32, stream);

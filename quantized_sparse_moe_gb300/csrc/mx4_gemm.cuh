@@ -19,6 +19,7 @@ struct GemmParams {
   CUtensorMap a, a32;    // codes of a, boxes of 128 and of 32 rows
   CUtensorMap w, w_sh;   // codes of w (routed, shared), boxes of BN rows (gate_up: 128)
   CUtensorMap y_map;     // y, boxes of 32 rows (where vec)
+  CUtensorMap a_sf, w_sf;  // scale tiles, boxes of two (pairs of CTAs)
   const uint8_t* a_scales;
   const uint8_t* w_scales;
   const uint8_t* w_scales_sh;

@@ -33,12 +33,6 @@
 // TMA with the 128-byte swizzle, scale tiles by bulk copy), warp 1 issues the
 // scale copies and MMAs, warps 4-7 are the epilogue, the other ten make the
 // digits of the next slot while the current one is multiplied.
-//
-// With one item per cluster (a few tokens) what counts is latency, and half
-// of that was instruction fetches: every part of the kernel runs once.  Such
-// a launch of the MoE layer first runs an item of zeros (the shared expert's
-// first tile) through the same code while the previous launch is still at
-// work, and drops its result.
 #include <mutex>
 #include <vector>
 
@@ -62,43 +56,10 @@ __host__ __device__ constexpr int digit_rows(int n) { return (kDigits * n + 7) /
 template <int MODE>
 constexpr int mats() { return MODE == kRowsGateUp ? 2 : 1; }  // row tiles of w per item
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// Arrive on the mbarrier at cluster address `addr`; this thread's (and,
-// through a preceding __syncwarp, its warp's) stores before it are visible
-// to whoever waits for the phase.
-__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                             int32_t* status) {
-  for (uint32_t i = 0; i < kWaitIters; ++i) {
-    if (try_wait_cluster(bar, parity)) return true;
-    if (*abort_flag) return false;
-  }
-  *abort_flag = 1;
-  set_status(status, QSM_DEV_TIMEOUT);
-  return false;
-}
-
-constexpr int kNone = -2, kWarm = -3;
+constexpr int kNone = -2;
 
 struct Slot {
-  int e;     // expert, -1: shared expert or dense, kNone: no such slot, kWarm
+  int e;     // expert, -1: shared expert or dense, kNone: no such slot
   int row0;  // first row of x (dense, shared) or first sorted row (routed)
   int cnt;
 };
@@ -132,12 +93,11 @@ __device__ __forceinline__ Slot slot_of(const StreamParams& p, const Slot* tab, 
   return r;
 }
 
-// Eight consecutive values of row i of the slot, from column c (zeros past K,
-// and of the warm-up slot).
+// Eight consecutive values of row i of the slot, from column c (zeros past K).
 template <int MODE>
 __device__ __forceinline__ void load_acts(const StreamParams& p, const Slot& s, int i, int c,
                                           float (&v)[8]) {
-  if (c >= p.K || s.e == kWarm) {
+  if (c >= p.K) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
     return;
@@ -240,57 +200,43 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
   // this CTA's stages of K
   const int nst = (p.K + kStageK - 1) / kStageK, cts = col_tiles(p.K);
   const int s0 = nst * rank >> p.cs_log, s1 = nst * (rank + 1) >> p.cs_log;
-  // This cluster's items, set by begin(): a contiguous run of (slot, tile), its
-  // share of all, or, with a cluster for every possible item, its own one.
-  int first = 0, last = 0, tab0 = 0;
-  // By every warp, when it is done with the warm-up item: waits for the
-  // previous launch and looks up the run's slots.  Down: the routing and the
-  // weights are older than the previous launch (which let this one start
-  // after its own wait), so the loading warp goes on without waiting; h is
-  // the previous launch's.
-  auto begin = [&]() {
-    if (MODE != kRowsDown) {
-      pdl_wait();
-      pdl_launch_dependents();
-    }
-    const uint32_t nclus = gridDim.x >> p.cs_log, clus = blockIdx.x >> p.cs_log;
-    first = (int)clus;
-    last = first + 1;
-    if (!p.single) {
-      const uint32_t slots = MODE == kRows ? p.slots : p.shared_tiles + uniform(__ldcg(p.n_tiles));
-      const uint32_t items = slots * p.ntiles.d, each = items / nclus, more = items - each * nclus;
-      first = (int)(clus * each + min(clus, more));
-      last = first + (int)(each + (clus < more ? 1 : 0));
-    }
-    tab0 = p.ntiles.div(first);
-    if (MODE != kRows) {
-      const int i = (int)threadIdx.x;
-      if (i < kSlotTab && first < last && i <= (int)p.ntiles.div(last - 1) - tab0)
-        tab[i] = load_slot<MODE>(p, tab0 + i);
-      asm volatile("barrier.sync 1, %0;" ::"n"(kThreads) : "memory");
-      if (p.single && tab[0].e == kNone) last = first;
-    }
-    if (MODE == kRowsDown && warp != 0) {
-      pdl_wait();
-      pdl_launch_dependents();
-    }
-  };
-  const int n0 = p.warm ? -1 : 0;  // item n of the run; -1: the warm-up one
-  const Slot warm = {kWarm, 0, 1};
+  // Down: the routing and the weights are older than the previous launch
+  // (which let this one start after its own wait), so the loading warp goes
+  // on without waiting; h is the previous launch's.
+  if (MODE != kRowsDown) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  // This cluster's contiguous run of items (slot, tile): its share of all,
+  // or, with a cluster for every possible item, its own one.
+  const uint32_t nclus = gridDim.x >> p.cs_log, clus = blockIdx.x >> p.cs_log;
+  int first = (int)clus, last = first + 1;
+  if (!p.single) {
+    const uint32_t slots = MODE == kRows ? p.slots : p.shared_tiles + uniform(__ldcg(p.n_tiles));
+    const uint32_t items = slots * p.ntiles.d, each = items / nclus, more = items - each * nclus;
+    first = (int)(clus * each + min(clus, more));
+    last = first + (int)(each + (clus < more ? 1 : 0));
+  }
+  const int tab0 = p.ntiles.div(first);
+  if (MODE != kRows) {
+    const int i = (int)threadIdx.x;
+    if (i < kSlotTab && first < last && i <= (int)p.ntiles.div(last - 1) - tab0)
+      tab[i] = load_slot<MODE>(p, tab0 + i);
+    __syncthreads();
+    if (p.single && tab[0].e == kNone) last = first;
+  }
+  if (MODE == kRowsDown && warp != 0) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
 
   if (warp == 0) {
     int st = 0, slot = -1;  // ring position
     uint32_t round = 0;     // how often it came round
-    Slot sl = warm;
-    for (int n = n0;; ++n) {
-      if (n == 0) begin();
-      if ((n >= 0 && first + n >= last) || warp_aborted(abort_p)) break;
-      int tile = 0;
-      if (n >= 0) {
-        const int s = p.ntiles.div(first + n);
-        tile = first + n - s * p.ntiles.d;
-        if (s != slot) sl = slot_of<MODE>(p, tab, tab0, slot = s);
-      }
+    Slot sl = {};
+    for (int item = first; item < last && !warp_aborted(abort_p); ++item) {
+      const int s = p.ntiles.div(item), tile = item - s * p.ntiles.d;
+      if (s != slot) sl = slot_of<MODE>(p, tab, tab0, slot = s);
       const bool sh = MODE != kRows && sl.e < 0;
       const CUtensorMap* wm = sh ? &p.w_sh : &p.w;
       const int row0 = (sl.e < 0 ? 0 : sl.e * p.N) + tile * 128;
@@ -324,22 +270,20 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
     }
     __syncwarp();
   } else if (warp == 1) {
-    int st = 0, slot = -1, db = 0, rows = digit_rows(1), ndig = 0, ab = 0;
+    int st = 0, slot = -1, db = 0, rows = 0, ndig = 0, ab = 0;
     uint32_t round = 0, acc_round = 0, fs = 0;
     const int sfc = 8 * NM + 8 * p.groups;  // scale columns of one stage
     const uint32_t sf0 = tmem + p.nacc * NM * p.acc_cols;
     const uint32_t base = smem_u32(smem);
     const uint64_t desc0 = tc::sw128_desc(base);
-    for (int n = n0;; ++n) {
-      if (n == 0) begin();
-      if ((n >= 0 && first + n >= last) || warp_aborted(abort_p)) break;
-      const int s = n < 0 ? -2 : (int)p.ntiles.div(first + n);
+    for (int item = first; item < last && !warp_aborted(abort_p); ++item) {
+      const int s = p.ntiles.div(item);
       bool ok = true;
       if (s != slot) {  // the next slot's digits; the previous one's are free
-        if (slot != -1 && elect_one()) tc::mma_commit(&dig_empty[db]);
+        if (slot >= 0 && elect_one()) tc::mma_commit(&dig_empty[db]);
         __syncwarp();
         slot = s;
-        if (n >= 0) rows = digit_rows(slot_of<MODE>(p, tab, tab0, s).cnt);
+        rows = digit_rows(slot_of<MODE>(p, tab, tab0, s).cnt);
         db = p.nb == 2 ? ndig & 1 : 0;
         if (!warp_wait(&dig_full[db], (p.nb == 2 ? ndig >> 1 : ndig) & 1, abort_p, p.status)) break;
         ++ndig;
@@ -397,10 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
     const int ct = (warp < 4 ? warp - 2 : warp - 6) * 32 + lane;
     int ndig = 0, slot = -1;
     bool bad = false;
-    for (int n = n0;; ++n) {
-      if (n == 0) begin();
-      if (n >= 0 && first + n >= last) break;
-      const int s = n < 0 ? -2 : (int)p.ntiles.div(first + n);
+    for (int item = first; item < last; ++item) {
+      const int s = p.ntiles.div(item);
       if (s == slot) continue;
       slot = s;
       const int db = p.nb == 2 ? ndig & 1 : 0;
@@ -408,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
           !warp_wait(&dig_empty[db], ((p.nb == 2 ? ndig >> 1 : ndig) - 1) & 1, abort_p, p.status))
         break;
       ++ndig;
-      const Slot sl = n < 0 ? warm : slot_of<MODE>(p, tab, tab0, s);
+      const Slot sl = slot_of<MODE>(p, tab, tab0, s);
       // groups of 8 columns, 32 to a row and segment; u / 32 / cnt by a
       // multiplication (exact below 2^11)
       const int total = (s1 - s0) * sl.cnt * 32;
@@ -458,17 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
     float* part = reinterpret_cast<float*>(smem + p.part_off);
     int slot = -1, j = 0, ab = 0;
     uint32_t acc_round = 0;
-    Slot sl = warm;
-    for (int n = n0;; ++n, ++j) {
-      if (n == 0) begin();
-      if (n >= 0 && first + n >= last) break;
+    Slot sl = {};
+    for (int item = first; item < last; ++item, ++j) {
       const int pb = j & 1;
-      int tile = 0;
-      if (n >= 0) {
-        const int s = p.ntiles.div(first + n);
-        tile = first + n - s * p.ntiles.d;
-        if (s != slot) sl = slot_of<MODE>(p, tab, tab0, slot = s);
-      }
+      const int s = p.ntiles.div(item), tile = item - s * p.ntiles.d;
+      if (s != slot) sl = slot_of<MODE>(p, tab, tab0, slot = s);
       if (!warp_wait(&acc_full[ab], acc_round & 1, abort_p, p.status)) break;
       tc::tc_fence_after();
       if (cs > 1 && j >= 2 &&
@@ -478,7 +414,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       auto put = [&](int i, int rr, float a, float b) {
         const size_t hrow = (size_t)(sl.e < 0 ? p.T * p.k : 0) + sl.row0 + i;
         const int c = tile * 128 + rr;
-        if (n < 0) return;
         if (MODE == kRowsGateUp) p.h[hrow * p.I + c] = silu(a) * b;
         else if (MODE == kRowsDown) p.o[hrow * p.H + c] = a;
         else if (c < p.N)
@@ -608,7 +543,6 @@ qsm_status launch_mode(StreamParams& p, int items, cudaStream_t stream) {
   // own need: the next launch's CTAs then start beside it.
   const int per = (items + nc - 1) / nc;
   p.single = per == 1 && MODE != kRows;
-  p.warm = p.single;
   if (per == 1) p.nb = p.nacc = 1;
   if (per * p.segs < p.stages) p.stages = per * p.segs;
   p.cs_log = p.cs == 8 ? 3 : p.cs / 2;

@@ -37,8 +37,9 @@ struct StreamParams {
   // geometry (host): CTAs per cluster (the split of K), rows of x per slot,
   // digit buffers, ring stages, accumulators, and shared-memory offsets
   int cs, tok, nb, segs, stages, nacc, acc_cols, groups, tmem_cols;
-  int single, warm;     // a cluster for every possible item; a warm-up item first
-  int cs_log, seg_bytes;
+  int single;           // a cluster for every possible item
+  int cs_log;           // log2 cs
+  int seg_bytes;        // digits of one stage's columns
   int dig_off, sf_off, part_off;
 };
 
