@@ -40,7 +40,7 @@ __host__ __device__ inline size_t scale_word(int r, int ct, int cts) {
 // multiplication", 1994).
 struct FastDiv {
   uint32_t d, m, l;
-  __host__ explicit FastDiv(uint32_t div = 1) : d(div), m(0), l(0) {
+  __host__ FastDiv(uint32_t div = 1) : d(div), m(0), l(0) {
     while ((1ull << l) < d) ++l;
     m = (uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
   }

@@ -11,13 +11,14 @@
 // product of two codes is exact, and the sums are fp32.
 //
 // Roles in a persistent CTA (one per SM): warp 0 loads, warp 1 issues the
-// scale copies and the MMAs, warps 4-11 are the epilogue.  One accumulator
-// of BN columns: the epilogue's threads take their half rows into registers
-// at once (BN / 2 columns each), hand the accumulator back and convert and
-// store while the next tile's MMAs run.  The outputs leave through swizzled
+// scale copies and the MMAs, warps 4-11 are the epilogue.  Two accumulators
+// of BN columns, or one of 256 (two leave no tensor memory for the scales).
+// The epilogue's threads take their half rows into registers at once (BN / 2
+// columns each), hand the accumulator back and convert and store while the
+// next tile's MMAs run.  The outputs leave through swizzled
 // boxes of 32 rows x 128 bytes per warp and TMA stores (or, where rows of y
 // are not 16-byte aligned, through padded boxes and plain stores).  Of a
-// short tile only the 32-row groups that exist are loaded and stored.
+// short tile only the rows that exist are loaded and stored, in groups of 8.
 #include <mutex>
 
 #include "mx4_gemm.cuh"
@@ -27,14 +28,14 @@ namespace mx4 {
 
 namespace {
 
-// Rows of y (pitch ldy elements) as boxes of 32 rows.
+// Rows of y (pitch ldy elements) as boxes of box_rows rows.
 bool make_out_map(CUtensorMap* m, void* y, CUtensorMapDataType dt, int el, uint64_t rows, int cols,
-                  size_t ldy, int box_cols, CUtensorMapSwizzle swz) {
+                  size_t ldy, int box_cols, int box_rows, CUtensorMapSwizzle swz) {
   tc::EncodeTiledFn fn = tc::encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, rows};
   const cuuint64_t strides[1] = {ldy * el};
-  const cuuint32_t box[2] = {(cuuint32_t)box_cols, 32};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, dt, 2, y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -46,27 +47,28 @@ constexpr int kStagePitch = 144;  // bytes of a row in a padded box (128 + 16)
 
 template <int MODE, int BN, bool F32>
 struct Cfg {
-  static constexpr int kGroups = BN >= 128 ? BN / 128 : 1;  // scale tiles per column tile of w
+  static constexpr int kGroups = (BN + 127) / 128;  // scale tiles per column tile of w
   static constexpr int kABytes = 128 * 128;
   static constexpr int kWBytes = BN * 128;
   static constexpr int kSfaBytes = 2 * kTileBytes;
   static constexpr int kSfwBytes = 2 * kTileBytes * kGroups;
   static constexpr int kStage = kABytes + kWBytes + kSfaBytes + kSfwBytes;
-  static constexpr int kStages = MODE == kGateUp ? 4 : BN == 256 ? 3 : BN == 128 ? 4 : 6;
+  static constexpr int kStages = MODE == kGateUp ? 4 : BN == 256 ? 3 : BN >= 128 ? 4 : 6;
   // the epilogue: a thread's columns, the bytes of them that make a box's
-  // row, and the boxes of a warp (at most two at a time)
+  // row, and the boxes of a warp at a time
   static constexpr int NC = BN / 2;
   static constexpr int kEl = F32 ? 4 : 2;
-  static constexpr int kInner = NC * kEl < 128 ? NC * kEl : 128;
+  static constexpr int kInner = NC * kEl % 128 == 0 ? 128 : 64;
   static constexpr int kBoxCols = kInner / kEl;
-  static constexpr int kBoxes = NC / kBoxCols < 2 ? 1 : 2;
+  static constexpr int kBoxes = NC / kBoxCols < 4 ? NC / kBoxCols : 2;
   static constexpr int kBoxBytes = kBoxes * 32 * kInner;
   static constexpr int kWarpBytes = MODE == kGateUp ? 0
                                     : kBoxBytes > 32 * kStagePitch ? kBoxBytes : (32 * kStagePitch + 1023) / 1024 * 1024;
   static constexpr int kSmem = kStages * kStage + kEpiWarps * kWarpBytes + 1024;
   static constexpr int kSfCols = 8 + 8 * kGroups;  // scale columns of one stage
-  static constexpr int kTmem = BN == 256 ? 512 : BN == 128 ? 256 : 128;
-  static_assert(kStage % 1024 == 0 && BN + 2 * kSfCols <= kTmem && kSmem <= 226 * 1024, "tile");
+  static constexpr int kAcc = BN == 256 ? 1 : 2;   // accumulators
+  static constexpr int kTmem = BN == 64 ? 256 : 512;
+  static_assert(kStage % 1024 == 0 && kAcc * BN + 2 * kSfCols <= kTmem && kSmem <= 226 * 1024, "tile");
 };
 
 // Where a tile's operands and results lie.
@@ -106,8 +108,8 @@ __device__ __forceinline__ Tile tile_of(const GemmParams& p, int item) {
   } else {
     t.n0 = sub * BN;
     t.w_row[0] = t.w_row[1] = ebase + t.n0;
-    t.w_tile[0] = (ebase >> 7) + (t.n0 >> 7);
-    t.w_tile[1] = t.n0 + 128 < p.N ? t.w_tile[0] + 1 : -1;
+    t.w_tile[0] = t.w_row[0] >> 7;
+    t.w_tile[1] = (t.n0 & ~127) + 128 < p.N ? t.w_tile[0] + 1 : -1;
   }
   return t;
 }
@@ -180,7 +182,7 @@ __device__ __forceinline__ void store_tile(const GemmParams& p, const uint32_t (
       const float a = __uint_as_float(r[c + 2 * i]), b = __uint_as_float(r[c + 2 * i + 1]);
       if (MODE == kDown) {  // fp16 of 1/16 the value
         const __half2 h = __floats2half2_rn(a * kOutScale, b * kOutScale);
-        top = __hmax2(top, __habs2(h));
+        if (col + c / C::kBoxCols * C::kBoxCols < p.N) top = __hmax2(top, __habs2(h));
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       } else {
         w[i] = pack_bf16(a, b);
@@ -203,11 +205,19 @@ __device__ __forceinline__ void store_tile(const GemmParams& p, const uint32_t (
       tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) {
+        const int rows = cnt - 32 * q4;  // that exist of the warp's 32
 #pragma unroll
-        for (int box = 0; box < C::kBoxes; ++box)
-          if (col + c0 + box * C::kBoxCols < p.N)
-            tma_store_2d(&p.y_map, stage + box * 32 * C::kInner, col + c0 + box * C::kBoxCols,
-                         row0 + 32 * q4);
+        for (int box = 0; box < C::kBoxes; ++box) {
+          const int at = col + c0 + box * C::kBoxCols;
+          if (at >= p.N) break;
+          unsigned char* src = stage + box * 32 * C::kInner;
+          if (rows > 24) {
+            tma_store_2d(&p.y_map, src, at, row0 + 32 * q4);
+          } else {
+            for (int i = 0; i < rows; i += 8)
+              tma_store_2d(&p.y8_map, src + i * C::kInner, at, row0 + 32 * q4 + i);
+          }
+        }
         store_commit();
       }
     } else {
@@ -240,7 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], acc_full, acc_empty, done;
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], acc_full[C::kAcc],
+      acc_empty[C::kAcc], done;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   volatile int* abort_p = &abort_flag;
@@ -251,8 +262,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(&acc_full, 1);
-    mbar_init(&acc_empty, kEpiWarps);
+    for (int b = 0; b < C::kAcc; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], kEpiWarps);
+    }
     mbar_init(&done, 1);
     abort_flag = 0;
     fence_mbar_init();
@@ -297,8 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
       const uint8_t* asf = p.a_scales + (size_t)t.a_tile * cts * kTileBytes;
       const uint8_t* wsf0 = wsc + (size_t)t.w_tile[0] * cts * kTileBytes;
       const uint8_t* wsf1 = wsc + (size_t)(groups == 2 ? t.w_tile[1] : 0) * cts * kTileBytes;
-      const int a32 = (t.cnt + 31) >> 5;  // groups of 32 rows of a that exist
-      const uint32_t abytes = a32 * 32 * 128;
+      // rows of a that exist, in groups of 8 (up to 32) or of 32
+      const int a8 = (t.cnt + 7) >> 3, a32 = (t.cnt + 31) >> 5;
+      const uint32_t abytes = (a8 <= 4 ? a8 * 8 : a32 * 32) * 128;
       auto load_w = [&](int ks, int s) {
         unsigned char* wb = smem + s * C::kStage + C::kABytes;
         const uint32_t sfb = (uint32_t)min(2, cts - 2 * ks) * kTileBytes;  // scale bytes of a row tile
@@ -314,9 +328,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
         const uint32_t sfb = (uint32_t)min(2, cts - 2 * ks) * kTileBytes;
         if (a32 == 4) {
           tc::tma_load_2d(base, &p.a, ks * 128, t.a_row, &full[s]);
-        } else {
+        } else if (a8 > 4) {
           for (int i = 0; i < a32; ++i)
             tc::tma_load_2d(base + i * 32 * 128, &p.a32, ks * 128, t.a_row + 32 * i, &full[s]);
+        } else {
+          for (int i = 0; i < a8; ++i)
+            tc::tma_load_2d(base + i * 8 * 128, &p.a8, ks * 128, t.a_row + 8 * i, &full[s]);
         }
         bulk_g2s(base + C::kABytes + C::kWBytes, asf + ks * 2 * kTileBytes, sfb, &full[s]);
       };
@@ -362,13 +379,15 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
     __syncwarp();
   } else if (warp == 1) {
     int st = 0, j = 0;
-    uint32_t round = 0;
+    uint32_t round = 0, fs = 0;
     const uint64_t desc0 = tc::sw128_desc(smem_u32(smem));
     for (int item = blockIdx.x; item < total && !warp_aborted(abort_p); item += gridDim.x, ++j) {
-      // in tiles of 64 rows of w, every other one starts in the middle of a
-      // scale tile: two columns on
-      const int sf_off = BN == 64 ? ((item % p.nsub) & 1) * 2 : 0;
-      if (j >= 1 && !warp_wait(&acc_empty, (j - 1) & 1, abort_p, p.status)) break;
+      // tiles of 64 or 192 rows of w: every other one starts in the middle
+      // of a scale tile, two columns on
+      const int sf_off = BN % 128 ? ((item % p.nsub) & 1) * 2 : 0;
+      const int ab = j % C::kAcc;
+      const uint32_t acc = tmem + ab * BN;
+      if (j >= C::kAcc && !warp_wait(&acc_empty[ab], (j / C::kAcc - 1) & 1, abort_p, p.status)) break;
       bool ok = true;
       for (int ks = 0; ks < nst; ++ks) {
         if (!warp_wait(&full[st], round & 1, abort_p, p.status)) {
@@ -380,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
           const uint64_t ad = desc0 + (uint64_t)(st * (C::kStage >> 4)), wd = ad + (C::kABytes >> 4);
           const uint32_t sfa_s = smem_u32(smem) + st * C::kStage + C::kABytes + C::kWBytes;
           const uint32_t sfw_s = sfa_s + C::kSfaBytes;
-          const uint32_t sfa = tmem + BN + (ks & 1) * C::kSfCols, sfw = sfa + 8;
+          const uint32_t sfa = tmem + C::kAcc * BN + (fs & 1) * C::kSfCols, sfw = sfa + 8;
           const int kv = min(kStageK, p.K - ks * kStageK);
 #pragma unroll
           for (int ct = 0; ct < 2; ++ct) {
@@ -393,13 +412,14 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (kk * 64 >= kv) break;
-            mma_mxf4(tmem, ad + 2 * kk, wd + 2 * kk, idesc_mxf4(BN, kk & 1), sfa + 4 * (kk >> 1),
+            mma_mxf4(acc, ad + 2 * kk, wd + 2 * kk, idesc_mxf4(BN, kk & 1), sfa + 4 * (kk >> 1),
                      sfw + 4 * C::kGroups * (kk >> 1) + sf_off, (ks > 0 || kk > 0) ? 1u : 0u);
           }
           tc::mma_commit(&empty[st]);
-          if (ks == nst - 1) tc::mma_commit(&acc_full);
+          if (ks == nst - 1) tc::mma_commit(&acc_full[ab]);
         }
         __syncwarp();
+        ++fs;
         if (++st == C::kStages) st = 0, ++round;
       }
       if (!ok) break;
@@ -418,19 +438,20 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
     for (int item = blockIdx.x; item < total; item += gridDim.x, ++j) {
       if (warp_aborted(abort_p)) break;
       const Tile t = tile_of<MODE, BN>(p, item);
-      if (!warp_wait(&acc_full, j & 1, abort_p, p.status)) break;
+      const int ab = j % C::kAcc;
+      if (!warp_wait(&acc_full[ab], (j / C::kAcc) & 1, abort_p, p.status)) break;
       tc::tc_fence_after();
       constexpr int NC = C::NC;
       if (32 * q4 >= t.cnt) {  // none of the warp's rows exist
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&acc_empty);
+        if (lane == 0) tc::mbar_arrive(&acc_empty[ab]);
         continue;
       }
       uint32_t r[NC];
-      take_acc<MODE, BN>(taddr, half, r);
+      take_acc<MODE, BN>(taddr + ab * BN, half, r);
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&acc_empty);
+      if (lane == 0) tc::mbar_arrive(&acc_empty[ab]);
       if (MODE == kGateUp) {
         // h of this row's 64 intermediates, quantized where it is formed
         if (row < t.cnt) {
@@ -675,6 +696,18 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_pair_kernel(const __grid
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
+// The output maps of p (where rows of y are aligned).
+template <typename C, bool F32>
+bool make_out_maps(GemmParams* p, bool fp16, uint64_t rows) {
+  if (!p->vec) return true;
+  const CUtensorMapDataType dt = fp16  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                 : F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle swz = C::kInner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  return make_out_map(&p->y_map, p->y, dt, C::kEl, rows, p->N, p->ldy, C::kBoxCols, 32, swz) &&
+         make_out_map(&p->y8_map, p->y, dt, C::kEl, rows, p->N, p->ldy, C::kBoxCols, 8, swz);
+}
+
 template <int MODE, int BN, bool F32>
 qsm_status launch_tile(GemmParams& p, int most, uint64_t rows, cudaStream_t stream) {
   using C = Cfg<MODE, BN, F32>;
@@ -686,13 +719,7 @@ qsm_status launch_tile(GemmParams& p, int most, uint64_t rows, cudaStream_t stre
     QSM_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
     ready_dev = dev;
   }
-  if (MODE != kGateUp && p.vec &&
-      !make_out_map(&p.y_map, p.y, MODE == kDown ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                   : F32         ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                    C::kEl, rows, p.N, p.ldy, C::kBoxCols,
-                    C::kInner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
-    return QSM_ERR_CUDA;
+  if (MODE != kGateUp && !make_out_maps<C, F32>(&p, MODE == kDown, rows)) return QSM_ERR_CUDA;
   const int grid = most < sm_count() ? most : sm_count();
   QSM_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(kThreads), C::kSmem, stream, p));
   return QSM_OK;
@@ -748,8 +775,7 @@ qsm_status launch_pair(GemmParams& p, const qsm_mx4* a, const qsm_mx4* w, cudaSt
   if (!make_codes_map(&p.w, w->codes, w->rows, w->cols, 128) ||
       !make_scales_map(&p.a_sf, a->scales, a->rows, a->cols) ||
       !make_scales_map(&p.w_sf, w->scales, w->rows, w->cols) ||
-      (p.vec && !make_out_map(&p.y_map, p.y, F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                              C::kEl, p.M, p.N, p.ldy, C::kBoxCols, CU_TENSOR_MAP_SWIZZLE_128B)))
+      !make_out_maps<C, F32>(&p, false, p.M))
     return QSM_ERR_CUDA;
   const int most = resident_pairs(reinterpret_cast<void*>(k), P::kSmem), items = p.tiles * p.nsub;
   if (most < 1) return QSM_ERR_CUDA;
@@ -771,13 +797,14 @@ qsm_status launch_dense(GemmParams& p, const qsm_mx4* w, bool f32, cudaStream_t 
 }  // namespace
 
 bool make_a_maps(GemmParams* p, const void* codes, uint64_t rows, int K) {
-  return make_codes_map(&p->a, codes, rows, K, 128) && make_codes_map(&p->a32, codes, rows, K, 32);
+  return make_codes_map(&p->a, codes, rows, K, 128) && make_codes_map(&p->a32, codes, rows, K, 32) &&
+         make_codes_map(&p->a8, codes, rows, K, 8);
 }
 
 qsm_status launch_grouped(GemmParams& p, int mode, uint64_t rows, cudaStream_t stream) {
   const int most = 1 << 30;  // how many tiles there are is known on the device only
   return mode == kGateUp ? launch_tile<kGateUp, 256, false>(p, most, rows, stream)
-                         : launch_tile<kDown, 256, false>(p, most, rows, stream);
+                         : launch_tile<kDown, kDownRows, false>(p, most, rows, stream);
 }
 
 }  // namespace mx4

@@ -14,11 +14,14 @@ namespace mx4 {
 enum { kDense = 0, kGateUp = 1, kDown = 2 };
 
 constexpr float kOutScale = 1.0f / 16.0f;  // of the grouped outputs held in fp16
+// Rows of w per tile of kDown: its items are short (K = I), so two accumulators,
+// which leave room for 192 columns each, gain more than wider tiles.
+constexpr int kDownRows = 192;
 
 struct GemmParams {
-  CUtensorMap a, a32;    // codes of a, boxes of 128 and of 32 rows
+  CUtensorMap a, a32, a8;  // codes of a, boxes of 128, 32 and 8 rows
   CUtensorMap w, w_sh;   // codes of w (routed, shared), boxes of BN rows (gate_up: 128)
-  CUtensorMap y_map;     // y, boxes of 32 rows (where vec)
+  CUtensorMap y_map, y8_map;  // y, boxes of 32 and 8 rows (where vec)
   CUtensorMap a_sf, w_sf;  // scale tiles, boxes of two (pairs of CTAs)
   const uint8_t* a_scales;
   const uint8_t* w_scales;

@@ -26,6 +26,7 @@ constexpr float kOutScaleInv = 16.0f;
 constexpr int kPrepThreads = 256;
 constexpr int kCombThreads = 128;
 constexpr int kCombCols = 8;
+constexpr int kCombCtas = 8;  // per SM: 64 registers; ten spilled and were slower
 constexpr int kMaxK = 32;
 
 // Exclusive prefix sums over the experts of their blocks of 128 rows, into
@@ -131,7 +132,7 @@ mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
 // fp32, rows inv_perm[t k + j] and T k + t.  A thread takes 8 columns of one
 // token, with the loads of eight assignments in flight.
 template <bool HALF>
-__global__ void __launch_bounds__(kCombThreads)
+__global__ void __launch_bounds__(kCombThreads, HALF ? kCombCtas : 4)
 mx4_combine_kernel(const void* __restrict__ o, const int32_t* __restrict__ at,
                    const float* __restrict__ topk_w, const uint16_t* __restrict__ x,
                    const float* __restrict__ sgate, int T, int k, int H,
@@ -269,7 +270,11 @@ bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
     return at;
   };
   const size_t A = (size_t)T * k;
-  p.route = take(moe_route_workspace_bytes(T, H, E));
+  // the routers' larger need: with k > 8 many tokens take the CUDA-core one,
+  // which keeps counters and logits [T, E]
+  const size_t plain = up256((size_t)(T + 7) / 8 * 4) + up256((size_t)T * E * 4);
+  const size_t route = moe_route_workspace_bytes(T, H, E);
+  p.route = take(route > plain ? route : plain);
   p.counts = take((size_t)E * 4);
   p.offsets = take((size_t)(E + 1) * 4);
   p.perm = take(A * 4);
@@ -378,15 +383,15 @@ qsm_status many_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x
   p.status = status;
   GemmParams d = p;
   ok &= make_a_maps(&d, p.h_codes, pl.rows, I) &&
-        make_codes_map(&d.w, L->down.codes, (uint64_t)E * H, I, 256) &&
-        make_codes_map(&d.w_sh, L->shared_down.codes, (uint64_t)H, I, 256);
+        make_codes_map(&d.w, L->down.codes, (uint64_t)E * H, I, kDownRows) &&
+        make_codes_map(&d.w_sh, L->shared_down.codes, (uint64_t)H, I, kDownRows);
   if (!ok) return QSM_ERR_CUDA;
   d.a_scales = p.h_scales;
   d.w_scales = L->down.scales;
   d.w_scales_sh = L->shared_down.scales;
   d.N = H;
   d.K = I;
-  d.nsub = (H + 255) / 256;
+  d.nsub = (H + kDownRows - 1) / kDownRows;
   d.y = ws + pl.o;
   d.ldy = H;
   d.vec = 1;
