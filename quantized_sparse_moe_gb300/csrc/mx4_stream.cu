@@ -47,6 +47,7 @@ constexpr int kConvWarps = 10;
 constexpr int kMaxStages = 12;
 constexpr int kSmemMax = 224 * 1024;  // dynamic; barriers and tables take some of the rest
 constexpr int kMaxSplit = 8;          // CTAs per cluster
+constexpr int kMaxSegs = 32;          // stages of K per CTA
 constexpr int kDigits = 6;
 constexpr uint32_t kDigitBias = 149796u;  // sum of 4 * 8^i, i < 6
 
@@ -157,12 +158,17 @@ __device__ __forceinline__ uint32_t digits_of(const float (&v)[8], uint32_t (&pl
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_constant__ StreamParams p) {
   constexpr int NM = mats<MODE>();
+  // the dense product starts on a segment's digits as soon as they are there
+  // (5 x 2048 x 8192: 9.3 -> 8.4 us); the layer's slots are short, and the
+  // code for it costs them more (T = 1: 20.3 -> 20.8 us)
+  constexpr bool kBySeg = MODE == kRows;
   constexpr int kStage = NM * (128 * 128 + 2 * kTileBytes);
   extern __shared__ unsigned char smem_raw[];
   // the same offset in every CTA of a cluster, so that a shared-memory
   // address of this CTA maps to the same place of the others
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], dig_full[2], dig_empty[2],
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], dig_full[2][kBySeg ? kMaxSegs : 1],
+      dig_empty[2],
       acc_full[2], acc_empty[2], part_full[2], part_empty[2], done;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
@@ -178,7 +184,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&dig_full[b], kConvWarps);
       mbar_init(&dig_empty[b], 1);
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 4);
@@ -187,6 +192,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
     }
     mbar_init(&done, 1);
     abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 3 && lane < (kBySeg ? p.segs : 1)) {
+    for (int b = 0; b < 2; ++b) mbar_init(&dig_full[b][lane], kConvWarps);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) tc::prefetch_map(&p.w);
@@ -271,28 +280,31 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
     __syncwarp();
   } else if (warp == 1) {
     int st = 0, slot = -1, db = 0, rows = 0, ndig = 0, ab = 0;
-    uint32_t round = 0, acc_round = 0, fs = 0;
+    uint32_t round = 0, acc_round = 0, fs = 0, dig_phase = 0;
     const int sfc = 8 * NM + 8 * p.groups;  // scale columns of one stage
     const uint32_t sf0 = tmem + p.nacc * NM * p.acc_cols;
     const uint32_t base = smem_u32(smem);
     const uint64_t desc0 = tc::sw128_desc(base);
     for (int item = first; item < last && !warp_aborted(abort_p); ++item) {
       const int s = p.ntiles.div(item);
+      const bool fresh = s != slot;
       bool ok = true;
-      if (s != slot) {  // the next slot's digits; the previous one's are free
+      if (fresh) {  // the next slot's digits; the previous one's are free
         if (slot >= 0 && elect_one()) tc::mma_commit(&dig_empty[db]);
         __syncwarp();
         slot = s;
         rows = digit_rows(slot_of<MODE>(p, tab, tab0, s).cnt);
         db = p.nb == 2 ? ndig & 1 : 0;
-        if (!warp_wait(&dig_full[db], (p.nb == 2 ? ndig >> 1 : ndig) & 1, abort_p, p.status)) break;
+        dig_phase = (p.nb == 2 ? ndig >> 1 : ndig) & 1;
         ++ndig;
       }
       if (acc_round > 0 && !warp_wait(&acc_empty[ab], (acc_round - 1) & 1, abort_p, p.status)) break;
       const uint32_t acc = tmem + ab * NM * p.acc_cols;
       for (int ks = s0; ks < s1; ++ks) {
         const int seg = ks - s0;
-        if (!warp_wait(&full[st], round & 1, abort_p, p.status)) {
+        if ((fresh && (kBySeg || seg == 0) &&
+             !warp_wait(&dig_full[db][kBySeg ? seg : 0], dig_phase, abort_p, p.status)) ||
+            !warp_wait(&full[st], round & 1, abort_p, p.status)) {
           ok = false;
           break;
         }
@@ -351,12 +363,21 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
         break;
       ++ndig;
       const Slot sl = slot_of<MODE>(p, tab, tab0, s);
-      // groups of 8 columns, 32 to a row and segment; u / 32 / cnt by a
-      // multiplication (exact below 2^11)
+      // groups of 8 columns, 32 to a row and segment, segment by segment (one
+      // is done when every warp has passed it); u / 32 / cnt by a multiplication
+      // (exact below 2^11)
       const int total = (s1 - s0) * sl.cnt * 32;
       const uint32_t magic = (65535u + (uint32_t)sl.cnt) / (uint32_t)sl.cnt;
       unsigned char* dig = smem + p.dig_off + db * p.segs * p.seg_bytes;
       unsigned char* sf = smem + p.sf_off + db * p.segs * 2 * p.groups * kTileBytes;
+      int told = 0;  // segments that this warp has reported
+      auto report = [&](int upto) {
+        tc::fence_async_smem();
+        __syncwarp();
+        if (!kBySeg && lane == 0) tc::mbar_arrive(&dig_full[db][0]);
+        for (; kBySeg && told < upto; ++told)
+          if (lane == 0) tc::mbar_arrive(&dig_full[db][told]);
+      };
       float next[8];
       auto fetch = [&](int u) {
         const int seg = (int)(((uint32_t)u >> 5) * magic >> 16), i = (u >> 5) - seg * sl.cnt;
@@ -365,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       if (ct - lane < total) fetch(ct);
       for (int u = ct; u - lane < total; u += 32 * kConvWarps) {  // total is a multiple of 32
         const int seg = (int)(((uint32_t)u >> 5) * magic >> 16), i = (u >> 5) - seg * sl.cnt, c8 = u & 31;
+        if (kBySeg && seg > told) report(seg);
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = next[j];
@@ -388,9 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
           }
         }
       }
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&dig_full[db]);
+      report(s1 - s0);
     }
     if (bad) set_status(p.status, QSM_DEV_NONFINITE);
   } else {
@@ -575,7 +595,7 @@ bool plan_rows(StreamParams* p, int mode, int tiles, int tok, int nsm) {
     p->stages = 0;
     const int room = (kSmemMax - layout(p, stage, nm)) / stage;
     p->stages = room < kMaxStages ? room : kMaxStages;
-    return room >= 3;
+    return room >= 3 && p->segs <= kMaxSegs;
   };
   // K is split as long as all items still run at once (clusters of 8 do not
   // fill every SM), and further until the digits fit
