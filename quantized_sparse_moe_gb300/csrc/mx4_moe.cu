@@ -29,15 +29,18 @@ constexpr int kCombCols = 8;
 constexpr int kCombCtas = 8;  // per SM: 64 registers; ten spilled and were slower
 constexpr int kMaxK = 32;
 
-// Exclusive prefix sums over the experts of their blocks of 128 rows, into
-// start[0 .. E - 1] (shared memory).
-__device__ __forceinline__ void block_starts(const int32_t* counts, int E, int* start) {
+// base[e] (shared memory): what takes a sorted position of expert e to its row
+// when every expert's rows are padded to blocks of 128, the first at row
+// 128 * first: 128 (first + blocks of the experts before) - offsets[e].
+__device__ __forceinline__ void block_bases(const int32_t* counts, const int32_t* offsets, int E, int first,
+                                            int* base) {
   __shared__ int warp_tot[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  int base = 0;
+  int done = first;
   for (int e0 = 0; e0 < E; e0 += blockDim.x) {
     const int e = e0 + tid;
     const int v = e < E ? (__ldcg(counts + e) + 127) >> 7 : 0;
+    const int off = e < E ? __ldcg(offsets + e) : 0;
     int incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -46,13 +49,13 @@ __device__ __forceinline__ void block_starts(const int32_t* counts, int E, int* 
     }
     if (lane == 31) warp_tot[warp] = incl;
     __syncthreads();
-    int before = base, all = base;
+    int before = done, all = done;
     for (int w = 0; w < nw; ++w) {
       if (w < warp) before += warp_tot[w];
       all += warp_tot[w];
     }
-    if (e < E) start[e] = before + incl - v;
-    base = all;
+    if (e < E) base[e] = 128 * (before + incl - v) - off;
+    done = all;
     __syncthreads();
   }
 }
@@ -71,29 +74,41 @@ mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
                    const int32_t* __restrict__ counts, const int32_t* __restrict__ offsets,
                    int shared_tiles, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                    int32_t* __restrict__ pos, int32_t* status) {
-  extern __shared__ int start[];  // [E]
+  extern __shared__ int base[];  // [E]
   pdl_wait();
   pdl_launch_dependents();
-  block_starts(counts, E, start);
   const int lane = threadIdx.x & 31;
   const int cts = col_tiles(H), cgs = (H + 1023) / 1024;
   const int units = T * cgs, stride = gridDim.x * (kPrepThreads / 32);
   bool bad = false;
-  for (int u = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5); u < units; u += stride) {
+  // the next unit's loads are under way while one is worked on
+  uint4 next[4];
+  int next_e = 0, next_at = -1;
+  auto fetch = [&](int u) {
+    const int t = u / cgs, b = (u - t * cgs) * 32 + lane;
+    const uint4* src = reinterpret_cast<const uint4*>(x + (size_t)t * H + (b * kBlock < H ? b : 0) * kBlock);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) next[i] = __ldg(src + i);
+    if (lane < k) {
+      next_e = __ldcg(topk_idx + (size_t)t * k + lane);
+      next_at = __ldcg(inv_perm + (size_t)t * k + lane);
+    }
+  };
+  int u = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
+  if (u < units) fetch(u);
+  block_bases(counts, offsets, E, shared_tiles, base);
+  for (; u < units; u += stride) {
     const int t = u / cgs, cg = u - t * cgs, b = cg * 32 + lane;  // token, block
     const bool live = b * kBlock < H;
     uint4 raw[4];
-    const uint4* src = reinterpret_cast<const uint4*>(x + (size_t)t * H + (live ? b : 0) * kBlock);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) raw[i] = __ldg(src + i);
+    for (int i = 0; i < 4; ++i) raw[i] = next[i];
     int dst = -1;  // lane j: the row of assignment (t, j)
     if (lane < k) {
-      const int e = __ldcg(topk_idx + (size_t)t * k + lane);
-      const int at = __ldcg(inv_perm + (size_t)t * k + lane);
-      if (at >= 0 && e >= 0 && e < E)
-        dst = 128 * (shared_tiles + start[e]) + at - __ldcg(offsets + e);
+      if (next_at >= 0 && next_e >= 0 && next_e < E) dst = base[next_e] + next_at;
       if (cg == 0) pos[(size_t)t * k + lane] = dst;
     }
+    if (u + stride < units) fetch(u + stride);
     const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
     uint32_t m = 0;
 #pragma unroll
@@ -357,7 +372,7 @@ qsm_status many_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x
   uint8_t* xs = reinterpret_cast<uint8_t*>(ws + pl.xs);
   const long long units = (long long)T * ((H + 1023) / 1024);
   const long long ctas = (units + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
-  const int grid = (int)(ctas < 8ll * sm_count() ? ctas : 8ll * sm_count());
+  const int grid = (int)(ctas < 4ll * sm_count() ? ctas : 4ll * sm_count());
   QSM_CUDA_TRY(launch_pdl(mx4_scatter_kernel, dim3(grid), dim3(kPrepThreads), (size_t)E * 4, stream, x,
                           T, (int)L->k, H, E, topk_idx, (const int32_t*)g.inv_perm,
                           (const int32_t*)g.counts, (const int32_t*)g.offsets, pl.shared_tiles, xc, xs,
