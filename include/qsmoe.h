@@ -523,8 +523,8 @@ QSM_API uint64_t qsm_launch_count(void);
  * kernels, 2 = always the prefill kernels (when T allows).  Process-wide. */
 QSM_API qsm_status qsm_debug_force_path(int32_t mode);
 
-/* Test hook for the bounded waits: make moe_decode_layer's logit exchange
- * wait for a call tag `skew` ahead of the call's own (0 = off, the
+/* Test hook for the bounded waits: make the logit exchange of moe_decode_layer
+ * (and of moe_mx4_forward's one-launch form) wait for a call tag `skew` ahead of the call's own (0 = off, the
  * default), so that no call can complete it: every wait runs out, the kernel sets QSM_DEV_TIMEOUT
  * in *dev_status, finishes with invalid results and returns, and the
  * context stays usable.  The call ticket stays consistent (every CTA still

@@ -15,10 +15,15 @@
 // Every assignment's output is written once and the combine adds them in a
 // fixed order, instead of reductions into y: the result does not depend on
 // timing, and nothing has to be zeroed.
+#include "mx4_decode.cuh"
 #include "mx4_gemm.cuh"
 #include "mx4_stream.cuh"
 
 namespace qsm {
+namespace dlayer {
+extern int g_barrier_skew;  // qsm_debug_barrier_skew
+}
+
 namespace mx4 {
 namespace {
 
@@ -240,6 +245,9 @@ struct Plan {
   int acts, tile_rows, shared_tiles, max_tiles;
   bool fused_route;         // routing and grouping in one launch
   StreamParams gu, dn;      // QSM_ACTS_BF16: geometry
+  bool one;                 // QSM_ACTS_BF16, few tokens: one launch
+  DecodeParams dec;
+  int dec_smem, dec_ctas;
   size_t rows;              // rows of h and o (BF16: T k + T; MX4: padded)
   size_t route, counts, offsets, perm, inv_perm, tile_map, n_tiles;
   size_t xc, xs, hc, hs, h, o, pos, total;
@@ -256,6 +264,12 @@ bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
   const int H = L->H, I = L->I, E = L->E, k = L->k;
   Plan p = {};
   p.acts = acts;
+  if (acts == QSM_ACTS_BF16 && plan_decode(L, T, &p.dec, &p.dec_smem, &p.dec_ctas)) {
+    p.one = true;
+    p.total = decode_workspace_bytes(p.dec);
+    *out = p;
+    return true;
+  }
   if (acts == QSM_ACTS_BF16) {
     if (T > QSM_MX4_MOE_MAX_ROWS) return false;
     const int touched = (long long)T * k < E ? T * k : E;
@@ -364,6 +378,37 @@ qsm_status few_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x,
   return st != QSM_OK ? st : launch_rows(d, kRowsDown, slots * (H / 128), stream);
 }
 
+qsm_status one_launch(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x, const float* w_router,
+                      const float* logit_bias, int flags, int32_t* topk_idx, float* topk_w, uint16_t* y,
+                      float* y32, char* ws, int32_t* status, cudaStream_t stream) {
+  const int H = L->H, I = L->I, E = L->E;
+  DecodeParams p = pl.dec;
+  if (!make_codes_map(&p.gu, L->gate_up.codes, (uint64_t)E * 2 * I, H, 128) ||
+      !make_codes_map(&p.gu_sh, L->shared_gate_up.codes, (uint64_t)2 * I, H, 128) ||
+      !make_codes_map(&p.dn, L->down.codes, (uint64_t)E * H, I, 128) ||
+      !make_codes_map(&p.dn_sh, L->shared_down.codes, (uint64_t)H, I, 128))
+    return QSM_ERR_CUDA;
+  p.gu_sc = L->gate_up.scales;
+  p.gu_sc_sh = L->shared_gate_up.scales;
+  p.dn_sc = L->down.scales;
+  p.dn_sc_sh = L->shared_down.scales;
+  p.x = x;
+  p.w_router = w_router;
+  p.bias = logit_bias;
+  p.sgate = L->shared_gate;
+  p.flags = flags;
+  p.skew = dlayer::g_barrier_skew;
+  p.topk_idx = topk_idx;
+  p.topk_w = topk_w;
+  p.y = y;
+  p.y32 = y32;
+  p.ticket = reinterpret_cast<unsigned long long*>(ws);
+  p.logits = reinterpret_cast<unsigned long long*>(ws + 256);
+  p.h = reinterpret_cast<unsigned long long*>(ws + 256 + up256((size_t)p.T * E * 8));
+  p.status = status;
+  return launch_decode(p, pl.dec_smem, pl.dec_ctas, stream);
+}
+
 qsm_status many_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x, int T,
                        const int32_t* topk_idx, const qsm_grouping& g, char* ws, int32_t* status,
                        cudaStream_t stream) {
@@ -447,6 +492,8 @@ extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x,
   if (!plan_of(L, T, acts, &p)) return QSM_ERR_UNSUPPORTED;
   if (workspace_bytes < p.total) return QSM_ERR_WORKSPACE_TOO_SMALL;
   char* ws = static_cast<char*>(workspace);
+  if (p.one)
+    return one_launch(L, p, x, w_router, logit_bias, flags, topk_idx, topk_w, y, y_f32, ws, dev_status, stream);
   auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
   const qsm_grouping g = {i32(p.counts),   i32(p.offsets), i32(p.perm), i32(p.inv_perm),
                           i32(p.tile_map), i32(p.n_tiles), p.tile_rows, p.max_tiles};

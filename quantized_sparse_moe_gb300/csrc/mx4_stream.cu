@@ -33,9 +33,6 @@
 // TMA with the 128-byte swizzle, scale tiles by bulk copy), warp 1 issues the
 // scale copies and MMAs, warps 4-7 are the epilogue, the other ten make the
 // digits of the next slot while the current one is multiplied.
-#include <mutex>
-#include <vector>
-
 #include "mx4_stream.cuh"
 
 namespace qsm {
@@ -48,12 +45,6 @@ constexpr int kMaxStages = 12;
 constexpr int kSmemMax = 224 * 1024;  // dynamic; barriers and tables take some of the rest
 constexpr int kMaxSplit = 8;          // CTAs per cluster
 constexpr int kMaxSegs = 32;          // stages of K per CTA
-constexpr int kDigits = 6;
-constexpr uint32_t kDigitBias = 149796u;  // sum of 4 * 8^i, i < 6
-
-// Rows of the MMA's digit operand for n rows of x.
-__host__ __device__ constexpr int digit_rows(int n) { return (kDigits * n + 7) / 8 * 8; }
-
 template <int MODE>
 constexpr int mats() { return MODE == kRowsGateUp ? 2 : 1; }  // row tiles of w per item
 
@@ -120,39 +111,6 @@ __device__ __forceinline__ void load_acts(const StreamParams& p, const Slot& s, 
       v[2 * j + 1] = bf16_hi(w[j]);
     }
   }
-}
-
-// The digit planes of eight values as e2m1 codes (one word each), and the
-// scale byte of plane 0 (plane i: + 3 i; 255: not a number).  Lanes 4 j ..
-// 4 j + 3 hold the four quarters of a block.
-__device__ __forceinline__ uint32_t digits_of(const float (&v)[8], uint32_t (&plane)[kDigits]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  // E, at least -111 so that 2^(15 - E) is finite; 127 and up (2^127,
-  // infinities, NaN) have no scale for their top digit
-  const int e = max((int)(m >> 23) - 127, -111);
-  const bool bad = e >= 127;
-  const float f = __uint_as_float((uint32_t)(15 - (bad ? 0 : e) + 127) << 23);
-  uint32_t y[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = (uint32_t)__float2int_rn(bad ? 0.f : v[j] * f) + kDigitBias;
-#pragma unroll
-  for (int i = 0; i < kDigits; ++i) {
-    uint32_t w = 0;  // eight unsigned digits 0..7, one per nibble
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int sh = 3 * i - 4 * j;
-      w |= (sh >= 0 ? y[j] >> (sh & 31) : y[j] << (-sh & 31)) & (7u << (4 * j));
-    }
-    // digit - 4 as a code: 4..7 -> 0..3, 0..3 -> sign and magnitude 4 - digit
-    const uint32_t low = w & 0x33333333u, neg = ~w & 0x44444444u;
-    const uint32_t mask = (neg << 2) - (neg >> 2);
-    plane[i] = (mask & (0xCCCCCCCCu - low)) | (~mask & low);
-  }
-  return bad ? 255u : (uint32_t)(e - 14 + 127);
 }
 
 template <int MODE>
@@ -394,21 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
         uint32_t plane[kDigits];
         const uint32_t sb = digits_of(v, plane);
         if (sb == 255u) bad = true;
-        unsigned char* d = dig + seg * p.seg_bytes;
-#pragma unroll
-        for (int pl = 0; pl < kDigits; ++pl) {
-          const int r = kDigits * i + pl;
-          *reinterpret_cast<uint32_t*>(d + r * 128 + (((c8 >> 2) ^ (r & 7)) << 4) + (c8 & 3) * 4) = plane[pl];
-        }
-        // the block's scales: lanes 0..2 of its four store two planes each
-        if ((lane & 3) < kDigits / 2) {
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const int pl = 2 * (lane & 3) + z, r = kDigits * i + pl;
-            sf[((seg * 2 + (c8 >> 4)) * p.groups + (r >> 7)) * kTileBytes + (r & 31) * 16 +
-               ((r >> 5) & 3) * 4 + ((c8 >> 2) & 3)] = (unsigned char)(sb == 255u ? 255u : sb + 3 * pl);
-          }
-        }
+        store_digits(plane, sb, i, c8, dig + seg * p.seg_bytes, sf + seg * 2 * p.groups * kTileBytes, p.groups);
       }
       report(s1 - s0);
     }
@@ -512,40 +456,6 @@ int layout(StreamParams* p, int stage, int nm) {
   return p->part_off + (p->cs > 1 ? 2 * nm * p->tok * 128 * 4 : 0) + 1024;
 }
 
-// Clusters of cs CTAs of `kernel` that the current device holds at once.
-int resident_clusters(void* kernel, int cs, int smem, int nsm) {
-  struct Key {
-    int dev;
-    void* k;
-    int cs, smem, n;
-  };
-  static std::mutex mu;
-  static std::vector<Key> cache;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  for (const Key& c : cache)
-    if (c.dev == dev && c.k == kernel && c.cs == cs && c.smem == smem) return c.n;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
-    return 0;
-  int n = nsm;
-  if (cs > 1) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(nsm / cs * cs);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cs;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
-  }
-  cache.push_back({dev, kernel, cs, smem, n});
-  return n;
-}
-
 void* kernel_of(int mode) {
   return mode == kRows         ? reinterpret_cast<void*>(mx4_rows_kernel<kRows>)
          : mode == kRowsGateUp ? reinterpret_cast<void*>(mx4_rows_kernel<kRowsGateUp>)
@@ -557,7 +467,7 @@ qsm_status launch_mode(StreamParams& p, int items, cudaStream_t stream) {
   auto* k = mx4_rows_kernel<MODE>;
   constexpr int NM = mats<MODE>();
   int smem = layout(&p, stage_bytes<MODE>(), NM);
-  const int nc = resident_clusters(reinterpret_cast<void*>(k), p.cs, smem, sm_count());
+  const int nc = resident_clusters(reinterpret_cast<void*>(k), p.cs, kThreads, smem, kSmemMax);
   if (nc < 1) return QSM_ERR_CUDA;
   // With few items a CTA takes only the shared and tensor memory that its
   // own need: the next launch's CTAs then start beside it.
@@ -601,7 +511,7 @@ bool plan_rows(StreamParams* p, int mode, int tiles, int tok, int nsm) {
   // fill every SM), and further until the digits fit
   int cs = 1;
   while (2 * cs <= kMaxSplit && 2 * cs <= nst && tiles * 2 * cs <= nsm && fit(2 * cs) &&
-         tiles <= resident_clusters(kernel_of(mode), 2 * cs, layout(p, stage, nm), nsm))
+         tiles <= resident_clusters(kernel_of(mode), 2 * cs, kThreads, layout(p, stage, nm), kSmemMax))
     cs *= 2;
   for (; cs <= kMaxSplit && cs <= nst; cs *= 2)
     if (fit(cs)) return true;

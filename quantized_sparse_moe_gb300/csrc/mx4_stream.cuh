@@ -3,7 +3,7 @@
 // 16-bit activations (mx4_moe.cu).
 #pragma once
 
-#include "mx4_common.cuh"
+#include "mx4_digits.cuh"
 
 namespace qsm {
 namespace mx4 {
