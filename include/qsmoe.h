@@ -497,6 +497,11 @@ QSM_API size_t moe_mx4_workspace_bytes(const qsm_mx4_layer* L, int32_t T, int32_
  *   workspace  >= moe_mx4_workspace_bytes(L, T, acts) bytes, zeros before
  *              its first use, and every call leaves it fit for the next of
  *              the same layer shape, T and acts.
+ * One or two tokens with QSM_ACTS_BF16 (and E <= 256, 768 < H, I <= 4096)
+ * run in one launch whose CTAs exchange words: all of them have to be resident
+ * at once, so a call that shares the GPU with work that holds SMs for a second
+ * sets QSM_DEV_TIMEOUT; its results are then invalid and the workspace has to
+ * be zeroed before the next call.
  * With QSM_ACTS_MX4 the outputs of the experts are held in fp16 (scaled by
  * 1/16) until they are summed: one beyond that range sets QSM_DEV_FP16_RANGE. */
 QSM_API qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x, int32_t T,

@@ -1,4 +1,4 @@
-// The MoE layer with MXFP4 weights and 16-bit activations for up to eight
+// The MoE layer with MXFP4 weights and 16-bit activations for one or two
 // tokens, in one launch: router, selection, gate_up + SwiGLU, down and
 // combine.
 //
@@ -19,7 +19,7 @@
 //   B  Every CTA collects the logits, selects (code of moe_route: same ids and
 //      weights) and forms the sorted set U of the chosen experts.  Slot 0 is the
 //      shared expert, slot s the s-th of U; a slot is computed for all T
-//      tokens (an MMA of 48 digit rows costs what one of 8 does).  Cluster q
+//      tokens (an MMA of 16 digit rows costs what one of 8 does).  Cluster q
 //      takes the items (slot, 128 intermediates) q, q + clusters, ..; its CTAs
 //      split H and exchange partial sums through distributed shared memory, as
 //      in mx4_stream.cu; h goes out as (tag, h) words in fp32.
@@ -29,6 +29,11 @@
 //      product; the four CTAs' sums are exchanged like the others and y is
 //      written once.  The down weights are requested as soon as U is known, ahead
 //      of h.
+//
+// With more tokens phase C, which has 64 SMs for the down weights, and the
+// computing of all pairs cost more than the launches save (T = 2: 21.2 us against
+// 24.4, T = 3: 28.5 against 25.2, T = 8: 83.8 against 42.3): they take the other
+// form.
 //
 // Sums run in a fixed order: y depends on nothing but the inputs.  Every wait
 // is bounded (QSM_DEV_TIMEOUT; the results are then invalid and the workspace
@@ -48,7 +53,7 @@ constexpr int kConvWarps = 10;        // of the down phase
 constexpr int kXWarps = 2;            // of the digits of x
 constexpr int kRouteThreads = 384;    // warps 4..15
 constexpr int kTPE = 128;             // threads per expert
-constexpr int kMaxT = 8;
+constexpr int kMaxT = 2;
 constexpr int kMaxE = 256;
 constexpr int kMaxK = 32;
 constexpr int kMaxStages = 6;
@@ -456,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_layer_kernel(const __grid_con
       float* part = reinterpret_cast<float*>(smem + p.part_off);  // [2][kCs][2 T][32]
       int j = 0;  // exchanges
       // this CTA's partial sums v[i] (i < n) of its row go to the CTA that owns
-      // the row.  There, row `lane`'s sums over the CTAs of values w i .. w i +
-      // w - 1, i = q4, q4 + 4, .. (w values to a token), come out in out[]
+      // the row.  There, row `lane`'s sums over the CTAs of the w values of token
+      // q4 come out in out[]
       auto exchange = [&](const float* v, int n, int w, float* out) {
         const int b = j & 1;
         if (j >= 2 && !__all_sync(0xffffffffu, wait_cluster(&part_empty[b], (j / 2 - 1) & 1, abort_p, p.status)))
@@ -471,10 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_layer_kernel(const __grid_con
         if (!__all_sync(0xffffffffu, wait_cluster(&part_full[b], (j / 2) & 1, abort_p, p.status))) return false;
         const float* mine = part + (size_t)b * kCs * 2 * kMaxT * 32 + lane;
 #pragma unroll
-        for (int z = 0; z < 2 * kMaxT / 4; ++z) {
-          const int i = w == 2 ? 2 * (q4 + 4 * (z / 2)) + z % 2 : q4 + 4 * z;
+        for (int z = 0; z < 2; ++z) {
+          const int i = w * q4 + z;
           float s = 0.f;
-          if (i < n)
+          if (z < w && i < n)
 #pragma unroll
             for (int c = 0; c < kCs; ++c) s += mine[(c * 2 * kMaxT + i) * 32];
           out[z] = s;
@@ -508,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_layer_kernel(const __grid_con
         if (!(ok = __all_sync(0xffffffffu, wait(&acc_full[ab], acc_round & 1)))) break;
         tc::tc_fence_after();
         // value 2 t: gate, 2 t + 1: up of token t
-        float g[kMaxT], u[kMaxT], v[2 * kMaxT], out[2 * kMaxT / 4];
+        float g[kMaxT], u[kMaxT], v[2 * kMaxT], out[2];
         digit_sums(tmem + ab * 2 * p.acc_cols, g);
         digit_sums(tmem + (ab * 2 + 1) * p.acc_cols, u);
 #pragma unroll
@@ -519,14 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_layer_kernel(const __grid_con
         if (++ab == 2) ab = 0, ++acc_round;
         if (!(ok = exchange(v, 2 * T, 2, out))) break;
         const int slot = item / ntI, c = (item - slot * ntI) * 128 + 32 * rank + lane;
-#pragma unroll
-        for (int z = 0; z < kMaxT / 4; ++z) {
-          const int t = q4 + 4 * z;
-          if (t < T) st_word(p.h + ((size_t)slot * T + t) * I + c, tag, silu(out[2 * z]) * out[2 * z + 1]);
-        }
+        if (q4 < T) st_word(p.h + ((size_t)slot * T + q4) * I + c, tag, silu(out[0]) * out[1]);
       }
       if (ok && owns) {
-        float v[2 * kMaxT], out[2 * kMaxT / 4];
+        float v[2 * kMaxT], out[2];
 #pragma unroll
         for (int i = 0; i < 2 * kMaxT; ++i) v[i] = 0.f;
         if (rank <= nu) {  // this CTA had a slot
@@ -536,13 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_layer_kernel(const __grid_con
         }
         if (ok && exchange(v, T, 1, out)) {
           const int r = clus * 128 + 32 * rank + lane;
-#pragma unroll
-          for (int z = 0; z < kMaxT / 4; ++z) {
-            const int t = q4 + 4 * z;
-            if (t < T) {
-              p.y[(size_t)t * H + r] = __bfloat16_as_ushort(__float2bfloat16_rn(out[z]));
-              if (p.y32) p.y32[(size_t)t * H + r] = out[z];
-            }
+          if (q4 < T) {
+            p.y[(size_t)q4 * H + r] = __bfloat16_as_ushort(__float2bfloat16_rn(out[0]));
+            if (p.y32) p.y32[(size_t)q4 * H + r] = out[0];
           }
         }
       }

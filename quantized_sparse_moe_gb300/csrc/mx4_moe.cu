@@ -243,7 +243,6 @@ inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 // Everything a call keeps in its workspace.
 struct Plan {
   int acts, tile_rows, shared_tiles, max_tiles;
-  bool fused_route;         // routing and grouping in one launch
   StreamParams gu, dn;      // QSM_ACTS_BF16: geometry
   bool one;                 // QSM_ACTS_BF16, few tokens: one launch
   DecodeParams dec;
@@ -290,7 +289,6 @@ bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
   }
   p.shared_tiles = (T + p.tile_rows - 1) / p.tile_rows;
   p.max_tiles = moe_group_max_tiles(T, k, E, p.tile_rows);
-  p.fused_route = T <= 8 && E <= 256;
   p.rows = acts == QSM_ACTS_BF16 ? (size_t)T * k + T : (size_t)(p.shared_tiles + p.max_tiles) * 128;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -498,15 +496,11 @@ extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x,
   const qsm_grouping g = {i32(p.counts),   i32(p.offsets), i32(p.perm), i32(p.inv_perm),
                           i32(p.tile_map), i32(p.n_tiles), p.tile_rows, p.max_tiles};
   const size_t route_bytes = p.counts - p.route;
-  qsm_status st;
-  if (p.fused_route) {
-    st = moe_route_group(x, w_router, logit_bias, T, L->H, L->E, L->k, flags, topk_idx, topk_w, &g,
-                         ws + p.route, route_bytes, dev_status, stream);
-  } else {
-    st = moe_route(x, w_router, logit_bias, T, L->H, L->E, L->k, flags, topk_idx, topk_w, ws + p.route,
-                   route_bytes, dev_status, stream);
-    if (st == QSM_OK) st = moe_group_tokens(topk_idx, T, L->k, L->E, &g, dev_status, stream);
-  }
+  // (one launch for both, moe_route_group, is slower from three tokens on: the
+  // grouping in the router's last CTA; T = 8: 49.4 us a layer against 42.3)
+  qsm_status st = moe_route(x, w_router, logit_bias, T, L->H, L->E, L->k, flags, topk_idx, topk_w,
+                            ws + p.route, route_bytes, dev_status, stream);
+  if (st == QSM_OK) st = moe_group_tokens(topk_idx, T, L->k, L->E, &g, dev_status, stream);
   if (st != QSM_OK) return st;
   st = acts == QSM_ACTS_BF16 ? few_tokens(L, p, x, T, g, ws, dev_status, stream)
                              : many_tokens(L, p, x, T, topk_idx, g, ws, dev_status, stream);

@@ -323,7 +323,11 @@ def check_layer(qsm, L, v, x, acts, renormalize=True, bias_select_only=False, f=
 # H of one column tile and of an odd number of them
 MOE16 = [(1, 128, 128, 4, 1), (1, 2048, 512, 256, 8), (2, 256, 128, 8, 8), (5, 384, 256, 16, 2),
          (8, 2048, 512, 64, 8), (9, 640, 384, 8, 3), (33, 256, 128, 1, 1), (40, 2048, 512, 256, 8),
-         (64, 512, 128, 300, 9), (17, 4096, 256, 8, 2)]
+         (64, 512, 128, 300, 9), (17, 4096, 256, 8, 2),
+         # one launch: ragged quarters of H, experts that do not fill a warp, most
+         # experts per token, one expert, an odd number of stages of I
+         (1, 896, 256, 8, 8), (2, 2048, 512, 256, 8), (2, 1024, 128, 64, 32), (1, 4096, 384, 33, 5),
+         (2, 1152, 640, 1, 1), (1, 2048, 128, 256, 1)]
 
 
 @pytest.mark.parametrize("t,h,i,e,k", MOE16)
@@ -378,11 +382,46 @@ def test_moe_calls_do_not_depend_on_one_another(qsm, acts):
     assert (y1.double() - outs[0][5:6].double()).norm() <= 1e-2 * y1.double().norm()
 
 
-@pytest.mark.parametrize("acts,t", [("bf16", 3), ("bf16", 20), ("mx4", 100)])
-def test_moe_on_another_stream_and_in_a_graph(qsm, acts, t):
-    L, v = layer(qsm, 256, 128, 16, 2, seed=8)
+def test_moe_one_launch_routing_variants(qsm):
+    """The one-launch form, many calls on one workspace: other inputs each
+    time, the same bits for the same ones."""
+    L, v = layer(qsm, 1024, 256, 48, 6, seed=11, bias=True, gate=True)
+    for t in (1, 2):
+        for renorm, only in ((True, False), (False, True)):
+            f = qsm.Mx4Forward(L, t, renormalize=renorm, bias_select_only=only, want_f32=True)
+            first = None
+            for s in (1, 2, 3, 1):
+                f, _ = check_layer(qsm, L, v, hidden(t, 1024, s), "bf16", renorm, only, f=f)
+                first = f.y_f32.clone() if first is None else first
+            assert torch.equal(f.y_f32, first)
+
+
+def test_moe_one_launch_timeout_is_reported(qsm):
+    """A wait that nothing ends runs out, the call reports it and returns, and
+    the context and (zeroed) workspace go on working."""
+    L, v = layer(qsm, 1024, 128, 16, 2, seed=12)
+    f = qsm.Mx4Forward(L, 1, want_f32=True)
+    x = hidden(1, 1024, 3)
+    want = f(x).clone()
+    torch.cuda.synchronize()
+    qsm.debug_barrier_skew(1)
+    try:
+        f(x)
+        torch.cuda.synchronize()
+    finally:
+        qsm.debug_barrier_skew(0)
+    assert f.dev_status.item() & qsm.DEV_TIMEOUT
+    f.dev_status.zero_()
+    f.workspace.zero_()
+    assert torch.equal(f(x), want)
+    check_layer(qsm, L, v, x, "bf16", f=f)
+
+
+@pytest.mark.parametrize("acts,t,h", [("bf16", 1, 1024), ("bf16", 3, 256), ("bf16", 20, 256), ("mx4", 100, 256)])
+def test_moe_on_another_stream_and_in_a_graph(qsm, acts, t, h):
+    L, v = layer(qsm, h, 128, 16, 2, seed=8)
     f = qsm.Mx4Forward(L, t, acts, want_f32=True)
-    x = hidden(t, 256, 1)
+    x = hidden(t, h, 1)
     want = f(x).clone()
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
@@ -397,7 +436,7 @@ def test_moe_on_another_stream_and_in_a_graph(qsm, acts, t):
         with torch.cuda.graph(g, stream=s):
             f(x)
             y = qsm.mx4_gemv(x[:2], L.shared_gate_up)
-    xn = hidden(t, 256, 2)
+    xn = hidden(t, h, 2)
     x.copy_(xn)
     g.replay()
     torch.cuda.synchronize()
