@@ -1,10 +1,11 @@
-// The MoE layer with MXFP4 weights: routing and grouping as in the other
-// paths, then the expert products in one of two ways, and the combine
+// The MoE layer with MXFP4 weights: routing as in the other paths, the expert
+// products in one of two ways, and the combine
 //   y[t] = g[t] o_shared(t) + sum_j w[t, j] o(t, j)      (j ascending).
 //
-// QSM_ACTS_BF16 (few tokens): gate_up + SwiGLU and down by the streaming
-// kernel (mx4_stream.cu) over slots of up to 8 tokens of an expert, with the
-// activations unrounded; h and o are fp32.  Bound by the touched weights.
+// QSM_ACTS_BF16 (few tokens): one launch for one or two (mx4_decode.cu); else
+// gate_up + SwiGLU and down by the streaming kernel (mx4_stream.cu) over slots
+// of up to 8 tokens of an expert, with activations of 16 bits and more; h and
+// o are fp32.  Bound by the touched weights.
 //
 // QSM_ACTS_MX4 (many tokens): the token rows are quantized once and written
 // to their places in the grouped order, each expert's rows padded to blocks
@@ -148,14 +149,14 @@ mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
 }
 
 // y[t] from the shared expert's output row and those of the token's
-// assignments.  HALF: o holds fp16 of 1/16, rows pos[t k + j] and t; else
-// fp32, rows inv_perm[t k + j] and T k + t.  A thread takes 8 columns of one
-// token, with the loads of eight assignments in flight.
+// assignments.  HALF: o holds fp16 of 1/16, rows at[t k + j] and t; else fp32,
+// rows t k + j (where at, the chosen expert, is valid) and T k + t.  A thread
+// takes 8 columns of one token, with the loads of eight assignments in flight.
 template <bool HALF>
 __global__ void __launch_bounds__(kCombThreads, HALF ? kCombCtas : 4)
 mx4_combine_kernel(const void* __restrict__ o, const int32_t* __restrict__ at,
                    const float* __restrict__ topk_w, const uint16_t* __restrict__ x,
-                   const float* __restrict__ sgate, int T, int k, int H,
+                   const float* __restrict__ sgate, int T, int k, int H, int E,
                    uint16_t* __restrict__ y, float* __restrict__ y32) {
   __shared__ int rows[kMaxK];
   __shared__ float wts[kMaxK], red[kCombThreads / 32];
@@ -164,7 +165,8 @@ mx4_combine_kernel(const void* __restrict__ o, const int32_t* __restrict__ at,
   const int per = (H / kCombCols + kCombThreads - 1) / kCombThreads;  // CTAs per token
   const int t = blockIdx.x / per, tid = threadIdx.x;
   if (tid < k) {
-    rows[tid] = __ldcg(at + (size_t)t * k + tid);
+    const int r = __ldcg(at + (size_t)t * k + tid);
+    rows[tid] = HALF ? r : (unsigned)r < (unsigned)E ? t * k + tid : -1;
     wts[tid] = __ldcg(topk_w + (size_t)t * k + tid);
   }
   float g = 1.f;
@@ -248,7 +250,7 @@ struct Plan {
   DecodeParams dec;
   int dec_smem, dec_ctas;
   size_t rows;              // rows of h and o (BF16: T k + T; MX4: padded)
-  size_t route, counts, offsets, perm, inv_perm, tile_map, n_tiles;
+  size_t route, route_end, counts, offsets, perm, inv_perm, tile_map, n_tiles;
   size_t xc, xs, hc, hs, h, o, pos, total;
 };
 
@@ -273,7 +275,9 @@ bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
     if (T > QSM_MX4_MOE_MAX_ROWS) return false;
     const int touched = (long long)T * k < E ? T * k : E;
     bool fit = false;
-    for (int tok = T < 8 ? T : 8; tok >= 1 && !fit; tok /= 2) {
+    int tok = 8;  // a power of two, no more than the tokens need
+    while (tok > 1 && tok / 2 >= T) tok /= 2;
+    for (; tok >= 1 && !fit; tok /= 2) {
       const int slots = touched + (T + tok - 1) / tok;
       p.gu.K = H;
       p.gu.N = 2 * I;
@@ -302,12 +306,15 @@ bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
   const size_t plain = up256((size_t)(T + 7) / 8 * 4) + up256((size_t)T * E * 4);
   const size_t route = moe_route_workspace_bytes(T, H, E);
   p.route = take(route > plain ? route : plain);
-  p.counts = take((size_t)E * 4);
-  p.offsets = take((size_t)(E + 1) * 4);
-  p.perm = take(A * 4);
-  p.inv_perm = take(A * 4);
-  p.tile_map = take((size_t)p.max_tiles * 8);
-  p.n_tiles = take(4);
+  p.route_end = off;
+  if (acts == QSM_ACTS_MX4) {
+    p.counts = take((size_t)E * 4);
+    p.offsets = take((size_t)(E + 1) * 4);
+    p.perm = take(A * 4);
+    p.inv_perm = take(A * 4);
+    p.tile_map = take((size_t)p.max_tiles * 8);
+    p.n_tiles = take(4);
+  }
   if (acts == QSM_ACTS_BF16) {
     p.h = take(p.rows * I * 4);
     p.o = take(p.rows * H * 4);
@@ -329,7 +336,7 @@ bool weights_ok(const qsm_mx4& w, int experts, int rows, int cols) {
 }
 
 qsm_status few_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x, int T,
-                      const qsm_grouping& g, char* ws, int32_t* status, cudaStream_t stream) {
+                      const int32_t* topk_idx, char* ws, int32_t* status, cudaStream_t stream) {
   const int H = L->H, I = L->I, E = L->E;
   StreamParams p = pl.gu;
   if (!make_codes_map(&p.w, L->gate_up.codes, (uint64_t)E * 2 * I, H, 128) ||
@@ -342,10 +349,10 @@ qsm_status few_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x,
   p.k = L->k;
   p.I = I;
   p.H = H;
-  p.perm = g.perm;
-  p.offsets = g.offsets;
-  p.tile_map = g.tile_map;
-  p.n_tiles = g.n_tiles;
+  p.topk_idx = topk_idx;
+  p.E = E;
+  p.k_div = FastDiv(L->k);
+  p.tok_log = pl.tile_rows == 8 ? 3 : pl.tile_rows / 2;
   p.shared_tiles = pl.shared_tiles;
   p.x = x;
   p.ldx = H;
@@ -363,10 +370,10 @@ qsm_status few_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x,
   d.k = L->k;
   d.I = I;
   d.H = H;
-  d.perm = g.perm;
-  d.offsets = g.offsets;
-  d.tile_map = g.tile_map;
-  d.n_tiles = g.n_tiles;
+  d.topk_idx = topk_idx;
+  d.E = E;
+  d.k_div = FastDiv(L->k);
+  d.tok_log = pl.tile_rows == 8 ? 3 : pl.tile_rows / 2;
   d.shared_tiles = pl.shared_tiles;
   d.h = p.h;
   d.o = p.o;
@@ -495,21 +502,19 @@ extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x,
   auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
   const qsm_grouping g = {i32(p.counts),   i32(p.offsets), i32(p.perm), i32(p.inv_perm),
                           i32(p.tile_map), i32(p.n_tiles), p.tile_rows, p.max_tiles};
-  const size_t route_bytes = p.counts - p.route;
-  // (one launch for both, moe_route_group, is slower from three tokens on: the
-  // grouping in the router's last CTA; T = 8: 49.4 us a layer against 42.3)
+  const size_t route_bytes = p.route_end - p.route;
+  const bool half = acts == QSM_ACTS_MX4;
   qsm_status st = moe_route(x, w_router, logit_bias, T, L->H, L->E, L->k, flags, topk_idx, topk_w,
                             ws + p.route, route_bytes, dev_status, stream);
-  if (st == QSM_OK) st = moe_group_tokens(topk_idx, T, L->k, L->E, &g, dev_status, stream);
+  if (st == QSM_OK && half) st = moe_group_tokens(topk_idx, T, L->k, L->E, &g, dev_status, stream);
   if (st != QSM_OK) return st;
-  st = acts == QSM_ACTS_BF16 ? few_tokens(L, p, x, T, g, ws, dev_status, stream)
-                             : many_tokens(L, p, x, T, topk_idx, g, ws, dev_status, stream);
+  st = half ? many_tokens(L, p, x, T, topk_idx, g, ws, dev_status, stream)
+            : few_tokens(L, p, x, T, topk_idx, ws, dev_status, stream);
   if (st != QSM_OK) return st;
-  const bool half = acts == QSM_ACTS_MX4;
   const dim3 grid((unsigned)T * ((L->H / kCombCols + kCombThreads - 1) / kCombThreads));
   auto* comb = half ? mx4_combine_kernel<true> : mx4_combine_kernel<false>;
   QSM_CUDA_TRY(launch_pdl(comb, grid, dim3(kCombThreads), 0, stream, (const void*)(ws + p.o),
-                          (const int32_t*)i32(half ? p.pos : p.inv_perm), (const float*)topk_w, x,
-                          L->shared_gate, T, (int)L->k, (int)L->H, y, y_f32));
+                          half ? (const int32_t*)i32(p.pos) : (const int32_t*)topk_idx, (const float*)topk_w,
+                          x, L->shared_gate, T, (int)L->k, (int)L->H, (int)L->E, y, y_f32));
   return QSM_OK;
 }

@@ -33,6 +33,15 @@
 // TMA with the 128-byte swizzle, scale tiles by bulk copy), warp 1 issues the
 // scale copies and MMAs, warps 4-7 are the epilogue, the other ten make the
 // digits of the next slot while the current one is multiplied.
+//
+// In the MoE layer the slots are formed here, by every CTA for itself, from
+// the router's choices (a bit per token and expert: counts and ranks; a prefix
+// sum; then the lists of the CTA's own slots), instead of by a launch of its
+// own (H 2048, I 512, 256 experts, 8 of them: T = 6: 38.6 -> 36.1 us a layer,
+// T = 37: 76.6 -> 74.6, T = 64: 99.0 -> 95.3; T = 4: 28.5 -> 28.9).  h and o
+// are indexed by the assignment t k + j.
+#include <type_traits>
+
 #include "mx4_stream.cuh"
 
 namespace qsm {
@@ -42,52 +51,139 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kConvWarps = 10;
 constexpr int kMaxStages = 12;
-constexpr int kSmemMax = 224 * 1024;  // dynamic; barriers and tables take some of the rest
+// dynamic shared memory; barriers and the table of slots take some of the rest
+constexpr int smem_max(int mode) { return (mode == kRows ? 224 : 218) * 1024; }
 constexpr int kMaxSplit = 8;          // CTAs per cluster
 constexpr int kMaxSegs = 32;          // stages of K per CTA
 template <int MODE>
 constexpr int mats() { return MODE == kRowsGateUp ? 2 : 1; }  // row tiles of w per item
 
-constexpr int kNone = -2;
-
 struct Slot {
-  int e;     // expert, -1: shared expert or dense, kNone: no such slot
-  int row0;  // first row of x (dense, shared) or first sorted row (routed)
+  int e;     // expert, -1: shared expert or dense
+  int row0;  // first row of x (dense, shared), or the slot's row of `list`
   int cnt;
 };
 
-template <int MODE>
-__device__ __forceinline__ Slot load_slot(const StreamParams& p, int s) {
-  Slot r;
-  if (MODE == kRows || s < p.shared_tiles) {
-    r.e = -1;
-    r.row0 = s * p.tok;
-    r.cnt = min(p.tok, p.T - r.row0);
-  } else {
-    const int2 te = __ldcg(reinterpret_cast<const int2*>(p.tile_map) + (s - p.shared_tiles));
-    r.e = te.x < 0 ? kNone : te.x;  // entries past the last block are -1
-    r.row0 = te.y;
-    r.cnt = te.x < 0 ? 0 : p.tok == 1 ? 1 : min(p.tok, __ldcg(p.offsets + te.x + 1) - te.y);
+constexpr int kSlotTab = 128;   // slots of a CTA's run of items
+constexpr int kMaxTok = 8;      // rows of a routed slot
+constexpr int kMaxE = 1024;
+constexpr int kMaxChunks = 4;   // of kThreads assignments: 64 tokens, 32 experts each
+
+// What a CTA knows about its run of slots.  In 16 bits, 7 KB: with twice that
+// the gate_up product of H = 2048 and 8 rows would not keep three stages of
+// its whole K (T = 37: 82 us a layer).
+struct SlotTable {
+  struct { int16_t e, row0, cnt; } slot[kSlotTab];
+  uint16_t list[kSlotTab][kMaxTok];  // a routed slot's assignments
+  uint16_t count[kMaxE], start[kMaxE];
+  int warp_sum[kThreads / 32];
+};
+
+// The expert of this thread's assignments (-1: none that is valid), their
+// ranks among the expert's, and the experts' counts.  A token has an expert
+// at most once, and there are at most 64: a bit per token in the expert's
+// mask (at `mask`, 8 bytes an expert) gives both, the same in every CTA.
+__device__ __forceinline__ void assign_ranks(const StreamParams& p, SlotTable& t, uint2* mask,
+                                             int (&id)[kMaxChunks], int (&rank)[kMaxChunks]) {
+  const int A = p.T * p.k, tid = threadIdx.x;
+  for (int e = tid; e < p.E; e += kThreads) mask[e] = make_uint2(0u, 0u);
+#pragma unroll
+  for (int c = 0; c < kMaxChunks; ++c) {
+    const int a = c * kThreads + tid;
+    id[c] = a < A ? __ldcg(p.topk_idx + a) : -1;
+    if (id[c] < 0 || id[c] >= p.E) id[c] = -1;
+    rank[c] = (int)p.k_div.div(a);  // the token
   }
-  return r;
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < kMaxChunks; ++c)
+    if (id[c] >= 0)
+      atomicOr(rank[c] < 32 ? &mask[id[c]].x : &mask[id[c]].y, 1u << (rank[c] & 31));
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < kMaxChunks; ++c) {
+    if (id[c] < 0) continue;
+    const uint2 m = mask[id[c]];
+    const uint32_t below = (1u << (rank[c] & 31)) - 1u;
+    rank[c] = rank[c] < 32 ? __popc(m.x & below) : __popc(m.x) + __popc(m.y & below);
+  }
+  for (int e = tid; e < p.E; e += kThreads) t.count[e] = (uint16_t)(__popc(mask[e].x) + __popc(mask[e].y));
+  tc::fence_async_smem();  // the ring's copies come next
 }
 
-// The slots of a CTA's run of items, looked up once by all threads together.
-constexpr int kSlotTab = 64;
+// The first slot of every expert, and how many slots there are.
+__device__ __forceinline__ int slot_starts(const StreamParams& p, SlotTable& t) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int done = p.shared_tiles;
+  for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+    const int e = e0 + tid;
+    const int v = e < p.E ? (t.count[e] + p.tok - 1) >> p.tok_log : 0;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) t.warp_sum[warp] = incl;
+    __syncthreads();
+    int before = done;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int n = t.warp_sum[w];
+      if (w < warp) before += n;
+      done += n;
+    }
+    if (e < p.E) t.start[e] = (uint16_t)(before + incl - v);
+    __syncthreads();
+  }
+  return done;
+}
+
+// The slots tab0 .. tab0 + n - 1.
+__device__ __forceinline__ void fill_slots(const StreamParams& p, SlotTable& t, const int (&id)[kMaxChunks],
+                                           const int (&rank)[kMaxChunks], int tab0, int n) {
+  const int tid = threadIdx.x;
+  if (tid < n && tab0 + tid < p.shared_tiles) {
+    const int row0 = (tab0 + tid) * p.tok;
+    t.slot[tid] = {-1, (int16_t)row0, (int16_t)min(p.tok, p.T - row0)};
+  }
+  for (int e = tid; e < p.E; e += kThreads) {
+    const int cnt = t.count[e], s0 = t.start[e] - tab0;
+    for (int m = 0; m * p.tok < cnt; ++m)
+      if (s0 + m >= 0 && s0 + m < n)
+        t.slot[s0 + m] = {(int16_t)e, (int16_t)(s0 + m), (int16_t)min(p.tok, cnt - m * p.tok)};
+  }
+#pragma unroll
+  for (int c = 0; c < kMaxChunks; ++c) {
+    if (id[c] < 0) continue;
+    const int s = t.start[id[c]] + (rank[c] >> p.tok_log) - tab0;
+    if (s >= 0 && s < n) t.list[s][rank[c] & (p.tok - 1)] = (uint16_t)(c * kThreads + tid);
+  }
+}
 
 // Slot s, by all lanes of a warp.
 template <int MODE>
-__device__ __forceinline__ Slot slot_of(const StreamParams& p, const Slot* tab, int tab0, int s) {
-  Slot r = MODE != kRows && s - tab0 < kSlotTab ? tab[s - tab0] : load_slot<MODE>(p, s);
+__device__ __forceinline__ Slot slot_of(const StreamParams& p, const SlotTable* t, int tab0, int s) {
+  Slot r;
+  if (MODE == kRows) {
+    r = {-1, s * p.tok, min(p.tok, p.T - s * p.tok)};
+  } else {
+    const auto& w = t->slot[s - tab0];
+    r = {w.e, w.row0, w.cnt};
+  }
   r.e = uniform(r.e);
   r.row0 = uniform(r.row0);
   r.cnt = uniform(r.cnt);
   return r;
 }
+// The row of h and o of the slot's row i.
+__device__ __forceinline__ int assignment(const StreamParams& p, const SlotTable* t, const Slot& s, int i) {
+  return s.e < 0 ? p.T * p.k + s.row0 + i : t->list[s.row0][i];
+}
 
 // Eight consecutive values of row i of the slot, from column c (zeros past K).
 template <int MODE>
-__device__ __forceinline__ void load_acts(const StreamParams& p, const Slot& s, int i, int c,
+__device__ __forceinline__ void load_acts(const StreamParams& p, const SlotTable* t, const Slot& s, int i, int c,
                                           float (&v)[8]) {
   if (c >= p.K) {
 #pragma unroll
@@ -95,15 +191,13 @@ __device__ __forceinline__ void load_acts(const StreamParams& p, const Slot& s, 
     return;
   }
   if (MODE == kRowsDown) {
-    const size_t row = (size_t)(s.e < 0 ? p.T * p.k : 0) + s.row0 + i;
-    const float4* src = reinterpret_cast<const float4*>(p.h + row * p.I + c);
+    const float4* src = reinterpret_cast<const float4*>(p.h + (size_t)assignment(p, t, s, i) * p.I + c);
     const float4 a = __ldcg(src), b = __ldcg(src + 1);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   } else {
-    int t = s.row0 + i;
-    if (MODE == kRowsGateUp && s.e >= 0) t = __ldcg(p.perm + t) / p.k;
-    const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p.x + (size_t)t * p.ldx + c));
+    const int row = MODE == kRowsGateUp && s.e >= 0 ? (int)p.k_div.div(t->list[s.row0][i]) : s.row0 + i;
+    const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p.x + (size_t)row * p.ldx + c));
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -130,7 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       acc_full[2], acc_empty[2], part_full[2], part_empty[2], done;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  __shared__ Slot tab[kSlotTab];
+  __shared__ typename std::conditional<MODE == kRows, char, SlotTable>::type tab_space;
+  SlotTable* tab = MODE == kRows ? nullptr : reinterpret_cast<SlotTable*>(&tab_space);
   volatile int* abort_p = &abort_flag;
 
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -174,23 +269,21 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
     pdl_wait();
     pdl_launch_dependents();
   }
-  // This cluster's contiguous run of items (slot, tile): its share of all,
-  // or, with a cluster for every possible item, its own one.
-  const uint32_t nclus = gridDim.x >> p.cs_log, clus = blockIdx.x >> p.cs_log;
-  int first = (int)clus, last = first + 1;
-  if (!p.single) {
-    const uint32_t slots = MODE == kRows ? p.slots : p.shared_tiles + uniform(__ldcg(p.n_tiles));
-    const uint32_t items = slots * p.ntiles.d, each = items / nclus, more = items - each * nclus;
-    first = (int)(clus * each + min(clus, more));
-    last = first + (int)(each + (clus < more ? 1 : 0));
+  // This cluster's contiguous run of items (slot, tile).
+  int id[kMaxChunks], rank_of[kMaxChunks];
+  uint32_t slots = p.slots;
+  if (MODE != kRows) {
+    assign_ranks(p, *tab, reinterpret_cast<uint2*>(smem), id, rank_of);
+    slots = slot_starts(p, *tab);
   }
+  const uint32_t nclus = gridDim.x >> p.cs_log, clus = blockIdx.x >> p.cs_log;
+  const uint32_t items = slots * p.ntiles.d, each = items / nclus, more = items - each * nclus;
+  const int first = uniform((int)(clus * each + min(clus, more)));
+  const int last = uniform(first + (int)(each + (clus < more ? 1 : 0)));
   const int tab0 = p.ntiles.div(first);
   if (MODE != kRows) {
-    const int i = (int)threadIdx.x;
-    if (i < kSlotTab && first < last && i <= (int)p.ntiles.div(last - 1) - tab0)
-      tab[i] = load_slot<MODE>(p, tab0 + i);
+    if (first < last) fill_slots(p, *tab, id, rank_of, tab0, (int)p.ntiles.div(last - 1) - tab0 + 1);
     __syncthreads();
-    if (p.single && tab[0].e == kNone) last = first;
   }
   if (MODE == kRowsDown && warp != 0) {
     pdl_wait();
@@ -339,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
       float next[8];
       auto fetch = [&](int u) {
         const int seg = (int)(((uint32_t)u >> 5) * magic >> 16), i = (u >> 5) - seg * sl.cnt;
-        load_acts<MODE>(p, sl, i, (s0 + seg) * kStageK + 8 * (u & 31), next);
+        load_acts<MODE>(p, tab, sl, i, (s0 + seg) * kStageK + 8 * (u & 31), next);
       };
       if (ct - lane < total) fetch(ct);
       for (int u = ct; u - lane < total; u += 32 * kConvWarps) {  // total is a multiple of 32
@@ -376,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
         break;
       // the value of (row `rr` of the tile, row i of the slot) goes out
       auto put = [&](int i, int rr, float a, float b) {
-        const size_t hrow = (size_t)(sl.e < 0 ? p.T * p.k : 0) + sl.row0 + i;
+        const size_t hrow = MODE == kRows ? 0 : (size_t)assignment(p, tab, sl, i);
         const int c = tile * 128 + rr;
         if (MODE == kRowsGateUp) p.h[hrow * p.I + c] = silu(a) * b;
         else if (MODE == kRowsDown) p.o[hrow * p.H + c] = a;
@@ -467,13 +560,13 @@ qsm_status launch_mode(StreamParams& p, int items, cudaStream_t stream) {
   auto* k = mx4_rows_kernel<MODE>;
   constexpr int NM = mats<MODE>();
   int smem = layout(&p, stage_bytes<MODE>(), NM);
-  const int nc = resident_clusters(reinterpret_cast<void*>(k), p.cs, kThreads, smem, kSmemMax);
+  const int nc = resident_clusters(reinterpret_cast<void*>(k), p.cs, kThreads, smem, smem_max(MODE));
   if (nc < 1) return QSM_ERR_CUDA;
   // With few items a CTA takes only the shared and tensor memory that its
   // own need: the next launch's CTAs then start beside it.
   const int per = (items + nc - 1) / nc;
-  p.single = per == 1 && MODE != kRows;
   if (per == 1) p.nb = p.nacc = 1;
+  if (MODE != kRows && per / (int)p.ntiles.d + 2 > kSlotTab) return QSM_ERR_UNSUPPORTED;
   if (per * p.segs < p.stages) p.stages = per * p.segs;
   p.cs_log = p.cs == 8 ? 3 : p.cs / 2;
   smem = layout(&p, stage_bytes<MODE>(), NM);
@@ -503,7 +596,7 @@ bool plan_rows(StreamParams* p, int mode, int tiles, int tok, int nsm) {
     p->cs = cs;
     p->segs = (nst + cs - 1) / cs;
     p->stages = 0;
-    const int room = (kSmemMax - layout(p, stage, nm)) / stage;
+    const int room = (smem_max(mode) - layout(p, stage, nm)) / stage;
     p->stages = room < kMaxStages ? room : kMaxStages;
     return room >= 3 && p->segs <= kMaxSegs;
   };
@@ -511,7 +604,7 @@ bool plan_rows(StreamParams* p, int mode, int tiles, int tok, int nsm) {
   // fill every SM), and further until the digits fit
   int cs = 1;
   while (2 * cs <= kMaxSplit && 2 * cs <= nst && tiles * 2 * cs <= nsm && fit(2 * cs) &&
-         tiles <= resident_clusters(kernel_of(mode), 2 * cs, kThreads, layout(p, stage, nm), kSmemMax))
+         tiles <= resident_clusters(kernel_of(mode), 2 * cs, kThreads, layout(p, stage, nm), smem_max(mode)))
     cs *= 2;
   for (; cs <= kMaxSplit && cs <= nst; cs *= 2)
     if (fit(cs)) return true;

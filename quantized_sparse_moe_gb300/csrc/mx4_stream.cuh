@@ -21,23 +21,21 @@ struct StreamParams {
   FastDiv ntiles;       // items per slot: row tiles of w (gate_up: pairs of them)
   int slots;            // kRows: groups of `tok` rows of x
   int T, k, I, H;
-  // routed slots: the blocks of tile_map (expert, first sorted row), after the
-  // `shared_tiles` groups of `tok` tokens of the shared expert
-  const int32_t* perm;
-  const int32_t* offsets;
-  const int32_t* tile_map;
-  const int32_t* n_tiles;
-  int shared_tiles;
+  // MoE: the router's choices [T, k], and the slots of the shared expert,
+  // which come first
+  const int32_t* topk_idx;
+  int E, shared_tiles, tok_log;
+  FastDiv k_div;
   const uint16_t* x;    // [T, ldx] bf16 (kRows, kRowsGateUp)
   size_t ldx;
-  float* h;             // [T k + T, I] fp32: written by gate_up, read by down
+  float* h;             // [T k + T, I] fp32, by assignment, then the shared expert's: written by gate_up,
+                        // read by down
   float* o;             // [T k + T, H] fp32 (kRowsDown)
   uint16_t* y;          // [T, N] bf16 (kRows)
   int32_t* status;
   // geometry (host): CTAs per cluster (the split of K), rows of x per slot,
   // digit buffers, ring stages, accumulators, and shared-memory offsets
   int cs, tok, nb, segs, stages, nacc, acc_cols, groups, tmem_cols;
-  int single;           // a cluster for every possible item
   int cs_log;           // log2 cs
   int seg_bytes;        // digits of one stage's columns
   int dig_off, sf_off, part_off;
