@@ -6,12 +6,23 @@
 //   y[r, c]    = code[r, c] * s[r, c / 32]
 //
 // Both are bound by memory: x once in, 4.25 bits a value out, and the
-// reverse.  Sixteen lanes take the 128 columns of one scale tile row, eight
-// columns each: their loads are 16 contiguous bytes (32 for fp32), the codes
-// of a lane one 32-bit word, the four scales of the row in the tile one more,
-// and a block's maximum is two shuffles.  Each thread has four such rows in
-// flight.  The scale is a power of two, so the division is exact and the one
+// reverse.  The scale is a power of two, so the division is exact and the one
 // rounding is the one to the code.
+//
+// Quantizing, eight lanes take the 128 columns of one column of scale tiles,
+// of the four rows r, r + 32, r + 64 and r + 96 that lie together in a tile: a
+// lane has two chunks of eight columns of each, all its loads are under way at
+// once, a block's maximum is two shuffles (16-bit ones two blocks at a time),
+// and the sixteen scales are one store.  4096 x 2048 bf16 takes 10.2 us with x in
+// HBM and 3.7 with it in L2, 65536 x 2048 65 us (5.2 TB/s), 2050 x 1056 fp32
+// 4.9, one row of 2048 2.7 (a launch).  A row per group with four groups in
+// turn, each with its own scale word, took 11.3 (4096 x 2048), 6.1 and 2.9: its
+// address arithmetic and shuffles per value are twice as many.  CTAs of 128
+// threads took 14.3, 5.0 and 2.8; of 512 10.5, 6.7 and 3.1.
+//
+// Dequantizing, sixteen lanes take 128 columns of a row, eight each (a 32-bit
+// word of codes), four such rows in flight: 65536 x 2048 to bf16 72 us (4.7
+// TB/s).
 #include "mx4_common.cuh"
 
 namespace qsm {
@@ -22,27 +33,21 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 constexpr size_t kMaxUnits = 1u << 30;  // (row, column tile) pairs of a call: 2^37 values
 
-// Eight columns of a row as raw words (16 or 32 bytes).
+// Eight columns of a row as raw words.
 template <int DT>
 struct Raw {
-  uint4 a, b;
+  uint4 v[DT == QSM_FP32 ? 2 : 1];
 };
 template <int DT>
-__device__ __forceinline__ Raw<DT> load8(const void* x, size_t i) {
+__device__ __forceinline__ Raw<DT> load8(const char* p) {
   Raw<DT> r;
-  if (DT == QSM_FP32) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + i);
-    r.a = __ldcg(p);
-    r.b = __ldcg(p + 1);
-  } else {
-    r.a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i));
-    r.b = make_uint4(0u, 0u, 0u, 0u);
-  }
+  r.v[0] = __ldg(reinterpret_cast<const uint4*>(p));
+  if (DT == QSM_FP32) r.v[DT == QSM_FP32] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
   return r;
 }
 template <int DT>
 __device__ __forceinline__ void widen(const Raw<DT>& r, float (&v)[8]) {
-  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(r.v);
   if (DT == QSM_FP32) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
@@ -61,56 +66,85 @@ __device__ __forceinline__ void widen(const Raw<DT>& r, float (&v)[8]) {
     }
   }
 }
+// The fp32 bits of the largest magnitudes of a's and b's blocks, whose 32
+// columns four lanes hold: magnitudes compare as integers, 16-bit ones two at
+// a time.
+template <int DT>
+__device__ __forceinline__ uint2 block_max(const Raw<DT>& a, const Raw<DT>& b) {
+  const uint32_t* wa = reinterpret_cast<const uint32_t*>(a.v);
+  const uint32_t* wb = reinterpret_cast<const uint32_t*>(b.v);
+  uint32_t ma = 0, mb = 0;
+  if constexpr (DT == QSM_FP32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ma = max(ma, wa[i] & 0x7fffffffu);
+      mb = max(mb, wb[i] & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      ma = max(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    }
+    return make_uint2(ma, mb);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ma = __vmaxu2(ma, wa[i] & 0x7fff7fffu);
+      mb = __vmaxu2(mb, wb[i] & 0x7fff7fffu);
+    }
+    uint32_t m = __vmaxu2(__byte_perm(ma, mb, 0x5410), __byte_perm(ma, mb, 0x7632));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (DT == QSM_BF16) return make_uint2(m << 16, m & 0xffff0000u);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return make_uint2(__float_as_uint(f.x), __float_as_uint(f.y));
+  }
+}
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
-mx4_quantize_kernel(const void* __restrict__ x, size_t row_stride, uint32_t rows, uint32_t cols,
-                    FastDiv cts, uint32_t units, uint8_t* __restrict__ codes,
+mx4_quantize_kernel(const char* __restrict__ x, size_t row_bytes, uint32_t rows, uint32_t cols,
+                    FastDiv cts, uint32_t groups, uint8_t* __restrict__ codes,
                     uint8_t* __restrict__ scales, int32_t* status) {
+  constexpr int kSize = DT == QSM_FP32 ? 4 : 2;
   pdl_wait();
   pdl_launch_dependents();
-  const uint32_t l16 = threadIdx.x & 15;
-  const uint32_t stride = gridDim.x * (kThreads / 16);
-  bool bad = false;
-  // units: (row, column tile), padded rows included; an even number, so the
-  // two halves of a warp stay together
-  for (uint32_t u0 = blockIdx.x * (kThreads / 16) + threadIdx.x / 16; u0 < units; u0 += kUnroll * stride) {
-    Raw<DT> raw[kUnroll];
-    uint32_t row[kUnroll], ct[kUnroll];
+  const uint32_t g = (blockIdx.x * kThreads + threadIdx.x) >> 3, l = threadIdx.x & 7;
+  if (g >= groups) return;  // whole warps: groups is a multiple of 32
+  const uint32_t q = cts.div(g), ct = g - q * cts.d;
+  const uint32_t r0 = (q >> 5) * kTileRows + (q & 31), c = ct * kTileCols + 8 * l;
+  const char* src = x + (size_t)r0 * row_bytes + (size_t)c * kSize;
+  const bool live[2] = {c < cols, c + 64 < cols};
+  Raw<DT> raw[4][2];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const uint32_t u = u0 + k * stride;
-      row[k] = cts.div(u);
-      ct[k] = u - row[k] * cts.d;
-      const uint32_t c = ct[k] * kTileCols + 8 * l16;
-      raw[k].a = raw[k].b = make_uint4(0u, 0u, 0u, 0u);
-      if (row[k] < rows && c < cols) raw[k] = load8<DT>(x, (size_t)row[k] * row_stride + c);
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      raw[k][h] = {};
+      if (live[h] && r0 + 32 * k < rows) raw[k][h] = load8<DT>(src + (size_t)(32 * k) * row_bytes + 64 * kSize * h);
     }
+  uint8_t* dst = codes + ((size_t)r0 * cols + c) / 2;
+  uint32_t sw[4];
+  bool bad = false;
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const uint32_t r = row[k], c = ct[k] * kTileCols + 8 * l16;
+  for (int k = 0; k < 4; ++k) {
+    const uint2 m = block_max<DT>(raw[k][0], raw[k][1]);
+    const uint32_t s[2] = {scale_of(m.x), scale_of(m.y)};
+    bad |= s[0] == 255u || s[1] == 255u;
+    sw[k] = (s[0] | s[1] << 16) << (8 * (l >> 2));
+    sw[k] |= __shfl_xor_sync(0xffffffffu, sw[k], 4);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float inv = s[h] == 255u ? 0.f : inv_scale(s[h]);
       float v[8];
-      widen<DT>(raw[k], v);
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const uint32_t s = scale_of(m);
-      // the row's four scales in one word, in its first lane
-      uint32_t sw = s << (8 * (l16 >> 2));
-      sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
-      sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
-      if (u0 + k * stride >= units) continue;
-      if (l16 == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(r, ct[k], cts.d)) = sw;
-      if (r >= rows || c >= cols) continue;
-      if (s == 255u) bad = true;
-      const float inv = s == 255u ? 0.f : inv_scale(s);
+      widen<DT>(raw[k][h], v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= inv;
-      *reinterpret_cast<uint32_t*>(codes + ((size_t)r * cols + c) / 2) = f32x8_to_e2m1x8(v);
+      if (live[h] && r0 + 32 * k < rows)
+        *reinterpret_cast<uint32_t*>(dst + (size_t)(16 * k) * cols + 32 * h) = f32x8_to_e2m1x8(v);
     }
   }
+  if (l == 0) *reinterpret_cast<uint4*>(scales + scale_word(r0, ct, cts.d)) = make_uint4(sw[0], sw[1], sw[2], sw[3]);
   if (bad) set_status(status, QSM_DEV_NONFINITE);
 }
 
@@ -213,14 +247,15 @@ extern "C" qsm_status mx4_quantize(const void* x, int32_t dtype, int64_t row_str
       !aligned16(scales) || !aligned4(dev_status))
     return QSM_ERR_INVALID_ARGUMENT;
   const int cts = col_tiles(cols);
-  const size_t units = (size_t)row_tiles(rows) * kTileRows * cts;
-  if (units > kMaxUnits) return QSM_ERR_UNSUPPORTED;
-  const dim3 grid(grid_for(units));
+  const size_t groups = (size_t)row_tiles(rows) * 32 * cts;
+  if (groups > kMaxUnits / 4) return QSM_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)((groups + kThreads / 8 - 1) / (kThreads / 8)));
   auto* kernel = dtype == QSM_BF16   ? mx4_quantize_kernel<QSM_BF16>
                  : dtype == QSM_FP16 ? mx4_quantize_kernel<QSM_FP16>
                                      : mx4_quantize_kernel<QSM_FP32>;
-  QSM_CUDA_TRY(launch_pdl(kernel, grid, dim3(kThreads), 0, stream, x, (size_t)row_stride,
-                          (uint32_t)rows, (uint32_t)cols, FastDiv(cts), (uint32_t)units, codes,
+  QSM_CUDA_TRY(launch_pdl(kernel, grid, dim3(kThreads), 0, stream, static_cast<const char*>(x),
+                          (size_t)row_stride * (dtype == QSM_FP32 ? 4 : 2), (uint32_t)rows,
+                          (uint32_t)cols, FastDiv(cts), (uint32_t)groups, codes,
                           scales, dev_status));
   return QSM_OK;
 }
