@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
     uint32_t round = 0, fs = 0;
     const uint64_t desc0 = tc::sw128_desc(smem_u32(smem));
     for (int item = blockIdx.x; item < total && !warp_aborted(abort_p); item += gridDim.x, ++j) {
-      // tiles of 64 or 192 rows of w: every other one starts in the middle
+      // tiles of 64 rows of w: every other one starts in the middle
       // of a scale tile, two columns on
       const int sf_off = BN % 128 ? ((item % p.nsub) & 1) * 2 : 0;
       const int ab = j % C::kAcc;
@@ -852,13 +852,25 @@ extern "C" qsm_status mx4_gemm(const qsm_mx4* a, const qsm_mx4* w, int32_t dtype
   p.w_scales = w->scales;
   p.status = dev_status;
   if (!make_a_maps(&p, a->codes, a->rows, a->cols)) return QSM_ERR_CUDA;
-  // the widest tile that still gives every SM one (a pair, two)
+  // The width with the least waves of tiles x cost of a wave, which is about
+  // 6 : 7 : 12 for tiles of 64, 128 and 256 columns, and 12 for 256 x 256 on
+  // a pair of SMs (2.3, 2.8, 4.9 and 4.7 us at K = 2048).  Measured, in that
+  // order (us, N x 2048): 128 x 2048 4.6 5.1 6.2 4.6, 300 x 2048 4.6 5.2 6.5
+  // 6.8, 512 x 4096 6.8 5.3 6.6 6.9, 640 x 8192 13.7 10.2 10.5 10.9,
+  // 1024 x 4096 11.4 8.0 6.7 7.5, 1024 x 8192 18.8 13.8 12.4 12.2,
+  // 2048 x 8192 35.4 23.7 22.8 21.4, 4096 x 8192 65.0 41.2 37.4 34.6.  Among
+  // equals the pair wins from two waves on, and the wider tile.
   const int nsm = sm_count();
-  const long long t256 = (long long)p.tiles * ((p.N + 255) / 256);
-  const long long t128 = (long long)p.tiles * ((p.N + 127) / 128);
   const bool f32 = dtype == QSM_FP32;
-  if (t256 >= 2 * nsm) return f32 ? launch_pair<true>(p, a, w, stream) : launch_pair<false>(p, a, w, stream);
-  if (t256 >= nsm) return launch_dense<256>(p, w, f32, stream);
-  if (t128 >= nsm) return launch_dense<128>(p, w, f32, stream);
+  auto waves = [](long long tiles, int at_once) { return (tiles + at_once - 1) / at_once; };
+  auto tiles = [&](int bn) { return (long long)p.tiles * ((p.N + bn - 1) / bn); };
+  const long long c64 = 6 * waves(tiles(64), nsm), c128 = 7 * waves(tiles(128), nsm),
+                  c256 = 12 * waves(tiles(256), nsm),
+                  pair = 12 * waves((p.tiles + 1) / 2 * (long long)((p.N + 255) / 256), nsm / 2);
+  const long long least = c64 < c128 ? (c64 < c256 ? c64 : c256) : (c128 < c256 ? c128 : c256);
+  if (pair >= 24 && pair <= least)
+    return f32 ? launch_pair<true>(p, a, w, stream) : launch_pair<false>(p, a, w, stream);
+  if (c256 == least) return launch_dense<256>(p, w, f32, stream);
+  if (c128 == least) return launch_dense<128>(p, w, f32, stream);
   return launch_dense<64>(p, w, f32, stream);
 }

@@ -144,7 +144,8 @@ def near(y, want, b):
 # one tile and less; two CTAs on one scale tile (64 columns); the wider tiles;
 # K below, at and past a stage, and an odd number of blocks; pairs of SMs
 GEMM = [(1, 1, 32), (5, 70, 64), (128, 64, 96), (130, 200, 256), (33, 257, 288), (200, 640, 1056),
-        (1000, 2600, 352), (128 * 19, 4096, 64), (2401, 4200, 96), (700, 15001, 544)]
+        (1000, 2600, 352), (128 * 19, 4096, 64), (2401, 4200, 96), (700, 15001, 544), (500, 4100, 288),
+        (2100, 4096, 96), (2177, 4090, 544)]
 
 
 @pytest.mark.parametrize("m,n,k", GEMM)
@@ -160,7 +161,7 @@ def test_gemm(qsm, m, n, k, dtype):
     assert st.item() == 0
 
 
-@pytest.mark.parametrize("m,n,k", [(130, 200, 256), (2432, 4096, 64)])
+@pytest.mark.parametrize("m,n,k", [(130, 200, 256), (2432, 4096, 64), (2250, 4096, 64)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_gemm_writes_only_its_part_of_y(qsm, m, n, k, dtype):
     a, _ = mx4(qsm, ref.draw(m, k, 1))
@@ -174,7 +175,7 @@ def test_gemm_writes_only_its_part_of_y(qsm, m, n, k, dtype):
         assert (big == 7.0).all()
 
 
-@pytest.mark.parametrize("m,n", [(130, 200), (2432, 4096)])
+@pytest.mark.parametrize("m,n", [(130, 200), (2432, 4096), (2250, 4096)])
 def test_gemm_keeps_what_is_not_a_number_apart(qsm, m, n):
     x, z = ref.draw(m, 128, 5), ref.draw(n, 128, 6)
     want = qsm.mx4_gemm(mx4(qsm, x)[0], mx4(qsm, z)[0])
