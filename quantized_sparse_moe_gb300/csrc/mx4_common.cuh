@@ -64,19 +64,9 @@ __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_
 
 // --------------------------------------------------------------- e2m1 codes
 
-// Two fp32 values (already divided by the block's scale) to one byte of
-// codes, `lo` in the low nibble: round to nearest, ties to the even code,
+// Eight values (already divided by the block's scale) to eight codes, the
+// first in the lowest nibble: round to nearest, ties to the even code,
 // magnitudes over 6 become 6.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n"
-      " cvt.u32.u8 %0, t;\n}\n"
-      : "=r"(r)
-      : "f"(lo), "f"(hi));
-  return r;
-}
-
-// Eight values to eight codes, the first in the lowest nibble.
 __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&v)[8]) {
   uint32_t r;
   asm("{\n .reg .b8 a, b, c, d;\n"

@@ -30,6 +30,10 @@
 //      written once.  The down weights are requested as soon as U is known, ahead
 //      of h.
 //
+// One token takes 15.7 us (17 MB; H 2048, I 512, 256 experts, 8 of them), against
+// 20.6 in separate launches: what is left is the latency of the chain from the
+// router's rows to y.
+//
 // With more tokens phase C, which has 64 SMs for the down weights, and the
 // computing of all pairs cost more than the launches save (T = 2: 21.2 us against
 // 24.4, T = 3: 28.5 against 25.2, T = 8: 83.8 against 42.3): they take the other

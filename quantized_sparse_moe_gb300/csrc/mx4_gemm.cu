@@ -19,6 +19,11 @@
 // boxes of 32 rows x 128 bytes per warp and TMA stores (or, where rows of y
 // are not 16-byte aligned, through padded boxes and plain stores).  Of a
 // short tile only the rows that exist are loaded and stored, in groups of 8.
+//
+// Measured (graph replay): 300 x 2048 x 2048 4.6 us, 4096 x 8192 x 2048 34.4 us
+// (4.0 PFLOP/s; a pair of SMs per tile, see there).  In the MoE layer of H 2048,
+// I 512 and 256 experts, gate_up takes 50 us at 300 tokens (286 MB of weights, 5.7
+// TB/s: HBM) and 55 at 4096 (811 MB through L2, 14 TB/s: that), down 24 and 46.
 #include <mutex>
 
 #include "mx4_gemm.cuh"
@@ -520,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
 // half from its neighbour: 256 rows a stage and CTA instead of 384, which is
 // what counts, because a 128 x 256 tile on one SM is bound by what an SM can
 // take from L2 (55 bytes a cycle, 26 us for 4096 x 8192 x 2048, where the MMAs
-// need 15).  Every copy of either CTA reports to the leader's (rank 0)
+// need 15; with the pair the copies alone take 16 us, with the MMAs 25, with the
+// 67 MB of outputs 34).  Every copy of either CTA reports to the leader's (rank 0)
 // barrier; the leader issues the scale copies, which move each CTA's tiles
 // into its own tensor memory, and the MMAs, and its commits arrive in both.
 // The scales of w are needed whole in both.

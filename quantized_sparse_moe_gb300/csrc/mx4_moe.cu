@@ -73,7 +73,10 @@ __device__ __forceinline__ void block_bases(const int32_t* counts, const int32_t
 // 32 blocks (1024 columns) of a token, a block to a lane: x is read once, the
 // maximum needs no other lane, and each of the k + 1 copies of a block's
 // codes is one 16-byte store.  The lanes whose block starts a scale tile's
-// row store the row's four scales.
+// row store the row's four scales.  Bound by the copies, 9 of 1.1 KB a token:
+// 4096 tokens of 2048 with 8 experts each 15 us (57 MB, 3.7 TB/s).  CTAs that
+// stay, with the next token's loads under way, made the layer 191.2 -> 187.8 us
+// against one pass of as many CTAs as it takes.
 __global__ void __launch_bounds__(kPrepThreads)
 mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
                    const int32_t* __restrict__ topk_idx, const int32_t* __restrict__ inv_perm,
@@ -152,6 +155,9 @@ mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
 // assignments.  HALF: o holds fp16 of 1/16, rows at[t k + j] and t; else fp32,
 // rows t k + j (where at, the chosen expert, is valid) and T k + t.  A thread
 // takes 8 columns of one token, with the loads of eight assignments in flight.
+// Bound by reading o: 4096 tokens of 2048 with 8 experts each 35.5 us (168 MB in,
+// 17 out, 5.2 TB/s).  A warp to 256 columns of a token took the layer from 197 to
+// 212 us, column passes that keep o in L2 from 197.6 to 199.5.
 template <bool HALF>
 __global__ void __launch_bounds__(kCombThreads, HALF ? kCombCtas : 4)
 mx4_combine_kernel(const void* __restrict__ o, const int32_t* __restrict__ at,

@@ -9,20 +9,21 @@
 // reverse.  The scale is a power of two, so the division is exact and the one
 // rounding is the one to the code.
 //
-// Quantizing, eight lanes take the 128 columns of one column of scale tiles,
-// of the four rows r, r + 32, r + 64 and r + 96 that lie together in a tile: a
-// lane has two chunks of eight columns of each, all its loads are under way at
+// Eight lanes take the 128 columns of one column of scale tiles, of the four
+// rows r, r + 32, r + 64 and r + 96 whose scales lie together in a tile: a lane
+// has two chunks of eight columns of each, all its loads are under way at
 // once, a block's maximum is two shuffles (16-bit ones two blocks at a time),
-// and the sixteen scales are one store.  4096 x 2048 bf16 takes 10.2 us with x in
-// HBM and 3.7 with it in L2, 65536 x 2048 65 us (5.2 TB/s), 2050 x 1056 fp32
-// 4.9, one row of 2048 2.7 (a launch).  A row per group with four groups in
-// turn, each with its own scale word, took 11.3 (4096 x 2048), 6.1 and 2.9: its
-// address arithmetic and shuffles per value are twice as many.  CTAs of 128
-// threads took 14.3, 5.0 and 2.8; of 512 10.5, 6.7 and 3.1.
+// and the sixteen scales are one load or store.
 //
-// Dequantizing, sixteen lanes take 128 columns of a row, eight each (a 32-bit
-// word of codes), four such rows in flight: 65536 x 2048 to bf16 72 us (4.7
-// TB/s).
+// Quantizing 4096 x 2048 bf16 takes 6.3 us of GPU time (3.4 TB/s, half of it
+// launch and latency), 65536 x 2048 63 us (5.4 TB/s), 2050 x 1056 fp32 4.1, one
+// row of 2048 1.6; dequantizing the same 5.6, 50.5 (6.7 TB/s), 4.1 and 1.4.
+// One after the other, the bf16 sizes take 9.0 and (one row) 3.0, 2050 x 1056
+// fp32 4.4.  Before, each group of lanes worked on
+// one row with its own scale word, four such in turn: twice the address
+// arithmetic and shuffles a value (4096 x 2048, both: 11.3; dequantizing 65536
+// x 2048: 72).  CTAs of 128 threads: 14.3 for that, of 512 10.5, where 256 took
+// 10.2.
 #include "mx4_common.cuh"
 
 namespace qsm {
@@ -30,8 +31,7 @@ namespace mx4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
-constexpr size_t kMaxUnits = 1u << 30;  // (row, column tile) pairs of a call: 2^37 values
+constexpr size_t kMaxGroups = 1u << 28;  // of a call, eight lanes and 512 values each
 
 // Eight columns of a row as raw words.
 template <int DT>
@@ -148,72 +148,68 @@ mx4_quantize_kernel(const char* __restrict__ x, size_t row_bytes, uint32_t rows,
   if (bad) set_status(status, QSM_DEV_NONFINITE);
 }
 
-// An e2m1 code as fp16 bits, without the factor 2^14: sign, exponent and
-// mantissa keep their order, subnormals included.
-__device__ __forceinline__ float code_value(uint32_t n) {
-  const uint32_t h = ((n & 8u) << 12) | ((n & 7u) << 9);
-  return __half2float(__ushort_as_half((unsigned short)h)) * 16384.f;
+// Two e2m1 codes (a byte, the first in the low nibble) as fp32 values.
+__device__ __forceinline__ float2 code_values(uint32_t byte) {
+  uint32_t h;
+  asm("{\n .reg .b8 t, u, v, w;\n mov.b32 {t, u, v, w}, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h) : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
 mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                      FastDiv rows, uint32_t cols, FastDiv cts, uint32_t units, size_t scale_bytes,
-                      void* __restrict__ y) {
+                      uint32_t rows, FastDiv rts, uint32_t cols, FastDiv cts, uint32_t groups,
+                      char* __restrict__ y) {
+  constexpr int kSize = DT == QSM_FP32 ? 4 : 2;
   pdl_wait();
   pdl_launch_dependents();
-  const uint32_t l16 = threadIdx.x & 15;
-  const uint32_t stride = gridDim.x * (kThreads / 16);
-  for (uint32_t u0 = blockIdx.x * (kThreads / 16) + threadIdx.x / 16; u0 < units; u0 += kUnroll * stride) {
-    uint32_t w[kUnroll], sw[kUnroll], row[kUnroll], c[kUnroll];  // row: of all experts
+  const uint32_t g = (blockIdx.x * kThreads + threadIdx.x) >> 3, l = threadIdx.x & 7;
+  if (g >= groups) return;
+  const uint32_t q = cts.div(g), ct = g - q * cts.d, rt = q >> 5;  // rt: row tile of all experts
+  const uint32_t e = rts.div(rt), r0 = (rt - e * rts.d) * kTileRows + (q & 31), c = ct * kTileCols + 8 * l;
+  const uint4 sv = __ldg(reinterpret_cast<const uint4*>(scales + ((size_t)rt * cts.d + ct) * kTileBytes + (q & 31) * 16));
+  const size_t at = ((size_t)e * rows + r0) * cols + c;  // the first value
+  const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
+  const bool live[2] = {c < cols, c + 64 < cols};
+  uint32_t w[4][2];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const uint32_t u = u0 + k * stride;
-      row[k] = cts.div(u);
-      const uint32_t ct = u - row[k] * cts.d;
-      c[k] = u < units ? ct * kTileCols + 8 * l16 : cols;
-      if (c[k] >= cols) continue;
-      const uint32_t e = rows.div(row[k]), r = row[k] - e * rows.d;
-      w[k] = __ldcg(reinterpret_cast<const uint32_t*>(codes + ((size_t)row[k] * cols + c[k]) / 2));
-      sw[k] = __ldcg(reinterpret_cast<const uint32_t*>(scales + e * scale_bytes + scale_word(r, ct, cts.d)));
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      w[k][h] = 0;
+      if (live[h] && r0 + 32 * k < rows)
+        w[k][h] = __ldg(reinterpret_cast<const uint32_t*>(codes + at / 2 + (size_t)(16 * k) * cols + 32 * h));
     }
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      if (c[k] >= cols) continue;
-      const float s = scale_value((sw[k] >> (8 * (l16 >> 2))) & 255u);
-      float v[8];
+  for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = code_value((w[k] >> (4 * i)) & 15u) * s;
-      const size_t o = (size_t)row[k] * cols + c[k];
-      if (DT == QSM_FP32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(y) + o);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        uint32_t q[4];
+    for (int h = 0; h < 2; ++h) {
+      const float s = scale_value((sw[k] >> (16 * h + 8 * (l >> 2))) & 255u);
+      uint32_t v[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (DT == QSM_BF16) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            q[i] = *reinterpret_cast<const uint32_t*>(&b);
-          } else {
-            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-            q[i] = *reinterpret_cast<const uint32_t*>(&h);
-          }
+      for (int i = 0; i < 4; ++i) {
+        float2 f = code_values(w[k][h] >> (8 * i));
+        f.x *= s;
+        f.y *= s;
+        if (DT == QSM_FP32) {
+          v[2 * i] = __float_as_uint(f.x);
+          v[2 * i + 1] = __float_as_uint(f.y);
+        } else if (DT == QSM_BF16) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+          v[i] = *reinterpret_cast<const uint32_t*>(&b);
+        } else {
+          const __half2 b = __floats2half2_rn(f.x, f.y);
+          v[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + o) = make_uint4(q[0], q[1], q[2], q[3]);
       }
+      if (!live[h] || r0 + 32 * k >= rows) continue;
+      uint4* dst = reinterpret_cast<uint4*>(y + (at + (size_t)(32 * k) * cols + 64 * h) * kSize);
+      dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      if (DT == QSM_FP32) dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
-  }
 }
 
-// CTAs for `units` groups of 16 lanes, each thread taking kUnroll of them:
-// enough for one pass, at most eight CTAs (all that fit) per SM.
-int grid_for(size_t units) {
-  const size_t per = (kThreads / 16) * (size_t)kUnroll;
-  const size_t need = (units + per - 1) / per, most = (size_t)sm_count() * 8;
-  return (int)(need < 1 ? 1 : need < most ? need : most);
-}
+unsigned grid_for(size_t groups) { return (unsigned)((groups + kThreads / 8 - 1) / (kThreads / 8)); }
 
 bool valid_dtype(int dt) { return dt == QSM_BF16 || dt == QSM_FP16 || dt == QSM_FP32; }
 
@@ -248,8 +244,8 @@ extern "C" qsm_status mx4_quantize(const void* x, int32_t dtype, int64_t row_str
     return QSM_ERR_INVALID_ARGUMENT;
   const int cts = col_tiles(cols);
   const size_t groups = (size_t)row_tiles(rows) * 32 * cts;
-  if (groups > kMaxUnits / 4) return QSM_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)((groups + kThreads / 8 - 1) / (kThreads / 8)));
+  if (groups > kMaxGroups) return QSM_ERR_UNSUPPORTED;
+  const dim3 grid(grid_for(groups));
   auto* kernel = dtype == QSM_BF16   ? mx4_quantize_kernel<QSM_BF16>
                  : dtype == QSM_FP16 ? mx4_quantize_kernel<QSM_FP16>
                                      : mx4_quantize_kernel<QSM_FP32>;
@@ -268,14 +264,15 @@ extern "C" qsm_status mx4_dequantize(const qsm_mx4* a, int32_t dtype, void* y,
   if (a->rows == 0 && a->experts >= 1) return QSM_OK;
   if (!mx4_valid(a) || !y || !aligned16(y)) return QSM_ERR_INVALID_ARGUMENT;
   const int cts = col_tiles(a->cols);
-  const size_t units = (size_t)a->experts * a->rows * cts;
-  if (units > kMaxUnits) return QSM_ERR_UNSUPPORTED;
-  const dim3 grid(grid_for(units));
+  const int rts = row_tiles(a->rows);
+  const size_t groups = (size_t)a->experts * rts * 32 * cts;
+  if (groups > kMaxGroups) return QSM_ERR_UNSUPPORTED;
+  const dim3 grid(grid_for(groups));
   auto* kernel = dtype == QSM_BF16   ? mx4_dequantize_kernel<QSM_BF16>
                  : dtype == QSM_FP16 ? mx4_dequantize_kernel<QSM_FP16>
                                      : mx4_dequantize_kernel<QSM_FP32>;
   QSM_CUDA_TRY(launch_pdl(kernel, grid, dim3(kThreads), 0, stream, a->codes, a->scales,
-                          FastDiv(a->rows), (uint32_t)a->cols, FastDiv(cts), (uint32_t)units,
-                          mx4_scale_bytes(a->rows, a->cols), y));
+                          (uint32_t)a->rows, FastDiv(rts), (uint32_t)a->cols, FastDiv(cts),
+                          (uint32_t)groups, static_cast<char*>(y)));
   return QSM_OK;
 }

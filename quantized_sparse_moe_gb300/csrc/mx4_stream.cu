@@ -34,6 +34,10 @@
 // scale copies and MMAs, warps 4-7 are the epilogue, the other ten make the
 // digits of the next slot while the current one is multiplied.
 //
+// Measured (graph replay): 1 x 512 x 2048 4.5 us, 5 x 2048 x 8192 8.4, 1 x 128256
+// x 2048 27.0 (139.7 MB, 5.2 TB/s); 37 tokens of the layer below 37 us in gate_up
+// (204 MB, 5.5 TB/s) and 22 in down (103 MB, 4.7 TB/s).
+//
 // In the MoE layer the slots are formed here, by every CTA for itself, from
 // the router's choices (a bit per token and expert: counts and ranks; a prefix
 // sum; then the lists of the CTA's own slots), instead of by a launch of its
