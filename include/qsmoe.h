@@ -529,10 +529,11 @@ QSM_API uint64_t qsm_launch_count(void);
 QSM_API qsm_status qsm_debug_force_path(int32_t mode);
 
 /* Test hook for the bounded waits: make the logit exchange of moe_decode_layer
- * (and of moe_mx4_forward's one-launch form) wait for a call tag `skew` ahead of the call's own (0 = off, the
- * default), so that no call can complete it: every wait runs out, the kernel sets QSM_DEV_TIMEOUT
- * in *dev_status, finishes with invalid results and returns, and the
- * context stays usable.  The call ticket stays consistent (every CTA still
+ * (and of moe_mx4_forward's one-launch form) wait for a call tag `skew` ahead
+ * of the call's own (0 = off, the default), so that no call can complete it:
+ * every wait runs out, the kernel sets QSM_DEV_TIMEOUT in *dev_status,
+ * finishes with invalid results (mx4: the workspace then has to be zeroed) and
+ * returns, and the context stays usable.  The call ticket stays consistent (every CTA still
  * arrives once).  Process-wide; skew in [0, 1024]. */
 QSM_API qsm_status qsm_debug_barrier_skew(int32_t skew);
 
@@ -540,8 +541,8 @@ QSM_API qsm_status qsm_debug_barrier_skew(int32_t skew);
  * ("oMLX MoE gate/up 融合优化", "融合原理": the rows of the [gate; up]
  * concatenation come out bit-identical to separate gate and up
  * projections).  With buf set (a device buffer of n_floats fp32), every
- * kernel that computes gate_up also writes, before SwiGLU, the fp32 gate
- * value of intermediate i to buf[row * 2I + i] and the up value to
+ * kernel that computes gate_up from Q8_0 or affine-4 weights also writes,
+ * before SwiGLU, the fp32 gate value of intermediate i to buf[row * 2I + i] and the up value to
  * buf[row * 2I + I + i], where row is the row of h the kernel writes:
  *   moe_ffn_forward (decode and prefill paths): the sorted assignment row
  *     (< T*k), then T*k + t for token t of the shared expert: at least

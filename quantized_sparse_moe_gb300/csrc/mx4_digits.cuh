@@ -3,7 +3,6 @@
 #pragma once
 
 #include <mutex>
-#include <vector>
 
 #include "mx4_common.cuh"
 
@@ -71,21 +70,23 @@ __device__ __forceinline__ void store_digits(const uint32_t (&plane)[kDigits], u
   }
 }
 
-// Clusters of cs CTAs of `kernel` that the current device holds at once (asked
-// once per device, kernel and size); 0 when the query fails.  Allows the kernel
-// smem_max bytes of dynamic shared memory.
+// Clusters of cs CTAs of `kernel` that the current device holds at once; 0 when
+// the query fails.  Allows the kernel smem_max bytes of dynamic shared memory.
+// The last kKept answers (device, kernel, sizes) are kept: the query takes
+// longer than a small product.
 inline int resident_clusters(void* kernel, int cs, int threads, int smem, int smem_max) {
-  struct Key {
+  constexpr int kKept = 64;
+  static std::mutex mu;
+  static struct {
     int dev;
     void* k;
     int cs, smem, n;
-  };
-  static std::mutex mu;
-  static std::vector<Key> cache;
+  } kept[kKept];
+  static int next = 0;  // a kernel of null: not yet written
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   std::lock_guard<std::mutex> lock(mu);
-  for (const Key& c : cache)
+  for (const auto& c : kept)
     if (c.dev == dev && c.k == kernel && c.cs == cs && c.smem == smem) return c.n;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) != cudaSuccess)
     return 0;
@@ -103,7 +104,8 @@ inline int resident_clusters(void* kernel, int cs, int threads, int smem, int sm
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
   }
-  cache.push_back({dev, kernel, cs, smem, n});
+  kept[next] = {dev, kernel, cs, smem, n};
+  next = (next + 1) % kKept;
   return n;
 }
 

@@ -81,6 +81,23 @@ def _word(device: int) -> int:
     return w[0]
 
 
+def _status(t, dev: int, what: str) -> int:
+    """The address of a status word to use: the caller's t, or the device's."""
+    if t is None:
+        return _word(dev)
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.numel() < 1:
+        raise QSMError(f"{what}: dev_status must be an int32 tensor on the operands' device")
+    return t.data_ptr()
+
+
+def _fp32(t, shape, dev: int, what: str):
+    """t, None or a contiguous fp32 tensor of that shape on the device."""
+    if t is not None and (t.dtype is not torch.float32 or tuple(t.shape) != shape
+                          or not t.is_contiguous() or t.get_device() != dev):
+        raise QSMError(f"{what} must be contiguous fp32 {list(shape)} on the weights' device")
+    return t
+
+
 def _matrix(x: torch.Tensor, what: str):
     """(device, rows, columns, row stride) of a CUDA matrix whose rows are
     contiguous."""
@@ -155,7 +172,7 @@ def mx4_quantize(x: torch.Tensor, out: Mx4Tensor | None = None, dev_status=None,
         raise QSMError("mx4_quantize: out has another shape or device")
     rc = (_lib or _load()).mx4_quantize(
         x.data_ptr(), dtype, ld, rows, cols, out.c.codes, out.c.scales,
-        _word(dev) if dev_status is None else dev_status.data_ptr(),
+        _status(dev_status, dev, "mx4_quantize"),
         _stream_of(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "mx4_quantize")
@@ -196,7 +213,7 @@ def mx4_gemm(a: Mx4Tensor, w: Mx4Tensor, dtype=torch.bfloat16, y=None, dev_statu
             raise QSMError("mx4_gemm: y must be [M, N] of dtype on the operands' device")
     rc = (_lib or _load()).mx4_gemm(
         a.ref, w.ref, _DTYPES[dtype], y.data_ptr(), ld,
-        _word(dev) if dev_status is None else dev_status.data_ptr(),
+        _status(dev_status, dev, "mx4_gemm"),
         _stream_of(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "mx4_gemm")
@@ -217,7 +234,7 @@ def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, y=None, dev_status=None, stream=None
         raise QSMError("mx4_gemv: y must be a contiguous bf16 [T, N] on x's device")
     rc = (_lib or _load()).mx4_gemv(
         x.data_ptr(), ld, T, w.ref, y.data_ptr(),
-        _word(dev) if dev_status is None else dev_status.data_ptr(),
+        _status(dev_status, dev, "mx4_gemv"),
         _stream_of(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "mx4_gemv")
@@ -235,6 +252,12 @@ class Mx4Layer:
         self.w_router, self.logit_bias, self.shared_gate = w_router, logit_bias, shared_gate
         self.gate_up, self.down = gate_up, down
         self.shared_gate_up, self.shared_down = shared_gate_up, shared_down
+        self.device = gate_up.device
+        if any(m.device != self.device for m in (down, shared_gate_up, shared_down)):
+            raise QSMError("Mx4Layer: the weights must be on one GPU")
+        # what self.c points to
+        self._keep = (gate_up, down, shared_gate_up, shared_down,
+                      _fp32(shared_gate, (H,), self.device, "Mx4Layer: shared_gate"))
         self.c = Mx4LayerC(H, I, E, k, gate_up.c, down.c, shared_gate_up.c, shared_down.c,
                            None if shared_gate is None else shared_gate.data_ptr())
 
@@ -254,7 +277,7 @@ class Mx4Layer:
 
 def moe_mx4_workspace_bytes(layer: Mx4Layer, T: int, acts: str = "bf16") -> int:
     """0 when the layer, T or acts is not supported."""
-    return int(lib().moe_mx4_workspace_bytes(ctypes.byref(layer.c), T, _ACTS[acts]))
+    return int(lib().moe_mx4_workspace_bytes(ctypes.byref(layer.c), T, _ACTS.get(acts, -1)))
 
 
 class Mx4Forward:
@@ -268,8 +291,13 @@ class Mx4Forward:
         if acts not in _ACTS:
             raise QSMError('Mx4Forward: acts must be "bf16" or "mx4"')
         need = moe_mx4_workspace_bytes(layer, T, acts)
-        if need == 0 and T > 0:
+        if T < 0 or (need == 0 and T > 0):
             raise QSMError("Mx4Forward: unsupported layer or token count")
+        # the router as it is now (what the calls point to)
+        self._router = (_fp32(layer.w_router, (layer.E, layer.H), layer.device, "Mx4Forward: w_router"),
+                        _fp32(layer.logit_bias, (layer.E,), layer.device, "Mx4Forward: logit_bias"))
+        if self._router[0] is None:
+            raise QSMError("Mx4Forward: the layer has no router")
         self.layer, self.T, self.acts = layer, T, acts
         k, H = layer.k, layer.H
         self.topk_idx = torch.empty((T, k), dtype=torch.int32, device=device)
@@ -285,14 +313,18 @@ class Mx4Forward:
         self._tail = (p(self.y_f32), p(self.workspace), self.workspace.numel(), p(self.dev_status))
         self._layer_ref = ctypes.byref(layer.c)
         self._device, self._shape = self.y.get_device(), self.y.shape
+        if self._device != layer.device:
+            raise QSMError("Mx4Forward: device is not the weights'")
 
     def __call__(self, x: torch.Tensor, stream=None, out=None) -> torch.Tensor:
         """Run the layer on x [T, H] bf16; the result goes to out (a [T, H] bf16
         tensor, contiguous) when given, else to self.y.  Returns it."""
         y = self.y if out is None else out
         for t in (x,) if out is None else (x, out):
-            if t.dtype is not torch.bfloat16 or t.shape != self._shape or not t.is_contiguous():
-                raise QSMError("Mx4Forward: x and out must be contiguous [T, H] bf16 tensors")
+            if (t.dtype is not torch.bfloat16 or t.shape != self._shape or not t.is_contiguous()
+                    or t.get_device() != self._device):
+                raise QSMError("Mx4Forward: x and out must be contiguous [T, H] bf16 tensors on "
+                               "the layer's device")
         rc = self._fn(self._layer_ref, x.data_ptr(), *self._mid, y.data_ptr(), *self._tail,
                       _stream_of(self._device) if stream is None else stream.cuda_stream)
         if rc:

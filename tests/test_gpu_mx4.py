@@ -486,6 +486,33 @@ def test_moe_refuses(qsm):
     assert qsm.Mx4Forward(L, 0)(torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")).shape == (0, 256)
 
 
+def test_refuses_what_is_on_the_host_or_of_another_type(qsm):
+    """No launch may ever see a host address or a short array."""
+    L, _ = layer(qsm, 256, 128, 8, 2, seed=1)
+    f = qsm.Mx4Forward(L, 4)
+    x = hidden(4, 256, 1)
+    for call in (lambda: f(x.cpu()), lambda: f(x, out=torch.empty(4, 256, dtype=torch.bfloat16)),
+                 lambda: qsm.mx4_quantize(x.cpu()), lambda: qsm.mx4_gemv(x.cpu(), L.shared_gate_up),
+                 lambda: qsm.mx4_gemv(x, L.shared_gate_up, dev_status=torch.zeros(1, dtype=torch.int32)),
+                 lambda: qsm.mx4_quantize(x, dev_status=torch.zeros(1, device="cuda"))):
+        with pytest.raises(qsm.QSMError):
+            call()
+    good = L.w_router
+    for bad in (good.cpu(), good.double(), good[:7], good.t(), None):
+        L.w_router = bad
+        with pytest.raises(qsm.QSMError):
+            qsm.Mx4Forward(L, 4)
+    L.w_router, L.logit_bias = good, torch.zeros(7, device="cuda")
+    with pytest.raises(qsm.QSMError):
+        qsm.Mx4Forward(L, 4)
+    with pytest.raises(qsm.QSMError):
+        qsm.Mx4Layer(256, 128, 8, 2, L.gate_up, L.down, L.shared_gate_up, L.shared_down, good,
+                     shared_gate=torch.zeros(256, device="cuda", dtype=torch.bfloat16))
+    with pytest.raises(qsm.QSMError):
+        qsm.Mx4Forward(L, -1)
+    assert qsm.moe_mx4_workspace_bytes(L, 4, "fp8") == 0
+
+
 def test_layer_from_dense_weights(qsm):
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
