@@ -34,9 +34,11 @@
 // scale copies and MMAs, warps 4-7 are the epilogue, the other ten make the
 // digits of the next slot while the current one is multiplied.
 //
-// Measured (graph replay): 1 x 512 x 2048 4.5 us, 5 x 2048 x 8192 8.4, 1 x 128256
-// x 2048 27.0 (139.7 MB, 5.2 TB/s); 37 tokens of the layer below 37 us in gate_up
-// (204 MB, 5.5 TB/s) and 22 in down (103 MB, 4.7 TB/s).
+// Measured (graph replay): 1 x 512 x 2048 4.4 us, 5 x 2048 x 8192 7.9, 1 x 128256
+// x 2048 25.3 (139.7 MB, 5.5 TB/s), 16 rows of the same 35.8: a row of 2048 costs
+// a CTA about half a microsecond of integer instructions for its digits.  37
+// tokens of the layer below take 36 us in gate_up (204 MB, 5.7 TB/s) and 21 in
+// down (103 MB, 4.9 TB/s).
 //
 // In the MoE layer the slots are formed here, by every CTA for itself, from
 // the router's choices (a bit per token and expert: counts and ranks; a prefix
@@ -53,8 +55,8 @@ namespace mx4 {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kConvWarps = 10;
-constexpr int kMaxStages = 12;
+constexpr int kConvWarps = 10;  // of the digits: 24 x 128256 x 2048 44.5 us, 8 47.5
+constexpr int kMaxStages = 7;  // of the ring: 1 x 128256 x 2048 25.4 us, 4 25.8, 9 25.8, 12 27.1
 // dynamic shared memory; barriers and the table of slots take some of the rest
 constexpr int smem_max(int mode) { return (mode == kRows ? 224 : 218) * 1024; }
 constexpr int kMaxSplit = 8;          // CTAs per cluster
