@@ -37,14 +37,15 @@
 // Measured (graph replay): 1 x 512 x 2048 4.4 us, 5 x 2048 x 8192 7.9, 1 x 128256
 // x 2048 25.3 (139.7 MB, 5.5 TB/s), 16 rows of the same 35.8: a row of 2048 costs
 // a CTA about half a microsecond of integer instructions for its digits.  37
-// tokens of the layer below take 36 us in gate_up (204 MB, 5.7 TB/s) and 21 in
-// down (103 MB, 4.9 TB/s).
+// tokens of the layer below take 37 us in gate_up (204 MB, 5.5 TB/s) and 22 in
+// down (103 MB, 4.6 TB/s).
 //
 // In the MoE layer the slots are formed here, by every CTA for itself, from
 // the router's choices (a bit per token and expert: counts and ranks; a prefix
 // sum; then the lists of the CTA's own slots), instead of by a launch of its
 // own (H 2048, I 512, 256 experts, 8 of them: T = 6: 38.6 -> 36.1 us a layer,
-// T = 37: 76.6 -> 74.6, T = 64: 99.0 -> 95.3; T = 4: 28.5 -> 28.9).  h and o
+// T = 37: 76.6 -> 74.6, T = 64: 99.0 -> 95.3; T = 4: 28.5 -> 28.9; since then
+// T = 3: 23.8, 8: 40.3, 37: 72.5, 64: 93.1).  h and o
 // are indexed by the assignment t k + j.
 #include <type_traits>
 
@@ -608,7 +609,8 @@ bool plan_rows(StreamParams* p, int mode, int tiles, int tok, int nsm) {
   };
   // K is split as long as all items still run at once (clusters of 8 do not
   // fill every SM): 1 x 512 x 2048 4.5 us against 5.6 unsplit, 5 x 2048 x 8192
-  // 8.4 against 18.2, 32 x 2048 x 2048 11.5 against 18.3; and further until the
+  // 8.4 against 18.2, 32 x 2048 x 2048 11.5 against 18.3 (before the digits
+  // became faster); and further until the
   // digits fit
   int cs = 1;
   while (2 * cs <= kMaxSplit && 2 * cs <= nst && tiles * 2 * cs <= nsm && fit(2 * cs) &&
