@@ -15,13 +15,11 @@
 // of BN columns, or one of 256 (two leave no tensor memory for the scales).
 // The epilogue's threads take their half rows into registers at once (BN / 2
 // columns each), hand the accumulator back and convert and store while the
-// next tile's MMAs run.  The outputs leave through swizzled
-// boxes of 32 rows x 128 bytes per warp and TMA stores (or, where rows of y
-// are not 16-byte aligned, through padded boxes and plain stores).  Of a
-// short tile only the rows that exist are loaded and stored, in groups of 8.
+// next tile's MMAs run.  Of a short tile only the rows that exist are loaded
+// (in groups of 8) and stored.
 //
-// Measured (graph replay): 300 x 2048 x 2048 4.6 us, 4096 x 8192 x 2048 34.4 us
-// (4.0 PFLOP/s; a pair of SMs per tile, see there).  In the MoE layer of H 2048,
+// Measured (graph replay): 300 x 2048 x 2048 4.5 us, 4096 x 8192 x 2048 31 us (4.4
+// PFLOP/s), x 8192 78 us (7.0; a pair of SMs per tile, see there).  In the MoE layer of H 2048,
 // I 512 and 256 experts, gate_up takes 50 us at 300 tokens (286 MB of weights, 5.7
 // TB/s: HBM) and 55 at 4096 (811 MB through L2, 14 TB/s: that), down 26 and 49.
 #include <mutex>
@@ -33,22 +31,17 @@ namespace mx4 {
 
 namespace {
 
-// Rows of y (pitch ldy elements) as boxes of box_rows rows.
-bool make_out_map(CUtensorMap* m, void* y, CUtensorMapDataType dt, int el, uint64_t rows, int cols,
-                  size_t ldy, int box_cols, int box_rows, CUtensorMapSwizzle swz) {
-  tc::EncodeTiledFn fn = tc::encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, rows};
-  const cuuint64_t strides[1] = {ldy * el};
-  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, dt, 2, y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// fp16 outputs [rows, cols] as swizzled boxes of 64 columns and box_rows rows.
+bool make_out_map(CUtensorMap* m, void* y, uint64_t rows, int cols, int box_rows) {
+  return tc::make_map_2d(m, y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rows, cols, 64, box_rows,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
-constexpr int kStagePitch = 144;  // bytes of a row in a padded box (128 + 16)
+constexpr int kDownBox = 32 * 128;  // bytes of a swizzled box of down: 32 rows of 64 outputs
+constexpr int kBoxBytes = 64;   // of a row in a warp's box, for outputs that are not aligned
+constexpr int kBoxPitch = 80;   // 16 more: the rows fall in different banks
 
 template <int MODE, int BN, bool F32>
 struct Cfg {
@@ -58,17 +51,9 @@ struct Cfg {
   static constexpr int kSfaBytes = 2 * kTileBytes;
   static constexpr int kSfwBytes = 2 * kTileBytes * kGroups;
   static constexpr int kStage = kABytes + kWBytes + kSfaBytes + kSfwBytes;
-  static constexpr int kStages = MODE == kGateUp ? 4 : BN == 256 ? 3 : BN >= 128 ? 4 : 6;
-  // the epilogue: a thread's columns, the bytes of them that make a box's
-  // row, and the boxes of a warp at a time
-  static constexpr int NC = BN / 2;
-  static constexpr int kEl = F32 ? 4 : 2;
-  static constexpr int kInner = NC * kEl % 128 == 0 ? 128 : 64;
-  static constexpr int kBoxCols = kInner / kEl;
-  static constexpr int kBoxes = NC / kBoxCols < 4 ? NC / kBoxCols : 2;
-  static constexpr int kBoxBytes = kBoxes * 32 * kInner;
-  static constexpr int kWarpBytes = MODE == kGateUp ? 0
-                                    : kBoxBytes > 32 * kStagePitch ? kBoxBytes : (32 * kStagePitch + 1023) / 1024 * 1024;
+  static constexpr int kStages = MODE == kDown ? 3 : BN == 256 ? 4 : 6;
+  static constexpr int NC = BN / 2;  // columns of an epilogue thread
+  static constexpr int kWarpBytes = MODE == kGateUp ? 0 : MODE == kDown ? NC / 64 * kDownBox : 32 * kBoxPitch;
   static constexpr int kSmem = kStages * kStage + kEpiWarps * kWarpBytes + 1024;
   static constexpr int kSfCols = 8 + 8 * kGroups;  // scale columns of one stage
   static constexpr int kAcc = BN == 256 ? 1 : 2;   // accumulators
@@ -154,6 +139,12 @@ __device__ __forceinline__ void store_chunk(void* y, size_t off, int n, int N, u
   }
 }
 
+__device__ __forceinline__ void store_sector(void* dst, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y),
+               "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -176,87 +167,104 @@ __device__ __forceinline__ void take_acc(uint32_t taddr, int half, uint32_t (&r)
 }
 
 // The NC outputs that each lane of a warp holds of its row (row 32 q4 + lane of
-// the cnt that exist from row0 on), columns col .. of y, by way of the warp's
-// boxes at `stage`.
-template <int MODE, int BN, bool F32>
-__device__ __forceinline__ void store_tile(const GemmParams& p, const uint32_t (&r)[BN / 2], int row0,
-                                           int cnt, int col, int q4, int lane, unsigned char* stage,
-                                           bool& bad) {
-  using C = Cfg<MODE, BN, F32>;
-  constexpr int kStep = C::kBoxes * C::kBoxCols;  // columns staged at a time
-  constexpr int kPer = 16 / C::kEl;               // columns in a 16-byte piece
-  __half2 top = __half2half2(__ushort_as_half(0));
+// the cnt that exist from row0 on), columns col .. of y.  Where rows of y are
+// aligned they go out from the registers, a sector of 32 bytes per lane and
+// instruction: shared memory has enough to do with the operands (4096 x 8192 x
+// 2048: 31.3 us; by swizzled boxes and TMA 34.7).  Else by way of the warp's box
+// at `stage`, so that lanes write neighbouring bytes.
+template <int BN, bool F32>
+__device__ __forceinline__ void store_dense(const GemmParams& p, const uint32_t (&r)[BN / 2], int row0,
+                                            int cnt, int col, int q4, int lane, unsigned char* stage) {
+  using C = Cfg<kDense, BN, F32>;
+  constexpr int kEl = F32 ? 4 : 2, kPer = 16 / kEl;  // kPer: columns in a 16-byte piece
   auto piece = [&](int c) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (F32) {
-        w[i] = r[c + i];
-        continue;
-      }
-      const float a = __uint_as_float(r[c + 2 * i]), b = __uint_as_float(r[c + 2 * i + 1]);
-      if (MODE == kDown) {  // fp16 of 1/16 the value
-        const __half2 h = __floats2half2_rn(a * kOutScale, b * kOutScale);
-        if (col + c / C::kBoxCols * C::kBoxCols < p.N) top = __hmax2(top, __habs2(h));
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        w[i] = pack_bf16(a, b);
-      }
-    }
+    for (int i = 0; i < 4; ++i)
+      w[i] = F32 ? r[c + i] : pack_bf16(__uint_as_float(r[c + 2 * i]), __uint_as_float(r[c + 2 * i + 1]));
     return make_uint4(w[0], w[1], w[2], w[3]);
   };
+  if (p.align >= 16) {
+    if (32 * q4 + lane >= cnt) return;
+    const size_t at = ((size_t)row0 + 32 * q4 + lane) * p.ldy + col;
 #pragma unroll
-  for (int c0 = 0; c0 < C::NC; c0 += kStep) {
-    if (p.vec) {
-      if (lane == 0) store_wait_read();  // the boxes may be written again
+    for (int c = 0; c < C::NC; c += 2 * kPer) {
+      const uint4 v0 = piece(c), v1 = piece(c + kPer);
+      if (col + c + 2 * kPer <= p.N) {
+        char* dst = static_cast<char*>(p.y) + (at + c) * kEl;
+        if (p.align == 32) {
+          store_sector(dst, v0, v1);
+        } else {
+          reinterpret_cast<uint4*>(dst)[0] = v0;
+          reinterpret_cast<uint4*>(dst)[1] = v1;
+        }
+      } else {
+        store_chunk<F32>(p.y, at + c, col + c, p.N, v0);
+        store_chunk<F32>(p.y, at + c + kPer, col + c + kPer, p.N, v1);
+      }
+    }
+  } else {
+    constexpr int kChunks = kBoxBytes / 16;
+#pragma unroll
+    for (int c0 = 0; c0 < C::NC; c0 += kChunks * kPer) {
       __syncwarp();
 #pragma unroll
-      for (int c = 0; c < kStep; c += kPer) {
-        const int box = c / C::kBoxCols, ch = c % C::kBoxCols / kPer;
-        const int sw = C::kInner == 128 ? lane & 7 : (lane >> 1) & 3;
-        *reinterpret_cast<uint4*>(stage + box * 32 * C::kInner + lane * C::kInner + ((ch ^ sw) << 4)) =
-            piece(c0 + c);
-      }
-      tc::fence_async_smem();
+      for (int ch = 0; ch < kChunks; ++ch)
+        *reinterpret_cast<uint4*>(stage + lane * kBoxPitch + ch * 16) = piece(c0 + ch * kPer);
       __syncwarp();
-      if (lane == 0) {
-        const int rows = cnt - 32 * q4;  // that exist of the warp's 32
-#pragma unroll
-        for (int box = 0; box < C::kBoxes; ++box) {
-          const int at = col + c0 + box * C::kBoxCols;
-          if (at >= p.N) break;
-          unsigned char* src = stage + box * 32 * C::kInner;
-          if (rows > 24) {
-            tma_store_2d(&p.y_map, src, at, row0 + 32 * q4);
-          } else {
-            for (int i = 0; i < rows; i += 8)
-              tma_store_2d(&p.y8_map, src + i * C::kInner, at, row0 + 32 * q4 + i);
-          }
-        }
-        store_commit();
-      }
-    } else {
-#pragma unroll
-      for (int box = 0; box < C::kBoxes; ++box) {
-        __syncwarp();
-#pragma unroll
-        for (int ch = 0; ch < C::kInner / 16; ++ch)
-          *reinterpret_cast<uint4*>(stage + lane * kStagePitch + ch * 16) =
-              piece(c0 + box * C::kBoxCols + ch * kPer);
-        __syncwarp();
-        constexpr int kChunks = C::kInner / 16;
-        for (int i = lane; i < 32 * kChunks; i += 32) {
-          const int rr = i / kChunks, ch = i % kChunks;
-          const int n = col + c0 + box * C::kBoxCols + ch * kPer;
-          if (32 * q4 + rr < cnt && n < p.N)
-            store_chunk<F32>(p.y, ((size_t)row0 + 32 * q4 + rr) * p.ldy + n, n, p.N,
-                             *reinterpret_cast<const uint4*>(stage + rr * kStagePitch + ch * 16));
-        }
+      for (int i = lane; i < 32 * kChunks; i += 32) {
+        const int rr = i / kChunks, ch = i % kChunks;
+        const int n = col + c0 + ch * kPer;
+        if (32 * q4 + rr < cnt && n < p.N)
+          store_chunk<F32>(p.y, ((size_t)row0 + 32 * q4 + rr) * p.ldy + n, n, p.N,
+                           *reinterpret_cast<const uint4*>(stage + rr * kBoxPitch + ch * 16));
       }
     }
   }
-  if (MODE == kDown && 32 * q4 + lane < cnt && (__hisinf(__low2half(top)) || __hisinf(__high2half(top))))
-    bad = true;
+}
+
+// The same of down: fp16 of 1/16 the value (bad: one does not fit), by way of
+// swizzled boxes of 32 rows x 128 bytes at `stage` and TMA: with two stages
+// of K per tile the outputs are what counts, and whole lines cost L2 less than
+// sectors (4096 tokens, H = 2048: 185.1 us a layer, with sectors 188.6).
+template <int BN>
+__device__ __forceinline__ void store_down(const GemmParams& p, const uint32_t (&r)[BN / 2], int row0, int cnt,
+                                           int col, int q4, int lane, unsigned char* stage, bool& bad) {
+  constexpr int NC = BN / 2;
+  __half2 top = __half2half2(__ushort_as_half(0));
+  if (lane == 0) store_wait_read();  // the boxes may be written again
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < NC; c += 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(__uint_as_float(r[c + 2 * i]) * kOutScale,
+                                          __uint_as_float(r[c + 2 * i + 1]) * kOutScale);
+      if (col + c < p.N) top = __hmax2(top, __habs2(h));
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(stage + c / 64 * kDownBox + lane * 128 + ((c % 64 / 8 ^ (lane & 7)) << 4)) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  tc::fence_async_smem();
+  __syncwarp();
+  const int rows = cnt - 32 * q4;  // that exist of the warp's 32
+  if (lane == 0) {
+#pragma unroll
+    for (int box = 0; box < NC / 64; ++box) {
+      if (col + 64 * box >= p.N) break;
+      const unsigned char* src = stage + box * kDownBox;
+      if (rows > 24) {
+        tma_store_2d(&p.y_map, src, col + 64 * box, row0 + 32 * q4);
+      } else {
+        for (int i = 0; i < rows; i += 8)
+          tma_store_2d(&p.y8_map, src + i * 128, col + 64 * box, row0 + 32 * q4 + i);
+      }
+    }
+    store_commit();
+  }
+  if (lane < rows && (__hisinf(__low2half(top)) || __hisinf(__high2half(top)))) bad = true;
 }
 
 template <int MODE, int BN, bool F32>
@@ -506,11 +514,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
           uint8_t* sw = p.h_scales + scale_word((int)pos, t.n0 >> 7, p.I >> 7);
           *reinterpret_cast<uint16_t*>(sw + 2 * half) = (uint16_t)sbytes;
         }
+      } else if constexpr (MODE == kDown) {
+        store_down<BN>(p, r, t.a_row, t.cnt, t.n0 + half * NC, q4, lane, stage, bad);
       } else {
-        store_tile<MODE, BN, F32>(p, r, t.a_row, t.cnt, t.n0 + half * C::NC, q4, lane, stage, bad);
+        store_dense<BN, F32>(p, r, t.a_row, t.cnt, t.n0 + half * NC, q4, lane, stage);
       }
     }
-    if (MODE != kGateUp && lane == 0) store_wait();
+    if (MODE == kDown && lane == 0) store_wait();
     if (bad) set_status(p.status, MODE == kGateUp ? QSM_DEV_NONFINITE : QSM_DEV_FP16_RANGE);
   }
   tc::tc_fence_before();
@@ -526,16 +536,17 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
 // what counts, because a 128 x 256 tile on one SM is bound by what an SM can
 // take from L2 (55 bytes a cycle, 26 us for 4096 x 8192 x 2048, where the MMAs
 // need 15; with the pair the copies alone take 16 us, with the MMAs 25, with the
-// 67 MB of outputs 34).  Every copy of either CTA reports to the leader's (rank 0)
-// barrier; the leader issues the scale copies, which move each CTA's tiles
-// into its own tensor memory, and the MMAs, and its commits arrive in both.
-// The scales of w are needed whole in both.
+// 67 MB of outputs 31; with four stages of K instead of five 33).  Every copy
+// of either CTA reports to the leader's (rank 0) barrier; the leader issues the
+// scale copies, which move each CTA's tiles into its own tensor memory, and the
+// MMAs, and its commits arrive in both.  The scales of w are needed whole in
+// both.
 template <bool F32>
 struct Pair {
   using C = Cfg<kDense, 256, F32>;
   static constexpr int kHalf = 128 * 128;  // codes of 128 rows
   static constexpr int kStage = 2 * kHalf + 6 * kTileBytes;
-  static constexpr int kStages = 4;
+  static constexpr int kStages = 5;
   static constexpr int kSmem = kStages * kStage + kEpiWarps * C::kWarpBytes + 1024;
   static_assert(kStage % 1024 == 0 && kSmem <= 226 * 1024, "stages");
 };
@@ -693,7 +704,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_pair_kernel(const __grid
     unsigned char* stage = smem + P::kStages * P::kStage + (warp - 4) * C::kWarpBytes;
     const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16);
     const uint32_t acc_bar = dsmem_addr(&acc_empty, 0);
-    bool bad = false;
     int j = 0;
     for (int item = pair; item < total; item += pairs, ++j) {
       if (warp_aborted(abort_p)) break;
@@ -706,10 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_pair_kernel(const __grid
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_cluster(acc_bar);
-      if (32 * q4 < cnt)
-        store_tile<kDense, 256, F32>(p, r, row0, cnt, nt * 256 + half * C::NC, q4, lane, stage, bad);
+      if (32 * q4 < cnt) store_dense<256, F32>(p, r, row0, cnt, nt * 256 + half * C::NC, q4, lane, stage);
     }
-    if (lane == 0) store_wait();
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -719,20 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_pair_kernel(const __grid
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// The output maps of p (where rows of y are aligned).
-template <typename C, bool F32>
-bool make_out_maps(GemmParams* p, bool fp16, uint64_t rows) {
-  if (!p->vec) return true;
-  const CUtensorMapDataType dt = fp16  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                 : F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const CUtensorMapSwizzle swz = C::kInner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  return make_out_map(&p->y_map, p->y, dt, C::kEl, rows, p->N, p->ldy, C::kBoxCols, 32, swz) &&
-         make_out_map(&p->y8_map, p->y, dt, C::kEl, rows, p->N, p->ldy, C::kBoxCols, 8, swz);
-}
-
 template <int MODE, int BN, bool F32>
-qsm_status launch_tile(GemmParams& p, int most, uint64_t rows, cudaStream_t stream) {
+qsm_status launch_tile(GemmParams& p, int most, cudaStream_t stream) {
   using C = Cfg<MODE, BN, F32>;
   auto* k = mx4_gemm_kernel<MODE, BN, F32>;
   static thread_local int ready_dev = -1;  // the attribute is per device
@@ -742,7 +738,6 @@ qsm_status launch_tile(GemmParams& p, int most, uint64_t rows, cudaStream_t stre
     QSM_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
     ready_dev = dev;
   }
-  if (MODE != kGateUp && !make_out_maps<C, F32>(&p, MODE == kDown, rows)) return QSM_ERR_CUDA;
   const int grid = most < sm_count() ? most : sm_count();
   QSM_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(kThreads), C::kSmem, stream, p));
   return QSM_OK;
@@ -783,7 +778,6 @@ bool make_scales_map(CUtensorMap* m, const uint8_t* scales, int rows, int cols) 
 template <bool F32>
 qsm_status launch_pair(GemmParams& p, const qsm_mx4* a, const qsm_mx4* w, cudaStream_t stream) {
   using P = Pair<F32>;
-  using C = Cfg<kDense, 256, F32>;
   auto* k = mx4_gemm_pair_kernel<F32>;
   static thread_local int ready_dev = -1;
   int dev = 0;
@@ -797,8 +791,7 @@ qsm_status launch_pair(GemmParams& p, const qsm_mx4* a, const qsm_mx4* w, cudaSt
   if ((long long)p.tiles * p.nsub > (1ll << 30)) return QSM_ERR_UNSUPPORTED;
   if (!make_codes_map(&p.w, w->codes, w->rows, w->cols, 128) ||
       !make_scales_map(&p.a_sf, a->scales, a->rows, a->cols) ||
-      !make_scales_map(&p.w_sf, w->scales, w->rows, w->cols) ||
-      !make_out_maps<C, F32>(&p, false, p.M))
+      !make_scales_map(&p.w_sf, w->scales, w->rows, w->cols))
     return QSM_ERR_CUDA;
   const int most = resident_pairs(reinterpret_cast<void*>(k), P::kSmem), items = p.tiles * p.nsub;
   if (most < 1) return QSM_ERR_CUDA;
@@ -813,8 +806,8 @@ qsm_status launch_dense(GemmParams& p, const qsm_mx4* w, bool f32, cudaStream_t 
   p.nsub = (p.N + BN - 1) / BN;
   if ((long long)p.tiles * p.nsub > (1ll << 30)) return QSM_ERR_UNSUPPORTED;
   const int most = p.tiles * p.nsub;
-  return f32 ? launch_tile<kDense, BN, true>(p, most, p.M, stream)
-             : launch_tile<kDense, BN, false>(p, most, p.M, stream);
+  return f32 ? launch_tile<kDense, BN, true>(p, most, stream)
+             : launch_tile<kDense, BN, false>(p, most, stream);
 }
 
 }  // namespace
@@ -826,8 +819,10 @@ bool make_a_maps(GemmParams* p, const void* codes, uint64_t rows, int K) {
 
 qsm_status launch_grouped(GemmParams& p, int mode, uint64_t rows, cudaStream_t stream) {
   const int most = 1 << 30;  // how many tiles there are is known on the device only
-  return mode == kGateUp ? launch_tile<kGateUp, 256, false>(p, most, rows, stream)
-                         : launch_tile<kDown, kDownRows, false>(p, most, rows, stream);
+  if (mode == kDown && (!make_out_map(&p.y_map, p.y, rows, p.N, 32) || !make_out_map(&p.y8_map, p.y, rows, p.N, 8)))
+    return QSM_ERR_CUDA;
+  return mode == kGateUp ? launch_tile<kGateUp, 256, false>(p, most, stream)
+                         : launch_tile<kDown, kDownRows, false>(p, most, stream);
 }
 
 }  // namespace mx4
@@ -853,28 +848,30 @@ extern "C" qsm_status mx4_gemm(const qsm_mx4* a, const qsm_mx4* w, int32_t dtype
   p.tiles = row_tiles(p.M);
   p.y = y;
   p.ldy = (size_t)ldy;
-  p.vec = aligned16(y) && (size_t)ldy * el % 16 == 0;
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(y) | (uintptr_t)ldy * el;
+  p.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0;
   p.a_scales = a->scales;
   p.w_scales = w->scales;
   p.status = dev_status;
   if (!make_a_maps(&p, a->codes, a->rows, a->cols)) return QSM_ERR_CUDA;
   // The width with the least waves of tiles x cost of a wave, which is about
   // 6 : 7 : 12 for tiles of 64, 128 and 256 columns, and 12 for 256 x 256 on
-  // a pair of SMs (2.3, 2.8, 4.9 and 4.7 us at K = 2048).  Measured, in that
-  // order (us, N x 2048): 128 x 2048 4.6 5.1 6.2 4.6, 300 x 2048 4.6 5.2 6.5
-  // 6.8, 512 x 4096 6.8 5.3 6.6 6.9, 640 x 8192 13.7 10.2 10.5 10.9,
-  // 1024 x 4096 11.4 8.0 6.7 7.5, 1024 x 8192 18.8 13.8 12.4 12.2,
-  // 2048 x 8192 35.4 23.7 22.8 21.4, 4096 x 8192 65.0 41.2 37.4 34.6.  Among
-  // equals the pair wins from two waves on, and the wider tile.
+  // a pair of SMs.  Measured, in that order (us): 300 x 2048 x 2048 4.5 5.1 6.6
+  // 7.0, 512 x 4096 x 2048 6.7 5.3 6.8 7.2, 640 x 8192 x 2048 13.7 9.8 10.1 10.8,
+  // 1024 x 4096 x 2048 11.5 7.7 6.9 7.8, 2048 x 4096 x 2048 18.5 12.5 10.7 11.6.
+  // Among equals the wider tile, and the pair where its smaller operand traffic
+  // pays (128, 256, pair): 4096 x 8192 x 1024 23.8 22.1 24.4, x 2048 36.9 31.5
+  // 31.2, x 4096 67.0 51.0 47.3, x 8192 126 89.2 78.6; 1024 x 8192 x 2048 13.0
+  // 11.2 11.9, x 4096 21.2 16.4 16.0, x 8192 38.7 28.9 26.6.
   const int nsm = sm_count();
   const bool f32 = dtype == QSM_FP32;
   auto waves = [](long long tiles, int at_once) { return (tiles + at_once - 1) / at_once; };
   auto tiles = [&](int bn) { return (long long)p.tiles * ((p.N + bn - 1) / bn); };
   const long long c64 = 6 * waves(tiles(64), nsm), c128 = 7 * waves(tiles(128), nsm),
                   c256 = 12 * waves(tiles(256), nsm),
-                  pair = 12 * waves((p.tiles + 1) / 2 * (long long)((p.N + 255) / 256), nsm / 2);
+                  pair = waves((p.tiles + 1) / 2 * (long long)((p.N + 255) / 256), nsm / 2);
   const long long least = c64 < c128 ? (c64 < c256 ? c64 : c256) : (c128 < c256 ? c128 : c256);
-  if (pair >= 24 && pair <= least)
+  if (12 * pair <= least && p.K >= 2048 && pair * p.K >= 8192)
     return f32 ? launch_pair<true>(p, a, w, stream) : launch_pair<false>(p, a, w, stream);
   if (c256 == least) return launch_dense<256>(p, w, f32, stream);
   if (c128 == least) return launch_dense<128>(p, w, f32, stream);

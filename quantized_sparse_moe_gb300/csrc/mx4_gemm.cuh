@@ -22,7 +22,7 @@ constexpr int kDownRows = 256;
 struct GemmParams {
   CUtensorMap a, a32, a8;  // codes of a, boxes of 128, 32 and 8 rows
   CUtensorMap w, w_sh;   // codes of w (routed, shared), boxes of BN rows (gate_up: 128)
-  CUtensorMap y_map, y8_map;  // y, boxes of 32 and 8 rows (where vec)
+  CUtensorMap y_map, y8_map;  // down: the outputs, boxes of 32 and 8 rows
   CUtensorMap a_sf, w_sf;  // scale tiles, boxes of two (pairs of CTAs)
   const uint8_t* a_scales;
   const uint8_t* w_scales;
@@ -30,10 +30,9 @@ struct GemmParams {
   int M, N, K;           // N: rows of w (per expert)
   int tiles;             // row tiles of a (dense)
   int nsub;              // column tiles
-  // dense and down
-  void* y;
-  size_t ldy;
-  int vec;               // rows of y are 16-byte aligned: stored by TMA
+  void* y;               // dense and down
+  size_t ldy;            // dense
+  int align;             // dense, of the rows of y: 32 or 16 bytes, 0: less
   // grouped: tile tau < shared_tiles holds tokens 128 tau .. of the shared
   // expert, the others the blocks of tile_map (expert, first sorted row);
   // tile tau's rows of a (and of h and of y) start at 128 tau

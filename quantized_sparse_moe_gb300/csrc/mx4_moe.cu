@@ -464,8 +464,6 @@ qsm_status many_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x
   d.K = I;
   d.nsub = (H + kDownRows - 1) / kDownRows;
   d.y = ws + pl.o;
-  d.ldy = H;
-  d.vec = 1;
   const qsm_status st = launch_grouped(p, kGateUp, pl.rows, stream);
   return st != QSM_OK ? st : launch_grouped(d, kDown, pl.rows, stream);
 }

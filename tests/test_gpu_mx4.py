@@ -145,7 +145,10 @@ def near(y, want, b):
 # K below, at and past a stage, and an odd number of blocks; pairs of SMs
 GEMM = [(1, 1, 32), (5, 70, 64), (128, 64, 96), (130, 200, 256), (33, 257, 288), (200, 640, 1056),
         (1000, 2600, 352), (128 * 19, 4096, 64), (2401, 4200, 96), (700, 15001, 544), (500, 4100, 288),
-        (2100, 4096, 96), (2177, 4090, 544)]
+        (2100, 4096, 96), (2177, 4090, 544),
+        # long sums on pairs of SMs: an odd number of row tiles, a last tile of one
+        # row, columns that end inside a tile, an odd number of blocks
+        (2100, 4096, 4128), (2177, 4090, 4096), (130, 2000, 8192), (4000, 8001, 2080)]
 
 
 @pytest.mark.parametrize("m,n,k", GEMM)
@@ -161,7 +164,7 @@ def test_gemm(qsm, m, n, k, dtype):
     assert st.item() == 0
 
 
-@pytest.mark.parametrize("m,n,k", [(130, 200, 256), (2432, 4096, 64), (2250, 4096, 64)])
+@pytest.mark.parametrize("m,n,k", [(130, 200, 256), (2432, 4096, 64), (2250, 4096, 64), (2250, 4096, 4096)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_gemm_writes_only_its_part_of_y(qsm, m, n, k, dtype):
     a, _ = mx4(qsm, ref.draw(m, k, 1))
@@ -175,9 +178,9 @@ def test_gemm_writes_only_its_part_of_y(qsm, m, n, k, dtype):
         assert (big == 7.0).all()
 
 
-@pytest.mark.parametrize("m,n", [(130, 200), (2432, 4096), (2250, 4096)])
-def test_gemm_keeps_what_is_not_a_number_apart(qsm, m, n):
-    x, z = ref.draw(m, 128, 5), ref.draw(n, 128, 6)
+@pytest.mark.parametrize("m,n,k", [(130, 200, 128), (2432, 4096, 128), (2250, 4096, 128), (2250, 4096, 4096)])
+def test_gemm_keeps_what_is_not_a_number_apart(qsm, m, n, k):
+    x, z = ref.draw(m, k, 5), ref.draw(n, k, 6)
     want = qsm.mx4_gemm(mx4(qsm, x)[0], mx4(qsm, z)[0])
     x[7, 40], z[150, 100] = math.nan, math.inf
     y = qsm.mx4_gemm(qsm.mx4_quantize(x), qsm.mx4_quantize(z))
