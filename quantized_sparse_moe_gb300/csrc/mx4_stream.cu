@@ -657,6 +657,17 @@ extern "C" qsm_status mx4_gemv(const uint16_t* x, int64_t row_stride, int32_t T,
   int tok = T;  // all rows at once, or as many as fit
   while (tok > 0 && !plan_rows(&p, kRows, ntiles, tok, sm_count())) --tok;
   if (tok == 0) return QSM_ERR_UNSUPPORTED;
+  // Where K is split only because the digits of all rows do not fit (every SM
+  // has a tile without), halves of the rows that need no split are faster up to
+  // K of 4096, although the weights are read twice, the second time in part from
+  // L2: 32 x 128256 x 2048 58.6 us against 85.6, 28 x 19456 x 2048 14.8 against
+  // 20.0, 24 x 65536 x 2560 41.1 against 44.5, 28 x 65536 x 3328 57.1 against 68.9,
+  // 26 x 32768 x 3840 41.9 against 41.1; 16 x 65536 x 4096 52.0 against 45.9,
+  // 8 x 32768 x 8192 46.3 against 36.3.
+  if (p.cs > 1 && ntiles >= sm_count() && p.K < 4096) {
+    StreamParams half = p;
+    if (plan_rows(&half, kRows, ntiles, (T + 1) / 2, sm_count()) && half.cs == 1) p = half;
+  }
   p.slots = (T + p.tok - 1) / p.tok;
   if (!make_codes_map(&p.w, w->codes, w->rows, w->cols, 128)) return QSM_ERR_CUDA;
   if ((long long)p.slots * ntiles > (1ll << 30)) return QSM_ERR_UNSUPPORTED;

@@ -213,7 +213,8 @@ def rows_bound(x, w):
 # one stage and less, splits of K over 2, 4 and 8 CTAs, a ragged last stage,
 # more rows than fit at once
 GEMV = [(1, 1, 32), (1, 512, 2048), (2, 130, 96), (3, 200, 512), (7, 300, 1056), (8, 2048, 2048),
-        (9, 129, 4064), (17, 1000, 288), (32, 640, 2048), (31, 257, 8192), (32, 200, 16384), (5, 40000, 256)]
+        (9, 129, 4064), (17, 1000, 288), (32, 640, 2048), (31, 257, 8192), (32, 200, 16384), (5, 40000, 256),
+        (29, 19500, 2048), (32, 19456, 2560)]   # in halves
 
 
 @pytest.mark.parametrize("t,n,k", GEMV)
