@@ -21,7 +21,7 @@
 // Measured (graph replay): 300 x 2048 x 2048 4.5 us, 4096 x 8192 x 2048 31 us (4.4
 // PFLOP/s), x 8192 78 us (7.0; a pair of SMs per tile, see there).  In the MoE layer of H 2048,
 // I 512 and 256 experts, gate_up takes 50 us at 300 tokens (286 MB of weights, 5.7
-// TB/s: HBM) and 55 at 4096 (811 MB through L2, 14 TB/s: that), down 26 and 49.
+// TB/s: HBM) and 55 at 4096 (802 MB through L2, 14 TB/s: that), down 26 and 49.
 #include <mutex>
 
 #include "mx4_gemm.cuh"
