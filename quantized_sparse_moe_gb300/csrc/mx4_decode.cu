@@ -36,7 +36,7 @@
 //
 // With more tokens phase C, which has 64 SMs for the down weights, and the
 // computing of all pairs cost more than the launches save (T = 2: 21.2 us against
-// 24.4, T = 3: 28.5 against 25.2 (now 23.8), T = 8: 83.8 against 42.3 (40.3)): they take the other
+// 24.4, T = 3: 28.5 against 25.2 (now 23.8), T = 8: 83.8 against 42.3 (38.7)): they take the other
 // form.
 //
 // Sums run in a fixed order: y depends on nothing but the inputs.  Every wait

@@ -4,7 +4,7 @@
 //
 // QSM_ACTS_BF16 (few tokens): one launch for one or two (mx4_decode.cu); else
 // gate_up + SwiGLU and down by the streaming kernel (mx4_stream.cu) over slots
-// of up to 8 tokens of an expert, with activations of 16 bits and more; h and
+// of up to 4 or 8 tokens of an expert, with activations of 16 bits and more; h and
 // o are fp32.  Bound by the touched weights.
 //
 // QSM_ACTS_MX4 (many tokens): the token rows are quantized once and written
@@ -281,7 +281,13 @@ bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
     if (T > QSM_MX4_MOE_MAX_ROWS) return false;
     const int touched = (long long)T * k < E ? T * k : E;
     bool fit = false;
-    int tok = 8;  // a power of two, no more than the tokens need
+    // Rows of a slot: a power of two, no more than the tokens need.  Four leave
+    // more shared memory to the ring of weights, eight read the weights of an
+    // expert with many tokens less often.  H 2048, I 512, four against eight (us):
+    // 256 experts, 8 of them: T = 8 38.7 40.8, 16 50.7 51.9, 37 72.5 72.6, the
+    // same with uneven routing: 24 41.0 40.2, 37 48.0 44.6, 64 65.3 58.4; 64
+    // experts, 8: 16 38.2 40.3, 64 57.3 48.7; 8 experts, 2: 12 21.3 22.8.
+    int tok = T <= 16 ? 4 : 8;
     while (tok > 1 && tok / 2 >= T) tok /= 2;
     for (; tok >= 1 && !fit; tok /= 2) {
       const int slots = touched + (T + tok - 1) / tok;

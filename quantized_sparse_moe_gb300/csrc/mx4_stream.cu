@@ -45,7 +45,7 @@
 // sum; then the lists of the CTA's own slots), instead of by a launch of its
 // own (H 2048, I 512, 256 experts, 8 of them: T = 6: 38.6 -> 36.1 us a layer,
 // T = 37: 76.6 -> 74.6, T = 64: 99.0 -> 95.3; T = 4: 28.5 -> 28.9; since then
-// T = 3: 23.8, 8: 40.3, 37: 72.5, 64: 93.1).  h and o
+// T = 3: 23.8, 8: 38.7, 37: 72.5, 64: 93.0).  h and o
 // are indexed by the assignment t k + j.
 #include <type_traits>
 
