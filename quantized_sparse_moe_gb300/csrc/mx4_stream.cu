@@ -45,7 +45,7 @@
 // sum; then the lists of the CTA's own slots), instead of by a launch of its
 // own (H 2048, I 512, 256 experts, 8 of them: T = 6: 38.6 -> 36.1 us a layer,
 // T = 37: 76.6 -> 74.6, T = 64: 99.0 -> 95.3; T = 4: 28.5 -> 28.9; since then
-// T = 3: 23.8, 8: 38.7, 37: 72.5, 64: 93.0).  h and o
+// T = 3: 24.3, 8: 37.8, 37: 72.5, 64: 93.3).  h and o
 // are indexed by the assignment t k + j.
 #include <type_traits>
 
@@ -86,22 +86,27 @@ struct SlotTable {
   int warp_sum[kThreads / 32];
 };
 
-// The expert of this thread's assignments (-1: none that is valid), their
-// ranks among the expert's, and the experts' counts.  A token has an expert
-// at most once, and there are at most 64: a bit per token in the expert's
-// mask (at `mask`, 8 bytes an expert) gives both, the same in every CTA.
-__device__ __forceinline__ void assign_ranks(const StreamParams& p, SlotTable& t, uint2* mask,
-                                             int (&id)[kMaxChunks], int (&rank)[kMaxChunks]) {
-  const int A = p.T * p.k, tid = threadIdx.x;
-  for (int e = tid; e < p.E; e += kThreads) mask[e] = make_uint2(0u, 0u);
+// The chosen experts of this thread's assignments.
+__device__ __forceinline__ void load_choices(const StreamParams& p, int (&id)[kMaxChunks]) {
+  const int A = p.T * p.k;
 #pragma unroll
   for (int c = 0; c < kMaxChunks; ++c) {
-    const int a = c * kThreads + tid;
+    const int a = c * kThreads + threadIdx.x;
     id[c] = a < A ? __ldcg(p.topk_idx + a) : -1;
-    if (id[c] < 0 || id[c] >= p.E) id[c] = -1;
-    rank[c] = (int)p.k_div.div(a);  // the token
   }
-  __syncthreads();
+}
+// Of those the valid ones (others become -1), their ranks among the expert's,
+// and the experts' counts.  A token has an expert at most once, and there are
+// at most 64: a bit per token in the expert's mask (at `mask`, 8 bytes an
+// expert, zeros) gives both, the same in every CTA.
+__device__ __forceinline__ void assign_ranks(const StreamParams& p, SlotTable& t, uint2* mask,
+                                             int (&id)[kMaxChunks], int (&rank)[kMaxChunks]) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int c = 0; c < kMaxChunks; ++c) {
+    if (id[c] < 0 || id[c] >= p.E) id[c] = -1;
+    rank[c] = (int)p.k_div.div(c * kThreads + tid);  // the token
+  }
 #pragma unroll
   for (int c = 0; c < kMaxChunks; ++c)
     if (id[c] >= 0)
@@ -237,6 +242,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
 
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int cs = p.cs, stages = p.stages;
+  // Down: the routing and the weights are older than the previous launch
+  // (which let this one start after its own wait), so the slots are formed and
+  // the loading warp goes on without waiting; h is the previous launch's.
+  int id[kMaxChunks], rank_of[kMaxChunks];
+  if (MODE == kRowsDown) load_choices(p, id);
+  if (MODE != kRows)
+    for (int e = threadIdx.x; e < p.E; e += kThreads) reinterpret_cast<uint2*>(smem)[e] = make_uint2(0u, 0u);
   const int rank = cs > 1 ? (int)cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -269,17 +281,14 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_rows_kernel(const __grid_cons
   // this CTA's stages of K
   const int nst = (p.K + kStageK - 1) / kStageK, cts = col_tiles(p.K);
   const int s0 = nst * rank >> p.cs_log, s1 = nst * (rank + 1) >> p.cs_log;
-  // Down: the routing and the weights are older than the previous launch
-  // (which let this one start after its own wait), so the loading warp goes
-  // on without waiting; h is the previous launch's.
   if (MODE != kRowsDown) {
     pdl_wait();
     pdl_launch_dependents();
   }
   // This cluster's contiguous run of items (slot, tile).
-  int id[kMaxChunks], rank_of[kMaxChunks];
   uint32_t slots = p.slots;
   if (MODE != kRows) {
+    if (MODE == kRowsGateUp) load_choices(p, id);
     assign_ranks(p, *tab, reinterpret_cast<uint2*>(smem), id, rank_of);
     slots = slot_starts(p, *tab);
   }
