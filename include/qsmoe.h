@@ -144,7 +144,7 @@ typedef struct {
 /* ----------------------------------------------------------------- router */
 
 /* Bytes of workspace moe_route needs for T tokens, hidden size H and E
- * experts. */
+ * experts, whatever k is. */
 QSM_API size_t moe_route_workspace_bytes(int32_t T, int32_t H, int32_t E);
 
 /* Route flags (the `renormalize` argument of the routing calls). */

@@ -313,11 +313,7 @@ bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
     return at;
   };
   const size_t A = (size_t)T * k;
-  // the routers' larger need: with k > 8 many tokens take the CUDA-core one,
-  // which keeps counters and logits [T, E]
-  const size_t plain = up256((size_t)(T + 7) / 8 * 4) + up256((size_t)T * E * 4);
-  const size_t route = moe_route_workspace_bytes(T, H, E);
-  p.route = take(route > plain ? route : plain);
+  p.route = take(moe_route_workspace_bytes(T, H, E));
   p.route_end = off;
   if (acts == QSM_ACTS_MX4) {
     p.counts = take((size_t)E * 4);

@@ -252,10 +252,23 @@ qsm_status route_tc_launch(const uint16_t* x, const float* w_router,
                            cudaStream_t stream);
 }  // namespace qsm
 
+namespace qsm {
+namespace {
+// What the router that takes k experts a token keeps in its workspace: many
+// tokens with k <= 8 the tensor-core one's split weights, all others the
+// CUDA-core one's counters and logits.
+size_t workspace_need(int T, int H, int E, int k) {
+  if (route_tc_supported(T, H, E, k)) return route_tc_workspace_bytes(T, H, E);
+  return counters_bytes(T) + (((size_t)T * E * sizeof(float) + 255) & ~size_t(255));
+}
+}  // namespace
+}  // namespace qsm
+
 extern "C" size_t moe_route_workspace_bytes(int32_t T, int32_t H, int32_t E) {
   if (T < 0 || H <= 0 || E <= 0) return 0;
-  if (qsm::route_tc_supported(T, H, E, 1)) return qsm::route_tc_workspace_bytes(T, H, E);
-  return qsm::counters_bytes(T) + (((size_t)T * E * sizeof(float) + 255) & ~size_t(255));
+  // whatever k is: the larger need of the two routers
+  const size_t few = qsm::workspace_need(T, H, E, 1), many = qsm::workspace_need(T, H, E, qsm::kMaxK);
+  return few > many ? few : many;
 }
 
 extern "C" qsm_status moe_route(const uint16_t* x, const float* w_router,
@@ -275,8 +288,7 @@ extern "C" qsm_status moe_route(const uint16_t* x, const float* w_router,
       !aligned4(topk_idx) || !aligned4(topk_w) || !aligned4(dev_status) ||
       (logit_bias && !aligned4(logit_bias)))
     return QSM_ERR_INVALID_ARGUMENT;
-  if (workspace_bytes < moe_route_workspace_bytes(T, H, E))
-    return QSM_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < workspace_need(T, H, E, k)) return QSM_ERR_WORKSPACE_TOO_SMALL;
   if (route_tc_supported(T, H, E, k))  // many tokens: tensor-core logits
     return route_tc_launch(x, w_router, logit_bias, T, H, E, k, renormalize,
                            topk_idx, topk_w, workspace, dev_status, stream);
@@ -319,8 +331,7 @@ extern "C" qsm_status moe_route_group(const uint16_t* x, const float* w_router,
       !aligned4(topk_idx) || !aligned4(topk_w) || !aligned4(dev_status) ||
       (logit_bias && !aligned4(logit_bias)))
     return QSM_ERR_INVALID_ARGUMENT;
-  if (workspace_bytes < moe_route_workspace_bytes(T, H, E))
-    return QSM_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < workspace_need(T, H, E, k)) return QSM_ERR_WORKSPACE_TOO_SMALL;
   unsigned* counters = static_cast<unsigned*>(workspace);
   float* logits = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                            counters_bytes(T));
