@@ -502,8 +502,11 @@ QSM_API size_t moe_mx4_workspace_bytes(const qsm_mx4_layer* L, int32_t T, int32_
  * at once, so a call that shares the GPU with work that holds SMs for a second
  * sets QSM_DEV_TIMEOUT; its results are then invalid and the workspace has to
  * be zeroed before the next call.
- * With QSM_ACTS_MX4 the outputs of the experts are held in fp16 (scaled by
- * 1/16) until they are summed: one beyond that range sets QSM_DEV_FP16_RANGE. */
+ * With QSM_ACTS_MX4 the outputs of the experts are held in fp16 until they are
+ * summed, with a power of two of their own for every 128 columns of a row: to
+ * 2^-11 of the value, and 2^-39 of the largest magnitude of the 128.  Magnitudes
+ * of 2^20 and more do not fit and set QSM_DEV_FP16_RANGE (their y is infinite
+ * or not a number). */
 QSM_API qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x, int32_t T,
                                    int32_t acts, const float* w_router, const float* logit_bias,
                                    int32_t flags, int32_t* topk_idx, float* topk_w, uint16_t* y,

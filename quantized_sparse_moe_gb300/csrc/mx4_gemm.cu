@@ -223,7 +223,11 @@ __device__ __forceinline__ void store_dense(const GemmParams& p, const uint32_t 
   }
 }
 
-// The same of down: fp16 of 1/16 the value (bad: one does not fit), by way of
+// The same of down, in fp16 with a power of two of the row's 128 columns taken
+// out, which goes to y_scale: the largest magnitude lies in 2^14 .. 2^15 then,
+// and what is down to 2^-29 of it keeps 11 bits (the bf16 result has 8), whatever
+// the magnitude; under 2^-86 the power stays 2^-100.  It is at most 2^4, so
+// that an output that does not fit (2^20 and more) is reported (bad).  By way of
 // swizzled boxes of 32 rows x 128 bytes at `stage` and TMA: with two stages
 // of K per tile the outputs are what counts, and whole lines cost L2 less than
 // sectors (4096 tokens, H = 2048: 185.1 us a layer, with sectors 188.6).
@@ -231,7 +235,13 @@ template <int BN>
 __device__ __forceinline__ void store_down(const GemmParams& p, const uint32_t (&r)[BN / 2], int row0, int cnt,
                                            int col, int q4, int lane, unsigned char* stage, bool& bad) {
   constexpr int NC = BN / 2;
-  __half2 top = __half2half2(__ushort_as_half(0));
+  static_assert(NC == kOutCols, "a thread has a power of two's columns");
+  if (col >= p.N) return;  // N is a multiple of NC: all of them
+  float top = 0.f;  // (a NaN does not count, and stays one)
+#pragma unroll
+  for (int c = 0; c < NC; ++c) top = fmaxf(top, fabsf(__uint_as_float(r[c])));
+  const int sh = min(max(14 + 127 - (int)(__float_as_uint(top) >> 23), -4), 100);
+  const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
   if (lane == 0) store_wait_read();  // the boxes may be written again
   __syncwarp();
 #pragma unroll
@@ -239,9 +249,8 @@ __device__ __forceinline__ void store_down(const GemmParams& p, const uint32_t (
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __half2 h = __floats2half2_rn(__uint_as_float(r[c + 2 * i]) * kOutScale,
-                                          __uint_as_float(r[c + 2 * i + 1]) * kOutScale);
-      if (col + c < p.N) top = __hmax2(top, __habs2(h));
+      const __half2 h = __floats2half2_rn(__uint_as_float(r[c + 2 * i]) * f,
+                                          __uint_as_float(r[c + 2 * i + 1]) * f);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     *reinterpret_cast<uint4*>(stage + c / 64 * kDownBox + lane * 128 + ((c % 64 / 8 ^ (lane & 7)) << 4)) =
@@ -253,7 +262,6 @@ __device__ __forceinline__ void store_down(const GemmParams& p, const uint32_t (
   if (lane == 0) {
 #pragma unroll
     for (int box = 0; box < NC / 64; ++box) {
-      if (col + 64 * box >= p.N) break;
       const unsigned char* src = stage + box * kDownBox;
       if (rows > 24) {
         tma_store_2d(&p.y_map, src, col + 64 * box, row0 + 32 * q4);
@@ -264,7 +272,10 @@ __device__ __forceinline__ void store_down(const GemmParams& p, const uint32_t (
     }
     store_commit();
   }
-  if (lane < rows && (__hisinf(__low2half(top)) || __hisinf(__high2half(top)))) bad = true;
+  if (lane < rows) {
+    p.y_scale[((size_t)row0 + 32 * q4 + lane) * (p.N / NC) + col / NC] = __uint_as_float((uint32_t)(127 - sh) << 23);
+    if (top >= 65520.f * 16.f) bad = true;  // rounds past the largest fp16 (or is infinite)
+  }
 }
 
 template <int MODE, int BN, bool F32>

@@ -9,11 +9,11 @@ namespace mx4 {
 
 // kDense: y = a w^T.  kGateUp: rows of a grouped by expert, 128 gate and the
 // 128 up rows of the same intermediates, h = silu(gate) * up quantized to
-// MXFP4.  kDown: the grouped h times the expert's down rows, fp16 of the
-// outputs scaled by 1/16, one row per row of a.
+// MXFP4.  kDown: the grouped h times the expert's down rows, one row per row
+// of a, in fp16 with a power of two per row and kOutCols columns.
 enum { kDense = 0, kGateUp = 1, kDown = 2 };
 
-constexpr float kOutScale = 1.0f / 16.0f;  // of the grouped outputs held in fp16
+constexpr int kOutCols = 128;  // columns of the grouped outputs that share a power of two
 // Rows of w per tile of kDown (H = 2048, I = 512: 183.9 us a layer at 4096
 // tokens and 109.7 at 300; 192, which leave room for two accumulators: 186.7
 // and 110.0; 128: 190.6 and 113.3).
@@ -31,6 +31,7 @@ struct GemmParams {
   int tiles;             // row tiles of a (dense)
   int nsub;              // column tiles
   void* y;               // dense and down
+  float* y_scale;        // down: [rows, N / kOutCols], what the fp16 in y are to be multiplied with
   size_t ldy;            // dense
   int align;             // dense, of the rows of y: 32 or 16 bytes, 0: less
   // grouped: tile tau < shared_tiles holds tokens 128 tau .. of the shared
@@ -48,7 +49,7 @@ struct GemmParams {
 bool mx4_valid(const qsm_mx4* w);
 // The maps of a (rows x K codes).
 bool make_a_maps(GemmParams* p, const void* codes, uint64_t rows, int K);
-// gate_up, or down with p.y of `rows` rows of p.N fp16.
+// gate_up, or down with p.y of `rows` rows of p.N fp16 and p.y_scale.
 qsm_status launch_grouped(GemmParams& p, int mode, uint64_t rows, cudaStream_t stream);
 
 }  // namespace mx4

@@ -10,8 +10,10 @@
 // QSM_ACTS_MX4 (many tokens): the token rows are quantized once and written
 // to their places in the grouped order, each expert's rows padded to blocks
 // of 128 (so that every block starts a scale tile); one grouped product
-// forms h, quantized in its epilogue, and a second one o, in fp16 scaled by
-// 1/16 (11 bits against the 8 of the bf16 result).
+// forms h, quantized in its epilogue, and a second one o, in fp16 with a power of
+// two per row and 128 columns (11 bits against the 8 of the bf16 result, at every
+// magnitude; with a fixed 1/16 outputs lost bits below 2^-10 and were 0 below
+// 2^-21).
 //
 // Every assignment's output is written once and the combine adds them in a
 // fixed order, instead of reductions into y: the result does not depend on
@@ -28,7 +30,6 @@ extern int g_barrier_skew;  // qsm_debug_barrier_skew
 namespace mx4 {
 namespace {
 
-constexpr float kOutScaleInv = 16.0f;
 constexpr int kPrepThreads = 256;
 constexpr int kCombThreads = 128;
 constexpr int kCombCols = 8;
@@ -152,7 +153,8 @@ mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
 }
 
 // y[t] from the shared expert's output row and those of the token's
-// assignments.  HALF: o holds fp16 of 1/16, rows at[t k + j] and t; else fp32,
+// assignments.  HALF: o holds fp16 to be multiplied with oscale [row, H / kOutCols],
+// rows at[t k + j] and t; else fp32,
 // rows t k + j (where at, the chosen expert, is valid) and T k + t.  A thread
 // takes 8 columns of one token, with the loads of eight assignments in flight.
 // Bound by reading o: 4096 tokens of 2048 with 8 experts each 35.5 us (168 MB in,
@@ -160,7 +162,7 @@ mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
 // 212 us, column passes that keep o in L2 from 197.6 to 199.5.
 template <bool HALF>
 __global__ void __launch_bounds__(kCombThreads, HALF ? kCombCtas : 4)
-mx4_combine_kernel(const void* __restrict__ o, const int32_t* __restrict__ at,
+mx4_combine_kernel(const void* __restrict__ o, const float* __restrict__ oscale, const int32_t* __restrict__ at,
                    const float* __restrict__ topk_w, const uint16_t* __restrict__ x,
                    const float* __restrict__ sgate, int T, int k, int H, int E,
                    uint16_t* __restrict__ y, float* __restrict__ y32) {
@@ -195,16 +197,19 @@ mx4_combine_kernel(const void* __restrict__ o, const int32_t* __restrict__ at,
   constexpr int NV = HALF ? 1 : 2;  // 16-byte loads per row
   struct Row {
     uint4 v[NV];
+    float s;
   };
   auto load = [&](size_t row) {
     Row r;
+    r.s = HALF ? __ldcg(oscale + row * (H / kOutCols) + c / kOutCols) : 1.f;
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(o) + (row * H + c) * (HALF ? 2 : 4));
 #pragma unroll
     for (int i = 0; i < NV; ++i) r.v[i] = __ldcg(src + i);
     return r;
   };
   auto add = [&](float (&s)[kCombCols], const Row& r, float w) {
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(&r);
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(r.v);
+    if (HALF) w *= r.s;  // exact
 #pragma unroll
     for (int i = 0; i < kCombCols; ++i) {
       float v;
@@ -233,7 +238,6 @@ mx4_combine_kernel(const void* __restrict__ o, const int32_t* __restrict__ at,
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (HALF) s[2 * i] *= kOutScaleInv, s[2 * i + 1] *= kOutScaleInv;
     const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * i], s[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
@@ -257,7 +261,7 @@ struct Plan {
   int dec_smem, dec_ctas;
   size_t rows;              // rows of h and o (BF16: T k + T; MX4: padded)
   size_t route, route_end, counts, offsets, perm, inv_perm, tile_map, n_tiles;
-  size_t xc, xs, hc, hs, h, o, pos, total;
+  size_t xc, xs, hc, hs, h, o, oscale, pos, total;
 };
 
 bool shape_ok(const qsm_mx4_layer* L) {
@@ -332,6 +336,7 @@ bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
     p.hc = take(p.rows * I / 2);
     p.hs = take(mx4_scale_bytes((int)p.rows, I));
     p.o = take(p.rows * H * 2);
+    p.oscale = take(p.rows * (H / kOutCols) * 4);
     p.pos = take(A * 4);
   }
   p.total = off;
@@ -466,6 +471,7 @@ qsm_status many_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x
   d.K = I;
   d.nsub = (H + kDownRows - 1) / kDownRows;
   d.y = ws + pl.o;
+  d.y_scale = reinterpret_cast<float*>(ws + pl.oscale);
   const qsm_status st = launch_grouped(p, kGateUp, pl.rows, stream);
   return st != QSM_OK ? st : launch_grouped(d, kDown, pl.rows, stream);
 }
@@ -520,7 +526,7 @@ extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x,
   const dim3 grid((unsigned)T * ((L->H / kCombCols + kCombThreads - 1) / kCombThreads));
   auto* comb = half ? mx4_combine_kernel<true> : mx4_combine_kernel<false>;
   QSM_CUDA_TRY(launch_pdl(comb, grid, dim3(kCombThreads), 0, stream, (const void*)(ws + p.o),
-                          half ? (const int32_t*)i32(p.pos) : (const int32_t*)topk_idx, (const float*)topk_w,
+                          (const float*)(ws + p.oscale), half ? (const int32_t*)i32(p.pos) : (const int32_t*)topk_idx, (const float*)topk_w,
                           x, L->shared_gate, T, (int)L->k, (int)L->H, (int)L->E, y, y_f32));
   return QSM_OK;
 }
