@@ -493,7 +493,8 @@ QSM_API size_t moe_mx4_workspace_bytes(const qsm_mx4_layer* L, int32_t T, int32_
  * The sums over j run in ascending j, the shared expert first: y does not
  * depend on timing.
  *   x [T, H] bf16;  flags, w_router, logit_bias, topk_idx, topk_w, y, y_f32
- *   as for moe_layer_forward;
+ *   as for moe_layer_forward; y may be x itself; with a shared_gate y may not
+ *   overlap x otherwise, and y_f32 not at all (QSM_ERR_INVALID_ARGUMENT);
  *   workspace  >= moe_mx4_workspace_bytes(L, T, acts) bytes, zeros before
  *              its first use, and every call leaves it fit for the next of
  *              the same layer shape, T and acts.

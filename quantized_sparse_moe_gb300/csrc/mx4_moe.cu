@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kPrepThreads = 256;
 constexpr int kCombThreads = 128;
+constexpr int kGatedThreads = 512;  // at most, with a shared gate
 constexpr int kCombCols = 8;
 constexpr int kCombCtas = 8;  // per SM: 64 registers; ten spilled and were slower
 constexpr int kMaxK = 32;
@@ -158,19 +159,25 @@ mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
 // rows t k + j (where at, the chosen expert, is valid) and T k + t.  A thread
 // takes 8 columns of one token, with the loads of eight assignments in flight.
 // Bound by reading o: 4096 tokens of 2048 with 8 experts each 35.5 us (168 MB in,
-// 17 out, 5.2 TB/s).  A warp to 256 columns of a token took the layer from 197 to
-// 212 us, column passes that keep o in L2 from 197.6 to 199.5.
-template <bool HALF>
-__global__ void __launch_bounds__(kCombThreads, HALF ? kCombCtas : 4)
+// 17 out, 5.2 TB/s), and 4 more for the powers of two.  A warp to 256 columns of a
+// token took the layer from 197 to 212 us, column passes that keep o in L2 from
+// 197.6 to 199.5, the powers by way of shared memory from 191.5 to 198.7 (spills).
+//
+// GATED: one CTA has a whole token, because y may be x: it has read all of x[t]
+// for the gate when it writes y[t], and no other CTA reads x[t].  (The 128
+// threads that add up x . shared_gate are those of an ungated CTA.)
+template <bool HALF, bool GATED>
+__global__ void __launch_bounds__(GATED ? kGatedThreads : kCombThreads,
+                                  GATED ? (HALF ? 2 : 1) : (HALF ? kCombCtas : 4))
 mx4_combine_kernel(const void* __restrict__ o, const float* __restrict__ oscale, const int32_t* __restrict__ at,
-                   const float* __restrict__ topk_w, const uint16_t* __restrict__ x,
+                   const float* __restrict__ topk_w, const uint16_t* x,
                    const float* __restrict__ sgate, int T, int k, int H, int E,
-                   uint16_t* __restrict__ y, float* __restrict__ y32) {
+                   uint16_t* y, float* y32) {
   __shared__ int rows[kMaxK];
   __shared__ float wts[kMaxK], red[kCombThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
-  const int per = (H / kCombCols + kCombThreads - 1) / kCombThreads;  // CTAs per token
+  const int per = GATED ? 1 : (H / kCombCols + kCombThreads - 1) / kCombThreads;  // CTAs per token
   const int t = blockIdx.x / per, tid = threadIdx.x;
   if (tid < k) {
     const int r = __ldcg(at + (size_t)t * k + tid);
@@ -178,73 +185,79 @@ mx4_combine_kernel(const void* __restrict__ o, const float* __restrict__ oscale,
     wts[tid] = __ldcg(topk_w + (size_t)t * k + tid);
   }
   float g = 1.f;
-  if (sgate) {
+  if (GATED && tid < kCombThreads) {
     float z = 0.f;
     for (int c = tid; c < H; c += kCombThreads)
-      z = fmaf(__uint_as_float((uint32_t)__ldg(x + (size_t)t * H + c) << 16), __ldg(sgate + c), z);
+      z = fmaf(__uint_as_float((uint32_t)x[(size_t)t * H + c] << 16), __ldg(sgate + c), z);
     z = warp_sum(z);
     if ((tid & 31) == 0) red[tid >> 5] = z;
   }
   __syncthreads();
-  if (sgate) {
+  if (GATED) {
     float z = 0.f;
 #pragma unroll
     for (int w = 0; w < kCombThreads / 32; ++w) z += red[w];
     g = 1.0f / (1.0f + __expf(-z));
   }
-  const int c = (blockIdx.x % per * kCombThreads + tid) * kCombCols;
-  if (c >= H) return;
   constexpr int NV = HALF ? 1 : 2;  // 16-byte loads per row
   struct Row {
     uint4 v[NV];
     float s;
   };
-  auto load = [&](size_t row) {
-    Row r;
-    r.s = HALF ? __ldcg(oscale + row * (H / kOutCols) + c / kOutCols) : 1.f;
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(o) + (row * H + c) * (HALF ? 2 : 4));
+  auto columns = [&](const int c) {  // columns c .. c + 7 of y[t]
+    auto load = [&](size_t row) {
+      Row r;
+      r.s = HALF ? __ldcg(oscale + row * (H / kOutCols) + c / kOutCols) : 1.f;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(o) + (row * H + c) * (HALF ? 2 : 4));
 #pragma unroll
-    for (int i = 0; i < NV; ++i) r.v[i] = __ldcg(src + i);
-    return r;
-  };
-  auto add = [&](float (&s)[kCombCols], const Row& r, float w) {
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(r.v);
-    if (HALF) w *= r.s;  // exact
+      for (int i = 0; i < NV; ++i) r.v[i] = __ldcg(src + i);
+      return r;
+    };
+    auto add = [&](float (&s)[kCombCols], const Row& r, float w) {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(r.v);
+      if (HALF) w *= r.s;  // exact
 #pragma unroll
-    for (int i = 0; i < kCombCols; ++i) {
-      float v;
-      if (HALF) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(q + i / 2));
-        v = i & 1 ? f.y : f.x;
-      } else {
-        v = __uint_as_float(q[i]);
+      for (int i = 0; i < kCombCols; ++i) {
+        float v;
+        if (HALF) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(q + i / 2));
+          v = i & 1 ? f.y : f.x;
+        } else {
+          v = __uint_as_float(q[i]);
+        }
+        s[i] = fmaf(w, v, s[i]);
       }
-      s[i] = fmaf(w, v, s[i]);
+    };
+    float s[kCombCols] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const Row first = load(HALF ? (size_t)t : (size_t)T * k + t);
+    for (int j0 = 0; j0 < k; j0 += 8) {  // eight rows' loads in flight
+      Row v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < k && rows[j0 + j] >= 0) v[j] = load((size_t)rows[j0 + j]);
+      if (j0 == 0) add(s, first, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < k && rows[j0 + j] >= 0) add(s, v[j], wts[j0 + j]);
+    }
+    const size_t off = (size_t)t * H + c;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * i], s[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(y + off) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (y32) {
+      *reinterpret_cast<float4*>(y32 + off) = make_float4(s[0], s[1], s[2], s[3]);
+      *reinterpret_cast<float4*>(y32 + off + 4) = make_float4(s[4], s[5], s[6], s[7]);
     }
   };
-  float s[kCombCols] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const Row first = load(HALF ? (size_t)t : (size_t)T * k + t);
-  for (int j0 = 0; j0 < k; j0 += 8) {  // eight rows' loads in flight
-    Row v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j0 + j < k && rows[j0 + j] >= 0) v[j] = load((size_t)rows[j0 + j]);
-    if (j0 == 0) add(s, first, g);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j0 + j < k && rows[j0 + j] >= 0) add(s, v[j], wts[j0 + j]);
-  }
-  const size_t off = (size_t)t * H + c;
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * i], s[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  *reinterpret_cast<uint4*>(y + off) = make_uint4(w[0], w[1], w[2], w[3]);
-  if (y32) {
-    *reinterpret_cast<float4*>(y32 + off) = make_float4(s[0], s[1], s[2], s[3]);
-    *reinterpret_cast<float4*>(y32 + off + 4) = make_float4(s[4], s[5], s[6], s[7]);
+  if (GATED) {
+    for (int c = tid * kCombCols; c < H; c += blockDim.x * kCombCols) columns(c);
+  } else {
+    const int c = (blockIdx.x % per * kCombThreads + tid) * kCombCols;
+    if (c < H) columns(c);
   }
 }
 
@@ -346,6 +359,11 @@ bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
 
 bool weights_ok(const qsm_mx4& w, int experts, int rows, int cols) {
   return mx4_valid(&w) && w.experts == experts && w.rows == rows && w.cols == cols;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + nb && q < p + na;
 }
 
 qsm_status few_tokens(const qsm_mx4_layer* L, const Plan& pl, const uint16_t* x, int T,
@@ -505,6 +523,10 @@ extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x,
   if (!weights_ok(L->gate_up, L->E, 2 * L->I, L->H) || !weights_ok(L->down, L->E, L->H, L->I) ||
       !weights_ok(L->shared_gate_up, 1, 2 * L->I, L->H) || !weights_ok(L->shared_down, 1, L->H, L->I))
     return QSM_ERR_INVALID_ARGUMENT;
+  // y may be x, but x is read until y is written
+  const size_t n = (size_t)T * L->H;
+  if (L->shared_gate && ((y != x && overlap(y, n * 2, x, n * 2)) || (y_f32 && overlap(y_f32, n * 4, x, n * 2))))
+    return QSM_ERR_INVALID_ARGUMENT;
   Plan p;
   if (!plan_of(L, T, acts, &p)) return QSM_ERR_UNSUPPORTED;
   if (workspace_bytes < p.total) return QSM_ERR_WORKSPACE_TOO_SMALL;
@@ -523,10 +545,17 @@ extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x,
   st = half ? many_tokens(L, p, x, T, topk_idx, g, ws, dev_status, stream)
             : few_tokens(L, p, x, T, topk_idx, ws, dev_status, stream);
   if (st != QSM_OK) return st;
-  const dim3 grid((unsigned)T * ((L->H / kCombCols + kCombThreads - 1) / kCombThreads));
-  auto* comb = half ? mx4_combine_kernel<true> : mx4_combine_kernel<false>;
-  QSM_CUDA_TRY(launch_pdl(comb, grid, dim3(kCombThreads), 0, stream, (const void*)(ws + p.o),
-                          (const float*)(ws + p.oscale), half ? (const int32_t*)i32(p.pos) : (const int32_t*)topk_idx, (const float*)topk_w,
-                          x, L->shared_gate, T, (int)L->k, (int)L->H, (int)L->E, y, y_f32));
+  const bool gated = L->shared_gate != nullptr;
+  int threads = kCombThreads;
+  if (gated) {
+    const int all = (L->H / kCombCols + 31) / 32 * 32;
+    threads = all < kCombThreads ? kCombThreads : all < kGatedThreads ? all : kGatedThreads;
+  }
+  const dim3 grid((unsigned)T * (gated ? 1 : (L->H / kCombCols + kCombThreads - 1) / kCombThreads));
+  auto* comb = half ? (gated ? mx4_combine_kernel<true, true> : mx4_combine_kernel<true, false>)
+                    : (gated ? mx4_combine_kernel<false, true> : mx4_combine_kernel<false, false>);
+  QSM_CUDA_TRY(launch_pdl(comb, grid, dim3(threads), 0, stream, (const void*)(ws + p.o),
+                          (const float*)(ws + p.oscale), half ? (const int32_t*)i32(p.pos) : (const int32_t*)topk_idx,
+                          (const float*)topk_w, x, L->shared_gate, T, (int)L->k, (int)L->H, (int)L->E, y, y_f32));
   return QSM_OK;
 }

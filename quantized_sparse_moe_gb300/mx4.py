@@ -330,7 +330,7 @@ class Mx4Forward:
 
     def __call__(self, x: torch.Tensor, stream=None, out=None) -> torch.Tensor:
         """Run the layer on x [T, H] bf16; the result goes to out (a [T, H] bf16
-        tensor, contiguous) when given, else to self.y.  Returns it."""
+        tensor, contiguous; x itself is fine) when given, else to self.y.  Returns it."""
         y = self.y if out is None else out
         for t in (x,) if out is None else (x, out):
             if (t.dtype is not torch.bfloat16 or t.shape != self._shape or not t.is_contiguous()

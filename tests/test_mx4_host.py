@@ -134,3 +134,27 @@ def test_binding_refuses_bad_tensors():
         qsm.mx4_quantize(torch.zeros(4, 64))                                     # not on a GPU
     with pytest.raises(qsm.QSMError):
         qsm.mx4_quantize(torch.zeros(4, 64, dtype=torch.float64))
+
+
+@nvcc
+def test_layer_refuses_outputs_that_overlap_its_input():
+    """With a gated shared expert x is read until y is written: y is x, or apart
+    from it (refused before anything is enqueued)."""
+    import quantized_sparse_moe_gb300 as qsm
+    from quantized_sparse_moe_gb300 import mx4
+    H, I, E, p = 256, 128, 8, 1 << 20
+    L = mx4.Mx4LayerC(H, I, E, 2, mx4.Mx4C(E, 2 * I, H, p, p), mx4.Mx4C(E, H, I, p, p),
+                      mx4.Mx4C(1, 2 * I, H, p, p), mx4.Mx4C(1, H, I, p, p), p)
+
+    def fwd(y, y32=None, acts=0, ws=0):   # no workspace: what is not refused before stops there
+        return qsm.lib().moe_mx4_forward(ctypes.byref(L), p, 4, acts, p, None, 1, p, p, y, y32, p, ws, p, None)
+    for acts in (0, 1):
+        for off in (16, 4 * H * 2 - 16, -16, 16 - 4 * H * 2):
+            assert fwd(p + off, acts=acts) == 1
+        for off in (0, 4 * H * 2, -4 * H * 2):
+            assert fwd(p + off, acts=acts) == 3
+        assert fwd(p, p + 16, acts=acts) == 1 and fwd(p, p, acts=acts) == 1
+        assert fwd(p, p + 4 * H * 2, acts=acts) == 3 and fwd(p, p - 4 * H * 4, acts=acts) == 3
+        L.shared_gate = None
+        assert fwd(p + 16, acts=acts) == 3
+        L.shared_gate = p
