@@ -67,6 +67,7 @@ except ImportError:  # a torch without it
     _strided = None
 _lib = None
 _stream_of = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _words: dict = {}
 
 
@@ -86,11 +87,23 @@ def _word(device: int) -> int:
     return w[0]
 
 
-def _empty(rows: int, cols: int, dtype, device: int) -> torch.Tensor:
-    """A [rows, cols] tensor (the short way takes the current device)."""
-    if _strided is not None and torch._C._cuda_getDevice() == device:
+def _empty(rows: int, cols: int, dtype) -> torch.Tensor:
+    """A [rows, cols] tensor on the current device."""
+    if _strided is not None:
         return _strided((rows, cols), (cols or 1, 1), dtype)
-    return torch.empty((rows, cols), dtype=dtype, device=f"cuda:{device}")
+    return torch.empty((rows, cols), dtype=dtype, device="cuda")
+
+
+def _handle(dev: int, stream, what: str) -> int:
+    """The stream to launch on: the given one, or the current one.  The library
+    launches on the current device, so operands and stream have to be there."""
+    if dev != _current_device():
+        raise QSMError(f"{what}: the operands' device (cuda:{dev}) has to be the current one")
+    if stream is None:
+        return _stream_of(dev)
+    if stream.device_index != dev:
+        raise QSMError(f"{what}: the stream is not on the operands' device (cuda:{dev})")
+    return stream.cuda_stream
 
 
 def _status(t, dev: int, what: str) -> int:
@@ -178,14 +191,14 @@ def mx4_quantize(x: torch.Tensor, out: Mx4Tensor | None = None, dev_status=None,
     if dtype is None:
         raise QSMError("mx4_quantize: x must be bf16, fp16 or fp32")
     dev, rows, cols, ld = _matrix(x, "mx4_quantize")
+    on = _handle(dev, stream, "mx4_quantize")
     if out is None:
         out = Mx4Tensor.empty(rows, cols, device=x.device)
     elif out.rows != rows or out.cols != cols or out.experts != 1 or out.device != dev:
         raise QSMError("mx4_quantize: out has another shape or device")
     rc = (_lib or _load()).mx4_quantize(
         x.data_ptr(), dtype, ld, rows, cols, out.c.codes, out.c.scales,
-        _status(dev_status, dev, "mx4_quantize"),
-        _stream_of(dev) if stream is None else stream.cuda_stream)
+        _status(dev_status, dev, "mx4_quantize"), on)
     if rc:
         _check(rc, "mx4_quantize")
     return out
@@ -196,13 +209,13 @@ def mx4_dequantize(a: Mx4Tensor, dtype=torch.bfloat16, y=None, stream=None) -> t
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise QSMError("mx4_dequantize: dtype must be bf16, fp16 or fp32")
+    on = _handle(a.device, stream, "mx4_dequantize")
     if y is None:
-        y = _empty(a.experts * a.rows, a.cols, dtype, a.device)
+        y = _empty(a.experts * a.rows, a.cols, dtype)
     elif (y.dtype != dtype or not y.is_contiguous() or y.numel() != a.experts * a.rows * a.cols
           or y.get_device() != a.device):
         raise QSMError("mx4_dequantize: y must be contiguous, of a's size and device, and dtype")
-    rc = (_lib or _load()).mx4_dequantize(
-        a.ref, dt, y.data_ptr(), _stream_of(a.device) if stream is None else stream.cuda_stream)
+    rc = (_lib or _load()).mx4_dequantize(a.ref, dt, y.data_ptr(), on)
     if rc:
         _check(rc, "mx4_dequantize")
     return y
@@ -216,8 +229,9 @@ def mx4_gemm(a: Mx4Tensor, w: Mx4Tensor, dtype=torch.bfloat16, y=None, dev_statu
         raise QSMError("mx4_gemm: dtype must be bf16 or fp32")
     if w.device != dev:
         raise QSMError("mx4_gemm: a and w are on different devices")
+    on = _handle(dev, stream, "mx4_gemm")
     if y is None:
-        y = _empty(M, N, dtype, dev)
+        y = _empty(M, N, dtype)
         ld = N
     else:
         ydev, rows, cols, ld = _matrix(y, "mx4_gemm: y")
@@ -225,8 +239,7 @@ def mx4_gemm(a: Mx4Tensor, w: Mx4Tensor, dtype=torch.bfloat16, y=None, dev_statu
             raise QSMError("mx4_gemm: y must be [M, N] of dtype on the operands' device")
     rc = (_lib or _load()).mx4_gemm(
         a.ref, w.ref, _DTYPES[dtype], y.data_ptr(), ld,
-        _status(dev_status, dev, "mx4_gemm"),
-        _stream_of(dev) if stream is None else stream.cuda_stream)
+        _status(dev_status, dev, "mx4_gemm"), on)
     if rc:
         _check(rc, "mx4_gemm")
     return y
@@ -239,15 +252,15 @@ def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, y=None, dev_status=None, stream=None
     dev, T, K, ld = _matrix(x, "mx4_gemv")
     if K != w.cols or w.device != dev:
         raise QSMError("mx4_gemv: x and w differ in K or device")
+    on = _handle(dev, stream, "mx4_gemv")
     if y is None:
-        y = _empty(T, w.rows, torch.bfloat16, dev)
+        y = _empty(T, w.rows, torch.bfloat16)
     elif (y.dtype != torch.bfloat16 or tuple(y.shape) != (T, w.rows) or not y.is_contiguous()
           or y.get_device() != dev):
         raise QSMError("mx4_gemv: y must be a contiguous bf16 [T, N] on x's device")
     rc = (_lib or _load()).mx4_gemv(
         x.data_ptr(), ld, T, w.ref, y.data_ptr(),
-        _status(dev_status, dev, "mx4_gemv"),
-        _stream_of(dev) if stream is None else stream.cuda_stream)
+        _status(dev_status, dev, "mx4_gemv"), on)
     if rc:
         _check(rc, "mx4_gemv")
     return y
@@ -288,7 +301,9 @@ class Mx4Layer:
 
 
 def moe_mx4_workspace_bytes(layer: Mx4Layer, T: int, acts: str = "bf16") -> int:
-    """0 when the layer, T or acts is not supported."""
+    """0 when the layer, T or acts is not supported (on the current device, which
+    has to be the weights')."""
+    _handle(layer.device, None, "moe_mx4_workspace_bytes")
     return int(lib().moe_mx4_workspace_bytes(ctypes.byref(layer.c), T, _ACTS.get(acts, -1)))
 
 
@@ -337,8 +352,8 @@ class Mx4Forward:
                     or t.get_device() != self._device):
                 raise QSMError("Mx4Forward: x and out must be contiguous [T, H] bf16 tensors on "
                                "the layer's device")
-        rc = self._fn(self._layer_ref, x.data_ptr(), *self._mid, y.data_ptr(), *self._tail,
-                      _stream_of(self._device) if stream is None else stream.cuda_stream)
+        on = _handle(self._device, stream, "Mx4Forward")
+        rc = self._fn(self._layer_ref, x.data_ptr(), *self._mid, y.data_ptr(), *self._tail, on)
         if rc:
             _check(rc, "moe_mx4_forward")
         return y
