@@ -490,19 +490,28 @@ QSM_API size_t moe_mx4_workspace_bytes(const qsm_mx4_layer* L, int32_t T, int32_
  * the same for the shared expert, and
  *     y[t] = sum_j topk_w[t, j] * o(t, j) + g[t] * o_shared(t),
  * g[t] = sigmoid(x[t] . shared_gate), or 1 when shared_gate is NULL.
- * The sums over j run in ascending j, the shared expert first: y does not
- * depend on timing.
+ * The sums over j run in ascending j, the shared expert first (but see the
+ * one-launch form below): y does not depend on timing, and with QSM_ACTS_BF16
+ * a token's y not on the other tokens of the call.
  *   x [T, H] bf16;  flags, w_router, logit_bias, topk_idx, topk_w, y, y_f32
  *   as for moe_layer_forward; y may be x itself; with a shared_gate y may not
  *   overlap x otherwise, and y_f32 not at all (QSM_ERR_INVALID_ARGUMENT);
  *   workspace  >= moe_mx4_workspace_bytes(L, T, acts) bytes, zeros before
  *              its first use, and every call leaves it fit for the next of
  *              the same layer shape, T and acts.
- * One or two tokens with QSM_ACTS_BF16 (and E <= 256, 768 < H, I <= 4096)
- * run in one launch whose CTAs exchange words: all of them have to be resident
- * at once, so a call that shares the GPU with work that holds SMs for a second
- * sets QSM_DEV_TIMEOUT; its results are then invalid and the workspace has to
- * be zeroed before the next call.
+ * One or two tokens with QSM_ACTS_BF16 run in one launch whose CTAs exchange
+ * words, if E <= 256, H > 768, I <= 4096, the device holds H / 128 clusters of four
+ * such CTAs at once (a GB300: H <= 4864), and their shared memory holds three
+ * stages of weights beside the router rows of a CTA's experts and the digits of x
+ * (or of two slots' h): T, k and the shape alone decide.
+ *  - All CTAs have to be resident at once, so a call that shares the GPU with
+ *    work that holds SMs for a second sets QSM_DEV_TIMEOUT; its results are then
+ *    invalid and the workspace has to be zeroed before the next call.
+ *  - Its order of sums: the call's distinct experts in ascending id, the shared
+ *    expert before them, are dealt to four CTAs in turn; each accumulates the
+ *    products of weight x h of all its experts in fp32, and the four sums are
+ *    added.  y does not depend on timing, but with two tokens the last fp32 bits
+ *    of one's y may depend on the experts that the other chose.
  * With QSM_ACTS_MX4 the outputs of the experts are held in fp16 until they are
  * summed, with a power of two of their own for every 128 columns of a row: to
  * 2^-11 of the value, and 2^-39 of the largest magnitude of the 128.  Magnitudes

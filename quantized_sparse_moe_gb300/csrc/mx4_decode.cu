@@ -39,7 +39,10 @@
 // 24.4, T = 3: 28.5 against 25.2 (now 23.8), T = 8: 83.8 against 42.3 (38.7)): they take the other
 // form.
 //
-// Sums run in a fixed order: y depends on nothing but the inputs.  Every wait
+// Sums run in a fixed order (by slot within a CTA, then the four CTAs): y depends
+// on nothing but the inputs.  With two tokens U holds the experts of both, so
+// which slots share an accumulator, and with it the last fp32 bits of one
+// token's y, depends on the other token's choices.  Every wait
 // is bounded (QSM_DEV_TIMEOUT; the results are then invalid and the workspace
 // must be zeroed).  The tag is 1 + the calls so far, from a ticket that every
 // CTA adds 1 to; every word that a call reads it has written before.

@@ -17,7 +17,8 @@
 //
 // Every assignment's output is written once and the combine adds them in a
 // fixed order, instead of reductions into y: the result does not depend on
-// timing, and nothing has to be zeroed.
+// timing, and nothing has to be zeroed.  (The one launch has no combine: its
+// order of sums is fixed too, but another one, see mx4_decode.cu.)
 #include "mx4_decode.cuh"
 #include "mx4_gemm.cuh"
 #include "mx4_stream.cuh"
