@@ -478,10 +478,14 @@ typedef struct {
  *   QSM_ACTS_MX4   x and h quantized to MXFP4 by the rule of mx4_quantize (any
  *                  number of tokens: grouped 4-bit products) */
 typedef enum { QSM_ACTS_BF16 = 0, QSM_ACTS_MX4 = 1 } qsm_acts;
+/* Added to QSM_ACTS_BF16: never the one-launch form, whose CTAs wait for one
+ * another (see moe_mx4_forward), for callers whose GPU runs other work beside
+ * the call. */
+#define QSM_ACTS_SEPARATE_LAUNCHES 16
 #define QSM_MX4_MOE_MAX_ROWS 64
 
-/* Bytes of workspace moe_mx4_forward needs; 0 if the layer, T or acts is not
- * supported. */
+/* Bytes of workspace moe_mx4_forward needs (for the same acts, its flag included);
+ * 0 if the layer, T or acts is not supported. */
 QSM_API size_t moe_mx4_workspace_bytes(const qsm_mx4_layer* L, int32_t T, int32_t acts);
 
 /* The whole layer: route (as moe_route, ids and weights the same bits),
@@ -507,6 +511,7 @@ QSM_API size_t moe_mx4_workspace_bytes(const qsm_mx4_layer* L, int32_t T, int32_
  *  - All CTAs have to be resident at once, so a call that shares the GPU with
  *    work that holds SMs for a second sets QSM_DEV_TIMEOUT; its results are then
  *    invalid and the workspace has to be zeroed before the next call.
+ *    QSM_ACTS_SEPARATE_LAUNCHES keeps a call out of this form.
  *  - Its order of sums: the call's distinct experts in ascending id, the shared
  *    expert before them, are dealt to four CTAs in turn; each accumulates the
  *    products of weight x h of all its experts in fp32, and the four sums are

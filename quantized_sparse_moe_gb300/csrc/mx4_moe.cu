@@ -283,13 +283,22 @@ bool shape_ok(const qsm_mx4_layer* L) {
          L->I <= 16384 && L->E >= 1 && L->E <= 1024 && L->k >= 1 && L->k <= L->E && L->k <= kMaxK;
 }
 
-bool plan_of(const qsm_mx4_layer* L, int T, int acts, Plan* out) {
-  if (!shape_ok(L) || T < 1 || (acts != QSM_ACTS_BF16 && acts != QSM_ACTS_MX4)) return false;
+// Splits the acts argument: false when it is none of the values.
+bool acts_of(int arg, int* acts, bool* one_launch) {
+  *one_launch = (arg & QSM_ACTS_SEPARATE_LAUNCHES) == 0;
+  *acts = arg & ~QSM_ACTS_SEPARATE_LAUNCHES;
+  return *acts == QSM_ACTS_BF16 || (*acts == QSM_ACTS_MX4 && *one_launch);
+}
+
+bool plan_of(const qsm_mx4_layer* L, int T, int acts_arg, Plan* out) {
+  int acts;
+  bool one_launch;
+  if (!shape_ok(L) || T < 1 || !acts_of(acts_arg, &acts, &one_launch)) return false;
   if ((long long)T * L->k > (1 << 24)) return false;
   const int H = L->H, I = L->I, E = L->E, k = L->k;
   Plan p = {};
   p.acts = acts;
-  if (acts == QSM_ACTS_BF16 && plan_decode(L, T, &p.dec, &p.dec_smem, &p.dec_ctas)) {
+  if (acts == QSM_ACTS_BF16 && one_launch && plan_decode(L, T, &p.dec, &p.dec_smem, &p.dec_ctas)) {
     p.one = true;
     p.total = decode_workspace_bytes(p.dec);
     *out = p;
@@ -511,7 +520,9 @@ extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x,
                                       int32_t* dev_status, cudaStream_t stream) {
   using namespace qsm;
   using namespace qsm::mx4;
-  if (!L || T < 0 || (acts != QSM_ACTS_BF16 && acts != QSM_ACTS_MX4) ||
+  int kind;
+  bool one;
+  if (!L || T < 0 || !acts_of(acts, &kind, &one) ||
       (flags & ~(QSM_ROUTE_RENORMALIZE | QSM_ROUTE_BIAS_SELECT_ONLY)))
     return QSM_ERR_INVALID_ARGUMENT;
   if (!shape_ok(L)) return QSM_ERR_UNSUPPORTED;
@@ -538,7 +549,7 @@ extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x,
   const qsm_grouping g = {i32(p.counts),   i32(p.offsets), i32(p.perm), i32(p.inv_perm),
                           i32(p.tile_map), i32(p.n_tiles), p.tile_rows, p.max_tiles};
   const size_t route_bytes = p.route_end - p.route;
-  const bool half = acts == QSM_ACTS_MX4;
+  const bool half = kind == QSM_ACTS_MX4;
   qsm_status st = moe_route(x, w_router, logit_bias, T, L->H, L->E, L->k, flags, topk_idx, topk_w,
                             ws + p.route, route_bytes, dev_status, stream);
   if (st == QSM_OK && half) st = moe_group_tokens(topk_idx, T, L->k, L->E, &g, dev_status, stream);

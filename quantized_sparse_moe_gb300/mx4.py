@@ -23,6 +23,11 @@ MOE_MAX_ROWS = 64     # of acts="bf16"
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _ACTS = {"bf16": 0, "mx4": 1}
+_SEPARATE = 16        # with "bf16": never the one-launch form
+
+
+def _acts(acts: str, one_launch: bool) -> int:
+    return _ACTS.get(acts, -1) if one_launch or acts != "bf16" else _SEPARATE
 
 
 class Mx4C(ctypes.Structure):
@@ -300,24 +305,26 @@ class Mx4Layer:
                    w_router, logit_bias, shared_gate)
 
 
-def moe_mx4_workspace_bytes(layer: Mx4Layer, T: int, acts: str = "bf16") -> int:
+def moe_mx4_workspace_bytes(layer: Mx4Layer, T: int, acts: str = "bf16", one_launch=True) -> int:
     """0 when the layer, T or acts is not supported (on the current device, which
     has to be the weights')."""
     _handle(layer.device, None, "moe_mx4_workspace_bytes")
-    return int(lib().moe_mx4_workspace_bytes(ctypes.byref(layer.c), T, _ACTS.get(acts, -1)))
+    return int(lib().moe_mx4_workspace_bytes(ctypes.byref(layer.c), T, _acts(acts, one_launch)))
 
 
 class Mx4Forward:
     """Buffers of one call of an MXFP4 MoE layer for T tokens, and the call.
     acts="bf16" (T <= 64) multiplies the weights with x and h unrounded,
-    acts="mx4" with their MXFP4 forms.  Results: y (returned), topk_idx,
+    acts="mx4" with their MXFP4 forms.  One or two tokens with acts="bf16" run
+    in one launch whose CTAs wait for one another, unless one_launch=False (for a
+    GPU that runs other work beside the call).  Results: y (returned), topk_idx,
     topk_w, and y_f32 with want_f32."""
 
     def __init__(self, layer: Mx4Layer, T: int, acts: str = "bf16", device="cuda",
-                 renormalize=True, want_f32=False, *, bias_select_only=False):
+                 renormalize=True, want_f32=False, *, bias_select_only=False, one_launch=True):
         if acts not in _ACTS:
             raise QSMError('Mx4Forward: acts must be "bf16" or "mx4"')
-        need = moe_mx4_workspace_bytes(layer, T, acts)
+        need = moe_mx4_workspace_bytes(layer, T, acts, one_launch)
         if T < 0 or (need == 0 and T > 0):
             raise QSMError("Mx4Forward: unsupported layer or token count")
         # the router as it is now (what the calls point to)
@@ -335,7 +342,7 @@ class Mx4Forward:
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=device)
         self._fn = lib().moe_mx4_forward
         p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        self._mid = (T, _ACTS[acts], p(layer.w_router), p(layer.logit_bias),
+        self._mid = (T, _acts(acts, one_launch), p(layer.w_router), p(layer.logit_bias),
                      route_flags(renormalize, bias_select_only), p(self.topk_idx), p(self.topk_w))
         self._tail = (p(self.y_f32), p(self.workspace), self.workspace.numel(), p(self.dev_status))
         self._layer_ref = ctypes.byref(layer.c)

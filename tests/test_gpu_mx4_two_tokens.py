@@ -58,3 +58,19 @@ def test_in_separate_launches_a_token_does_not_see_the_others(qsm, t):
         x[1:] = hidden(t - 1, 512, s)
         f(x)
         assert torch.equal(f.y_f32[0], want)
+
+
+@pytest.mark.parametrize("t,h,i,e,k", [(1, 2048, 512, 256, 8), (2, 2048, 512, 256, 8), (1, 1024, 128, 64, 32)])
+def test_the_one_launch_form_can_be_left_out(qsm, t, h, i, e, k):
+    L, v = layer(qsm, h, i, e, k, seed=t + 20, gate=True)
+    x = hidden(t, h, 3)
+    one = qsm.Mx4Forward(L, t, want_f32=True)
+    n = qsm.launch_count()
+    check_layer(qsm, L, v, x, "bf16", f=one)
+    few = qsm.launch_count() - n
+    many = qsm.Mx4Forward(L, t, want_f32=True, one_launch=False)
+    n = qsm.launch_count()
+    check_layer(qsm, L, v, x, "bf16", f=many)
+    assert qsm.launch_count() - n == few + 3          # route, gate_up, down, combine
+    assert many.workspace.numel() >= qsm.moe_mx4_workspace_bytes(L, t, one_launch=False) > 0
+    assert torch.equal(one.topk_idx, many.topk_idx) and torch.equal(one.topk_w, many.topk_w)

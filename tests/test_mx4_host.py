@@ -158,3 +158,16 @@ def test_layer_refuses_outputs_that_overlap_its_input():
         L.shared_gate = None
         assert fwd(p + 16, acts=acts) == 3
         L.shared_gate = p
+
+
+@nvcc
+def test_separate_launches_are_a_value_of_acts():
+    import quantized_sparse_moe_gb300 as qsm
+    from quantized_sparse_moe_gb300 import mx4
+    H, I, E, p = 256, 128, 8, 1 << 20
+    L = mx4.Mx4LayerC(H, I, E, 2, mx4.Mx4C(E, 2 * I, H, p, p), mx4.Mx4C(E, H, I, p, p),
+                      mx4.Mx4C(1, 2 * I, H, p, p), mx4.Mx4C(1, H, I, p, p), None)
+    lib, ref = qsm.lib(), ctypes.byref(L)
+    for acts, want in ((16, 3), (17, 1), (32, 1), (-1, 1), (18, 1)):
+        assert lib.moe_mx4_forward(ref, p, 4, acts, p, None, 1, p, p, p, None, p, 0, p, None) == want
+        assert (lib.moe_mx4_workspace_bytes(ref, 4, acts) > 0) == (want == 3)
