@@ -663,6 +663,19 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_pair_kernel(const __grid
       }
       if (!ok) break;
     }
+    // after an abort, let the copies in flight land before the CTAs exit (neither
+    // does before the cluster barrier at the end): the leader waits for both
+    // CTAs' on its barriers, which the other cannot wait on; as the two may have
+    // stopped at different stages, each stays for a millisecond besides, hundreds
+    // of times what a copy takes
+    if (rank == 0)
+      for (int i = 0; i < P::kStages; ++i) {
+        const uint32_t r = i < st ? round : round - 1;  // the last round of this position
+        if (i < st || round > 0) mbar_wait_bounded(&full[i], r & 1, 1u << 16);
+      }
+    if (warp_aborted(abort_p))
+      for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
       int st = 0, j = 0;
