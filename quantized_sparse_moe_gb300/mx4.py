@@ -92,8 +92,13 @@ def _word(device: int) -> int:
     return w[0]
 
 
-def _empty(rows: int, cols: int, dtype) -> torch.Tensor:
-    """A [rows, cols] tensor on the current device."""
+def _empty(rows: int, cols: int, dtype, stream) -> torch.Tensor:
+    """A [rows, cols] tensor on the current device, from the memory of the stream
+    that will write it: what the current stream has given back may still be in
+    use there, and another stream does not wait for that."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty((rows, cols), dtype=dtype, device="cuda")
     if _strided is not None:
         return _strided((rows, cols), (cols or 1, 1), dtype)
     return torch.empty((rows, cols), dtype=dtype, device="cuda")
@@ -198,7 +203,11 @@ def mx4_quantize(x: torch.Tensor, out: Mx4Tensor | None = None, dev_status=None,
     dev, rows, cols, ld = _matrix(x, "mx4_quantize")
     on = _handle(dev, stream, "mx4_quantize")
     if out is None:
-        out = Mx4Tensor.empty(rows, cols, device=x.device)
+        if stream is None:
+            out = Mx4Tensor.empty(rows, cols, device=x.device)
+        else:  # as _empty
+            with torch.cuda.stream(stream):
+                out = Mx4Tensor.empty(rows, cols, device=x.device)
     elif out.rows != rows or out.cols != cols or out.experts != 1 or out.device != dev:
         raise QSMError("mx4_quantize: out has another shape or device")
     rc = (_lib or _load()).mx4_quantize(
@@ -216,7 +225,7 @@ def mx4_dequantize(a: Mx4Tensor, dtype=torch.bfloat16, y=None, stream=None) -> t
         raise QSMError("mx4_dequantize: dtype must be bf16, fp16 or fp32")
     on = _handle(a.device, stream, "mx4_dequantize")
     if y is None:
-        y = _empty(a.experts * a.rows, a.cols, dtype)
+        y = _empty(a.experts * a.rows, a.cols, dtype, stream)
     elif (y.dtype != dtype or not y.is_contiguous() or y.numel() != a.experts * a.rows * a.cols
           or y.get_device() != a.device):
         raise QSMError("mx4_dequantize: y must be contiguous, of a's size and device, and dtype")
@@ -236,7 +245,7 @@ def mx4_gemm(a: Mx4Tensor, w: Mx4Tensor, dtype=torch.bfloat16, y=None, dev_statu
         raise QSMError("mx4_gemm: a and w are on different devices")
     on = _handle(dev, stream, "mx4_gemm")
     if y is None:
-        y = _empty(M, N, dtype)
+        y = _empty(M, N, dtype, stream)
         ld = N
     else:
         ydev, rows, cols, ld = _matrix(y, "mx4_gemm: y")
@@ -259,7 +268,7 @@ def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, y=None, dev_status=None, stream=None
         raise QSMError("mx4_gemv: x and w differ in K or device")
     on = _handle(dev, stream, "mx4_gemv")
     if y is None:
-        y = _empty(T, w.rows, torch.bfloat16)
+        y = _empty(T, w.rows, torch.bfloat16, stream)
     elif (y.dtype != torch.bfloat16 or tuple(y.shape) != (T, w.rows) or not y.is_contiguous()
           or y.get_device() != dev):
         raise QSMError("mx4_gemv: y must be a contiguous bf16 [T, N] on x's device")
