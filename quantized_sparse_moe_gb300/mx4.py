@@ -358,6 +358,13 @@ class Mx4Forward:
         self._device, self._shape = self.y.get_device(), self.y.shape
         if self._device != layer.device:
             raise QSMError("Mx4Forward: device is not the weights'")
+        # the streams that are behind the zeroing of the buffers: this one, and
+        # those that have waited for the event
+        self._ready = {_stream_of(self._device)}
+        self._zeroed = None
+        if not torch.cuda.is_current_stream_capturing():
+            self._zeroed = torch.cuda.Event()
+            self._zeroed.record()
 
     def __call__(self, x: torch.Tensor, stream=None, out=None) -> torch.Tensor:
         """Run the layer on x [T, H] bf16; the result goes to out (a [T, H] bf16
@@ -369,7 +376,17 @@ class Mx4Forward:
                 raise QSMError("Mx4Forward: x and out must be contiguous [T, H] bf16 tensors on "
                                "the layer's device")
         on = _handle(self._device, stream, "Mx4Forward")
+        if on not in self._ready:
+            self._wait_ready(on, stream)
         rc = self._fn(self._layer_ref, x.data_ptr(), *self._mid, y.data_ptr(), *self._tail, on)
         if rc:
             _check(rc, "moe_mx4_forward")
         return y
+
+    def _wait_ready(self, on: int, stream) -> None:
+        """The first call on a stream waits for the zeroing.  A stream that is
+        being captured cannot wait for what came before the capture: there the
+        caller does it, with a call or a wait before the capture."""
+        if self._zeroed is not None and not torch.cuda.is_current_stream_capturing():
+            (torch.cuda.current_stream() if stream is None else stream).wait_event(self._zeroed)
+            self._ready.add(on)

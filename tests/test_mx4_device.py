@@ -46,7 +46,15 @@ class Library:
 
 class Stream:
     def __init__(self, dev):
-        self.cuda_stream, self.device_index = 7, dev
+        self.cuda_stream, self.device_index, self.waited = 7, dev, 0
+
+    def wait_event(self, event):
+        self.waited += 1
+
+
+class Event:
+    def record(self):
+        pass
 
 
 @pytest.fixture
@@ -57,6 +65,7 @@ def mx4(monkeypatch):
     monkeypatch.setattr(mx4, "lib", lambda: fake)
     monkeypatch.setattr(mx4, "_stream_of", lambda dev: 0)
     monkeypatch.setattr(mx4, "_current_device", lambda: HERE)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     mx4.fake = fake
     yield mx4
     del mx4.fake
@@ -112,6 +121,7 @@ def forward(mx4, monkeypatch, dev):
         m.setattr(mx4, "_current_device", lambda: dev)
         m.setattr(torch, "empty", make)
         m.setattr(torch, "zeros", make)
+        m.setattr(torch.cuda, "Event", Event)
         f = mx4.Mx4Forward(layer(mx4, dev), 4)
     mx4.fake.called.clear()
     return f
@@ -134,3 +144,19 @@ def test_a_layer_on_another_device_is_refused(mx4, monkeypatch):
             with pytest.raises(mx4.QSMError):
                 f(x, stream=stream)
             assert not mx4.fake.called
+
+
+def test_another_stream_waits_for_the_zeroed_buffers(mx4, monkeypatch):
+    """Once for each stream, and not inside a capture."""
+    f = forward(mx4, monkeypatch, HERE)
+    x, s = Fake((4, 256), torch.bfloat16, HERE), Stream(HERE)
+    capturing = [True]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    f(x, stream=s)
+    assert s.waited == 0
+    capturing[0] = False
+    f(x, stream=s)
+    f(x, stream=s)
+    assert s.waited == 1
+    f(x)                                   # the stream that the buffers were made on
+    assert mx4.fake.called == ["moe_mx4_forward"] * 4
