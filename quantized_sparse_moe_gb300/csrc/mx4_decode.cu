@@ -563,9 +563,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_layer_kernel(const __grid_con
         for (int u = ct; u - lane < total; u += 32 * kConvWarps) {
           const int q = u >> 5, seg = q / T, i = q - seg * T, c = seg * kStageK + 8 * lane;
           float wt = 0.f;
+          bool chosen = e < 0;
           if (e < 0) wt = p.sgate ? sgate_v[i] : 1.f;
           for (int z = 0; e >= 0 && z < k; ++z)
-            if (sel_e[i][z] == e) wt = sel_w[i][z];
+            if (sel_e[i][z] == e) wt = sel_w[i][z], chosen = true;
           float v[8];
 #pragma unroll
           for (int z = 0; z < 8; ++z) v[z] = 0.f;
@@ -585,8 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_layer_kernel(const __grid_con
 #pragma unroll
               for (int z = 0; z < 8; ++z)
                 if ((want & (1u << z)) && (uint32_t)(w[z] >> 32) == tag) {
-                  // a token that did not choose the expert adds nothing
-                  v[z] = wt != 0.f ? wt * __uint_as_float((uint32_t)w[z]) : 0.f;
+                  // a token that did not choose the expert adds nothing; a weight of 0
+                  // (an underflow) times an h that is not finite is not a number
+                  v[z] = chosen ? wt * __uint_as_float((uint32_t)w[z]) : 0.f;
                   want &= ~(1u << z);
                 }
               if (tries > 8) __nanosleep(32);
