@@ -160,3 +160,19 @@ def test_another_stream_waits_for_the_zeroed_buffers(mx4, monkeypatch):
     assert s.waited == 1
     f(x)                                   # the stream that the buffers were made on
     assert mx4.fake.called == ["moe_mx4_forward"] * 4
+
+
+def test_what_the_calls_point_to_cannot_be_replaced(mx4):
+    """The C structures hold addresses that were taken once: another tensor in
+    an attribute would not be seen, and the old one's memory be given back."""
+    t, L = tensor(mx4, 8, 64, HERE), layer(mx4, HERE)
+    for what, names in ((t, ("codes", "scales", "rows", "cols", "experts")),
+                        (L, ("gate_up", "down", "shared_gate_up", "shared_down", "shared_gate", "H", "k"))):
+        for name in names:
+            old = getattr(what, name)
+            with pytest.raises(AttributeError):
+                setattr(what, name, old)
+            assert getattr(what, name) is old
+    router = Fake((8, 256), torch.float32, HERE)
+    L.w_router, L.logit_bias = router, None    # taken when an Mx4Forward is made
+    assert L.w_router is router
