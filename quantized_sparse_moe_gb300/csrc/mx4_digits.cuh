@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "kept_answers.cuh"
 #include "mx4_common.cuh"
 
 namespace qsm {
@@ -99,25 +100,18 @@ __device__ __forceinline__ void store_digits(const uint32_t (&plane)[kDigits], u
 
 // Clusters of cs CTAs of `kernel` that the current device holds at once; 0 when
 // the query fails.  Allows the kernel smem_max bytes of dynamic shared memory.
-// The last kKept answers (device, kernel, sizes) are kept: the query takes
-// longer than a small product.
+// Answers are kept: a program with several projections and a varying number of
+// rows asks for hundreds of geometries in turn.
 inline int resident_clusters(void* kernel, int cs, int threads, int smem, int smem_max) {
-  constexpr int kKept = 64;
   static std::mutex mu;
-  static struct {
-    int dev;
-    void* k;
-    int cs, smem, n;
-  } kept[kKept];
-  static int next = 0;  // a kernel of null: not yet written
-  int dev = 0;
+  static KeptAnswers kept;
+  int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   std::lock_guard<std::mutex> lock(mu);
-  for (const auto& c : kept)
-    if (c.dev == dev && c.k == kernel && c.cs == cs && c.smem == smem) return c.n;
+  if (kept.find(dev, kernel, cs, smem, &n)) return n;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) != cudaSuccess)
     return 0;
-  int n = sm_count();
+  n = sm_count();
   if (cs > 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n / cs * cs);
@@ -131,8 +125,7 @@ inline int resident_clusters(void* kernel, int cs, int threads, int smem, int sm
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
   }
-  kept[next] = {dev, kernel, cs, smem, n};
-  next = (next + 1) % kKept;
+  kept.put(dev, kernel, cs, smem, n);
   return n;
 }
 
