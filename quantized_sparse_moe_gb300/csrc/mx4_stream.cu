@@ -668,12 +668,14 @@ extern "C" qsm_status mx4_gemv(const uint16_t* x, int64_t row_stride, int32_t T,
   if (tok == 0) return QSM_ERR_UNSUPPORTED;
   // Where K is split only because the digits of all rows do not fit (every SM
   // has a tile without), halves of the rows that need no split are faster up to
-  // K of 4096, although the weights are read twice, the second time in part from
-  // L2: 32 x 128256 x 2048 58.6 us against 85.6, 28 x 19456 x 2048 14.8 against
-  // 20.0, 24 x 65536 x 2560 41.1 against 44.5, 28 x 65536 x 3328 57.1 against 68.9,
-  // 26 x 32768 x 3840 41.9 against 41.1; 16 x 65536 x 4096 52.0 against 45.9,
-  // 8 x 32768 x 8192 46.3 against 36.3.
-  if (p.cs > 1 && ntiles >= sm_count() && p.K < 4096) {
+  // K of 4096, below 24 rows of 3584, although the weights are read twice, the second
+  // time in part from L2.  N of 19456, 32768, 65536, halves against the split (us):
+  //   K 2048, 26 rows 14.0 18.9, 22.9 27.9, 35.5 41.8; 32 rows 15.7 21.7, 25.9 32.0, 39.2 48.8
+  //   K 3328, 18 rows 16.7 19.0, 26.9 27.9, 45.0 43.6; 22 rows 18.4 21.8, 30.6 30.9, 49.1 48.1
+  //   K 3584, 18 rows 17.5 19.2, 30.2 27.8, 48.7 44.5; 22 rows 19.3 22.0, 34.4 31.2, 53.2 48.8
+  //   K 3584, 26 rows 21.4 27.4, 37.7 38.7, 58.4 66.5; K 3840 22.8 27.8, 41.1 39.2, 61.9 68.5
+  // and beyond: 16 x 65536 x 4096 52.0 45.9, 8 x 32768 x 8192 46.3 36.3.
+  if (p.cs > 1 && ntiles >= sm_count() && p.K < (T < 24 ? 3584 : 4096)) {
     StreamParams half = p;
     if (plan_rows(&half, kRows, ntiles, (T + 1) / 2, sm_count()) && half.cs == 1) p = half;
   }
