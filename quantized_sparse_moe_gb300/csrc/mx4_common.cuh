@@ -26,8 +26,9 @@ constexpr int kTileCols = 128;    // columns of a scale tile
 constexpr int kTileBytes = 512;
 constexpr int kStageK = 256;      // columns per pipeline stage: 128 bytes of codes a row
 
-__host__ __device__ inline int col_tiles(int cols) { return (cols + kTileCols - 1) / kTileCols; }
-__host__ __device__ inline int row_tiles(int rows) { return (rows + kTileRows - 1) / kTileRows; }
+// (any size up to 2^31 - 1)
+__host__ __device__ inline int col_tiles(int cols) { return cols / kTileCols + (cols % kTileCols != 0); }
+__host__ __device__ inline int row_tiles(int rows) { return rows / kTileRows + (rows % kTileRows != 0); }
 
 // Byte offset, within a matrix's scale tiles, of the four scales of row r
 // in column tile ct.

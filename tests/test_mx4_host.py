@@ -171,3 +171,11 @@ def test_separate_launches_are_a_value_of_acts():
     for acts, want in ((16, 3), (17, 1), (32, 1), (-1, 1), (18, 1)):
         assert lib.moe_mx4_forward(ref, p, 4, acts, p, None, 1, p, p, p, None, p, 0, p, None) == want
         assert (lib.moe_mx4_workspace_bytes(ref, 4, acts) > 0) == (want == 3)
+
+
+@nvcc
+def test_scale_bytes_of_the_largest_sizes():
+    import quantized_sparse_moe_gb300 as qsm
+    n = 2 ** 31 - 1
+    for rows, cols in ((n, 32), (n - 126, 160), (1, n - 31), (300, n)):
+        assert qsm.lib().mx4_scale_bytes(rows, cols) == qsm.mx4_scale_bytes(rows, cols)
