@@ -28,6 +28,7 @@ constexpr int kStageK = 256;      // columns per pipeline stage: 128 bytes of co
 
 // (any size up to 2^31 - 1)
 __host__ __device__ inline int col_tiles(int cols) { return cols / kTileCols + (cols % kTileCols != 0); }
+__host__ __device__ inline int k_stages(int cols) { return cols / kStageK + (cols % kStageK != 0); }
 __host__ __device__ inline int row_tiles(int rows) { return rows / kTileRows + (rows % kTileRows != 0); }
 
 // Byte offset, within a matrix's scale tiles, of the four scales of row r

@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
   }
   const int tiles = MODE == kDense ? p.tiles : p.shared_tiles + uniform(__ldcg(p.n_tiles));
   const int total = tiles * p.nsub;
-  const int nst = (p.K + kStageK - 1) / kStageK;
+  const int nst = k_stages(p.K);
   const int cts = col_tiles(p.K);
   if (MODE != kDense) {
     const int item = blockIdx.x + threadIdx.x * gridDim.x;
@@ -361,8 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
         tc::tma_load_2d(wb, wm, ks * 128, t.w_row[0], &full[s]);
         if (MODE == kGateUp) tc::tma_load_2d(wb + 128 * 128, wm, ks * 128, t.w_row[1], &full[s]);
         unsigned char* sf = wb + C::kWBytes + C::kSfaBytes;
-        bulk_g2s(sf, wsf0 + ks * 2 * kTileBytes, sfb, &full[s]);
-        if (groups == 2) bulk_g2s(sf + 2 * kTileBytes, wsf1 + ks * 2 * kTileBytes, sfb, &full[s]);
+        bulk_g2s(sf, wsf0 + (size_t)ks * 2 * kTileBytes, sfb, &full[s]);
+        if (groups == 2) bulk_g2s(sf + 2 * kTileBytes, wsf1 + (size_t)ks * 2 * kTileBytes, sfb, &full[s]);
       };
       auto load_a = [&](int ks, int s) {
         unsigned char* base = smem + s * C::kStage;
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
           for (int i = 0; i < a8; ++i)
             tc::tma_load_2d(base + i * 8 * 128, &p.a8, ks * 128, t.a_row + 8 * i, &full[s]);
         }
-        bulk_g2s(base + C::kABytes + C::kWBytes, asf + ks * 2 * kTileBytes, sfb, &full[s]);
+        bulk_g2s(base + C::kABytes + C::kWBytes, asf + (size_t)ks * 2 * kTileBytes, sfb, &full[s]);
       };
       int k0 = 0;
       if (!waited) {  // the ring is empty
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_pair_kernel(const __grid
   pdl_wait();
   pdl_launch_dependents();
   const int total = p.tiles * p.nsub, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
-  const int nst = (p.K + kStageK - 1) / kStageK, cts = col_tiles(p.K);
+  const int nst = k_stages(p.K), cts = col_tiles(p.K);
 
   if (warp == 0) {
     int st = 0;
