@@ -76,15 +76,6 @@ split_kernel(const float* __restrict__ w, __nv_bfloat16* __restrict__ out, size_
   }
 }
 
-// True in one thread of the (converged) warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n"
-      : "=r"(r));
-  return r != 0;
-}
-
 // Instruction descriptor, kind::f16 with bf16 A and B (K-major), fp32 D.
 __device__ __forceinline__ uint32_t idesc_bf16_m128(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
@@ -161,7 +152,7 @@ route_tc_kernel(const __grid_constant__ Params p) {
     for (int st = 0, s = 0; st < steps; ++st) {
       if (!__all_sync(0xffffffffu, wait(&full_bar[s], (st / kStages) & 1))) break;
       tc::tc_fence_after();
-      if (elect_one()) {
+      if (tc::elect_one()) {
         const uint32_t a0 = smem_u32(smem + s * STAGE);
         const uint32_t b0 = a0 + A_BYTES;
 #pragma unroll
