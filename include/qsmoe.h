@@ -164,8 +164,8 @@ QSM_API size_t moe_route_workspace_bytes(int32_t T, int32_t H, int32_t E);
  *   logit_bias [E] fp32 or NULL (added to the logits before selection)
  *   topk_idx   [T, k] int32 (out), topk_w [T, k] fp32 (out)
  *   workspace  >= moe_route_workspace_bytes(T, H, E) bytes.  It must hold
- *              zeros before its first use; every call leaves the part that
- *              must start at zero zeroed again.
+ *              zeros before its first use; every call leaves it fit for the
+ *              next, of any T, E and k that it is large enough for.
  * Few tokens run on CUDA cores (fp32 FMA); many tokens (T > 64, E a multiple
  * of 16 up to 256, k <= 8) run one tcgen05 GEMM over an exact three-way
  * bf16 split of w_router, which keeps fp32-accurate logits.

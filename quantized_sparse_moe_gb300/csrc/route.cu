@@ -295,6 +295,11 @@ extern "C" qsm_status moe_route(const uint16_t* x, const float* w_router,
   unsigned* counters = static_cast<unsigned*>(workspace);
   float* logits = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                            counters_bytes(T));
+  // Every call leaves its counters at zero, but the counters of more than 512
+  // tokens lie where a call of fewer has its logits, and one of the other router
+  // its split weights: they are zeroed here (2 us, of some hundreds).
+  if (counters_bytes(T) > 256)
+    QSM_CUDA_TRY(cudaMemsetAsync(counters, 0, counters_bytes(T), stream));
   dim3 grid((E + kExpertsPerCta - 1) / kExpertsPerCta,
             (T + kTokPerCta - 1) / kTokPerCta);
   const GroupOut none = {};

@@ -54,3 +54,21 @@ def test_many_experts_a_token_stay_inside_the_workspace(qsm, T, H, E, k):
     # what the exponential and the division round (2^-20 covers both)
     want = torch.softmax(got, dim=1)
     assert ((wt.double() - want).abs() <= want * (4 * b.amax(dim=1, keepdim=True) + 2.0 ** -20)).all()
+
+
+@pytest.mark.gpu
+def test_one_workspace_serves_calls_of_other_sizes(qsm):
+    """Calls of few and many tokens, and of both routers, one after the other on
+    one workspace that was zeroed once."""
+    H, E = 128, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    w = torch.randn((E, H), generator=g, device="cuda") * 0.05
+    space = torch.zeros(qsm.route_workspace_bytes(4100, H, E), dtype=torch.uint8, device="cuda")
+    for T, k in ((1000, 9), (4100, 9), (700, 12), (2000, 8), (4100, 10), (8, 4), (3000, 9), (64, 9), (513, 9)):
+        x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+        want = qsm.moe_route(x, w, k)                    # on a fresh workspace
+        idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+        wt = torch.full((T, k), -7.0, device="cuda")
+        qsm.moe_route(x, w, k, topk_idx=idx, topk_w=wt, workspace=space)
+        assert torch.equal(idx, want[0]) and torch.equal(wt, want[1])
