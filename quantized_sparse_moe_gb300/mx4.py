@@ -158,12 +158,23 @@ def mx4_tile_scales(scales: torch.Tensor) -> torch.Tensor:
     return t.permute(0, 1, 4, 3, 2, 5).reshape(-1).contiguous()
 
 
-@dataclasses.dataclass(eq=False, frozen=True)
-class Mx4Tensor:
+class _Fixed:
+    """Attributes that cannot be replaced once they are set (`a.x -= 1`, which
+    puts the same object back, is fine), but for those in _free."""
+    _free: tuple = ()
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__ and name not in self._free and self.__dict__[name] is not value:
+            raise AttributeError(f"{type(self).__name__}: {name} cannot be replaced; make another one")
+        super().__setattr__(name, value)
+
+
+@dataclasses.dataclass(eq=False)
+class Mx4Tensor(_Fixed):
     """An MXFP4 matrix, or `experts` of them: codes uint8
     [experts * rows, cols / 2] (any shape of that size) and scale tiles uint8,
     both contiguous on one GPU.  The calls use the addresses taken here: the
-    contents may change, the attributes may not."""
+    contents may change, the attributes not be replaced."""
     codes: torch.Tensor
     scales: torch.Tensor
     rows: int
@@ -178,12 +189,12 @@ class Mx4Tensor:
         for t, size, what in ((self.codes, n, "codes"), (self.scales, sb, "scales")):
             if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != size:
                 raise QSMError(f"Mx4Tensor: {what} must be {size} contiguous bytes")
-        device = self.codes.get_device()
-        if device < 0 or self.scales.get_device() != device:
+        self.device = self.codes.get_device()
+        if self.device < 0 or self.scales.get_device() != self.device:
             raise QSMError("Mx4Tensor: codes and scales must be on one GPU")
-        c = Mx4C(self.experts, self.rows, self.cols, self.codes.data_ptr(), self.scales.data_ptr())
-        for name, value in (("device", device), ("c", c), ("ref", ctypes.byref(c))):
-            object.__setattr__(self, name, value)
+        self.c = Mx4C(self.experts, self.rows, self.cols, self.codes.data_ptr(),
+                      self.scales.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, rows: int, cols: int, experts: int = 1, device="cuda") -> "Mx4Tensor":
@@ -281,16 +292,12 @@ def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, y=None, dev_status=None, stream=None
     return y
 
 
-class Mx4Layer:
+class Mx4Layer(_Fixed):
     """One MoE layer with MXFP4 weights (gate_up [E, 2I, H], down [E, H, I] and
     the shared expert's); keeps the tensors alive.  The weights' contents may
-    change, the attributes may not, but for the router's (w_router and
+    change, the attributes not be replaced, but for the router's (w_router and
     logit_bias), which an Mx4Forward takes as they are when it is made."""
-
-    def __setattr__(self, name, value):
-        if hasattr(self, "c") and name not in ("w_router", "logit_bias"):
-            raise AttributeError(f"Mx4Layer: {name} cannot be changed; make another layer")
-        super().__setattr__(name, value)
+    _free = ("w_router", "logit_bias")
 
     def __init__(self, H, I, E, k, gate_up: Mx4Tensor, down: Mx4Tensor,
                  shared_gate_up: Mx4Tensor, shared_down: Mx4Tensor, w_router,

@@ -171,8 +171,9 @@ def test_what_the_calls_point_to_cannot_be_replaced(mx4):
         for name in names:
             old = getattr(what, name)
             with pytest.raises(AttributeError):
-                setattr(what, name, old)
+                setattr(what, name, Fake((1,), torch.uint8, HERE))
             assert getattr(what, name) is old
+            setattr(what, name, old)       # as an update in place (a.x -= 1) does
     router = Fake((8, 256), torch.float32, HERE)
     L.w_router, L.logit_bias = router, None    # taken when an Mx4Forward is made
     assert L.w_router is router
