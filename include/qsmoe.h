@@ -475,8 +475,8 @@ typedef struct {
 /* What the expert products of moe_mx4_forward multiply the weights with:
  *   QSM_ACTS_BF16  x and h in 16 bits or more, as mx4_gemv (T <= QSM_MX4_MOE_MAX_ROWS:
  *                  every touched weight is read once, few tokens each)
- *   QSM_ACTS_MX4   x and h quantized to MXFP4 by the rule of mx4_quantize (any
- *                  number of tokens: grouped 4-bit products) */
+ *   QSM_ACTS_MX4   x and h quantized to MXFP4 by the rule of mx4_quantize (T k
+ *                  up to 2^24: grouped 4-bit products) */
 typedef enum { QSM_ACTS_BF16 = 0, QSM_ACTS_MX4 = 1 } qsm_acts;
 /* Added to QSM_ACTS_BF16: never the one-launch form, whose CTAs wait for one
  * another (see moe_mx4_forward), for callers whose GPU runs other work beside
@@ -519,8 +519,9 @@ QSM_API size_t moe_mx4_workspace_bytes(const qsm_mx4_layer* L, int32_t T, int32_
  *    of one's y may depend on the experts that the other chose.
  * With QSM_ACTS_MX4 the outputs of the experts are held in fp16 until they are
  * summed, with a power of two of their own for every 128 columns of a row: to
- * 2^-11 of the value, and 2^-39 of the largest magnitude of the 128.  Magnitudes
- * of 2^20 and more do not fit and set QSM_DEV_FP16_RANGE (their y is infinite
+ * 2^-11 of the value, and 2^-39 of the largest magnitude of the 128; y_f32 is the
+ * sum of these.  Magnitudes of 2^20 and more do not fit and set
+ * QSM_DEV_FP16_RANGE (their y is infinite
  * or not a number). */
 QSM_API qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x, int32_t T,
                                    int32_t acts, const float* w_router, const float* logit_bias,

@@ -30,8 +30,8 @@
 //      written once.  The down weights are requested as soon as U is known, ahead
 //      of h.
 //
-// One token takes 15.7 us (17 MB; H 2048, I 512, 256 experts, 8 of them), against
-// 20.6 in separate launches: what is left is the latency of the chain from the
+// One token takes 15.6 us (17 MB in L2; H 2048, I 512, 256 experts, 8 of them; 16.8 with
+// the weights from HBM), against 20.6 in separate launches: what is left is the latency of the chain from the
 // router's rows to y.
 //
 // With more tokens phase C, which has 64 SMs for the down weights, and the

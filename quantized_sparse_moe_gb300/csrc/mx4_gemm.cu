@@ -21,7 +21,7 @@
 // Measured (graph replay): 300 x 2048 x 2048 4.5 us, 4096 x 8192 x 2048 31 us (4.4
 // PFLOP/s), x 8192 78 us (7.0; a pair of SMs per tile, see there).  In the MoE layer of H 2048,
 // I 512 and 256 experts, gate_up takes 50 us at 300 tokens (286 MB of weights, 5.7
-// TB/s: HBM) and 55 at 4096 (802 MB through L2, 14 TB/s: that), down 26 and 49.
+// TB/s: HBM) and 55 at 4096 (802 MB through L2, 14 TB/s: that), down 26 and 51.
 #include <mutex>
 
 #include "mx4_gemm.cuh"
@@ -230,7 +230,8 @@ __device__ __forceinline__ void store_dense(const GemmParams& p, const uint32_t 
 // that an output that does not fit (2^20 and more) is reported (bad).  By way of
 // swizzled boxes of 32 rows x 128 bytes at `stage` and TMA: with two stages
 // of K per tile the outputs are what counts, and whole lines cost L2 less than
-// sectors (4096 tokens, H = 2048: 185.1 us a layer, with sectors 188.6).
+// sectors (4096 tokens, H = 2048: 185.1 us a layer, with sectors 188.6, both
+// before the powers of two).
 template <int BN>
 __device__ __forceinline__ void store_down(const GemmParams& p, const uint32_t (&r)[BN / 2], int row0, int cnt,
                                            int col, int q4, int lane, unsigned char* stage, bool& bad) {

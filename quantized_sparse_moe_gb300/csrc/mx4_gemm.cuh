@@ -16,7 +16,7 @@ enum { kDense = 0, kGateUp = 1, kDown = 2 };
 constexpr int kOutCols = 128;  // columns of the grouped outputs that share a power of two
 // Rows of w per tile of kDown (H = 2048, I = 512: 183.9 us a layer at 4096
 // tokens and 109.7 at 300; 192, which leave room for two accumulators: 186.7
-// and 110.0; 128: 190.6 and 113.3).
+// and 110.0; 128: 190.6 and 113.3; all before the outputs' powers of two).
 constexpr int kDownRows = 256;
 
 struct GemmParams {

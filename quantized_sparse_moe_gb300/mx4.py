@@ -4,7 +4,9 @@ with MXFP4 weights (contracts in include/qsmoe.h).
 
 As the rest of the binding, argument marshalling only: outputs and
 workspaces are allocated with torch when the caller does not pass them, and a
-non-zero status raises ``QSMError``.  Import the names from the package."""
+non-zero status raises ``QSMError``.  What only shows on the device (a value
+that is not finite) goes to dev_status, an int32 tensor; without one it is not
+reported.  Import the names from the package."""
 from __future__ import annotations
 
 import ctypes
