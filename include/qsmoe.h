@@ -521,8 +521,7 @@ QSM_API size_t moe_mx4_workspace_bytes(const qsm_mx4_layer* L, int32_t T, int32_
  * summed, with a power of two of their own for every 128 columns of a row: to
  * 2^-11 of the value, and 2^-39 of the largest magnitude of the 128; y_f32 is the
  * sum of these.  Magnitudes of 2^20 and more do not fit and set
- * QSM_DEV_FP16_RANGE (their y is infinite
- * or not a number). */
+ * QSM_DEV_FP16_RANGE (their y is infinite or not a number). */
 QSM_API qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x, int32_t T,
                                    int32_t acts, const float* w_router, const float* logit_bias,
                                    int32_t flags, int32_t* topk_idx, float* topk_w, uint16_t* y,
