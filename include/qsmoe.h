@@ -528,6 +528,61 @@ QSM_API qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x, in
                                    float* y_f32, void* workspace, size_t workspace_bytes,
                                    int32_t* dev_status, cudaStream_t stream);
 
+/* ---------------------------------------------- norms around a block */
+
+/* n(v) = w v / sqrt(mean(v^2) + eps) + b (RMS), or the same of v - mean(v)
+ * (LAYER), over the H columns of a row.
+ *   weight, bias  [H] fp32, 16-byte aligned, or NULL (1 and 0) */
+typedef enum { QSM_NORM_NONE = 0, QSM_NORM_RMS = 1, QSM_NORM_LAYER = 2 } qsm_norm_kind;
+typedef struct {
+  int32_t kind; /* qsm_norm_kind; NONE has no weight and no bias */
+  float eps;    /* >= 0 */
+  const float* weight;
+  const float* bias;
+} qsm_norm;
+
+/* What the gate holds: nothing; a value for each column, a row of them for
+ * each token or (stride 0) one for all; or one value for each token. */
+typedef enum { QSM_GATE_NONE = 0, QSM_GATE_ROWS = 1, QSM_GATE_TOKENS = 2 } qsm_gate;
+
+/* h_dtype of residual_norm, beside the qsm_dtype values: MXFP4. */
+#define QSM_MXFP4 3
+
+typedef struct {
+  int32_t H;                    /* columns: a multiple of 8, at most 16384 */
+  int32_t x_dtype, y_dtype;     /* qsm_dtype of x and x_out, and of y */
+  int32_t gate_dtype;           /* qsm_dtype of the gate */
+  int32_t h_dtype;              /* qsm_dtype of h, or QSM_MXFP4 (H a multiple of 32) */
+  int32_t gate;                 /* qsm_gate */
+  int32_t gate_sigmoid;         /* 1: the gate's values pass a sigmoid first */
+  float scale;                  /* finite */
+  qsm_norm post, pre;
+} qsm_residual_norm;
+
+/* The residual stream around a block, in one pass (fp32 between the loads and
+ * the stores):
+ *   x_out[t] = x[t] + scale * gate[t] * post(y[t])
+ *   h[t]     = pre(x_out[t])              of x_out before it is rounded
+ * y is the output of the block before (NULL: x_out = x), h the input of the
+ * block after.  Infinities and NaN take their way through the formulas.
+ *   x, y, x_out, h  [T, H] with ldx, ldy, ldo, ldh elements from row to row
+ *       (at least H; rows 16-byte aligned).  x_out or h may be NULL, not both;
+ *       h needs a pre.
+ *   gate  QSM_GATE_ROWS: [T, H] as above with ldg, or ldg = 0: [H] for all
+ *         tokens; QSM_GATE_TOKENS: value t at gate[t ldg], ldg >= 0; needs a y
+ *   h as QSM_MXFP4: the codes of h, dense [T, H / 2] bytes (ldh is not used),
+ *       and h_scales its scale tiles, mx4_scale_bytes(T, H) bytes, padding
+ *       included; the rule is mx4_quantize's, on the fp32 values.  A block with
+ *       an infinity or a NaN sets QSM_DEV_NONFINITE in *dev_status (which may
+ *       be NULL for other types).
+ * x_out and h may be x or y themselves (same address, stride and element
+ * size); what is written may overlap nothing else (QSM_ERR_INVALID_ARGUMENT),
+ * but may lie beside it in the rows of one matrix.  T at most 2^30. */
+QSM_API qsm_status residual_norm(const qsm_residual_norm* n, int32_t T, const void* x, int64_t ldx,
+                                 const void* y, int64_t ldy, const void* gate, int64_t ldg,
+                                 void* x_out, int64_t ldo, void* h, int64_t ldh, uint8_t* h_scales,
+                                 int32_t* dev_status, cudaStream_t stream);
+
 /* ------------------------------------------------------------------ misc */
 
 /* Static description of a status code. */

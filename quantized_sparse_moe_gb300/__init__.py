@@ -11,7 +11,8 @@ importing the binding's functions fails.
 Entry points (see include/qsmoe.h for the exact contracts):
   moe_route, moe_group_tokens, moe_ffn_forward, q8_gemv
 plus ``MoEForward``, which owns the buffers of one layer call and issues the
-three calls in order on one stream; the MXFP4 calls are in mx4.py.
+three calls in order on one stream; the MXFP4 calls are in mx4.py, those around
+the products (the residual stream and its norms) in block.py.
 """
 from __future__ import annotations
 
@@ -125,6 +126,7 @@ def lib() -> ctypes.CDLL:
             L.qsm_launch_count.argtypes = []
             L.qsm_launch_count.restype = ctypes.c_uint64
             _mx4.declare(L)
+            _block.declare(L)
             _lib = L
     return _lib
 
@@ -588,3 +590,8 @@ from . import mx4 as _mx4  # noqa: E402
 from .mx4 import (Mx4Forward, Mx4Layer, Mx4Tensor, moe_mx4_workspace_bytes,  # noqa: E402, F401
                   mx4_dequantize, mx4_gemm, mx4_gemv, mx4_quantize, mx4_scale_bytes,
                   mx4_tile_scales)
+
+# ------------------------------------------------------- around the products
+
+from . import block as _block  # noqa: E402
+from .block import Norm, ResidualNorm  # noqa: E402, F401

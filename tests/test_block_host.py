@@ -1,0 +1,105 @@
+"""The calls around the products on the host: the argument checks of the C
+entry points (they answer before anything is enqueued, so they need no GPU) and
+of the binding."""
+import ctypes
+import os
+import shutil
+
+import pytest
+import torch
+
+nvcc = pytest.mark.skipif(shutil.which("nvcc") is None and
+                          not os.path.exists("/usr/local/cuda/bin/nvcc"), reason="nvcc missing")
+OK, BAD, UNSUP, SMALL = 0, 1, 2, 3
+P = 1 << 20            # never dereferenced: every call below is refused, or has no rows
+FAR = 1 << 30          # between the operands
+
+
+def at(n):
+    return P + n * FAR
+
+
+@nvcc
+def test_residual_norm_refuses_bad_arguments():
+    import quantized_sparse_moe_gb300 as qsm
+    from quantized_sparse_moe_gb300 import block
+    f = qsm.lib().residual_norm
+    none, rms = block.NormC(0, 0.0, None, None), block.NormC(1, 1e-6, at(20), None)
+
+    def call(T=4, H=64, xt=0, yt=0, gt=0, ht=0, gate=0, sig=0, scale=1.0, post=none, pre=rms,
+             x=at(0), ldx=64, y=at(1), ldy=64, g=None, ldg=0, o=at(2), ldo=64, h=at(3), ldh=64,
+             hs=at(4), st=at(5)):
+        c = block.ResidualNormC(H, xt, yt, gt, ht, gate, sig, scale, post, pre)
+        return f(ctypes.byref(c), T, x, ldx, y, ldy, g, ldg, o, ldo, h, ldh, hs, st, None)
+
+    assert call(T=0) == OK
+    assert f(None, 4, P, 64, P, 64, None, 0, P, 64, P, 64, None, None, None) == BAD
+    assert call(T=-1) == BAD and call(H=60) == BAD and call(H=0) == BAD
+    assert call(H=16392, ldx=16392, ldy=16392, ldo=16392, ldh=16392) == UNSUP
+    assert call(T=(1 << 30) + 1) == UNSUP
+    assert call(x=None) == BAD and call(h=None, o=None) == BAD
+    for odd in ("x", "y", "o", "h"):
+        assert call(**{odd: at(7) + 8}) == BAD
+    for ld in ("ldx", "ldy", "ldo", "ldh"):
+        assert call(**{ld: 56}) == BAD and call(**{ld: 68}) == BAD
+    for t in ("xt", "yt", "ht"):
+        assert call(**{t: 4}) == BAD and call(**{t: -1}) == BAD
+    assert call(xt=3) == BAD
+    assert call(scale=float("nan")) == BAD and call(scale=float("inf")) == BAD
+    assert call(sig=2) == BAD and call(gate=3, g=at(6)) == BAD
+    # norms
+    assert call(pre=none) == BAD                                       # h without a pre
+    assert call(pre=block.NormC(3, 1e-6, None, None)) == BAD
+    assert call(pre=block.NormC(1, -1.0, None, None)) == BAD
+    assert call(pre=block.NormC(1, float("nan"), None, None)) == BAD
+    assert call(pre=block.NormC(1, 1e-6, at(20) + 4, None)) == BAD
+    assert call(post=block.NormC(0, 0.0, at(20), None)) == BAD
+    # gates
+    assert call(gate=1) == BAD and call(g=at(6)) == BAD                # kind without values, and the reverse
+    assert call(gate=1, g=at(6), ldg=8) == BAD and call(gate=1, g=at(6) + 8) == BAD
+    assert call(gate=2, g=at(6) + 1) == BAD and call(gate=2, g=at(6), ldg=-1) == BAD
+    assert call(gate=1, g=at(6), gt=3) == BAD
+    assert call(gate=1, g=at(6), y=None) == BAD
+    # MXFP4
+    assert call(ht=3, H=72, ldx=72, ldy=72, ldo=72) == BAD             # H % 32
+    assert call(ht=3, hs=None) == BAD and call(ht=3, st=None) == BAD and call(ht=3, hs=at(4) + 8) == BAD
+
+
+@nvcc
+def test_residual_norm_refuses_overlaps():
+    """What is written may be x or y, lie beside them in one matrix, and nothing else.  The
+    accepted layouts run on the GPU (test_gpu_residual_norm)."""
+    import quantized_sparse_moe_gb300 as qsm
+    from quantized_sparse_moe_gb300 import block
+    f = qsm.lib().residual_norm
+    none, rms = block.NormC(0, 0.0, None, None), block.NormC(1, 1e-6, at(20), None)
+
+    def call(o=at(2), ldo=64, h=at(3), ldh=64, ht=0, g=None, gate=0, hs=at(4), T=4, ldx=64):
+        c = block.ResidualNormC(64, 0, 0, 0, ht, gate, 0, 1.0, none, rms)
+        return f(ctypes.byref(c), T, at(0), ldx, at(1), 64, g, 0, o, ldo, h, ldh, hs, at(5), None)
+
+    assert call(o=at(0) + 128) == BAD and call(h=at(0) + 128) == BAD      # a row further on
+    assert call(o=at(1) + 16) == BAD and call(h=at(1) + 16) == BAD
+    assert call(h=at(2)) == BAD and call(o=at(3) + 3 * 128) == BAD        # each other
+    assert call(h=at(0), ht=2) == BAD and call(h=at(0), ht=3) == BAD      # x, with another size
+    assert call(o=at(20)) == BAD and call(h=at(20)) == BAD                # a weight
+    assert call(o=at(6), g=at(6), gate=1) == BAD
+    assert call(o=at(0), ldo=128) == BAD                                  # x, with another stride
+    assert call(ht=3, hs=at(0)) == BAD and call(ht=3, hs=at(2)) == BAD and call(ht=3, hs=at(3)) == BAD
+    assert call(o=at(0) + 64, ldo=128, ldx=128) == BAD                    # half of it beside x
+
+
+def test_binding_refuses_bad_norms():
+    import quantized_sparse_moe_gb300 as qsm
+    for kw in (dict(kind="max"), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf"))):
+        with pytest.raises(qsm.QSMError):
+            qsm.Norm(**kw)
+    with pytest.raises(qsm.QSMError):
+        qsm.Norm(torch.ones(1, 64))
+    with pytest.raises(qsm.QSMError):
+        qsm.ResidualNorm(64, device="cpu")
+    n = qsm.Norm(torch.ones(64))
+    with pytest.raises(AttributeError):
+        n.weight = torch.ones(64)
+    with pytest.raises(qsm.QSMError):
+        qsm.ResidualNorm(64, pre=n, device="cuda:0")                      # weight not on the GPU
