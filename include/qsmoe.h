@@ -177,6 +177,49 @@ QSM_API qsm_status moe_route(const uint16_t* x, const float* w_router,
                      float* topk_w, void* workspace, size_t workspace_bytes,
                      int32_t* dev_status, cudaStream_t stream);
 
+/* Scores of moe_route_scores: softmax over all experts, or a sigmoid of each. */
+typedef enum { QSM_SCORE_SOFTMAX = 0, QSM_SCORE_SIGMOID = 1 } qsm_score;
+
+/* A router by scores: H, E, k as a layer's;
+ *   score  qsm_score
+ *   groups, groups_kept, group_best  the experts lie in `groups` equal groups
+ *       (e / (E / groups)); a group is worth the sum of its group_best (1 or 2)
+ *       largest biased scores, the groups_kept best groups stay; 1, 1, 1: no groups
+ *   renormalize  1: the weights are divided by their sum
+ *   scale  factor of the weights, finite
+ *   w_split  the weights as moe_router_split writes them
+ *   bias  [E] fp32 or NULL, added to the scores for the choice only.  -infinity
+ *       closes an expert: it is taken after all others, with weight 0. */
+typedef struct {
+  int32_t H, E, k, score;
+  int32_t groups, groups_kept, group_best, renormalize;
+  float scale;
+  const uint16_t* w_split;
+  const float* bias;
+} qsm_router;
+
+/* Bytes of w_split, and the exact split of w_router [E, H] fp32 into three
+ * bf16 parts (once per weight).  H a multiple of 64; both 16-byte aligned. */
+QSM_API size_t moe_router_split_bytes(int32_t E, int32_t H);
+QSM_API qsm_status moe_router_split(const float* w_router, int32_t E, int32_t H, uint16_t* w_split,
+                                    cudaStream_t stream);
+
+/* Routing by scores, for any number of tokens in one launch: logits l = x W^T
+ * with fp32 accuracy, scores s = softmax(l) or sigmoid(l), biased scores
+ * c = s + bias; of the kept groups' experts the k with the largest c (ties,
+ * of groups too, to the lower index) in descending c, weighted with s.
+ *   x [T, H] bf16, ldx elements from row to row (a multiple of 8, at least H);
+ *   topk_idx [T, k] int32, topk_w [T, k] fp32 (out), as moe_group_tokens,
+ *   moe_ffn_forward and moe_mx4_experts take them.
+ * Needs no workspace.  A logit that is not finite closes its expert, and so
+ * does a bias of +infinity or NaN; either sets QSM_DEV_NONFINITE.  Where the taken
+ * weights sum to 0 they are 0.
+ * Requires H % 64 == 0, E <= 512, k <= 32 and <= the kept groups' experts,
+ * groups <= 32 dividing E. */
+QSM_API qsm_status moe_route_scores(const qsm_router* r, const uint16_t* x, int64_t ldx, int32_t T,
+                                    int32_t* topk_idx, float* topk_w, int32_t* dev_status,
+                                    cudaStream_t stream);
+
 /* --------------------------------------------------------------- grouping */
 
 /* Upper bound on the number of blocks of tile_rows rows over any routing:

@@ -594,4 +594,4 @@ from .mx4 import (Mx4Forward, Mx4Layer, Mx4Tensor, moe_mx4_workspace_bytes,  # n
 # ------------------------------------------------------- around the products
 
 from . import block as _block  # noqa: E402
-from .block import Norm, ResidualNorm  # noqa: E402, F401
+from .block import (MoERouter, Norm, ResidualNorm, moe_route_scores)  # noqa: E402, F401

@@ -1,5 +1,6 @@
 """Binding of the calls around the expert and projection products: the
-residual stream with its norms (contracts in include/qsmoe.h).
+residual stream with its norms, and routing by scores (contracts in
+include/qsmoe.h).
 
 As the rest of the binding, argument marshalling only: outputs are allocated
 with torch when the caller does not pass them, and a non-zero status raises
@@ -14,7 +15,7 @@ import torch
 
 from . import QSMError, _check, lib
 from .mx4 import (Mx4Tensor, _DTYPES, _empty, _Fixed, _fp32, _handle, _matrix,
-                  _status)
+                  _status, _stream_of)
 
 _KINDS = {"rms": 1, "layer": 2}
 _MX4 = 3              # h_dtype of MXFP4
@@ -33,9 +34,24 @@ class ResidualNormC(ctypes.Structure):
                 ("post", NormC), ("pre", NormC)]
 
 
+class RouterC(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("groups_kept", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("w_split", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
 def declare(L: ctypes.CDLL) -> None:
     """Argument and result types of the entry points of library L."""
     P, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    L.moe_router_split_bytes.argtypes = [i32, i32]
+    L.moe_router_split_bytes.restype = ctypes.c_size_t
+    L.moe_router_split.argtypes = [P, i32, i32, P, P]
+    L.moe_router_split.restype = ctypes.c_int
+    L.moe_route_scores.argtypes = [ctypes.POINTER(RouterC), P, i64, i32, P, P, P, P]
+    L.moe_route_scores.restype = ctypes.c_int
     L.residual_norm.argtypes = [ctypes.POINTER(ResidualNormC), i32, P, i64, P, i64, P, i64,
                                 P, i64, P, i64, P, P, P]
     L.residual_norm.restype = ctypes.c_int
@@ -185,3 +201,104 @@ class ResidualNorm(_Fixed):
         if rc:
             _check(rc, "residual_norm")
         return (x if x_out is None else x_out), h
+
+
+# ------------------------------------------------------------------ routing
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class MoERouter(_Fixed):
+    """A router by scores: w_router [E, H] fp32, k experts a token.
+      score   "softmax" (over all experts) or "sigmoid" (of each)
+      bias    [E] fp32 or None, added to the scores for the choice, not for the weights;
+              -inf closes an expert
+      groups, groups_kept, group_best  equal groups of experts, how many of them stay,
+              and by how many of their best experts (1 or 2) they are ranked
+      renormalize, scale  the weights are divided by their sum; and multiplied
+    The weights are taken as they are now (split into three bf16 parts, which is what the
+    calls read); the contents of bias may change.  The attributes cannot be replaced."""
+
+    def __init__(self, w_router: torch.Tensor, k: int, score: str = "softmax", bias=None, *,
+                 groups: int = 1, groups_kept: int = 1, group_best: int = 1,
+                 renormalize: bool = True, scale: float = 1.0):
+        what = "MoERouter"
+        if score not in _SCORES:
+            raise QSMError(f'{what}: score must be "softmax" or "sigmoid"')
+        if (w_router.dim() != 2 or w_router.dtype is not torch.float32
+                or not w_router.is_contiguous() or w_router.get_device() < 0):
+            raise QSMError(f"{what}: w_router must be a contiguous fp32 [E, H] on a GPU")
+        self.E, self.H = w_router.shape
+        self.k, self.score, self.bias = int(k), score, bias
+        self.groups, self.groups_kept, self.group_best = int(groups), int(groups_kept), int(group_best)
+        self.renormalize, self.scale = bool(renormalize), float(scale)
+        self.device = w_router.get_device()
+        _fp32(bias, (self.E,), self.device, f"{what}: bias")
+        on = _handle(self.device, None, what)
+        if (self.E < 1 or self.H < 64 or self.H % 64 or self.E > 512 or not 1 <= self.k <= min(32, self.E)
+                or not 1 <= self.groups <= 32 or self.E % self.groups
+                or not 1 <= self.groups_kept <= self.groups
+                or not 1 <= self.group_best <= min(2, self.E // self.groups)
+                or self.groups_kept * (self.E // self.groups) < self.k
+                or not abs(self.scale) < float("inf")):
+            raise QSMError(f"{what}: H must be a multiple of 64, E at most 512, k at most 32 and no more than "
+                           "the kept groups hold, groups at most 32 dividing E, group_best 1 or 2, scale finite")
+        L = lib()
+        self._split = torch.empty(int(L.moe_router_split_bytes(self.E, self.H)), dtype=torch.uint8,
+                                  device=w_router.device)
+        _check(L.moe_router_split(w_router.data_ptr(), self.E, self.H, self._split.data_ptr(), on),
+               "moe_router_split")
+        self.c = RouterC(self.H, self.E, self.k, _SCORES[score], self.groups, self.groups_kept,
+                         self.group_best, int(self.renormalize), self.scale, self._split.data_ptr(),
+                         None if bias is None else bias.data_ptr())
+        self.ref = ctypes.byref(self.c)
+        self._ready = Ready(self.device)
+
+
+class Ready:
+    """What an object's constructor has enqueued on the stream that was the
+    current one: the first call on another stream waits for it.  A stream that
+    is being captured cannot wait for what came before the capture: there the
+    caller does it, with a call or a wait before the capture."""
+
+    def __init__(self, device: int):
+        self.streams = {_stream_of(device)}
+        self.event = None
+        if not torch.cuda.is_current_stream_capturing():
+            self.event = torch.cuda.Event()
+            self.event.record()
+
+    def wait(self, on: int, stream) -> None:
+        if self.event is not None and not torch.cuda.is_current_stream_capturing():
+            (torch.cuda.current_stream() if stream is None else stream).wait_event(self.event)
+            self.streams.add(on)
+
+
+def moe_route_scores(x: torch.Tensor, router: MoERouter, topk_idx=None, topk_w=None,
+                     dev_status=None, stream=None):
+    """The router's choice for x [T, H] bf16 (rows contiguous) -> (topk_idx [T, k] int32,
+    topk_w [T, k] fp32)."""
+    what = "moe_route_scores"
+    dev, T, H, ldx = _matrix(x, what)
+    if x.dtype is not torch.bfloat16 or H != router.H or dev != router.device:
+        raise QSMError(f"{what}: x must be [T, {router.H}] bf16 on the router's device")
+    on = _handle(dev, stream, what)
+    k = router.k
+    if topk_idx is None:
+        topk_idx = _empty(T, k, torch.int32, stream)
+    elif (topk_idx.dtype is not torch.int32 or tuple(topk_idx.shape) != (T, k)
+          or not topk_idx.is_contiguous() or topk_idx.get_device() != dev):
+        raise QSMError(f"{what}: topk_idx must be a contiguous int32 [T, k] on x's device")
+    if topk_w is None:
+        topk_w = _empty(T, k, torch.float32, stream)
+    elif (topk_w.dtype is not torch.float32 or tuple(topk_w.shape) != (T, k)
+          or not topk_w.is_contiguous() or topk_w.get_device() != dev):
+        raise QSMError(f"{what}: topk_w must be a contiguous fp32 [T, k] on x's device")
+    if on not in router._ready.streams:
+        router._ready.wait(on, stream)
+    rc = (_lib or _load()).moe_route_scores(
+        router.ref, x.data_ptr(), ldx, T, topk_idx.data_ptr(), topk_w.data_ptr(),
+        _status(dev_status, dev, what), on)
+    if rc:
+        _check(rc, what)
+    return topk_idx, topk_w

@@ -103,3 +103,34 @@ def test_binding_refuses_bad_norms():
         n.weight = torch.ones(64)
     with pytest.raises(qsm.QSMError):
         qsm.ResidualNorm(64, pre=n, device="cuda:0")                      # weight not on the GPU
+
+
+@nvcc
+def test_route_scores_refuses_bad_arguments():
+    import quantized_sparse_moe_gb300 as qsm
+    from quantized_sparse_moe_gb300 import block
+    L = qsm.lib()
+    assert L.moe_router_split_bytes(8, 64) == 3 * 8 * 64 * 2 and L.moe_router_split_bytes(0, 64) == 0
+    for a in ((None, 8, 64, P, None), (P, 8, 96, P, None), (P, 0, 64, P, None), (P, 8, 64, None, None),
+              (P + 4, 8, 64, P, None), (P, 8, 64, P + 8, None)):
+        assert L.moe_router_split(*a) == BAD
+
+    def call(T=4, x=at(0), ldx=128, idx=at(1), w=at(2), st=at(3), **over):
+        f = dict(H=128, E=16, k=4, score=0, groups=1, groups_kept=1, group_best=1, renormalize=1, scale=1.0,
+                 w_split=at(4), bias=None)
+        f.update(over)
+        return L.moe_route_scores(ctypes.byref(block.RouterC(*f.values())), x, ldx, T, idx, w, st, None)
+    assert call(T=0) == OK
+    assert L.moe_route_scores(None, P, 128, 4, P, P, P, None) == BAD
+    assert call(T=-1) == BAD and call(H=96) == BAD and call(H=0) == BAD and call(E=0) == BAD
+    assert call(k=0) == BAD and call(k=17) == BAD and call(score=2) == BAD and call(renormalize=2) == BAD
+    assert call(groups=3) == BAD and call(groups=4, groups_kept=0) == BAD and call(groups=4, groups_kept=5) == BAD
+    assert call(groups=0) == BAD and call(groups=8, groups_kept=1) == BAD    # two experts for k = 4
+    assert call(group_best=0) == BAD and call(group_best=3) == BAD
+    assert call(groups=16, groups_kept=8, group_best=2) == BAD               # a group of one
+    assert call(scale=float("nan")) == BAD and call(scale=float("inf")) == BAD
+    assert call(E=513, k=4) == UNSUP and call(E=512, k=33) == UNSUP and call(E=128, groups=64, groups_kept=8) == UNSUP
+    for none in ("x", "idx", "w", "st", "w_split"):
+        assert call(**{none: None}) == BAD
+    assert call(x=at(0) + 8) == BAD and call(idx=at(1) + 2) == BAD and call(bias=at(5) + 2) == BAD
+    assert call(ldx=120) == BAD and call(ldx=132) == BAD
