@@ -78,6 +78,7 @@ typedef enum {
                                    tagged logits or h of
                                    moe_decode_layer) ran out: the kernel
                                    returned, its results are invalid */
+#define QSM_DEV_BAD_ADAPTER_ID 16 /* an adapter id of n or more */
 
 typedef enum { QSM_Q8_0 = 0, QSM_AFFINE4_G64 = 1 } qsm_qtype;
 
@@ -625,6 +626,38 @@ QSM_API qsm_status residual_norm(const qsm_residual_norm* n, int32_t T, const vo
                                  const void* y, int64_t ldy, const void* gate, int64_t ldg,
                                  void* x_out, int64_t ldo, void* h, int64_t ldh, uint8_t* h_scales,
                                  int32_t* dev_status, cudaStream_t stream);
+
+/* --------------------------------------------------- low-rank adapters */
+
+/* n adapters for a projection of K inputs and N outputs, of at most `rank`
+ * ranks each:
+ *   a      [n, rank, K] bf16, b [n, N, rank] bf16, 16-byte aligned
+ *   scale  [n] fp32 or NULL (1)
+ *   ranks  [n] int32 or NULL (all `rank`): how many ranks of an adapter count,
+ *          taken into 0 .. rank; the others are not used, whatever they hold
+ * K a multiple of 8, rank a multiple of 8 and at most 128, N >= 1. */
+typedef struct {
+  int32_t n, rank, K, N;
+  const uint16_t* a;
+  const uint16_t* b;
+  const float* scale;
+  const int32_t* ranks;
+} qsm_lora;
+
+/* The adapters of a batch beside a shared projection, one launch:
+ *   out[t] = y[t] + scale[i] * b[i] (a[i] x[t]),  i = ids[t];
+ * a negative id: none, out[t] = y[t].  Sums in fp32, out rounded once (a bf16
+ * out: a[i] x[t] enters the second product to 2^-17).  A token's result does not depend
+ * on the other tokens' values.
+ *   x [T, K] bf16, ldx elements from row to row (a multiple of 8, at least
+ *   K), 16-byte aligned;  ids [T] int32;  y [T, N] (NULL: zeros) and out [T, N] of type
+ *   dtype (QSM_BF16 or QSM_FP32), ldy and ldo elements from row to row (at least N),
+ *   aligned to their elements (16-byte rows and N a multiple of 8 are faster).
+ * out may be y itself (same address and stride); other overlaps are refused.
+ * An id of n or more counts as none and sets QSM_DEV_BAD_ADAPTER_ID. */
+QSM_API qsm_status lora_add(const qsm_lora* L, const uint16_t* x, int64_t ldx, int32_t T,
+                            const int32_t* ids, int32_t dtype, const void* y, int64_t ldy, void* out,
+                            int64_t ldo, int32_t* dev_status, cudaStream_t stream);
 
 /* ------------------------------------------------------------------ misc */
 

@@ -31,6 +31,7 @@ DEV_BAD_EXPERT_ID = 1
 DEV_NONFINITE = 2
 DEV_FP16_RANGE = 4
 DEV_TIMEOUT = 8
+DEV_BAD_ADAPTER_ID = 16
 
 _lock = threading.Lock()
 _lib = None
@@ -594,4 +595,5 @@ from .mx4 import (Mx4Forward, Mx4Layer, Mx4Tensor, moe_mx4_workspace_bytes,  # n
 # ------------------------------------------------------- around the products
 
 from . import block as _block  # noqa: E402
-from .block import (MoERouter, Norm, ResidualNorm, moe_route_scores)  # noqa: E402, F401
+from .block import (LoraAdapters, MoERouter, Norm, ResidualNorm, lora_add,  # noqa: E402, F401
+                    moe_route_scores)

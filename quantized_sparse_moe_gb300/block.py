@@ -1,6 +1,6 @@
 """Binding of the calls around the expert and projection products: the
-residual stream with its norms, and routing by scores (contracts in
-include/qsmoe.h).
+residual stream with its norms, routing by scores, and low-rank adapters
+(contracts in include/qsmoe.h).
 
 As the rest of the binding, argument marshalling only: outputs are allocated
 with torch when the caller does not pass them, and a non-zero status raises
@@ -43,6 +43,13 @@ class RouterC(ctypes.Structure):
                 ("bias", ctypes.c_void_p)]
 
 
+class LoraC(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("ranks", ctypes.c_void_p)]
+
+
 def declare(L: ctypes.CDLL) -> None:
     """Argument and result types of the entry points of library L."""
     P, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
@@ -52,6 +59,8 @@ def declare(L: ctypes.CDLL) -> None:
     L.moe_router_split.restype = ctypes.c_int
     L.moe_route_scores.argtypes = [ctypes.POINTER(RouterC), P, i64, i32, P, P, P, P]
     L.moe_route_scores.restype = ctypes.c_int
+    L.lora_add.argtypes = [ctypes.POINTER(LoraC), P, i64, i32, P, i32, P, i64, P, i64, P, P]
+    L.lora_add.restype = ctypes.c_int
     L.residual_norm.argtypes = [ctypes.POINTER(ResidualNormC), i32, P, i64, P, i64, P, i64,
                                 P, i64, P, i64, P, P, P]
     L.residual_norm.restype = ctypes.c_int
@@ -302,3 +311,76 @@ def moe_route_scores(x: torch.Tensor, router: MoERouter, topk_idx=None, topk_w=N
     if rc:
         _check(rc, what)
     return topk_idx, topk_w
+
+
+# ----------------------------------------------------------------- adapters
+
+_LORA_DTYPES = {torch.bfloat16: 0, torch.float32: 2}
+
+
+class LoraAdapters(_Fixed):
+    """Low-rank adapters for one projection of K inputs and N outputs: a
+    [n, rank, K] and b [n, N, rank] bf16, scale [n] fp32 or None (1), ranks [n]
+    int32 or None: how many ranks of each adapter count (the others are not
+    used, whatever they hold).  rank a multiple of 8, at most 128.  The contents
+    may change (an adapter loaded into a place), the attributes not be replaced."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale=None, ranks=None):
+        what = "LoraAdapters"
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise QSMError(f"{what}: a must be [n, rank, K] and b [n, N, rank]")
+        self.n, self.rank, self.K = a.shape
+        self.N, self.device = b.shape[1], a.get_device()
+        if (self.n < 1 or self.rank < 8 or self.rank % 8 or self.rank > 128 or self.K < 8 or self.K % 8
+                or self.N < 1):
+            raise QSMError(f"{what}: rank must be a multiple of 8 up to 128, K one of 8, n and N positive")
+        for t in (a, b):
+            if t.dtype is not torch.bfloat16 or not t.is_contiguous() or t.get_device() != self.device or self.device < 0:
+                raise QSMError(f"{what}: a and b must be contiguous bf16 tensors on one GPU")
+        _fp32(scale, (self.n,), self.device, f"{what}: scale")
+        if ranks is not None and (ranks.dtype is not torch.int32 or tuple(ranks.shape) != (self.n,)
+                                  or not ranks.is_contiguous() or ranks.get_device() != self.device):
+            raise QSMError(f"{what}: ranks must be a contiguous int32 [n] on the adapters' device")
+        self.a, self.b, self.scale, self.ranks = a, b, scale, ranks
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.c = LoraC(self.n, self.rank, self.K, self.N, p(a), p(b), p(scale), p(ranks))
+        self.ref = ctypes.byref(self.c)
+
+
+def lora_add(x: torch.Tensor, adapters: LoraAdapters, ids: torch.Tensor, y=None, out=None,
+             dtype=None, dev_status=None, stream=None) -> torch.Tensor:
+    """out [T, N] = y [T, N] + scale * b (a x) of each token's adapter.
+      x [T, K] bf16;  ids [T] int32, negative: no adapter
+      y  the projection's output, bf16 or fp32, or None (zeros: then dtype, or out's
+         type, or bf16);  out  None (a new tensor) or where to write: y itself is fine"""
+    what = "lora_add"
+    dev, T, K, ldx = _matrix(x, what)
+    if x.dtype is not torch.bfloat16 or K != adapters.K or dev != adapters.device:
+        raise QSMError(f"{what}: x must be [T, {adapters.K}] bf16 on the adapters' device")
+    if (ids.dtype is not torch.int32 or ids.dim() != 1 or ids.shape[0] != T or not ids.is_contiguous()
+            or ids.get_device() != dev):
+        raise QSMError(f"{what}: ids must be a contiguous int32 [T] on x's device")
+    on = _handle(dev, stream, what)
+    N = adapters.N
+    kind = y.dtype if y is not None else out.dtype if out is not None else dtype or torch.bfloat16
+    dt = _LORA_DTYPES.get(kind)
+    if dt is None or (dtype is not None and dtype != kind):
+        raise QSMError(f"{what}: y and out must be bf16 or fp32, and of dtype where it is given")
+    yp, ldy = None, 0
+    if y is not None:
+        ydev, rows, cols, ldy = _matrix(y, what + ": y")
+        if rows != T or cols != N or ydev != dev:
+            raise QSMError(f"{what}: y must be [T, N] on x's device")
+        yp = y.data_ptr()
+    if out is None:
+        out, ldo = _empty(T, N, kind, stream), N
+    else:
+        odev, rows, cols, ldo = _matrix(out, what + ": out")
+        if out.dtype != kind or rows != T or cols != N or odev != dev:
+            raise QSMError(f"{what}: out must be [T, N] of y's type and device")
+    rc = (_lib or _load()).lora_add(
+        adapters.ref, x.data_ptr(), ldx, T, ids.data_ptr(), dt, yp, ldy, out.data_ptr(), ldo,
+        _status(dev_status, dev, what), on)
+    if rc:
+        _check(rc, what)
+    return out

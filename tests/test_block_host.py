@@ -134,3 +134,40 @@ def test_route_scores_refuses_bad_arguments():
         assert call(**{none: None}) == BAD
     assert call(x=at(0) + 8) == BAD and call(idx=at(1) + 2) == BAD and call(bias=at(5) + 2) == BAD
     assert call(ldx=120) == BAD and call(ldx=132) == BAD
+
+
+@nvcc
+def test_lora_refuses_bad_arguments():
+    import quantized_sparse_moe_gb300 as qsm
+    from quantized_sparse_moe_gb300 import block
+    f = qsm.lib().lora_add
+
+    def call(n=3, rank=16, K=64, N=48, a=at(10), b=at(11), scale=None, ranks=None, T=4, x=at(0), ldx=64,
+             ids=at(1), dt=0, y=at(2), ldy=48, o=at(3), ldo=48, st=at(4)):
+        c = block.LoraC(n, rank, K, N, a, b, scale, ranks)
+        return f(ctypes.byref(c), x, ldx, T, ids, dt, y, ldy, o, ldo, st, None)
+    assert call(T=0) == OK
+    assert f(None, P, 64, 4, P, 0, P, 48, P, 48, P, None) == BAD
+    for kw in (dict(n=0), dict(rank=0), dict(rank=12), dict(K=60), dict(K=0), dict(N=0), dict(T=-1), dict(dt=1), dict(dt=3)):
+        assert call(**kw) == BAD
+    assert call(rank=136) == UNSUP
+    for none in ("a", "b", "x", "ids", "o", "st"):
+        assert call(**{none: None}) == BAD
+    for odd in (dict(a=at(10) + 8), dict(b=at(11) + 8), dict(x=at(0) + 8), dict(ids=at(1) + 2), dict(y=at(2) + 1),
+                dict(o=at(3) + 1), dict(o=at(3) + 2, dt=2, y=None), dict(scale=at(12) + 2), dict(ranks=at(12) + 2), dict(st=at(4) + 1)):
+        assert call(**odd) == BAD
+    for ld in (dict(ldx=56), dict(ldx=68), dict(ldy=47), dict(ldo=47)):
+        assert call(**ld) == BAD
+    # overlaps: out may be y, or lie beside it in one matrix
+    assert call(o=at(0)) == BAD and call(o=at(2) + 96) == BAD and call(o=at(2), ldo=64) == BAD
+    assert call(o=at(1)) == BAD and call(o=at(10)) == BAD and call(o=at(11)) == BAD
+    assert call(o=at(12), scale=at(12)) == BAD and call(o=at(12), ranks=at(12)) == BAD
+    assert call(o=at(2) + 32, ldy=96, ldo=96) == BAD
+
+
+def test_binding_refuses_bad_adapters():
+    import quantized_sparse_moe_gb300 as qsm
+    a, b = torch.zeros(2, 8, 64).bfloat16(), torch.zeros(2, 32, 8).bfloat16()
+    for bad in ((a, b), (a[0], b), (a, b[:1]), (a, b[:, :, :4]), (a[:, :4], b[:, :, :4]), (a.float(), b.float())):
+        with pytest.raises(qsm.QSMError):
+            qsm.LoraAdapters(*bad)                                         # not on a GPU, or misshapen
