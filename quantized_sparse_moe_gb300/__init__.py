@@ -488,12 +488,19 @@ class MoEForward:
     """Buffers of one MoE layer call for T tokens, and the call sequence on
     one stream (nothing is read back).  When moe_decode_layer supports the
     layer and T (T <= 8), one launch (one_launch=True); otherwise route ->
-    group -> FFN, with the fused moe_route_group launch for T <= 8."""
+    group -> FFN, with the fused moe_route_group launch for T <= 8.  With router,
+    an MoERouter of the layer's H, E and k, the tokens are routed by its scores
+    (route -> group -> FFN); the layer's own router, renormalize and
+    bias_select_only are not used then."""
 
     def __init__(self, layer: Layer, T: int, device="cuda", renormalize=True,
                  want_f32=False, fuse_route_group=True, *, bias_select_only=False,
-                 one_launch=True):
-        self.layer, self.T = layer, T
+                 one_launch=True, router=None):
+        self.layer, self.T, self.router = layer, T, router
+        if router is not None:
+            if (router.H, router.E, router.k) != (layer.H, layer.E, layer.k):
+                raise QSMError("MoEForward: the router's H, E and k must be the layer's")
+            one_launch = False
         self.renormalize = route_flags(renormalize, bias_select_only)
         self.fuse_route_group = fuse_route_group
         dl = decode_layer_workspace_bytes(layer, T) if one_launch else 0
@@ -541,7 +548,12 @@ class MoEForward:
                 _check(rc, "moe_decode_layer")
             return y
         fused = None
-        if self.fuse_route_group and self.T <= 8:
+        if self.router is not None:
+            self.router.route(x, self.topk_idx, self.topk_w, self.dev_status, stream)
+            moe_group_tokens(self.topk_idx, L.E, self.grouping.tile_rows,
+                             self.grouping, self.dev_status, stream)
+            fused = True
+        elif self.fuse_route_group and self.T <= 8:
             fused = moe_route_group(x, L.w_router, L.k, self.grouping,
                                     L.logit_bias, self.renormalize,
                                     self.topk_idx, self.topk_w, self.route_ws,

@@ -263,6 +263,10 @@ class MoERouter(_Fixed):
         self.ref = ctypes.byref(self.c)
         self._ready = Ready(self.device)
 
+    def route(self, x, topk_idx=None, topk_w=None, dev_status=None, stream=None):
+        """moe_route_scores(x, self, ...)."""
+        return moe_route_scores(x, self, topk_idx, topk_w, dev_status, stream)
+
 
 class Ready:
     """What an object's constructor has enqueued on the stream that was the

@@ -513,24 +513,28 @@ extern "C" size_t moe_mx4_workspace_bytes(const qsm_mx4_layer* L, int32_t T, int
   return qsm::mx4::plan_of(L, T, acts, &p) ? p.total : 0;
 }
 
-extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x, int32_t T,
-                                      int32_t acts, const float* w_router, const float* logit_bias,
-                                      int32_t flags, int32_t* topk_idx, float* topk_w, uint16_t* y,
-                                      float* y_f32, void* workspace, size_t workspace_bytes,
-                                      int32_t* dev_status, cudaStream_t stream) {
-  using namespace qsm;
-  using namespace qsm::mx4;
+namespace qsm {
+namespace mx4 {
+namespace {
+
+// moe_mx4_forward, or with `routed` moe_mx4_experts: topk_idx and topk_w are
+// there already, there is no w_router, and no one-launch form.
+qsm_status forward(const qsm_mx4_layer* L, const uint16_t* x, int32_t T, int32_t acts, bool routed,
+                   const float* w_router, const float* logit_bias, int32_t flags, int32_t* topk_idx,
+                   float* topk_w, uint16_t* y, float* y_f32, void* workspace, size_t workspace_bytes,
+                   int32_t* dev_status, cudaStream_t stream) {
   int kind;
   bool one;
   if (!L || T < 0 || !acts_of(acts, &kind, &one) ||
       (flags & ~(QSM_ROUTE_RENORMALIZE | QSM_ROUTE_BIAS_SELECT_ONLY)))
     return QSM_ERR_INVALID_ARGUMENT;
+  if (routed && kind == QSM_ACTS_BF16) acts = kind | QSM_ACTS_SEPARATE_LAUNCHES;
   if (!shape_ok(L)) return QSM_ERR_UNSUPPORTED;
   if (T == 0) return QSM_OK;
-  if (!x || !w_router || !topk_idx || !topk_w || !y || !workspace || !dev_status || !aligned16(x) ||
-      !aligned16(w_router) || !aligned16(workspace) || !aligned16(topk_idx) || !aligned16(topk_w) ||
-      !aligned16(y) || (y_f32 && !aligned16(y_f32)) || !aligned4(dev_status) ||
-      (logit_bias && !aligned4(logit_bias)) || (L->shared_gate && !aligned16(L->shared_gate)))
+  if (!x || (!routed && !w_router) || !topk_idx || !topk_w || !y || !workspace || !dev_status || !aligned16(x) ||
+      !aligned16(w_router) || !aligned16(workspace) || (!routed && (!aligned16(topk_idx) || !aligned16(topk_w))) ||
+      !aligned4(topk_idx) || !aligned4(topk_w) || !aligned16(y) || (y_f32 && !aligned16(y_f32)) ||
+      !aligned4(dev_status) || (logit_bias && !aligned4(logit_bias)) || (L->shared_gate && !aligned16(L->shared_gate)))
     return QSM_ERR_INVALID_ARGUMENT;
   if (!weights_ok(L->gate_up, L->E, 2 * L->I, L->H) || !weights_ok(L->down, L->E, L->H, L->I) ||
       !weights_ok(L->shared_gate_up, 1, 2 * L->I, L->H) || !weights_ok(L->shared_down, 1, L->H, L->I))
@@ -550,8 +554,9 @@ extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x,
                           i32(p.tile_map), i32(p.n_tiles), p.tile_rows, p.max_tiles};
   const size_t route_bytes = p.route_end - p.route;
   const bool half = kind == QSM_ACTS_MX4;
-  qsm_status st = moe_route(x, w_router, logit_bias, T, L->H, L->E, L->k, flags, topk_idx, topk_w,
-                            ws + p.route, route_bytes, dev_status, stream);
+  qsm_status st = routed ? QSM_OK
+                         : moe_route(x, w_router, logit_bias, T, L->H, L->E, L->k, flags, topk_idx, topk_w,
+                                     ws + p.route, route_bytes, dev_status, stream);
   if (st == QSM_OK && half) st = moe_group_tokens(topk_idx, T, L->k, L->E, &g, dev_status, stream);
   if (st != QSM_OK) return st;
   st = half ? many_tokens(L, p, x, T, topk_idx, g, ws, dev_status, stream)
@@ -570,4 +575,25 @@ extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x,
                           (const float*)(ws + p.oscale), half ? (const int32_t*)i32(p.pos) : (const int32_t*)topk_idx,
                           (const float*)topk_w, x, L->shared_gate, T, (int)L->k, (int)L->H, (int)L->E, y, y_f32));
   return QSM_OK;
+}
+
+}  // namespace
+}  // namespace mx4
+}  // namespace qsm
+
+extern "C" qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x, int32_t T,
+                                      int32_t acts, const float* w_router, const float* logit_bias,
+                                      int32_t flags, int32_t* topk_idx, float* topk_w, uint16_t* y,
+                                      float* y_f32, void* workspace, size_t workspace_bytes,
+                                      int32_t* dev_status, cudaStream_t stream) {
+  return qsm::mx4::forward(L, x, T, acts, false, w_router, logit_bias, flags, topk_idx, topk_w, y, y_f32,
+                           workspace, workspace_bytes, dev_status, stream);
+}
+
+extern "C" qsm_status moe_mx4_experts(const qsm_mx4_layer* L, const uint16_t* x, int32_t T, int32_t acts,
+                                      const int32_t* topk_idx, const float* topk_w, uint16_t* y, float* y_f32,
+                                      void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                      cudaStream_t stream) {
+  return qsm::mx4::forward(L, x, T, acts, true, nullptr, nullptr, 0, const_cast<int32_t*>(topk_idx),
+                           const_cast<float*>(topk_w), y, y_f32, workspace, workspace_bytes, dev_status, stream);
 }

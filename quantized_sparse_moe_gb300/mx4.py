@@ -59,7 +59,9 @@ def declare(L: ctypes.CDLL) -> None:
     L.moe_mx4_workspace_bytes.restype = sz
     L.moe_mx4_forward.argtypes = [ctypes.POINTER(Mx4LayerC), P, i32, i32, P, P, i32,
                                   P, P, P, P, P, sz, P, P]
-    for f in (L.mx4_quantize, L.mx4_dequantize, L.mx4_gemm, L.mx4_gemv, L.moe_mx4_forward):
+    L.moe_mx4_experts.argtypes = [ctypes.POINTER(Mx4LayerC), P, i32, i32, P, P, P, P, P, sz, P, P]
+    for f in (L.mx4_quantize, L.mx4_dequantize, L.mx4_gemm, L.mx4_gemv, L.moe_mx4_forward,
+              L.moe_mx4_experts):
         f.restype = st
 
 
@@ -343,20 +345,29 @@ class Mx4Forward:
     acts="bf16" (T <= 64) multiplies the weights with x and h unrounded,
     acts="mx4" with their MXFP4 forms.  One or two tokens with acts="bf16" run
     in one launch whose CTAs wait for one another, unless one_launch=False (for a
-    GPU that runs other work beside the call).  Results: y (returned), topk_idx,
-    topk_w, and y_f32 with want_f32."""
+    GPU that runs other work beside the call).  With router, an MoERouter of the
+    layer's H, E and k, the tokens are routed by its scores (always separate
+    launches); the layer's own router, renormalize and bias_select_only are not
+    used then.  Results: y (returned), topk_idx, topk_w, and y_f32 with want_f32."""
 
     def __init__(self, layer: Mx4Layer, T: int, acts: str = "bf16", device="cuda",
-                 renormalize=True, want_f32=False, *, bias_select_only=False, one_launch=True):
+                 renormalize=True, want_f32=False, *, bias_select_only=False, one_launch=True,
+                 router=None):
         if acts not in _ACTS:
             raise QSMError('Mx4Forward: acts must be "bf16" or "mx4"')
+        if router is not None:
+            if (router.H, router.E, router.k, router.device) != (layer.H, layer.E, layer.k, layer.device):
+                raise QSMError("Mx4Forward: the router's H, E, k and device must be the layer's")
+            one_launch = False
+        self.router = router
         need = moe_mx4_workspace_bytes(layer, T, acts, one_launch)
         if T < 0 or (need == 0 and T > 0):
             raise QSMError("Mx4Forward: unsupported layer or token count")
-        # the router as it is now (what the calls point to)
-        self._router = (_fp32(layer.w_router, (layer.E, layer.H), layer.device, "Mx4Forward: w_router"),
-                        _fp32(layer.logit_bias, (layer.E,), layer.device, "Mx4Forward: logit_bias"))
-        if self._router[0] is None:
+        # the layer's own router as it is now (what the calls point to)
+        self._router = (None, None) if router is not None else (
+            _fp32(layer.w_router, (layer.E, layer.H), layer.device, "Mx4Forward: w_router"),
+            _fp32(layer.logit_bias, (layer.E,), layer.device, "Mx4Forward: logit_bias"))
+        if self._router[0] is None and router is None:
             raise QSMError("Mx4Forward: the layer has no router")
         self.layer, self.T, self.acts = layer, T, acts
         k, H = layer.k, layer.H
@@ -366,10 +377,14 @@ class Mx4Forward:
         self.y_f32 = torch.empty((T, H), dtype=torch.float32, device=device) if want_f32 else None
         self.workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=device)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=device)
-        self._fn = lib().moe_mx4_forward
         p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        self._mid = (T, _acts(acts, one_launch), p(layer.w_router), p(layer.logit_bias),
-                     route_flags(renormalize, bias_select_only), p(self.topk_idx), p(self.topk_w))
+        if router is None:
+            self._fn = lib().moe_mx4_forward
+            self._mid = (T, _acts(acts, one_launch), p(layer.w_router), p(layer.logit_bias),
+                         route_flags(renormalize, bias_select_only), p(self.topk_idx), p(self.topk_w))
+        else:
+            self._fn = lib().moe_mx4_experts
+            self._mid = (T, _acts(acts, one_launch), p(self.topk_idx), p(self.topk_w))
         self._tail = (p(self.y_f32), p(self.workspace), self.workspace.numel(), p(self.dev_status))
         self._layer_ref = ctypes.byref(layer.c)
         self._device, self._shape = self.y.get_device(), self.y.shape
@@ -395,9 +410,11 @@ class Mx4Forward:
         on = _handle(self._device, stream, "Mx4Forward")
         if on not in self._ready:
             self._wait_ready(on, stream)
+        if self.router is not None:
+            self.router.route(x, self.topk_idx, self.topk_w, self.dev_status, stream)
         rc = self._fn(self._layer_ref, x.data_ptr(), *self._mid, y.data_ptr(), *self._tail, on)
         if rc:
-            _check(rc, "moe_mx4_forward")
+            _check(rc, "moe_mx4_forward" if self.router is None else "moe_mx4_experts")
         return y
 
     def _wait_ready(self, on: int, stream) -> None:

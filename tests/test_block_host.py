@@ -171,3 +171,32 @@ def test_binding_refuses_bad_adapters():
     for bad in ((a, b), (a[0], b), (a, b[:1]), (a, b[:, :, :4]), (a[:, :4], b[:, :, :4]), (a.float(), b.float())):
         with pytest.raises(qsm.QSMError):
             qsm.LoraAdapters(*bad)                                         # not on a GPU, or misshapen
+
+
+@nvcc
+def test_experts_refuse_bad_arguments():
+    import quantized_sparse_moe_gb300 as qsm
+    from quantized_sparse_moe_gb300 import mx4
+    lib = qsm.lib()
+
+    def layer(H=256, I=128, E=8, k=2, **over):
+        f = dict(gate_up=mx4.Mx4C(E, 2 * I, H, P, P), down=mx4.Mx4C(E, H, I, P, P),
+                 shared_gate_up=mx4.Mx4C(1, 2 * I, H, P, P), shared_down=mx4.Mx4C(1, H, I, P, P),
+                 shared_gate=None)
+        f.update(over)
+        return mx4.Mx4LayerC(H, I, E, k, *f.values())
+
+    def call(L, T=4, acts=0, x=P, idx=P, w=P, y=P, ws=1 << 40):
+        return lib.moe_mx4_experts(ctypes.byref(L), x, T, acts, idx, w, y, None, P, ws, P, None)
+    assert call(layer(), T=0) == OK
+    assert call(layer(), T=-1) == BAD and call(layer(), acts=2) == BAD and call(layer(), acts=17) == BAD
+    assert call(layer(H=192)) == UNSUP and call(layer(k=9)) == UNSUP and call(layer(), T=65) == UNSUP
+    assert call(layer(), x=None) == BAD and call(layer(), idx=None) == BAD and call(layer(), w=None) == BAD
+    assert call(layer(), idx=P + 2) == BAD and call(layer(), w=P + 1) == BAD and call(layer(), y=P + 4) == BAD
+    assert call(layer(down=mx4.Mx4C(8, 256, 160, P, P))) == BAD
+    ws = lib.moe_mx4_workspace_bytes
+    for T, acts, sized in ((1, 0, 16), (2, 16, 16), (40, 0, 16), (65, 1, 1)):
+        need = ws(ctypes.byref(layer()), T, sized)
+        assert need > 0 and call(layer(), T=T, acts=acts, ws=need - 1) == SMALL
+    with pytest.raises(qsm.QSMError):
+        qsm.MoEForward(type("L", (), dict(H=256, E=8, k=2))(), 4, router=type("R", (), dict(H=256, E=8, k=3))())
