@@ -20,6 +20,8 @@ namespace {
 constexpr int kMaxH = 16384;
 constexpr int kMaxT = 1 << 30;
 constexpr int kWarpRows = 4;       // rows of a CTA when a warp holds a row
+constexpr size_t kBuffers = 216 * 1024;        // shared memory of the many-row kernel
+constexpr long long kManyValues = 3 << 20;
 
 struct Side {  // a norm
   int kind;
@@ -43,29 +45,28 @@ struct Params {
   int32_t* status;
 };
 
+// Eight columns as they lie in memory.
+template <int DT>
 struct Raw {
-  uint4 v[2];
+  uint4 v[DT == QSM_FP32 ? 2 : 1];
 };
 
-__device__ __forceinline__ Raw load8(const char* row, int c, int type) {
-  Raw r;
-  if (type == QSM_FP32) {
-    const uint4* p = reinterpret_cast<const uint4*>(row) + 2 * c;
-    r.v[0] = p[0];
-    r.v[1] = p[1];
-  } else {
-    r.v[0] = reinterpret_cast<const uint4*>(row)[c];
-    r.v[1] = make_uint4(0, 0, 0, 0);
-  }
+template <int DT>
+__device__ __forceinline__ Raw<DT> load8(const char* row, int c) {
+  Raw<DT> r;
+  const uint4* p = reinterpret_cast<const uint4*>(row) + (DT == QSM_FP32 ? 2 : 1) * c;
+  r.v[0] = *p;
+  if (DT == QSM_FP32) r.v[DT == QSM_FP32] = p[1];
   return r;
 }
 
-__device__ __forceinline__ void widen(const Raw& r, int type, float (&v)[8]) {
-  const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
-  if (type == QSM_FP32) {
+template <int DT>
+__device__ __forceinline__ void widen(const Raw<DT>& r, float (&v)[8]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(r.v);
+  if (DT == QSM_FP32) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-  } else if (type == QSM_BF16) {
+  } else if (DT == QSM_BF16) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = bf16_lo(w[i]);
@@ -81,48 +82,57 @@ __device__ __forceinline__ void widen(const Raw& r, int type, float (&v)[8]) {
   }
 }
 
-__device__ __forceinline__ void store8(char* row, int c, int type, const float (&v)[8]) {
-  if (type == QSM_FP32) {
+template <int DT>
+__device__ __forceinline__ void store8(char* row, int c, const float (&v)[8]) {
+  if constexpr (DT == QSM_FP32) {
     float4* p = reinterpret_cast<float4*>(row) + 2 * c;
     p[0] = make_float4(v[0], v[1], v[2], v[3]);
     p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    return;
-  }
-  uint32_t w[4];
-  if (type == QSM_BF16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
   } else {
+    uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __half2 b = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      if (DT == QSM_BF16) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      } else {
+        const __half2 b = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
     }
+    reinterpret_cast<uint4*>(row)[c] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  reinterpret_cast<uint4*>(row)[c] = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Sum over the threads that hold the row.  Calls alternate between two
 // buffers, so that one barrier a call is enough.
 struct RowSum {
   float (*red)[32];
-  int tpr, turn;
+  int tpr, turn, bar;  // the hardware barrier of these threads, 0: the CTA's
+  __device__ __forceinline__ void sync() const {
+    if (tpr == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
+  }
   __device__ __forceinline__ float operator()(float v) {
     v = warp_sum(v);
     if (tpr == 32) return v;
     float* r = red[turn];
     turn ^= 1;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) r[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return warp_sum(lane < (tpr >> 5) ? r[lane] : 0.f);
+    const int lane = threadIdx.x & 31, warps = tpr >> 5;
+    if (lane == 0) r[(threadIdx.x >> 5) % warps] = v;
+    sync();
+    return warp_sum(lane < warps ? r[lane] : 0.f);
   }
 };
 
-// v <- n(v); live[i]: whether the thread has a chunk i (the others hold zeros).
+// Eight fp32 of a vector (in global memory, or in the CTA's shared memory).
+__device__ __forceinline__ void eight(const float* p, int c, float (&u)[8]) {
+  const float4* at = reinterpret_cast<const float4*>(p) + 2 * c;
+  const float4 a = at[0], b = at[1];
+  u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w, u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
+}
+
+// v <- n(v); chunks past the row hold zeros and stay so.
 template <int V>
 __device__ __forceinline__ void normalize(float (&v)[V][8], const Side& n, int H, int c0, int step, RowSum& sum) {
   if (n.kind == QSM_NORM_NONE) return;
@@ -146,23 +156,28 @@ __device__ __forceinline__ void normalize(float (&v)[V][8], const Side& n, int H
     for (int j = 0; j < 8; ++j) q = fmaf(v[i][j], v[i][j], q);
   const float f = __frsqrt_rn(sum(q) / (float)H + n.eps);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = c0 + i * step;
-    if (c * 8 >= H) continue;
+  for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[i][j] *= f;
-    if (n.w) {
-      const float4* w = reinterpret_cast<const float4*>(n.w) + 2 * c;
-      const float4 a = __ldg(w), b = __ldg(w + 1);
-      v[i][0] *= a.x, v[i][1] *= a.y, v[i][2] *= a.z, v[i][3] *= a.w;
-      v[i][4] *= b.x, v[i][5] *= b.y, v[i][6] *= b.z, v[i][7] *= b.w;
-    }
-    if (n.b) {
-      const float4* w = reinterpret_cast<const float4*>(n.b) + 2 * c;
-      const float4 a = __ldg(w), b = __ldg(w + 1);
-      v[i][0] += a.x, v[i][1] += a.y, v[i][2] += a.z, v[i][3] += a.w;
-      v[i][4] += b.x, v[i][5] += b.y, v[i][6] += b.z, v[i][7] += b.w;
-    }
+  if (n.w) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if ((c0 + i * step) * 8 < H) {
+        float u[8];
+        eight(n.w, c0 + i * step, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= u[j];
+      }
+  }
+  if (n.b) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if ((c0 + i * step) * 8 < H) {
+        float u[8];
+        eight(n.b, c0 + i * step, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += u[j];
+      }
   }
 }
 
@@ -191,89 +206,208 @@ __device__ __forceinline__ void store_mx4(const Params& p, int row, int c, const
     *reinterpret_cast<uint32_t*>(p.hs + mx4::scale_word(row, c >> 4, mx4::col_tiles(p.H))) = sw;
 }
 
-// Threads of a row at most: 128 registers hold four chunks.
-constexpr int max_threads(int v) { return v == 1 ? 1024 : 512; }
+// v *= gate (of whatever type); gr: the row's values, or value.
+template <int V, int DT>
+__device__ __forceinline__ void apply_gate(const Params& p, const char* gr, int c0, float (&v)[V][8]) {
+  const auto value = [&](float g) { return p.sigmoid ? 1.0f / (1.0f + expf(-g)) : g; };
+  if (p.gate_kind == QSM_GATE_TOKENS) {
+    float one;
+    if (DT == QSM_FP32) one = *reinterpret_cast<const float*>(gr);
+    else if (DT == QSM_BF16) one = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(gr));
+    else one = __half2float(*reinterpret_cast<const __half*>(gr));
+    one = value(one);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= one;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = c0 + i * p.tpr;
+    if (c * 8 >= p.H) continue;
+    float g[8];
+    widen<DT>(load8<DT>(gr, c), g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] *= value(g[j]);
+  }
+}
 
-template <int V>
-__global__ void __launch_bounds__(max_threads(V))
-residual_norm_kernel(const __grid_constant__ Params p) {
+template <int V, int DT>
+__device__ __forceinline__ void store_row(char* row, int H, int c0, int step, const float (&v)[V][8]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if ((c0 + i * step) * 8 < H) store8<DT>(row, c0 + i * step, v[i]);
+}
+
+// Between the loads and the stores of one row: v holds y (or, without y, x)
+// on entry; x(i, u) gives the row's x of chunk i.
+template <int V, int XT, typename GetX, typename Read>
+__device__ __forceinline__ void one_row(const Params& p, const Side& post, const Side& pre, const char* gate, int row, int c0, float (&v)[V][8], RowSum& sum, bool& bad,
+                                        GetX x, Read read) {
+  const int H = p.H;
+  if (p.y) {
+    normalize<V>(v, post, H, c0, p.tpr, sum);
+    if (p.gate_kind != QSM_GATE_NONE) {
+      if (p.gt == QSM_BF16) apply_gate<V, QSM_BF16>(p, gate, c0, v);
+      else if (p.gt == QSM_FP32) apply_gate<V, QSM_FP32>(p, gate, c0, v);
+      else apply_gate<V, QSM_FP16>(p, gate, c0, v);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float u[8];
+      x(i, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = fmaf(p.scale, v[i][j], u[j]);
+    }
+  }
+  read();  // the row's inputs are in registers
+  if (p.xo) store_row<V, XT>(p.xo + (size_t)row * p.ldo, H, c0, p.tpr, v);
+  if (!p.h) return;
+  normalize<V>(v, pre, H, c0, p.tpr, sum);
+  char* hr = p.h + (size_t)row * p.ldh;
+  if (p.ht == QSM_MXFP4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) store_mx4(p, row, c0 + i * p.tpr, v[i], bad);
+  } else if (p.ht == QSM_BF16) {
+    store_row<V, QSM_BF16>(hr, H, c0, p.tpr, v);
+  } else if (p.ht == QSM_FP32) {
+    store_row<V, QSM_FP32>(hr, H, c0, p.tpr, v);
+  } else {
+    store_row<V, QSM_FP16>(hr, H, c0, p.tpr, v);
+  }
+}
+
+// Whether the gate has a row for each token.
+__host__ __device__ inline bool gate_rows(const Params& p) { return p.gate_kind == QSM_GATE_ROWS && p.ldg != 0; }
+
+// Zero scales of a row past the last one of a scale tile.
+__device__ __forceinline__ void pad_row(const Params& p, int row, int c0) {
+  for (int ct = c0; ct < mx4::col_tiles(p.H); ct += p.tpr)
+    *reinterpret_cast<uint32_t*>(p.hs + mx4::scale_word(row, ct, mx4::col_tiles(p.H))) = 0u;
+}
+
+// Few rows: a CTA (for short rows, a warp) has one, a thread eight columns of it.
+template <int XT, int YT>
+__global__ void __launch_bounds__(1024)
+row_kernel(const __grid_constant__ Params p) {
   __shared__ float red[2][32];
   pdl_wait();
   pdl_launch_dependents();
   const int per = blockDim.x / p.tpr;  // rows of this CTA
-  const int sub = per > 1 ? threadIdx.x >> 5 : 0;
-  const int row = blockIdx.x * per + sub, c0 = threadIdx.x - sub * p.tpr, H = p.H;
+  const int sub = per > 1 ? threadIdx.x >> 5 : 0, row = blockIdx.x * per + sub, c0 = threadIdx.x - sub * p.tpr;
   if (row >= p.rows) return;  // whole rows, and no barrier where a CTA has several
-  if (row >= p.T) {           // past the last row of a scale tile: zero scales
-    for (int ct = c0; ct < mx4::col_tiles(H); ct += p.tpr)
-      *reinterpret_cast<uint32_t*>(p.hs + mx4::scale_word(row, ct, mx4::col_tiles(H))) = 0u;
-    return;
+  if (row >= p.T) return pad_row(p, row, c0);
+  RowSum sum{red, p.tpr, 0, 0};
+  Raw<XT> xraw = {};
+  Raw<YT> yraw = {};
+  if (c0 * 8 < p.H) {
+    xraw = load8<XT>(p.x + (size_t)row * p.ldx, c0);
+    if (p.y) yraw = load8<YT>(p.y + (size_t)row * p.ldy, c0);
   }
-  RowSum sum{red, p.tpr, 0};
-  const char* xr = p.x + (size_t)row * p.ldx;
-  Raw xraw[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    xraw[i] = {};
-    if ((c0 + i * p.tpr) * 8 < H) xraw[i] = load8(xr, c0 + i * p.tpr, p.xt);
+  float v[1][8];
+  bool bad = false;
+  if (p.y) widen<YT>(yraw, v[0]);
+  else widen<XT>(xraw, v[0]);
+  one_row<1, XT>(p, p.post, p.pre, p.gate + (size_t)row * p.ldg, row, c0, v, sum, bad, [&](int, float (&u)[8]) { widen<XT>(xraw, u); }, [] {});
+  if (bad) set_status(p.status, QSM_DEV_NONFINITE);
+}
+
+// Many rows: a CTA per SM, groups of tpr threads that take row after row.  Each
+// group has a buffer in shared memory, which bulk copies fill with the next
+// row (x, y and the gate) as soon as the present one is in registers; the
+// norms' vectors lie beside them.  Eight chunks a thread: a row of 2048 is a
+// warp's, and its sums need no barrier.
+constexpr int kRowsThreads = 384, kMaxGroups = kRowsThreads / 32;
+
+template <int V, int XT, int YT>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+rows_kernel(const __grid_constant__ Params p, int groups, int vectors) {
+  extern __shared__ __align__(128) unsigned char buffers[];
+  __shared__ float red[kMaxGroups][2][32];
+  __shared__ __align__(8) uint64_t full[kMaxGroups], vec_bar;
+  __shared__ int abort_flag;
+  constexpr int kX = XT == QSM_FP32 ? 4 : 2, kY = YT == QSM_FP32 ? 4 : 2;
+  const int g = threadIdx.x / p.tpr, c0 = threadIdx.x - g * p.tpr, H = p.H;
+  const uint32_t xb = (uint32_t)H * kX, yb = p.y ? (uint32_t)H * kY : 0u;
+  const uint32_t gb = gate_rows(p) ? (uint32_t)H * (p.gt == QSM_FP32 ? 4 : 2) : 0u, bytes = xb + yb + gb;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < groups; ++i) mbar_init(&full[i], 1);
+    mbar_init(&vec_bar, 1);
+    abort_flag = 0;
+    fence_mbar_init();
   }
-  float v[V][8];
-  if (p.y) {
-    const char* yr = p.y + (size_t)row * p.ldy;
-    Raw raw[V];
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  // the norms' vectors, once per CTA, before the rows (which would hold them up)
+  Side post = p.post, pre = p.pre;
+  if (vectors) {
+    unsigned char* at = buffers + (size_t)groups * bytes;
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&vec_bar, (uint32_t)vectors * H * 4);
+    const auto keep = [&](const float*& src) {
+      if (!src) return;
+      if (threadIdx.x == 0) bulk_g2s(at, src, (uint32_t)H * 4, &vec_bar);
+      src = reinterpret_cast<const float*>(at);
+      at += (size_t)H * 4;
+    };
+    keep(post.w);
+    keep(post.b);
+    keep(pre.w);
+    keep(pre.b);
+    __syncthreads();
+  }
+  unsigned char* mine = buffers + (size_t)g * bytes;
+  const int stride = gridDim.x * groups;
+  uint32_t issued = 0;  // copies that this thread has asked for
+  const auto fetch = [&](int row) {
+    ++issued;
+    mbar_arrive_expect_tx(&full[g], bytes);
+    bulk_g2s(mine, p.x + (size_t)row * p.ldx, xb, &full[g]);
+    if (yb) bulk_g2s(mine + xb, p.y + (size_t)row * p.ldy, yb, &full[g]);
+    if (gb) bulk_g2s(mine + xb + yb, p.gate + (size_t)row * p.ldg, gb, &full[g]);
+  };
+  int row = blockIdx.x * groups + g;
+  if (c0 == 0 && row < p.T) fetch(row);
+  // a copy that never comes: the rows go on with what is there, no more are
+  // asked for, and the call is reported
+  volatile int* abort_p = &abort_flag;
+  if (vectors) mx4::wait_or_abort(&vec_bar, 0, abort_p, p.status);
+  RowSum sum{red[g], p.tpr, 0, g + 1};
+  bool bad = false;
+  const char* xs = reinterpret_cast<const char*>(mine);
+  const char* ys = xs + xb;
+  for (uint32_t parity = 0; row < p.T; row += stride, parity ^= 1) {
+    mx4::wait_or_abort(&full[g], parity, abort_p, p.status);
+    float v[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      raw[i] = {};
-      if ((c0 + i * p.tpr) * 8 < H) raw[i] = load8(yr, c0 + i * p.tpr, p.yt);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) widen(raw[i], p.yt, v[i]);
-    normalize<V>(v, p.post, H, c0, p.tpr, sum);
-    if (p.gate_kind != QSM_GATE_NONE) {
-      const char* gr = p.gate + (size_t)row * p.ldg;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = c0 + i * p.tpr;
-        if (c * 8 >= H) continue;
-        float g[8];
-        if (p.gate_kind == QSM_GATE_TOKENS) {
-          float one;
-          if (p.gt == QSM_FP32) one = *reinterpret_cast<const float*>(gr);
-          else if (p.gt == QSM_BF16) one = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(gr));
-          else one = __half2float(*reinterpret_cast<const __half*>(gr));
-#pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = one;
-        } else {
-          widen(load8(gr, c, p.gt), p.gt, g);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= p.sigmoid ? 1.0f / (1.0f + expf(-g[j])) : g[j];
+      const int c = c0 + i * p.tpr;
+      if (p.y) {
+        Raw<YT> y = {};
+        if (c * 8 < H) y = load8<YT>(ys, c);
+        widen<YT>(y, v[i]);
+      } else {
+        Raw<XT> x = {};
+        if (c * 8 < H) x = load8<XT>(xs, c);
+        widen<XT>(x, v[i]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float x[8];
-      widen(xraw[i], p.xt, x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = fmaf(p.scale, v[i][j], x[j]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) widen(xraw[i], p.xt, v[i]);
+    one_row<V, XT>(p, post, pre, gb ? ys + yb : p.gate + (size_t)row * p.ldg, row, c0, v, sum, bad,
+                   [&](int i, float (&u)[8]) {
+                     Raw<XT> x = {};
+                     if ((c0 + i * p.tpr) * 8 < H) x = load8<XT>(xs, c0 + i * p.tpr);
+                     widen<XT>(x, u);
+                   },
+                   [&] {
+                     sum.sync();
+                     if (c0 == 0 && row + (long long)stride < p.T && !*abort_p) fetch(row + stride);
+                   });
   }
-  if (p.xo) {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if ((c0 + i * p.tpr) * 8 < H) store8(p.xo + (size_t)row * p.ldo, c0 + i * p.tpr, p.xt, v[i]);
-  }
-  if (!p.h) return;
-  normalize<V>(v, p.pre, H, c0, p.tpr, sum);
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = c0 + i * p.tpr;
-    if (p.ht == QSM_MXFP4) store_mx4(p, row, c, v[i], bad);
-    else if (c * 8 < H) store8(p.h + (size_t)row * p.ldh, c, p.ht, v[i]);
+  for (; row < p.rows; row += stride) pad_row(p, row, c0);
+  if (*abort_p) {  // the copies in flight land before the CTA leaves
+    if (issued) mbar_wait_bounded(&full[g], (issued - 1) & 1, kWaitIters);
+    if (vectors) mbar_wait_bounded(&vec_bar, 0, kWaitIters);
   }
   if (bad) set_status(p.status, QSM_DEV_NONFINITE);
 }
@@ -305,6 +439,39 @@ bool overlap(const Rows& a, const Rows& b, int T) {
   return !(d >= a.bytes && d + b.bytes <= a.ld);
 }
 bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.ld == b.ld && a.bytes == b.bytes; }
+
+// Which kernel.  The few-row one has many warps on an SM and starts at once, but
+// each of them goes through a row's latencies alone: from 3 M values on (1216
+// rows of 2048: 6.9 us against 7.5; 2432: 14.2 against 13.0; 4864 of 1024: 13.5
+// against 10.7) the other is faster, unless a fourth of its lanes' chunks lie
+// past the row (9728 rows of 512: 13.4 against 15.1).
+template <int XT, int YT>
+qsm_status launch(Params& p, cudaStream_t stream) {
+  const int chunks = p.H / 8, sms = mx4::sm_count();
+  const auto threads = [&](int v) { return ((chunks + v - 1) / v + 31) / 32 * 32; };
+  const int v = threads(4) <= kRowsThreads && 4 * threads(4) < 8 * threads(8) ? 4 : 8;
+  const bool many = (long long)p.T * p.H > kManyValues && 4 * chunks >= 3 * v * threads(v);
+  if (!many && chunks <= 1024) {
+    p.tpr = threads(1);
+    const int per = p.tpr == 32 ? kWarpRows : 1;
+    QSM_CUDA_TRY(launch_pdl(row_kernel<XT, YT>, dim3((p.rows + per - 1) / per), dim3(p.tpr * per), 0, stream, p));
+    return QSM_OK;
+  }
+  p.tpr = threads(v);
+  const size_t row = (size_t)p.H * ((XT == QSM_FP32 ? 4 : 2) + (p.y ? YT == QSM_FP32 ? 4 : 2 : 0) +
+                                    (gate_rows(p) ? p.gt == QSM_FP32 ? 4 : 2 : 0));
+  int groups = kRowsThreads / p.tpr;
+  while (groups > 1 && groups * row > kBuffers) --groups;
+  int ctas = (p.rows + groups - 1) / groups;
+  if (ctas > sms) ctas = sms;
+  int vectors = (p.post.w != nullptr) + (p.post.b != nullptr) + (p.pre.w != nullptr) + (p.pre.b != nullptr);
+  if (groups * row + (size_t)vectors * p.H * 4 > kBuffers) vectors = 0;  // they stay in global memory
+  const size_t smem = groups * row + (size_t)vectors * p.H * 4;
+  auto* kernel = v == 4 ? rows_kernel<4, XT, YT> : rows_kernel<8, XT, YT>;
+  QSM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBuffers));
+  QSM_CUDA_TRY(launch_pdl(kernel, dim3(ctas), dim3(p.tpr * groups), smem, stream, p, groups, vectors));
+  return QSM_OK;
+}
 
 }  // namespace
 }  // namespace rnorm
@@ -392,16 +559,15 @@ extern "C" qsm_status residual_norm(const qsm_residual_norm* n, int32_t T, const
   p.post = {n->post.kind, n->post.eps, n->post.weight, n->post.bias};
   p.pre = {n->pre.kind, n->pre.eps, n->pre.weight, n->pre.bias};
   p.status = dev_status;
-  // Few rows: one chunk a thread, the shortest way through a row; many rows:
-  // as many chunks as registers hold, fewer barriers and more loads in flight.
-  const int chunks = H / 8;
-  int v = T <= mx4::sm_count() ? 1 : 4;
-  while ((chunks + v - 1) / v > max_threads(v)) v *= 2;
-  while (v > 1 && (chunks + v - 1) / v <= 16) v /= 2;
-  p.tpr = ((chunks + v - 1) / v + 31) / 32 * 32;
-  const int per = p.tpr == 32 ? kWarpRows : 1;
-  const dim3 grid((p.rows + per - 1) / per), block(p.tpr * per);
-  auto* kernel = v == 1 ? residual_norm_kernel<1> : v == 2 ? residual_norm_kernel<2> : residual_norm_kernel<4>;
-  QSM_CUDA_TRY(launch_pdl(kernel, grid, block, 0, stream, p));
-  return QSM_OK;
+  switch (3 * n->x_dtype + (y ? n->y_dtype : n->x_dtype)) {
+    case 0: return launch<QSM_BF16, QSM_BF16>(p, stream);
+    case 1: return launch<QSM_BF16, QSM_FP16>(p, stream);
+    case 2: return launch<QSM_BF16, QSM_FP32>(p, stream);
+    case 3: return launch<QSM_FP16, QSM_BF16>(p, stream);
+    case 4: return launch<QSM_FP16, QSM_FP16>(p, stream);
+    case 5: return launch<QSM_FP16, QSM_FP32>(p, stream);
+    case 6: return launch<QSM_FP32, QSM_BF16>(p, stream);
+    case 7: return launch<QSM_FP32, QSM_FP16>(p, stream);
+    default: return launch<QSM_FP32, QSM_FP32>(p, stream);
+  }
 }

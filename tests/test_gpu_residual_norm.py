@@ -126,6 +126,34 @@ def test_four_bits(qsm, T, H):
     check_codes(h, None, wh, eh)
 
 
+@pytest.mark.parametrize("post,pre,gate", [("rms", "rms", "none"), (None, "layer", "full"), ("layer", None, "channel"), (None, "rms", "token")])
+@pytest.mark.parametrize("T,H", [(4096, 1024), (1700, 2048), (3400, 1000), (800, 5120), (200, 16384), (1, 16384)])
+def test_many_rows(qsm, T, H, post, pre, gate):
+    """Rows that follow one another through the same threads; in place, too."""
+    for xt, yt, gt in ((torch.bfloat16, torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32, torch.float32)):
+        x, y = draw((T, H), T + H, xt), draw((T, H), T + H + 1, yt)
+        g = gate_of(gate, T, H, 5, gt)
+        npost, rpost = side(qsm, post, H, 10)
+        npre, rpre = side(qsm, pre, H, 20, bias=pre == "layer")
+        n = qsm.ResidualNorm(H, pre=npre, post=npost, scale=0.22)
+        (wx, ex), wh = ref.residual(x, y, g, n.scale, rpost, rpre)
+        xo, h = n(x, y, g)
+        assert ref.lies_between(xo, wx, ex) and (h is None or ref.lies_between(h, *wh))
+        n(x, y, g, x_out=x, h=None if h is None else y)
+        assert torch.equal(x, xo) and (h is None or torch.equal(y, h))
+
+
+@pytest.mark.parametrize("T,H", [(1700, 2048), (3401, 1024), (200, 16384)])
+def test_four_bits_of_many_rows(qsm, T, H):
+    x = draw((T, H), 6, torch.bfloat16)
+    npre, rpre = side(qsm, "rms", H, 60)
+    out = qsm.Mx4Tensor.empty(T, H)
+    out.scales.fill_(77)
+    _, h = qsm.ResidualNorm(H, pre=npre)(x, h=out)
+    _, (wh, eh) = ref.residual(x, None, None, 1.0, None, rpre)
+    check_codes(h, None, wh, eh)
+
+
 def test_large_values_sum_in_range(qsm):
     # squares of 1e4 over 4096 columns, an offset a thousand times the spread: the centred sum keeps it
     H = 4096
