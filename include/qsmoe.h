@@ -188,7 +188,7 @@ typedef enum { QSM_SCORE_SOFTMAX = 0, QSM_SCORE_SIGMOID = 1 } qsm_score;
  *       largest biased scores, the groups_kept best groups stay; 1, 1, 1: no groups
  *   renormalize  1: the weights are divided by their sum
  *   scale  factor of the weights, finite
- *   w_split  the weights as moe_router_split writes them
+ *   w_split  the weights as moe_router_split writes them (for this H and E)
  *   bias  [E] fp32 or NULL, added to the scores for the choice only.  -infinity
  *       closes an expert: it is taken after all others, with weight 0. */
 typedef struct {
@@ -199,8 +199,9 @@ typedef struct {
   const float* bias;
 } qsm_router;
 
-/* Bytes of w_split, and the exact split of w_router [E, H] fp32 into three
- * bf16 parts (once per weight).  H a multiple of 64; both 16-byte aligned. */
+/* Bytes of w_split (0: not supported), and the exact split of w_router [E, H]
+ * fp32 into three bf16 parts, in the order that the kernel reads (once per weight).
+ * H a multiple of 64, E <= 512; both 16-byte aligned. */
 QSM_API size_t moe_router_split_bytes(int32_t E, int32_t H);
 QSM_API qsm_status moe_router_split(const float* w_router, int32_t E, int32_t H, uint16_t* w_split,
                                     cudaStream_t stream);

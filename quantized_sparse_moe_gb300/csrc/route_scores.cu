@@ -24,11 +24,14 @@
 // share of the tile's tokens: a warp reads a token's slices through
 // distributed shared memory, adds them in slice order, and selects.  The
 // call needs no workspace and leaves nothing behind.
-#include "mx4_common.cuh"
+//
+// The split weights lie in the order in which a CTA takes them: for each 64
+// columns and each 128 experts the three parts, 128 x 64 each, in the image
+// that the MMA reads (rows of 128 bytes, 16-byte unit u of row r at u ^ (r & 7)), so
+// that a step's 48 KB are one plain bulk copy.  Missing experts are zeros.
+#include "mx4_digits.cuh"
 
 namespace qsm {
-qsm_status route_split_launch(const float* w, size_t n, void* out, cudaStream_t stream);
-
 namespace rscores {
 namespace {
 
@@ -44,15 +47,47 @@ constexpr int kEpiWarp = 4;              // first of eight (or four) warps that 
 
 struct Params {
   CUtensorMap x;  // [T, H] bf16, box {64, nt}
-  CUtensorMap w;  // [3 E, H] bf16, box {64, 128}
+  const unsigned char* w;  // the split weights
   const float* bias;
-  int T, H, E, k, nt, ks, stages;
+  int T, H, E, k, nt, ks, stages, scratch;  // scratch: offset of the warps' own
   int sigmoid, groups, kept, best, gsize, renorm;
+  mx4::FastDiv gdiv;  // by gsize
   float scale;
   int32_t* idx;
   float* wts;
   int32_t* status;
 };
+
+int row_blocks(int E) { return E <= BM ? 1 : E <= 2 * BM ? 2 : 4; }
+
+// The split of w_router [E, H]: a thread has eight columns of a row.
+__global__ void __launch_bounds__(256)
+split_kernel(const float* __restrict__ w, int E, int H, int mb, unsigned char* __restrict__ out, long long units) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long u = blockIdx.x * 256ll + threadIdx.x;
+  if (u >= units) return;
+  const int c8 = (int)(u % (H / 8)), e = (int)(u / (H / 8));  // eight columns, row (of all blocks)
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (e < E) {
+    const float4* src = reinterpret_cast<const float4*>(w + (size_t)e * H) + 2 * c8;
+    const float4 a = __ldg(src), b = __ldg(src + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  const int r = e % BM, step = c8 / (BK / 8), unit = c8 % (BK / 8);
+  unsigned char* dst = out + ((size_t)step * mb + e / BM) * 3 * kPartBytes + r * 128 + ((unit ^ (r & 7)) << 4);
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+    uint32_t o[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat16 h = __float2bfloat16_rn(v[i]);
+      v[i] -= __bfloat162float(h);  // exact
+      o[i / 2] |= (uint32_t)__bfloat16_as_ushort(h) << (16 * (i & 1));
+    }
+    *reinterpret_cast<uint4*>(dst + (size_t)part * kPartBytes) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
 
 // bf16 A and B (K-major), fp32 D, M = 128.
 __device__ __forceinline__ uint32_t idesc_bf16(int n) {
@@ -81,137 +116,231 @@ __device__ __forceinline__ void sort_desc(unsigned long long* c) {
   }
 }
 
-// One token by one warp.  l: its logits, expert 128 m + 4 lane + j at
-// l[4 m + j]; sc: the warp's scratch [E]; grp: the groups of the lane's
-// experts.
+// The expert at position i of lane `lane`: a lane has four that follow one
+// another of every 128.
+__device__ __forceinline__ int expert_at(int i, int lane) { return 128 * (i >> 2) + 4 * lane + (i & 3); }
+
+// A warp's scratch, in floats: one for each of the 128 MB experts, the ids and the
+// order keys of the taken ones, and (up to 256 experts) the lanes' sorted lists.
 template <int MB>
-__device__ __forceinline__ void select_token(const Params& p, float (&l)[4 * MB], const int (&grp)[4 * MB],
-                                             float* sc, int lane, size_t t) {
+__host__ __device__ constexpr int scratch_floats() {
+  return 128 * MB + 2 * kMaxK + (MB <= 2 ? 2 * 128 * MB : 0);
+}
+
+// What a lane knows of its experts, once for all tokens.
+template <int MB>
+struct Experts {
+  float bias[4 * MB];   // -infinity for those that are closed
+  uint32_t group[MB];   // four groups, a byte each
+  uint32_t in;          // bit i: there is such an expert
+  int per, plog, start; // group values: lanes per group, its logarithm, and where this lane starts
+};
+
+template <int MB>
+__device__ __forceinline__ Experts<MB> load_experts(const Params& p, int lane) {
+  Experts<MB> x;
+  x.in = 0;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4 * MB; ++i) {
+    const int e = expert_at(i, lane);
+    x.bias[i] = 0.f;
+    if (e < p.E) {
+      x.in |= 1u << i;
+      if (p.bias) x.bias[i] = __ldg(p.bias + e);
+      if (!(x.bias[i] < INFINITY)) {  // +infinity or NaN
+        bad = true;
+        x.bias[i] = -INFINITY;
+      }
+    }
+    if ((i & 3) == 0) x.group[i >> 2] = 0;
+    x.group[i >> 2] |= (uint32_t)min((int)p.gdiv.div(e), 31) << (8 * (i & 3));
+  }
+  if (bad) set_status(p.status, QSM_DEV_NONFINITE);
+  x.plog = 5;
+  while ((p.groups << x.plog) > 32 || (1 << x.plog) > p.gsize) --x.plog;
+  x.per = 1 << x.plog;
+  const int at = (lane & (x.per - 1)) + (lane >> x.plog);
+  x.start = at - (int)p.gdiv.div(at) * p.gsize;
+  return x;
+}
+
+// One token by one warp.  l: its logits, in the order of expert_at; sc: the
+// warp's scratch.  dry: goes through the motions and writes nothing.
+template <int MB>
+__device__ __forceinline__ void select_token(const Params& p, const Experts<MB>& x, float (&l)[4 * MB], float* sc,
+                                             int lane, size_t t, bool dry) {
   constexpr int N = 4 * MB;
   constexpr uint32_t kAll = 0xffffffffu;
-  const auto expert = [&](int i) { return 128 * (i >> 2) + 4 * lane + (i & 3); };
-  bool bad = false;
-  uint32_t fine = 0;  // finite logits of experts that exist
+  unsigned long long* taken = reinterpret_cast<unsigned long long*>(sc + 128 * MB);
+  uint32_t fine = x.in;
+  float zero[MB];  // NaN when a logit is not finite
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const bool in = expert(i) < p.E, ok = isfinite(l[i]);
-    if (in && ok) fine |= 1u << i;
-    bad |= in && !ok;
+    if (!((x.in >> i) & 1u)) l[i] = 0.f;
+    zero[i >> 2] = (i & 3) ? fmaf(l[i], 0.f, zero[i >> 2]) : l[i] * 0.f;
+  }
+#pragma unroll
+  for (int b = 1; b < MB; ++b) zero[0] += zero[b];
+  if (__any_sync(kAll, zero[0] != 0.f)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!isfinite(l[i])) {
+        fine &= ~(1u << i);
+        l[i] = 0.f;
+      }
+    if (lane == 0 && !dry) set_status(p.status, QSM_DEV_NONFINITE);
   }
   float s[N];
   if (p.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = (fine >> i) & 1u ? 1.0f / (1.0f + expf(-l[i])) : 0.f;
+    for (int i = 0; i < N; ++i) s[i] = __fdividef(1.0f, 1.0f + __expf(-l[i]));
   } else {
     float top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if ((fine >> i) & 1u) top = fmaxf(top, l[i]);
-    top = warp_max(top);
+    top = key_value(__reduce_max_sync(kAll, order_key(top)));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      s[i] = (fine >> i) & 1u ? expf(l[i] - top) : 0.f;
+      s[i] = (fine >> i) & 1u ? __expf(l[i] - top) : 0.f;
       sum += s[i];
     }
     sum = warp_sum(sum);
-    if (sum > 0.f) {
+    const float inv = sum > 0.f ? __fdividef(1.0f, sum) : 0.f;  // 1 .. E
 #pragma unroll
-      for (int i = 0; i < N; ++i) s[i] /= sum;
-    }
+    for (int i = 0; i < N; ++i) s[i] *= inv;
   }
   float c[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int e = expert(i);
-    c[i] = -INFINITY;
-    if ((fine >> i) & 1u) {
-      c[i] = p.bias ? s[i] + __ldg(p.bias + e) : s[i];
-      if (!(c[i] < INFINITY)) {  // a bias that is +infinity or NaN
-        bad = true;
-        c[i] = -INFINITY;
-      }
-    }
+    const bool ok = (fine >> i) & 1u;
+    if (!ok) s[i] = 0.f;
+    c[i] = ok ? s[i] + x.bias[i] : -INFINITY;
   }
-  if (__any_sync(kAll, bad) && lane == 0) set_status(p.status, QSM_DEV_NONFINITE);
 
-  uint32_t keep = kAll;  // bit g: group g stays
+  uint32_t allowed = x.in;  // bit i: expert i of this lane may be taken
   if (p.kept < p.groups) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (expert(i) < p.E) sc[expert(i)] = c[i];
+    for (int b = 0; b < MB; ++b)
+      reinterpret_cast<float4*>(sc)[32 * b + lane] = make_float4(c[4 * b], c[4 * b + 1], c[4 * b + 2], c[4 * b + 3]);
     __syncwarp();
     // `per` lanes a group (a power of two) look through its experts, from
     // different places so that their reads fall into different banks
-    int per = 32;
-    while (per * p.groups > 32) per >>= 1;
-    const int g = lane / per, q = lane - g * per;
+    const int g = lane >> x.plog;
     float a = -INFINITY, b = -INFINITY;
-    if (g < p.groups)
-      for (int j = q, at = (q + g) % p.gsize; j < p.gsize; j += per) {
-        best_two(a, b, sc[g * p.gsize + at], -INFINITY);
-        at += per;
-        if (at >= p.gsize) at %= p.gsize;
+    if (g < p.groups) {
+      const float* gc = sc + g * p.gsize;
+      int at = x.start;
+#pragma unroll 4
+      for (int j = lane & (x.per - 1); j < p.gsize; j += x.per) {
+        best_two(a, b, gc[at], -INFINITY);
+        at += x.per;
+        if (at >= p.gsize) at -= p.gsize;
       }
-    for (int o = 1; o < per; o <<= 1) {
+    }
+    for (int o = 1; o < x.per; o <<= 1) {
       const float c2 = __shfl_xor_sync(kAll, a, o), d2 = __shfl_xor_sync(kAll, b, o);
       best_two(a, b, c2, d2);
     }
     const float value = p.best == 2 ? a + b : a;
     int rank = 0;
+#pragma unroll 4
     for (int o = 0; o < p.groups; ++o) {
-      const float v = __shfl_sync(kAll, value, o * per);
+      const float v = __shfl_sync(kAll, value, o << x.plog);
       rank += v > value || (v == value && o < g);
     }
-    const uint32_t in = __ballot_sync(kAll, g < p.groups && q == 0 && rank < p.kept);
-    keep = 0;
-    for (int o = 0; o < p.groups; ++o) keep |= ((in >> (o * per)) & 1u) << o;
-    __syncwarp();
+    // lane o finds out about group o
+    const uint32_t in = __ballot_sync(kAll, g < p.groups && rank < p.kept);
+    const uint32_t keep = __ballot_sync(kAll, lane < p.groups && ((in >> ((lane << x.plog) & 31)) & 1u));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!((keep >> ((x.group[i >> 2] >> (8 * (i & 3))) & 31)) & 1u)) allowed &= ~(1u << i);
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (expert(i) < p.E) sc[expert(i)] = s[i];
+  for (int b = 0; b < MB; ++b)
+    reinterpret_cast<float4*>(sc)[32 * b + lane] = make_float4(s[4 * b], s[4 * b + 1], s[4 * b + 2], s[4 * b + 3]);
 
-  unsigned long long key[N];  // (order of c, ~expert): a strict order; 0 where there is none
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const bool in = expert(i) < p.E && ((keep >> grp[i]) & 1u);
-    key[i] = in ? ((unsigned long long)order_key(c[i]) << 32) | (uint32_t)~expert(i) : 0ull;
-  }
+  // The k rounds take the best head of the lanes' sorted lists.  Two lanes with
+  // the same key are rare: the first time through, a round only notes that it
+  // saw them (the vote is not waited for), and then all is done again with care.
   constexpr int kList = N < 8 ? N : 8;
+#pragma unroll 1
+  for (int careful = 0; careful < 2; ++careful) {
+    unsigned long long key[N];  // (order of c, ~expert): a strict order; 0 where there is none
 #pragma unroll
-  for (int n = 0; n < N; n += kList) sort_desc<kList>(key + n);
-  int my_e = 0;
-  float my_c = -INFINITY;
-  for (int j = 0; j < p.k; ++j) {
-    unsigned long long head = key[0];
-    if constexpr (N > 8) head = key[0] > key[8] ? key[0] : key[8];
-    const uint32_t hk = (uint32_t)(head >> 32), hi = (uint32_t)head;
-    const uint32_t mk = __reduce_max_sync(kAll, hk);
-    const uint32_t mi = __reduce_max_sync(kAll, hk == mk ? hi : 0u);
-    if (hk == mk && hi == mi) {  // this lane's: drop it
-      if (N <= 8 || key[0] == head) {
+    for (int i = 0; i < N; ++i)
+      key[i] = (allowed >> i) & 1u ? ((unsigned long long)order_key(c[i]) << 32) | (uint32_t)~expert_at(i, lane) : 0ull;
 #pragma unroll
-        for (int i = 0; i < kList - 1; ++i) key[i] = key[i + 1];
-        key[kList - 1] = 0ull;
+    for (int n = 0; n < N; n += kList) sort_desc<kList>(key + n);
+    uint32_t twice = 0;
+    // Whether this lane's head is the best one.  (Ties dropped by several lanes can
+    // empty all lists before round k: a head of 0 is none, and never the best.)
+    const auto best = [&](unsigned long long head) {
+      const uint32_t hk = (uint32_t)(head >> 32);
+      const bool mine = hk == __reduce_max_sync(kAll, hk) && hk != 0;
+      const uint32_t who = __ballot_sync(kAll, mine);
+      twice |= who & (who - 1);
+      return mine;
+    };
+    const auto one_of = [&](bool mine, unsigned long long head) {
+      return (uint32_t)head == __reduce_max_sync(kAll, mine ? (uint32_t)head : 0u) && mine;
+    };
+    if constexpr (N <= 8) {  // the lists lie in shared memory: a round reads one key, in place of moving eight
+      unsigned long long* next = reinterpret_cast<unsigned long long*>(sc + 128 * MB + 2 * kMaxK) + lane;
+#pragma unroll
+      for (int i = 1; i < N; ++i) next[32 * (i - 1)] = key[i];
+      next[32 * (N - 1)] = 0ull;
+      unsigned long long head = key[0];
+      if (!careful) {
+#pragma unroll 4
+        for (int j = 0; j < p.k; ++j)
+          if (best(head)) {
+            taken[j] = head;
+            head = *next;
+            next += 32;
+          }
       } else {
+#pragma unroll 1
+        for (int j = 0; j < p.k; ++j)
+          if (one_of(best(head), head)) {
+            taken[j] = head;
+            head = *next;
+            next += 32;
+          }
+      }
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < p.k; ++j) {
+        const bool second = key[8] > key[0];  // the head is the second list's
+        const unsigned long long head = second ? key[8] : key[0];
+        bool mine = best(head);
+        if (careful) mine = one_of(mine, head);
+        if (mine) taken[j] = head;
 #pragma unroll
-        for (int i = N - kList; i < N - 1; ++i) key[i] = key[i + 1];
-        key[N - 1] = 0ull;
+        for (int n = 0; n < N; n += kList) {
+          const bool pop = mine && second == (n > 0);
+#pragma unroll
+          for (int i = n; i < n + kList; ++i) key[i] = !pop ? key[i] : i + 1 < n + kList ? key[i + 1] : 0ull;
+        }
       }
     }
-    if (lane == j) {
-      my_c = key_value(mk);
-      my_e = (int)~mi;
-    }
+    if (twice == 0) break;
   }
   __syncwarp();
   float w = 0.f;
-  if (lane < p.k && my_c > -INFINITY) w = sc[my_e];  // a closed expert has weight 0
-  if (p.renorm) {
-    const float sum = warp_sum(w);
-    w = sum > 0.f ? w / sum : 0.f;
-  }
+  int my_e = 0;
   if (lane < p.k) {
+    const unsigned long long mine = taken[lane];
+    my_e = min((int)~(uint32_t)mine & 0x7fffffff, 128 * MB - 1);  // (always less than E)
+    if (key_value((uint32_t)(mine >> 32)) > -INFINITY) w = sc[my_e];  // a closed expert has weight 0
+  }
+  if (p.renorm) {
+    float sum = w;
+    for (int o = 1; o < p.k; o <<= 1) sum += __shfl_xor_sync(kAll, sum, o);  // the lanes from k on hold zeros
+    w = sum > 1e-30f ? __fdividef(w, sum) : sum > 0.f ? w / sum : 0.f;
+  }
+  if (lane < p.k && !dry) {
     p.idx[t * p.k + lane] = my_e;
     p.wts[t * p.k + lane] = w * p.scale;
   }
@@ -230,7 +359,9 @@ route_scores_kernel(const __grid_constant__ Params p) {
   const int cta = (int)mx4::cluster_rank(), q = cta / MB, m = cta - q * MB;
   const int nt = p.nt, csize = p.ks * MB, tile = blockIdx.x / csize;
   const int stage_bytes = 3 * kPartBytes + nt * BK * 2;
-  const int cols = nt < 16 ? 32 : 2 * nt;  // of tensor memory
+  int cols = 32;  // of tensor memory
+  while (cols < 2 * nt) cols *= 2;
+  float* sc = reinterpret_cast<float*>(smem + p.scratch) + warp * scratch_floats<MB>();
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full_bar[s], 1);
@@ -240,7 +371,6 @@ route_scores_kernel(const __grid_constant__ Params p) {
     abort_flag = 0;
     fence_mbar_init();
     tc::prefetch_map(&p.x);
-    tc::prefetch_map(&p.w);
   }
   if (warp == 1) tc::tmem_alloc(&tmem_base, cols);
   tc::tc_fence_before();
@@ -252,115 +382,136 @@ route_scores_kernel(const __grid_constant__ Params p) {
   volatile int* abort_p = &abort_flag;
   const int all = p.H / BK, first = (int)((long long)all * q / p.ks);
   const int steps = (int)((long long)all * (q + 1) / p.ks) - first;
+  Experts<MB> experts;
+  if (warp != 0) experts = load_experts<MB>(p, lane);  // the copies' warp has no time for it yet
 
-  if (warp == 0) {
-    int st = 0;
-    for (int s = 0, round = 0; st < steps; ++st) {
-      if (round > 0 && !mx4::warp_wait(&empty_bar[s], (round - 1) & 1, abort_p, p.status)) break;
-      if (mx4::warp_aborted(abort_p)) break;
-      if (tc::elect_one()) {
-        unsigned char* sb = smem + s * stage_bytes;
-        mbar_arrive_expect_tx(&full_bar[s], stage_bytes);
+  const auto product = [&] {
+    if (warp == 0) {
+      int st = 0;
+      for (int s = 0, round = 0; st < steps; ++st) {
+        if (round > 0 && !mx4::warp_wait(&empty_bar[s], (round - 1) & 1, abort_p, p.status)) break;
+        if (mx4::warp_aborted(abort_p)) break;
+        if (tc::elect_one()) {
+          unsigned char* sb = smem + s * stage_bytes;
+          mbar_arrive_expect_tx(&full_bar[s], stage_bytes);
+          bulk_g2s(sb, p.w + ((size_t)(first + st) * MB + m) * 3 * kPartBytes, 3 * kPartBytes, &full_bar[s]);
+          tc::tma_load_2d(sb + 3 * kPartBytes, &p.x, (first + st) * BK, tile * nt, &full_bar[s]);
+        }
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          ++round;
+        }
+      }
+      if (mx4::warp_aborted(abort_p))  // the copies in flight land before the CTA leaves
+        for (int i = st > p.stages ? st - p.stages : 0; i < st; ++i)
+          mbar_wait_bounded(&full_bar[i % p.stages], (i / p.stages) & 1, kWaitIters);
+    } else if (warp == 1) {
+      const uint32_t idesc = idesc_bf16(nt);
+      int st = 0;
+      for (int s = 0, round = 0; st < steps; ++st) {
+        if (!mx4::warp_wait(&full_bar[s], round & 1, abort_p, p.status)) break;
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
+          const uint32_t a0 = smem_u32(smem + s * stage_bytes), b0 = a0 + 3 * kPartBytes;
 #pragma unroll
-        for (int part = 0; part < 3; ++part)
-          tc::tma_load_2d(sb + part * kPartBytes, &p.w, (first + st) * BK, part * p.E + m * BM, &full_bar[s]);
-        tc::tma_load_2d(sb + 3 * kPartBytes, &p.x, (first + st) * BK, tile * nt, &full_bar[s]);
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t b = tc::sw128_desc(b0 + kk * 32);
+            const uint32_t more = st > 0 || kk > 0;
+            tc::mma_f16(tmem + nt, tc::sw128_desc(a0 + 2 * kPartBytes + kk * 32), b, idesc, more);
+            tc::mma_f16(tmem + nt, tc::sw128_desc(a0 + kPartBytes + kk * 32), b, idesc, 1u);
+            tc::mma_f16(tmem, tc::sw128_desc(a0 + kk * 32), b, idesc, more);
+          }
+          tc::mma_commit(&empty_bar[s]);
+          if (st == steps - 1) tc::mma_commit(&done_bar);
+        }
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          ++round;
+        }
       }
-      __syncwarp();
-      if (++s == p.stages) {
-        s = 0;
-        ++round;
+      if (st < steps) {  // gave up: the MMAs in flight end before tensor memory is freed
+        if (tc::elect_one()) tc::mma_commit(&done_bar);
+        __syncwarp();
+        mbar_wait_bounded(&done_bar, 0, kWaitIters);
       }
-    }
-    if (mx4::warp_aborted(abort_p))  // the copies in flight land before the CTA leaves
-      for (int i = st > p.stages ? st - p.stages : 0; i < st; ++i)
-        mbar_wait_bounded(&full_bar[i % p.stages], (i / p.stages) & 1, kWaitIters);
-  } else if (warp == 1) {
-    const uint32_t idesc = idesc_bf16(nt);
-    int st = 0;
-    for (int s = 0, round = 0; st < steps; ++st) {
-      if (!mx4::warp_wait(&full_bar[s], round & 1, abort_p, p.status)) break;
+    } else if (warp >= kEpiWarp && warp < kEpiWarp + 8) {
+      // lane = expert, column = token: to [token][expert], over the stages
+      // (every MMA has completed)
+      const int quarter = warp & 3, half = (warp - kEpiWarp) >> 2;
+      const bool ok = mx4::warp_wait(&done_bar, 0, abort_p, p.status);
       tc::tc_fence_after();
-      if (tc::elect_one()) {
-        const uint32_t a0 = smem_u32(smem + s * stage_bytes), b0 = a0 + 3 * kPartBytes;
+      float* out = reinterpret_cast<float*>(smem) + 32 * quarter + lane;
+      const uint32_t taddr = tmem + ((uint32_t)(32 * quarter) << 16);
+      if (ok) {
+        for (int c = 16 * half; c < nt; c += 32) {
+          uint32_t hi[16], lo[16];
+          tc::tmem_ld16_nowait(taddr + c, hi);
+          tc::tmem_ld16_nowait(taddr + nt + c, lo);
+          tc::tmem_wait_ld(hi, lo);
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint64_t b = tc::sw128_desc(b0 + kk * 32);
-          const uint32_t more = st > 0 || kk > 0;
-          tc::mma_f16(tmem + nt, tc::sw128_desc(a0 + 2 * kPartBytes + kk * 32), b, idesc, more);
-          tc::mma_f16(tmem + nt, tc::sw128_desc(a0 + kPartBytes + kk * 32), b, idesc, 1u);
-          tc::mma_f16(tmem, tc::sw128_desc(a0 + kk * 32), b, idesc, more);
+          for (int i = 0; i < 16; ++i)
+            out[(c + i) * kRowFloats] = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
         }
-        tc::mma_commit(&empty_bar[s]);
-        if (st == steps - 1) tc::mma_commit(&done_bar);
-      }
-      __syncwarp();
-      if (++s == p.stages) {
-        s = 0;
-        ++round;
       }
     }
-    if (st < steps) {  // gave up: the MMAs in flight end before tensor memory is freed
-      if (tc::elect_one()) tc::mma_commit(&done_bar);
-      __syncwarp();
-      mbar_wait_bounded(&done_bar, 0, kWaitIters);
-    }
-  } else if (warp >= kEpiWarp && warp < kEpiWarp + 8) {
-    // lane = expert, column = token: to [token][expert], over the stages
-    // (every MMA has completed)
-    const int quarter = warp & 3, half = (warp - kEpiWarp) >> 2;
-    const bool ok = mx4::warp_wait(&done_bar, 0, abort_p, p.status);
-    tc::tc_fence_after();
-    float* out = reinterpret_cast<float*>(smem) + 32 * quarter + lane;
-    const uint32_t taddr = tmem + ((uint32_t)(32 * quarter) << 16);
-    if (ok) {
-      for (int c = 16 * half; c < nt; c += 32) {
-        uint32_t hi[16], lo[16];
-        tc::tmem_ld16_nowait(taddr + c, hi);
-        tc::tmem_ld16_nowait(taddr + nt + c, lo);
-        tc::tmem_wait_ld(hi, lo);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          out[(c + i) * kRowFloats] = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
-      }
-    }
-  }
-  tc::tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc::tc_fence_after();
-    tc::tmem_dealloc(tmem, cols);
-  }
-  cluster_sync_all();  // every slice of the tile is in its CTA's shared memory
+  };
 
-  // a CTA that gave up leaves no logits: its flag is read with them
-  const int per = nt / csize, rows = min(nt, p.T - tile * nt);
-  int aborted = 0;
-  for (int r = 0; r < csize; ++r) {
-    int f;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(f) : "r"(dsmem_addr(&abort_flag, r)) : "memory");
-    aborted |= f;
-  }
-  if (!aborted) {
-    int grp[4 * MB];
-#pragma unroll
-    for (int i = 0; i < 4 * MB; ++i) grp[i] = min((128 * (i >> 2) + 4 * lane + (i & 3)) / p.gsize, 31);
-    float* sc = reinterpret_cast<float*>(smem + (size_t)nt * kRowFloats * 4) + warp * p.E;
-    for (int i = warp; i < per; i += kWarps) {
-      const int row = cta * per + i;
-      if (row >= rows) break;
-      float l[4 * MB];
-      const uint32_t at = smem_u32(smem) + (row * kRowFloats + 4 * lane) * 4;
-#pragma unroll
-      for (int b = 0; b < MB; ++b) {
-        float4 a = dsmem_ld_f4(dsmem_addr_u32(at, b));
-        for (int s = 1; s < p.ks; ++s) {
-          const float4 v = dsmem_ld_f4(dsmem_addr_u32(at, s * MB + b));
-          a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-        }
-        l[4 * b] = a.x, l[4 * b + 1] = a.y, l[4 * b + 2] = a.z, l[4 * b + 3] = a.w;
+  // The selection stands here once and is gone through twice: first by the warps
+  // that have no part in the product, which fetch its code meanwhile, then
+  // by all.
+  int tokens = 0, row0 = 0, aborted = 0;  // this warp's, every kWarps-th row from row0 on
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    const bool dry = pass == 0;
+    if (dry) {
+      if (warp >= kEpiWarp + 8) tokens = 1;
+      else product();
+      if (warp == 0) experts = load_experts<MB>(p, lane);
+    } else {
+      tc::tc_fence_before();
+      __syncthreads();
+      if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, cols);
       }
-      select_token<MB>(p, l, grp, sc, lane, (size_t)tile * nt + row);
+      cluster_sync_all();  // every slice of the tile is in its CTA's shared memory
+      // a CTA that gave up leaves no logits: its flag is read with them
+      if (lane < csize)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(aborted) : "r"(dsmem_addr(&abort_flag, lane)) : "memory");
+      const int per = (nt + csize - 1) / csize;
+      const int rows = min(min(nt, p.T - tile * nt), (cta + 1) * per);
+      row0 = cta * per + warp;
+      tokens = row0 >= rows ? 0 : (rows - row0 + kWarps - 1) / kWarps;
+    }
+#pragma unroll 1
+    for (int i = 0; i < tokens; ++i) {
+      const int row = row0 + i * kWarps;
+      float l[4 * MB];
+#pragma unroll
+      for (int j = 0; j < 4 * MB; ++j) l[j] = 0.f;
+      if (!dry) {
+        const uint32_t at = smem_u32(smem) + (row * kRowFloats + 4 * lane) * 4;
+        for (int s0 = 0; s0 < p.ks; s0 += 4) {  // four slices' reads under way at once
+          float4 v[4][MB];
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+              if (s0 + s < p.ks) v[s][b] = dsmem_ld_f4(dsmem_addr_u32(at, (s0 + s) * MB + b));
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+              if (s0 + s < p.ks) {
+                l[4 * b] += v[s][b].x, l[4 * b + 1] += v[s][b].y;
+                l[4 * b + 2] += v[s][b].z, l[4 * b + 3] += v[s][b].w;
+              }
+        }
+      }
+      if (__any_sync(0xffffffffu, aborted)) break;
+      select_token<MB>(p, experts, l, sc, lane, (size_t)tile * nt + row, dry);
     }
   }
   cluster_sync_all();  // no CTA leaves while another still reads its slices
@@ -368,27 +519,7 @@ route_scores_kernel(const __grid_constant__ Params p) {
 
 // ---------------------------------------------------------------------- host
 
-struct Config {
-  int nt, ks, stages;
-  size_t smem;
-};
-
 constexpr size_t kSmem = 220 * 1024;  // dynamic, of the 227 KB; the rest is static
-
-// Stages and shared memory of a tile of nt tokens.
-bool fit(int nt, int E, Config* c) {
-  const size_t stage = 3 * kPartBytes + (size_t)nt * BK * 2;
-  const size_t rows = (size_t)nt * kRowFloats * 4 + (size_t)kWarps * E * 4;  // over the stages, later
-  if (rows + 1024 > kSmem) return false;
-  int stages = (int)((kSmem - 1024) / stage);
-  c->nt = nt;
-  c->stages = stages < kMaxStages ? stages : kMaxStages;
-  const size_t ring = (size_t)c->stages * stage;
-  c->smem = (ring > rows ? ring : rows) + 1024;
-  return c->stages >= 2;
-}
-
-int row_blocks(int E) { return E <= BM ? 1 : E <= 2 * BM ? 2 : 4; }
 
 bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
   tc::EncodeTiledFn fn = tc::encode_fn();
@@ -408,16 +539,79 @@ bool router_ok(const qsm_router* r) {
          (long long)r->groups_kept * (r->E / r->groups) >= r->k && r->scale > -INFINITY && r->scale < INFINITY;
 }
 
-long long tiles_of(int T, int nt) { return ((long long)T + nt - 1) / nt; }
+void* kernel_of(int mb) {
+  return mb == 1   ? reinterpret_cast<void*>(route_scores_kernel<1>)
+         : mb == 2 ? reinterpret_cast<void*>(route_scores_kernel<2>)
+                   : reinterpret_cast<void*>(route_scores_kernel<4>);
+}
 
-void choose(const qsm_router* r, int T, Config* out) {
+// Clusters of 16 CTAs have to be allowed, once per device and kernel.
+bool allow_large_clusters(int mb) {
+  static std::atomic<uint64_t> done[5];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < 64 && (done[mb].load() >> dev & 1u)) return true;
+  if (cudaFuncSetAttribute(kernel_of(mb), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  if (dev < 64) done[mb].fetch_or(1ull << dev);
+  return true;
+}
+
+// How a call is cut up: nt tokens a tile, the sum over H in ks slices.
+struct Config {
+  int nt, ks, stages, scratch;
+  long long tiles;
+  size_t smem;
+};
+
+// A cluster of ks x mb CTAs has a tile; the device holds so many at once (a
+// GB300: 76 of 2, 36 of 4, 15 of 8, 7 of 16), and with tiles for all of them a launch takes one
+// wave.  Least time, by what the parts of it measured: a CTA's copies (55 bytes a cycle),
+// reading the accumulators, selecting with sixteen warps, and the rest.
+Config choose(const qsm_router* r, int T) {
+  struct Kept {
+    int dev, T, H, E;
+    Config c;
+  };
+  static thread_local Kept kept[4];  // the last answers of this thread: asking takes longer than a small call
+  static thread_local unsigned turn = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return Config{};
+  for (const Kept& k : kept)
+    if (k.T == T && k.H == r->H && k.E == r->E && k.dev == dev) return k.c;
   const int mb = row_blocks(r->E), steps = r->H / BK;
-  const int most = 8 / mb;  // slices of a portable cluster
-  int nt = 16;
-  while (nt < 256 && tiles_of(T, nt) * 8 > mx4::sm_count()) nt *= 2;
-  while (!fit(nt, r->E, out)) nt /= 2;
-  out->ks = 1;
-  while (out->ks * 2 <= most && out->ks * 2 <= steps) out->ks *= 2;
+  Config best = {};
+  double least = 0;
+  static const int kSlices[] = {1, 2, 3, 4, 6, 8, 16};
+  const int most_ctas = allow_large_clusters(mb) ? 16 : 8;
+  for (int ks : kSlices) {
+    if (ks * mb > most_ctas || ks > steps) break;
+    const int resident = mx4::resident_clusters(kernel_of(mb), ks * mb, kThreads, (int)kSmem, (int)kSmem);
+    if (resident < 1) continue;
+    Config c = {};
+    const long long each = ((long long)T + resident - 1) / resident;
+    c.nt = each > 256 ? 256 : (int)(each + 15) / 16 * 16;
+    c.ks = ks;
+    c.tiles = ((long long)T + c.nt - 1) / c.nt;
+    const long long waves = (c.tiles + resident - 1) / resident;
+    const double us = (double)waves * (3.0 + (steps + ks - 1) / ks * (3 * kPartBytes + c.nt * BK * 2) / 105e3 + c.nt * 0.006 +
+                                       ((c.nt + ks * mb - 1) / (ks * mb) + kWarps - 1) / kWarps * 1.2 + 0.1 * ks);
+    if (best.nt == 0 || us < least) {
+      best = c;
+      least = us;
+    }
+  }
+  if (best.nt == 0) return best;
+  const int stage = 3 * kPartBytes + best.nt * BK * 2, rows = best.nt * kRowFloats * 4, sc = kWarps * 4 * (mb == 1 ? scratch_floats<1>() : mb == 2 ? scratch_floats<2>() : scratch_floats<4>());
+  int most = (int)((kSmem - 1024 - sc) / stage);
+  if (most > kMaxStages) most = kMaxStages;
+  best.stages = most;
+  best.scratch = most * stage > rows ? most * stage : rows;
+  best.smem = (size_t)best.scratch + sc + 1024;
+  kept[turn++ % 4] = {dev, T, r->H, r->E, best};
+  return best;
 }
 
 }  // namespace
@@ -425,16 +619,23 @@ void choose(const qsm_router* r, int T, Config* out) {
 }  // namespace qsm
 
 extern "C" size_t moe_router_split_bytes(int32_t E, int32_t H) {
-  return E < 1 || H < 1 ? 0 : (size_t)3 * E * H * 2;
+  using namespace qsm::rscores;
+  if (E < 1 || E > kMaxE || H < BK || H % BK) return 0;
+  return (size_t)(H / BK) * row_blocks(E) * 3 * kPartBytes;
 }
 
 extern "C" qsm_status moe_router_split(const float* w_router, int32_t E, int32_t H, uint16_t* w_split,
                                        cudaStream_t stream) {
   using namespace qsm;
-  if (E < 1 || H < rscores::BK || H % rscores::BK || !w_router || !w_split || !aligned16(w_router) ||
-      !aligned16(w_split))
+  using namespace qsm::rscores;
+  if (E < 1 || H < BK || H % BK || !w_router || !w_split || !aligned16(w_router) || !aligned16(w_split))
     return QSM_ERR_INVALID_ARGUMENT;
-  return route_split_launch(w_router, (size_t)E * H, w_split, stream);
+  if (E > kMaxE) return QSM_ERR_UNSUPPORTED;
+  const int mb = row_blocks(E);
+  const long long units = (long long)mb * BM * (H / 8);
+  QSM_CUDA_TRY(launch_pdl(split_kernel, dim3((unsigned)((units + 255) / 256)), dim3(256), 0, stream, w_router, (int)E,
+                          (int)H, mb, reinterpret_cast<unsigned char*>(w_split), units));
+  return QSM_OK;
 }
 
 extern "C" qsm_status moe_route_scores(const qsm_router* r, const uint16_t* x, int64_t ldx, int32_t T,
@@ -451,13 +652,13 @@ extern "C" qsm_status moe_route_scores(const qsm_router* r, const uint16_t* x, i
       ldx < r->H || ldx % 8)
     return QSM_ERR_INVALID_ARGUMENT;
   const int mb = row_blocks(r->E);
-  Config c;
-  choose(r, T, &c);
-  const long long ctas = tiles_of(T, c.nt) * c.ks * mb;
+  const Config c = choose(r, T);
+  if (c.nt == 0) return QSM_ERR_CUDA;
+  const long long ctas = c.tiles * c.ks * mb;
   if (ctas > 0x7fffffffll || ldx > (1ll << 38)) return QSM_ERR_UNSUPPORTED;
   Params p = {};
-  if (!make_map(&p.x, x, T, r->H, ldx, c.nt) || !make_map(&p.w, r->w_split, 3ull * r->E, r->H, r->H, BM))
-    return QSM_ERR_CUDA;
+  if (!make_map(&p.x, x, T, r->H, ldx, c.nt)) return QSM_ERR_CUDA;
+  p.w = reinterpret_cast<const unsigned char*>(r->w_split);
   p.bias = r->bias;
   p.T = T;
   p.H = r->H;
@@ -466,18 +667,20 @@ extern "C" qsm_status moe_route_scores(const qsm_router* r, const uint16_t* x, i
   p.nt = c.nt;
   p.ks = c.ks;
   p.stages = c.stages;
+  p.scratch = c.scratch;
   p.sigmoid = r->score == QSM_SCORE_SIGMOID;
   p.groups = r->groups;
   p.kept = r->groups_kept;
   p.best = r->group_best;
   p.gsize = r->E / r->groups;
+  p.gdiv = mx4::FastDiv(p.gsize);
   p.renorm = r->renormalize;
   p.scale = r->scale;
   p.idx = topk_idx;
   p.wts = topk_w;
   p.status = dev_status;
   auto* kernel = mb == 1 ? route_scores_kernel<1> : mb == 2 ? route_scores_kernel<2> : route_scores_kernel<4>;
-  QSM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
+  // (choose has allowed the kernel its shared memory and clusters)
   QSM_CUDA_TRY(launch_pdl_cluster(kernel, dim3((unsigned)ctas), dim3(kThreads), c.ks * mb, c.smem, stream, p));
   return QSM_OK;
 }

@@ -257,14 +257,6 @@ int k_slices(int H) { return H % (4 * BK) == 0 ? 4 : (H % (2 * BK) == 0 ? 2 : 1)
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 }  // namespace route_tc
 
-// The three parts of n weights (n % 4 == 0), one after another: 3 n bf16.
-qsm_status route_split_launch(const float* w, size_t n, void* out, cudaStream_t stream) {
-  using namespace route_tc;
-  QSM_CUDA_TRY(launch_pdl(split_kernel, dim3(sm_count_route()), dim3(256), 0, stream, w,
-                          static_cast<__nv_bfloat16*>(out), n));
-  return QSM_OK;
-}
-
 // [256-byte header, zero][split router weight 3*E*H bf16]
 size_t route_tc_workspace_bytes(int T, int H, int E) {
   using namespace route_tc;
@@ -282,8 +274,9 @@ qsm_status route_tc_launch(const uint16_t* x, const float* w_router,
   const int ntiles = (T + BM - 1) / BM;
   char* ws = static_cast<char*>(split_buf);
   __nv_bfloat16* split = reinterpret_cast<__nv_bfloat16*>(ws + 256);
-  const qsm_status st = route_split_launch(w_router, n, split, stream);
-  if (st != QSM_OK) return st;
+  const int nsm = sm_count_route();
+  QSM_CUDA_TRY(launch_pdl(split_kernel, dim3(nsm), dim3(256), 0, stream, w_router,
+                          split, n));
   Params p = {};
   if (!tc::make_map_2d(&p.xa, x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, T, H, BK, BM,
                        CU_TENSOR_MAP_SWIZZLE_128B) ||

@@ -110,7 +110,8 @@ def test_route_scores_refuses_bad_arguments():
     import quantized_sparse_moe_gb300 as qsm
     from quantized_sparse_moe_gb300 import block
     L = qsm.lib()
-    assert L.moe_router_split_bytes(8, 64) == 3 * 8 * 64 * 2 and L.moe_router_split_bytes(0, 64) == 0
+    assert L.moe_router_split_bytes(8, 64) == 3 * 128 * 64 * 2 and L.moe_router_split_bytes(0, 64) == 0
+    assert L.moe_router_split_bytes(300, 128) == 3 * 512 * 128 * 2 and L.moe_router_split_bytes(8, 96) == 0
     for a in ((None, 8, 64, P, None), (P, 8, 96, P, None), (P, 0, 64, P, None), (P, 8, 64, None, None),
               (P + 4, 8, 64, P, None), (P, 8, 64, P + 8, None)):
         assert L.moe_router_split(*a) == BAD

@@ -135,6 +135,25 @@ def test_ties_go_to_the_lower_index(qsm):
         assert ids[0].tolist() == [40, 41, 42, 43, 44, 45, 46, 47, 0, 1]
 
 
+@pytest.mark.parametrize("E", [1, 5, 33, 48, 128, 130, 256, 300, 512])
+def test_ties_of_many(qsm, E):
+    """Equal and two-valued scores: the lanes of a warp run out of experts at different times."""
+    H, T, k = 64, 21, min(E, 32)
+    x = torch.zeros(T, H, device="cuda")
+    x[:, 0] = 1
+    x = x.bfloat16()
+    w = torch.zeros(E, H, device="cuda")
+    ids, _ = qsm.moe_route_scores(x, qsm.MoERouter(w, k))
+    assert torch.equal(ids, torch.arange(k, device="cuda", dtype=torch.int32).expand(T, k))
+    for seed in range(3):
+        high = torch.rand(E, generator=gen(seed), device="cuda") < 0.3
+        w[:, 0] = torch.where(high, 1.0, -1.0)
+        ids, wt = qsm.moe_route_scores(x, qsm.MoERouter(w, k, "sigmoid", renormalize=False))
+        want = torch.sort((~high).int(), stable=True).indices[:k]
+        assert torch.equal(ids.long(), want.expand(T, k))
+        assert torch.allclose(wt[0], torch.sigmoid(w[want, 0]), rtol=1e-6)
+
+
 def test_closed_experts(qsm):
     T, H, E = 4, 256, 16
     x = torch.randn((T, H), generator=gen(2), device="cuda").to(torch.bfloat16)
