@@ -648,7 +648,8 @@ QSM_API qsm_status residual_norm(const qsm_residual_norm* n, int32_t T, const vo
  *   scale  [n] fp32 or NULL (1)
  *   ranks  [n] int32 or NULL (all `rank`): how many ranks of an adapter count,
  *          taken into 0 .. rank; the others are not used, whatever they hold
- * K a multiple of 8, rank a multiple of 8 and at most 128, N >= 1. */
+ * K a multiple of 8, rank a multiple of 8 and at most 128, N >= 1, both K and N at
+ * most 2^28. */
 typedef struct {
   int32_t n, rank, K, N;
   const uint16_t* a;

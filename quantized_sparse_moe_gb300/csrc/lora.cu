@@ -27,7 +27,7 @@
 // v is rounded for the second product: c v is split into bf16 parts, two of them
 // (2^-17 relative) for 16-bit outputs, which are rounded to 2^-9 anyway, three
 // (exact but for fp32's own rounding) for 32-bit ones.
-#include "mx4_common.cuh"
+#include "mx4_digits.cuh"
 
 namespace qsm {
 namespace lora {
@@ -37,6 +37,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 64;    // tokens
 constexpr int kMaxRank = 128;
+constexpr int kMaxSide = 1 << 28;  // of K and N
 
 struct Params {
   const uint16_t* x;
@@ -101,6 +102,297 @@ __host__ __device__ constexpr size_t smem_bytes(int rows) {
   return (a > b ? a : b) + (size_t)rows * Shape<RK>::kRanks * 4;
 }
 
+// Eight columns of y or out in one row, as they lie in memory.
+template <bool F32>
+struct Raw {
+  uint4 v[F32 ? 2 : 1];
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load_y(const Params& p, int64_t t, int n) {
+  Raw<F32> r;
+  r.v[0] = make_uint4(0, 0, 0, 0);
+  if (F32) r.v[F32] = make_uint4(0, 0, 0, 0);
+  if (!p.y || n >= p.N) return r;
+  const char* src = p.y + (t * p.ldy + n) * (F32 ? 4 : 2);
+  if (p.vec) {
+    r.v[0] = *reinterpret_cast<const uint4*>(src);
+    if (F32) r.v[F32] = reinterpret_cast<const uint4*>(src)[1];
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      w[e] = n + e >= p.N ? 0u
+             : F32        ? reinterpret_cast<const uint32_t*>(src)[e]
+                          : (uint32_t)reinterpret_cast<const uint16_t*>(src)[e];
+    if (F32) {
+      r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      r.v[F32] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+      r.v[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+  }
+  return r;
+}
+
+// out = y + d for eight columns; the MMAs of tiles 0 .. 3 hold two of them each,
+// at d[j][at] and d[j][at + 1].
+template <bool F32>
+__device__ __forceinline__ void store_out(const Params& p, int64_t t, int n, const Raw<F32>& y, const float (&d)[4][4],
+                                          int at) {
+  if (n >= p.N) return;
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(y.v);
+  uint32_t o[F32 ? 8 : 4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (F32) {
+      o[2 * j] = __float_as_uint(__uint_as_float(w[2 * j]) + d[j][at]);
+      o[2 * j + 1] = __float_as_uint(__uint_as_float(w[2 * j + 1]) + d[j][at + 1]);
+    } else {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(bf16_lo(w[j]) + d[j][at], bf16_hi(w[j]) + d[j][at + 1]);
+      o[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  char* dst = p.out + (t * p.ldo + n) * (F32 ? 4 : 2);
+  if (p.vec) {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    if (F32) reinterpret_cast<uint4*>(dst)[F32] = make_uint4(o[4 * F32], o[1 + 4 * F32], o[2 + 4 * F32], o[3 + 4 * F32]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (n + e < p.N) {
+        if (F32) reinterpret_cast<uint32_t*>(dst)[e] = o[e];
+        else reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+      }
+  }
+}
+
+// Sixteen ranks' rows of A (from r0 on), 8 columns at k: an MMA's rows g and g + 8.
+__device__ __forceinline__ void load_a(const uint16_t* A, int K, int rank, int r0, int k, bool in, uint4& lo, uint4& hi) {
+  const int g = (threadIdx.x & 31) >> 2;
+  lo = hi = make_uint4(0, 0, 0, 0);
+  if (in && r0 + g < rank) lo = __ldg(reinterpret_cast<const uint4*>(A + (size_t)(r0 + g) * K + k));
+  if (in && r0 + 8 + g < rank) hi = __ldg(reinterpret_cast<const uint4*>(A + (size_t)(r0 + 8 + g) * K + k));
+}
+
+// 32 columns of B: tile j's column g is row n of it, and the lane has 8 ranks of
+// each block of 32.
+template <int RK>
+__device__ __forceinline__ void load_b(const Params& p, const uint16_t* B, int rank, int chunk, uint4 (&w)[4][RK]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = chunk * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
+#pragma unroll
+    for (int b = 0; b < RK; ++b) {
+      const int r = 32 * b + 8 * tq;
+      w[j][b] = make_uint4(0, 0, 0, 0);
+      if (n < p.N && r < rank) w[j][b] = first_of(__ldg(reinterpret_cast<const uint4*>(B + (size_t)n * p.R + r)), rank - r);
+    }
+  }
+}
+
+// The slot's tokens' share of v from this warp's blocks of K, into its partial
+// sums [token][rank].  At most 8 tokens: sixteen rows of A are under way at
+// once, of as many blocks as that makes.
+template <int RK>
+__device__ __forceinline__ void shrink_few(const Params& p, const uint16_t* A, int rank, const int* mem, int64_t t0, int m,
+                                           int kfirst, int klast, float* mine) {
+  using S = Shape<RK>;
+  constexpr int U = 4 / RK;
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  float acc[S::kRowTiles][4];
+#pragma unroll
+  for (int i = 0; i < S::kRowTiles; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+  const uint16_t* xr = g < m ? p.x + (t0 + mem[g]) * p.ldx : nullptr;
+#pragma unroll 1
+  for (int kb = kfirst; kb < klast; kb += U) {
+    uint4 xv[U], lo[U][S::kRowTiles], hi[U][S::kRowTiles];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (kb + u) * 32 + 8 * tq;
+      const bool in = kb + u < klast && k < p.K;
+      xv[u] = make_uint4(0, 0, 0, 0);
+      if (in && xr) xv[u] = __ldg(reinterpret_cast<const uint4*>(xr + k));
+#pragma unroll
+      for (int i = 0; i < S::kRowTiles; ++i) load_a(A, p.K, rank, 16 * i, k, in, lo[u][i], hi[u][i]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < S::kRowTiles; ++i) {
+        mma_bf16(acc[i], lo[u][i].x, hi[u][i].x, lo[u][i].y, hi[u][i].y, xv[u].x, xv[u].y);
+        mma_bf16(acc[i], lo[u][i].z, hi[u][i].z, lo[u][i].w, hi[u][i].w, xv[u].z, xv[u].w);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < S::kRowTiles; ++i) {
+    if (16 * i >= rank) break;
+    float* at = mine + 2 * tq * S::kPartRow + 16 * i + g;
+    at[0] = acc[i][0];
+    at[S::kPartRow] = acc[i][1];
+    at[8] = acc[i][2];
+    at[S::kPartRow + 8] = acc[i][3];
+  }
+}
+
+// The same for up to 8 kTokTiles tokens.
+template <int RK>
+__device__ __forceinline__ void shrink_many(const Params& p, const uint16_t* A, int rank, const int* mem, int64_t t0,
+                                            int m, int kfirst, int klast, float* mine) {
+  using S = Shape<RK>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  float acc[S::kRowTiles][S::kTokTiles][4];
+#pragma unroll
+  for (int i = 0; i < S::kRowTiles; ++i)
+#pragma unroll
+    for (int j = 0; j < S::kTokTiles; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+  int row[S::kTokTiles];
+#pragma unroll
+  for (int j = 0; j < S::kTokTiles; ++j) row[j] = 8 * j + g < m ? mem[8 * j + g] : -1;
+#pragma unroll 1
+  for (int kb = kfirst; kb < klast; ++kb) {
+    const int k = kb * 32 + 8 * tq;
+    const bool in = k < p.K;
+    uint4 xv[S::kTokTiles];
+#pragma unroll
+    for (int j = 0; j < S::kTokTiles; ++j) {
+      xv[j] = make_uint4(0, 0, 0, 0);
+      if (in && row[j] >= 0) xv[j] = __ldg(reinterpret_cast<const uint4*>(p.x + (t0 + row[j]) * p.ldx + k));
+    }
+#pragma unroll
+    for (int i = 0; i < S::kRowTiles; ++i) {
+      uint4 lo, hi;
+      load_a(A, p.K, rank, 16 * i, k, in, lo, hi);
+#pragma unroll
+      for (int j = 0; j < S::kTokTiles; ++j) {
+        mma_bf16(acc[i][j], lo.x, hi.x, lo.y, hi.y, xv[j].x, xv[j].y);
+        mma_bf16(acc[i][j], lo.z, hi.z, lo.w, hi.w, xv[j].z, xv[j].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < S::kRowTiles; ++i)
+#pragma unroll
+    for (int j = 0; j < S::kTokTiles; ++j) {
+      if (16 * i >= rank || 8 * j >= m) break;
+      float* at = mine + (8 * j + 2 * tq) * S::kPartRow + 16 * i + g;
+      at[0] = acc[i][j][0];
+      at[S::kPartRow] = acc[i][j][1];
+      at[8] = acc[i][j][2];
+      at[S::kPartRow + 8] = acc[i][j][3];
+    }
+}
+
+// This warp's columns of at most 8 tokens: v stays in registers, and the rows of B
+// of two chunks (one, for many ranks) and their y are under way at once.
+template <int RK, bool F32>
+__device__ __forceinline__ void expand_few(const Params& p, const uint16_t* B, int rank, const int* mem, int64_t t0, int m,
+                                           const __nv_bfloat16* vbuf, int vrows, int chunk0, int chunks, int stride) {
+  using S = Shape<RK>;
+  constexpr int SPLIT = F32 ? 3 : 2, U = RK == 1 ? 2 : 1;
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  const int64_t t = t0 + (g < m ? mem[g] : 0);
+  uint4 v[SPLIT][RK];
+#pragma unroll
+  for (int s = 0; s < SPLIT; ++s)
+#pragma unroll
+    for (int b = 0; b < RK; ++b) {
+      v[s][b] = make_uint4(0, 0, 0, 0);
+      if (32 * b < rank) v[s][b] = *reinterpret_cast<const uint4*>(vbuf + ((size_t)s * vrows + g) * S::kVRow + 32 * b + 8 * tq);
+    }
+#pragma unroll 1
+  for (int ch = chunk0; ch < chunks; ch += U * stride) {
+    uint4 w[U][4][RK];
+    Raw<F32> y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = ch + u * stride;  // past the end: no row of B, no column of y
+      load_b<RK>(p, B, rank, c, w[u]);
+      y[u] = load_y<F32>(p, t, g < m ? c * 32 + 8 * tq : p.N);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float d[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[j][e] = 0.f;
+#pragma unroll
+      for (int b = 0; b < RK; ++b)
+#pragma unroll
+        for (int s = SPLIT - 1; s >= 0; --s)  // the small parts first
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mma_bf16(d[j], v[s][b].x, 0u, v[s][b].y, 0u, w[u][j][b].x, w[u][j][b].y);
+            mma_bf16(d[j], v[s][b].z, 0u, v[s][b].w, 0u, w[u][j][b].z, w[u][j][b].w);
+          }
+      store_out<F32>(p, t, g < m ? (ch + u * stride) * 32 + 8 * tq : p.N, y[u], d, 0);
+    }
+  }
+}
+
+// This warp's columns of any number of tokens: v comes from shared memory, the
+// y of 64 tokens (32 of fp32) is under way at once.
+template <int RK, bool F32>
+__device__ __forceinline__ void expand_many(const Params& p, const uint16_t* B, int rank, const int* mem, int64_t t0,
+                                            int m, const __nv_bfloat16* vbuf, int vrows, int chunk0, int chunks,
+                                            int stride) {
+  using S = Shape<RK>;
+  constexpr int SPLIT = F32 ? 3 : 2, U = F32 || RK == 4 ? 2 : 4;
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+#pragma unroll 1
+  for (int ch = chunk0; ch < chunks; ch += stride) {
+    uint4 w[4][RK];
+    load_b<RK>(p, B, rank, ch, w);
+    const int n = ch * 32 + 8 * tq;  // this lane's eight columns of tokens g and g + 8
+#pragma unroll 1
+    for (int m0 = 0; m0 < m; m0 += 16 * U) {
+      Raw<F32> y[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = m0 + 16 * u + 8 * h + g;
+          y[u][h] = load_y<F32>(p, row < m ? t0 + mem[row] : 0, row < m ? n : p.N);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int mt = m0 + 16 * u;
+        if (mt >= m) break;
+        float d[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[j][e] = 0.f;
+#pragma unroll
+        for (int b = 0; b < RK; ++b) {
+          if (32 * b >= rank) break;
+#pragma unroll
+          for (int s = SPLIT - 1; s >= 0; --s) {
+            const __nv_bfloat16* vr = vbuf + ((size_t)s * vrows + mt + g) * S::kVRow + 32 * b + 8 * tq;
+            const uint4 lo = *reinterpret_cast<const uint4*>(vr), hi = *reinterpret_cast<const uint4*>(vr + 8 * S::kVRow);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              mma_bf16(d[j], lo.x, hi.x, lo.y, hi.y, w[j][b].x, w[j][b].y);
+              mma_bf16(d[j], lo.z, hi.z, lo.w, hi.w, w[j][b].z, w[j][b].w);
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = mt + 8 * h + g;
+          store_out<F32>(p, row < m ? t0 + mem[row] : 0, row < m ? n : p.N, y[u][h], d, 2 * h);
+        }
+      }
+    }
+  }
+}
+
 template <int RK, bool F32>
 __global__ void __launch_bounds__(kThreads, 2)
 lora_kernel(const __grid_constant__ Params p) {
@@ -110,13 +402,14 @@ lora_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(16) int ids[kTile];
   __shared__ unsigned long long slot_tokens[kTile];
   __shared__ int slot_id[kTile], mem[kTile], leaders[2];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank_cta = p.cs > 1 ? (int)mx4::cluster_rank() : 0;
   int cl = blockIdx.x / p.cs;  // cluster: (tile, slot lane, column part), the part fastest
   const int part = cl % p.parts;
   cl /= p.parts;
-  const int slot0 = cl % p.lanes, t0 = cl / p.lanes * kTile;
-  const int count = min(kTile, p.T - t0);
+  const int slot0 = cl % p.lanes;
+  const int64_t t0 = (int64_t)(cl / p.lanes) * kTile;
+  const int count = (int)min((int64_t)kTile, p.T - t0);
   pdl_wait();
   pdl_launch_dependents();
 
@@ -157,7 +450,7 @@ lora_kernel(const __grid_constant__ Params p) {
   __nv_bfloat16* vbuf = reinterpret_cast<__nv_bfloat16*>(smem);  // after the partial sums
   const size_t psum_at = max(parts_bytes<RK>(p.rows), v_bytes<RK, SPLIT>(p.rows));
   float* psum = reinterpret_cast<float*>(smem + psum_at);        // [token][rank], read by the cluster
-  const int at_once = min(p.rows, 8 * S::kTokTiles);
+  const int at_once = min(p.rows, 8 * S::kTokTiles), vrows = (p.rows + 15) / 16 * 16;
 
   const int kblocks = (p.K + 31) / 32, kw = p.cs * kWarps;
   const int kfirst = (int)((long long)kblocks * (rank_cta * kWarps + warp) / kw);
@@ -172,65 +465,25 @@ lora_kernel(const __grid_constant__ Params p) {
     if (tid < kTile && ((tokens >> tid) & 1ull)) mem[__popcll(tokens & ((1ull << tid) - 1))] = tid;
     int rank = 0;
     if (id >= 0) rank = p.ranks ? min(max(__ldg(p.ranks + id), 0), p.R) : p.R;
+    const float c = id >= 0 && p.scale ? __ldg(p.scale + id) : 1.f;
     __syncthreads();
     const uint16_t* A = p.a + (size_t)(id < 0 ? 0 : id) * p.R * p.K;
     const uint16_t* B = p.b + (size_t)(id < 0 ? 0 : id) * p.N * p.R;
 
     if (rank > 0) {
-      if (chunk0 < chunks) {  // the first columns' rows of B are on their way to L2 meanwhile
-        const int nrow = chunk0 * 32 + lane;
-        if (nrow < p.N) prefetch_l2(B + (size_t)nrow * p.R);
+      // what the second product will read is on its way to L2 meanwhile
+      for (int ch = chunk0; ch < chunks && ch < chunk0 + 4 * stride; ch += stride) {
+        const int n = ch * 32 + lane;
+        if (n < p.N) prefetch_l2(B + (size_t)n * p.R);
+        if (p.y && m <= 8 && lane < m && ch * 32 < p.N) prefetch_l2(p.y + ((t0 + mem[lane]) * p.ldy + ch * 32) * (F32 ? 4 : 2));
       }
+      float* mine = parts + (size_t)warp * at_once * S::kPartRow;
+      const int used = (rank + 15) / 16 * 16;
       for (int c0 = 0; c0 < m; c0 += 8 * S::kTokTiles) {  // tokens at once
         const int mt = min(m - c0, 8 * S::kTokTiles);
-        float acc[S::kRowTiles][S::kTokTiles][4];
-#pragma unroll
-        for (int i = 0; i < S::kRowTiles; ++i)
-#pragma unroll
-          for (int j = 0; j < S::kTokTiles; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-        const uint16_t* xr[S::kTokTiles];
-#pragma unroll
-        for (int j = 0; j < S::kTokTiles; ++j)
-          xr[j] = 8 * j + g < mt ? p.x + (size_t)(t0 + mem[c0 + 8 * j + g]) * p.ldx : nullptr;
-        for (int kb = kfirst; kb < klast; ++kb) {
-          const int k = kb * 32 + 8 * tq;
-          const bool in = k < p.K;
-          uint4 xv[S::kTokTiles];
-#pragma unroll
-          for (int j = 0; j < S::kTokTiles; ++j) {
-            xv[j] = make_uint4(0, 0, 0, 0);
-            if (in && xr[j]) xv[j] = __ldg(reinterpret_cast<const uint4*>(xr[j] + k));
-          }
-#pragma unroll
-          for (int i = 0; i < S::kRowTiles; ++i) {
-            if (16 * i >= rank) break;
-            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            if (in && 16 * i + g < rank) lo = __ldg(reinterpret_cast<const uint4*>(A + (size_t)(16 * i + g) * p.K + k));
-            if (in && 16 * i + 8 + g < rank) hi = __ldg(reinterpret_cast<const uint4*>(A + (size_t)(16 * i + 8 + g) * p.K + k));
-#pragma unroll
-            for (int j = 0; j < S::kTokTiles; ++j) {
-              if (8 * j >= mt) break;
-              mma_bf16(acc[i][j], lo.x, hi.x, lo.y, hi.y, xv[j].x, xv[j].y);
-              mma_bf16(acc[i][j], lo.z, hi.z, lo.w, hi.w, xv[j].z, xv[j].w);
-            }
-          }
-        }
-        float* mine = parts + (size_t)warp * at_once * S::kPartRow;
-#pragma unroll
-        for (int i = 0; i < S::kRowTiles; ++i)
-#pragma unroll
-          for (int j = 0; j < S::kTokTiles; ++j) {
-            if (16 * i >= rank || 8 * j >= mt) break;
-            float* at = mine + (8 * j + 2 * tq) * S::kPartRow + 16 * i + g;
-            at[0] = acc[i][j][0];
-            at[S::kPartRow] = acc[i][j][1];
-            at[8] = acc[i][j][2];
-            at[S::kPartRow + 8] = acc[i][j][3];
-          }
+        if (mt <= 8) shrink_few<RK>(p, A, rank, mem + c0, t0, mt, kfirst, klast, mine);
+        else shrink_many<RK>(p, A, rank, mem + c0, t0, mt, kfirst, klast, mine);
         __syncthreads();
-        const int used = (rank + 15) / 16 * 16;
         for (int e = tid; e < mt * (used / 4); e += kThreads) {  // four ranks of a token
           const int tok = e / (used / 4), r = (e - tok * (used / 4)) * 4;
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -245,16 +498,23 @@ lora_kernel(const __grid_constant__ Params p) {
       }
       if (p.cs > 1) cluster_sync_all();  // every CTA's sums are there
       // c v in bf16 parts, zeros up to whole MMAs
-      const float c = p.scale ? __ldg(p.scale + id) : 1.f;
-      const int blocks = (rank + 31) / 32, vrows = (m + 15) / 16 * 16;
-      for (int e = tid; e < vrows * blocks * 8; e += kThreads) {
+      const int blocks = (rank + 31) / 32, rows = (m + 15) / 16 * 16;
+      for (int e = tid; e < rows * blocks * 8; e += kThreads) {
         const int tok = e / (blocks * 8), r = (e - tok * (blocks * 8)) * 4;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (tok < m && r < (rank + 15) / 16 * 16) {
+        if (tok < m && r < used) {
           const uint32_t at = smem_u32(psum + tok * S::kRanks + r);
-          for (int q = 0; q < p.cs; ++q) {
-            const float4 u = p.cs > 1 ? dsmem_ld_f4(dsmem_addr_u32(at, q)) : *reinterpret_cast<const float4*>(psum + tok * S::kRanks + r);
-            v[0] += u.x, v[1] += u.y, v[2] += u.z, v[3] += u.w;
+          if (p.cs > 1) {
+            float4 u[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (q < p.cs) u[q] = dsmem_ld_f4(dsmem_addr_u32(at, q));
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (q < p.cs) v[0] += u[q].x, v[1] += u[q].y, v[2] += u[q].z, v[3] += u[q].w;
+          } else {
+            const float4 u = *reinterpret_cast<const float4*>(psum + tok * S::kRanks + r);
+            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
           }
         }
         uint32_t w[SPLIT][2];
@@ -273,125 +533,42 @@ lora_kernel(const __grid_constant__ Params p) {
         }
 #pragma unroll
         for (int s = 0; s < SPLIT; ++s)
-          *reinterpret_cast<uint2*>(vbuf + ((size_t)s * ((p.rows + 15) / 16 * 16) + tok) * S::kVRow + r) =
-              make_uint2(w[s][0], w[s][1]);
+          *reinterpret_cast<uint2*>(vbuf + ((size_t)s * vrows + tok) * S::kVRow + r) = make_uint2(w[s][0], w[s][1]);
       }
       __syncthreads();
     }
-
-    // columns
-    const int blocks = (rank + 31) / 32;
-    for (int ch = chunk0; ch < chunks; ch += stride) {
-      uint4 bw[4][RK];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = ch * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
-#pragma unroll
-        for (int b = 0; b < RK; ++b) {
-          const int r = 32 * b + 8 * tq;
-          bw[j][b] = make_uint4(0, 0, 0, 0);
-          if (n < p.N && r < rank)
-            bw[j][b] = first_of(__ldg(reinterpret_cast<const uint4*>(B + (size_t)n * p.R + r)), rank - r);
-        }
-      }
-      const int n = ch * 32 + 8 * tq;  // this lane's eight columns of tokens g and g + 8
-      for (int mt = 0; mt < m; mt += 16) {
-        float d[4][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) d[j][e] = 0.f;
-        float base[2][8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = mt + 8 * h + g;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) base[h][e] = 0.f;
-          if (!p.y || row >= m || n >= p.N) continue;
-          const char* src = p.y + ((size_t)(t0 + mem[row]) * p.ldy + n) * (F32 ? 4 : 2);
-          if (p.vec) {
-            if (F32) {
-              const float4 u = *reinterpret_cast<const float4*>(src), v = *reinterpret_cast<const float4*>(src + 16);
-              base[h][0] = u.x, base[h][1] = u.y, base[h][2] = u.z, base[h][3] = u.w;
-              base[h][4] = v.x, base[h][5] = v.y, base[h][6] = v.z, base[h][7] = v.w;
-            } else {
-              const uint4 u = *reinterpret_cast<const uint4*>(src);
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                base[h][2 * e] = bf16_lo(w[e]);
-                base[h][2 * e + 1] = bf16_hi(w[e]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (n + e < p.N)
-                base[h][e] = F32 ? reinterpret_cast<const float*>(src)[e]
-                                 : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[e] << 16);
-          }
-        }
-#pragma unroll
-        for (int b = 0; b < RK; ++b) {
-          if (b >= blocks) break;
-#pragma unroll
-          for (int s = SPLIT - 1; s >= 0; --s) {  // the small parts first
-            const __nv_bfloat16* vr = vbuf + ((size_t)s * ((p.rows + 15) / 16 * 16) + mt + g) * S::kVRow + 32 * b + 8 * tq;
-            const uint4 lo = *reinterpret_cast<const uint4*>(vr), hi = *reinterpret_cast<const uint4*>(vr + 8 * S::kVRow);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma_bf16(d[j], lo.x, hi.x, lo.y, hi.y, bw[j][b].x, bw[j][b].y);
-              mma_bf16(d[j], lo.z, hi.z, lo.w, hi.w, bw[j][b].z, bw[j][b].w);
-            }
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = mt + 8 * h + g;
-          if (row >= m || n >= p.N) continue;
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = base[h][e] + d[e >> 1][2 * h + (e & 1)];
-          char* dst = p.out + ((size_t)(t0 + mem[row]) * p.ldo + n) * (F32 ? 4 : 2);
-          if (F32) {
-            if (p.vec) {
-              reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-              reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (n + e < p.N) reinterpret_cast<float*>(dst)[e] = v[e];
-            }
-          } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-              w[e] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            if (p.vec) {
-              *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (n + e < p.N) reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-            }
-          }
-        }
-      }
-    }
+    if (m <= 8) expand_few<RK, F32>(p, B, rank, mem, t0, m, vbuf, vrows, chunk0, chunks, stride);
+    else expand_many<RK, F32>(p, B, rank, mem, t0, m, vbuf, vrows, chunk0, chunks, stride);
     // the sums have been read everywhere, mem and v here, before they are written again (or the CTA leaves)
     if (p.cs > 1 && rank > 0) cluster_sync_all();
     else __syncthreads();
   }
 }
 
+// The cut: a launch in one wave if it can be.  Clusters of 8 CTAs, fewer when there are more
+// tiles and slots than such clusters fit on the device at once (a GB300, two CTAs
+// an SM: 36 of 8, 74 of 4, 152 of 2); as many slots' lanes as a tile can have
+// slots while they fit; and columns in parts while SMs would be idle.
 template <int RK>
-qsm_status launch(const Params& p, bool f32, long long ctas, cudaStream_t stream) {
+qsm_status launch(Params& p, bool f32, cudaStream_t stream) {
   auto* kernel = f32 ? lora_kernel<RK, true> : lora_kernel<RK, false>;
   const size_t smem = f32 ? smem_bytes<RK, 3>(p.rows) : smem_bytes<RK, 2>(p.rows);
   const size_t most = f32 ? smem_bytes<RK, 3>(kTile) : smem_bytes<RK, 2>(kTile);
-  QSM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
+  const auto resident = [&](int cs) {
+    return (long long)mx4::resident_clusters(reinterpret_cast<void*>(kernel), cs, kThreads, (int)smem, (int)most) * (cs == 1 ? 2 : 1);
+  };
+  const long long tiles = ((long long)p.T + kTile - 1) / kTile;
+  const int in_tile = p.T < kTile ? p.T : kTile, slots = p.n + 1ll < in_tile ? p.n + 1 : in_tile;
+  p.cs = 8;
+  while (p.cs > 1 && tiles * (tiles == 1 ? slots : 1) > resident(p.cs)) p.cs /= 2;
+  const long long room = resident(p.cs);
+  if (room < 1) return QSM_ERR_CUDA;
+  p.lanes = (int)(tiles * slots <= room ? slots : room / tiles < 1 ? 1 : room / tiles);
+  p.parts = 1;
+  const int chunks = (p.N + 31) / 32;
+  while (tiles * p.lanes * p.parts * 2 <= room && p.parts * 2 * p.cs * kWarps <= chunks) p.parts *= 2;
+  const long long ctas = tiles * p.lanes * p.parts * p.cs;
+  if (ctas > 0x7fffffffll) return QSM_ERR_UNSUPPORTED;
   QSM_CUDA_TRY(launch_pdl_cluster(kernel, dim3((unsigned)ctas), dim3(kThreads), p.cs, smem, stream, p));
   return QSM_OK;
 }
@@ -424,7 +601,7 @@ extern "C" qsm_status lora_add(const qsm_lora* L, const uint16_t* x, int64_t ldx
   if (!L || T < 0 || L->n < 1 || L->K < 8 || L->K % 8 || L->N < 1 || L->rank < 8 || L->rank % 8 ||
       (dtype != QSM_BF16 && dtype != QSM_FP32))
     return QSM_ERR_INVALID_ARGUMENT;
-  if (L->rank > kMaxRank) return QSM_ERR_UNSUPPORTED;
+  if (L->rank > kMaxRank || L->K > kMaxSide || L->N > kMaxSide) return QSM_ERR_UNSUPPORTED;
   if (T == 0) return QSM_OK;
   if (T == 1) {
     ldx = L->K;
@@ -469,19 +646,7 @@ extern "C" qsm_status lora_add(const qsm_lora* L, const uint16_t* x, int64_t ldx
   p.vec = N % 8 == 0 && on(out, 16) && ldo % wide == 0 && (!y || (on(y, 16) && ldy % wide == 0));
   p.copy = !same;
   p.status = dev_status;
-  // Clusters of 8 CTAs; as many slots' lanes as a tile can have slots while there are few tiles,
-  // and columns in parts while that leaves SMs idle.
-  p.cs = 8;
-  const long long tiles = ((long long)T + kTile - 1) / kTile;
-  const int slots = L->n + 1ll < (T < kTile ? T : kTile) ? L->n + 1 : (T < kTile ? T : kTile);
-  const long long want = 4ll * mx4::sm_count() / p.cs;
-  p.lanes = (int)(tiles * slots <= want ? slots : want / tiles < 1 ? 1 : want / tiles);
-  p.parts = 1;
-  const int chunks = (int)((N + 31) / 32);
-  while (tiles * p.lanes * p.parts * 2 * p.cs <= mx4::sm_count() && p.parts * 2 * p.cs * kWarps <= chunks) p.parts *= 2;
-  const long long ctas = tiles * p.lanes * p.parts * p.cs;
-  if (ctas > 0x7fffffffll) return QSM_ERR_UNSUPPORTED;
-  return L->rank <= 32 ? launch<1>(p, dtype == QSM_FP32, ctas, stream)
-         : L->rank <= 64 ? launch<2>(p, dtype == QSM_FP32, ctas, stream)
-                         : launch<4>(p, dtype == QSM_FP32, ctas, stream);
+  return L->rank <= 32 ? launch<1>(p, dtype == QSM_FP32, stream)
+         : L->rank <= 64 ? launch<2>(p, dtype == QSM_FP32, stream)
+                         : launch<4>(p, dtype == QSM_FP32, stream);
 }

@@ -151,7 +151,7 @@ def test_lora_refuses_bad_arguments():
     assert f(None, P, 64, 4, P, 0, P, 48, P, 48, P, None) == BAD
     for kw in (dict(n=0), dict(rank=0), dict(rank=12), dict(K=60), dict(K=0), dict(N=0), dict(T=-1), dict(dt=1), dict(dt=3)):
         assert call(**kw) == BAD
-    assert call(rank=136) == UNSUP
+    assert call(rank=136) == UNSUP and call(K=(1 << 28) + 8, ldx=1 << 29) == UNSUP and call(N=(1 << 28) + 1) == UNSUP
     for none in ("a", "b", "x", "ids", "o", "st"):
         assert call(**{none: None}) == BAD
     for odd in (dict(a=at(10) + 8), dict(b=at(11) + 8), dict(x=at(0) + 8), dict(ids=at(1) + 2), dict(y=at(2) + 1),
