@@ -80,7 +80,6 @@ __device__ __forceinline__ uint4 first_of(uint4 v, int n) {
 template <int RK>
 struct Shape {
   static constexpr int kRanks = 32 * RK;
-  static constexpr int kRowTiles = 2 * RK;            // of 16 ranks
   static constexpr int kTokTiles = 8 / RK;            // of 8 tokens, at once: 64 accumulators a lane
   static constexpr int kPartRow = kRanks + 4;         // floats: banks 8 apart for a lane's tokens
   static constexpr int kVRow = kRanks + (RK == 1 ? 0 : 32);  // bf16: rows 16 banks apart
@@ -108,23 +107,20 @@ struct Raw {
   uint4 v[F32 ? 2 : 1];
 };
 
-template <bool F32>
-__device__ __forceinline__ Raw<F32> load_y(const Params& p, int64_t t, int n) {
+// left: columns from here to the last.
+template <bool F32, bool VEC>
+__device__ __forceinline__ Raw<F32> load_y(const char* src, int left) {
   Raw<F32> r;
-  r.v[0] = make_uint4(0, 0, 0, 0);
-  if (F32) r.v[F32] = make_uint4(0, 0, 0, 0);
-  if (!p.y || n >= p.N) return r;
-  const char* src = p.y + (t * p.ldy + n) * (F32 ? 4 : 2);
-  if (p.vec) {
+  if (VEC) {
     r.v[0] = *reinterpret_cast<const uint4*>(src);
     if (F32) r.v[F32] = reinterpret_cast<const uint4*>(src)[1];
   } else {
     uint32_t w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      w[e] = n + e >= p.N ? 0u
-             : F32        ? reinterpret_cast<const uint32_t*>(src)[e]
-                          : (uint32_t)reinterpret_cast<const uint16_t*>(src)[e];
+      w[e] = e >= left ? 0u
+             : F32     ? reinterpret_cast<const uint32_t*>(src)[e]
+                       : (uint32_t)reinterpret_cast<const uint16_t*>(src)[e];
     if (F32) {
       r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
       r.v[F32] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -135,259 +131,231 @@ __device__ __forceinline__ Raw<F32> load_y(const Params& p, int64_t t, int n) {
   return r;
 }
 
-// out = y + d for eight columns; the MMAs of tiles 0 .. 3 hold two of them each,
-// at d[j][at] and d[j][at + 1].
-template <bool F32>
-__device__ __forceinline__ void store_out(const Params& p, int64_t t, int n, const Raw<F32>& y, const float (&d)[4][4],
-                                          int at) {
-  if (n >= p.N) return;
+// Eight columns of out: the MMAs of tiles 0 .. 3 hold two of them each, at d[j][at]
+// and d[j][at + 1], bf16 with y in the sum, fp32 without.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void store_out(char* dst, int left, const Raw<F32>& y, const float (&d)[4][4], int at) {
   const uint32_t* w = reinterpret_cast<const uint32_t*>(y.v);
-  uint32_t o[F32 ? 8 : 4];
+  uint32_t o[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (F32) {
-      o[2 * j] = __float_as_uint(__uint_as_float(w[2 * j]) + d[j][at]);
-      o[2 * j + 1] = __float_as_uint(__uint_as_float(w[2 * j + 1]) + d[j][at + 1]);
+      o[2 * j] = __float_as_uint(__uint_as_float(w[2 * j * F32]) + d[j][at]);
+      o[2 * j + 1] = __float_as_uint(__uint_as_float(w[(2 * j + 1) * F32]) + d[j][at + 1]);
     } else {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(bf16_lo(w[j]) + d[j][at], bf16_hi(w[j]) + d[j][at + 1]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(d[j][at], d[j][at + 1]);
       o[j] = *reinterpret_cast<const uint32_t*>(&b);
     }
   }
-  char* dst = p.out + (t * p.ldo + n) * (F32 ? 4 : 2);
-  if (p.vec) {
+  if (VEC) {
     reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    if (F32) reinterpret_cast<uint4*>(dst)[F32] = make_uint4(o[4 * F32], o[1 + 4 * F32], o[2 + 4 * F32], o[3 + 4 * F32]);
+    if (F32) reinterpret_cast<uint4*>(dst)[F32] = make_uint4(o[4], o[5], o[6], o[7]);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (n + e < p.N) {
+      if (e < left) {
         if (F32) reinterpret_cast<uint32_t*>(dst)[e] = o[e];
         else reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
       }
   }
 }
 
-// Sixteen ranks' rows of A (from r0 on), 8 columns at k: an MMA's rows g and g + 8.
-__device__ __forceinline__ void load_a(const uint16_t* A, int K, int rank, int r0, int k, bool in, uint4& lo, uint4& hi) {
-  const int g = (threadIdx.x & 31) >> 2;
-  lo = hi = make_uint4(0, 0, 0, 0);
-  if (in && r0 + g < rank) lo = __ldg(reinterpret_cast<const uint4*>(A + (size_t)(r0 + g) * K + k));
-  if (in && r0 + 8 + g < rank) hi = __ldg(reinterpret_cast<const uint4*>(A + (size_t)(r0 + 8 + g) * K + k));
-}
-
 // 32 columns of B: tile j's column g is row n of it, and the lane has 8 ranks of
-// each block of 32.
+// each block of 32.  Rows past the last column repeat it (their sums are not used);
+// ranks that do not count are zeros (they may hold anything, and 0 x NaN is not 0).
 template <int RK>
 __device__ __forceinline__ void load_b(const Params& p, const uint16_t* B, int rank, int chunk, uint4 (&w)[4][RK]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3, n = chunk * 32 + 8 * (g >> 1) + (g & 1);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int n = chunk * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
+    const uint16_t* row = B + (size_t)min(n + 2 * j, p.N - 1) * p.R + 8 * tq;
 #pragma unroll
-    for (int b = 0; b < RK; ++b) {
-      const int r = 32 * b + 8 * tq;
-      w[j][b] = make_uint4(0, 0, 0, 0);
-      if (n < p.N && r < rank) w[j][b] = first_of(__ldg(reinterpret_cast<const uint4*>(B + (size_t)n * p.R + r)), rank - r);
-    }
+    for (int b = 0; b < RK; ++b)
+      w[j][b] = 32 * b + 8 * tq < rank ? __ldg(reinterpret_cast<const uint4*>(row + 32 * b)) : make_uint4(0, 0, 0, 0);
+  }
+  if (rank & 7) {
+#pragma unroll
+    for (int b = 0; b < RK; ++b)
+      if (rank - (32 * b + 8 * tq) < 8)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j][b] = first_of(w[j][b], max(rank - (32 * b + 8 * tq), 0));
   }
 }
 
-// The slot's tokens' share of v from this warp's blocks of K, into its partial
-// sums [token][rank].  At most 8 tokens: sixteen rows of A are under way at
-// once, of as many blocks as that makes.
+// N blocks of 32 columns from k on; in: whether this lane's columns exist.
+template <int RK, int NT, int N>
+__device__ __forceinline__ void shrink_blocks(const uint16_t* const (&ap)[2 * RK][2], const uint16_t* const (&xp)[NT], int k,
+                                              bool in, int tiles, float (&acc)[2 * RK][NT][4]) {
+  uint4 xv[N][NT], av[N][2 * RK][2];
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      xv[u][j] = in ? __ldg(reinterpret_cast<const uint4*>(xp[j] + k + 32 * u)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * RK; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        av[u][i][h] = in && i < tiles ? __ldg(reinterpret_cast<const uint4*>(ap[i][h] + k + 32 * u)) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < N; ++u)
+#pragma unroll
+    for (int i = 0; i < 2 * RK; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const uint4 &lo = av[u][i][0], &hi = av[u][i][1];
+        mma_bf16(acc[i][j], lo.x, hi.x, lo.y, hi.y, xv[u][j].x, xv[u][j].y);
+        mma_bf16(acc[i][j], lo.z, hi.z, lo.w, hi.w, xv[u][j].z, xv[u][j].w);
+      }
+}
+
+template <int RK, int NT>
+__device__ __forceinline__ void put_sums(const float (&acc)[2 * RK][NT][4], int tiles, int m, float* mine) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2 * RK; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if (i >= tiles || 8 * j >= m) break;
+      float* at = mine + (8 * j + 2 * tq) * Shape<RK>::kPartRow + 16 * i + g;
+      at[0] = acc[i][j][0];
+      at[Shape<RK>::kPartRow] = acc[i][j][1];
+      at[8] = acc[i][j][2];
+      at[Shape<RK>::kPartRow + 8] = acc[i][j][3];
+    }
+}
+
+// v of at most 8 tokens over blocks kfirst .. klast - 1 of 32 columns, into this
+// warp's partial sums [token][rank]; sixteen rows of A are under way at once, of
+// as many blocks as that makes.  Rows past the last rank and tokens past the last one
+// repeat that one: their sums are not used.
 template <int RK>
 __device__ __forceinline__ void shrink_few(const Params& p, const uint16_t* A, int rank, const int* mem, int64_t t0, int m,
                                            int kfirst, int klast, float* mine) {
-  using S = Shape<RK>;
   constexpr int U = 4 / RK;
-  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  float acc[S::kRowTiles][4];
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3, tiles = (rank + 15) / 16;
+  float acc[2 * RK][1][4] = {};
+  const uint16_t *ap[2 * RK][2], *xp[1];
 #pragma unroll
-  for (int i = 0; i < S::kRowTiles; ++i)
+  for (int i = 0; i < 2 * RK; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-  const uint16_t* xr = g < m ? p.x + (t0 + mem[g]) * p.ldx : nullptr;
+    for (int h = 0; h < 2; ++h) ap[i][h] = A + (size_t)min(16 * i + 8 * h + g, rank - 1) * p.K + 8 * tq;
+  xp[0] = p.x + (t0 + mem[min(g, m - 1)]) * p.ldx + 8 * tq;
+  const int whole = min(klast, p.K / 32);  // the blocks before it have no column past K
+  int kb = kfirst;
 #pragma unroll 1
-  for (int kb = kfirst; kb < klast; kb += U) {
-    uint4 xv[U], lo[U][S::kRowTiles], hi[U][S::kRowTiles];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = (kb + u) * 32 + 8 * tq;
-      const bool in = kb + u < klast && k < p.K;
-      xv[u] = make_uint4(0, 0, 0, 0);
-      if (in && xr) xv[u] = __ldg(reinterpret_cast<const uint4*>(xr + k));
-#pragma unroll
-      for (int i = 0; i < S::kRowTiles; ++i) load_a(A, p.K, rank, 16 * i, k, in, lo[u][i], hi[u][i]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < S::kRowTiles; ++i) {
-        mma_bf16(acc[i], lo[u][i].x, hi[u][i].x, lo[u][i].y, hi[u][i].y, xv[u].x, xv[u].y);
-        mma_bf16(acc[i], lo[u][i].z, hi[u][i].z, lo[u][i].w, hi[u][i].w, xv[u].z, xv[u].w);
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < S::kRowTiles; ++i) {
-    if (16 * i >= rank) break;
-    float* at = mine + 2 * tq * S::kPartRow + 16 * i + g;
-    at[0] = acc[i][0];
-    at[S::kPartRow] = acc[i][1];
-    at[8] = acc[i][2];
-    at[S::kPartRow + 8] = acc[i][3];
-  }
+  for (; kb + U <= whole; kb += U) shrink_blocks<RK, 1, U>(ap, xp, kb * 32, true, tiles, acc);
+#pragma unroll 1
+  for (; kb < klast; ++kb) shrink_blocks<RK, 1, 1>(ap, xp, kb * 32, kb * 32 + 8 * tq < p.K, tiles, acc);
+  put_sums<RK, 1>(acc, tiles, m, mine);
 }
 
-// The same for up to 8 kTokTiles tokens.
+// The same for up to 8 kTokTiles tokens, block by block.
 template <int RK>
 __device__ __forceinline__ void shrink_many(const Params& p, const uint16_t* A, int rank, const int* mem, int64_t t0,
                                             int m, int kfirst, int klast, float* mine) {
-  using S = Shape<RK>;
-  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  float acc[S::kRowTiles][S::kTokTiles][4];
+  constexpr int NT = Shape<RK>::kTokTiles;
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3, tiles = (rank + 15) / 16;
+  float acc[2 * RK][NT][4] = {};
+  int row[NT];
 #pragma unroll
-  for (int i = 0; i < S::kRowTiles; ++i)
-#pragma unroll
-    for (int j = 0; j < S::kTokTiles; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-  int row[S::kTokTiles];
-#pragma unroll
-  for (int j = 0; j < S::kTokTiles; ++j) row[j] = 8 * j + g < m ? mem[8 * j + g] : -1;
+  for (int j = 0; j < NT; ++j) row[j] = mem[min(8 * j + g, m - 1)];
 #pragma unroll 1
   for (int kb = kfirst; kb < klast; ++kb) {
     const int k = kb * 32 + 8 * tq;
     const bool in = k < p.K;
-    uint4 xv[S::kTokTiles];
+    uint4 xv[NT];
 #pragma unroll
-    for (int j = 0; j < S::kTokTiles; ++j) {
-      xv[j] = make_uint4(0, 0, 0, 0);
-      if (in && row[j] >= 0) xv[j] = __ldg(reinterpret_cast<const uint4*>(p.x + (t0 + row[j]) * p.ldx + k));
-    }
+    for (int j = 0; j < NT; ++j)
+      xv[j] = in ? __ldg(reinterpret_cast<const uint4*>(p.x + (t0 + row[j]) * p.ldx + k)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < S::kRowTiles; ++i) {
-      uint4 lo, hi;
-      load_a(A, p.K, rank, 16 * i, k, in, lo, hi);
+    for (int i = 0; i < 2 * RK; ++i) {
+      if (i >= tiles) break;
+      uint4 a[2];
 #pragma unroll
-      for (int j = 0; j < S::kTokTiles; ++j) {
-        mma_bf16(acc[i][j], lo.x, hi.x, lo.y, hi.y, xv[j].x, xv[j].y);
-        mma_bf16(acc[i][j], lo.z, hi.z, lo.w, hi.w, xv[j].z, xv[j].w);
+      for (int h = 0; h < 2; ++h)
+        a[h] = in ? __ldg(reinterpret_cast<const uint4*>(A + (size_t)min(16 * i + 8 * h + g, rank - 1) * p.K + k)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        mma_bf16(acc[i][j], a[0].x, a[1].x, a[0].y, a[1].y, xv[j].x, xv[j].y);
+        mma_bf16(acc[i][j], a[0].z, a[1].z, a[0].w, a[1].w, xv[j].z, xv[j].w);
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < S::kRowTiles; ++i)
-#pragma unroll
-    for (int j = 0; j < S::kTokTiles; ++j) {
-      if (16 * i >= rank || 8 * j >= m) break;
-      float* at = mine + (8 * j + 2 * tq) * S::kPartRow + 16 * i + g;
-      at[0] = acc[i][j][0];
-      at[S::kPartRow] = acc[i][j][1];
-      at[8] = acc[i][j][2];
-      at[S::kPartRow + 8] = acc[i][j][3];
-    }
+  put_sums<RK, NT>(acc, tiles, m, mine);
 }
 
-// This warp's columns of at most 8 tokens: v stays in registers, and the rows of B
-// of two chunks (one, for many ranks) and their y are under way at once.
-template <int RK, bool F32>
-__device__ __forceinline__ void expand_few(const Params& p, const uint16_t* B, int rank, const int* mem, int64_t t0, int m,
-                                           const __nv_bfloat16* vbuf, int vrows, int chunk0, int chunks, int stride) {
-  using S = Shape<RK>;
-  constexpr int SPLIT = F32 ? 3 : 2, U = RK == 1 ? 2 : 1;
-  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  const int64_t t = t0 + (g < m ? mem[g] : 0);
-  uint4 v[SPLIT][RK];
+// d (+)= v B^T for 16 tokens (8 with H = 1) and the 32 columns whose rows of B are in w.
+template <int RK, int SPLIT, int H>
+__device__ __forceinline__ void product(const __nv_bfloat16* v, int part, int rank, const uint4 (&w)[4][RK],
+                                        float (&d)[4][4]) {
 #pragma unroll
-  for (int s = 0; s < SPLIT; ++s)
+  for (int b = 0; b < RK; ++b) {
+    if (32 * b >= rank) break;
 #pragma unroll
-    for (int b = 0; b < RK; ++b) {
-      v[s][b] = make_uint4(0, 0, 0, 0);
-      if (32 * b < rank) v[s][b] = *reinterpret_cast<const uint4*>(vbuf + ((size_t)s * vrows + g) * S::kVRow + 32 * b + 8 * tq);
-    }
-#pragma unroll 1
-  for (int ch = chunk0; ch < chunks; ch += U * stride) {
-    uint4 w[U][4][RK];
-    Raw<F32> y[U];
+    for (int s = SPLIT - 1; s >= 0; --s) {  // the small parts first
+      const uint4 lo = *reinterpret_cast<const uint4*>(v + s * part + 32 * b);
+      uint4 hi = make_uint4(0, 0, 0, 0);
+      if (H == 2) hi = *reinterpret_cast<const uint4*>(v + s * part + 32 * b + 8 * Shape<RK>::kVRow);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = ch + u * stride;  // past the end: no row of B, no column of y
-      load_b<RK>(p, B, rank, c, w[u]);
-      y[u] = load_y<F32>(p, t, g < m ? c * 32 + 8 * tq : p.N);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float d[4][4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[j][e] = 0.f;
-#pragma unroll
-      for (int b = 0; b < RK; ++b)
-#pragma unroll
-        for (int s = SPLIT - 1; s >= 0; --s)  // the small parts first
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            mma_bf16(d[j], v[s][b].x, 0u, v[s][b].y, 0u, w[u][j][b].x, w[u][j][b].y);
-            mma_bf16(d[j], v[s][b].z, 0u, v[s][b].w, 0u, w[u][j][b].z, w[u][j][b].w);
-          }
-      store_out<F32>(p, t, g < m ? (ch + u * stride) * 32 + 8 * tq : p.N, y[u], d, 0);
+      for (int j = 0; j < 4; ++j) {
+        mma_bf16(d[j], lo.x, hi.x, lo.y, hi.y, w[j][b].x, w[j][b].y);
+        mma_bf16(d[j], lo.z, hi.z, lo.w, hi.w, w[j][b].z, w[j][b].w);
+      }
     }
   }
 }
 
-// This warp's columns of any number of tokens: v comes from shared memory, the
-// y of 64 tokens (32 of fp32) is under way at once.
-template <int RK, bool F32>
-__device__ __forceinline__ void expand_many(const Params& p, const uint16_t* B, int rank, const int* mem, int64_t t0,
-                                            int m, const __nv_bfloat16* vbuf, int vrows, int chunk0, int chunks,
-                                            int stride) {
+// This warp's columns of the slot's tokens, 16 at a time (8, with H = 1, where there are no
+// more).  Lanes g, tq: columns 8 tq .. 8 tq + 7 of a chunk of 32, of tokens g and g + 8; U
+// times 16 tokens' y are under way at once.  VEC: y and out have those columns as
+// whole 16-byte units.
+template <int RK, bool F32, bool VEC, int H, int U>
+__device__ __forceinline__ void expand(const Params& p, const uint16_t* B, int rank, const int64_t* yrow,
+                                       const int64_t* orow, int m, const __nv_bfloat16* vbuf, int vrows, int chunk0,
+                                       int chunks, int stride) {
   using S = Shape<RK>;
-  constexpr int SPLIT = F32 ? 3 : 2, U = F32 || RK == 4 ? 2 : 4;
+  constexpr int kEl = F32 ? 4 : 2;
   const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  const __nv_bfloat16* v = vbuf + (size_t)g * S::kVRow + 8 * tq;
+  const int part = vrows * S::kVRow;
 #pragma unroll 1
   for (int ch = chunk0; ch < chunks; ch += stride) {
+    const int n = ch * 32 + 8 * tq;
     uint4 w[4][RK];
     load_b<RK>(p, B, rank, ch, w);
-    const int n = ch * 32 + 8 * tq;  // this lane's eight columns of tokens g and g + 8
 #pragma unroll 1
     for (int m0 = 0; m0 < m; m0 += 16 * U) {
-      Raw<F32> y[U][2];
+      Raw<F32> y[U][H];
+      bool in[U][H];
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < H; ++h) {
           const int row = m0 + 16 * u + 8 * h + g;
-          y[u][h] = load_y<F32>(p, row < m ? t0 + mem[row] : 0, row < m ? n : p.N);
+          in[u][h] = row < m && n < p.N;
+          y[u][h] = {};
+          if (p.y && in[u][h]) y[u][h] = load_y<F32, VEC>(p.y + (yrow[row] + n) * kEl, p.N - n);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int mt = m0 + 16 * u;
-        if (mt >= m) break;
+        if (m0 + 16 * u >= m) break;
         float d[4][4];
+        // bf16: the sum begins with y; fp32: y comes last, for its full accuracy, and
+        // the sum begins with -0, which leaves y as it is where there is no adapter
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) d[j][e] = 0.f;
-#pragma unroll
-        for (int b = 0; b < RK; ++b) {
-          if (32 * b >= rank) break;
-#pragma unroll
-          for (int s = SPLIT - 1; s >= 0; --s) {
-            const __nv_bfloat16* vr = vbuf + ((size_t)s * vrows + mt + g) * S::kVRow + 32 * b + 8 * tq;
-            const uint4 lo = *reinterpret_cast<const uint4*>(vr), hi = *reinterpret_cast<const uint4*>(vr + 8 * S::kVRow);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma_bf16(d[j], lo.x, hi.x, lo.y, hi.y, w[j][b].x, w[j][b].y);
-              mma_bf16(d[j], lo.z, hi.z, lo.w, hi.w, w[j][b].z, w[j][b].w);
-            }
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t pair = h < H && !F32 ? reinterpret_cast<const uint32_t*>(y[u][h < H ? h : 0].v)[j] : F32 ? 0x80008000u : 0u;
+            d[j][2 * h] = bf16_lo(pair);
+            d[j][2 * h + 1] = bf16_hi(pair);
           }
-        }
+        product<RK, F32 ? 3 : 2, H>(v + (m0 + 16 * u) * S::kVRow, part, rank, w, d);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = mt + 8 * h + g;
-          store_out<F32>(p, row < m ? t0 + mem[row] : 0, row < m ? n : p.N, y[u][h], d, 2 * h);
-        }
+        for (int h = 0; h < H; ++h)
+          if (in[u][h]) store_out<F32, VEC>(p.out + (orow[m0 + 16 * u + 8 * h + g] + n) * kEl, p.N - n, y[u][h], d, 2 * h);
       }
     }
   }
@@ -402,6 +370,7 @@ lora_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(16) int ids[kTile];
   __shared__ unsigned long long slot_tokens[kTile];
   __shared__ int slot_id[kTile], mem[kTile], leaders[2];
+  __shared__ int64_t yrow[kTile], orow[kTile];  // where the slot's tokens have their rows, in elements
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank_cta = p.cs > 1 ? (int)mx4::cluster_rank() : 0;
   int cl = blockIdx.x / p.cs;  // cluster: (tile, slot lane, column part), the part fastest
@@ -462,7 +431,12 @@ lora_kernel(const __grid_constant__ Params p) {
     const int id = slot_id[slot];
     const unsigned long long tokens = slot_tokens[slot];
     const int m = __popcll(tokens);
-    if (tid < kTile && ((tokens >> tid) & 1ull)) mem[__popcll(tokens & ((1ull << tid) - 1))] = tid;
+    if (tid < kTile && ((tokens >> tid) & 1ull)) {
+      const int at = __popcll(tokens & ((1ull << tid) - 1));
+      mem[at] = tid;
+      yrow[at] = (t0 + tid) * p.ldy;
+      orow[at] = (t0 + tid) * p.ldo;
+    }
     int rank = 0;
     if (id >= 0) rank = p.ranks ? min(max(__ldg(p.ranks + id), 0), p.R) : p.R;
     const float c = id >= 0 && p.scale ? __ldg(p.scale + id) : 1.f;
@@ -472,11 +446,11 @@ lora_kernel(const __grid_constant__ Params p) {
 
     if (rank > 0) {
       // what the second product will read is on its way to L2 meanwhile
-      for (int ch = chunk0; ch < chunks && ch < chunk0 + 4 * stride; ch += stride) {
-        const int n = ch * 32 + lane;
-        if (n < p.N) prefetch_l2(B + (size_t)n * p.R);
-        if (p.y && m <= 8 && lane < m && ch * 32 < p.N) prefetch_l2(p.y + ((t0 + mem[lane]) * p.ldy + ch * 32) * (F32 ? 4 : 2));
-      }
+      if (m <= 8)
+        for (int ch = chunk0; ch < chunks && ch < chunk0 + 4 * stride; ch += stride) {
+          if (lane == 0) bulk_prefetch_l2(B + (size_t)ch * 32 * p.R, (uint32_t)min(32, p.N - ch * 32) * p.R * 2);
+          if (p.y && lane < m) prefetch_l2(p.y + (yrow[lane] + ch * 32) * (F32 ? 4 : 2));
+        }
       float* mine = parts + (size_t)warp * at_once * S::kPartRow;
       const int used = (rank + 15) / 16 * 16;
       for (int c0 = 0; c0 < m; c0 += 8 * S::kTokTiles) {  // tokens at once
@@ -537,8 +511,9 @@ lora_kernel(const __grid_constant__ Params p) {
       }
       __syncthreads();
     }
-    if (m <= 8) expand_few<RK, F32>(p, B, rank, mem, t0, m, vbuf, vrows, chunk0, chunks, stride);
-    else expand_many<RK, F32>(p, B, rank, mem, t0, m, vbuf, vrows, chunk0, chunks, stride);
+    if (!p.vec) expand<RK, F32, false, 2, 1>(p, B, rank, yrow, orow, m, vbuf, vrows, chunk0, chunks, stride);
+    else if (m <= 8) expand<RK, F32, true, 1, 1>(p, B, rank, yrow, orow, m, vbuf, vrows, chunk0, chunks, stride);
+    else expand<RK, F32, true, 2, F32 || RK == 4 ? 2 : 4>(p, B, rank, yrow, orow, m, vbuf, vrows, chunk0, chunks, stride);
     // the sums have been read everywhere, mem and v here, before they are written again (or the CTA leaves)
     if (p.cs > 1 && rank > 0) cluster_sync_all();
     else __syncthreads();
