@@ -53,6 +53,7 @@ struct Params {
   int cs, lanes, parts;   // CTAs of a cluster, slots' lanes S, column parts NS
   int rows;               // tokens of a tile, rounded up to 8: what the buffers hold
   int vec;                // whether eight columns of y and out can be one access
+  int wide_in, wide_out;  // whether sixteen of a and x, and of bf16 y and out, can be one access
   int copy;               // whether tokens without an adapter have to be copied
   int32_t* status;
 };
@@ -91,9 +92,10 @@ __host__ __device__ constexpr size_t parts_bytes(int rows) {
   const int at_once = rows < 8 * Shape<RK>::kTokTiles ? rows : 8 * Shape<RK>::kTokTiles;
   return (size_t)kWarps * at_once * Shape<RK>::kPartRow * 4;
 }
+__host__ __device__ constexpr int v_rows(int rows) { return rows + 16; }  // an MMA may read 15 behind the last
 template <int RK, int SPLIT>
 __host__ __device__ constexpr size_t v_bytes(int rows) {
-  return (size_t)SPLIT * ((rows + 15) / 16 * 16) * Shape<RK>::kVRow * 2;
+  return (size_t)SPLIT * v_rows(rows) * Shape<RK>::kVRow * 2;
 }
 template <int RK, int SPLIT>
 __host__ __device__ constexpr size_t smem_bytes(int rows) {
@@ -160,12 +162,12 @@ __device__ __forceinline__ void store_out(char* dst, int left, const Raw<F32>& y
   }
 }
 
-// 32 columns of B: tile j's column g is row n of it, and the lane has 8 ranks of
-// each block of 32.  Rows past the last column repeat it (their sums are not used);
+// 32 columns of B: tile j's column g is row n + 2 j of it (n: the lane's), and the lane
+// has 8 ranks of each block of 32.  Rows past the last column repeat it (their sums are not used);
 // ranks that do not count are zeros (they may hold anything, and 0 x NaN is not 0).
 template <int RK>
-__device__ __forceinline__ void load_b(const Params& p, const uint16_t* B, int rank, int chunk, uint4 (&w)[4][RK]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3, n = chunk * 32 + 8 * (g >> 1) + (g & 1);
+__device__ __forceinline__ void load_b(const Params& p, const uint16_t* B, int rank, int n, uint4 (&w)[4][RK]) {
+  const int tq = threadIdx.x & 3;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint16_t* row = B + (size_t)min(n + 2 * j, p.N - 1) * p.R + 8 * tq;
@@ -180,6 +182,62 @@ __device__ __forceinline__ void load_b(const Params& p, const uint16_t* B, int r
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j][b] = first_of(w[j][b], max(rank - (32 * b + 8 * tq), 0));
   }
+}
+
+// Sixteen bf16 in one access (32-byte aligned).
+struct Wide {
+  uint4 v[2];
+};
+__device__ __forceinline__ Wide load_wide(const uint16_t* p) {
+  Wide w;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w.v[0].x), "=r"(w.v[0].y), "=r"(w.v[0].z), "=r"(w.v[0].w), "=r"(w.v[1].x), "=r"(w.v[1].y),
+                 "=r"(w.v[1].z), "=r"(w.v[1].w)
+               : "l"(p));
+  return w;
+}
+
+// The same of memory that this launch writes, and the store.
+__device__ __forceinline__ Wide load_wide_rw(const uint16_t* p) {
+  Wide w;
+  asm volatile("ld.global.L2::256B.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w.v[0].x), "=r"(w.v[0].y), "=r"(w.v[0].z), "=r"(w.v[0].w), "=r"(w.v[1].x), "=r"(w.v[1].y),
+                 "=r"(w.v[1].z), "=r"(w.v[1].w)
+               : "l"(p));
+  return w;
+}
+__device__ __forceinline__ void store_wide(uint16_t* p, const Wide& w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w.v[0].x), "r"(w.v[0].y), "r"(w.v[0].z),
+               "r"(w.v[0].w), "r"(w.v[1].x), "r"(w.v[1].y), "r"(w.v[1].z), "r"(w.v[1].w)
+               : "memory");
+}
+
+// N blocks of 64 columns from k on, 16 of them a lane: whole 128-byte lines of the
+// rows.
+template <int RK, int N>
+__device__ __forceinline__ void shrink_wide(const uint16_t* const (&ap)[2 * RK][2], const uint16_t* xp, int k, int tiles,
+                                            float (&acc)[2 * RK][1][4]) {
+  Wide xv[N], av[N][2 * RK][2];
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    xv[u] = load_wide(xp + k + 64 * u);
+#pragma unroll
+    for (int i = 0; i < 2 * RK; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (i < tiles) av[u][i][h] = load_wide(ap[i][h] + 8 * (threadIdx.x & 3) + k + 64 * u);
+        else av[u][i][h] = {};
+  }
+#pragma unroll
+  for (int u = 0; u < N; ++u)
+#pragma unroll
+    for (int i = 0; i < 2 * RK; ++i)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint4 &lo = av[u][i][0].v[q], &hi = av[u][i][1].v[q], &x = xv[u].v[q];
+        mma_bf16(acc[i][0], lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+        mma_bf16(acc[i][0], lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+      }
 }
 
 // N blocks of 32 columns from k on; in: whether this lane's columns exist.
@@ -226,9 +284,10 @@ __device__ __forceinline__ void put_sums(const float (&acc)[2 * RK][NT][4], int 
     }
 }
 
-// v of at most 8 tokens over blocks kfirst .. klast - 1 of 32 columns, into this
-// warp's partial sums [token][rank]; sixteen rows of A are under way at once, of
-// as many blocks as that makes.  Rows past the last rank and tokens past the last one
+// v of at most 8 tokens over the CTA's blocks kfirst .. klast - 1 of 32 columns, into
+// the warps' partial sums [token][rank].  Sixteen rows of A are under way at once, of
+// as many blocks as that makes; the warps take them in turn, so that they read up to a KB
+// of each row together.  Rows past the last rank and tokens past the last one
 // repeat that one: their sums are not used.
 template <int RK>
 __device__ __forceinline__ void shrink_few(const Params& p, const uint16_t* A, int rank, const int* mem, int64_t t0, int m,
@@ -242,12 +301,18 @@ __device__ __forceinline__ void shrink_few(const Params& p, const uint16_t* A, i
 #pragma unroll
     for (int h = 0; h < 2; ++h) ap[i][h] = A + (size_t)min(16 * i + 8 * h + g, rank - 1) * p.K + 8 * tq;
   xp[0] = p.x + (t0 + mem[min(g, m - 1)]) * p.ldx + 8 * tq;
-  const int whole = min(klast, p.K / 32);  // the blocks before it have no column past K
+  const int warp = threadIdx.x >> 5, whole = min(klast, p.K / 32);  // the blocks before it have no column past K
   int kb = kfirst;
+  if (RK <= 2 && p.wide_in) {
 #pragma unroll 1
-  for (; kb + U <= whole; kb += U) shrink_blocks<RK, 1, U>(ap, xp, kb * 32, true, tiles, acc);
+    for (; kb + U * kWarps <= whole; kb += U * kWarps)  // (8 tq more: 16 columns a lane)
+      shrink_wide<RK, U >= 2 ? U / 2 : 1>(ap, xp[0] + 8 * tq, (kb + U * warp) * 32, tiles, acc);
+  }
 #pragma unroll 1
-  for (; kb < klast; ++kb) shrink_blocks<RK, 1, 1>(ap, xp, kb * 32, kb * 32 + 8 * tq < p.K, tiles, acc);
+  for (; kb + U * kWarps <= whole; kb += U * kWarps)
+    shrink_blocks<RK, 1, U>(ap, xp, (kb + U * warp) * 32, true, tiles, acc);
+#pragma unroll 1
+  for (kb += warp; kb < klast; kb += kWarps) shrink_blocks<RK, 1, 1>(ap, xp, kb * 32, kb * 32 + 8 * tq < p.K, tiles, acc);
   put_sums<RK, 1>(acc, tiles, m, mine);
 }
 
@@ -262,7 +327,7 @@ __device__ __forceinline__ void shrink_many(const Params& p, const uint16_t* A, 
 #pragma unroll
   for (int j = 0; j < NT; ++j) row[j] = mem[min(8 * j + g, m - 1)];
 #pragma unroll 1
-  for (int kb = kfirst; kb < klast; ++kb) {
+  for (int kb = kfirst + (int)(threadIdx.x >> 5); kb < klast; kb += kWarps) {
     const int k = kb * 32 + 8 * tq;
     const bool in = k < p.K;
     uint4 xv[NT];
@@ -324,7 +389,7 @@ __device__ __forceinline__ void expand(const Params& p, const uint16_t* B, int r
   for (int ch = chunk0; ch < chunks; ch += stride) {
     const int n = ch * 32 + 8 * tq;
     uint4 w[4][RK];
-    load_b<RK>(p, B, rank, ch, w);
+    load_b<RK>(p, B, rank, ch * 32 + 8 * (g >> 1) + (g & 1), w);
 #pragma unroll 1
     for (int m0 = 0; m0 < m; m0 += 16 * U) {
       Raw<F32> y[U][H];
@@ -361,6 +426,70 @@ __device__ __forceinline__ void expand(const Params& p, const uint16_t* B, int r
   }
 }
 
+// The same for bf16 and at most 32 ranks in chunks of 64 columns, sixteen of them a lane:
+// whole 128-byte lines of y and out.
+template <int U>
+__device__ __forceinline__ void expand_wide(const Params& p, const uint16_t* B, int rank, const int64_t* yrow,
+                                            const int64_t* orow, int m, const __nv_bfloat16* vbuf, int vrows, int chunk0,
+                                            int chunks, int stride) {
+  using S = Shape<1>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  const __nv_bfloat16* v = vbuf + (size_t)g * S::kVRow + 8 * tq;
+  const int part = vrows * S::kVRow;
+  const uint16_t* y = reinterpret_cast<const uint16_t*>(p.y);
+  uint16_t* out = reinterpret_cast<uint16_t*>(p.out);
+#pragma unroll 1
+  for (int ch = chunk0; ch < chunks; ch += stride) {
+    const int n = ch * 64 + 16 * tq;
+    uint4 w[2][4][1];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) load_b<1>(p, B, rank, ch * 64 + 16 * (g >> 1) + 8 * q + (g & 1), w[q]);
+#pragma unroll 1
+    for (int m0 = 0; m0 < m; m0 += 16 * U) {
+      Wide in[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = m0 + 16 * u + 8 * h + g;
+          in[u][h] = {};
+          if (y && row < m && n < p.N) in[u][h] = load_wide_rw(y + yrow[row] + n);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (m0 + 16 * u >= m) break;
+        Wide o[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float d[4][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4& s = in[u][h].v[q];
+            d[0][2 * h] = bf16_lo(s.x), d[0][2 * h + 1] = bf16_hi(s.x), d[1][2 * h] = bf16_lo(s.y), d[1][2 * h + 1] = bf16_hi(s.y);
+            d[2][2 * h] = bf16_lo(s.z), d[2][2 * h + 1] = bf16_hi(s.z), d[3][2 * h] = bf16_lo(s.w), d[3][2 * h + 1] = bf16_hi(s.w);
+          }
+          product<1, 2, 2>(v + (m0 + 16 * u) * S::kVRow, part, rank, w[q], d);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 two = __floats2bfloat162_rn(d[j][2 * h], d[j][2 * h + 1]);
+              b[j] = *reinterpret_cast<const uint32_t*>(&two);
+            }
+            o[h].v[q] = make_uint4(b[0], b[1], b[2], b[3]);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = m0 + 16 * u + 8 * h + g;
+          if (row < m && n < p.N) store_wide(out + orow[row] + n, o[h]);
+        }
+      }
+    }
+  }
+}
+
 template <int RK, bool F32>
 __global__ void __launch_bounds__(kThreads, 2)
 lora_kernel(const __grid_constant__ Params p) {
@@ -369,7 +498,8 @@ lora_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) int ids[kTile];
   __shared__ unsigned long long slot_tokens[kTile];
-  __shared__ int slot_id[kTile], mem[kTile], leaders[2];
+  __shared__ int slot_id[kTile], mem[kTile], ranks[kTile], leaders[2];
+  __shared__ float factor[kTile];
   __shared__ int64_t yrow[kTile], orow[kTile];  // where the slot's tokens have their rows, in elements
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank_cta = p.cs > 1 ? (int)mx4::cluster_rank() : 0;
@@ -414,49 +544,52 @@ lora_kernel(const __grid_constant__ Params p) {
   }
   __syncthreads();
   const int slots = __popc((uint32_t)leaders[0]) + __popc((uint32_t)leaders[1]);
+  if (slot0 >= slots) return;  // the whole cluster
 
   float* parts = reinterpret_cast<float*>(smem);
   __nv_bfloat16* vbuf = reinterpret_cast<__nv_bfloat16*>(smem);  // after the partial sums
   const size_t psum_at = max(parts_bytes<RK>(p.rows), v_bytes<RK, SPLIT>(p.rows));
   float* psum = reinterpret_cast<float*>(smem + psum_at);        // [token][rank], read by the cluster
-  const int at_once = min(p.rows, 8 * S::kTokTiles), vrows = (p.rows + 15) / 16 * 16;
+  const int at_once = min(p.rows, 8 * S::kTokTiles), vrows = v_rows(p.rows);
+  float* mine = parts + (size_t)warp * at_once * S::kPartRow;
 
-  const int kblocks = (p.K + 31) / 32, kw = p.cs * kWarps;
-  const int kfirst = (int)((long long)kblocks * (rank_cta * kWarps + warp) / kw);
-  const int klast = (int)((long long)kblocks * (rank_cta * kWarps + warp + 1) / kw);
-  const int chunks = (p.N + 31) / 32, stride = p.parts * kw;  // of 32 columns
-  const int chunk0 = (part * p.cs + rank_cta) * kWarps + warp;
+  const int kblocks = (p.K + 31) / 32;  // this CTA's blocks of K
+  const int kfirst = (int)((long long)kblocks * rank_cta / p.cs), klast = (int)((long long)kblocks * (rank_cta + 1) / p.cs);
+  const int stride = p.parts * p.cs * kWarps, chunk0 = (part * p.cs + rank_cta) * kWarps + warp;  // of columns
 
+  // The tokens of this cluster's slots, slot by slot.
+  int total = 0;
   for (int slot = slot0; slot < slots; slot += p.lanes) {
-    const int id = slot_id[slot];
     const unsigned long long tokens = slot_tokens[slot];
-    const int m = __popcll(tokens);
     if (tid < kTile && ((tokens >> tid) & 1ull)) {
-      const int at = __popcll(tokens & ((1ull << tid) - 1));
+      const int at = total + __popcll(tokens & ((1ull << tid) - 1)), id = ids[tid];
       mem[at] = tid;
       yrow[at] = (t0 + tid) * p.ldy;
       orow[at] = (t0 + tid) * p.ldo;
+      ranks[at] = id < 0 ? 0 : p.ranks ? min(max(__ldg(p.ranks + id), 0), p.R) : p.R;
+      factor[at] = id >= 0 && p.scale ? __ldg(p.scale + id) : 1.f;
     }
-    int rank = 0;
-    if (id >= 0) rank = p.ranks ? min(max(__ldg(p.ranks + id), 0), p.R) : p.R;
-    const float c = id >= 0 && p.scale ? __ldg(p.scale + id) : 1.f;
-    __syncthreads();
-    const uint16_t* A = p.a + (size_t)(id < 0 ? 0 : id) * p.R * p.K;
-    const uint16_t* B = p.b + (size_t)(id < 0 ? 0 : id) * p.N * p.R;
+    total += __popcll(tokens);
+  }
+  __syncthreads();
 
+  // v of all of them
+  for (int slot = slot0, at = 0; slot < slots; slot += p.lanes) {
+    const int id = slot_id[slot], m = __popcll(slot_tokens[slot]), rank = ranks[at];
     if (rank > 0) {
+      const uint16_t* A = p.a + (size_t)id * p.R * p.K;
+      const uint16_t* B = p.b + (size_t)id * p.N * p.R;
       // what the second product will read is on its way to L2 meanwhile
       if (m <= 8)
-        for (int ch = chunk0; ch < chunks && ch < chunk0 + 4 * stride; ch += stride) {
-          if (lane == 0) bulk_prefetch_l2(B + (size_t)ch * 32 * p.R, (uint32_t)min(32, p.N - ch * 32) * p.R * 2);
-          if (p.y && lane < m) prefetch_l2(p.y + (yrow[lane] + ch * 32) * (F32 ? 4 : 2));
+        for (int n = chunk0 * 32; n < p.N && n < (chunk0 + 4 * stride) * 32; n += stride * 32) {
+          if (lane == 0) bulk_prefetch_l2(B + (size_t)n * p.R, (uint32_t)min(32, p.N - n) * p.R * 2);
+          if (p.y && lane < m) prefetch_l2(p.y + (yrow[at + lane] + n) * (F32 ? 4 : 2));
         }
-      float* mine = parts + (size_t)warp * at_once * S::kPartRow;
       const int used = (rank + 15) / 16 * 16;
       for (int c0 = 0; c0 < m; c0 += 8 * S::kTokTiles) {  // tokens at once
         const int mt = min(m - c0, 8 * S::kTokTiles);
-        if (mt <= 8) shrink_few<RK>(p, A, rank, mem + c0, t0, mt, kfirst, klast, mine);
-        else shrink_many<RK>(p, A, rank, mem + c0, t0, mt, kfirst, klast, mine);
+        if (mt <= 8) shrink_few<RK>(p, A, rank, mem + at + c0, t0, mt, kfirst, klast, mine);
+        else shrink_many<RK>(p, A, rank, mem + at + c0, t0, mt, kfirst, klast, mine);
         __syncthreads();
         for (int e = tid; e < mt * (used / 4); e += kThreads) {  // four ranks of a token
           const int tok = e / (used / 4), r = (e - tok * (used / 4)) * 4;
@@ -466,58 +599,77 @@ lora_kernel(const __grid_constant__ Params p) {
             const float4 v = *reinterpret_cast<const float4*>(parts + ((size_t)w * at_once + tok) * S::kPartRow + r);
             s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
           }
-          *reinterpret_cast<float4*>(psum + (c0 + tok) * S::kRanks + r) = s;
+          *reinterpret_cast<float4*>(psum + (at + c0 + tok) * S::kRanks + r) = s;
         }
         __syncthreads();
       }
-      if (p.cs > 1) cluster_sync_all();  // every CTA's sums are there
-      // c v in bf16 parts, zeros up to whole MMAs
-      const int blocks = (rank + 31) / 32, rows = (m + 15) / 16 * 16;
-      for (int e = tid; e < rows * blocks * 8; e += kThreads) {
-        const int tok = e / (blocks * 8), r = (e - tok * (blocks * 8)) * 4;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (tok < m && r < used) {
-          const uint32_t at = smem_u32(psum + tok * S::kRanks + r);
-          if (p.cs > 1) {
-            float4 u[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (q < p.cs) u[q] = dsmem_ld_f4(dsmem_addr_u32(at, q));
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (q < p.cs) v[0] += u[q].x, v[1] += u[q].y, v[2] += u[q].z, v[3] += u[q].w;
-          } else {
-            const float4 u = *reinterpret_cast<const float4*>(psum + tok * S::kRanks + r);
-            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-          }
-        }
-        uint32_t w[SPLIT][2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float rest = r + i < rank ? v[i] * c : 0.f;
-#pragma unroll
-          for (int s = 0; s < SPLIT; ++s) {
-            const __nv_bfloat16 h = __float2bfloat16_rn(rest);
-            const uint32_t bits = __bfloat16_as_ushort(h);
-            if (i & 1) w[s][i / 2] |= bits << 16;
-            else w[s][i / 2] = bits;
-            // an infinity stays one: its rest would be infinity - infinity
-            rest = isfinite(__bfloat162float(h)) ? rest - __bfloat162float(h) : 0.f;
-          }
-        }
-#pragma unroll
-        for (int s = 0; s < SPLIT; ++s)
-          *reinterpret_cast<uint2*>(vbuf + ((size_t)s * vrows + tok) * S::kVRow + r) = make_uint2(w[s][0], w[s][1]);
-      }
-      __syncthreads();
     }
-    if (!p.vec) expand<RK, F32, false, 2, 1>(p, B, rank, yrow, orow, m, vbuf, vrows, chunk0, chunks, stride);
-    else if (m <= 8) expand<RK, F32, true, 1, 1>(p, B, rank, yrow, orow, m, vbuf, vrows, chunk0, chunks, stride);
-    else expand<RK, F32, true, 2, F32 || RK == 4 ? 2 : 4>(p, B, rank, yrow, orow, m, vbuf, vrows, chunk0, chunks, stride);
-    // the sums have been read everywhere, mem and v here, before they are written again (or the CTA leaves)
-    if (p.cs > 1 && rank > 0) cluster_sync_all();
-    else __syncthreads();
+    at += m;
   }
+  if (p.cs > 1) cluster_sync_all();  // every CTA's sums are there
+  // c v in bf16 parts, zeros behind the ranks
+  for (int e = tid; e < total * (S::kRanks / 4); e += kThreads) {
+    const int tok = e / (S::kRanks / 4), r = (e - tok * (S::kRanks / 4)) * 4, rank = ranks[tok];
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r < rank) {
+      const uint32_t at = smem_u32(psum + tok * S::kRanks + r);
+      if (p.cs > 1) {
+        float4 u[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < p.cs) u[q] = dsmem_ld_f4(dsmem_addr_u32(at, q));
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < p.cs) v[0] += u[q].x, v[1] += u[q].y, v[2] += u[q].z, v[3] += u[q].w;
+      } else {
+        const float4 u = *reinterpret_cast<const float4*>(psum + tok * S::kRanks + r);
+        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+      }
+    }
+    uint32_t w[SPLIT][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float rest = r + i < rank ? v[i] * factor[tok] : 0.f;
+#pragma unroll
+      for (int s = 0; s < SPLIT; ++s) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(rest);
+        const uint32_t bits = __bfloat16_as_ushort(h);
+        if (i & 1) w[s][i / 2] |= bits << 16;
+        else w[s][i / 2] = bits;
+        // an infinity stays one: its rest would be infinity - infinity
+        rest = isfinite(__bfloat162float(h)) ? rest - __bfloat162float(h) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < SPLIT; ++s)
+      *reinterpret_cast<uint2*>(vbuf + ((size_t)s * vrows + tok) * S::kVRow + r) = make_uint2(w[s][0], w[s][1]);
+  }
+  __syncthreads();
+  if (p.cs > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // has read the others' sums
+
+  // out of all of them (an MMA reads the rows of up to 15 tokens behind a slot's last one: their sums are not used)
+  for (int slot = slot0, at = 0; slot < slots; slot += p.lanes) {
+    const int id = slot_id[slot], m = __popcll(slot_tokens[slot]), rank = ranks[at];
+    const uint16_t* B = p.b + (size_t)(id < 0 ? 0 : id) * p.N * p.R;
+    const __nv_bfloat16* v = vbuf + (size_t)at * S::kVRow;
+    const int64_t *yr = yrow + at, *og = orow + at;
+    const int chunks = (p.N + 31) / 32;
+    if (!p.vec) {
+      expand<RK, F32, false, 2, 1>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride);
+    } else if (m <= 8) {
+      expand<RK, F32, true, 1, 1>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride);
+    } else {
+      bool wide = false;
+      if constexpr (RK == 1 && !F32) {
+        wide = p.wide_out;
+        if (wide) expand_wide<2>(p, B, rank, yr, og, m, v, vrows, chunk0, (p.N + 63) / 64, stride);
+      }
+      if (!wide) expand<RK, F32, true, 2, F32 || RK == 4 ? 2 : 4>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride);
+    }
+    at += m;
+  }
+  // no CTA leaves while another may still read its sums
+  if (p.cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // The cut: a launch in one wave if it can be.  Clusters of 8 CTAs, fewer when there are more
@@ -619,6 +771,9 @@ extern "C" qsm_status lora_add(const qsm_lora* L, const uint16_t* x, int64_t ldx
   p.rows = T < kTile ? (T + 7) / 8 * 8 : kTile;
   const int64_t wide = 16 / (int64_t)el < 8 ? 4 : 8;
   p.vec = N % 8 == 0 && on(out, 16) && ldo % wide == 0 && (!y || (on(y, 16) && ldy % wide == 0));
+  const auto on32 = [&](const void* q) { return on(q, 32); };
+  p.wide_in = on32(x) && on32(L->a) && L->K % 16 == 0 && ldx % 16 == 0;
+  p.wide_out = dtype == QSM_BF16 && N % 16 == 0 && on32(out) && ldo % 16 == 0 && (!y || (on32(y) && ldy % 16 == 0));
   p.copy = !same;
   p.status = dev_status;
   return L->rank <= 32 ? launch<1>(p, dtype == QSM_FP32, stream)

@@ -229,3 +229,25 @@ def test_refusals(qsm):
             qsm.LoraAdapters(**bad)
     with pytest.raises(AttributeError):
         L.a = a.clone()
+
+
+@pytest.mark.parametrize("off", [0, 8, 16])
+@pytest.mark.parametrize("K,N", [(4096, 2048), (4104, 2056), (8192, 96)])
+def test_rows_on_every_16_bytes(qsm, off, K, N):
+    """a, x, y and out at addresses and strides that are or are not multiples of 32 bytes."""
+    n, R = 2, 16
+    def view(shape, seed, dtype=torch.bfloat16, pad=off):
+        t = torch.empty(shape[0], shape[1] + pad, dtype=dtype, device="cuda").fill_(float("nan"))
+        t[:, pad:] = randn(*shape, seed=seed).to(dtype) * shape[1] ** -0.5
+        return t[:, pad:]
+    buf = torch.empty(n * R * K + 16, dtype=torch.bfloat16, device="cuda")
+    a = buf[off:off + n * R * K].view(n, R, K)
+    a.copy_(randn(n, R, K, seed=1) * K ** -0.5)
+    L = qsm.LoraAdapters(a, (randn(n, N, R, seed=2) / 4).bfloat16())
+    for T in (5, 40):
+        x, y = view((T, K), 3), view((T, N), 4)
+        out = torch.full((T, N + off), 7.0, dtype=torch.bfloat16, device="cuda")
+        ids = (torch.arange(T, device="cuda") % 3 - 1).int()
+        qsm.lora_add(x, L, ids, y, out=out[:, off:])
+        want, err = definition(x, L, ids, y, torch.bfloat16)
+        assert ref.lies_between(out[:, off:], want, err) and (out[:, :off] == 7).all()
