@@ -75,6 +75,13 @@ def _load():
     return _lib
 
 
+def _ld(t: torch.Tensor, shape, dev: int, what: str) -> int:
+    """The row stride of a matrix of that shape on the device, rows contiguous."""
+    if t.shape != shape or t.get_device() != dev:
+        raise QSMError(f"{what} must be {list(shape)} on the same device")
+    return shape[1] if t.is_contiguous() else _matrix(t, what)[3]
+
+
 # ------------------------------------------------------------------- norms
 
 class Norm(_Fixed):
@@ -137,51 +144,49 @@ class ResidualNorm(_Fixed):
                 where to write it: a tensor (x or y itself is fine) or an Mx4Tensor.  Without a
                 pre there is no h, and None is returned."""
         what = "ResidualNorm"
-        dev, T, H, ldx = _matrix(x, what)
-        xt = _DTYPES.get(x.dtype)
-        if xt is None or H != self.H or dev != self.device:
-            raise QSMError(f"{what}: x must be [T, {self.H}] bf16, fp16 or fp32 on cuda:{self.device}")
+        shape, dev, xt = x.shape, self.device, _DTYPES.get(x.dtype)
+        if xt is None or len(shape) != 2 or shape[1] != self.H or x.get_device() != dev:
+            raise QSMError(f"{what}: x must be [T, {self.H}] bf16, fp16 or fp32 on cuda:{dev}")
+        T, H = shape
+        ldx = H if x.is_contiguous() else _matrix(x, what)[3]
         on = _handle(dev, stream, what)
         yp = gp = op = hp = sp = None
-        yt = gt = gate_kind = ldy = ldg = ldo = ldh = 0
+        yt = gt = gate_kind = ldy = ldg = ldo = ht = ldh = 0
         if y is not None:
-            ydev, rows, cols, ldy = _matrix(y, what + ": y")
             yt = _DTYPES.get(y.dtype)
-            if yt is None or rows != T or cols != H or ydev != dev:
-                raise QSMError(f"{what}: y must be [T, H] bf16, fp16 or fp32 on x's device")
+            if yt is None:
+                raise QSMError(f"{what}: y must be bf16, fp16 or fp32")
+            ldy = _ld(y, shape, dev, "ResidualNorm: y")
             yp = y.data_ptr()
         if gate is not None:
-            gt = _DTYPES.get(gate.dtype)
-            shape = gate.shape
+            gt, gs = _DTYPES.get(gate.dtype), gate.shape
             if y is None or gt is None or gate.get_device() != dev:
                 raise QSMError(f"{what}: a gate needs a y, and must be bf16, fp16 or fp32 on x's device")
-            if len(shape) == 1 and shape[0] == H and gate.is_contiguous():
-                gate_kind, ldg = 1, 0
-            elif len(shape) == 2 and shape[0] == T and shape[1] == 1 != H:
+            if len(gs) == 1 and gs[0] == H and gate.is_contiguous():
+                gate_kind = 1
+            elif len(gs) == 2 and gs[0] == T and gs[1] == 1 != H:
                 gate_kind, ldg = 2, gate.stride(0)
-            elif len(shape) == 2 and shape[0] == T and shape[1] == H:
-                gate_kind, ldg = 1, _matrix(gate, what + ": gate")[3]
+            elif gs == shape:
+                gate_kind, ldg = 1, _ld(gate, shape, dev, "ResidualNorm: gate")
             else:
                 raise QSMError(f"{what}: gate must be [H], [T, 1] or [T, H]")
             gp = gate.data_ptr()
-        if x_out is None:
-            if y is not None:
-                x_out = _empty(T, H, x.dtype, stream)
-                op, ldo = x_out.data_ptr(), H
-        else:
-            odev, rows, cols, ldo = _matrix(x_out, what + ": x_out")
-            if x_out.dtype != x.dtype or rows != T or cols != H or odev != dev:
-                raise QSMError(f"{what}: x_out must be [T, H] of x's type and device")
+        if x_out is not None:
+            if x_out.dtype != x.dtype:
+                raise QSMError(f"{what}: x_out must be of x's type")
+            ldo = _ld(x_out, shape, dev, "ResidualNorm: x_out")
             op = x_out.data_ptr()
-        ht = 0
+        elif y is not None:
+            x_out = _empty(T, H, x.dtype, stream)
+            op, ldo = x_out.data_ptr(), H
         if self.pre is None:
             if h is not None:
                 raise QSMError(f"{what}: without a pre there is no h")
         elif isinstance(h, torch.Tensor):
-            hdev, rows, cols, ldh = _matrix(h, what + ": h")
             ht = _DTYPES.get(h.dtype)
-            if ht is None or rows != T or cols != H or hdev != dev:
-                raise QSMError(f"{what}: h must be [T, H] bf16, fp16 or fp32 on x's device")
+            if ht is None:
+                raise QSMError(f"{what}: h must be bf16, fp16 or fp32")
+            ldh = _ld(h, shape, dev, "ResidualNorm: h")
             hp = h.data_ptr()
         elif isinstance(h, Mx4Tensor) or h == "mx4":
             ht = _MX4
@@ -292,11 +297,12 @@ def moe_route_scores(x: torch.Tensor, router: MoERouter, topk_idx=None, topk_w=N
     """The router's choice for x [T, H] bf16 (rows contiguous) -> (topk_idx [T, k] int32,
     topk_w [T, k] fp32)."""
     what = "moe_route_scores"
-    dev, T, H, ldx = _matrix(x, what)
-    if x.dtype is not torch.bfloat16 or H != router.H or dev != router.device:
+    shape, dev, k = x.shape, router.device, router.k
+    if x.dtype is not torch.bfloat16 or len(shape) != 2 or shape[1] != router.H or x.get_device() != dev:
         raise QSMError(f"{what}: x must be [T, {router.H}] bf16 on the router's device")
+    T = shape[0]
+    ldx = shape[1] if x.is_contiguous() else _matrix(x, what)[3]
     on = _handle(dev, stream, what)
-    k = router.k
     if topk_idx is None:
         topk_idx = _empty(T, k, torch.int32, stream)
     elif (topk_idx.dtype is not torch.int32 or tuple(topk_idx.shape) != (T, k)
@@ -358,30 +364,27 @@ def lora_add(x: torch.Tensor, adapters: LoraAdapters, ids: torch.Tensor, y=None,
       y  the projection's output, bf16 or fp32, or None (zeros: then dtype, or out's
          type, or bf16);  out  None (a new tensor) or where to write: y itself is fine"""
     what = "lora_add"
-    dev, T, K, ldx = _matrix(x, what)
-    if x.dtype is not torch.bfloat16 or K != adapters.K or dev != adapters.device:
+    shape, dev, N = x.shape, adapters.device, adapters.N
+    if x.dtype is not torch.bfloat16 or len(shape) != 2 or shape[1] != adapters.K or x.get_device() != dev:
         raise QSMError(f"{what}: x must be [T, {adapters.K}] bf16 on the adapters' device")
-    if (ids.dtype is not torch.int32 or ids.dim() != 1 or ids.shape[0] != T or not ids.is_contiguous()
-            or ids.get_device() != dev):
+    T = shape[0]
+    ldx = shape[1] if x.is_contiguous() else _matrix(x, what)[3]
+    if ids.dtype is not torch.int32 or ids.shape != (T,) or not ids.is_contiguous() or ids.get_device() != dev:
         raise QSMError(f"{what}: ids must be a contiguous int32 [T] on x's device")
     on = _handle(dev, stream, what)
-    N = adapters.N
     kind = y.dtype if y is not None else out.dtype if out is not None else dtype or torch.bfloat16
     dt = _LORA_DTYPES.get(kind)
     if dt is None or (dtype is not None and dtype != kind):
         raise QSMError(f"{what}: y and out must be bf16 or fp32, and of dtype where it is given")
     yp, ldy = None, 0
     if y is not None:
-        ydev, rows, cols, ldy = _matrix(y, what + ": y")
-        if rows != T or cols != N or ydev != dev:
-            raise QSMError(f"{what}: y must be [T, N] on x's device")
-        yp = y.data_ptr()
+        yp, ldy = y.data_ptr(), _ld(y, (T, N), dev, "lora_add: y")
     if out is None:
         out, ldo = _empty(T, N, kind, stream), N
     else:
-        odev, rows, cols, ldo = _matrix(out, what + ": out")
-        if out.dtype != kind or rows != T or cols != N or odev != dev:
-            raise QSMError(f"{what}: out must be [T, N] of y's type and device")
+        if out.dtype != kind:
+            raise QSMError(f"{what}: out must be of y's type")
+        ldo = _ld(out, (T, N), dev, "lora_add: out")
     rc = (_lib or _load()).lora_add(
         adapters.ref, x.data_ptr(), ldx, T, ids.data_ptr(), dt, yp, ldy, out.data_ptr(), ldo,
         _status(dev_status, dev, what), on)
