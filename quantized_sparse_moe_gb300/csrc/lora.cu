@@ -35,9 +35,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 64;    // tokens
+constexpr int kTile = 64;    // tokens, at most
 constexpr int kMaxRank = 128;
 constexpr int kMaxSide = 1 << 28;  // of K and N
+constexpr int kMostSmem = 200 * 1024;  // dynamic
 
 struct Params {
   const uint16_t* x;
@@ -51,9 +52,10 @@ struct Params {
   int64_t ldx, ldy, ldo;  // elements
   int T, K, N, R, n;      // R: ranks that an adapter has room for
   int cs, lanes, parts;   // CTAs of a cluster, slots' lanes S, column parts NS
-  int rows;               // tokens of a tile, rounded up to 8: what the buffers hold
+  int tile, rows;         // tokens of a tile, and that rounded up to 8: what the buffers hold
   int vec;                // whether eight columns of y and out can be one access
-  int wide_in, wide_out;  // whether sixteen of a and x, and of bf16 y and out, can be one access
+  int wide_in, wide_out;  // whether 32 bytes of a and x, and of out, can be one access
+  int units;              // whether there is shared memory for units of y
   int copy;               // whether tokens without an adapter have to be copied
   int32_t* status;
 };
@@ -86,6 +88,9 @@ struct Shape {
   static constexpr int kVRow = kRanks + (RK == 1 ? 0 : 32);  // bf16: rows 16 banks apart
 };
 
+// A warp's units of y (16 rows of 128 bytes), three of them, and 64 rows of B.
+constexpr int kUnitBytes = 16 * 128, kUnits = 3, kWarpBytes = kUnits * kUnitBytes + 64 * 64;
+
 // Bytes of shared memory for tiles of `rows` tokens.
 template <int RK>
 __host__ __device__ constexpr size_t parts_bytes(int rows) {
@@ -97,10 +102,21 @@ template <int RK, int SPLIT>
 __host__ __device__ constexpr size_t v_bytes(int rows) {
   return (size_t)SPLIT * v_rows(rows) * Shape<RK>::kVRow * 2;
 }
+// Where v and the CTA's sums lie: v over the partial sums, which have been read by
+// then; where there are units of y, those come over the partial sums, and v behind.
 template <int RK, int SPLIT>
-__host__ __device__ constexpr size_t smem_bytes(int rows) {
-  const size_t a = parts_bytes<RK>(rows), b = v_bytes<RK, SPLIT>(rows);
-  return (a > b ? a : b) + (size_t)rows * Shape<RK>::kRanks * 4;
+__host__ __device__ constexpr size_t v_at(int rows, bool units) {
+  const size_t a = parts_bytes<RK>(rows), b = (size_t)kWarps * kWarpBytes;
+  return RK == 1 && units ? (a > b ? a : b) : 0;
+}
+template <int RK, int SPLIT>
+__host__ __device__ constexpr size_t sums_at(int rows, bool units) {
+  const size_t a = parts_bytes<RK>(rows), b = v_at<RK, SPLIT>(rows, units) + v_bytes<RK, SPLIT>(rows);
+  return a > b ? a : b;
+}
+template <int RK, int SPLIT>
+__host__ __device__ constexpr size_t smem_bytes(int rows, bool units) {
+  return sums_at<RK, SPLIT>(rows, units) + (size_t)rows * Shape<RK>::kRanks * 4;
 }
 
 // Eight columns of y or out in one row, as they lie in memory.
@@ -195,21 +211,6 @@ __device__ __forceinline__ Wide load_wide(const uint16_t* p) {
                  "=r"(w.v[1].z), "=r"(w.v[1].w)
                : "l"(p));
   return w;
-}
-
-// The same of memory that this launch writes, and the store.
-__device__ __forceinline__ Wide load_wide_rw(const uint16_t* p) {
-  Wide w;
-  asm volatile("ld.global.L2::256B.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(w.v[0].x), "=r"(w.v[0].y), "=r"(w.v[0].z), "=r"(w.v[0].w), "=r"(w.v[1].x), "=r"(w.v[1].y),
-                 "=r"(w.v[1].z), "=r"(w.v[1].w)
-               : "l"(p));
-  return w;
-}
-__device__ __forceinline__ void store_wide(uint16_t* p, const Wide& w) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w.v[0].x), "r"(w.v[0].y), "r"(w.v[0].z),
-               "r"(w.v[0].w), "r"(w.v[1].x), "r"(w.v[1].y), "r"(w.v[1].z), "r"(w.v[1].w)
-               : "memory");
 }
 
 // N blocks of 64 columns from k on, 16 of them a lane: whole 128-byte lines of the
@@ -426,68 +427,143 @@ __device__ __forceinline__ void expand(const Params& p, const uint16_t* B, int r
   }
 }
 
-// The same for bf16 and at most 32 ranks in chunks of 64 columns, sixteen of them a lane:
-// whole 128-byte lines of y and out.
-template <int U>
-__device__ __forceinline__ void expand_wide(const Params& p, const uint16_t* B, int rank, const int64_t* yrow,
-                                            const int64_t* orow, int m, const __nv_bfloat16* vbuf, int vrows, int chunk0,
-                                            int chunks, int stride) {
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last n groups of this thread's copies have landed.
+template <int n>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
+// The same for adapters of at most 32 ranks and more than 8 tokens.  A warp works on
+// units of 16 tokens and 128 bytes of their rows (64 columns, 32 of fp32), whole
+// lines; two units' y and the next columns' rows of B are on their way into the warp's own
+// shared memory while one is worked on.  (With y straight into registers the loads waited for
+// the MMAs and stores before them: 4096 x 8192 bf16 33 us without an adapter, a plain copy 21.)
+template <bool F32>
+__device__ __forceinline__ void expand_units(const Params& p, const uint16_t* B, int rank, const int64_t* yrow,
+                                             const int64_t* orow, int m, const __nv_bfloat16* vbuf, int vrows, int chunk0,
+                                             int stride, unsigned char* mine) {
   using S = Shape<1>;
+  constexpr int kEl = F32 ? 4 : 2, kCols = 128 / kEl, Q = kCols / 32, SPLIT = F32 ? 3 : 2;
   const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  const __nv_bfloat16* v = vbuf + (size_t)g * S::kVRow + 8 * tq;
-  const int part = vrows * S::kVRow;
-  const uint16_t* y = reinterpret_cast<const uint16_t*>(p.y);
-  uint16_t* out = reinterpret_cast<uint16_t*>(p.out);
+  const int chunks = (p.N + kCols - 1) / kCols, tiles = (m + 15) / 16;
+  const int total = chunk0 < chunks ? ((chunks - chunk0 + stride - 1) / stride) * tiles : 0;
+  unsigned char* bbuf = mine + kUnits * kUnitBytes;
+  const auto columns = [&](int u) { return (chunk0 + u / tiles * stride) * kCols; };
+  // 16 bytes c of row r of a unit lie at unit c ^ (r & 7) of the row: eight lanes' reads are in different banks
+  const auto fetch = [&](int u) {
+    if (u < total && p.y) {
+      const int n = columns(u) + (lane & 7) * (16 / kEl), mt = u % tiles * 16;
+      unsigned char* to = mine + u % kUnits * kUnitBytes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = (lane >> 3) + 4 * i;
+        if (mt + r < m && n < p.N) copy16(to + r * 128 + (((lane & 7) ^ (r & 7)) << 4), p.y + (yrow[mt + r] + n) * kEl);
+      }
+    }
+    copies_commit();
+  };
+  const auto fetch_b = [&](int n0) {  // rows of B as they are, R ranks each
+    if (rank > 0 && n0 < p.N)
+      for (int i = lane; i < min(kCols, p.N - n0) * p.R / 8; i += 32) copy16(bbuf + i * 16, B + (size_t)n0 * p.R + i * 8);
+  };
+  fetch_b(columns(0));
+  fetch(0);
+  fetch(1);
+  uint4 w[Q][4];
 #pragma unroll 1
-  for (int ch = chunk0; ch < chunks; ch += stride) {
-    const int n = ch * 64 + 16 * tq;
-    uint4 w[2][4][1];
+  for (int u = 0; u < total; ++u) {
+    const int n0 = columns(u), mt = u % tiles * 16;
+    if (tiles == 1) copies_wait<0>();  // (the rows of B came with the last unit)
+    else copies_wait<1>();
+    __syncwarp();
+    if (mt == 0) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) load_b<1>(p, B, rank, ch * 64 + 16 * (g >> 1) + 8 * q + (g & 1), w[q]);
-#pragma unroll 1
-    for (int m0 = 0; m0 < m; m0 += 16 * U) {
-      Wide in[U][2];
+      for (int q = 0; q < Q; ++q)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = m0 + 16 * u + 8 * h + g;
-          in[u][h] = {};
-          if (y && row < m && n < p.N) in[u][h] = load_wide_rw(y + yrow[row] + n);
+        for (int j = 0; j < 4; ++j) {
+          // the lane's columns of a unit are 8 Q tq .. 8 Q tq + 8 Q - 1; past the last column it repeats
+          const int n = min(8 * Q * (g >> 1) + 8 * q + 2 * j + (g & 1), p.N - 1 - n0);
+          w[q][j] = make_uint4(0, 0, 0, 0);
+          if (8 * tq < rank) w[q][j] = first_of(*reinterpret_cast<const uint4*>(bbuf + (n * p.R + 8 * tq) * 2), rank - 8 * tq);
         }
+      __syncwarp();
+      fetch_b(n0 + stride * kCols);
+    }
+    const unsigned char* from = mine + u % kUnits * kUnitBytes;
+    Raw<true> y[2];  // 32 bytes
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (m0 + 16 * u >= m) break;
-        Wide o[2];
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float d[4][4];
+      for (int i = 0; i < 2; ++i)
+        y[h].v[i] = p.y ? *reinterpret_cast<const uint4*>(from + (8 * h + g) * 128 + (((2 * tq + i) ^ g) << 4)) : make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    fetch(u + 2);  // over the unit before this one
+    const __nv_bfloat16* vr = vbuf + (size_t)(mt + g) * S::kVRow + 8 * tq;
+    uint4 v[SPLIT][2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4& s = in[u][h].v[q];
-            d[0][2 * h] = bf16_lo(s.x), d[0][2 * h + 1] = bf16_hi(s.x), d[1][2 * h] = bf16_lo(s.y), d[1][2 * h + 1] = bf16_hi(s.y);
-            d[2][2 * h] = bf16_lo(s.z), d[2][2 * h + 1] = bf16_hi(s.z), d[3][2 * h] = bf16_lo(s.w), d[3][2 * h + 1] = bf16_hi(s.w);
+    for (int s = 0; s < SPLIT; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[s][h] = *reinterpret_cast<const uint4*>(vr + (size_t)(s * vrows + 8 * h) * S::kVRow);
+    Raw<true> o[2];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float d[4][4];
+      // bf16: the sum begins with y; fp32: y comes last (see expand)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t pair = F32 ? 0x80008000u : reinterpret_cast<const uint32_t*>(y[h].v)[4 * q + j];
+          d[j][2 * h] = bf16_lo(pair);
+          d[j][2 * h + 1] = bf16_hi(pair);
+        }
+      if (rank > 0) {
+#pragma unroll
+        for (int s = SPLIT - 1; s >= 0; --s)  // the small parts first
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mma_bf16(d[j], v[s][0].x, v[s][1].x, v[s][0].y, v[s][1].y, w[q][j].x, w[q][j].y);
+            mma_bf16(d[j], v[s][0].z, v[s][1].z, v[s][0].w, v[s][1].w, w[q][j].z, w[q][j].w);
           }
-          product<1, 2, 2>(v + (m0 + 16 * u) * S::kVRow, part, rank, w[q], d);
+      }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t b[4];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 two = __floats2bfloat162_rn(d[j][2 * h], d[j][2 * h + 1]);
-              b[j] = *reinterpret_cast<const uint32_t*>(&two);
-            }
-            o[h].v[q] = make_uint4(b[0], b[1], b[2], b[3]);
+        for (int j = 0; j < 4; ++j) {
+          uint32_t* out = reinterpret_cast<uint32_t*>(o[h].v);
+          if (F32) {
+            const uint32_t* in = reinterpret_cast<const uint32_t*>(y[h].v);
+            out[2 * j] = __float_as_uint(__uint_as_float(in[2 * j]) + d[j][2 * h]);
+            out[2 * j + 1] = __float_as_uint(__uint_as_float(in[2 * j + 1]) + d[j][2 * h + 1]);
+          } else {
+            const __nv_bfloat162 two = __floats2bfloat162_rn(d[j][2 * h], d[j][2 * h + 1]);
+            out[4 * q + j] = *reinterpret_cast<const uint32_t*>(&two);
           }
         }
+    }
+    const int n = n0 + 8 * Q * tq;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = m0 + 16 * u + 8 * h + g;
-          if (row < m && n < p.N) store_wide(out + orow[row] + n, o[h]);
-        }
+    for (int h = 0; h < 2; ++h) {
+      const int row = mt + 8 * h + g;
+      if (row >= m) continue;
+      char* to = p.out + (orow[row] + n) * kEl;
+      if (p.wide_out && n + 8 * Q <= p.N) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(o[h].v[0].x), "r"(o[h].v[0].y),
+                     "r"(o[h].v[0].z), "r"(o[h].v[0].w), "r"(o[h].v[1].x), "r"(o[h].v[1].y), "r"(o[h].v[1].z), "r"(o[h].v[1].w)
+                     : "memory");
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (n + i * (16 / kEl) < p.N) reinterpret_cast<uint4*>(to)[i] = o[h].v[i];
       }
     }
   }
+  copies_wait<0>();
+  __syncwarp();
 }
 
 template <int RK, bool F32>
@@ -507,8 +583,8 @@ lora_kernel(const __grid_constant__ Params p) {
   const int part = cl % p.parts;
   cl /= p.parts;
   const int slot0 = cl % p.lanes;
-  const int64_t t0 = (int64_t)(cl / p.lanes) * kTile;
-  const int count = (int)min((int64_t)kTile, p.T - t0);
+  const int64_t t0 = (int64_t)(cl / p.lanes) * p.tile;
+  const int count = (int)min((int64_t)p.tile, p.T - t0);
   pdl_wait();
   pdl_launch_dependents();
 
@@ -547,9 +623,8 @@ lora_kernel(const __grid_constant__ Params p) {
   if (slot0 >= slots) return;  // the whole cluster
 
   float* parts = reinterpret_cast<float*>(smem);
-  __nv_bfloat16* vbuf = reinterpret_cast<__nv_bfloat16*>(smem);  // after the partial sums
-  const size_t psum_at = max(parts_bytes<RK>(p.rows), v_bytes<RK, SPLIT>(p.rows));
-  float* psum = reinterpret_cast<float*>(smem + psum_at);        // [token][rank], read by the cluster
+  __nv_bfloat16* vbuf = reinterpret_cast<__nv_bfloat16*>(smem + v_at<RK, SPLIT>(p.rows, p.units));
+  float* psum = reinterpret_cast<float*>(smem + sums_at<RK, SPLIT>(p.rows, p.units));  // [token][rank], read by the cluster
   const int at_once = min(p.rows, 8 * S::kTokTiles), vrows = v_rows(p.rows);
   float* mine = parts + (size_t)warp * at_once * S::kPartRow;
 
@@ -659,12 +734,8 @@ lora_kernel(const __grid_constant__ Params p) {
     } else if (m <= 8) {
       expand<RK, F32, true, 1, 1>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride);
     } else {
-      bool wide = false;
-      if constexpr (RK == 1 && !F32) {
-        wide = p.wide_out;
-        if (wide) expand_wide<2>(p, B, rank, yr, og, m, v, vrows, chunk0, (p.N + 63) / 64, stride);
-      }
-      if (!wide) expand<RK, F32, true, 2, F32 || RK == 4 ? 2 : 4>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride);
+      if constexpr (RK == 1) expand_units<F32>(p, B, rank, yr, og, m, v, vrows, chunk0, stride, smem + warp * kWarpBytes);
+      else expand<RK, F32, true, 2, F32 || RK == 4 ? 2 : 4>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride);
     }
     at += m;
   }
@@ -674,29 +745,40 @@ lora_kernel(const __grid_constant__ Params p) {
 
 // The cut: a launch in one wave if it can be.  Clusters of 8 CTAs, fewer when there are more
 // tiles and slots than such clusters fit on the device at once (a GB300, two CTAs
-// an SM: 36 of 8, 74 of 4, 152 of 2); as many slots' lanes as a tile can have
-// slots while they fit; and columns in parts while SMs would be idle.
+// an SM: 36 of 8, 74 of 4, 152 of 2).  More than 64 tokens: tiles of as many as give each of
+// those clusters one, 16 to 64 (4096 tokens: 74 tiles of 56).  As many slots' lanes
+// as a tile can have slots while they fit; and columns in parts while SMs would be idle.
 template <int RK>
 qsm_status launch(Params& p, bool f32, cudaStream_t stream) {
   auto* kernel = f32 ? lora_kernel<RK, true> : lora_kernel<RK, false>;
-  const size_t smem = f32 ? smem_bytes<RK, 3>(p.rows) : smem_bytes<RK, 2>(p.rows);
-  const size_t most = f32 ? smem_bytes<RK, 3>(kTile) : smem_bytes<RK, 2>(kTile);
+  p.units = p.vec && p.T > 8;
+  const auto smem_of = [&](int rows) { return (int)(f32 ? smem_bytes<RK, 3>(rows, p.units) : smem_bytes<RK, 2>(rows, p.units)); };
   const auto resident = [&](int cs) {
-    return (long long)mx4::resident_clusters(reinterpret_cast<void*>(kernel), cs, kThreads, (int)smem, (int)most) * (cs == 1 ? 2 : 1);
+    return (long long)mx4::resident_clusters(reinterpret_cast<void*>(kernel), cs, kThreads, smem_of(p.rows), kMostSmem) *
+           (cs == 1 ? 2 : 1);
   };
-  const long long tiles = ((long long)p.T + kTile - 1) / kTile;
-  const int in_tile = p.T < kTile ? p.T : kTile, slots = p.n + 1ll < in_tile ? p.n + 1 : in_tile;
+  const auto tiles_of = [&](int tile) { return ((long long)p.T + tile - 1) / tile; };
+  p.tile = p.T < kTile ? p.T : kTile;
+  p.rows = (p.tile + 7) / 8 * 8;
+  const int one = p.n + 1ll < p.tile ? p.n + 1 : p.tile;  // slots of a tile at most
   p.cs = 8;
-  while (p.cs > 1 && tiles * (tiles == 1 ? slots : 1) > resident(p.cs)) p.cs /= 2;
+  while (p.cs > 1 && (p.T <= kTile ? one : tiles_of(kTile)) > resident(p.cs)) p.cs /= 2;
   const long long room = resident(p.cs);
   if (room < 1) return QSM_ERR_CUDA;
+  if (p.T > kTile) {
+    const long long each = (tiles_of((int)(room < p.T ? room : p.T)) + 7) / 8 * 8;
+    p.tile = each < 16 ? 16 : each > kTile ? kTile : (int)each;
+    p.rows = p.tile;
+  }
+  const long long tiles = tiles_of(p.tile);
+  const int slots = one < p.tile ? one : p.tile;
   p.lanes = (int)(tiles * slots <= room ? slots : room / tiles < 1 ? 1 : room / tiles);
   p.parts = 1;
   const int chunks = (p.N + 31) / 32;
   while (tiles * p.lanes * p.parts * 2 <= room && p.parts * 2 * p.cs * kWarps <= chunks) p.parts *= 2;
   const long long ctas = tiles * p.lanes * p.parts * p.cs;
   if (ctas > 0x7fffffffll) return QSM_ERR_UNSUPPORTED;
-  QSM_CUDA_TRY(launch_pdl_cluster(kernel, dim3((unsigned)ctas), dim3(kThreads), p.cs, smem, stream, p));
+  QSM_CUDA_TRY(launch_pdl_cluster(kernel, dim3((unsigned)ctas), dim3(kThreads), p.cs, (size_t)smem_of(p.rows), stream, p));
   return QSM_OK;
 }
 
@@ -768,12 +850,11 @@ extern "C" qsm_status lora_add(const qsm_lora* L, const uint16_t* x, int64_t ldx
   p.N = L->N;
   p.R = L->rank;
   p.n = L->n;
-  p.rows = T < kTile ? (T + 7) / 8 * 8 : kTile;
   const int64_t wide = 16 / (int64_t)el < 8 ? 4 : 8;
   p.vec = N % 8 == 0 && on(out, 16) && ldo % wide == 0 && (!y || (on(y, 16) && ldy % wide == 0));
   const auto on32 = [&](const void* q) { return on(q, 32); };
   p.wide_in = on32(x) && on32(L->a) && L->K % 16 == 0 && ldx % 16 == 0;
-  p.wide_out = dtype == QSM_BF16 && N % 16 == 0 && on32(out) && ldo % 16 == 0 && (!y || (on32(y) && ldy % 16 == 0));
+  p.wide_out = on32(out) && ldo * el % 32 == 0;
   p.copy = !same;
   p.status = dev_status;
   return L->rank <= 32 ? launch<1>(p, dtype == QSM_FP32, stream)
