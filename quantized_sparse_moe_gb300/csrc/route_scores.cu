@@ -221,24 +221,44 @@ __device__ __forceinline__ void select_token(const Params& p, const Experts<MB>&
 
   uint32_t allowed = x.in;  // bit i: expert i of this lane may be taken
   if (p.kept < p.groups) {
-#pragma unroll
-    for (int b = 0; b < MB; ++b)
-      reinterpret_cast<float4*>(sc)[32 * b + lane] = make_float4(c[4 * b], c[4 * b + 1], c[4 * b + 2], c[4 * b + 3]);
-    __syncwarp();
-    // `per` lanes a group (a power of two) look through its experts, from
-    // different places so that their reads fall into different banks
+    // `per` lanes a group (a power of two) look through its experts
     const int g = lane >> x.plog;
     float a = -INFINITY, b = -INFINITY;
-    if (g < p.groups) {
-      const float* gc = sc + g * p.gsize;
-      int at = x.start;
-#pragma unroll 4
-      for (int j = lane & (x.per - 1); j < p.gsize; j += x.per) {
-        best_two(a, b, gc[at], -INFINITY);
-        at += x.per;
-        if (at >= p.gsize) at -= p.gsize;
+    if ((p.gsize & 3) == 0) {  // a lane's four neighbours are of one group: their best two stand for them
+      float2* two = reinterpret_cast<float2*>(sc);
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const float hi = fmaxf(c[4 * i], c[4 * i + 1]), lo = fminf(c[4 * i], c[4 * i + 1]);
+        float2 v = make_float2(hi, lo);
+        best_two(v.x, v.y, fmaxf(c[4 * i + 2], c[4 * i + 3]), fminf(c[4 * i + 2], c[4 * i + 3]));
+        two[32 * i + lane] = v;
+      }
+      __syncwarp();
+      if (g < p.groups) {
+        const int quads = p.gsize >> 2;
+#pragma unroll 2
+        for (int j = lane & (x.per - 1); j < quads; j += x.per) {
+          const float2 v = two[g * quads + j];
+          best_two(a, b, v.x, v.y);
+        }
+      }
+    } else {  // from different places, so that the lanes' reads fall into different banks
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+        reinterpret_cast<float4*>(sc)[32 * i + lane] = make_float4(c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]);
+      __syncwarp();
+      if (g < p.groups) {
+        const float* gc = sc + g * p.gsize;
+        int at = x.start;
+#pragma unroll 1
+        for (int j = lane & (x.per - 1); j < p.gsize; j += x.per) {
+          best_two(a, b, gc[at], -INFINITY);
+          at += x.per;
+          if (at >= p.gsize) at -= p.gsize;
+        }
       }
     }
+    __syncwarp();
     for (int o = 1; o < x.per; o <<= 1) {
       const float c2 = __shfl_xor_sync(kAll, a, o), d2 = __shfl_xor_sync(kAll, b, o);
       best_two(a, b, c2, d2);
