@@ -183,12 +183,14 @@ __device__ __forceinline__ void normalize(float (&v)[V][8], const Side& n, int H
 
 // The row's eight columns of chunk c as MXFP4 (mx4_common.cuh): four lanes
 // hold a block, sixteen the four blocks of a scale word.  All lanes of a warp
-// come here, those past the row with zeros.
+// come here; those past the row stand for blocks of zeros (what they hold is NaN
+// when the row is).
 __device__ __forceinline__ void store_mx4(const Params& p, int row, int c, const float (&v)[8], bool& bad) {
   const int lane = threadIdx.x & 31;
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+  if (c * 8 >= p.H) m = 0;
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   const uint32_t s = mx4::scale_of(m);

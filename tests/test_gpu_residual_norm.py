@@ -254,3 +254,19 @@ def test_another_stream_and_a_graph(qsm):
         wx, wh = n(x, y)
         g.replay()
         assert torch.equal(xo, wx) and torch.equal(h, wh)
+
+
+@pytest.mark.parametrize("T,H", [(5, 96), (3401, 992)])
+def test_padding_scales_are_zeros_beside_rows_that_are_not_finite(qsm, T, H):
+    """Few rows and many; a row with a NaN, one of zeros under eps = 0 (0 / 0)."""
+    x = draw((T, H), 17, torch.bfloat16)
+    x[1, 3] = float("nan")
+    x[T - 1] = 0
+    out = qsm.Mx4Tensor.empty(T, H)
+    out.scales.fill_(77)
+    st = status()
+    qsm.ResidualNorm(H, pre=qsm.Norm(kind="rms", eps=0.0))(x, h=out, dev_status=st)
+    there = qsm.mx4_tile_scales(torch.ones((T, H // 32), dtype=torch.uint8)).cuda().bool()
+    s = out.scales.view(torch.uint8).reshape(-1)
+    assert st.item() == 2 and not s[~there].any()
+    assert s[there].eq(255).sum().item() == 2 * (H // 32)
