@@ -782,22 +782,6 @@ qsm_status launch(Params& p, bool f32, cudaStream_t stream) {
   return QSM_OK;
 }
 
-// A matrix of T rows of `bytes` bytes, `ld` bytes apart: whether two of them may
-// have a byte in common (rows side by side in one matrix do not).
-struct Rows {
-  const void* p;
-  size_t ld, bytes;
-};
-bool overlap(const Rows& a, size_t ta, const Rows& b, size_t tb) {
-  if (!a.p || !b.p || !ta || !tb) return false;
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
-  const size_t sa = (ta - 1) * a.ld + a.bytes, sb = (tb - 1) * b.ld + b.bytes;
-  if (pa + sa <= pb || pb + sb <= pa) return false;
-  if (a.ld != b.ld || a.ld == 0) return true;
-  const size_t d = pb >= pa ? (pb - pa) % a.ld : (a.ld - (pa - pb) % a.ld) % a.ld;
-  return !(d >= a.bytes && d + b.bytes <= a.ld);
-}
-
 }  // namespace
 }  // namespace lora
 }  // namespace qsm
@@ -823,15 +807,15 @@ extern "C" qsm_status lora_add(const qsm_lora* L, const uint16_t* x, int64_t ldx
       (L->ranks && !aligned4(L->ranks)) || !on(out, el) || (y && !on(y, el)) || ldx < L->K || ldx % 8 ||
       (y && ldy < L->N) || ldo < L->N)
     return QSM_ERR_INVALID_ARGUMENT;
+  using mx4::Rows;
   const size_t t = T, N = L->N;
-  const Rows rx = {x, (size_t)ldx * 2, (size_t)L->K * 2}, ry = {y, (size_t)ldy * el, N * el};
-  const Rows ro = {out, (size_t)ldo * el, N * el};
-  const auto flat = [](const void* p, size_t bytes) { return Rows{p, 0, bytes}; };
+  const Rows rx = {x, t, (size_t)ldx * 2, (size_t)L->K * 2}, ry = {y, t, (size_t)ldy * el, N * el};
+  const Rows ro = {out, t, (size_t)ldo * el, N * el};
+  const auto meets = [&](const void* p, size_t bytes) { return mx4::overlap(ro, Rows{p, 1, 0, bytes}); };
   const bool same = y == out && ldy == ldo;
-  if (overlap(ro, t, rx, t) || (!same && overlap(ro, t, ry, t)) || overlap(ro, t, flat(ids, t * 4), 1) ||
-      overlap(ro, t, flat(L->a, (size_t)L->n * L->rank * L->K * 2), 1) ||
-      overlap(ro, t, flat(L->b, (size_t)L->n * L->rank * N * 2), 1) ||
-      overlap(ro, t, flat(L->scale, (size_t)L->n * 4), 1) || overlap(ro, t, flat(L->ranks, (size_t)L->n * 4), 1))
+  if (mx4::overlap(ro, rx) || (!same && mx4::overlap(ro, ry)) || meets(ids, t * 4) ||
+      meets(L->a, (size_t)L->n * L->rank * L->K * 2) || meets(L->b, (size_t)L->n * L->rank * N * 2) ||
+      meets(L->scale, (size_t)L->n * 4) || meets(L->ranks, (size_t)L->n * 4))
     return QSM_ERR_INVALID_ARGUMENT;
   Params p = {};
   p.x = x;

@@ -258,5 +258,25 @@ inline bool make_codes_map(CUtensorMap* m, const void* codes, uint64_t rows, int
                          128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Rows of `bytes` bytes in memory, `ld` bytes apart; one row, or ld 0: a vector.
+struct Rows {
+  const void* p;
+  size_t n, ld, bytes;
+};
+
+// Whether rows of a and b may have a byte in common.  Exact for rows of the same
+// stride and for a vector beside rows; true for others whose extents meet.
+inline bool overlap(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p || !a.n || !b.n) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const size_t lda = a.n > 1 ? a.ld : 0, ldb = b.n > 1 ? b.ld : 0;
+  if (pa + (a.n - 1) * lda + a.bytes <= pb || pb + (b.n - 1) * ldb + b.bytes <= pa) return false;
+  const size_t ld = lda ? lda : ldb;
+  if (!ld || (lda && ldb && lda != ldb)) return true;
+  // b's place in a row of a, up to whole rows; in a column of their own they do not meet
+  const size_t d = pb >= pa ? (pb - pa) % ld : (ld - (pa - pb) % ld) % ld;
+  return !(d >= a.bytes && d + b.bytes <= ld);
+}
+
 }  // namespace mx4
 }  // namespace qsm

@@ -423,23 +423,7 @@ bool norm_ok(const qsm_norm& n) {
          (!n.weight || aligned16(n.weight)) && (!n.bias || aligned16(n.bias));
 }
 
-// T rows of `bytes` bytes, `ld` bytes apart.
-struct Rows {
-  const void* p;
-  size_t ld, bytes;
-};
-
-// Whether rows of a and b have a byte in common.
-bool overlap(const Rows& a, const Rows& b, int T) {
-  if (!a.p || !b.p) return false;
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
-  const size_t sa = (size_t)(T - 1) * a.ld + a.bytes, sb = (size_t)(T - 1) * b.ld + b.bytes;
-  if (pa + sa <= pb || pb + sb <= pa) return false;
-  if (a.ld != b.ld || a.ld == 0) return true;
-  // columns side by side in one matrix
-  const size_t d = pb >= pa ? (pb - pa) % a.ld : (a.ld - (pa - pb) % a.ld) % a.ld;
-  return !(d >= a.bytes && d + b.bytes <= a.ld);
-}
+using mx4::Rows;
 bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.ld == b.ld && a.bytes == b.bytes; }
 
 // Which kernel.  The few-row one has many warps on an SM and starts at once, but
@@ -516,25 +500,26 @@ extern "C" qsm_status residual_norm(const qsm_residual_norm* n, int32_t T, const
   // x_out and h may be x or y (a thread reads its columns of both before it
   // writes them); nothing that is written may be read or written otherwise
   const auto rows = [&](const void* p, int64_t ld, int type) {
-    return Rows{p, (T == 1 ? 0 : (size_t)ld) * size_of(type), (size_t)H * size_of(type)};
+    return Rows{p, (size_t)T, (T == 1 ? 0 : (size_t)ld) * size_of(type), (size_t)H * size_of(type)};
   };
   const Rows rx = rows(x, ldx, n->x_dtype), ry = rows(y, ldy, n->y_dtype), ro = rows(x_out, ldo, n->x_dtype);
-  const Rows rh = mx ? Rows{h, (size_t)H / 2, (size_t)H / 2} : rows(h, ldh, n->h_dtype);
+  const Rows rh = mx ? Rows{h, (size_t)T, (size_t)H / 2, (size_t)H / 2} : rows(h, ldh, n->h_dtype);
   const Rows rg = n->gate == QSM_GATE_TOKENS
-                      ? Rows{gate, (size_t)ldg * size_of(n->gate_dtype), size_of(n->gate_dtype)}
+                      ? Rows{gate, (size_t)T, (size_t)ldg * size_of(n->gate_dtype), size_of(n->gate_dtype)}
                       : rows(gate, ldg, n->gate_dtype);
-  const Rows all_scales = {mx && h ? h_scales : nullptr, 0, mx4_scale_bytes(T, H)};
-  const auto H4 = [&](const float* p) { return Rows{p, 0, (size_t)H * 4}; };
-  const Rows weights[4] = {H4(n->post.weight), H4(n->post.bias), H4(n->pre.weight), H4(n->pre.bias)};
-  const Rows written[3] = {ro, rh, all_scales};
+  const auto vec = [](const void* p, size_t bytes) { return Rows{p, 1, 0, bytes}; };
+  const size_t H4 = (size_t)H * 4;
+  const Rows weights[4] = {vec(n->post.weight, H4), vec(n->post.bias, H4), vec(n->pre.weight, H4), vec(n->pre.bias, H4)};
+  const Rows written[3] = {ro, rh, vec(mx && h ? h_scales : nullptr, mx4_scale_bytes(T, H))};
+  using mx4::overlap;
   for (int i = 0; i < 3; ++i) {
     const Rows& w = written[i];
-    if ((overlap(w, rx, T) && !same(w, rx)) || (overlap(w, ry, T) && !same(w, ry)) || overlap(w, rg, T))
+    if ((overlap(w, rx) && !same(w, rx)) || (overlap(w, ry) && !same(w, ry)) || overlap(w, rg))
       return QSM_ERR_INVALID_ARGUMENT;
     for (const Rows& r : weights)
-      if (overlap(w, r, T)) return QSM_ERR_INVALID_ARGUMENT;
+      if (overlap(w, r)) return QSM_ERR_INVALID_ARGUMENT;
     for (int j = 0; j < i; ++j)
-      if (overlap(w, written[j], T)) return QSM_ERR_INVALID_ARGUMENT;
+      if (overlap(w, written[j])) return QSM_ERR_INVALID_ARGUMENT;
   }
   Params p = {};
   p.x = static_cast<const char*>(x);

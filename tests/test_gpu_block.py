@@ -199,6 +199,71 @@ def test_a_step_captured_and_replayed(qsm):
         assert torch.equal(got[4], want[4]) and torch.equal(got[1], want[1])
 
 
+def test_two_threads_at_once(qsm):
+    """The same plans from two threads, each on a stream of its own."""
+    import threading
+    s = Step(qsm, 3, "bf16")
+    plans = s.routers[0], qsm.ResidualNorm(s.H, pre=qsm.Norm()), s.lora
+    ids = torch.tensor([0, -1, 1], device="cuda").int()
+    y = torch.randn((3, s.lora.N), generator=gen(60), device="cuda").bfloat16()
+
+    def calls(x):
+        _, h = plans[1](x, x)
+        return (h, *qsm.moe_route_scores(h, plans[0]), qsm.lora_add(h, plans[2], ids, y))
+
+    xs = [torch.randn((3, s.H), generator=gen(61 + i), device="cuda").bfloat16() for i in range(2)]
+    want = [calls(x) for x in xs]
+    torch.cuda.synchronize()
+    good = [False, False]
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [calls(xs[i]) for _ in range(200)]
+            torch.cuda.current_stream().synchronize()
+            good[i] = all(torch.equal(a, b) for g in got for a, b in zip(g, want[i]))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert good == [True, True]
+
+
+def test_first_calls_inside_a_capture(qsm):
+    """Sizes that no call had before, captured at once; two graphs replayed on two streams."""
+    s = Step(qsm, 6, "bf16")
+    H, T = s.H, 11
+    n = qsm.ResidualNorm(H, pre=qsm.Norm())
+    y = torch.randn((T, s.lora.N), generator=gen(70), device="cuda").bfloat16()
+    ids = (torch.arange(T, device="cuda") % 3 - 1).int()
+    xs = [torch.randn((T, H), generator=gen(71 + i), device="cuda").bfloat16() for i in range(2)]
+    kept = dict(qsm._mx4._words)
+    qsm._mx4._words.clear()
+
+    def calls(x):
+        _, h = n(x, x)
+        _, q = n(x, x, h="mx4")
+        return (h, q.codes, *s.routers[0].route(h), qsm.lora_add(h, s.lora, ids, y))
+
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for x in xs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(calls(x))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for x, g in zip(xs, got):
+        assert all(torch.equal(a, b) for a, b in zip(calls(x), g))
+    qsm._mx4._words.update(kept)
+
+
 def test_the_example_runs_with_all_of_them():
     import os
     import subprocess

@@ -251,3 +251,28 @@ def test_rows_on_every_16_bytes(qsm, off, K, N):
         qsm.lora_add(x, L, ids, y, out=out[:, off:])
         want, err = definition(x, L, ids, y, torch.bfloat16)
         assert ref.lies_between(out[:, off:], want, err) and (out[:, :off] == 7).all()
+
+
+def test_offsets_that_pass_32_bits(qsm):
+    """Adapters, x and y past 2^32 elements; the last ones as a call of their own."""
+    n, R, K, N = 70, 128, 1 << 19, 24
+    a = torch.zeros((n, R, K), dtype=torch.bfloat16, device="cuda")
+    a[-1] = 1
+    b = torch.ones((n, N, R), dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros((3, K), dtype=torch.bfloat16, device="cuda")
+    x[:, ::1024] = 1
+    ids = torch.tensor([n - 1, 0, -1], device="cuda").int()
+    out = qsm.lora_add(x, qsm.LoraAdapters(a, b), ids, dtype=torch.float32)
+    assert (out[0] == K // 1024 * R).all() and not out[1:].any()    # whole numbers: exact
+    del a, x
+    T, N = (1 << 18) + 37, (1 << 14) + 8
+    L = adapters(qsm, 2, 8, 64, N, 50, mixed=False)
+    x = randn(T, 64, seed=51).bfloat16()
+    y = torch.zeros((T, N), dtype=torch.bfloat16, device="cuda")
+    y[-40:] = randn(40, N, seed=52).bfloat16()
+    ids = torch.full((T,), -1, device="cuda").int()
+    ids[-40:] = (torch.arange(40, device="cuda") % 3 - 1).int()
+    tail = x[-40:].clone(), ids[-40:].clone(), y[-40:].clone()
+    want, err = definition(tail[0], L, tail[1], tail[2], torch.bfloat16)
+    qsm.lora_add(x, L, ids, y, out=y)
+    assert ref.lies_between(y[-40:], want, err) and not y[:-40].any()

@@ -270,3 +270,35 @@ def test_padding_scales_are_zeros_beside_rows_that_are_not_finite(qsm, T, H):
     s = out.scales.view(torch.uint8).reshape(-1)
     assert st.item() == 2 and not s[~there].any()
     assert s[there].eq(255).sum().item() == 2 * (H // 32)
+
+
+@pytest.mark.parametrize("T", [1, 9])
+def test_a_gate_for_all_tokens_beside_what_is_written(qsm, T):
+    """The gate in a row of the matrix whose other columns are written."""
+    H = 128
+    x, y, g = draw((T, H), 18, torch.bfloat16), draw((T, H), 19, torch.bfloat16), draw((H,), 20, torch.bfloat16)
+    n = qsm.ResidualNorm(H, pre=qsm.Norm())
+    wx, wh = n(x, y, g)
+    m = torch.full((T, 3 * H), 7.0, dtype=torch.bfloat16, device="cuda")
+    m[T // 2, H:2 * H] = g
+    n(x, y, m[T // 2, H:2 * H], x_out=m[:, :H], h=m[:, 2 * H:])
+    assert torch.equal(m[:, :H], wx) and torch.equal(m[:, 2 * H:], wh) and torch.equal(m[T // 2, H:2 * H], g)
+    with pytest.raises(qsm.QSMError):
+        n(x, y, m[T // 2, H - 8:2 * H - 8], x_out=m[:, :H])
+
+
+def test_offsets_that_pass_32_bits(qsm):
+    """2^32 elements and more, in rows and in scales; the last rows as a call of their own."""
+    T, H = (1 << 18) + 37, 16384
+    n = qsm.ResidualNorm(H, pre=qsm.Norm())
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    x[-40:] = draw((40, H), 21, torch.bfloat16)
+    want, want4 = n(x[-40:].clone())[1], n(x[-40:].clone(), h="mx4")[1]
+    _, h = n(x)
+    assert torch.equal(h[-40:], want) and not h[:1000].any()
+    del h
+    _, q = n(x, h="mx4")
+    codes = q.codes.view(torch.uint8).reshape(T, H // 2)
+    assert torch.equal(codes[-40:], want4.codes.view(torch.uint8).reshape(40, H // 2))
+    n(x, x, x_out=x)
+    assert torch.equal(n(x[-40:].clone())[1], want)       # x + x is twice x: the same norm but for eps

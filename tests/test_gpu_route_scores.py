@@ -280,3 +280,15 @@ def test_refusals(qsm):
             f()
     with pytest.raises(AttributeError):
         r.k = 3
+
+
+def test_offsets_that_pass_32_bits(qsm):
+    """x and its row offsets past 2^32 elements; the last tokens as a call of their own."""
+    T, H, E, k = (1 << 20) + 37, 4096, 48, 6
+    r = qsm.MoERouter(torch.randn((E, H), generator=gen(70), device="cuda"), k, "sigmoid", groups=6, groups_kept=3)
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    x[-40:] = (torch.randn((40, H), generator=gen(71), device="cuda") * H ** -0.5).bfloat16()
+    ids, w = r.route(x)
+    want, ww = r.route(x[-40:].clone())
+    assert torch.equal(ids[-40:], want) and (w[-40:] - ww).abs().max().item() <= 1e-5
+    assert torch.equal(ids[:1000], torch.arange(k, device="cuda", dtype=torch.int32).expand(1000, k))
