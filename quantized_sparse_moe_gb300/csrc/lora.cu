@@ -53,9 +53,8 @@ struct Params {
   int T, K, N, R, n;      // R: ranks that an adapter has room for
   int cs, lanes, parts;   // CTAs of a cluster, slots' lanes S, column parts NS
   int tile, rows;         // tokens of a tile, and that rounded up to 8: what the buffers hold
-  int vec;                // whether eight columns of y and out can be one access
   int wide_in, wide_out;  // whether 32 bytes of a and x, and of out, can be one access
-  int units;              // whether there is shared memory for units of y
+  int how;                // kRagged, kUnitsOfY or kDirect
   int copy;               // whether tokens without an adapter have to be copied
   int32_t* status;
 };
@@ -88,6 +87,8 @@ struct Shape {
   static constexpr int kVRow = kRanks + (RK == 1 ? 0 : 32);  // bf16: rows 16 banks apart
 };
 
+// A warp's rows of expand_ragged.
+constexpr int kStageBytes = 16 * 128;
 // A warp's units of y (16 rows of 128 bytes), three of them, and 64 rows of B.
 constexpr int kUnitBytes = 16 * 128, kUnits = 3, kWarpBytes = kUnits * kUnitBytes + 64 * 64;
 
@@ -102,21 +103,28 @@ template <int RK, int SPLIT>
 __host__ __device__ constexpr size_t v_bytes(int rows) {
   return (size_t)SPLIT * v_rows(rows) * Shape<RK>::kVRow * 2;
 }
+// How y and out are read and written: rows that are not whole 16-byte units; units of y
+// through shared memory (where RK = 1); straight from and to global memory.
+enum { kRagged = 0, kUnitsOfY = 1, kDirect = 2 };
 // Where v and the CTA's sums lie: v over the partial sums, which have been read by
 // then; where there are units of y, those come over the partial sums, and v behind.
 template <int RK, int SPLIT>
-__host__ __device__ constexpr size_t v_at(int rows, bool units) {
+__host__ __device__ constexpr size_t v_at(int rows, int how) {
   const size_t a = parts_bytes<RK>(rows), b = (size_t)kWarps * kWarpBytes;
-  return RK == 1 && units ? (a > b ? a : b) : 0;
+  return RK == 1 && how == kUnitsOfY ? (a > b ? a : b) : 0;
 }
 template <int RK, int SPLIT>
-__host__ __device__ constexpr size_t sums_at(int rows, bool units) {
-  const size_t a = parts_bytes<RK>(rows), b = v_at<RK, SPLIT>(rows, units) + v_bytes<RK, SPLIT>(rows);
+__host__ __device__ constexpr size_t stage_at(int rows, int how) {
+  return v_at<RK, SPLIT>(rows, how) + v_bytes<RK, SPLIT>(rows);
+}
+template <int RK, int SPLIT>
+__host__ __device__ constexpr size_t sums_at(int rows, int how) {
+  const size_t a = parts_bytes<RK>(rows), b = stage_at<RK, SPLIT>(rows, how) + (how == kRagged ? kWarps * kStageBytes : 0);
   return a > b ? a : b;
 }
 template <int RK, int SPLIT>
-__host__ __device__ constexpr size_t smem_bytes(int rows, bool units) {
-  return sums_at<RK, SPLIT>(rows, units) + (size_t)rows * Shape<RK>::kRanks * 4;
+__host__ __device__ constexpr size_t smem_bytes(int rows, int how) {
+  return sums_at<RK, SPLIT>(rows, how) + (size_t)rows * Shape<RK>::kRanks * 4;
 }
 
 // Eight columns of y or out in one row, as they lie in memory.
@@ -125,34 +133,42 @@ struct Raw {
   uint4 v[F32 ? 2 : 1];
 };
 
-// left: columns from here to the last.
-template <bool F32, bool VEC>
-__device__ __forceinline__ Raw<F32> load_y(const char* src, int left) {
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load_raw(const void* src) {
   Raw<F32> r;
-  if (VEC) {
-    r.v[0] = *reinterpret_cast<const uint4*>(src);
-    if (F32) r.v[F32] = reinterpret_cast<const uint4*>(src)[1];
-  } else {
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      w[e] = e >= left ? 0u
-             : F32     ? reinterpret_cast<const uint32_t*>(src)[e]
-                       : (uint32_t)reinterpret_cast<const uint16_t*>(src)[e];
-    if (F32) {
-      r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      r.v[F32] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-      r.v[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-    }
-  }
+  r.v[0] = *reinterpret_cast<const uint4*>(src);
+  if (F32) r.v[F32] = reinterpret_cast<const uint4*>(src)[1];
   return r;
 }
 
+template <bool F32>
+struct Element {
+  using type = uint16_t;
+};
+template <>
+struct Element<true> {
+  using type = uint32_t;
+};
+
+// The accumulators of 16 tokens (8, with H = 1) and 32 columns begin: bf16 with y;
+// fp32 with -0, which leaves y as it is where there is no adapter: y comes last, for its full
+// accuracy.  y: of tokens g and g + 8.
+template <bool F32, int H>
+__device__ __forceinline__ void begin_sums(const Raw<F32> (&y)[H], float (&d)[4][4]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t pair = h < H && !F32 ? reinterpret_cast<const uint32_t*>(y[h < H ? h : 0].v)[j] : F32 ? 0x80008000u : 0u;
+      d[j][2 * h] = bf16_lo(pair);
+      d[j][2 * h + 1] = bf16_hi(pair);
+    }
+}
+
 // Eight columns of out: the MMAs of tiles 0 .. 3 hold two of them each, at d[j][at]
-// and d[j][at + 1], bf16 with y in the sum, fp32 without.
-template <bool F32, bool VEC>
-__device__ __forceinline__ void store_out(char* dst, int left, const Raw<F32>& y, const float (&d)[4][4], int at) {
+// and d[j][at + 1].
+template <bool F32>
+__device__ __forceinline__ void store_out(void* dst, const Raw<F32>& y, const float (&d)[4][4], int at) {
   const uint32_t* w = reinterpret_cast<const uint32_t*>(y.v);
   uint32_t o[8];
 #pragma unroll
@@ -165,17 +181,8 @@ __device__ __forceinline__ void store_out(char* dst, int left, const Raw<F32>& y
       o[j] = *reinterpret_cast<const uint32_t*>(&b);
     }
   }
-  if (VEC) {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    if (F32) reinterpret_cast<uint4*>(dst)[F32] = make_uint4(o[4], o[5], o[6], o[7]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) {
-        if (F32) reinterpret_cast<uint32_t*>(dst)[e] = o[e];
-        else reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
-      }
-  }
+  reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  if (F32) reinterpret_cast<uint4*>(dst)[F32] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // 32 columns of B: tile j's column g is row n + 2 j of it (n: the lane's), and the lane
@@ -375,9 +382,8 @@ __device__ __forceinline__ void product(const __nv_bfloat16* v, int part, int ra
 
 // This warp's columns of the slot's tokens, 16 at a time (8, with H = 1, where there are no
 // more).  Lanes g, tq: columns 8 tq .. 8 tq + 7 of a chunk of 32, of tokens g and g + 8; U
-// times 16 tokens' y are under way at once.  VEC: y and out have those columns as
-// whole 16-byte units.
-template <int RK, bool F32, bool VEC, int H, int U>
+// times 16 tokens' y are under way at once.  y and out have those columns as whole 16-byte units.
+template <int RK, bool F32, int H, int U>
 __device__ __forceinline__ void expand(const Params& p, const uint16_t* B, int rank, const int64_t* yrow,
                                        const int64_t* orow, int m, const __nv_bfloat16* vbuf, int vrows, int chunk0,
                                        int chunks, int stride) {
@@ -402,27 +408,73 @@ __device__ __forceinline__ void expand(const Params& p, const uint16_t* B, int r
           const int row = m0 + 16 * u + 8 * h + g;
           in[u][h] = row < m && n < p.N;
           y[u][h] = {};
-          if (p.y && in[u][h]) y[u][h] = load_y<F32, VEC>(p.y + (yrow[row] + n) * kEl, p.N - n);
+          if (p.y && in[u][h]) y[u][h] = load_raw<F32>(p.y + (yrow[row] + n) * kEl);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (m0 + 16 * u >= m) break;
         float d[4][4];
-        // bf16: the sum begins with y; fp32: y comes last, for its full accuracy, and
-        // the sum begins with -0, which leaves y as it is where there is no adapter
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t pair = h < H && !F32 ? reinterpret_cast<const uint32_t*>(y[u][h < H ? h : 0].v)[j] : F32 ? 0x80008000u : 0u;
-            d[j][2 * h] = bf16_lo(pair);
-            d[j][2 * h + 1] = bf16_hi(pair);
-          }
+        begin_sums<F32, H>(y[u], d);
         product<RK, F32 ? 3 : 2, H>(v + (m0 + 16 * u) * S::kVRow, part, rank, w, d);
 #pragma unroll
         for (int h = 0; h < H; ++h)
-          if (in[u][h]) store_out<F32, VEC>(p.out + (orow[m0 + 16 * u + 8 * h + g] + n) * kEl, p.N - n, y[u][h], d, 2 * h);
+          if (in[u][h]) store_out<F32>(p.out + (orow[m0 + 16 * u + 8 * h + g] + n) * kEl, y[u][h], d, 2 * h);
       }
+    }
+  }
+}
+
+// The same for rows that begin anywhere, or end inside a unit of 16 bytes: the warp reads
+// and writes its columns of a row side by side, an element a lane, and turns them into
+// fragments in 16 rows of its own shared memory; the next rows are on their way meanwhile.
+// (An element at a time straight into the fragments' lanes, 4096 x 8191 bf16 took 179 us.)
+template <int RK, bool F32, int H>
+__device__ __forceinline__ void expand_ragged(const Params& p, const uint16_t* B, int rank, const int64_t* yrow,
+                                              const int64_t* orow, int m, const __nv_bfloat16* vbuf, int vrows, int chunk0,
+                                              int chunks, int stride, unsigned char* stage) {
+  using S = Shape<RK>;
+  using El = typename Element<F32>::type;
+  constexpr int kRow = 32 * sizeof(El);
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  const __nv_bfloat16* v = vbuf + (size_t)g * S::kVRow + 8 * tq;
+  const int part = vrows * S::kVRow;
+  const El* y = reinterpret_cast<const El*>(p.y) + lane;
+  El* out = reinterpret_cast<El*>(p.out) + lane;
+  El* mine = reinterpret_cast<El*>(stage) + lane;
+  unsigned char* frag = stage + g * kRow + 8 * tq * sizeof(El);
+  El next[8 * H];
+  const auto load = [&](int ch, int m0) {
+    const bool in = p.y && ch * 32 + lane < p.N;
+#pragma unroll
+    for (int r = 0; r < 8 * H; ++r) next[r] = in && m0 + r < m ? y[yrow[m0 + r] + ch * 32] : El(0);
+  };
+  if (chunk0 < chunks) load(chunk0, 0);
+#pragma unroll 1
+  for (int ch = chunk0; ch < chunks; ch += stride) {
+    const bool in = ch * 32 + lane < p.N;
+    uint4 w[4][RK];
+    load_b<RK>(p, B, rank, ch * 32 + 8 * (g >> 1) + (g & 1), w);
+#pragma unroll 1
+    for (int m0 = 0; m0 < m; m0 += 8 * H) {
+#pragma unroll
+      for (int r = 0; r < 8 * H; ++r) mine[32 * r] = next[r];
+      __syncwarp();
+      if (m0 + 8 * H < m) load(ch, m0 + 8 * H);
+      else if (ch + stride < chunks) load(ch + stride, 0);
+      Raw<F32> u[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) u[h] = load_raw<F32>(frag + 8 * h * kRow);
+      float d[4][4];
+      begin_sums<F32, H>(u, d);
+      product<RK, F32 ? 3 : 2, H>(v + m0 * S::kVRow, part, rank, w, d);
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < H; ++h) store_out<F32>(frag + 8 * h * kRow, u[h], d, 2 * h);
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < 8 * H; ++r)
+        if (in && m0 + r < m) out[orow[m0 + r] + ch * 32] = mine[32 * r];
+      __syncwarp();
     }
   }
 }
@@ -623,8 +675,8 @@ lora_kernel(const __grid_constant__ Params p) {
   if (slot0 >= slots) return;  // the whole cluster
 
   float* parts = reinterpret_cast<float*>(smem);
-  __nv_bfloat16* vbuf = reinterpret_cast<__nv_bfloat16*>(smem + v_at<RK, SPLIT>(p.rows, p.units));
-  float* psum = reinterpret_cast<float*>(smem + sums_at<RK, SPLIT>(p.rows, p.units));  // [token][rank], read by the cluster
+  __nv_bfloat16* vbuf = reinterpret_cast<__nv_bfloat16*>(smem + v_at<RK, SPLIT>(p.rows, p.how));
+  float* psum = reinterpret_cast<float*>(smem + sums_at<RK, SPLIT>(p.rows, p.how));  // [token][rank], read by the cluster
   const int at_once = min(p.rows, 8 * S::kTokTiles), vrows = v_rows(p.rows);
   float* mine = parts + (size_t)warp * at_once * S::kPartRow;
 
@@ -729,13 +781,15 @@ lora_kernel(const __grid_constant__ Params p) {
     const __nv_bfloat16* v = vbuf + (size_t)at * S::kVRow;
     const int64_t *yr = yrow + at, *og = orow + at;
     const int chunks = (p.N + 31) / 32;
-    if (!p.vec) {
-      expand<RK, F32, false, 2, 1>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride);
+    if (p.how == kRagged) {
+      unsigned char* stage = smem + stage_at<RK, SPLIT>(p.rows, kRagged) + warp * kStageBytes;
+      if (m <= 8) expand_ragged<RK, F32, 1>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride, stage);
+      else expand_ragged<RK, F32, 2>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride, stage);
     } else if (m <= 8) {
-      expand<RK, F32, true, 1, 1>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride);
+      expand<RK, F32, 1, 1>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride);
     } else {
       if constexpr (RK == 1) expand_units<F32>(p, B, rank, yr, og, m, v, vrows, chunk0, stride, smem + warp * kWarpBytes);
-      else expand<RK, F32, true, 2, F32 || RK == 4 ? 2 : 4>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride);
+      else expand<RK, F32, 2, F32 || RK == 4 ? 2 : 4>(p, B, rank, yr, og, m, v, vrows, chunk0, chunks, stride);
     }
     at += m;
   }
@@ -751,8 +805,8 @@ lora_kernel(const __grid_constant__ Params p) {
 template <int RK>
 qsm_status launch(Params& p, bool f32, cudaStream_t stream) {
   auto* kernel = f32 ? lora_kernel<RK, true> : lora_kernel<RK, false>;
-  p.units = p.vec && p.T > 8;
-  const auto smem_of = [&](int rows) { return (int)(f32 ? smem_bytes<RK, 3>(rows, p.units) : smem_bytes<RK, 2>(rows, p.units)); };
+  if (p.how != kRagged) p.how = RK == 1 && p.T > 8 ? kUnitsOfY : kDirect;
+  const auto smem_of = [&](int rows) { return (int)(f32 ? smem_bytes<RK, 3>(rows, p.how) : smem_bytes<RK, 2>(rows, p.how)); };
   const auto resident = [&](int cs) {
     return (long long)mx4::resident_clusters(reinterpret_cast<void*>(kernel), cs, kThreads, smem_of(p.rows), kMostSmem) *
            (cs == 1 ? 2 : 1);
@@ -835,7 +889,7 @@ extern "C" qsm_status lora_add(const qsm_lora* L, const uint16_t* x, int64_t ldx
   p.R = L->rank;
   p.n = L->n;
   const int64_t wide = 16 / (int64_t)el < 8 ? 4 : 8;
-  p.vec = N % 8 == 0 && on(out, 16) && ldo % wide == 0 && (!y || (on(y, 16) && ldy % wide == 0));
+  p.how = N % 8 == 0 && on(out, 16) && ldo % wide == 0 && (!y || (on(y, 16) && ldy % wide == 0)) ? kDirect : kRagged;
   const auto on32 = [&](const void* q) { return on(q, 32); };
   p.wide_in = on32(x) && on32(L->a) && L->K % 16 == 0 && ldx % 16 == 0;
   p.wide_out = on32(out) && ldo * el % 32 == 0;
