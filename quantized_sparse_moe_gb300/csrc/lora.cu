@@ -39,6 +39,8 @@ constexpr int kTile = 64;    // tokens, at most
 constexpr int kMaxRank = 128;
 constexpr int kMaxSide = 1 << 28;  // of K and N
 constexpr int kMostSmem = 200 * 1024;  // dynamic
+constexpr int kMostCounted = 1023;      // adapters whose tokens a CTA counts
+constexpr int kMostGrouped = 1 << 14;   // tokens that a CTA looks through
 
 struct Params {
   const uint16_t* x;
@@ -51,7 +53,8 @@ struct Params {
   char* out;
   int64_t ldx, ldy, ldo;  // elements
   int T, K, N, R, n;      // R: ranks that an adapter has room for
-  int cs, lanes, parts;   // CTAs of a cluster, slots' lanes S, column parts NS
+  int cs, lanes, parts;   // CTAs of a cluster, slots' lanes S (or clusters for items), column parts NS
+  int room;               // items that run at once
   int tile, rows;         // tokens of a tile, and that rounded up to 8: what the buffers hold
   int wide_in, wide_out;  // whether 32 bytes of a and x, and of out, can be one access
   int how;                // kRagged, kUnitsOfY or kDirect
@@ -618,7 +621,88 @@ __device__ __forceinline__ void expand_units(const Params& p, const uint16_t* B,
   __syncwarp();
 }
 
-template <int RK, bool F32>
+// The token's adapter, n for those without one.
+__device__ __forceinline__ int adapter_of(const Params& p, int t) {
+  return (int)min((uint32_t)__ldg(p.ids + t), (uint32_t)p.n);
+}
+
+// Item `item` of many tokens, the same cut in every CTA: the tokens of an adapter, wherever
+// they are (those without one come last), are shared out evenly over as few items as the tile
+// allows, in their order; the tile is the smallest that makes no more items than
+// run at once.  Its tokens go to mem, m of them (0: there is no such item).  Returns the adapter,
+// -1: none.  cnt: n + 1 counters.
+__device__ __forceinline__ int find_item(const Params& p, int item, int* cnt, int* mem, int* sums, int& m) {
+  constexpr int kTiles = kTile / 8 - 1;  // of 16, 24, ..
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i <= p.n; i += kThreads) cnt[i] = 0;
+  __syncthreads();
+  const int per = (p.T + 32 * kWarps - 1) / (32 * kWarps) * 32, t0 = warp * per, t1 = min(t0 + per, p.T);  // this warp's
+  bool bad = false;
+#pragma unroll 8
+  for (int t = t0 + lane; t < t1; t += 32) {
+    const int id = __ldg(p.ids + t);
+    bad |= id >= p.n;
+    atomicAdd(cnt + min((uint32_t)id, (uint32_t)p.n), 1);
+  }
+  if (bad && blockIdx.x == 0) set_status(p.status, QSM_DEV_BAD_ADAPTER_ID);
+  __syncthreads();
+  const int ids = p.n + p.copy;  // whose tokens have to be looked at
+  int tile = kTile;
+  {
+    int all[kTiles] = {};
+    for (int i = lane; i < ids; i += 32) {
+      const int c = cnt[i];
+#pragma unroll
+      for (int k = 0; k < kTiles; ++k) all[k] += (c + 8 * k + 15) / (8 * k + 16);
+    }
+#pragma unroll
+    for (int k = kTiles - 2; k >= 0; --k)
+      if (__reduce_add_sync(0xffffffffu, all[k]) <= p.room) tile = 8 * k + 16;
+  }
+  int id = 0, from = 0, before = 0;
+  m = 0;
+  for (int i0 = 0; i0 < ids; i0 += 32) {  // the adapter whose items have it among them
+    const int c = i0 + lane < ids ? cnt[i0 + lane] : 0, parts = (c + tile - 1) / tile;
+    int upto = parts;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    upto += before;
+    const uint32_t in = __ballot_sync(0xffffffffu, upto > item);
+    if (in) {
+      const int at = __ffs(in) - 1, nth = item - (upto - parts);
+      id = i0 + at;
+      from = __shfl_sync(0xffffffffu, parts ? (int)((long long)c * nth / parts) : 0, at);
+      m = __shfl_sync(0xffffffffu, parts ? (int)((long long)c * (nth + 1) / parts) : 0, at) - from;
+      break;
+    }
+    before = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (m == 0) return -1;
+  int mine = 0;
+#pragma unroll 8
+  for (int t = t0 + lane; t < t1; t += 32) mine += adapter_of(p, t) == id;
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) sums[warp] = mine;
+  __syncthreads();
+  int rank = -from;
+  for (int w = 0; w < warp; ++w) rank += sums[w];
+  if (mine && rank < m && rank + mine > 0)
+    for (int t = t0; t < t1 && rank < m; t += 32) {
+      const bool is = t + lane < t1 && adapter_of(p, t + lane) == id;
+      const uint32_t all = __ballot_sync(0xffffffffu, is);
+      const int at = rank + __popc(all & ((1u << lane) - 1));
+      if (is && at >= 0 && at < m) mem[at] = t + lane;
+      rank += __popc(all);
+    }
+  __syncthreads();
+  return id < p.n ? id : -1;
+}
+
+// GROUPED: many tokens, a cluster has one item; otherwise it has slots of a tile.
+template <int RK, bool F32, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 2)
 lora_kernel(const __grid_constant__ Params p) {
   using S = Shape<RK>;
@@ -626,7 +710,7 @@ lora_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) int ids[kTile];
   __shared__ unsigned long long slot_tokens[kTile];
-  __shared__ int slot_id[kTile], mem[kTile], ranks[kTile], leaders[2];
+  __shared__ int slot_id[kTile], mem[kTile], ranks[kTile], leaders[2], sums[kWarps];
   __shared__ float factor[kTile];
   __shared__ int64_t yrow[kTile], orow[kTile];  // where the slot's tokens have their rows, in elements
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -634,45 +718,74 @@ lora_kernel(const __grid_constant__ Params p) {
   int cl = blockIdx.x / p.cs;  // cluster: (tile, slot lane, column part), the part fastest
   const int part = cl % p.parts;
   cl /= p.parts;
-  const int slot0 = cl % p.lanes;
-  const int64_t t0 = (int64_t)(cl / p.lanes) * p.tile;
-  const int count = (int)min((int64_t)p.tile, p.T - t0);
+  const int slot0 = GROUPED ? 0 : cl % p.lanes, lanes = GROUPED ? 1 : p.lanes;
+  const int64_t t0 = GROUPED ? 0 : (int64_t)(cl / p.lanes) * p.tile;
   pdl_wait();
   pdl_launch_dependents();
 
-  // ids of the tile; -1: none
-  if (tid < kTile) {
-    int id = tid < count ? __ldg(p.ids + t0 + tid) : -2;
-    if (tid < count && id < 0) id = -1;
-    if (id >= p.n) {
-      id = -1;
-      if (rank_cta == 0 && slot0 == 0 && part == 0) set_status(p.status, QSM_DEV_BAD_ADAPTER_ID);
+  int slots = 1, total = 0;
+  if constexpr (GROUPED) {
+    int* cnt = reinterpret_cast<int*>(smem + smem_bytes<RK, SPLIT>(p.rows, p.how));
+    const int id = find_item(p, cl, cnt, mem, sums, total);
+    if (total == 0) return;  // the whole cluster
+    if (tid < total) {
+      yrow[tid] = mem[tid] * p.ldy;
+      orow[tid] = mem[tid] * p.ldo;
+      ranks[tid] = id < 0 ? 0 : p.ranks ? min(max(__ldg(p.ranks + id), 0), p.R) : p.R;
+      factor[tid] = id >= 0 && p.scale ? __ldg(p.scale + id) : 1.f;
     }
-    ids[tid] = id;
-  }
-  __syncthreads();
-  // slots in the order of their first tokens
-  if (tid < kTile) {
-    const int id = ids[tid];
-    unsigned long long same = 0;
+    if (tid == 0) slot_id[0] = id;
+  } else {
+    const int count = (int)min((int64_t)p.tile, p.T - t0);
+    // ids of the tile; -1: none
+    if (tid < kTile) {
+      int id = tid < count ? __ldg(p.ids + t0 + tid) : -2;
+      if (tid < count && id < 0) id = -1;
+      if (id >= p.n) {
+        id = -1;
+        if (rank_cta == 0 && slot0 == 0 && part == 0) set_status(p.status, QSM_DEV_BAD_ADAPTER_ID);
+      }
+      ids[tid] = id;
+    }
+    __syncthreads();
+    // slots in the order of their first tokens
+    if (tid < kTile) {
+      const int id = ids[tid];
+      unsigned long long same = 0;
 #pragma unroll
-    for (int j = 0; j < kTile; j += 4) {
-      const int4 o = *reinterpret_cast<const int4*>(ids + j);
-      same |= (unsigned long long)((o.x == id) | (o.y == id) << 1 | (o.z == id) << 2 | (o.w == id) << 3) << j;
+      for (int j = 0; j < kTile; j += 4) {
+        const int4 o = *reinterpret_cast<const int4*>(ids + j);
+        same |= (unsigned long long)((o.x == id) | (o.y == id) << 1 | (o.z == id) << 2 | (o.w == id) << 3) << j;
+      }
+      const bool leader = id != -2 && (same & ((1ull << tid) - 1)) == 0 && (id != -1 || p.copy);
+      const uint32_t all = __ballot_sync(0xffffffffu, leader);
+      if (lane == 0) leaders[warp] = (int)all;
+      asm volatile("bar.sync 1, 64;" ::: "memory");
+      if (leader) {
+        const int at = __popc(all & ((1u << lane) - 1)) + (warp ? __popc((uint32_t)leaders[0]) : 0);
+        slot_id[at] = id;
+        slot_tokens[at] = same;
+      }
     }
-    const bool leader = id != -2 && (same & ((1ull << tid) - 1)) == 0 && (id != -1 || p.copy);
-    const uint32_t all = __ballot_sync(0xffffffffu, leader);
-    if (lane == 0) leaders[warp] = (int)all;
-    asm volatile("bar.sync 1, 64;" ::: "memory");
-    if (leader) {
-      const int at = __popc(all & ((1u << lane) - 1)) + (warp ? __popc((uint32_t)leaders[0]) : 0);
-      slot_id[at] = id;
-      slot_tokens[at] = same;
+    __syncthreads();
+    slots = __popc((uint32_t)leaders[0]) + __popc((uint32_t)leaders[1]);
+    if (slot0 >= slots) return;  // the whole cluster
+
+    // The tokens of this cluster's slots, slot by slot.
+    for (int slot = slot0; slot < slots; slot += lanes) {
+      const unsigned long long tokens = slot_tokens[slot];
+      if (tid < kTile && ((tokens >> tid) & 1ull)) {
+        const int at = total + __popcll(tokens & ((1ull << tid) - 1)), id = ids[tid];
+        mem[at] = tid;
+        yrow[at] = (t0 + tid) * p.ldy;
+        orow[at] = (t0 + tid) * p.ldo;
+        ranks[at] = id < 0 ? 0 : p.ranks ? min(max(__ldg(p.ranks + id), 0), p.R) : p.R;
+        factor[at] = id >= 0 && p.scale ? __ldg(p.scale + id) : 1.f;
+      }
+      total += __popcll(tokens);
     }
   }
   __syncthreads();
-  const int slots = __popc((uint32_t)leaders[0]) + __popc((uint32_t)leaders[1]);
-  if (slot0 >= slots) return;  // the whole cluster
 
   float* parts = reinterpret_cast<float*>(smem);
   __nv_bfloat16* vbuf = reinterpret_cast<__nv_bfloat16*>(smem + v_at<RK, SPLIT>(p.rows, p.how));
@@ -684,25 +797,9 @@ lora_kernel(const __grid_constant__ Params p) {
   const int kfirst = (int)((long long)kblocks * rank_cta / p.cs), klast = (int)((long long)kblocks * (rank_cta + 1) / p.cs);
   const int stride = p.parts * p.cs * kWarps, chunk0 = (part * p.cs + rank_cta) * kWarps + warp;  // of columns
 
-  // The tokens of this cluster's slots, slot by slot.
-  int total = 0;
-  for (int slot = slot0; slot < slots; slot += p.lanes) {
-    const unsigned long long tokens = slot_tokens[slot];
-    if (tid < kTile && ((tokens >> tid) & 1ull)) {
-      const int at = total + __popcll(tokens & ((1ull << tid) - 1)), id = ids[tid];
-      mem[at] = tid;
-      yrow[at] = (t0 + tid) * p.ldy;
-      orow[at] = (t0 + tid) * p.ldo;
-      ranks[at] = id < 0 ? 0 : p.ranks ? min(max(__ldg(p.ranks + id), 0), p.R) : p.R;
-      factor[at] = id >= 0 && p.scale ? __ldg(p.scale + id) : 1.f;
-    }
-    total += __popcll(tokens);
-  }
-  __syncthreads();
-
   // v of all of them
-  for (int slot = slot0, at = 0; slot < slots; slot += p.lanes) {
-    const int id = slot_id[slot], m = __popcll(slot_tokens[slot]), rank = ranks[at];
+  for (int slot = slot0, at = 0; slot < slots; slot += lanes) {
+    const int id = slot_id[slot], m = GROUPED ? total : __popcll(slot_tokens[slot]), rank = ranks[at];
     if (rank > 0) {
       const uint16_t* A = p.a + (size_t)id * p.R * p.K;
       const uint16_t* B = p.b + (size_t)id * p.N * p.R;
@@ -775,8 +872,8 @@ lora_kernel(const __grid_constant__ Params p) {
   if (p.cs > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // has read the others' sums
 
   // out of all of them (an MMA reads the rows of up to 15 tokens behind a slot's last one: their sums are not used)
-  for (int slot = slot0, at = 0; slot < slots; slot += p.lanes) {
-    const int id = slot_id[slot], m = __popcll(slot_tokens[slot]), rank = ranks[at];
+  for (int slot = slot0, at = 0; slot < slots; slot += lanes) {
+    const int id = slot_id[slot], m = GROUPED ? total : __popcll(slot_tokens[slot]), rank = ranks[at];
     const uint16_t* B = p.b + (size_t)(id < 0 ? 0 : id) * p.N * p.R;
     const __nv_bfloat16* v = vbuf + (size_t)at * S::kVRow;
     const int64_t *yr = yrow + at, *og = orow + at;
@@ -802,37 +899,35 @@ lora_kernel(const __grid_constant__ Params p) {
 // an SM: 36 of 8, 74 of 4, 152 of 2).  More than 64 tokens: tiles of as many as give each of
 // those clusters one, 16 to 64 (4096 tokens: 74 tiles of 56).  As many slots' lanes
 // as a tile can have slots while they fit; and columns in parts while SMs would be idle.
-template <int RK>
+template <int RK, bool GROUPED>
 qsm_status launch(Params& p, bool f32, cudaStream_t stream) {
-  auto* kernel = f32 ? lora_kernel<RK, true> : lora_kernel<RK, false>;
+  auto* kernel = f32 ? lora_kernel<RK, true, GROUPED> : lora_kernel<RK, false, GROUPED>;
   if (p.how != kRagged) p.how = RK == 1 && p.T > 8 ? kUnitsOfY : kDirect;
-  const auto smem_of = [&](int rows) { return (int)(f32 ? smem_bytes<RK, 3>(rows, p.how) : smem_bytes<RK, 2>(rows, p.how)); };
+  p.tile = p.T < kTile ? p.T : kTile;
+  p.rows = (p.tile + 7) / 8 * 8;
+  const int smem = (int)(f32 ? smem_bytes<RK, 3>(p.rows, p.how) : smem_bytes<RK, 2>(p.rows, p.how)) + (GROUPED ? (p.n + 1) * 4 : 0);
   const auto resident = [&](int cs) {
-    return (long long)mx4::resident_clusters(reinterpret_cast<void*>(kernel), cs, kThreads, smem_of(p.rows), kMostSmem) *
+    return (long long)mx4::resident_clusters(reinterpret_cast<void*>(kernel), cs, kThreads, smem, kMostSmem) *
            (cs == 1 ? 2 : 1);
   };
   const auto tiles_of = [&](int tile) { return ((long long)p.T + tile - 1) / tile; };
-  p.tile = p.T < kTile ? p.T : kTile;
-  p.rows = (p.tile + 7) / 8 * 8;
+  const auto items_of = [&](int tile) { return tiles_of(tile) + (p.n + 1ll < p.T ? p.n + 1 : p.T); };  // at most
   const int one = p.n + 1ll < p.tile ? p.n + 1 : p.tile;  // slots of a tile at most
   p.cs = 8;
-  while (p.cs > 1 && (p.T <= kTile ? one : tiles_of(kTile)) > resident(p.cs)) p.cs /= 2;
+  while (p.cs > 1 && (GROUPED ? items_of(kTile) : p.T <= kTile ? one : tiles_of(kTile)) > resident(p.cs)) p.cs /= 2;
   const long long room = resident(p.cs);
   if (room < 1) return QSM_ERR_CUDA;
-  if (p.T > kTile) {
-    const long long each = (tiles_of((int)(room < p.T ? room : p.T)) + 7) / 8 * 8;
-    p.tile = each < 16 ? 16 : each > kTile ? kTile : (int)each;
-    p.rows = p.tile;
-  }
-  const long long tiles = tiles_of(p.tile);
-  const int slots = one < p.tile ? one : p.tile;
-  p.lanes = (int)(tiles * slots <= room ? slots : room / tiles < 1 ? 1 : room / tiles);
+  const long long tiles = GROUPED ? 1 : tiles_of(p.tile);
+  long long lanes = tiles * one <= room ? one : room / tiles < 1 ? 1 : room / tiles;
+  if (GROUPED) lanes = items_of(16) < room ? items_of(16) : items_of(kTile) > room ? items_of(kTile) : room;
+  p.lanes = (int)lanes;
   p.parts = 1;
   const int chunks = (p.N + 31) / 32;
-  while (tiles * p.lanes * p.parts * 2 <= room && p.parts * 2 * p.cs * kWarps <= chunks) p.parts *= 2;
-  const long long ctas = tiles * p.lanes * p.parts * p.cs;
+  while (tiles * lanes * p.parts * 2 <= room && p.parts * 2 * p.cs * kWarps <= chunks) p.parts *= 2;
+  p.room = (int)(lanes < room / p.parts ? lanes : room / p.parts);
+  const long long ctas = tiles * lanes * p.parts * p.cs;
   if (ctas > 0x7fffffffll) return QSM_ERR_UNSUPPORTED;
-  QSM_CUDA_TRY(launch_pdl_cluster(kernel, dim3((unsigned)ctas), dim3(kThreads), p.cs, (size_t)smem_of(p.rows), stream, p));
+  QSM_CUDA_TRY(launch_pdl_cluster(kernel, dim3((unsigned)ctas), dim3(kThreads), p.cs, (size_t)smem, stream, p));
   return QSM_OK;
 }
 
@@ -895,7 +990,8 @@ extern "C" qsm_status lora_add(const qsm_lora* L, const uint16_t* x, int64_t ldx
   p.wide_out = on32(out) && ldo * el % 32 == 0;
   p.copy = !same;
   p.status = dev_status;
-  return L->rank <= 32 ? launch<1>(p, dtype == QSM_FP32, stream)
-         : L->rank <= 64 ? launch<2>(p, dtype == QSM_FP32, stream)
-                         : launch<4>(p, dtype == QSM_FP32, stream);
+  const bool f32 = dtype == QSM_FP32;
+  if (T > kTile && T <= kMostGrouped && L->n <= kMostCounted)
+    return L->rank <= 32 ? launch<1, true>(p, f32, stream) : L->rank <= 64 ? launch<2, true>(p, f32, stream) : launch<4, true>(p, f32, stream);
+  return L->rank <= 32 ? launch<1, false>(p, f32, stream) : L->rank <= 64 ? launch<2, false>(p, f32, stream) : launch<4, false>(p, f32, stream);
 }

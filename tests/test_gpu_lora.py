@@ -276,3 +276,31 @@ def test_offsets_that_pass_32_bits(qsm):
     want, err = definition(tail[0], L, tail[1], tail[2], torch.bfloat16)
     qsm.lora_add(x, L, ids, y, out=y)
     assert ref.lies_between(y[-40:], want, err) and not y[:-40].any()
+
+
+@pytest.mark.parametrize("T,n", [(65, 1), (300, 40), (600, 500), (1000, 1023), (100, 1100), (700, 2000), (16500, 9)])
+def test_adapters_in_any_order(qsm, T, n):
+    """More items than run at once, tokens of an adapter anywhere, more adapters than a CTA counts
+    (1100, 2000), more tokens than it looks through (16500); out over y, ids out of range."""
+    L = adapters(qsm, n, 8, 64, 40, 60, mixed=False)
+    x, y = randn(T, 64, seed=61).bfloat16(), randn(T, 40, seed=62).bfloat16()
+    ids = torch.randint(-1, n, (T,), generator=gen(63), device="cuda").int()
+    if T > 2000:
+        ids[:9000] = 3
+    used = {i: torch.nonzero(ids == i)[:, 0] for i in set(ids.tolist()) if i >= 0}
+    want, err = y.double(), torch.zeros(T, 40, dtype=torch.float64, device="cuda")
+    for i, t in used.items():   # the bound of definition(), adapter by adapter
+        a, b, c, xv = L.a[i].double(), L.b[i].double(), L.scale[i].double(), x[t].double()
+        v, dv = xv @ a.T * c, (64 / 128 + 40) * 2 * U * (xv.abs() @ a.abs().T) * abs(c)
+        dv = dv + (2.0 ** -17 + 2 * U) * v.abs()
+        want[t] += v @ b.T
+        err[t] = dv @ b.abs().T + 42 * 2 * U * ((v.abs() + dv) @ b.abs().T)
+    err = err + 2 * U * (want.abs() + err)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = qsm.lora_add(x, L, ids, y, dev_status=st)
+    assert ref.lies_between(out, want.cpu(), err.cpu()) and st.item() == 0
+    assert torch.equal(out[ids < 0], y[ids < 0])
+    bad = torch.where(ids < 0, n + 5, ids)
+    z = y.clone()
+    qsm.lora_add(x, L, bad, z, out=z, dev_status=st)
+    assert torch.equal(z, out) and st.item() == (16 if (ids < 0).any() else 0)
