@@ -660,7 +660,7 @@ typedef struct {
 
 /* The adapters of a batch beside a shared projection, one launch:
  *   out[t] = y[t] + scale[i] * b[i] (a[i] x[t]),  i = ids[t];
- * a negative id: none, out[t] = y[t].  Sums in fp32, out rounded once (a bf16
+ * a negative id: none, out[t] = y[t].  The ids may come in any order.  Sums in fp32, out rounded once (a bf16
  * out: a[i] x[t] enters the second product to 2^-17).  A token's result does not depend
  * on the other tokens' values.
  *   x [T, K] bf16, ldx elements from row to row (a multiple of 8, at least

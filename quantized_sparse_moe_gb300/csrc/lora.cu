@@ -2,27 +2,41 @@
 //
 //   out[t] = y[t] + c[a] B[a] (A[a] x[t]),     a = ids[t] (none: out[t] = y[t])
 //
-// in one launch.  The tokens are cut into tiles of 64 that follow one another;
-// the distinct adapters of a tile are its slots, and a cluster of CTAs takes
-// the slots s, s + S, ... of a tile and one of NS parts of the columns:
+// in one launch.  A cluster of CTAs has tokens of one adapter after another:
 //
-//   1. v = A[a] x[t] for the slot's tokens: every warp of the cluster has a
-//      piece of K for all ranks and tokens (16 ranks x 8 tokens x 16 per MMA);
-//      the warps' partial sums are added in a fixed order, first in the CTA,
-//      then over the cluster through distributed shared memory;
-//   2. out = y + (c v) B[a]^T: a warp takes 32 columns of all the slot's tokens
-//      (16 tokens x 8 columns x 16 per MMA) and adds y in fp32.
+//   up to 64 tokens: the distinct adapters of the call are its slots, and a cluster
+//     takes the slots s, s + S, ...;
+//   more: the tokens of each adapter, wherever they are, make items of up to 64 tokens
+//     each, an item a cluster.  Every CTA counts the ids for itself (2 to 3 us for 4096), so
+//     there is neither a second launch nor a workspace;
+//
+// and one of NS parts of the columns.  For a slot or an item:
+//
+//   1. v = A[a] x[t]: every warp of the cluster has a piece of K for all ranks and
+//      tokens (16 ranks x 8 tokens x 16 per MMA); the warps' partial sums are added
+//      in a fixed order, first in the CTA, then over the cluster through distributed
+//      shared memory;
+//   2. out = y + (c v) B[a]^T: a warp takes 32 or 64 columns of all the tokens (16 tokens
+//      x 8 columns x 16 per MMA) and adds y in fp32.
 //
 // With NS > 1 each part forms v again for itself (A comes from L2 then), which
 // is cheaper than a launch or a grid-wide exchange between the two products.
-// A few tokens: bound by the latency of two dependent rounds of loads; many
-// adapters: by reading them; prompts: by x, y and out.
+// Measured (bf16; GPU time of a replayed call, inputs from HBM or L2 as they come):
+//   1 token, 2048 x 2048, rank 16: 5.3 us; latency (ids, A, exchange, B and y in turn)
+//   37 tokens, 2048 x 8192, up to 64 ranks: 10 us; the same, with 12 MB of A and B
+//   64 tokens with adapters of their own, 8192 x 2048, rank 64: 24.4 us = 3.5 TB/s of A and
+//     B; the SMs have one or two CTAs each, and plain loads give at most 5.4 TB/s
+//   4096 tokens, 2048 x 8192, rank 32: 46 us = 3.3 TB/s: 3 the items, 10 the first product
+//     and its exchange, the rest y and out at the rate of a plain copy
+// The products themselves are small: mma.sync with operands in registers does
+// not limit any of them (tensor pipe 17% busy in the last case).
 //
 // Operands go from global memory straight into MMA fragments: the order of the
-// products of a sum is free, so a lane takes 8 consecutive values (16 bytes) of
+// products of a sum is free, so a lane takes 8 or 16 consecutive values (16 or 32 bytes) of
 // a row where the fragment's own order would have it take four times two.  In
-// the same way the columns of four MMAs are dealt so that a lane ends up with 8
-// consecutive columns of a token.
+// the same way the columns of the second product's MMAs are dealt so that a lane ends up
+// with 8 or 16 consecutive columns of a token.  (A staged in shared memory by copies of
+// 512 bytes was slower, 2 TB/s; so were y's lines asked for in L2 ahead, 57 us for 54.)
 //
 // v is rounded for the second product: c v is split into bf16 parts, two of them
 // (2^-17 relative) for 16-bit outputs, which are rounded to 2^-9 anyway, three
@@ -430,7 +444,8 @@ __device__ __forceinline__ void expand(const Params& p, const uint16_t* B, int r
 // The same for rows that begin anywhere, or end inside a unit of 16 bytes: the warp reads
 // and writes its columns of a row side by side, an element a lane, and turns them into
 // fragments in 16 rows of its own shared memory; the next rows are on their way meanwhile.
-// (An element at a time straight into the fragments' lanes, 4096 x 8191 bf16 took 179 us.)
+// (4096 x 8191 bf16, rank 32: 90 us; with an element at a
+// time straight into the fragments' lanes 179.  Two elements a lane: 95, for want of registers.)
 template <int RK, bool F32, int H>
 __device__ __forceinline__ void expand_ragged(const Params& p, const uint16_t* B, int rank, const int64_t* yrow,
                                               const int64_t* orow, int m, const __nv_bfloat16* vbuf, int vrows, int chunk0,
@@ -701,7 +716,7 @@ __device__ __forceinline__ int find_item(const Params& p, int item, int* cnt, in
   return id < p.n ? id : -1;
 }
 
-// GROUPED: many tokens, a cluster has one item; otherwise it has slots of a tile.
+// GROUPED: a cluster has one item; otherwise it has slots of a tile.
 template <int RK, bool F32, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 2)
 lora_kernel(const __grid_constant__ Params p) {
@@ -715,7 +730,7 @@ lora_kernel(const __grid_constant__ Params p) {
   __shared__ int64_t yrow[kTile], orow[kTile];  // where the slot's tokens have their rows, in elements
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank_cta = p.cs > 1 ? (int)mx4::cluster_rank() : 0;
-  int cl = blockIdx.x / p.cs;  // cluster: (tile, slot lane, column part), the part fastest
+  int cl = blockIdx.x / p.cs;  // cluster: (tile, slot lane or item, column part), the part fastest
   const int part = cl % p.parts;
   cl /= p.parts;
   const int slot0 = GROUPED ? 0 : cl % p.lanes, lanes = GROUPED ? 1 : p.lanes;
@@ -895,10 +910,15 @@ lora_kernel(const __grid_constant__ Params p) {
 }
 
 // The cut: a launch in one wave if it can be.  Clusters of 8 CTAs, fewer when there are more
-// tiles and slots than such clusters fit on the device at once (a GB300, two CTAs
-// an SM: 36 of 8, 74 of 4, 152 of 2).  More than 64 tokens: tiles of as many as give each of
-// those clusters one, 16 to 64 (4096 tokens: 74 tiles of 56).  As many slots' lanes
-// as a tile can have slots while they fit; and columns in parts while SMs would be idle.
+// slots or items than such clusters fit on the device at once (a GB300, two CTAs an SM: 36
+// of 8, 74 of 4, 152 of 2).  The items' tile is the smallest that fits (4096 tokens of a
+// few adapters: 56 of 16 to 64; with 28 it took 64 us for 54, with 40 68).  Slots have a cluster each
+// while they fit; and columns come in parts while SMs would be idle.
+// Items against tiles of 64 tokens as they follow one another, whose adapters a cluster takes in
+// turn (us; 2048 x 8192, rank 32): 4096 tokens of six adapters in six runs 46 against 54, in no
+// order 47 against 92, of 64 adapters 60 against 444; 16384 in six runs 153 against 176.  2048 x 2048:
+// 32768 in six runs 188 against 146: beyond kMostGrouped tokens, or kMostCounted adapters, every
+// CTA would look through too much, and it is tiles (32768 in no order: 302 against 193).
 template <int RK, bool GROUPED>
 qsm_status launch(Params& p, bool f32, cudaStream_t stream) {
   auto* kernel = f32 ? lora_kernel<RK, true, GROUPED> : lora_kernel<RK, false, GROUPED>;
