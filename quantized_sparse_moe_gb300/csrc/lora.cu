@@ -26,7 +26,7 @@
 //   37 tokens, 2048 x 8192, up to 64 ranks: 10 us; the same, with 12 MB of A and B
 //   64 tokens with adapters of their own, 8192 x 2048, rank 64: 24.4 us = 3.5 TB/s of A and
 //     B; the SMs have one or two CTAs each, and plain loads give at most 5.4 TB/s
-//   4096 tokens, 2048 x 8192, rank 32: 46 us = 3.3 TB/s: 3 the items, 10 the first product
+//   4096 tokens, 2048 x 8192, rank 32: 47 us = 3.3 TB/s: 3 the items, 10 the first product
 //     and its exchange, the rest y and out at the rate of a plain copy
 // The products themselves are small: mma.sync with operands in registers does
 // not limit any of them (tensor pipe 17% busy in the last case).
@@ -911,11 +911,16 @@ lora_kernel(const __grid_constant__ Params p) {
 
 // The cut: a launch in one wave if it can be.  Clusters of 8 CTAs, fewer when there are more
 // slots or items than such clusters fit on the device at once (a GB300, two CTAs an SM: 36
-// of 8, 74 of 4, 152 of 2).  The items' tile is the smallest that fits (4096 tokens of a
-// few adapters: 56 of 16 to 64; with 28 it took 64 us for 54, with 40 68).  Slots have a cluster each
-// while they fit; and columns come in parts while SMs would be idle.
+// of 8, 74 of 4, 152 of 2, 304 of 1).  Slots have a cluster each while they fit; and columns come
+// in parts while SMs would be idle.
+// Items are of 16 tokens with clusters of 8, up to 32 with 4 or 2, else what fits: less of a
+// product's latency hangs on one item (us, clusters of 8, 4, 2, 1; six adapters: 300 tokens 2048 x
+// 2048 11.6 12.4 15.1 19.6; 904 1216 x 734 20 12.5 13.8 14.9; 1714 496 x 248 24 14.2 12.6 11.3; 4096 2048 x
+// 8192 63 46.2 46.9 58).  In launches that follow one another closely not all those clusters
+// find room beside the early ones of the next launch (1024 x 1024, rank 16, us: 30 of 8 9.2, 31
+// 11.5, 36 15.2; 70 of 4 10.4, 74 13.8): the shares left out below.
 // Items against tiles of 64 tokens as they follow one another, whose adapters a cluster takes in
-// turn (us; 2048 x 8192, rank 32): 4096 tokens of six adapters in six runs 46 against 54, in no
+// turn (us; 2048 x 8192, rank 32): 4096 tokens of six adapters in six runs 47 against 54, in no
 // order 47 against 92, of 64 adapters 60 against 444; 16384 in six runs 153 against 176.  2048 x 2048:
 // 32768 in six runs 188 against 146: beyond kMostGrouped tokens, or kMostCounted adapters, every
 // CTA would look through too much, and it is tiles (32768 in no order: 302 against 193).
@@ -927,14 +932,14 @@ qsm_status launch(Params& p, bool f32, cudaStream_t stream) {
   p.rows = (p.tile + 7) / 8 * 8;
   const int smem = (int)(f32 ? smem_bytes<RK, 3>(p.rows, p.how) : smem_bytes<RK, 2>(p.rows, p.how)) + (GROUPED ? (p.n + 1) * 4 : 0);
   const auto resident = [&](int cs) {
-    return (long long)mx4::resident_clusters(reinterpret_cast<void*>(kernel), cs, kThreads, smem, kMostSmem) *
-           (cs == 1 ? 2 : 1);
+    const long long r = mx4::resident_clusters(reinterpret_cast<void*>(kernel), cs, kThreads, smem, kMostSmem);
+    return cs == 1 ? 2 * r : !GROUPED ? r : cs == 8 ? r - r / 6 : cs == 4 ? r - r / 18 : r;
   };
   const auto tiles_of = [&](int tile) { return ((long long)p.T + tile - 1) / tile; };
   const auto items_of = [&](int tile) { return tiles_of(tile) + (p.n + 1ll < p.T ? p.n + 1 : p.T); };  // at most
   const int one = p.n + 1ll < p.tile ? p.n + 1 : p.tile;  // slots of a tile at most
   p.cs = 8;
-  while (p.cs > 1 && (GROUPED ? items_of(kTile) : p.T <= kTile ? one : tiles_of(kTile)) > resident(p.cs)) p.cs /= 2;
+  while (p.cs > 1 && (GROUPED ? items_of(p.cs == 8 ? 16 : 32) : p.T <= kTile ? one : tiles_of(kTile)) > resident(p.cs)) p.cs /= 2;
   const long long room = resident(p.cs);
   if (room < 1) return QSM_ERR_CUDA;
   const long long tiles = GROUPED ? 1 : tiles_of(p.tile);
