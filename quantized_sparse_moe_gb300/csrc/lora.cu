@@ -341,6 +341,28 @@ __device__ __forceinline__ void shrink_few(const Params& p, const uint16_t* A, i
   put_sums<RK, 1>(acc, tiles, m, mine);
 }
 
+// The same for up to 8 NT tokens, N blocks under way at once.
+template <int RK, int NT, int N>
+__device__ __forceinline__ void shrink_some(const Params& p, const uint16_t* A, int rank, const int* mem, int m, int kfirst,
+                                            int klast, float* mine) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3, tiles = (rank + 15) / 16;
+  float acc[2 * RK][NT][4] = {};
+  const uint16_t *ap[2 * RK][2], *xp[NT];
+#pragma unroll
+  for (int i = 0; i < 2 * RK; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) ap[i][h] = A + (size_t)min(16 * i + 8 * h + g, rank - 1) * p.K + 8 * tq;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) xp[j] = p.x + mem[min(8 * j + g, m - 1)] * p.ldx + 8 * tq;
+  const int warp = threadIdx.x >> 5, whole = min(klast, p.K / 32);  // the blocks before it have no column past K
+  int kb = kfirst;
+#pragma unroll 1
+  for (; kb + N * kWarps <= whole; kb += N * kWarps) shrink_blocks<RK, NT, N>(ap, xp, (kb + N * warp) * 32, true, tiles, acc);
+#pragma unroll 1
+  for (kb += warp; kb < klast; kb += kWarps) shrink_blocks<RK, NT, 1>(ap, xp, kb * 32, kb * 32 + 8 * tq < p.K, tiles, acc);
+  put_sums<RK, NT>(acc, tiles, m, mine);
+}
+
 // The same for up to 8 kTokTiles tokens, block by block.
 template <int RK>
 __device__ __forceinline__ void shrink_many(const Params& p, const uint16_t* A, int rank, const int* mem, int64_t t0,
@@ -828,6 +850,8 @@ lora_kernel(const __grid_constant__ Params p) {
       for (int c0 = 0; c0 < m; c0 += 8 * S::kTokTiles) {  // tokens at once
         const int mt = min(m - c0, 8 * S::kTokTiles);
         if (mt <= 8) shrink_few<RK>(p, A, rank, mem + at + c0, t0, mt, kfirst, klast, mine);
+        else if (GROUPED && RK == 1 && mt <= 16) shrink_some<RK, 2, 4>(p, A, rank, mem + at + c0, mt, kfirst, klast, mine);
+        else if (GROUPED && RK == 1 && mt <= 32) shrink_some<RK, 4, 2>(p, A, rank, mem + at + c0, mt, kfirst, klast, mine);
         else shrink_many<RK>(p, A, rank, mem + at + c0, t0, mt, kfirst, klast, mine);
         __syncthreads();
         for (int e = tid; e < mt * (used / 4); e += kThreads) {  // four ranks of a token
