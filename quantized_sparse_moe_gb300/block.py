@@ -14,7 +14,7 @@ import ctypes
 import torch
 
 from . import QSMError, _check, lib
-from .mx4 import (Mx4Tensor, _DTYPES, _empty, _Fixed, _fp32, _handle, _matrix,
+from .mx4 import (Mx4Tensor, _DTYPES, _empty, _empty_mx4, _Fixed, _fp32, _handle, _matrix,
                   _status, _stream_of)
 
 _KINDS = {"rms": 1, "layer": 2}
@@ -191,11 +191,7 @@ class ResidualNorm(_Fixed):
         elif isinstance(h, Mx4Tensor) or h == "mx4":
             ht = _MX4
             if h == "mx4":
-                if stream is None:
-                    h = Mx4Tensor.empty(T, H, device=x.device)
-                else:  # as _empty
-                    with torch.cuda.stream(stream):
-                        h = Mx4Tensor.empty(T, H, device=x.device)
+                h = _empty_mx4(T, H, dev, stream)
             elif h.rows != T or h.cols != H or h.experts != 1 or h.device != dev:
                 raise QSMError(f"{what}: h has another shape or device")
             hp, sp = h.c.codes, h.c.scales
