@@ -27,7 +27,7 @@
 //
 // Measured (GPU time of a replayed call; H 2048, 256 experts unless said):
 //   1 token 8.5 us: latency.  The copies of the 3.1 MB of split weights take 3.3, the exchanges take 2.5 and the selection 2
-//   37 tokens 8.3 us, 300 tokens of H 1024 and 64 experts 7.5: the same chain
+//   37 tokens 8.3 us, 300 tokens of H 1024 and 64 experts 7.2: the same chain
 //   4096 tokens in 8 groups 21.5 us: 9 of copies (each tile of tokens reads all the weights: 110 MB
 //     from L2), 6 of selection, the rest launch, accumulators and exchanges; the
 //     MMAs alone would take 6.7.  (With clusters that come in two waves it took 50.)
@@ -595,11 +595,12 @@ struct Config {
 
 // A cluster of ks x mb CTAs has a tile; the device holds so many at once (a
 // GB300: 76 of 2, 36 of 4, 15 of 8, 7 of 16), and with tiles for all of them a launch takes one
-// wave.  Least time, by what the parts of it measured: a CTA's copies (55 bytes a cycle),
-// reading the accumulators, selecting with sixteen warps, and the rest.
-// H 2048, 256 experts, by slices and tokens a tile (us): 4096 tokens 3 and 192 22.2 (chosen), 2 and
-// 128 22.9; one token 8 slices 8.6 (chosen), 4 9.6.  H 1024, 64 experts, 300 tokens: 8 and 32 7.5
-// (chosen), 4 and 16 7.1.
+// wave.  Least time, by the terms of a fit to 20 sizes from 1 to 16384 tokens and 8 to 384 experts: a
+// CTA's copies, its accumulators, the tokens of a warp, and the exchange, which grows with the cluster.
+// The choice is within 5% of the best one for each of them; us for 1, 2, 3, 4, 6, 8, 16 slices:
+//   H 2048, 256 experts: 1 token 19.5 12.4 10.3 8.8 8.4 8.3 -, 1000 20.4 13.9 12.5 12.4 13.1 13.3 -,
+//     4096 25.8 20.3 20.0 38.6 38.4 51.8 -
+//   H 2048, 64 experts: 1 token 18.5 11.7 9.6 8.3 7.6 6.5 7.0, 4096 21.5 15.6 14.3 13.7 15.1 28.7 44.9
 Config choose(const qsm_router* r, int T) {
   struct Kept {
     int dev, T, H, E;
@@ -626,8 +627,9 @@ Config choose(const qsm_router* r, int T) {
     c.ks = ks;
     c.tiles = ((long long)T + c.nt - 1) / c.nt;
     const long long waves = (c.tiles + resident - 1) / resident;
-    const double us = (double)waves * (3.0 + (steps + ks - 1) / ks * (3 * kPartBytes + c.nt * BK * 2) / 105e3 + c.nt * 0.006 +
-                                       ((c.nt + ks * mb - 1) / (ks * mb) + kWarps - 1) / kWarps * 1.2 + 0.1 * ks);
+    const int cut = ks * mb, rounds = ((c.nt + cut - 1) / cut + kWarps - 1) / kWarps;
+    const double us = (double)waves * (3.0 + (steps + ks - 1) / ks * (3 * kPartBytes + c.nt * BK * 2) / 131e3 +
+                                       c.nt * 0.01 + rounds * 0.8 + cut * 0.15);
     if (best.nt == 0 || us < least) {
       best = c;
       least = us;
