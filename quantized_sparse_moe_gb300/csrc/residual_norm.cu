@@ -28,7 +28,7 @@ constexpr int kMaxH = 16384;
 constexpr int kMaxT = 1 << 30;
 constexpr int kWarpRows = 4;       // rows of a CTA when a warp holds a row
 constexpr size_t kBuffers = 216 * 1024;        // shared memory of the many-row kernel
-constexpr long long kManyValues = 3 << 20;
+constexpr long long kManyValues = 5 << 19;
 
 struct Side {  // a norm
   int kind;
@@ -434,16 +434,17 @@ using mx4::Rows;
 bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.ld == b.ld && a.bytes == b.bytes; }
 
 // Which kernel.  The few-row one has many warps on an SM and starts at once, but
-// each of them goes through a row's latencies alone: from 3 M values on (1216
-// rows of 2048: 6.9 us against 7.5; 2432: 14.2 against 13.0; 4864 of 1024: 13.5
-// against 10.7) the other is faster, unless a fourth of its lanes' chunks lie
-// past the row (9728 rows of 512: 13.4 against 15.1).
+// each of them goes through a row's latencies alone; the other takes about 7 us for
+// each round of rows.  From 2.5 M values on that is faster (bf16, both norms, us, few rows'
+// kernel and the other: 2 M values as 1024 x 2048 6.9 6.9, 2.5 M 7.2 6.9, 3 M 9.1 6.9, 4 M 11.8 11.2, 6 M
+// 17.2 12.6; 320 x 8192 11.2 7.7; with a gate for each value and fp32 h, 2.5 M as 1280 x 2048 9.8
+// 10.6, 3 M 13.0 12.1), unless a fourth of its lanes' chunks lie past the row (6144 x 512: 9.1 10.3).
 template <int XT, int YT>
 qsm_status launch(Params& p, cudaStream_t stream) {
   const int chunks = p.H / 8, sms = mx4::sm_count();
   const auto threads = [&](int v) { return ((chunks + v - 1) / v + 31) / 32 * 32; };
   const int v = threads(4) <= kRowsThreads && 4 * threads(4) < 8 * threads(8) ? 4 : 8;
-  const bool many = (long long)p.T * p.H > kManyValues && 4 * chunks >= 3 * v * threads(v);
+  const bool many = (long long)p.T * p.H >= kManyValues && 4 * chunks >= 3 * v * threads(v);
   if (!many && chunks <= 1024) {
     p.tpr = threads(1);
     const int per = p.tpr == 32 ? kWarpRows : 1;
