@@ -15,9 +15,9 @@
 // Bound by memory for many rows, by latency and the launch for few.  Measured (GPU time
 // of a replayed call, inputs rotating over more than L2 where they are large):
 //   1 x 2048 bf16 2.1 us; 300 x 2048 with a gate to MXFP4 (and dequantized again) 5.6
-//   4096 x 2048 bf16, both norms 16.4 us = 4.1 TB/s, 16384 x 2048 44.9 = 6.0 TB/s: 5 us of a
-//     launch are its first rows' latency, 12 rows an SM at once, and the last ones
-//   2050 x 1056 fp32, layer norm and a bias 8.9 us = 3.4 TB/s; the same
+//   4096 x 2048 bf16, both norms 15.0 us = 4.5 TB/s, 16384 x 2048 45.0 = 6.0 TB/s: 4 us of a
+//     launch are its first rows' latency, ten rows an SM at once, and the last ones
+//   2050 x 1056 fp32, layer norm and a bias 9.0 us = 3.4 TB/s; the same
 #include "mx4_common.cuh"
 
 namespace qsm {
@@ -28,7 +28,7 @@ constexpr int kMaxH = 16384;
 constexpr int kMaxT = 1 << 30;
 constexpr int kWarpRows = 4;       // rows of a CTA when a warp holds a row
 constexpr size_t kBuffers = 216 * 1024;        // shared memory of the many-row kernel
-constexpr long long kManyValues = 5 << 19;
+constexpr long long kManyValues = 3 << 19;
 
 struct Side {  // a norm
   int kind;
@@ -325,13 +325,15 @@ row_kernel(const __grid_constant__ Params p) {
 // Many rows: a CTA per SM, groups of tpr threads that take row after row.  Each
 // group has a buffer in shared memory, which bulk copies fill with the next
 // row (x, y and the gate) as soon as the present one is in registers; the
-// norms' vectors lie beside them.  Eight chunks a thread: a row of 2048 is a
-// warp's, and its sums need no barrier.
-constexpr int kRowsThreads = 384, kMaxGroups = kRowsThreads / 32;
+// norms' vectors lie beside them.  Four chunks a thread and up to twenty groups
+// (4096 x 2048 15.0 us; eight chunks, whose rows of 2048 are a warp's without a barrier, and twelve
+// groups 16.3, 4096 x 5120 32 against 44).
+constexpr int kRowsThreads = 640, kMaxGroups = kRowsThreads / 32, kChunks = 4;
 
-template <int V, int XT, int YT>
+template <int XT, int YT>
 __global__ void __launch_bounds__(kRowsThreads, 1)
 rows_kernel(const __grid_constant__ Params p, int groups, int vectors) {
+  constexpr int V = kChunks;
   extern __shared__ __align__(128) unsigned char buffers[];
   __shared__ float red[kMaxGroups][2][32];
   __shared__ __align__(8) uint64_t full[kMaxGroups], vec_bar;
@@ -434,34 +436,36 @@ using mx4::Rows;
 bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.ld == b.ld && a.bytes == b.bytes; }
 
 // Which kernel.  The few-row one has many warps on an SM and starts at once, but
-// each of them goes through a row's latencies alone; the other takes about 7 us for
-// each round of rows.  From 2.5 M values on that is faster (bf16, both norms, us, few rows'
-// kernel and the other: 2 M values as 1024 x 2048 6.9 6.9, 2.5 M 7.2 6.9, 3 M 9.1 6.9, 4 M 11.8 11.2, 6 M
-// 17.2 12.6; 320 x 8192 11.2 7.7; with a gate for each value and fp32 h, 2.5 M as 1280 x 2048 9.8
-// 10.6, 3 M 13.0 12.1), unless a fourth of its lanes' chunks lie past the row (6144 x 512: 9.1 10.3).
+// each of them goes through a row's latencies alone.  From 1.5 M values on the
+// other is faster (bf16, both norms, us, few rows' kernel and the other: 1 M values as 512 x 2048 4.6 4.7,
+// 1.5 M 6.0 5.2, 2 M 7.0 5.5, 3 M 9.0 8.3, 6 M 17.3 13.5; 192 x 8192 7.8 6.2; with a gate for each value
+// and fp32 h 768 x 2048 7.3 7.3, 1024 8.6 7.6), unless five eighths of its lanes' chunks lie past the row
+// (4096 x 384 6.5 6.5; 6144 x 256 4.7 8.5).
 template <int XT, int YT>
 qsm_status launch(Params& p, cudaStream_t stream) {
   const int chunks = p.H / 8, sms = mx4::sm_count();
   const auto threads = [&](int v) { return ((chunks + v - 1) / v + 31) / 32 * 32; };
-  const int v = threads(4) <= kRowsThreads && 4 * threads(4) < 8 * threads(8) ? 4 : 8;
-  const bool many = (long long)p.T * p.H >= kManyValues && 4 * chunks >= 3 * v * threads(v);
+  const bool many = (long long)p.T * p.H >= kManyValues && 8 * chunks >= 3 * kChunks * threads(kChunks);
   if (!many && chunks <= 1024) {
     p.tpr = threads(1);
     const int per = p.tpr == 32 ? kWarpRows : 1;
     QSM_CUDA_TRY(launch_pdl(row_kernel<XT, YT>, dim3((p.rows + per - 1) / per), dim3(p.tpr * per), 0, stream, p));
     return QSM_OK;
   }
-  p.tpr = threads(v);
+  p.tpr = threads(kChunks);
   const size_t row = (size_t)p.H * ((XT == QSM_FP32 ? 4 : 2) + (p.y ? YT == QSM_FP32 ? 4 : 2 : 0) +
                                     (gate_rows(p) ? p.gt == QSM_FP32 ? 4 : 2 : 0));
   int groups = kRowsThreads / p.tpr;
   while (groups > 1 && groups * row > kBuffers) --groups;
+  // as few groups as take no more rounds (4096 x 2048, three rounds: nine 15.0 us, ten 15.4, eleven 16.4)
+  const int rounds = (p.T + groups * sms - 1) / (groups * sms);
+  groups = (p.T + rounds * sms - 1) / (rounds * sms);
   int ctas = (p.rows + groups - 1) / groups;
   if (ctas > sms) ctas = sms;
   int vectors = (p.post.w != nullptr) + (p.post.b != nullptr) + (p.pre.w != nullptr) + (p.pre.b != nullptr);
   if (groups * row + (size_t)vectors * p.H * 4 > kBuffers) vectors = 0;  // they stay in global memory
   const size_t smem = groups * row + (size_t)vectors * p.H * 4;
-  auto* kernel = v == 4 ? rows_kernel<4, XT, YT> : rows_kernel<8, XT, YT>;
+  auto* kernel = rows_kernel<XT, YT>;
   QSM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBuffers));
   QSM_CUDA_TRY(launch_pdl(kernel, dim3(ctas), dim3(p.tpr * groups), smem, stream, p, groups, vectors));
   return QSM_OK;

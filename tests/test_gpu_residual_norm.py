@@ -300,5 +300,6 @@ def test_offsets_that_pass_32_bits(qsm):
     _, q = n(x, h="mx4")
     codes = q.codes.view(torch.uint8).reshape(T, H // 2)
     assert torch.equal(codes[-40:], want4.codes.view(torch.uint8).reshape(40, H // 2))
+    last = x[-40:].clone()
     n(x, x, x_out=x)
-    assert torch.equal(n(x[-40:].clone())[1], want)       # x + x is twice x: the same norm but for eps
+    assert torch.equal(x[-40:], 2 * last) and not x[:1000].any()   # x + x: exact
