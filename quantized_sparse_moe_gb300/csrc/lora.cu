@@ -543,35 +543,37 @@ __device__ __forceinline__ void expand_units(const Params& p, const uint16_t* B,
   using S = Shape<1>;
   constexpr int kEl = F32 ? 4 : 2, kCols = 128 / kEl, Q = kCols / 32, SPLIT = F32 ? 3 : 2;
   const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  const int chunks = (p.N + kCols - 1) / kCols, tiles = (m + 15) / 16;
-  const int total = chunk0 < chunks ? ((chunks - chunk0 + stride - 1) / stride) * tiles : 0;
+  const int first = chunk0 * kCols, step = stride * kCols;
   unsigned char* bbuf = mine + kUnits * kUnitBytes;
-  const auto columns = [&](int u) { return (chunk0 + u / tiles * stride) * kCols; };
   // 16 bytes c of row r of a unit lie at unit c ^ (r & 7) of the row: eight lanes' reads are in different banks
-  const auto fetch = [&](int u) {
-    if (u < total && p.y) {
-      const int n = columns(u) + (lane & 7) * (16 / kEl), mt = u % tiles * 16;
-      unsigned char* to = mine + u % kUnits * kUnitBytes;
+  int ahead_m = 0, ahead_n = first, ahead_at = 0;  // the unit that is fetched next, and where to
+  const auto fetch = [&] {
+    if (ahead_n < p.N && p.y) {
+      const int n = ahead_n + (lane & 7) * (16 / kEl);
+      unsigned char* to = mine + ahead_at;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = (lane >> 3) + 4 * i;
-        if (mt + r < m && n < p.N) copy16(to + r * 128 + (((lane & 7) ^ (r & 7)) << 4), p.y + (yrow[mt + r] + n) * kEl);
+        if (ahead_m + r < m && n < p.N) copy16(to + r * 128 + (((lane & 7) ^ (r & 7)) << 4), p.y + (yrow[ahead_m + r] + n) * kEl);
       }
     }
     copies_commit();
+    ahead_m += 16;
+    if (ahead_m >= m) ahead_m = 0, ahead_n += step;
+    ahead_at = ahead_at == (kUnits - 1) * kUnitBytes ? 0 : ahead_at + kUnitBytes;
   };
   const auto fetch_b = [&](int n0) {  // rows of B as they are, R ranks each
     if (rank > 0 && n0 < p.N)
       for (int i = lane; i < min(kCols, p.N - n0) * p.R / 8; i += 32) copy16(bbuf + i * 16, B + (size_t)n0 * p.R + i * 8);
   };
-  fetch_b(columns(0));
-  fetch(0);
-  fetch(1);
+  fetch_b(first);
+  fetch();
+  fetch();
   uint4 w[Q][4];
+  int at = 0;
 #pragma unroll 1
-  for (int u = 0; u < total; ++u) {
-    const int n0 = columns(u), mt = u % tiles * 16;
-    if (tiles == 1) copies_wait<0>();  // (the rows of B came with the last unit)
+  for (int n0 = first, mt = 0; n0 < p.N;) {
+    if (m <= 16) copies_wait<0>();  // (the rows of B came with the last unit)
     else copies_wait<1>();
     __syncwarp();
     if (mt == 0) {
@@ -585,9 +587,10 @@ __device__ __forceinline__ void expand_units(const Params& p, const uint16_t* B,
           if (8 * tq < rank) w[q][j] = first_of(*reinterpret_cast<const uint4*>(bbuf + (n * p.R + 8 * tq) * 2), rank - 8 * tq);
         }
       __syncwarp();
-      fetch_b(n0 + stride * kCols);
+      fetch_b(n0 + step);
     }
-    const unsigned char* from = mine + u % kUnits * kUnitBytes;
+    const unsigned char* from = mine + at;
+    at = at == (kUnits - 1) * kUnitBytes ? 0 : at + kUnitBytes;
     Raw<true> y[2];  // 32 bytes
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -595,7 +598,7 @@ __device__ __forceinline__ void expand_units(const Params& p, const uint16_t* B,
       for (int i = 0; i < 2; ++i)
         y[h].v[i] = p.y ? *reinterpret_cast<const uint4*>(from + (8 * h + g) * 128 + (((2 * tq + i) ^ g) << 4)) : make_uint4(0, 0, 0, 0);
     __syncwarp();
-    fetch(u + 2);  // over the unit before this one
+    fetch();  // over the unit before this one
     const __nv_bfloat16* vr = vbuf + (size_t)(mt + g) * S::kVRow + 8 * tq;
     uint4 v[SPLIT][2];
 #pragma unroll
@@ -655,6 +658,8 @@ __device__ __forceinline__ void expand_units(const Params& p, const uint16_t* B,
           if (n + i * (16 / kEl) < p.N) reinterpret_cast<uint4*>(to)[i] = o[h].v[i];
       }
     }
+    mt += 16;
+    if (mt >= m) mt = 0, n0 += step;
   }
   copies_wait<0>();
   __syncwarp();
