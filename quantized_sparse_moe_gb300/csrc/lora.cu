@@ -54,7 +54,7 @@ constexpr int kMaxRank = 128;
 constexpr int kMaxSide = 1 << 28;  // of K and N
 constexpr int kMostSmem = 200 * 1024;  // dynamic
 constexpr int kMostCounted = 1023;      // adapters whose tokens a CTA counts
-constexpr int kMostGrouped = 1 << 14;   // tokens that a CTA looks through
+constexpr int kMostGrouped = 1 << 14;   // tokens that a CTA looks through; their ids fit where the partial sums will lie
 
 struct Params {
   const uint16_t* x;
@@ -665,43 +665,46 @@ __device__ __forceinline__ void expand_units(const Params& p, const uint16_t* B,
   __syncwarp();
 }
 
-// The token's adapter, n for those without one.
-__device__ __forceinline__ int adapter_of(const Params& p, int t) {
-  return (int)min((uint32_t)__ldg(p.ids + t), (uint32_t)p.n);
-}
-
 // Item `item` of many tokens, the same cut in every CTA: the tokens of an adapter, wherever
 // they are (those without one come last), are shared out evenly over as few items as the tile
 // allows, in their order; the tile is the smallest that makes no more items than
 // run at once.  Its tokens go to mem, m of them (0: there is no such item).  Returns the adapter,
-// -1: none.  cnt: n + 1 counters.
-__device__ __forceinline__ int find_item(const Params& p, int item, int* cnt, int* mem, int* sums, int& m) {
-  constexpr int kTiles = kTile / 8 - 1;  // of 16, 24, ..
+// -1: none.  cnt: n + 1 counters; all: room for the ids.  (The code is gone through once, so that its
+// size counts, too: with 16 ids of a lane in registers it took 6.5 us for 5.)
+__device__ __forceinline__ int find_item(const Params& p, int item, int* cnt, int* all, int* mem, int* sums, int& m) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+#pragma unroll 1
+  for (int t = tid; t < p.T; t += kThreads)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(all + t)), "l"(p.ids + t) : "memory");
+  copies_commit();
+#pragma unroll 1
   for (int i = tid; i <= p.n; i += kThreads) cnt[i] = 0;
+  copies_wait<0>();
   __syncthreads();
   const int per = (p.T + 32 * kWarps - 1) / (32 * kWarps) * 32, t0 = warp * per, t1 = min(t0 + per, p.T);  // this warp's
   bool bad = false;
-#pragma unroll 8
+#pragma unroll 4
   for (int t = t0 + lane; t < t1; t += 32) {
-    const int id = __ldg(p.ids + t);
+    const int id = all[t], of = (int)min((uint32_t)id, (uint32_t)p.n);
     bad |= id >= p.n;
-    atomicAdd(cnt + min((uint32_t)id, (uint32_t)p.n), 1);
+    all[t] = of;
+    atomicAdd(cnt + of, 1);
   }
   if (bad && blockIdx.x == 0) set_status(p.status, QSM_DEV_BAD_ADAPTER_ID);
   __syncthreads();
   const int ids = p.n + p.copy;  // whose tokens have to be looked at
-  int tile = kTile;
+  int tile = kTile + 8;  // the smallest that will do
   {
-    int all[kTiles] = {};
-    for (int i = lane; i < ids; i += 32) {
-      const int c = cnt[i];
-#pragma unroll
-      for (int k = 0; k < kTiles; ++k) all[k] += (c + 8 * k + 15) / (8 * k + 16);
-    }
-#pragma unroll
-    for (int k = kTiles - 2; k >= 0; --k)
-      if (__reduce_add_sync(0xffffffffu, all[k]) <= p.room) tile = 8 * k + 16;
+    int count = 0;
+#pragma unroll 1
+    do {
+      tile -= 8;
+      count = 0;
+#pragma unroll 1
+      for (int i = lane; i < ids; i += 32) count += (cnt[i] + tile - 1) / tile;
+      count = __reduce_add_sync(0xffffffffu, count);
+    } while (count <= p.room && tile > 16);
+    if (count > p.room) tile = min(tile + 8, kTile);
   }
   int id = 0, from = 0, before = 0;
   m = 0;
@@ -718,28 +721,29 @@ __device__ __forceinline__ int find_item(const Params& p, int item, int* cnt, in
     if (in) {
       const int at = __ffs(in) - 1, nth = item - (upto - parts);
       id = i0 + at;
-      from = __shfl_sync(0xffffffffu, parts ? (int)((long long)c * nth / parts) : 0, at);
-      m = __shfl_sync(0xffffffffu, parts ? (int)((long long)c * (nth + 1) / parts) : 0, at) - from;
+      from = __shfl_sync(0xffffffffu, parts ? c * nth / parts : 0, at);
+      m = __shfl_sync(0xffffffffu, parts ? c * (nth + 1) / parts : 0, at) - from;
       break;
     }
     before = __shfl_sync(0xffffffffu, upto, 31);
   }
   if (m == 0) return -1;
   int mine = 0;
-#pragma unroll 8
-  for (int t = t0 + lane; t < t1; t += 32) mine += adapter_of(p, t) == id;
+#pragma unroll 4
+  for (int t = t0 + lane; t < t1; t += 32) mine += all[t] == id;
   mine = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) sums[warp] = mine;
   __syncthreads();
   int rank = -from;
   for (int w = 0; w < warp; ++w) rank += sums[w];
   if (mine && rank < m && rank + mine > 0)
+#pragma unroll 1
     for (int t = t0; t < t1 && rank < m; t += 32) {
-      const bool is = t + lane < t1 && adapter_of(p, t + lane) == id;
-      const uint32_t all = __ballot_sync(0xffffffffu, is);
-      const int at = rank + __popc(all & ((1u << lane) - 1));
+      const bool is = t + lane < t1 && all[t + lane] == id;
+      const uint32_t who = __ballot_sync(0xffffffffu, is);
+      const int at = rank + __popc(who & ((1u << lane) - 1));
       if (is && at >= 0 && at < m) mem[at] = t + lane;
-      rank += __popc(all);
+      rank += __popc(who);
     }
   __syncthreads();
   return id < p.n ? id : -1;
@@ -770,7 +774,7 @@ lora_kernel(const __grid_constant__ Params p) {
   int slots = 1, total = 0;
   if constexpr (GROUPED) {
     int* cnt = reinterpret_cast<int*>(smem + smem_bytes<RK, SPLIT>(p.rows, p.how));
-    const int id = find_item(p, cl, cnt, mem, sums, total);
+    const int id = find_item(p, cl, cnt, reinterpret_cast<int*>(smem), mem, sums, total);
     if (total == 0) return;  // the whole cluster
     if (tid < total) {
       yrow[tid] = mem[tid] * p.ldy;
@@ -957,6 +961,7 @@ lora_kernel(const __grid_constant__ Params p) {
 // CTA would look through too much, and it is tiles (32768 in no order: 302 against 193).
 template <int RK, bool GROUPED>
 qsm_status launch(Params& p, bool f32, cudaStream_t stream) {
+  static_assert(parts_bytes<RK>(kTile) >= kMostGrouped * 4, "find_item has the ids there");
   auto* kernel = f32 ? lora_kernel<RK, true, GROUPED> : lora_kernel<RK, false, GROUPED>;
   if (p.how != kRagged) p.how = RK == 1 && p.T > 8 ? kUnitsOfY : kDirect;
   p.tile = p.T < kTile ? p.T : kTile;
