@@ -7,7 +7,7 @@
 //   up to 64 tokens: the distinct adapters of the call are its slots, and a cluster
 //     takes the slots s, s + S, ...;
 //   more: the tokens of each adapter, wherever they are, make items of up to 64 tokens
-//     each, an item a cluster.  Every CTA counts the ids for itself (2 to 3 us for 4096), so
+//     each, an item a cluster.  Every CTA counts the ids for itself (3 us for 4096), so
 //     there is neither a second launch nor a workspace;
 //
 // and one of NS parts of the columns.  For a slot or an item:
@@ -26,8 +26,8 @@
 //   37 tokens, 2048 x 8192, up to 64 ranks: 10 us; the same, with 12 MB of A and B
 //   64 tokens with adapters of their own, 8192 x 2048, rank 64: 24.4 us = 3.5 TB/s of A and
 //     B; the SMs have one or two CTAs each, and plain loads give at most 5.4 TB/s
-//   4096 tokens, 2048 x 8192, rank 32: 47 us = 3.3 TB/s: 3 the items, 10 the first product
-//     and its exchange, the rest y and out at the rate of a plain copy
+//   4096 tokens, 2048 x 8192, rank 32: 41 us = 3.7 TB/s: 5 the items and their rows, 10 the first
+//     product and its exchange, 23 y and out at the rate of a plain copy; 16384: 128 us = 4.7 TB/s
 // The products themselves are small: mma.sync with operands in registers does
 // not limit any of them (tensor pipe 17% busy in the last case).
 //
@@ -468,7 +468,7 @@ __device__ __forceinline__ void expand(const Params& p, const uint16_t* B, int r
 // The same for rows that begin anywhere, or end inside a unit of 16 bytes: the warp reads
 // and writes its columns of a row side by side, an element a lane, and turns them into
 // fragments in 16 rows of its own shared memory; the next rows are on their way meanwhile.
-// (4096 x 8191 bf16, rank 32: 90 us; with an element at a
+// (4096 x 8191 bf16, rank 32: 86 us; with an element at a
 // time straight into the fragments' lanes 179.  Two elements a lane: 95, for want of registers.)
 template <int RK, bool F32, int H>
 __device__ __forceinline__ void expand_ragged(const Params& p, const uint16_t* B, int rank, const int64_t* yrow,
@@ -670,7 +670,7 @@ __device__ __forceinline__ void expand_units(const Params& p, const uint16_t* B,
 // allows, in their order; the tile is the smallest that makes no more items than
 // run at once.  Its tokens go to mem, m of them (0: there is no such item).  Returns the adapter,
 // -1: none.  cnt: n + 1 counters; all: room for the ids.  (The code is gone through once, so that its
-// size counts, too: with 16 ids of a lane in registers it took 6.5 us for 5.)
+// size counts, too: with 16 ids of a lane in registers it took 6.5 us for 4096 tokens, so 5.)
 __device__ __forceinline__ int find_item(const Params& p, int item, int* cnt, int* all, int* mem, int* sums, int& m) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 #pragma unroll 1
@@ -693,18 +693,13 @@ __device__ __forceinline__ int find_item(const Params& p, int item, int* cnt, in
   if (bad && blockIdx.x == 0) set_status(p.status, QSM_DEV_BAD_ADAPTER_ID);
   __syncthreads();
   const int ids = p.n + p.copy;  // whose tokens have to be looked at
-  int tile = kTile + 8;  // the smallest that will do
-  {
+  int tile = min(max(((p.T + p.room - 1) / p.room + 7) / 8 * 8, 16), kTile);  // less makes too many
+#pragma unroll 1
+  for (; tile < kTile; tile += 8) {
     int count = 0;
 #pragma unroll 1
-    do {
-      tile -= 8;
-      count = 0;
-#pragma unroll 1
-      for (int i = lane; i < ids; i += 32) count += (cnt[i] + tile - 1) / tile;
-      count = __reduce_add_sync(0xffffffffu, count);
-    } while (count <= p.room && tile > 16);
-    if (count > p.room) tile = min(tile + 8, kTile);
+    for (int i = lane; i < ids; i += 32) count += (cnt[i] + tile - 1) / tile;
+    if (__reduce_add_sync(0xffffffffu, count) <= p.room) break;
   }
   int id = 0, from = 0, before = 0;
   m = 0;
@@ -955,8 +950,8 @@ lora_kernel(const __grid_constant__ Params p) {
 // find room beside the early ones of the next launch (1024 x 1024, rank 16, us: 30 of 8 9.2, 31
 // 11.5, 36 15.2; 70 of 4 10.4, 74 13.8): the shares left out below.
 // Items against tiles of 64 tokens as they follow one another, whose adapters a cluster takes in
-// turn (us; 2048 x 8192, rank 32): 4096 tokens of six adapters in six runs 47 against 54, in no
-// order 47 against 92, of 64 adapters 60 against 444; 16384 in six runs 153 against 176.  2048 x 2048:
+// turn (us; 2048 x 8192, rank 32): 4096 tokens of six adapters in six runs 41 against 54, in no
+// order 42 against 92, of 64 adapters 53 against 444; 16384 in six runs 128 against 176.  2048 x 2048:
 // 32768 in six runs 188 against 146: beyond kMostGrouped tokens, or kMostCounted adapters, every
 // CTA would look through too much, and it is tiles (32768 in no order: 302 against 193).
 template <int RK, bool GROUPED>
