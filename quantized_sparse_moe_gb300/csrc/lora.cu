@@ -29,7 +29,7 @@
 //   4096 tokens, 2048 x 8192, rank 32: 41 us = 3.7 TB/s: 5 the items and their rows, 10 the first
 //     product and its exchange, 23 y and out at the rate of a plain copy; 16384: 128 us = 4.7 TB/s
 // The products themselves are small: mma.sync with operands in registers does
-// not limit any of them (tensor pipe 17% busy in the last case).
+// not limit any of them (tensor pipe 19% busy in the last case).
 //
 // Operands go from global memory straight into MMA fragments: the order of the
 // products of a sum is free, so a lane takes 8 or 16 consecutive values (16 or 32 bytes) of
