@@ -39,7 +39,7 @@
 // 512 bytes was slower, 2 TB/s; so were y's lines asked for in L2 ahead, 57 us for 54.)
 //
 // v is rounded for the second product: c v is split into bf16 parts, two of them
-// (2^-17 relative) for 16-bit outputs, which are rounded to 2^-9 anyway, three
+// (2^-17 relative) for 16-bit outputs, which are rounded to 2^-8 anyway, three
 // (exact but for fp32's own rounding) for 32-bit ones.
 #include "mx4_digits.cuh"
 
@@ -944,9 +944,9 @@ lora_kernel(const __grid_constant__ Params p) {
 // of 8, 74 of 4, 152 of 2, 304 of 1).  Slots have a cluster each while they fit; and columns come
 // in parts while SMs would be idle.
 // Items are of 16 tokens with clusters of 8, up to 32 with 4 or 2, else what fits: less of a
-// product's latency hangs on one item (us, clusters of 8, 4, 2, 1; six adapters: 300 tokens 2048 x
-// 2048 11.6 12.4 15.1 19.6; 904 1216 x 734 20 12.5 13.8 14.9; 1714 496 x 248 24 14.2 12.6 11.3; 4096 2048 x
-// 8192 63 46.2 46.9 58).  In launches that follow one another closely not all those clusters
+// product's latency hangs on one item (us, clusters of 8, 4, 2, 1; six to sixteen adapters: 300 tokens
+// 2048 x 2048 10.0 10.1 11.0 12.4; 904 1216 x 734 16 10.1 11.0 10.5; 1714 496 x 248 19 11.0 10.0 8.3; 4096
+// 2048 x 8192 57 42.0 41.6 51).  In launches that follow one another closely not all those clusters
 // find room beside the early ones of the next launch (1024 x 1024, rank 16, us: 30 of 8 9.2, 31
 // 11.5, 36 15.2; 70 of 4 10.4, 74 13.8): the shares left out below.
 // Items against tiles of 64 tokens as they follow one another, whose adapters a cluster takes in
