@@ -201,7 +201,7 @@ typedef struct {
 
 /* Bytes of w_split (0: not supported), and the exact split of w_router [E, H]
  * fp32 into three bf16 parts, in the order that the kernel reads (once per weight).
- * H a multiple of 64, E <= 512; both 16-byte aligned. */
+ * H a multiple of 64, E <= 512; both 16-byte aligned, without a byte in common. */
 QSM_API size_t moe_router_split_bytes(int32_t E, int32_t H);
 QSM_API qsm_status moe_router_split(const float* w_router, int32_t E, int32_t H, uint16_t* w_split,
                                     cudaStream_t stream);
@@ -212,7 +212,8 @@ QSM_API qsm_status moe_router_split(const float* w_router, int32_t E, int32_t H,
  * of groups too, to the lower index) in descending c, weighted with s.
  *   x [T, H] bf16, ldx elements from row to row (a multiple of 8, at least H);
  *   topk_idx [T, k] int32, topk_w [T, k] fp32 (out), as moe_group_tokens,
- *   moe_ffn_forward and moe_mx4_experts take them.
+ *   moe_ffn_forward and moe_mx4_experts take them; they may overlap neither each
+ *   other nor x, w_split or bias (QSM_ERR_INVALID_ARGUMENT).
  * Needs no workspace.  A logit that is not finite closes its expert, and so
  * does a bias of +infinity or NaN; either sets QSM_DEV_NONFINITE.  Where the taken
  * weights sum to 0 they are 0.

@@ -664,6 +664,8 @@ extern "C" qsm_status moe_router_split(const float* w_router, int32_t E, int32_t
     return QSM_ERR_INVALID_ARGUMENT;
   if (E > kMaxE) return QSM_ERR_UNSUPPORTED;
   const int mb = row_blocks(E);
+  if (mx4::overlap(mx4::Rows{w_router, 1, 0, (size_t)E * H * 4}, mx4::Rows{w_split, 1, 0, moe_router_split_bytes(E, H)}))
+    return QSM_ERR_INVALID_ARGUMENT;
   const long long units = (long long)mb * BM * (H / 8);
   QSM_CUDA_TRY(launch_pdl(split_kernel, dim3((unsigned)((units + 255) / 256)), dim3(256), 0, stream, w_router, (int)E,
                           (int)H, mb, reinterpret_cast<unsigned char*>(w_split), units));
@@ -683,6 +685,15 @@ extern "C" qsm_status moe_route_scores(const qsm_router* r, const uint16_t* x, i
       !aligned4(topk_idx) || !aligned4(topk_w) || !aligned4(dev_status) || (r->bias && !aligned4(r->bias)) ||
       ldx < r->H || ldx % 8)
     return QSM_ERR_INVALID_ARGUMENT;
+  // the tokens are selected at different times: what is written may hold nothing that is read
+  const auto vec = [](const void* p, size_t bytes) { return mx4::Rows{p, 1, 0, bytes}; };
+  const size_t out = (size_t)T * r->k * 4;
+  const mx4::Rows rx = {x, (size_t)T, (size_t)ldx * 2, (size_t)r->H * 2};
+  const mx4::Rows ids = vec(topk_idx, out), wts = vec(topk_w, out), split = vec(r->w_split, moe_router_split_bytes(r->E, r->H));
+  const mx4::Rows bias = vec(r->bias, (size_t)r->E * 4);
+  if (mx4::overlap(ids, wts)) return QSM_ERR_INVALID_ARGUMENT;
+  for (const mx4::Rows& w : {ids, wts})
+    if (mx4::overlap(w, rx) || mx4::overlap(w, split) || mx4::overlap(w, bias)) return QSM_ERR_INVALID_ARGUMENT;
   const int mb = row_blocks(r->E);
   const Config c = choose(r, T);
   if (c.nt == 0) return QSM_ERR_CUDA;

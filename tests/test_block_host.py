@@ -138,6 +138,23 @@ def test_route_scores_refuses_bad_arguments():
 
 
 @nvcc
+def test_route_scores_refuses_overlaps():
+    """The ids and weights are written while other tokens' x, the weights and the bias are read."""
+    import quantized_sparse_moe_gb300 as qsm
+    from quantized_sparse_moe_gb300 import block
+    L = qsm.lib()
+
+    def call(idx=at(1), w=at(2), T=4, ldx=128):
+        r = block.RouterC(128, 16, 4, 0, 1, 1, 1, 1, 1.0, at(4), at(5))
+        return L.moe_route_scores(ctypes.byref(r), at(0), ldx, T, idx, w, at(3), None)
+    for there in (at(0), at(0) + 3 * 256 + 240, at(4), at(4) + 2 * 3 * 128 * 64 * 2 - 4, at(5) + 60):
+        assert call(idx=there) == BAD and call(w=there) == BAD
+    assert call(w=at(1)) == BAD and call(w=at(1) + 60) == BAD and call(idx=at(2) - 60) == BAD
+    assert call(idx=at(0) + 256, ldx=256, T=100) == BAD  # 1600 bytes from the gap of 256 behind a row on
+    assert L.moe_router_split(P, 16, 128, P, None) == BAD and L.moe_router_split(P, 16, 128, P + 16 * 128 * 4 - 16, None) == BAD
+
+
+@nvcc
 def test_lora_refuses_bad_arguments():
     import quantized_sparse_moe_gb300 as qsm
     from quantized_sparse_moe_gb300 import block
