@@ -579,8 +579,10 @@ QSM_API qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x, in
  * arithmetic, always in separate launches, on a workspace of
  * moe_mx4_workspace_bytes(L, T, acts), for QSM_ACTS_BF16 with
  * QSM_ACTS_SEPARATE_LAUNCHES added.  An id outside [0, E) sets QSM_DEV_BAD_EXPERT_ID
- * with QSM_ACTS_MX4; its assignment is left out in either form.  The k ids of a
- * token have to differ from one another, as a router's do. */
+ * with QSM_ACTS_MX4; its assignment is left out in either form.  An expert that a
+ * token names more than once counts with the sum of its weights with QSM_ACTS_MX4;
+ * with QSM_ACTS_BF16 the ids of a token have to differ, as a router's do: else that token's y is
+ * not a number and QSM_DEV_BAD_EXPERT_ID is set. */
 QSM_API qsm_status moe_mx4_experts(const qsm_mx4_layer* L, const uint16_t* x, int32_t T, int32_t acts,
                                    const int32_t* topk_idx, const float* topk_w, uint16_t* y, float* y_f32,
                                    void* workspace, size_t workspace_bytes, int32_t* dev_status,

@@ -164,6 +164,11 @@ mx4_scatter_kernel(const uint16_t* __restrict__ x, int T, int k, int H, int E,
 // token took the layer from 197 to 212 us, column passes that keep o in L2 from
 // 197.6 to 199.5, the powers by way of shared memory from 191.5 to 198.7 (spills).
 //
+// given: null, or the status word of a call whose choice is the caller's.  An
+// expert that a token names again has been worked on as one of the two, another
+// one in each CTA (mx4_stream.cu): such a token's y is not a number.  (Looking for it here
+// costs 0.1 us a layer; where the slots are formed, 0.5 to 1.3.)
+//
 // GATED: one CTA has a whole token, because y may be x: it has read all of x[t]
 // for the gate when it writes y[t], and no other CTA reads x[t].  (The 128
 // threads that add up x . shared_gate are those of an ungated CTA.)
@@ -173,7 +178,7 @@ __global__ void __launch_bounds__(GATED ? kGatedThreads : kCombThreads,
 mx4_combine_kernel(const void* __restrict__ o, const float* __restrict__ oscale, const int32_t* __restrict__ at,
                    const float* __restrict__ topk_w, const uint16_t* x,
                    const float* __restrict__ sgate, int T, int k, int H, int E,
-                   uint16_t* y, float* y32) {
+                   uint16_t* y, float* y32, int32_t* given) {
   __shared__ int rows[kMaxK];
   __shared__ float wts[kMaxK], red[kCombThreads / 32];
   pdl_wait();
@@ -184,6 +189,13 @@ mx4_combine_kernel(const void* __restrict__ o, const float* __restrict__ oscale,
     const int r = __ldcg(at + (size_t)t * k + tid);
     rows[tid] = HALF ? r : (unsigned)r < (unsigned)E ? t * k + tid : -1;
     wts[tid] = __ldcg(topk_w + (size_t)t * k + tid);
+    if (!HALF && given) {
+      const uint32_t same = __match_any_sync(0xffffffffu >> (32 - k), r);
+      if (rows[tid] >= 0 && (same & (same - 1)) != 0) {
+        wts[tid] = __uint_as_float(0x7fc00000u);
+        set_status(given, QSM_DEV_BAD_EXPERT_ID);
+      }
+    }
   }
   float g = 1.f;
   if (GATED && tid < kCombThreads) {
@@ -573,7 +585,8 @@ qsm_status forward(const qsm_mx4_layer* L, const uint16_t* x, int32_t T, int32_t
                     : (gated ? mx4_combine_kernel<false, true> : mx4_combine_kernel<false, false>);
   QSM_CUDA_TRY(launch_pdl(comb, grid, dim3(threads), 0, stream, (const void*)(ws + p.o),
                           (const float*)(ws + p.oscale), half ? (const int32_t*)i32(p.pos) : (const int32_t*)topk_idx,
-                          (const float*)topk_w, x, L->shared_gate, T, (int)L->k, (int)L->H, (int)L->E, y, y_f32));
+                          (const float*)topk_w, x, L->shared_gate, T, (int)L->k, (int)L->H, (int)L->E, y, y_f32,
+                          routed ? dev_status : nullptr));
   return QSM_OK;
 }
 

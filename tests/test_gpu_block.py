@@ -273,3 +273,41 @@ def test_the_example_runs_with_all_of_them():
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "tokens" in r.stdout
+
+
+@pytest.mark.parametrize("T,acts", [(1, "bf16"), (5, "bf16"), (17, "bf16"), (64, "bf16"), (5, "mx4"), (130, "mx4")])
+@pytest.mark.parametrize("k", [2, 4, 32])
+def test_an_expert_named_more_than_once(qsm, T, acts, k):
+    """moe_mx4_experts: with 4-bit activations its weights add up, with 16-bit ones such tokens are
+    refused on the device, the others as ever.  The workspace holds zeros, which would pass for an output."""
+    import ctypes
+    from quantized_sparse_moe_gb300 import mx4
+    H, I, E = 256, 128, 40
+    L, v, _ = mx4_layer(qsm, H, I, E, k, 5, router=False)
+    x = torch.randn((T, H), generator=gen(80 + T), device="cuda").bfloat16()
+    w = torch.rand((T, k), generator=gen(81), device="cuda") / k
+    ids = torch.stack([torch.randperm(E, generator=gen(82 + t), device="cuda")[:k] for t in range(T)]).int()
+    ids[0] = E - 1                                                      # all the same
+    ids[T // 2, 0] = ids[T // 2, k - 1]                                 # the first and the last one
+    if T > 2:
+        w[2], ids[2] = 0, 0                                             # padding
+        ids[1] = torch.arange(k, device="cuda").int()
+        ids[1, :2], w[1, :2] = E, 0                                     # out of range, twice: left out
+    twice = torch.tensor([len(set(row)) < len(row) for row in ids.tolist()], device="cuda")
+    twice[1:2] = False
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(qsm.moe_mx4_workspace_bytes(L, T, acts, False), dtype=torch.uint8, device="cuda")
+    y, y32 = torch.empty_like(x), torch.empty(T, H, device="cuda")
+    assert mx4.lib().moe_mx4_experts(ctypes.byref(L.c), x.data_ptr(), T, 16 if acts == "bf16" else 1, ids.data_ptr(), w.data_ptr(),
+                                     y.data_ptr(), y32.data_ptr(), ws.data_ptr(), ws.numel(), st.data_ptr(),
+                                     torch.cuda.current_stream().cuda_stream) == 0
+    one = lambda j, w: _mx4_ref.moe(x, ids[:, j:j + 1].long().clamp_max(E - 1), w[:, j:j + 1], *v, four=acts == "mx4")  # noqa: E731
+    shared = one(0, torch.zeros_like(w))
+    want = shared + sum(one(j, w) - shared for j in range(k))
+    if acts == "bf16":
+        assert y32[twice].isnan().all() and y[twice].isnan().all() and st.item() & 1
+        y, y32, want = y[~twice], y32[~twice], want[~twice]
+    d = y32.double() - want
+    if len(d):
+        assert (d.norm() / want.norm()).item() <= 3e-3 if acts == "mx4" else (d.abs().max() / want.abs().max()).item() <= 2e-3
+    assert torch.equal(y, y32.to(torch.bfloat16))
