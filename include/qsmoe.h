@@ -582,7 +582,8 @@ QSM_API qsm_status moe_mx4_forward(const qsm_mx4_layer* L, const uint16_t* x, in
  * with QSM_ACTS_MX4; its assignment is left out in either form.  An expert that a
  * token names more than once counts with the sum of its weights with QSM_ACTS_MX4;
  * with QSM_ACTS_BF16 the ids of a token have to differ, as a router's do: else that token's y is
- * not a number and QSM_DEV_BAD_EXPERT_ID is set. */
+ * not a number and QSM_DEV_BAD_EXPERT_ID is set.  y and y_f32 may not overlap
+ * topk_idx or topk_w (QSM_ERR_INVALID_ARGUMENT). */
 QSM_API qsm_status moe_mx4_experts(const qsm_mx4_layer* L, const uint16_t* x, int32_t T, int32_t acts,
                                    const int32_t* topk_idx, const float* topk_w, uint16_t* y, float* y_f32,
                                    void* workspace, size_t workspace_bytes, int32_t* dev_status,

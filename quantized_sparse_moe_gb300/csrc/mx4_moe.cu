@@ -558,6 +558,11 @@ qsm_status forward(const qsm_mx4_layer* L, const uint16_t* x, int32_t T, int32_t
   Plan p;
   if (!plan_of(L, T, acts, &p)) return QSM_ERR_UNSUPPORTED;
   if (workspace_bytes < p.total) return QSM_ERR_WORKSPACE_TOO_SMALL;
+  // one token's y is written while another's choice is read
+  const size_t choice = (size_t)T * L->k * 4;
+  if (routed && (overlap(y, n * 2, topk_idx, choice) || overlap(y, n * 2, topk_w, choice) ||
+                 (y_f32 && (overlap(y_f32, n * 4, topk_idx, choice) || overlap(y_f32, n * 4, topk_w, choice)))))
+    return QSM_ERR_INVALID_ARGUMENT;
   char* ws = static_cast<char*>(workspace);
   if (p.one)
     return one_launch(L, p, x, w_router, logit_bias, flags, topk_idx, topk_w, y, y_f32, ws, dev_status, stream);

@@ -218,3 +218,22 @@ def test_experts_refuse_bad_arguments():
         assert need > 0 and call(layer(), T=T, acts=acts, ws=need - 1) == SMALL
     with pytest.raises(qsm.QSMError):
         qsm.MoEForward(type("L", (), dict(H=256, E=8, k=2))(), 4, router=type("R", (), dict(H=256, E=8, k=3))())
+
+
+@nvcc
+def test_experts_refuse_outputs_over_the_choice():
+    """One token's y is written while another's ids and weights are read."""
+    import quantized_sparse_moe_gb300 as qsm
+    from quantized_sparse_moe_gb300 import mx4
+    lib = qsm.lib()
+    H, I, E, k, T = 256, 128, 8, 2, 4
+    L = mx4.Mx4LayerC(H, I, E, k, mx4.Mx4C(E, 2 * I, H, at(1), at(2)), mx4.Mx4C(E, H, I, at(3), at(4)),
+                      mx4.Mx4C(1, 2 * I, H, at(5), at(6)), mx4.Mx4C(1, H, I, at(7), at(8)), None)
+
+    def call(y=at(10), y32=at(11), idx=at(12), w=at(13), acts=0):
+        return lib.moe_mx4_experts(ctypes.byref(L), at(0), T, acts, idx, w, y, y32, at(14), 1 << 40, at(15), None)
+    n = T * H * 2
+    for acts in (0, 1):
+        assert call(idx=at(10), acts=acts) == BAD and call(w=at(10), acts=acts) == BAD
+        assert call(idx=at(10) + n - 4, acts=acts) == BAD and call(w=at(10) - 4, acts=acts) == BAD
+        assert call(idx=at(11) + 2 * n - 4, acts=acts) == BAD and call(w=at(11) - 28, acts=acts) == BAD
