@@ -12,7 +12,8 @@ Entry points (see include/qsmoe.h for the exact contracts):
   moe_route, moe_group_tokens, moe_ffn_forward, q8_gemv
 plus ``MoEForward``, which owns the buffers of one layer call and issues the
 three calls in order on one stream; the MXFP4 calls are in mx4.py, those around
-the products (the residual stream and its norms) in block.py.
+the products (the residual stream and its norms, routing by scores, low-rank
+adapters) in block.py.
 """
 from __future__ import annotations
 
@@ -500,6 +501,9 @@ class MoEForward:
         if router is not None:
             if (router.H, router.E, router.k) != (layer.H, layer.E, layer.k):
                 raise QSMError("MoEForward: the router's H, E and k must be the layer's")
+            on = torch.device(device)
+            if on.type != "cuda" or router.device != (torch.cuda.current_device() if on.index is None else on.index):
+                raise QSMError("MoEForward: the router is on another device")
             one_launch = False
         self.renormalize = route_flags(renormalize, bias_select_only)
         self.fuse_route_group = fuse_route_group
@@ -510,8 +514,9 @@ class MoEForward:
         i32 = dict(dtype=torch.int32, device=device)
         self.topk_idx = torch.empty((T, k), **i32)
         self.topk_w = torch.empty((T, k), dtype=torch.float32, device=device)
-        self.route_ws = torch.zeros(max(route_workspace_bytes(T, H, E), 256),
-                                    dtype=torch.uint8, device=device)
+        self.route_ws = (torch.zeros(max(route_workspace_bytes(T, H, E), 256),
+                                     dtype=torch.uint8, device=device)
+                         if router is None else None)
         self.grouping = Grouping.empty(T, k, E, ffn_tile_rows(T), device)
         self.ffn_ws = torch.empty(max(ffn_workspace_bytes(layer, T), 256),
                                   dtype=torch.uint8, device=device)

@@ -237,3 +237,11 @@ def test_experts_refuse_outputs_over_the_choice():
         assert call(idx=at(10), acts=acts) == BAD and call(w=at(10), acts=acts) == BAD
         assert call(idx=at(10) + n - 4, acts=acts) == BAD and call(w=at(10) - 4, acts=acts) == BAD
         assert call(idx=at(11) + 2 * n - 4, acts=acts) == BAD and call(w=at(11) - 28, acts=acts) == BAD
+
+
+def test_layer_refuses_a_router_of_another_device():
+    import quantized_sparse_moe_gb300 as qsm
+    layer, router = (type(n, (), dict(H=256, E=8, k=2, device=1)) for n in "LR")
+    for device in ("cuda:0", "cpu"):
+        with pytest.raises(qsm.QSMError):
+            qsm.MoEForward(layer(), 4, device, router=router())
