@@ -554,6 +554,8 @@ class MoEForward:
             return y
         fused = None
         if self.router is not None:
+            if not x.is_contiguous():  # the router would take it, the FFN does not
+                raise QSMError("MoEForward: x must be a contiguous bf16 tensor")
             self.router.route(x, self.topk_idx, self.topk_w, self.dev_status, stream)
             moe_group_tokens(self.topk_idx, L.E, self.grouping.tile_rows,
                              self.grouping, self.dev_status, stream)

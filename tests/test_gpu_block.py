@@ -93,6 +93,19 @@ def test_layers_refuse_other_routers(qsm):
         f(torch.zeros(5, 512, dtype=torch.bfloat16, device="cuda"))
 
 
+def test_q8_layer_routed_by_scores_refuses_strided_tokens(qsm):
+    """The router takes rows at any stride, the expert products do not: nothing is launched."""
+    shape = synth.TINY
+    Lg, _, wr, _ = cases.layer(shape)
+    r = qsm.MoERouter(Lg.w_router, shape.k)
+    L = qsm.Layer(shape.H, shape.I, shape.E, shape.k, Lg.gate_up, Lg.down, Lg.shared_gate_up, Lg.shared_down, None)
+    f = qsm.MoEForward(L, 4, router=r)
+    f.topk_idx.fill_(-7)
+    with pytest.raises(qsm.QSMError):
+        f(torch.zeros(4, 2 * shape.H, dtype=torch.bfloat16, device="cuda")[:, :shape.H])
+    assert (f.topk_idx == -7).all() and f.route_ws is None
+
+
 def test_ids_out_of_range_leave_their_assignment_out(qsm):
     """moe_mx4_experts itself."""
     import ctypes
