@@ -41,20 +41,16 @@
 // v is rounded for the second product: c v is split into bf16 parts, two of them
 // (2^-17 relative) for 16-bit outputs, which are rounded to 2^-8 anyway, three
 // (exact but for fp32's own rounding) for 32-bit ones.
+#include "lora_cut.cuh"
 #include "mx4_digits.cuh"
 
 namespace qsm {
 namespace lora {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 64;    // tokens, at most
 constexpr int kMaxRank = 128;
 constexpr int kMaxSide = 1 << 28;  // of K and N
 constexpr int kMostSmem = 200 * 1024;  // dynamic
-constexpr int kMostCounted = 1023;      // adapters whose tokens a CTA counts
-constexpr int kMostGrouped = 1 << 14;   // tokens that a CTA looks through; their ids fit where the partial sums will lie
 
 struct Params {
   const uint16_t* x;
@@ -696,10 +692,17 @@ __device__ __forceinline__ int find_item(const Params& p, int item, int* cnt, in
   int tile = min(max(((p.T + p.room - 1) / p.room + 7) / 8 * 8, 16), kTile);  // less makes too many
 #pragma unroll 1
   for (; tile < kTile; tile += 8) {
-    int count = 0;
+    int count = 0, used = 0;
 #pragma unroll 1
-    for (int i = lane; i < ids; i += 32) count += (cnt[i] + tile - 1) / tile;
+    for (int i = lane; i < ids; i += 32) {
+      count += (cnt[i] + tile - 1) / tile;
+      used += cnt[i] > 0;
+    }
     if (__reduce_add_sync(0xffffffffu, count) <= p.room) break;
+    if (__reduce_add_sync(0xffffffffu, used) > p.room) {  // no tile does
+      tile = kTile;
+      break;
+    }
   }
   int id = 0, from = 0, before = 0;
   m = 0;
@@ -939,21 +942,6 @@ lora_kernel(const __grid_constant__ Params p) {
   if (p.cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The cut: a launch in one wave if it can be.  Clusters of 8 CTAs, fewer when there are more
-// slots or items than such clusters fit on the device at once (a GB300, two CTAs an SM: 36
-// of 8, 74 of 4, 152 of 2, 304 of 1).  Slots have a cluster each while they fit; and columns come
-// in parts while SMs would be idle.
-// Items are of 16 tokens with clusters of 8, up to 32 with 4 or 2, else what fits: less of a
-// product's latency hangs on one item (us, clusters of 8, 4, 2, 1; six to sixteen adapters: 300 tokens
-// 2048 x 2048 10.0 10.1 11.0 12.4; 904 1216 x 734 16 10.1 11.0 10.5; 1714 496 x 248 19 11.0 10.0 8.3; 4096
-// 2048 x 8192 57 42.0 41.6 51).  In launches that follow one another closely not all those clusters
-// find room beside the early ones of the next launch (1024 x 1024, rank 16, us: 30 of 8 9.2, 31
-// 11.5, 36 15.2; 70 of 4 10.4, 74 13.8): the shares left out below.
-// Items against tiles of 64 tokens as they follow one another, whose adapters a cluster takes in
-// turn (us; 2048 x 8192, rank 32): 4096 tokens of six adapters in six runs 41 against 54, in no
-// order 42 against 92, of 64 adapters 53 against 444; 16384 in six runs 128 against 176.  2048 x 2048:
-// 32768 in six runs 188 against 146: beyond kMostGrouped tokens, or kMostCounted adapters, every
-// CTA would look through too much, and it is tiles (32768 in no order: 302 against 193).
 template <int RK, bool GROUPED>
 qsm_status launch(Params& p, bool f32, cudaStream_t stream) {
   static_assert(parts_bytes<RK>(kTile) >= kMostGrouped * 4, "find_item has the ids there");
@@ -962,28 +950,20 @@ qsm_status launch(Params& p, bool f32, cudaStream_t stream) {
   p.tile = p.T < kTile ? p.T : kTile;
   p.rows = (p.tile + 7) / 8 * 8;
   const int smem = (int)(f32 ? smem_bytes<RK, 3>(p.rows, p.how) : smem_bytes<RK, 2>(p.rows, p.how)) + (GROUPED ? (p.n + 1) * 4 : 0);
-  const auto resident = [&](int cs) {
-    const long long r = mx4::resident_clusters(reinterpret_cast<void*>(kernel), cs, kThreads, smem, kMostSmem);
-    return cs == 1 ? 2 * r : !GROUPED ? r : cs == 8 ? r - r / 6 : cs == 4 ? r - r / 18 : r;
-  };
-  const auto tiles_of = [&](int tile) { return ((long long)p.T + tile - 1) / tile; };
-  const auto items_of = [&](int tile) { return tiles_of(tile) + (p.n + 1ll < p.T ? p.n + 1 : p.T); };  // at most
-  const int one = p.n + 1ll < p.tile ? p.n + 1 : p.tile;  // slots of a tile at most
-  p.cs = 8;
-  while (p.cs > 1 && (GROUPED ? items_of(p.cs == 8 ? 16 : 32) : p.T <= kTile ? one : tiles_of(kTile)) > resident(p.cs)) p.cs /= 2;
-  const long long room = resident(p.cs);
-  if (room < 1) return QSM_ERR_CUDA;
-  const long long tiles = GROUPED ? 1 : tiles_of(p.tile);
-  long long lanes = tiles * one <= room ? one : room / tiles < 1 ? 1 : room / tiles;
-  if (GROUPED) lanes = items_of(16) < room ? items_of(16) : items_of(kTile) > room ? items_of(kTile) : room;
-  p.lanes = (int)lanes;
-  p.parts = 1;
-  const int chunks = (p.N + 31) / 32;
-  while (tiles * lanes * p.parts * 2 <= room && p.parts * 2 * p.cs * kWarps <= chunks) p.parts *= 2;
-  p.room = (int)(lanes < room / p.parts ? lanes : room / p.parts);
-  const long long ctas = tiles * lanes * p.parts * p.cs;
-  if (ctas > 0x7fffffffll) return QSM_ERR_UNSUPPORTED;
-  QSM_CUDA_TRY(launch_pdl_cluster(kernel, dim3((unsigned)ctas), dim3(kThreads), p.cs, (size_t)smem, stream, p));
+  void* asked = reinterpret_cast<void*>(kernel);
+  // Registers allow two CTAs an SM, shared memory only one to fp32 with more than 64 ranks where rows are not whole
+  // 16-byte units, or beside 820 adapters' counters (4096 tokens, 2048 x 2050, rank 128, 100 adapters: 265 us, cut for two 299).
+  int each = mx4::resident_ctas(asked, kThreads, smem, kMostSmem);
+  if (each > 2) each = 2;
+  const Cut c = cut(GROUPED, p.T, p.n, p.N, (long long)each * mx4::sm_count(),
+                    [&](int cs) { return mx4::resident_clusters(asked, cs, kThreads, smem, kMostSmem); });
+  if (c.ctas < 1) return QSM_ERR_CUDA;
+  p.cs = c.cs;
+  p.lanes = c.lanes;
+  p.parts = c.parts;
+  p.room = c.room;
+  if (c.ctas > 0x7fffffffll) return QSM_ERR_UNSUPPORTED;
+  QSM_CUDA_TRY(launch_pdl_cluster(kernel, dim3((unsigned)c.ctas), dim3(kThreads), p.cs, (size_t)smem, stream, p));
   return QSM_OK;
 }
 
@@ -1047,7 +1027,7 @@ extern "C" qsm_status lora_add(const qsm_lora* L, const uint16_t* x, int64_t ldx
   p.copy = !same;
   p.status = dev_status;
   const bool f32 = dtype == QSM_FP32;
-  if (T > kTile && T <= kMostGrouped && L->n <= kMostCounted)
+  if (grouped(T, L->n))
     return L->rank <= 32 ? launch<1, true>(p, f32, stream) : L->rank <= 64 ? launch<2, true>(p, f32, stream) : launch<4, true>(p, f32, stream);
   return L->rank <= 32 ? launch<1, false>(p, f32, stream) : L->rank <= 64 ? launch<2, false>(p, f32, stream) : launch<4, false>(p, f32, stream);
 }

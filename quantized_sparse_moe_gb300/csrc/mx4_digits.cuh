@@ -98,17 +98,25 @@ __device__ __forceinline__ void store_digits(const uint32_t (&plane)[kDigits], u
   }
 }
 
+struct KeptResidents {
+  std::mutex mu;
+  KeptAnswers answers;
+};
+inline KeptResidents& kept_residents() {
+  static KeptResidents k;
+  return k;
+}
+
 // Clusters of cs CTAs of `kernel` that the current device holds at once; 0 when
 // the query fails.  Allows the kernel smem_max bytes of dynamic shared memory.
 // Answers are kept: a program with several projections and a varying number of
 // rows asks for hundreds of geometries in turn.
 inline int resident_clusters(void* kernel, int cs, int threads, int smem, int smem_max) {
-  static std::mutex mu;
-  static KeptAnswers kept;
+  auto& k = kept_residents();
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  if (kept.find(dev, kernel, cs, smem, &n)) return n;
+  std::lock_guard<std::mutex> lock(k.mu);
+  if (k.answers.find(dev, kernel, cs, smem, &n)) return n;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) != cudaSuccess)
     return 0;
   n = sm_count();
@@ -125,7 +133,23 @@ inline int resident_clusters(void* kernel, int cs, int threads, int smem, int sm
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
   }
-  kept.put(dev, kernel, cs, smem, n);
+  k.answers.put(dev, kernel, cs, smem, n);
+  return n;
+}
+
+// The same for CTAs without a cluster: how many an SM holds at once (kept beside
+// the clusters' answers, as those of 0 CTAs).
+inline int resident_ctas(void* kernel, int threads, int smem, int smem_max) {
+  auto& k = kept_residents();
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(k.mu);
+  if (k.answers.find(dev, kernel, 0, smem, &n)) return n;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) != cudaSuccess)
+    return 0;
+  max_smem_carveout(kernel);  // as its launches
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) n = 0;
+  k.answers.put(dev, kernel, 0, smem, n);
   return n;
 }
 
