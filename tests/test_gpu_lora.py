@@ -304,3 +304,73 @@ def test_adapters_in_any_order(qsm, T, n):
     z = y.clone()
     qsm.lora_add(x, L, bad, z, out=z, dev_status=st)
     assert torch.equal(z, out) and st.item() == (16 if (ids < 0).any() else 0)
+
+
+@pytest.mark.parametrize("rank", [8, 40, 64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,n,N", [(100, 1100, 40), (700, 2000, 41), (130, 1030, 72), (16500, 9, 40), (16500, 3, 33)])
+def test_tiles_one_after_another(qsm, rank, dtype, T, n, N):
+    """More than 64 tokens that are not grouped by adapter (too many adapters, or tokens): several tiles, and
+    clusters that take many slots in turn, at every number of ranks."""
+    L = adapters(qsm, n, rank, 72, N, 70, scale=N % 2 == 0)
+    x = randn(T, 72, seed=75).bfloat16()
+    ids = torch.randint(-1, n, (T,), generator=gen(76), device="cuda").int()
+    if T > 2000:
+        ids[:9000] = 2
+    y = randn(T, N, seed=77).to(dtype)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = qsm.lora_add(x, L, ids, y, dev_status=st)
+    # the bound of definition(), all tokens at once
+    a, b = L.a.double().nan_to_num(0), L.b.double().nan_to_num(0)
+    i = ids.long().clamp_min(0)
+    c = (ids >= 0).double()[:, None] * (1.0 if L.scale is None else L.scale.double()[i][:, None])
+    split = 2.0 ** -17 if dtype is torch.bfloat16 else 2.0 ** -23
+    want, err = y.double(), torch.zeros(T, N, dtype=torch.float64, device="cuda")
+    for t in torch.arange(T, device="cuda").split(500):
+        at, bt, xt = a[i[t]], b[i[t]], x[t].double()
+        v = torch.einsum("tk,trk->tr", xt, at) * c[t]
+        dv = (72 / 128 + 40) * 2 * U * torch.einsum("tk,trk->tr", xt.abs(), at.abs()) * c[t].abs() + (split + 2 * U) * v.abs()
+        want[t] += torch.einsum("tr,tnr->tn", v, bt)
+        err[t] = torch.einsum("tr,tnr->tn", dv, bt.abs()) + (rank / 4 + 40) * 2 * U * torch.einsum("tr,tnr->tn", v.abs() + dv, bt.abs())
+    err = err + 2 * U * (want.abs() + err)
+    assert ref.lies_between(out, want.cpu(), err.cpu()) and st.item() == 0
+    assert torch.equal(out[ids < 0], y[ids < 0])
+
+
+@pytest.mark.parametrize("R", [24, 32, 64, 128])
+@pytest.mark.parametrize("T,n", [(5, 2), (40, 3), (64, 2), (200, 3), (200, 1100), (16500, 5)])
+def test_whole_numbers_are_exact(qsm, R, T, n):
+    """fp32 outputs: A x up to 2^22 in whole numbers, a row of B with a single one of 1, -2 or 4: exact,
+    whichever way the second product takes (slots, items or tiles; rows of whole 16-byte units or not)."""
+    K = 1024
+    a = torch.randint(-64, 65, (n, R, K), generator=gen(1), device="cuda").bfloat16()
+    x = torch.randint(-64, 65, (T, K), generator=gen(2), device="cuda").bfloat16()
+    ids = torch.randint(0, n, (T,), generator=gen(3), device="cuda").int()
+    v = torch.cat([torch.einsum("tk,trk->tr", x[t].float(), a[ids[t].long()].float()).double()   # whole: exact in fp32
+                   for t in torch.arange(T, device="cuda").split(256)])
+    assert v.abs().max() > 1 << 16 and v.abs().max() < 1 << 22
+    for N in (R, R + 5, 2 * R + 8):
+        row = torch.arange(N, device="cuda")
+        b = torch.zeros(n, N, R, device="cuda")
+        factor = torch.tensor([1.0, -2.0, 4.0], device="cuda")[row % 3]
+        b[:, row, (row * 7 + 3) % R] = factor
+        L = qsm.LoraAdapters(a, b.bfloat16())
+        want = v[:, (row * 7 + 3) % R] * factor.double()
+        assert torch.equal(qsm.lora_add(x, L, ids, dtype=torch.float32).double(), want)
+        y = torch.randint(-64, 65, (T, N), generator=gen(4), device="cuda").float()
+        assert torch.equal(qsm.lora_add(x, L, ids, y).double(), want + y.double())
+
+
+@pytest.mark.parametrize("T,n", [(50, 4), (500, 4), (500, 1100)])
+@pytest.mark.parametrize("rank", [16, 64])
+def test_a_token_does_not_depend_on_the_others_values(qsm, T, n, rank):
+    """The others' x and y change, the ids stay: the same bits, at a K of many blocks for each warp."""
+    L = adapters(qsm, n, rank, 8192, 264, 90, mixed=False)
+    ids = torch.randint(-1, 4, (T,), generator=gen(91), device="cuda").int()
+    x, y = randn(T, 8192, seed=92).bfloat16(), randn(T, 264, seed=93)
+    out = qsm.lora_add(x, L, ids, y)
+    keep = torch.rand(T, generator=gen(94), device="cuda") < 0.1
+    z = torch.where(keep[:, None], x, randn(T, 8192, seed=95).bfloat16())
+    z[~keep, 5] = float("nan")
+    w = torch.where(keep[:, None], y, randn(T, 264, seed=96))
+    assert torch.equal(qsm.lora_add(z, L, ids, w)[keep], out[keep])

@@ -292,3 +292,40 @@ def test_offsets_that_pass_32_bits(qsm):
     want, ww = r.route(x[-40:].clone())
     assert torch.equal(ids[-40:], want) and (w[-40:] - ww).abs().max().item() <= 1e-5
     assert torch.equal(ids[:1000], torch.arange(k, device="cuda", dtype=torch.int32).expand(1000, k))
+
+
+def last_bits(E, H):
+    """w [E, H] of 24 significant bits, whose order in each column lies in the last of them:
+    4 + (2^14 + 8 p + 3) 2^-21 with p = (e + column) mod E.  The first 8 bits are 4, the next
+    8 units of 2^-14, and p goes down to 2^-18."""
+    p = (torch.arange(E)[:, None] + torch.arange(H)[None]) % E
+    return p, (4 + (2 ** 14 + 8 * p + 3).double() * 2.0 ** -21).float()
+
+
+@pytest.mark.parametrize("E", [5, 100, 128, 256, 300, 512])
+@pytest.mark.parametrize("T,H", [(1, 64), (1, 2048), (37, 704), (300, 2048), (4096, 2048)])
+def test_every_bit_of_the_weights_counts(qsm, T, H, E):
+    """A token is a multiple of a unit vector: its logits are a column of w, exactly, so that ids and weights
+    hang on the last bits alone.
+    Softmax, logits of 64: neighbours are 2^-14 apart and all within 0.04 of the best one.  A weight collects
+    4 roundings of the exponential (two units in the last place), 21 of the sum and the exponentials in it
+    4 more, 4 of the quotient (two units), 1: 34 U; divided by the sum of k, twice that, k and 5 more.
+    Sigmoid, logits of -8: neighbours 2^-17 apart; the exponential of 8 to 11 units in the last place (22 U),
+    1, 4 of the quotient: 27 U.  Without the last 8 bits a weight would be off by up to 2^-11 and 2^-14."""
+    k = min(E, 8)
+    p, w = last_bits(E, H)
+    col = torch.arange(T) * 37 % H
+    r = w.cuda()
+    for score, f, bound in (("softmax", 16.0, 34 * U), ("sigmoid", -2.0, 27 * U)):
+        x = torch.zeros(T, H)
+        x[torch.arange(T), col] = f
+        l = f * w.double()[:, col].T                      # exact
+        s = torch.softmax(l, dim=1) if score == "softmax" else torch.sigmoid(l)
+        want = torch.sort(l, dim=1, descending=True).indices[:, :k]
+        for renorm in (False, True):
+            ids, wt = qsm.moe_route_scores(x.bfloat16().cuda(), qsm.MoERouter(r, k, score, renormalize=renorm))
+            ww, tol = s.gather(1, want), bound
+            if renorm:
+                ww, tol = ww / ww.sum(dim=1, keepdim=True), 2 * bound + (k + 5) * U
+            assert torch.equal(ids.cpu().long(), want)
+            assert ((wt.cpu().double() - ww).abs() <= tol * ww).all()
