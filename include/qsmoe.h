@@ -216,7 +216,8 @@ QSM_API qsm_status moe_router_split(const float* w_router, int32_t E, int32_t H,
  *   other nor x, w_split or bias (QSM_ERR_INVALID_ARGUMENT).
  * Needs no workspace.  A logit that is not finite closes its expert, and so
  * does a bias of +infinity or NaN; either sets QSM_DEV_NONFINITE.  Where the taken
- * weights sum to 0 they are 0.
+ * weights sum to 0 they are 0.  Scores are fp32 numbers: experts whose scores round to
+ * the same one tie (a sigmoid is 1 from logits of 17 on, and 0 below -87).
  * Requires H % 64 == 0, E <= 512, k <= 32 and <= the kept groups' experts,
  * groups <= 32 dividing E. */
 QSM_API qsm_status moe_route_scores(const qsm_router* r, const uint16_t* x, int64_t ldx, int32_t T,
@@ -625,7 +626,9 @@ typedef struct {
  *   x_out[t] = x[t] + scale * gate[t] * post(y[t])
  *   h[t]     = pre(x_out[t])              of x_out before it is rounded
  * y is the output of the block before (NULL: x_out = x), h the input of the
- * block after.  Infinities and NaN take their way through the formulas.
+ * block after.  Infinities and NaN take their way through the formulas, and so
+ * does a row whose squares add up to 2^128 or more, which fp32 does not hold: its
+ * norm is the bias, or 0.
  *   x, y, x_out, h  [T, H] with ldx, ldy, ldo, ldh elements from row to row
  *       (at least H; rows 16-byte aligned).  x_out or h may be NULL, not both;
  *       h needs a pre.
@@ -666,7 +669,9 @@ typedef struct {
  *   out[t] = y[t] + scale[i] * b[i] (a[i] x[t]),  i = ids[t];
  * a negative id: none, out[t] = y[t].  The ids may come in any order.  Sums in fp32, out rounded once (a bf16
  * out: a[i] x[t] enters the second product to 2^-17).  A token's result does not depend
- * on the other tokens' values.
+ * on the other tokens' values; the order of its sums may depend on T and on how many tokens share its
+ * adapter.  Where b holds an infinity the result may be NaN instead (scale[i] a[i] x[t] is
+ * multiplied with it in parts).
  *   x [T, K] bf16, ldx elements from row to row (a multiple of 8, at least
  *   K), 16-byte aligned;  ids [T] int32;  y [T, N] (NULL: zeros) and out [T, N] of type
  *   dtype (QSM_BF16 or QSM_FP32), ldy and ldo elements from row to row (at least N),

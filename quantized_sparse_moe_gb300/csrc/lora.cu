@@ -28,6 +28,9 @@
 //     B; the SMs have one or two CTAs each, and plain loads give at most 5.4 TB/s
 //   4096 tokens, 2048 x 8192, rank 32: 41 us = 3.7 TB/s: 5 the items and their rows, 10 the first
 //     product and its exchange, 23 y and out at the rate of a plain copy; 16384: 128 us = 4.7 TB/s
+//   the same with 64 ranks 65 us, 128 109; with fp32 y and out 59 (32 ranks), 92 (64), 154 (128)
+// At 128 registers a thread the kernels for up to 32 ranks spill 32 to 68 bytes, those for 65 to 128 ranks 32
+// to 276 (the latter's fp32 form); those between do not.
 // The products themselves are small: mma.sync with operands in registers does
 // not limit any of them (tensor pipe 19% busy in the last case).
 //

@@ -29,14 +29,18 @@ struct Cut {
 // Items are of 16 tokens with clusters of 8, up to 32 with 4 or 2, else what fits: less of a
 // product's latency hangs on one item (us, clusters of 8, 4, 2, 1; six to sixteen adapters: 300 tokens
 // 2048 x 2048 10.0 10.1 11.0 12.4; 904 1216 x 734 16 10.1 11.0 10.5; 1714 496 x 248 19 11.0 10.0 8.3; 4096
-// 2048 x 8192 57 42.0 41.6 51).  In launches that follow one another closely not all those clusters
+// 2048 x 8192 57 42.0 41.6 51: of the third, whose products are short, single CTAs would have the least;
+// the rule does not go by K and N).  In launches that follow one another closely not all those clusters
 // find room beside the early ones of the next launch (1024 x 1024, rank 16, us: 30 of 8 9.2, 31
 // 11.5, 36 15.2; 70 of 4 10.4, 74 13.8): the shares left out below.
 // Items against tiles of 64 tokens as they follow one another, whose adapters a cluster takes in
 // turn (us; 2048 x 8192, rank 32): 4096 tokens of six adapters in six runs 41 against 54, in no
-// order 42 against 92, of 64 adapters 53 against 444; 16384 in six runs 128 against 176.  2048 x 2048:
-// 32768 in six runs 188 against 146: beyond kMostGrouped tokens, or kMostCounted adapters, every
-// CTA would look through too much, and it is tiles (32768 in no order: 302 against 193).
+// order 42 against 92, of 64 adapters 53 against 444; 16384 in six runs 128 against 176.
+// Beyond kMostGrouped tokens, or kMostCounted adapters, every CTA would look through too much, and it
+// is tiles: 2048 x 2048, 32768 in six runs 131 against 188, but in no order 224 against 193.
+// The cut knows the adapters that are loaded, not those that the ids name (they are on the device): 300 tokens
+// of one adapter, 2048 x 8192, rank 32, take 11.6 us where it is the only one, 18.5 among 64, 36.8 among 256;
+// 64 tokens 13.5, 25.7, 25.8; 4096 40.7, 49.9, 50.5, among 1000 77.3.
 //
 // singles: single CTAs that the device holds; clusters(cs): clusters of cs.
 template <typename Clusters>

@@ -28,9 +28,12 @@
 // Measured (GPU time of a replayed call; H 2048, 256 experts unless said):
 //   1 token 8.5 us: latency.  The copies of the 3.1 MB of split weights take 3.3, the exchanges take 2.5 and the selection 2
 //   37 tokens 8.3 us, 300 tokens of H 1024 and 64 experts 7.2: the same chain
-//   4096 tokens in 8 groups 21.5 us: 9 of copies (each tile of tokens reads all the weights: 110 MB
-//     from L2), 6 of selection, the rest launch, accumulators and exchanges; the
-//     MMAs alone would take 6.7.  (With clusters that come in two waves it took 50.)
+//   4096 tokens in 8 groups 20.8 us: 22 clusters of six CTAs (three slices); each tile of tokens reads all
+//     the weights, 69 MB of the 81 that L2 moves.  In two slices, 36 tiles and 110 MB, it took 21.5,
+//     of which the copies took 9 and the selection 6; the MMAs alone would take 6.7.  (With clusters that
+//     come in two waves it took 50.)
+//   384 and 512 experts (both read as 512; that kernel spills 620 bytes a thread): 1 token 16.1 and 16.5 us,
+//     300 17.6 and 18.0, 4096 44 and 46
 //
 // The split weights lie in the order in which a CTA takes them: for each 64
 // columns and each 128 experts the three parts, 128 x 64 each, in the image
@@ -198,6 +201,11 @@ __device__ __forceinline__ void select_token(const Params& p, const Experts<MB>&
       }
     if (lane == 0 && !dry) set_status(p.status, QSM_DEV_NONFINITE);
   }
+  // The scores by the fast exponential and quotient: 2 units in the last place and |l| 2^-24, as much as a
+  // rounding of l itself changes e^l, and 2 units.  Largest relative errors of the weights against 64 bits
+  // (plain fp32 form, with expf and a division, so): 4096 tokens, sigmoid 9.4e-7 3.7e-7 4.1e-7; 300, softmax
+  // 4.7e-6 1.5e-6 1.8e-6; one token 1.5e-7 1.2e-7 1.3e-7.  expf and divisions: 0.5 to 0.9 us more a call, 1.9
+  // with more than 256 experts.
   float s[N];
   if (p.sigmoid) {
 #pragma unroll
